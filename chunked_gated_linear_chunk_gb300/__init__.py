@@ -11,6 +11,8 @@ Entry points (same names as the C ABI):
     gla_fwd(q, k, v, g, ...)            -> (o, final_state)
     gla_bwd(q, k, v, g, do, ...)        -> (dq, dk, dv, dg, dh0)
     ssd_fwd / ssd_bwd                   (scalar per-head gate, g [B,T,H])
+    gla_step / ssd_step                 -> o (new tokens on a pool of states)
+    layer_norm_fwd / layer_norm_bwd     -> (y, mean, rstd) / (dx, dw, db)
     count_docs(segment_ids)             -> int
     get_device_error()                  -> None or raises GlacoreError
 
@@ -29,12 +31,13 @@ __all__ = [
     "GlacoreError", "load", "gla_fwd", "gla_bwd", "ssd_fwd", "ssd_bwd", "count_docs",
     "get_device_error", "workspace_size", "Problem", "selftest_wait", "norm_gate_fwd", "norm_gate_bwd",
     "short_conv_fwd", "short_conv_bwd", "gla_fwd_state", "gla_bwd_state", "state_scan",
+    "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libglacore.so")
 
-OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_DOCS, ERR_RANGE = range(8)
+OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_WORKSPACE, ERR_DOCS, ERR_RANGE, ERR_INDEX = range(9)
 F32, BF16 = 0, 1
 
 EXPORTS = (
@@ -45,6 +48,7 @@ EXPORTS = (
     "glacore_selftest_wait", "norm_gate_fwd", "norm_gate_bwd", "norm_gate_bwd_workspace_size",
     "short_conv_fwd", "short_conv_bwd", "short_conv_bwd_workspace_size",
     "gla_fwd_state", "gla_bwd_state", "glacore_state_scan", "glacore_last_cuda_error",
+    "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size",
 )
 
 
@@ -146,6 +150,15 @@ def load(path: str | None = None):
         lib.glacore_state_scan.argtypes = [P, P, I64, I64, I64, I64, P, I64, I32, P, P]
         lib.short_conv_bwd.restype = ctypes.c_int
         lib.short_conv_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I32, I32, I32, P, P, P, P, ctypes.c_size_t, P]
+        for n in ("gla_step", "ssd_step"):
+            getattr(lib, n).restype = ctypes.c_int
+            getattr(lib, n).argtypes = [PP, P, I64, P, P, P]
+        lib.layer_norm_fwd.restype = ctypes.c_int
+        lib.layer_norm_fwd.argtypes = [P, P, P, I64, I64, I64, I32, F, P, P, P, P]
+        lib.layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
+        lib.layer_norm_bwd_workspace_size.argtypes = [I64, I64]
+        lib.layer_norm_bwd.restype = ctypes.c_int
+        lib.layer_norm_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I32, P, P, P, P, ctypes.c_size_t, P]
         if path is None:
             _lib = lib
         return lib
@@ -380,7 +393,97 @@ def ssd_bwd(q, k, v, g, do, scale=1.0, segment_ids=None, initial_state=None, dht
     return _bwd("ssd", q, k, v, g, do, scale, segment_ids, initial_state, dht, chunk_size, n_seqs, **kw)
 
 
+# ---- the recurrence token by token -------------------------------------------
+def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
+    n_seqs = q.shape[0] if q.shape[1] else 0
+    p, keep = _problem(q, k, v, g, scale, None, None, 0, n_seqs, kind == "ssd")
+    dev = keep[0].device
+    if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
+        raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
+    if state.dim() != 4 or tuple(state.shape[1:]) != (p.H, p.K, p.V):
+        raise ValueError(f"state must be [n_slots,{p.H},{p.K},{p.V}]")
+    idx = _contig(state_indices, torch.int32)
+    if idx is not None and tuple(idx.shape) != (p.B,):
+        raise ValueError("state_indices must be [B]")
+    o = out if out is not None else _new(tuple(keep[2].shape), keep[0].dtype, dev, poison)
+    name = kind + "_step"
+    _check(getattr(load(), name)(ctypes.byref(p), _ptr(state), state.shape[0], _ptr(idx), _ptr(o), _stream(dev)), name)
+    return o
+
+
+def gla_step(q, k, v, g, state, state_indices=None, scale=None, out=None, poison=False):
+    """New tokens of B sequences (q, k, v, g as in gla_fwd, T usually 1) on the
+    pool ``state`` [n_slots,H,K,V] fp32, which is updated in place.
+    state_indices [B] int32 names each sequence's slot (distinct; negative:
+    idle row, o = 0; None: slot b).  Returns o [B,T,H,V]."""
+    return _step("gla", q, k, v, g, state, state_indices, scale, out, poison)
+
+
+def ssd_step(q, k, v, g, state, state_indices=None, scale=1.0, out=None, poison=False):
+    """gla_step with one log decay per head, g [B,T,H]."""
+    return _step("ssd", q, k, v, g, state, state_indices, scale, out, poison)
+
+
 # ---- operations around the recurrence ---------------------------------------
+def _rows2d(t, name):
+    """(tensor, rows, D, row stride) of a [..., D] tensor seen as rows of D
+    values: evenly spaced rows are passed in place, anything else is copied."""
+    if not t.is_cuda:
+        raise ValueError("glacore takes CUDA tensors")
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must be [..., D] with D >= 1")
+    D = t.shape[-1]
+    rows = t.numel() // D
+    if t.is_contiguous():
+        return t, rows, D, 0
+    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= D:
+        return t, rows, D, t.stride(0)
+    return t.contiguous(), rows, D, 0
+
+
+def layer_norm_fwd(x, w=None, b=None, eps=1e-5, out=None):
+    """Layer norm over the last axis: y = (x - mean) * rstd * w + b.  x [..., D]
+    (bf16 or fp32; a 2-D x may have a row stride), w, b [D] fp32 or None.
+    Returns (y, mean, rstd), the row statistics fp32 with x's leading shape."""
+    x, rows, D, xs = _rows2d(x, "x")
+    w, b = _contig(w, torch.float32), _contig(b, torch.float32)
+    if (w is not None and tuple(w.shape) != (D,)) or (b is not None and tuple(b.shape) != (D,)):
+        raise ValueError("layer_norm: w and b must be [D]")
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
+    mean, rstd = stats[0], stats[1]
+    st = load().layer_norm_fwd(_ptr(x), _ptr(w), _ptr(b), rows, D, xs, _dtype_code(x), eps, _ptr(y), _ptr(mean),
+                               _ptr(rstd), _stream(x.device))
+    _check(st, "layer_norm_fwd")
+    return y, mean, rstd
+
+
+def layer_norm_bwd(x, w, mean, rstd, dy, outs=None, workspace=None):
+    """Returns (dx, dw, db) of layer_norm_fwd from its row statistics (dw and
+    db fp32, also when the layer has no w or b)."""
+    if x.shape != dy.shape or x.dtype != dy.dtype:
+        raise ValueError("layer_norm: x and dy must match")
+    x, rows, D, xs = _rows2d(x, "x")
+    dy, _, _, ys = _rows2d(dy, "dy")
+    w, mean, rstd = _contig(w, torch.float32), _contig(mean, torch.float32), _contig(rstd, torch.float32)
+    if (w is not None and tuple(w.shape) != (D,)) or mean.numel() != rows or rstd.numel() != rows:
+        raise ValueError("layer_norm: w must be [D], mean and rstd one value per row")
+    if outs is not None:
+        dx, dw, db = outs
+    else:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        grads = torch.empty((2, D), dtype=torch.float32, device=x.device)
+        dw, db = grads[0], grads[1]
+    lib = load()
+    need = lib.layer_norm_bwd_workspace_size(rows, D)
+    ws = workspace if workspace is not None and workspace.numel() >= need else torch.empty(
+        max(need, 256), dtype=torch.uint8, device=x.device)
+    st = lib.layer_norm_bwd(_ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dy), rows, D, xs, ys, _dtype_code(x),
+                            _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel(), _stream(x.device))
+    _check(st, "layer_norm_bwd")
+    return dx, dw, db
+
+
 def norm_gate_fwd(o, z, w, eps=1e-5, out=None):
     """Per-head RMSNorm times a swish gate over the last axis (V):
     y = o * rsqrt(mean(o^2) + eps) * w * z * sigmoid(z).  o, z [..., V]

@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "internal.cuh"
+#include "step.cuh"
 #include "tc.cuh"
 #include "tc_ssd.cuh"
 #include "tc_ptx.cuh"
@@ -42,7 +43,7 @@ void mark_launch(const char *label, cudaStream_t st) {
 // per device; kernels receive it as an argument).  The cache entries are
 // atomics: host threads may look the address up concurrently (they store
 // the same value).
-static int *device_error_ptr() {
+int *device_error_ptr() {
   static std::atomic<int *> cache[128];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return nullptr;
@@ -477,6 +478,19 @@ glacore_status run_bwd(const glacore_problem *p, bool head_gate, const void *dO,
   return GLACORE_OK;
 }
 
+glacore_status run_step(const glacore_problem *p, bool head_gate, float *state, int64_t n_slots,
+                        const int32_t *slots, void *o, cudaStream_t st) {
+  const glacore_status s = check_problem(p, head_gate);
+  if (s) return s;
+  if (p->segment_ids || p->initial_state || p->chunk_size != 0) return GLACORE_ERR_INVALID_ARG;
+  if (n_slots < 0 || (!slots && n_slots < p->B)) return GLACORE_ERR_INVALID_ARG;
+  if (p->B * p->T == 0) return GLACORE_OK;
+  if (!o || (n_slots > 0 && !state) || ((uintptr_t)state & 3) || ((uintptr_t)slots & 3)) return GLACORE_ERR_INVALID_ARG;
+  int *err = device_error_ptr();
+  if (!err) return GLACORE_ERR_CUDA;
+  return status_of(step::launch(p, head_gate, state, n_slots, slots, o, err, st));
+}
+
 size_t ws_size(const glacore_problem *p, bool head_gate, bool backward) {
   if (check_problem(p, head_gate) != GLACORE_OK) return 0;
   return layout(p, head_gate, backward).total;
@@ -513,6 +527,17 @@ glacore_status ssd_bwd(const glacore_problem *p, const void *do_, const float *d
                        void *dk, void *dv, float *dg, float *dh0, glacore_stream_t stream) {
   t_used = 0;
   return run_bwd(p, true, do_, dht, dq, dk, dv, dg, dh0, (cudaStream_t)stream);
+}
+
+glacore_status gla_step(const glacore_problem *p, float *state, int64_t n_slots, const int32_t *state_indices,
+                        void *o, glacore_stream_t stream) {
+  t_used = 0;
+  return run_step(p, false, state, n_slots, state_indices, o, (cudaStream_t)stream);
+}
+glacore_status ssd_step(const glacore_problem *p, float *state, int64_t n_slots, const int32_t *state_indices,
+                        void *o, glacore_stream_t stream) {
+  t_used = 0;
+  return run_step(p, true, state, n_slots, state_indices, o, (cudaStream_t)stream);
 }
 
 glacore_status glacore_count_docs(const int32_t *segment_ids, int64_t B, int64_t T,
@@ -611,6 +636,7 @@ const char *glacore_status_string(glacore_status s) {
     case GLACORE_ERR_RANGE:
       return "a chunk's summed log-decay is below the kernels' range (-80 per chunk; chunk_size 16 "
              "covers stronger decay)";
+    case GLACORE_ERR_INDEX: return "a state slot or a target token id is out of range";
   }
   return "unknown status";
 }

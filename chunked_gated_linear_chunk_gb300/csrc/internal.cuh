@@ -164,6 +164,10 @@ cudaError_t reduce_heads(int64_t BT, int64_t H, int64_t Hqk, const void *x, void
 cudaError_t sum_channels(int64_t rows, const float *x, float *dg, cudaStream_t st);
 }  // namespace ssdx
 
+// Device address of the error word on the current device (null if it cannot
+// be had); looked up once per device.
+int *device_error_ptr();
+
 // Records the next caller-provided timing event (if any) after a launch.
 void mark_launch(const char *label, cudaStream_t st);
 // Maps a CUDA result to a status, remembering the CUDA error of this host

@@ -19,6 +19,9 @@ constexpr int C = 64;
 constexpr int KD = 128;
 constexpr int VD = 128;
 
+// SMs of the current device (tc_pieces.cu; looked up once per device)
+int64_t sm_count();
+
 // exact sequence split (tc_pieces.cu)
 int64_t piece_len(const glacore_problem *p, bool backward);
 int64_t max_units_of(const glacore_problem *p, int64_t plen);

@@ -338,7 +338,7 @@ cudaError_t launch_order_units(const Units &us, int64_t n, int32_t *order, cudaS
 // unit) leaves most of the GPU's SMs idle, and then into about as many
 // pieces as make one wave.
 // SMs of the current device (one CTA of the chunk-walking kernels per SM).
-static int64_t sm_count() {
+int64_t sm_count() {
   static std::atomic<int> cache[128];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 148;

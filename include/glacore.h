@@ -79,7 +79,8 @@ typedef enum {
   GLACORE_ERR_TIMEOUT = 4,     /* a bounded device wait ran out */
   GLACORE_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than *_workspace_size */
   GLACORE_ERR_DOCS = 6,        /* device: document count != n_seqs */
-  GLACORE_ERR_RANGE = 7        /* device: a chunk's decay is outside the kernels' range (below) */
+  GLACORE_ERR_RANGE = 7,       /* device: a chunk's decay is outside the kernels' range (below) */
+  GLACORE_ERR_INDEX = 8        /* device: a state slot or a target token id is out of range */
 } glacore_status;
 
 typedef enum { GLACORE_F32 = 0, GLACORE_BF16 = 1 } glacore_dtype;
@@ -174,6 +175,35 @@ glacore_status ssd_fwd(const glacore_problem *p, void *o, float *final_state,
 glacore_status ssd_bwd(const glacore_problem *p, const void *do_,
                        const float *dht, void *dq, void *dk, void *dv,
                        float *dg, float *dh0, glacore_stream_t stream);
+
+/* ---- the recurrence token by token (decoding) --------------------------
+ * The T newest tokens (usually one) of each of B sequences, on a pool of
+ * states that is updated in place:
+ *     S <- diag(exp(g_t)) S + k_t v_t^T,   o_t = scale * S^T q_t
+ * with S slot state_indices[b] of the pool.  The pool's slots have the
+ * layout of gla_fwd's / ssd_fwd's final_state, so a prompt run by those and
+ * its new tokens run by these give what one call over all tokens gives.
+ *   p              B, T, H, Hqk, K, V, dtype, scale, q, k, v, g and the token
+ *                  strides as in the chunked calls (any stride, no alignment
+ *                  rule); n_seqs = B (0 if T = 0); segment_ids, initial_state
+ *                  NULL; chunk_size 0; no workspace
+ *   state          [n_slots, H, K, V] fp32, contiguous, read and written
+ *   state_indices  [B] int32 (device) or NULL (sequence b uses slot b;
+ *                  n_slots >= B).  The slots of one call must differ from
+ *                  one another.  A negative index marks an idle row: its o is
+ *                  zero and it has no state.  An index >= n_slots is treated
+ *                  as idle and sets GLACORE_ERR_INDEX in the device error word.
+ *   o              [B, T, H, V] dtype, written
+ * A decay of exactly zero (g = -inf) forgets the slot's content whatever it
+ * is, NaN included: a sequence starts on a used or uninitialised slot so.
+ * Any decay strength is exact here (no chunk, no decay range).  K and V up
+ * to 256.  One launch; the call reads and writes each state once. */
+glacore_status gla_step(const glacore_problem *p, float *state,
+                        int64_t n_slots, const int32_t *state_indices,
+                        void *o, glacore_stream_t stream);
+glacore_status ssd_step(const glacore_problem *p, float *state,
+                        int64_t n_slots, const int32_t *state_indices,
+                        void *o, glacore_stream_t stream);
 
 /* gla_bwd without a workspace, for callers that cannot allocate device
  * memory when they call the backward (for example a host framework that
@@ -285,6 +315,36 @@ glacore_status short_conv_bwd(const void *x, const float *w, const float *b,
                               float *dw, float *db, void *workspace,
                               size_t workspace_bytes, glacore_stream_t stream);
 
+/* Layer norm over rows of D values (the norm in front of a layer and before
+ * the output projection):
+ *     m = mean(x),  r = (mean((x - m)^2) + eps)^(-1/2),  y = (x - m) r w + b
+ *   x           [rows, D] (dtype), x_stride elements between rows (0: D)
+ *   w, b        [D] fp32, or NULL (1 and 0)
+ *   y           [rows, D] (dtype), contiguous, written
+ *   mean, rstd  [rows] fp32: m and r, written; both NULL if not wanted
+ *   D           1 .. 2^31 - 1, any; rows of up to 8192 values with D, the
+ *               strides and the addresses multiples of 16 bytes are the fast
+ *               case.  eps >= 0
+ * Backward (from mean and rstd of the forward), with n = (x - m) r and
+ * a = dy w:
+ *     dx = r (a - mean(a) - n mean(a n)),  dw = sum dy n,  db = sum dy
+ *   dy          [rows, D] (dtype), dy_stride elements between rows (0: D)
+ *   dx          [rows, D] (dtype), contiguous; dw, db [D] fp32: written (also
+ *               when the layer has no w or b)
+ * dw and db are reduced deterministically through the workspace (at least
+ * layer_norm_bwd_workspace_size bytes, 256-byte aligned). */
+glacore_status layer_norm_fwd(const void *x, const float *w, const float *b,
+                              int64_t rows, int64_t D, int64_t x_stride,
+                              int32_t dtype, float eps, void *y, float *mean,
+                              float *rstd, glacore_stream_t stream);
+size_t layer_norm_bwd_workspace_size(int64_t rows, int64_t D);
+glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean,
+                              const float *rstd, const void *dy, int64_t rows,
+                              int64_t D, int64_t x_stride, int64_t dy_stride,
+                              int32_t dtype, void *dx, float *dw, float *db,
+                              void *workspace, size_t workspace_bytes,
+                              glacore_stream_t stream);
+
 /* Counts the documents in segment_ids [B,T] (device pointer) and writes
  * the count, as int64, to *n_docs (DEVICE pointer, 8-byte aligned).
  * Asynchronous on `stream`; the caller reads the count after the stream
@@ -294,7 +354,7 @@ glacore_status glacore_count_docs(const int32_t *segment_ids, int64_t B,
                                   glacore_stream_t stream);
 
 /* Reads and clears the library's device error word (set by kernels for
- * GLACORE_ERR_DOCS, GLACORE_ERR_RANGE or GLACORE_ERR_TIMEOUT).  Synchronises `stream`.
+ * GLACORE_ERR_DOCS, GLACORE_ERR_RANGE, GLACORE_ERR_INDEX or GLACORE_ERR_TIMEOUT).  Synchronises `stream`.
  * Returns GLACORE_OK if no device error was recorded. */
 glacore_status glacore_get_device_error(glacore_stream_t stream);
 
