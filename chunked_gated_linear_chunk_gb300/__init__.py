@@ -13,6 +13,7 @@ Entry points (same names as the C ABI):
     ssd_fwd / ssd_bwd                   (scalar per-head gate, g [B,T,H])
     gla_step / ssd_step                 -> o (new tokens on a pool of states)
     layer_norm_fwd / layer_norm_bwd     -> (y, mean, rstd) / (dx, dw, db)
+    linear_ce_fwd / linear_ce_bwd       -> (loss, lse) / (dx, dw)
     count_docs(segment_ids)             -> int
     get_device_error()                  -> None or raises GlacoreError
 
@@ -31,7 +32,7 @@ __all__ = [
     "GlacoreError", "load", "gla_fwd", "gla_bwd", "ssd_fwd", "ssd_bwd", "count_docs",
     "get_device_error", "workspace_size", "Problem", "selftest_wait", "norm_gate_fwd", "norm_gate_bwd",
     "short_conv_fwd", "short_conv_bwd", "gla_fwd_state", "gla_bwd_state", "state_scan",
-    "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd",
+    "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd", "linear_ce_fwd", "linear_ce_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -49,6 +50,7 @@ EXPORTS = (
     "short_conv_fwd", "short_conv_bwd", "short_conv_bwd_workspace_size",
     "gla_fwd_state", "gla_bwd_state", "glacore_state_scan", "glacore_last_cuda_error",
     "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size",
+    "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_workspace_size", "linear_ce_bwd_workspace_size",
 )
 
 
@@ -159,6 +161,12 @@ def load(path: str | None = None):
         lib.layer_norm_bwd_workspace_size.argtypes = [I64, I64]
         lib.layer_norm_bwd.restype = ctypes.c_int
         lib.layer_norm_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I32, P, P, P, P, ctypes.c_size_t, P]
+        for n in ("linear_ce_fwd", "linear_ce_bwd"):
+            getattr(lib, n + "_workspace_size").restype = ctypes.c_size_t
+            getattr(lib, n + "_workspace_size").argtypes = [I64, I64, I64, I32]
+            getattr(lib, n).restype = ctypes.c_int
+        lib.linear_ce_fwd.argtypes = [P, P, P, I64, I64, I64, I64, I32, P, P, P, ctypes.c_size_t, P]
+        lib.linear_ce_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I32, P, P, P, ctypes.c_size_t, P]
         if path is None:
             _lib = lib
         return lib
@@ -522,6 +530,72 @@ def norm_gate_bwd(o, z, w, dy, eps=1e-5, outs=None, workspace=None):
                            _ptr(dz), _ptr(dw), _ptr(ws), ws.numel(), _stream(o.device))
     _check(st, "norm_gate_bwd")
     return do, dz, dw
+
+
+def _aligned16(t):
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _ce_args(x, w, target):
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
+        raise ValueError("linear_ce: x must be [N, D] and w [V, D] of one dtype")
+    if x.device != w.device or x.device != target.device:
+        raise ValueError("linear_ce: x, w and target must be on one device")
+    target = _contig(target, torch.int64)
+    if tuple(target.shape) != (x.shape[0],):
+        raise ValueError("linear_ce: target must be [N]")
+    x, N, D, xs = _rows2d(x, "x")
+    if x.dtype == torch.bfloat16 and D % 8 == 0 and xs % 8:
+        x, xs = x.contiguous(), 0
+    return _aligned16(x), _aligned16(_contig(w)), target, N, D, w.shape[0], xs
+
+
+def _scratch(need, device, workspace):
+    if workspace is not None and workspace.numel() >= need and workspace.data_ptr() % 256 == 0:
+        return workspace
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
+def linear_ce_fwd(x, w, target, outs=None, workspace=None):
+    """Softmax cross entropy of the output projection: for logits z = x w^T
+    (never kept), lse = logsumexp(z) and loss = lse - z[target] per token.
+    x [N, D] (may have a row stride), w [V, D] (bf16 or fp32), target [N] int64
+    (negative: not scored, loss 0).  Returns (loss, lse), [N] fp32."""
+    x, w, target, N, D, V, xs = _ce_args(x, w, target)
+    code = _dtype_code(x)
+    if outs is not None:
+        loss, lse = outs
+    else:
+        both = torch.empty((2, N), dtype=torch.float32, device=x.device)
+        loss, lse = both[0], both[1]
+    lib = load()
+    ws = _scratch(lib.linear_ce_fwd_workspace_size(N, D, V, code), x.device, workspace)
+    st = lib.linear_ce_fwd(_ptr(x), _ptr(w), _ptr(target), N, D, V, xs, code, _ptr(loss), _ptr(lse), _ptr(ws),
+                           ws.numel(), _stream(x.device))
+    _check(st, "linear_ce_fwd")
+    return loss, lse
+
+
+def linear_ce_bwd(x, w, target, lse, dloss, outs=None, workspace=None):
+    """Gradients of sum(dloss * loss) of linear_ce_fwd, from its lse: returns
+    (dx [N, D], dw [V, D]) in the operands' dtype.  dloss [N] fp32 (1 / count
+    for a mean)."""
+    x, w, target, N, D, V, xs = _ce_args(x, w, target)
+    lse, dloss = _contig(lse, torch.float32), _contig(dloss, torch.float32)
+    if tuple(lse.shape) != (N,) or tuple(dloss.shape) != (N,):
+        raise ValueError("linear_ce: lse and dloss must be [N]")
+    code = _dtype_code(x)
+    if outs is not None:
+        dx, dw = outs
+    else:
+        dx = torch.empty((N, D), dtype=x.dtype, device=x.device)
+        dw = torch.empty((V, D), dtype=x.dtype, device=x.device)
+    lib = load()
+    ws = _scratch(lib.linear_ce_bwd_workspace_size(N, D, V, code), x.device, workspace)
+    st = lib.linear_ce_bwd(_ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), N, D, V, xs, code, _ptr(dx),
+                           _ptr(dw), _ptr(ws), ws.numel(), _stream(x.device))
+    _check(st, "linear_ce_bwd")
+    return dx, dw
 
 
 def short_conv_fwd(x, w, b=None, segment_ids=None, activation=True, out=None):

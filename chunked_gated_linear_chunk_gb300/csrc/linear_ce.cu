@@ -1,0 +1,840 @@
+// linear_ce.cu -- softmax cross entropy of an output projection, forward and
+// backward, without keeping the logits (C ABI in include/glacore.h):
+//     z = x w^T  (x [N, D], w [V, D]),  lse_n = log sum_v exp(z_nv),
+//     loss_n = lse_n - z_n,target(n)
+//   backward, from lse and dloss:
+//     G_nv = (exp(z_nv - lse_n) - [v = target(n)]) dloss_n,
+//     dx = G w,  dw = G^T x
+//
+// Bound by the tensor cores: 2 N V D operations forward, 6 N V D backward
+// (the logits once more and two products).  One kernel body does all of it, a
+// persistent tcgen05 product of a pair of CTAs (M = 256, cta_group::2: each
+// CTA loads half of either operand, so every byte brought to an SM feeds
+// twice the products a single CTA's tile would) with three epilogues:
+//   STATS    a tile of logits becomes, per row, its maximum and its sum of
+//            exponentials (one pass, the running maximum rescaled every 32
+//            columns) and the target's logit; the tiles' pairs are merged by
+//            ce_merge_kernel.  The logits leave TMEM and are gone.
+//   GRAD     a tile of logits becomes a tile of G in bf16 (its products with w
+//            and x are bf16 tensor-core products), for one piece of the
+//            vocabulary at a time, so G takes a bounded workspace.
+//   PRODUCT  dx += G_piece w_piece and dw_piece = G_piece^T x as one list of
+//            units: dw's fill the last wave that dx's would leave open.  dx is
+//            summed over pieces and splits of the vocabulary in fp32 and
+//            rounded once.
+// Warps of a CTA (384 threads): 0 TMA, 1 MMA (of the pair's leader), 4..11
+// epilogue (a TMEM lane per thread, two warps per lane quarter, each half of
+// the tile's columns).  Two accumulators in TMEM, so the epilogue of one tile
+// runs under the products of the next.
+//
+// fp32 operands: each value is cut exactly into three bf16 parts (8 + 8 + 8
+// significant bits) and a product of two values is six of the nine products
+// of their parts (the rest is below 2^-24 of it).  The large product and the
+// five corrections have accumulators of their own, and both are added up in
+// fp32 registers every CHUNK k-blocks: the tensor core's running sum is not
+// rounded to nearest, and over thousands of steps that would show at fp32's
+// tolerances.
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "tc_pair.cuh"
+
+namespace glacore {
+namespace ce {
+
+using namespace ptx;
+using tc::pack_bf16;
+using tc::tmem_ld32;
+using tc::tmem_ld_wait32;
+using tc::WAIT_CYCLES;
+
+constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
+constexpr int BM = 256, BK = 64;   // rows of a pair's tile, K of a stage
+constexpr int CHUNK = 4;           // k-blocks between register sums (fp32 operands)
+constexpr uint32_t A_BYTES = 128 * BK * 2;
+constexpr int MAX_STAGES = 6;
+constexpr int GROUP_M = 8;         // row tiles that share a walk over the columns (L2 reuse)
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
+
+// One product C[m, n] = A B^T over k-blocks, tiles of BM x bn.
+struct Gemm {
+  CUtensorMap a, b;
+  int64_t m, n;
+  int32_t a_mn, b_mn;       // operand stored with its M / N axis contiguous
+  int32_t mt, nt, kb;       // tiles, k-blocks
+  int32_t splits, kb_split; // K cut into `splits` runs of kb_split blocks
+  // PRODUCT: where C goes.  out_f32: fp32, split s at out + s * m * n, added
+  // to what is there if `add`; otherwise the tensors' dtype.
+  void *out;
+  int32_t out_f32, add;
+};
+
+struct Args {
+  Gemm g[2];
+  int64_t units0, units;  // units of g[0], of both
+  int32_t bn;
+  int64_t N, V, v0;  // tokens, vocabulary, first column of the piece
+  const int64_t *target;
+  float2 *part;      // STATS: [2 * nt][N] (maximum * log2 e, sum)
+  float *zt;         // STATS: [N] the target's logit
+  const float *lse, *dloss;  // GRAD
+  __nv_bfloat16 *G;          // GRAD: [PARTS][N][gpitch]
+  int64_t gpitch;
+  int *err;
+};
+
+struct Tile {
+  int64_t m0, n0;
+  int which, split, kb0, kb1, nt;
+};
+
+__device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
+  Tile t;
+  t.which = u >= a.units0;
+  const Gemm &g = a.g[t.which];
+  int64_t r = t.which ? u - a.units0 : u;
+  const int64_t tiles = (int64_t)g.mt * g.nt;
+  t.split = (int)(r / tiles);
+  r -= t.split * tiles;
+  const int64_t band = (int64_t)GROUP_M * g.nt, first = r / band * GROUP_M;
+  const int64_t rows = g.mt - first < GROUP_M ? g.mt - first : GROUP_M;
+  r -= first * g.nt;
+  t.m0 = (first + r % rows) * BM;
+  t.nt = (int)(r / rows);
+  t.n0 = (int64_t)t.nt * a.bn;
+  t.kb0 = t.split * g.kb_split;
+  t.kb1 = min(t.kb0 + g.kb_split, g.kb);
+  return t;
+}
+
+template <int PARTS> struct Shape;
+template <> struct Shape<1> { static constexpr int STAGES = 6, CHUNKS = 1 << 30; };
+template <> struct Shape<3> { static constexpr int STAGES = 3, CHUNKS = CHUNK; };
+
+// The six products of parts (a, b), small ones first; the last is the large
+// one (bf16 operands: the only one).
+__device__ constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+
+template <int KIND, int PARTS>
+__global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_constant__ Args a) {
+  constexpr int STAGES = Shape<PARTS>::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drained;
+  __shared__ uint32_t tmem_ptr;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t b_bytes = (uint32_t)a.bn * BK;  // bn / 2 rows of BK bf16
+  const uint32_t stage_bytes = PARTS * (A_BYTES + b_bytes);
+  const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * EPI_WARPS);
+    }
+    mbar_init(&drained, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&tmem_ptr, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_ptr;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---- tile loads of this CTA; bytes complete on the leader's barrier
+      bool ok = true;
+      int64_t it = 0;
+      for (int64_t u = pair; u < a.units && ok; u += pairs) {
+        const Tile t = tile_of(a, u);
+        const Gemm &g = a.g[t.which];
+        const int am = (int)(t.m0 + rank * 128), bn0 = (int)(t.n0 + rank * (a.bn / 2));
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+          const int s = (int)(it % STAGES);
+          if (!mbar_wait_cluster(&empty[s], (uint32_t)(it / STAGES + 1) & 1, WAIT_CYCLES)) {
+            set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
+          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          const uint32_t sa = smem + s * stage_bytes, sb = sa + PARTS * A_BYTES;
+          const int k = kb * BK;
+          for (int p = 0; p < PARTS; ++p) {
+            if (g.a_mn) {
+              for (int i = 0; i < 2; ++i) tma_load_3d_pair(sa + p * A_BYTES + i * 8192, &g.a, am + 64 * i, k, p, bar);
+            } else {
+              tma_load_3d_pair(sa + p * A_BYTES, &g.a, k, am, p, bar);
+            }
+            if (g.b_mn) {
+              for (int i = 0; i < a.bn / 128; ++i)
+                tma_load_3d_pair(sb + p * b_bytes + i * 8192, &g.b, bn0 + 64 * i, k, p, bar);
+            } else {
+              tma_load_3d_pair(sb + p * b_bytes, &g.b, k, bn0, p, bar);
+            }
+          }
+        }
+      }
+      // every load has landed, and every release has arrived, before the CTA ends
+      for (int64_t i = it > STAGES ? it - STAGES : 0; i < it; ++i) {
+        const int s = (int)(i % STAGES);
+        if (rank == 0) mbar_wait_cluster(&full[s], (uint32_t)(i / STAGES) & 1, WAIT_CYCLES);
+        if (ok) ok = mbar_wait_cluster(&empty[s], (uint32_t)(i / STAGES) & 1, WAIT_CYCLES);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---- products of the pair
+      bool ok = true;
+      int64_t it = 0, hand = 0;
+      for (int64_t u = pair; u < a.units && ok; u += pairs) {
+        const Tile t = tile_of(a, u);
+        const Gemm &g = a.g[t.which];
+        const uint32_t idesc = idesc_bf16(BM, a.bn, g.a_mn, g.b_mn);
+        // bytes between 16-element steps of K, and the operand strides
+        const uint32_t astep = g.a_mn ? 2048 : 32, bstep = g.b_mn ? 2048 : 32;
+        for (int kb = t.kb0; kb < t.kb1 && ok;) {
+          const int buf = (int)(hand & 1);
+          if (!mbar_wait_cluster(&acc_empty[buf], (uint32_t)(hand / 2 + 1) & 1, WAIT_CYCLES)) {
+            set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int end = min(t.kb1 - kb, Shape<PARTS>::CHUNKS) + kb, kfirst = kb;
+          for (; kb < end; ++kb, ++it) {
+            const int s = (int)(it % STAGES);
+            if (!mbar_wait_cluster(&full[s], (uint32_t)(it / STAGES) & 1, WAIT_CYCLES)) {
+              set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem + s * stage_bytes, sb = sa + PARTS * A_BYTES;
+#pragma unroll
+            for (int i = PARTS == 1 ? 5 : 0; i < 6; ++i) {
+              const bool large = i == 5;
+              const uint32_t d = tmem + buf * 256 + (large ? 0 : 128);
+              const SDesc ad = sdesc_sw128(sa + (PARTS == 1 ? 0 : PA[i] * A_BYTES), g.a_mn ? 8192 : 16, 1024);
+              const SDesc bd = sdesc_sw128(sb + (PARTS == 1 ? 0 : PB[i] * b_bytes), g.b_mn ? 8192 : 16, 1024);
+#pragma unroll
+              for (int k = 0; k < BK / 16; ++k)
+                mma_bf16_pair(d, ad + k * astep, bd + k * bstep, idesc,
+                              !(kb == kfirst && k == 0 && (large || i == 0)));
+            }
+            mma_commit_pair(&empty[s]);
+          }
+          if (ok) mma_commit_pair(&acc_full[buf]);
+          ++hand;
+        }
+      }
+      mma_commit_pair(&drained);
+    }
+    // the products in flight end before TMEM and the operands of either CTA go
+    if (lane == 0) mbar_wait_cluster(&drained, 0, WAIT_CYCLES);
+    __syncwarp();
+  } else if (warp >= EPI_FIRST) {
+    // ---- epilogue: thread = row, half = which half of the tile's columns
+    const int quarter = warp & 3, half = (warp - EPI_FIRST) >> 2, cols = a.bn / 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * cols;
+    const uint32_t empty_at[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
+    int64_t hand = 0;
+    bool ok = true;
+    for (int64_t u = pair; u < a.units && ok; u += pairs) {
+      const Tile t = tile_of(a, u);
+      const Gemm &g = a.g[t.which];
+      const int64_t row = t.m0 + rank * 128 + quarter * 32 + lane;
+      const bool live = row < g.m;
+      const int64_t c0 = t.n0 + half * cols;  // first column of this warp (in the piece)
+      // per-row state of the epilogue
+      float mx = -INFINITY, sum = 0.f, lse = 0.f, dl = 0.f;
+      int64_t tgt = -1;
+      if (KIND != PRODUCT) {
+        if (live) tgt = a.target[row];
+        if (KIND == GRAD && live) {
+          lse = a.lse[row];
+          if (tgt >= a.V) {
+            set_device_error(a.err, GLACORE_ERR_INDEX);
+            tgt = -1;
+          }
+          dl = a.dloss[row];
+        }
+      }
+      // 32 columns c0 + c .. of the row
+      auto use = [&](int c, float (&v)[32]) {
+        const int64_t col = c0 + c;
+        if constexpr (KIND == STATS) {
+          const int64_t room = a.V - col;  // columns of the vocabulary here
+          if (room <= 0) return;
+          if (room < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= room) v[i] = -INFINITY;
+          }
+          if (tgt >= col && tgt < col + 32) {
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (tgt == col + i) z = v[i];
+            if (live) a.zt[row] = z;
+          }
+          float top = mx;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+          // a row of -inf so far: any finite reference gives sums of 0
+          const float ref = top == -INFINITY ? 0.f : top * LOG2E;
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[i & 3] += ex2(fmaf(v[i], LOG2E, -ref));
+          const float old = mx == -INFINITY ? 0.f : sum * ex2(mx * LOG2E - ref);
+          sum = old + ((s[0] + s[1]) + (s[2] + s[3]));
+          mx = top;
+        } else if constexpr (KIND == GRAD) {
+          const bool scored = tgt >= 0;
+          const int64_t hit = tgt - a.v0 - col;
+          // the difference first: a product of either with log2 e would round
+          // by more than 1 at logits of some 10^4
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            v[i] = PARTS == 1 ? ex2((v[i] - lse) * LOG2E) : expf(v[i] - lse);
+          if (hit >= 0 && hit < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (hit == i) v[i] -= 1.f;
+          }
+          // a token that is not scored has no gradient, whatever its logits are
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = scored ? v[i] * dl : 0.f;
+          if (!live) return;
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) {
+            __nv_bfloat16 *out = a.G + ((int64_t)p * a.N + row) * a.gpitch + col;
+#pragma unroll
+            for (int i = 0; i < 32; i += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float &x = v[i + 2 * j], &y = v[i + 2 * j + 1];
+                if (PARTS == 1) {
+                  w[j] = pack_bf16(x, y);
+                } else {  // the leading 8 bits of what is left, exactly
+                  const uint32_t xb = __float_as_uint(x) & 0xffff0000u, yb = __float_as_uint(y) & 0xffff0000u;
+                  w[j] = (xb >> 16) | yb;
+                  x -= __uint_as_float(xb);
+                  y -= __uint_as_float(yb);
+                }
+              }
+              st_global_v8(out + i, w);
+            }
+          }
+        } else {
+          if (!live || col >= g.n) return;
+          const int room = g.n - col < 32 ? (int)(g.n - col) : 32;
+          const bool whole = room == 32 && g.n % 8 == 0;
+          if (g.out_f32) {
+            float *out = reinterpret_cast<float *>(g.out) + ((int64_t)t.split * g.m + row) * g.n + col;
+            if (whole) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float4 f = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                if (g.add) {
+                  const float4 o = *reinterpret_cast<const float4 *>(out + i);
+                  f.x += o.x; f.y += o.y; f.z += o.z; f.w += o.w;
+                }
+                *reinterpret_cast<float4 *>(out + i) = f;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < room) out[i] = v[i] + (g.add ? out[i] : 0.f);
+            }
+          } else if (PARTS == 1) {
+            __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + row * g.n + col;
+            if (whole) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 8)
+                tc::st_global_v4(out + i, pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
+                                 pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < room) out[i] = __float2bfloat16_rn(v[i]);
+            }
+          }
+        }
+      };
+      if constexpr (PARTS == 1) {
+        const int buf = (int)(hand & 1);
+        if (!mbar_wait_cluster(&acc_full[buf], (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
+          if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int c = 0; c < cols; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(lanes + buf * 256 + c, r);
+          tmem_ld_wait32(r);
+          if (c + 32 >= cols) {  // the accumulator has been read
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_at[buf]);
+          }
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          use(c, v);
+        }
+        ++hand;
+      } else {
+        float acc[2][32];  // bn = 128: 64 columns
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
+        for (int kb = t.kb0; kb < t.kb1; kb += CHUNK, ++hand) {
+          const int buf = (int)(hand & 1);
+          if (!mbar_wait_cluster(&acc_full[buf], (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
+            if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t r[32];
+            tmem_ld32(lanes + buf * 256 + 128 + 32 * c, r);
+            tmem_ld_wait32(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
+            tmem_ld32(lanes + buf * 256 + 32 * c, r);
+            tmem_ld_wait32(r);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(empty_at[buf]);
+        }
+        if (!ok) break;
+        use(0, acc[0]);
+        use(32, acc[1]);
+      }
+      if (KIND == STATS && live && c0 < a.V)
+        a.part[(int64_t)(2 * t.nt + half) * a.N + row] = make_float2(mx == -INFINITY ? mx : mx * LOG2E, sum);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// lse and loss of 32 rows from the tiles' (maximum, sum) pairs: 8 threads per
+// row take every 8th pair, then merge in order.
+constexpr int MERGE_ROWS = 32, MERGE_LANES = 8;
+__global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
+    ce_merge_kernel(const float2 *__restrict__ part, int64_t slots, int64_t N, int64_t V,
+                    const int64_t *__restrict__ target, const float *__restrict__ zt, float *__restrict__ loss,
+                    float *__restrict__ lse, int *err) {
+  __shared__ float2 red[MERGE_LANES][MERGE_ROWS];
+  const int64_t row = (int64_t)blockIdx.x * MERGE_ROWS + threadIdx.x;
+  float m = -INFINITY, s = 0.f;
+  auto merge = [&](float2 p) {
+    const float top = fmaxf(m, p.x), ref = top == -INFINITY ? 0.f : top;
+    s = s * exp2f(m - ref) + p.y * exp2f(p.x - ref);
+    m = top;
+  };
+  if (row < N)
+    for (int64_t i = threadIdx.y; i < slots; i += MERGE_LANES) merge(part[i * N + row]);
+  red[threadIdx.y][threadIdx.x] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.y || row >= N) return;
+  for (int i = 1; i < MERGE_LANES; ++i) merge(red[i][threadIdx.x]);
+  const float l = (m + log2f(s)) * LN2;
+  lse[row] = l;
+  const int64_t t = target[row];
+  if (t >= V) set_device_error(err, GLACORE_ERR_INDEX);
+  loss[row] = t < 0 || t >= V ? 0.f : l - zt[row];
+}
+
+// dx = the sum of its splits, in order, rounded to its type.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    ce_dx_kernel(const float *__restrict__ part, int splits, int64_t n, T *__restrict__ dx) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float s = part[i];
+    for (int k = 1; k < splits; ++k) s += part[k * n + i];
+    dx[i] = from_f32<T>(s);
+  }
+}
+
+// Rows of bf16 with a pitch that TMA can address: a copy of bf16 values
+// (PARTS = 1), or the three exact parts of fp32 values.
+template <int PARTS, typename T>
+__global__ void __launch_bounds__(256)
+    ce_pack_kernel(const T *__restrict__ src, int64_t rows, int64_t D, int64_t stride, int64_t pitch,
+                   __nv_bfloat16 *__restrict__ dst) {
+  const int64_t n = rows * D;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / D, c = i - r * D;
+    if constexpr (PARTS == 1) {
+      dst[r * pitch + c] = src[r * stride + c];
+    } else {
+      float x = src[r * stride + c];
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const float hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+        dst[(p * rows + r) * pitch + c] = __float2bfloat16_rn(hi);
+        x = isinf(hi) ? 0.f : x - hi;  // an infinity stays one, in the first part
+      }
+    }
+  }
+}
+
+// ---- host ------------------------------------------------------------------
+constexpr size_t G_BYTES = (size_t)256 << 20;   // G of one piece of the vocabulary, about
+constexpr size_t DX_BYTES = (size_t)512 << 20;  // dx's splits, at most
+constexpr int MAX_SPLITS = 32;
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Layout {
+  int parts, bn;
+  bool pack;                         // x and w are copied to rows TMA can address
+  int64_t pitch, piece, pieces, gpitch;
+  int splits, run;  // dx's K axis: `splits` runs of `run` k-blocks (in the first, longest piece)
+  bool dx_f32;
+  size_t off_x, off_w, off_part, off_zt, off_g, off_dx, total;
+};
+
+// Pairs of CTAs that run at once on the current device.
+int64_t pair_count() {
+  static std::atomic<int> cache[128];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return tc::sm_count() / 2;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n <= 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tc::sm_count() / 2 * 2));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = Shape<1>::STAGES * 2 * A_BYTES + 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto *k = ce_product_kernel<STATS, 1>;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n <= 0) {
+      cudaGetLastError();  // no device here: a size query only
+      n = (int)(tc::sm_count() / 2);
+    }
+    cache[dev].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+// dx's K axis (a piece of the vocabulary) is cut so that the units of dx and
+// dw together load the pairs evenly: the cut with the shortest longest pair,
+// units dealt out in turn.
+int best_splits(int64_t tiles_x, int64_t kb_x, int64_t tiles_w, int64_t kb_w, int most) {
+  const int64_t pairs = pair_count();
+  int best = 1;
+  int64_t least = -1;
+  for (int s = 1; s <= most && s <= kb_x; ++s) {
+    const int64_t run = up(kb_x, s), ux = tiles_x * up(kb_x, run);
+    int64_t longest = 0;
+    for (int64_t p = 0; p < pairs; ++p) {
+      const int64_t nx = ux > p ? (ux - p + pairs - 1) / pairs : 0;
+      const int64_t all = ux + tiles_w > p ? (ux + tiles_w - p + pairs - 1) / pairs : 0;
+      longest = std::max(longest, nx * (run + 4) + (all - nx) * (kb_w + 4));  // 4: a unit's start and end
+    }
+    if (least < 0 || longest < least) {
+      least = longest;
+      best = s;
+    }
+  }
+  return best;
+}
+
+Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
+  Layout L;
+  memset(&L, 0, sizeof(L));
+  L.parts = dtype == GLACORE_F32 ? 3 : 1;
+  L.bn = L.parts == 3 ? 128 : 256;
+  L.pack = L.parts == 3 || D % 8 != 0;
+  L.pitch = up(D, 8) * 8;
+  size_t off = 0;
+  auto take = [&](size_t &o, size_t bytes) {
+    o = off;
+    off = align256(off + bytes);
+  };
+  if (L.pack) {
+    take(L.off_x, (size_t)L.parts * N * L.pitch * 2);
+    take(L.off_w, (size_t)L.parts * V * L.pitch * 2);
+  }
+  if (!backward) {
+    take(L.off_part, (size_t)up(V, L.bn) * 2 * N * sizeof(float2));
+    take(L.off_zt, (size_t)N * sizeof(float));
+  } else {
+    const int64_t most = std::max<int64_t>(2048, (int64_t)(G_BYTES / (2 * L.parts * (size_t)N)) / 256 * 256);
+    L.pieces = up(V, most);
+    L.piece = up(up(V, L.pieces), 256) * 256;
+    L.pieces = up(V, L.piece);
+    L.gpitch = L.piece;
+    take(L.off_g, (size_t)L.parts * N * L.gpitch * 2);
+    const int cap = (int)std::max<int64_t>(1, std::min<int64_t>(MAX_SPLITS, DX_BYTES / (4 * N * D)));
+    const int64_t first = std::min(L.piece, V), kb = up(first, BK);
+    L.run = (int)up(kb, best_splits(up(N, BM) * up(D, L.bn), kb, up(first, BM) * up(D, L.bn), up(N, BK), cap));
+    L.splits = (int)up(kb, L.run);
+    L.dx_f32 = L.splits > 1 || L.pieces > 1;
+    if (L.dx_f32) take(L.off_dx, (size_t)L.splits * N * D * sizeof(float));
+  }
+  L.total = off;
+  return L;
+}
+
+// [parts, rows, cols] bf16, `pitch` elements between rows, part_rows rows
+// between parts, box of 64 columns x box_rows.
+bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t parts, int64_t pitch,
+               int64_t part_rows, int box_rows) {
+  tc::EncodeFn enc = tc::encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)(pitch * 2), (cuuint64_t)(part_rows * pitch * 2)};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st) {
+  auto *k = ce_product_kernel<KIND, PARTS>;
+  const int smem = Shape<PARTS>::STAGES * PARTS * (int)(A_BYTES + a.bn * BK) + 1024;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(a.units, pair_count())));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, a);
+}
+template <int KIND> cudaError_t launch(const Args &a, int parts, cudaStream_t st) {
+  return parts == 3 ? launch<KIND, 3>(a, st) : launch<KIND, 1>(a, st);
+}
+
+void whole_k(Gemm &g, int64_t m, int64_t n, int64_t k, int bn) {
+  g.m = m;
+  g.n = n;
+  g.mt = (int32_t)up(m, BM);
+  g.nt = (int32_t)up(n, bn);
+  g.kb = g.kb_split = (int32_t)up(k, BK);
+  g.splits = 1;
+}
+
+// The bf16 rows of x and w: themselves, or packed into the workspace.
+struct Rows {
+  const void *x, *w;
+  int64_t xp, wp;  // pitches
+};
+cudaError_t rows_of(const Layout &L, const void *x, int64_t xs, const void *w, int64_t N, int64_t D, int64_t V,
+                    char *ws, Rows &r, cudaStream_t st) {
+  if (!L.pack) {
+    r = Rows{x, w, xs, D};
+    return cudaSuccess;
+  }
+  auto pack = [&](const void *src, int64_t rows, int64_t stride, size_t off) {
+    const unsigned grid = (unsigned)std::min<int64_t>(up(rows * D, 256), 16 * tc::sm_count());
+    __nv_bfloat16 *dst = (__nv_bfloat16 *)(ws + off);
+    if (L.parts == 3)
+      ce_pack_kernel<3, float><<<grid, 256, 0, st>>>((const float *)src, rows, D, stride, L.pitch, dst);
+    else
+      ce_pack_kernel<1, __nv_bfloat16><<<grid, 256, 0, st>>>((const __nv_bfloat16 *)src, rows, D, stride, L.pitch, dst);
+    mark_launch("ce_pack", st);
+    return cudaGetLastError();
+  };
+  r = Rows{ws + L.off_x, ws + L.off_w, L.pitch, L.pitch};
+  const cudaError_t e = pack(x, N, xs, L.off_x);
+  return e != cudaSuccess ? e : pack(w, V, D, L.off_w);
+}
+
+glacore_status check(const void *x, const void *w, int64_t N, int64_t D, int64_t V, int64_t xs, int32_t dtype) {
+  const int64_t lim = (int64_t)1 << 30;
+  if (N < 0 || D < 1 || V < 1 || N > lim || D > lim || V > lim || (xs != 0 && xs < D) ||
+      (dtype != GLACORE_BF16 && dtype != GLACORE_F32))
+    return GLACORE_ERR_INVALID_ARG;
+  if (N == 0) return GLACORE_OK;
+  if (!x || !w || ((uintptr_t)x & 15) || ((uintptr_t)w & 15)) return GLACORE_ERR_INVALID_ARG;
+  if (dtype == GLACORE_BF16 && D % 8 == 0 && xs % 8 != 0) return GLACORE_ERR_INVALID_ARG;
+  return GLACORE_OK;
+}
+
+}  // namespace ce
+}  // namespace glacore
+
+using namespace glacore;
+using namespace glacore::ce;
+
+extern "C" {
+
+size_t linear_ce_fwd_workspace_size(int64_t N, int64_t D, int64_t V, int32_t dtype) {
+  if (check(nullptr, nullptr, 0, D, V, 0, dtype) || N < 1 || N > ((int64_t)1 << 30)) return 0;
+  return ce::layout(N, D, V, dtype, false).total;
+}
+size_t linear_ce_bwd_workspace_size(int64_t N, int64_t D, int64_t V, int32_t dtype) {
+  if (check(nullptr, nullptr, 0, D, V, 0, dtype) || N < 1 || N > ((int64_t)1 << 30)) return 0;
+  return ce::layout(N, D, V, dtype, true).total;
+}
+
+glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target, int64_t N, int64_t D, int64_t V,
+                             int64_t x_stride, int32_t dtype, float *loss, float *lse, void *workspace,
+                             size_t workspace_bytes, glacore_stream_t stream) {
+  const glacore_status s = check(x, w, N, D, V, x_stride, dtype);
+  if (s || N == 0) return s;
+  if (!target || !loss || !lse) return GLACORE_ERR_INVALID_ARG;
+  const ce::Layout L = ce::layout(N, D, V, dtype, false);
+  if (!workspace || workspace_bytes < L.total || ((uintptr_t)workspace & 255)) return GLACORE_ERR_WORKSPACE;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (const cudaError_t be = tc::bind_context()) return status_of(be);
+  char *ws = (char *)workspace;
+  Rows r;
+  cudaError_t e = rows_of(L, x, x_stride ? x_stride : D, w, N, D, V, ws, r, st);
+  if (e != cudaSuccess) return status_of(e);
+  Args a;
+  memset(&a, 0, sizeof(a));
+  Gemm &g = a.g[0];
+  if (!make_map3(&g.a, r.x, D, N, L.parts, r.xp, N, 128) || !make_map3(&g.b, r.w, D, V, L.parts, r.wp, V, L.bn / 2))
+    return status_of(cudaErrorInvalidValue);
+  whole_k(g, N, V, D, L.bn);
+  a.units0 = a.units = (int64_t)g.mt * g.nt;
+  a.bn = L.bn;
+  a.N = N;
+  a.V = V;
+  a.target = target;
+  a.part = (float2 *)(ws + L.off_part);
+  a.zt = (float *)(ws + L.off_zt);
+  a.err = device_error_ptr();
+  e = ce::launch<STATS>(a, L.parts, st);
+  mark_launch("ce_stats", st);
+  if (e != cudaSuccess) return status_of(e);
+  // pairs of column halves that hold part of the vocabulary
+  const int64_t slots = up(V, L.bn / 2);
+  ce_merge_kernel<<<(unsigned)up(N, MERGE_ROWS), dim3(MERGE_ROWS, MERGE_LANES), 0, st>>>(a.part, slots, N, V, target,
+                                                                                       a.zt, loss, lse, a.err);
+  mark_launch("ce_merge", st);
+  return status_of(cudaGetLastError());
+}
+
+glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target, const float *lse,
+                             const float *dloss, int64_t N, int64_t D, int64_t V, int64_t x_stride, int32_t dtype,
+                             void *dx, void *dw, void *workspace, size_t workspace_bytes, glacore_stream_t stream) {
+  const glacore_status s = check(x, w, N, D, V, x_stride, dtype);
+  if (s) return s;
+  const size_t es = dtype == GLACORE_F32 ? 4 : 2;
+  if (!dw || ((uintptr_t)dw & 15) || ((uintptr_t)dx & 15)) return GLACORE_ERR_INVALID_ARG;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (N == 0) return status_of(cudaMemsetAsync(dw, 0, (size_t)V * D * es, st));
+  if (!target || !lse || !dloss || !dx) return GLACORE_ERR_INVALID_ARG;
+  const ce::Layout L = ce::layout(N, D, V, dtype, true);
+  if (!workspace || workspace_bytes < L.total || ((uintptr_t)workspace & 255)) return GLACORE_ERR_WORKSPACE;
+  if (const cudaError_t be = tc::bind_context()) return status_of(be);
+  char *ws = (char *)workspace;
+  Rows r;
+  cudaError_t e = rows_of(L, x, x_stride ? x_stride : D, w, N, D, V, ws, r, st);
+  if (e != cudaSuccess) return status_of(e);
+  int *err = device_error_ptr();
+  for (int64_t i = 0; i < L.pieces; ++i) {
+    const int64_t v0 = i * L.piece, cols = std::min(L.piece, V - v0);
+    // the piece's rows of w (its parts stay V rows apart)
+    const char *wp = (const char *)r.w + (size_t)v0 * r.wp * 2;
+    Args a;
+    memset(&a, 0, sizeof(a));
+    a.bn = L.bn;
+    a.N = N;
+    a.V = V;
+    a.v0 = v0;
+    a.target = target;
+    a.lse = lse;
+    a.dloss = dloss;
+    a.G = (__nv_bfloat16 *)(ws + L.off_g);
+    a.gpitch = L.gpitch;
+    a.err = err;
+    auto w_map = [&](CUtensorMap *m, int box_rows) {
+      return make_map3(m, wp, D, cols, L.parts, r.wp, V, box_rows);
+    };
+    auto g_map = [&](CUtensorMap *m, int box_rows) {
+      return make_map3(m, ws + L.off_g, cols, N, L.parts, L.gpitch, N, box_rows);
+    };
+    if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, 128) || !w_map(&a.g[0].b, L.bn / 2))
+      return status_of(cudaErrorInvalidValue);
+    whole_k(a.g[0], N, cols, D, L.bn);
+    a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
+    e = ce::launch<GRAD>(a, L.parts, st);
+    mark_launch("ce_grad", st);
+    if (e != cudaSuccess) return status_of(e);
+    // dx (K = the piece) and dw of the piece (K = the tokens)
+    Gemm &gx = a.g[0], &gw = a.g[1];
+    if (!g_map(&gx.a, 128) || !w_map(&gx.b, 64) || !g_map(&gw.a, 64) ||
+        !make_map3(&gw.b, r.x, D, N, L.parts, r.xp, N, 64))
+      return status_of(cudaErrorInvalidValue);
+    whole_k(gx, N, D, cols, L.bn);
+    gx.b_mn = 1;
+    gx.kb_split = L.run;
+    gx.splits = (int32_t)up(gx.kb, L.run);  // no more than the first piece's
+    gx.out_f32 = L.dx_f32 || dtype == GLACORE_F32;
+    gx.add = i > 0;
+    gx.out = L.dx_f32 ? (void *)(ws + L.off_dx) : dx;
+    whole_k(gw, cols, D, N, L.bn);
+    gw.a_mn = gw.b_mn = 1;
+    gw.out_f32 = dtype == GLACORE_F32;
+    gw.out = (char *)dw + (size_t)v0 * D * es;
+    a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
+    a.units = a.units0 + (int64_t)gw.mt * gw.nt;
+    e = ce::launch<PRODUCT>(a, L.parts, st);
+    mark_launch("ce_product", st);
+    if (e != cudaSuccess) return status_of(e);
+  }
+  if (L.dx_f32) {
+    const int64_t n = N * D;
+    const unsigned grid = (unsigned)std::min<int64_t>(up(n, 256), 16 * tc::sm_count());
+    if (dtype == GLACORE_BF16)
+      ce_dx_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>((const float *)(ws + L.off_dx), L.splits, n, (__nv_bfloat16 *)dx);
+    else
+      ce_dx_kernel<float><<<grid, 256, 0, st>>>((const float *)(ws + L.off_dx), L.splits, n, (float *)dx);
+    mark_launch("ce_dx", st);
+    e = cudaGetLastError();
+  }
+  return status_of(e);
+}
+
+}  // extern "C"

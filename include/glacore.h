@@ -345,6 +345,44 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean,
                               void *workspace, size_t workspace_bytes,
                               glacore_stream_t stream);
 
+/* Softmax cross entropy of an output projection, without keeping the logits:
+ *     z = x w^T,  lse_n = log sum_v exp(z_nv),  loss_n = lse_n - z_n,target(n)
+ *   x           [N, D] (dtype), x_stride elements between rows (0: D)
+ *   w           [V, D] (dtype), contiguous
+ *   target      [N] int64 token ids; a negative one marks a token that is
+ *               not scored (loss 0, no gradient); one >= V is treated so and
+ *               sets GLACORE_ERR_INDEX in the device error word
+ *   loss, lse   [N] fp32, written
+ * Backward of sum_n dloss_n loss_n, from the forward's lse:
+ *     G_nv = (exp(z_nv - lse_n) - [v = target(n)]) dloss_n (0 where not
+ *     scored),  dx = G w,  dw = G^T x
+ *   dloss       [N] fp32
+ *   dx          [N, D], dw [V, D] (dtype), contiguous, written
+ * Any N >= 0, D, V up to 2^30.  x, w, dx and dw 16-byte aligned; for bf16
+ * with D a multiple of 8, x_stride as well.  bf16 products run on the tensor
+ * cores with fp32 sums, G rounded to bf16 for them; fp32 operands are split
+ * exactly into three bf16 parts (results to fp32's accuracy).  x and w must be
+ * finite (an infinity in a row that is not scored still reaches dw as NaN).
+ * The workspace (the *_workspace_size bytes, 256-byte aligned) holds row
+ * statistics of the logits' tiles (forward), or G for one piece of the
+ * vocabulary and dx in fp32 (backward): it does not grow with N * V beyond one
+ * piece.  Results do not depend on the order in which CTAs run. */
+size_t linear_ce_fwd_workspace_size(int64_t N, int64_t D, int64_t V,
+                                    int32_t dtype);
+glacore_status linear_ce_fwd(const void *x, const void *w,
+                             const int64_t *target, int64_t N, int64_t D,
+                             int64_t V, int64_t x_stride, int32_t dtype,
+                             float *loss, float *lse, void *workspace,
+                             size_t workspace_bytes, glacore_stream_t stream);
+size_t linear_ce_bwd_workspace_size(int64_t N, int64_t D, int64_t V,
+                                    int32_t dtype);
+glacore_status linear_ce_bwd(const void *x, const void *w,
+                             const int64_t *target, const float *lse,
+                             const float *dloss, int64_t N, int64_t D,
+                             int64_t V, int64_t x_stride, int32_t dtype,
+                             void *dx, void *dw, void *workspace,
+                             size_t workspace_bytes, glacore_stream_t stream);
+
 /* Counts the documents in segment_ids [B,T] (device pointer) and writes
  * the count, as int64, to *n_docs (DEVICE pointer, 8-byte aligned).
  * Asynchronous on `stream`; the caller reads the count after the stream
