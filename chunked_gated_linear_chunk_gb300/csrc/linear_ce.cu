@@ -18,22 +18,29 @@
 //   GRAD     a tile of logits becomes a tile of G in bf16 (its products with w
 //            and x are bf16 tensor-core products), for one piece of the
 //            vocabulary at a time, so G takes a bounded workspace.
-//   PRODUCT  dx += G_piece w_piece and dw_piece = G_piece^T x as one list of
-//            units: dw's fill the last wave that dx's would leave open.  dx is
-//            summed over pieces and splits of the vocabulary in fp32 and
-//            rounded once.
-// Warps of a CTA (384 threads): 0 TMA, 1 MMA (of the pair's leader), 4..11
-// epilogue (a TMEM lane per thread, two warps per lane quarter, each half of
-// the tile's columns).  Two accumulators in TMEM, so the epilogue of one tile
+//   PRODUCT  dx^T += w_piece^T G_piece^T and dw_piece = G_piece^T x as one
+//            list of units: dw's fill the last wave that dx's would leave
+//            open.  dx is summed over pieces and splits of the vocabulary in
+//            fp32 and rounded once.
+// Operand layouts: a B operand with its N axis contiguous (MN-major) ran the
+// same product a quarter slower than a K-major one (8192 x 2048 x 15872: 425
+// against 334 us), an A operand did not (334 against 326 us).  So dx is
+// computed transposed (A = w^T as it lies, B = G as it lies), and x is
+// transposed once per call for dw's B.
+// Warps of a CTA (320 threads): 0..7 epilogue (a TMEM lane per thread, two
+// warps per lane quarter, each half of the tile's columns), 8 TMA, 9 MMA (of
+// the pair's leader).  Two accumulators in TMEM, so the epilogue of one tile
 // runs under the products of the next.
 //
 // fp32 operands: each value is cut exactly into three bf16 parts (8 + 8 + 8
 // significant bits) and a product of two values is six of the nine products
 // of their parts (the rest is below 2^-24 of it).  The large product and the
-// five corrections have accumulators of their own, and both are added up in
-// fp32 registers every CHUNK k-blocks: the tensor core's running sum is not
-// rounded to nearest, and over thousands of steps that would show at fp32's
-// tolerances.
+// five corrections have accumulators of their own.
+// Wherever a result is fp32 (the loss; everything of fp32 operands) the
+// accumulators are added up in fp32 registers every few k-blocks (chunk_of):
+// the tensor core's running sum is not rounded to nearest, and over hundreds
+// of steps that shows (loss of 8192 x 2048 x 32000: 1.2e-6 off with one sum
+// over K = 2048).
 #include <string.h>
 
 #include <algorithm>
@@ -50,9 +57,8 @@ using tc::tmem_ld32;
 using tc::tmem_ld_wait32;
 using tc::WAIT_CYCLES;
 
-constexpr int THREADS = 384, EPI_WARPS = 8, EPI_FIRST = 4;
+constexpr int THREADS = 320, EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;
 constexpr int BM = 256, BK = 64;   // rows of a pair's tile, K of a stage
-constexpr int CHUNK = 4;           // k-blocks between register sums (fp32 operands)
 constexpr uint32_t A_BYTES = 128 * BK * 2;
 constexpr int MAX_STAGES = 6;
 constexpr int GROUP_M = 8;         // row tiles that share a walk over the columns (L2 reuse)
@@ -64,13 +70,14 @@ enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
 struct Gemm {
   CUtensorMap a, b;
   int64_t m, n;
-  int32_t a_mn, b_mn;       // operand stored with its M / N axis contiguous
+  int32_t a_mn;             // A stored with its M axis contiguous (B: always its K axis)
   int32_t mt, nt, kb;       // tiles, k-blocks
   int32_t splits, kb_split; // K cut into `splits` runs of kb_split blocks
-  // PRODUCT: where C goes.  out_f32: fp32, split s at out + s * m * n, added
-  // to what is there if `add`; otherwise the tensors' dtype.
+  // PRODUCT: where C (C^T if `trans`) goes.  out_f32: fp32, split s at
+  // out + s * m * n, added to what is there if `add`; otherwise the tensors'
+  // dtype.
   void *out;
-  int32_t out_f32, add;
+  int32_t out_f32, add, trans;
 };
 
 struct Args {
@@ -82,6 +89,7 @@ struct Args {
   float2 *part;      // STATS: [2 * nt][N] (maximum * log2 e, sum)
   float *zt;         // STATS: [N] the target's logit
   const float *lse, *dloss;  // GRAD
+  const float *unit;         // G is in units of *unit (null: 1)
   __nv_bfloat16 *G;          // GRAD: [PARTS][N][gpitch]
   int64_t gpitch;
   int *err;
@@ -111,9 +119,9 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
   return t;
 }
 
-template <int PARTS> struct Shape;
-template <> struct Shape<1> { static constexpr int STAGES = 6, CHUNKS = 1 << 30; };
-template <> struct Shape<3> { static constexpr int STAGES = 3, CHUNKS = CHUNK; };
+constexpr int stages_of(int parts) { return parts == 1 ? 6 : 3; }
+// k-blocks whose products one accumulator sums
+constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 4 : kind == STATS ? 16 : 1 << 30; }
 
 // The six products of parts (a, b), small ones first; the last is the large
 // one (bf16 operands: the only one).
@@ -121,7 +129,7 @@ __device__ constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
 
 template <int KIND, int PARTS>
 __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_constant__ Args a) {
-  constexpr int STAGES = Shape<PARTS>::STAGES;
+  constexpr int STAGES = stages_of(PARTS), CHUNK = chunk_of(KIND, PARTS);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_ptr;
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     mbar_init(&drained, 1);
     fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == MMA_WARP) {
     tmem_alloc_pair(&tmem_ptr, 512);
     tmem_relinquish_pair();
   }
@@ -154,7 +162,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = tmem_ptr;
 
-  if (warp == 0) {
+  if (warp == TMA_WARP) {
     if (lane == 0) {
       // ---- tile loads of this CTA; bytes complete on the leader's barrier
       bool ok = true;
@@ -180,12 +188,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
             } else {
               tma_load_3d_pair(sa + p * A_BYTES, &g.a, k, am, p, bar);
             }
-            if (g.b_mn) {
-              for (int i = 0; i < a.bn / 128; ++i)
-                tma_load_3d_pair(sb + p * b_bytes + i * 8192, &g.b, bn0 + 64 * i, k, p, bar);
-            } else {
-              tma_load_3d_pair(sb + p * b_bytes, &g.b, k, bn0, p, bar);
-            }
+            tma_load_3d_pair(sb + p * b_bytes, &g.b, k, bn0, p, bar);
           }
         }
       }
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == MMA_WARP) {
     if (lane == 0 && rank == 0) {
       // ---- products of the pair
       bool ok = true;
@@ -205,9 +208,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       for (int64_t u = pair; u < a.units && ok; u += pairs) {
         const Tile t = tile_of(a, u);
         const Gemm &g = a.g[t.which];
-        const uint32_t idesc = idesc_bf16(BM, a.bn, g.a_mn, g.b_mn);
-        // bytes between 16-element steps of K, and the operand strides
-        const uint32_t astep = g.a_mn ? 2048 : 32, bstep = g.b_mn ? 2048 : 32;
+        const uint32_t idesc = idesc_bf16(BM, a.bn, g.a_mn, false);
+        const uint32_t astep = g.a_mn ? 2048 : 32;  // bytes between 16-element steps of K
         for (int kb = t.kb0; kb < t.kb1 && ok;) {
           const int buf = (int)(hand & 1);
           if (!mbar_wait_cluster(&acc_empty[buf], (uint32_t)(hand / 2 + 1) & 1, WAIT_CYCLES)) {
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
             break;
           }
           tc_fence_after();
-          const int end = min(t.kb1 - kb, Shape<PARTS>::CHUNKS) + kb, kfirst = kb;
+          const int end = min(t.kb1 - kb, CHUNK) + kb, kfirst = kb;
           for (; kb < end; ++kb, ++it) {
             const int s = (int)(it % STAGES);
             if (!mbar_wait_cluster(&full[s], (uint32_t)(it / STAGES) & 1, WAIT_CYCLES)) {
@@ -231,10 +233,10 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
               const bool large = i == 5;
               const uint32_t d = tmem + buf * 256 + (large ? 0 : 128);
               const SDesc ad = sdesc_sw128(sa + (PARTS == 1 ? 0 : PA[i] * A_BYTES), g.a_mn ? 8192 : 16, 1024);
-              const SDesc bd = sdesc_sw128(sb + (PARTS == 1 ? 0 : PB[i] * b_bytes), g.b_mn ? 8192 : 16, 1024);
+              const SDesc bd = sdesc_sw128(sb + (PARTS == 1 ? 0 : PB[i] * b_bytes), 16, 1024);
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                mma_bf16_pair(d, ad + k * astep, bd + k * bstep, idesc,
+                mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc,
                               !(kb == kfirst && k == 0 && (large || i == 0)));
             }
             mma_commit_pair(&empty[s]);
@@ -248,11 +250,16 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     // the products in flight end before TMEM and the operands of either CTA go
     if (lane == 0) mbar_wait_cluster(&drained, 0, WAIT_CYCLES);
     __syncwarp();
-  } else if (warp >= EPI_FIRST) {
+  } else {
     // ---- epilogue: thread = row, half = which half of the tile's columns
-    const int quarter = warp & 3, half = (warp - EPI_FIRST) >> 2, cols = a.bn / 2;
+    const int quarter = warp & 3, half = warp >> 2, cols = a.bn / 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * cols;
-    const uint32_t empty_at[2] = {mapa_shared(smem_u32(&acc_empty[0]), 0), mapa_shared(smem_u32(&acc_empty[1]), 0)};
+    auto release = [&](int buf) {  // this warp has read the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+    };
+    const float unit = KIND != STATS && a.unit ? *a.unit : 1.f;
     int64_t hand = 0;
     bool ok = true;
     for (int64_t u = pair; u < a.units && ok; u += pairs) {
@@ -272,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
             set_device_error(a.err, GLACORE_ERR_INDEX);
             tgt = -1;
           }
-          dl = a.dloss[row];
+          dl = a.dloss[row] / unit;
         }
       }
       // 32 columns c0 + c .. of the row
@@ -345,23 +352,37 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         } else {
           if (!live || col >= g.n) return;
           const int room = g.n - col < 32 ? (int)(g.n - col) : 32;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= unit;
+          if (g.trans) {  // the warp's 32 rows lie side by side
+            const int64_t at = col * g.m + row;
+            if (g.out_f32) {
+              float *out = reinterpret_cast<float *>(g.out) + (int64_t)t.split * g.m * g.n + at;
+              float old[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) old[i] = g.add && i < room ? out[i * g.m] : 0.f;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < room) out[i * g.m] = v[i] + old[i];
+            } else if (PARTS == 1) {
+              __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + at;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < room) out[i * g.m] = __float2bfloat16_rn(v[i]);
+            }
+            return;
+          }
           const bool whole = room == 32 && g.n % 8 == 0;
           if (g.out_f32) {
-            float *out = reinterpret_cast<float *>(g.out) + ((int64_t)t.split * g.m + row) * g.n + col;
+            float *out = reinterpret_cast<float *>(g.out) + row * g.n + col;
             if (whole) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float4 f = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                if (g.add) {
-                  const float4 o = *reinterpret_cast<const float4 *>(out + i);
-                  f.x += o.x; f.y += o.y; f.z += o.z; f.w += o.w;
-                }
-                *reinterpret_cast<float4 *>(out + i) = f;
-              }
+              for (int i = 0; i < 32; i += 4)
+                *reinterpret_cast<float4 *>(out + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (i < room) out[i] = v[i] + (g.add ? out[i] : 0.f);
+                if (i < room) out[i] = v[i];
             }
           } else if (PARTS == 1) {
             __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + row * g.n + col;
@@ -379,28 +400,47 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         }
       };
       if constexpr (PARTS == 1) {
-        const int buf = (int)(hand & 1);
-        if (!mbar_wait_cluster(&acc_full[buf], (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
-          if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int c = 0; c < cols; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(lanes + buf * 256 + c, r);
-          tmem_ld_wait32(r);
-          if (c + 32 >= cols) {  // the accumulator has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty_at[buf]);
-          }
-          float v[32];
+        // sums of the chunks before the last (bn = 256: 128 columns)
+        float acc[KIND == STATS ? 4 : 1][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          use(c, v);
+        for (int j = 0; j < (KIND == STATS ? 4 : 1); ++j)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
+        for (int kb = t.kb0; kb < t.kb1; kb += min(t.kb1 - kb, CHUNK), ++hand) {
+          const int buf = (int)(hand & 1);
+          if (!mbar_wait_cluster(&acc_full[buf], (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
+            if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool last = t.kb1 - kb <= CHUNK;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (KIND == STATS) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 16) {  // few registers beside the sums
+                uint32_t r[16];
+                tmem_ld16(lanes + buf * 256 + 32 * c + j, r);
+                tmem_ld_wait(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[c][i + j] += __uint_as_float(r[i]);
+              }
+              if (c == 3) release(buf);
+              if (last) use(32 * c, acc[c]);
+            } else {
+              uint32_t r[32];
+              tmem_ld32(lanes + buf * 256 + 32 * c, r);
+              tmem_ld_wait32(r);
+              if (c == 3) release(buf);
+              float v[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+              use(32 * c, v);
+            }
+          }
         }
-        ++hand;
+        if (!ok) break;
       } else {
         float acc[2][32];  // bn = 128: 64 columns
 #pragma unroll
@@ -427,9 +467,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
 #pragma unroll
             for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(empty_at[buf]);
+          release(buf);
         }
         if (!ok) break;
         use(0, acc[0]);
@@ -442,7 +480,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   tc_fence_before();
   __syncthreads();
   cluster_sync();
-  if (warp == 1) {
+  if (warp == MMA_WARP) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
@@ -476,15 +514,74 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
   loss[row] = t < 0 || t >= V ? 0.f : l - zt[row];
 }
 
-// dx = the sum of its splits, in order, rounded to its type.
-template <typename T>
+// dx = the sum of its splits, in order, rounded to its type.  WIDE: n is a
+// multiple of 4 (every split then starts on 16 bytes).
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256)
     ce_dx_kernel(const float *__restrict__ part, int splits, int64_t n, T *__restrict__ dx) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    float s = part[i];
-    for (int k = 1; k < splits; ++k) s += part[k * n + i];
-    dx[i] = from_f32<T>(s);
+  if constexpr (WIDE) {
+    const float4 *p = reinterpret_cast<const float4 *>(part);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += (int64_t)gridDim.x * 256) {
+      float4 s = p[i];
+#pragma unroll 4
+      for (int k = 1; k < splits; ++k) {
+        const float4 f = p[k * (n / 4) + i];
+        s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
+      }
+      if constexpr (sizeof(T) == 4)
+        reinterpret_cast<float4 *>(dx)[i] = s;
+      else
+        reinterpret_cast<uint2 *>(dx)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+    }
+  } else {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+      float s = part[i];
+      for (int k = 1; k < splits; ++k) s += part[k * n + i];
+      dx[i] = from_f32<T>(s);
+    }
   }
+}
+
+// The unit of G: the largest |dloss| of a scored token (1 if there is none).
+// With dloss one number for all tokens, the usual mean, G is then p - [v =
+// target] itself, and the -1 at the target of a token that is far from
+// foreseen, most of its gradient, is exact in bf16.
+__global__ void __launch_bounds__(1024)
+    ce_unit_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t N, int64_t V,
+                   float *__restrict__ unit) {
+  __shared__ float red[32];
+  float m = 0.f;
+  for (int64_t i = threadIdx.x; i < N; i += 1024) {
+    const int64_t t = target[i];
+    if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
+  }
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    m = red[threadIdx.x];
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (threadIdx.x == 0) *unit = m > 0.f && isfinite(m) ? m : 1.f;
+  }
+}
+
+// dst [parts, cols, dpitch] = src [parts, rows, spitch] transposed, 64 x 64 at
+// a time through shared memory.
+__global__ void __launch_bounds__(256)
+    ce_transpose_kernel(const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
+                        int64_t dpitch, __nv_bfloat16 *__restrict__ dst) {
+  __shared__ __nv_bfloat16 tile[64][66];
+  src += blockIdx.z * rows * spitch;
+  dst += blockIdx.z * cols * dpitch;
+  const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  for (int i = y; i < 64; i += 8)
+    for (int j = x; j < 64; j += 32)
+      if (r0 + i < rows && c0 + j < cols) tile[i][j] = src[(r0 + i) * spitch + c0 + j];
+  __syncthreads();
+  for (int j = y; j < 64; j += 8)
+    for (int i = x; i < 64; i += 32)
+      if (r0 + i < rows && c0 + j < cols) dst[(c0 + j) * dpitch + r0 + i] = tile[i][j];
 }
 
 // Rows of bf16 with a pitch that TMA can address: a copy of bf16 values
@@ -511,7 +608,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---- host ------------------------------------------------------------------
-constexpr size_t G_BYTES = (size_t)256 << 20;   // G of one piece of the vocabulary, about
+constexpr size_t G_BYTES = (size_t)512 << 20;   // G of one piece of the vocabulary, about
 constexpr size_t DX_BYTES = (size_t)512 << 20;  // dx's splits, at most
 constexpr int MAX_SPLITS = 32;
 
@@ -521,10 +618,10 @@ inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct Layout {
   int parts, bn;
   bool pack;                         // x and w are copied to rows TMA can address
-  int64_t pitch, piece, pieces, gpitch;
+  int64_t pitch, xt_pitch, piece, pieces, gpitch;
   int splits, run;  // dx's K axis: `splits` runs of `run` k-blocks (in the first, longest piece)
   bool dx_f32;
-  size_t off_x, off_w, off_part, off_zt, off_g, off_dx, total;
+  size_t off_x, off_w, off_part, off_zt, off_unit, off_xt, off_g, off_dx, total;
 };
 
 // Pairs of CTAs that run at once on the current device.
@@ -537,7 +634,7 @@ int64_t pair_count() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tc::sm_count() / 2 * 2));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = Shape<1>::STAGES * 2 * A_BYTES + 1024;
+    cfg.dynamicSmemBytes = stages_of(1) * 2 * A_BYTES + 1024;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -604,10 +701,13 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     L.piece = up(up(V, L.pieces), 256) * 256;
     L.pieces = up(V, L.piece);
     L.gpitch = L.piece;
+    L.xt_pitch = up(N, 8) * 8;
+    take(L.off_unit, sizeof(float));
+    take(L.off_xt, (size_t)L.parts * D * L.xt_pitch * 2);
     take(L.off_g, (size_t)L.parts * N * L.gpitch * 2);
     const int cap = (int)std::max<int64_t>(1, std::min<int64_t>(MAX_SPLITS, DX_BYTES / (4 * N * D)));
     const int64_t first = std::min(L.piece, V), kb = up(first, BK);
-    L.run = (int)up(kb, best_splits(up(N, BM) * up(D, L.bn), kb, up(first, BM) * up(D, L.bn), up(N, BK), cap));
+    L.run = (int)up(kb, best_splits(up(D, BM) * up(N, L.bn), kb, up(first, BM) * up(D, L.bn), up(N, BK), cap));
     L.splits = (int)up(kb, L.run);
     L.dx_f32 = L.splits > 1 || L.pieces > 1;
     if (L.dx_f32) take(L.off_dx, (size_t)L.splits * N * D * sizeof(float));
@@ -633,7 +733,7 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
-  const int smem = Shape<PARTS>::STAGES * PARTS * (int)(A_BYTES + a.bn * BK) + 1024;
+  const int smem = stages_of(PARTS) * PARTS * (int)(A_BYTES + a.bn * BK) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -773,6 +873,22 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   cudaError_t e = rows_of(L, x, x_stride ? x_stride : D, w, N, D, V, ws, r, st);
   if (e != cudaSuccess) return status_of(e);
   int *err = device_error_ptr();
+  const __nv_bfloat16 *xt = (const __nv_bfloat16 *)(ws + L.off_xt);
+  const float *unit = nullptr;
+  {
+    const dim3 grid((unsigned)up(N, 64), (unsigned)up(D, 64), (unsigned)L.parts);
+    if (grid.y > 65535u) return GLACORE_ERR_UNSUPPORTED;
+    ce_transpose_kernel<<<grid, 256, 0, st>>>((const __nv_bfloat16 *)r.x, N, D, r.xp, L.xt_pitch,
+                                              (__nv_bfloat16 *)(ws + L.off_xt));
+    mark_launch("ce_transpose", st);
+    if ((e = cudaGetLastError()) != cudaSuccess) return status_of(e);
+    if (L.parts == 1) {  // three parts hold dloss as it is
+      unit = (const float *)(ws + L.off_unit);
+      ce_unit_kernel<<<1, 1024, 0, st>>>(dloss, target, N, V, (float *)(ws + L.off_unit));
+      mark_launch("ce_unit", st);
+      if ((e = cudaGetLastError()) != cudaSuccess) return status_of(e);
+    }
+  }
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, cols = std::min(L.piece, V - v0);
     // the piece's rows of w (its parts stay V rows apart)
@@ -786,6 +902,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     a.target = target;
     a.lse = lse;
     a.dloss = dloss;
+    a.unit = unit;
     a.G = (__nv_bfloat16 *)(ws + L.off_g);
     a.gpitch = L.gpitch;
     a.err = err;
@@ -802,20 +919,21 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     e = ce::launch<GRAD>(a, L.parts, st);
     mark_launch("ce_grad", st);
     if (e != cudaSuccess) return status_of(e);
-    // dx (K = the piece) and dw of the piece (K = the tokens)
+    // dx^T (K = the piece) and dw of the piece (K = the tokens)
     Gemm &gx = a.g[0], &gw = a.g[1];
-    if (!g_map(&gx.a, 128) || !w_map(&gx.b, 64) || !g_map(&gw.a, 64) ||
-        !make_map3(&gw.b, r.x, D, N, L.parts, r.xp, N, 64))
+    if (!w_map(&gx.a, 64) || !g_map(&gx.b, L.bn / 2) || !g_map(&gw.a, 64) ||
+        !make_map3(&gw.b, xt, N, D, L.parts, L.xt_pitch, D, L.bn / 2))
       return status_of(cudaErrorInvalidValue);
-    whole_k(gx, N, D, cols, L.bn);
-    gx.b_mn = 1;
+    whole_k(gx, D, N, cols, L.bn);
+    gx.a_mn = 1;
     gx.kb_split = L.run;
     gx.splits = (int32_t)up(gx.kb, L.run);  // no more than the first piece's
     gx.out_f32 = L.dx_f32 || dtype == GLACORE_F32;
     gx.add = i > 0;
+    gx.trans = 1;
     gx.out = L.dx_f32 ? (void *)(ws + L.off_dx) : dx;
     whole_k(gw, cols, D, N, L.bn);
-    gw.a_mn = gw.b_mn = 1;
+    gw.a_mn = 1;
     gw.out_f32 = dtype == GLACORE_F32;
     gw.out = (char *)dw + (size_t)v0 * D * es;
     a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
@@ -826,11 +944,14 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   }
   if (L.dx_f32) {
     const int64_t n = N * D;
-    const unsigned grid = (unsigned)std::min<int64_t>(up(n, 256), 16 * tc::sm_count());
+    const unsigned grid = (unsigned)std::min<int64_t>(up(n, 1024), 16 * tc::sm_count());
+    const float *p = (const float *)(ws + L.off_dx);
     if (dtype == GLACORE_BF16)
-      ce_dx_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>((const float *)(ws + L.off_dx), L.splits, n, (__nv_bfloat16 *)dx);
+      n % 4 == 0 ? ce_dx_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p, L.splits, n, (__nv_bfloat16 *)dx)
+                 : ce_dx_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p, L.splits, n, (__nv_bfloat16 *)dx);
     else
-      ce_dx_kernel<float><<<grid, 256, 0, st>>>((const float *)(ws + L.off_dx), L.splits, n, (float *)dx);
+      n % 4 == 0 ? ce_dx_kernel<float, true><<<grid, 256, 0, st>>>(p, L.splits, n, (float *)dx)
+                 : ce_dx_kernel<float, false><<<grid, 256, 0, st>>>(p, L.splits, n, (float *)dx);
     mark_launch("ce_dx", st);
     e = cudaGetLastError();
   }
