@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -154,7 +155,7 @@ def load(path: str | None = None):
         lib.short_conv_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I32, I32, I32, P, P, P, P, ctypes.c_size_t, P]
         for n in ("gla_step", "ssd_step"):
             getattr(lib, n).restype = ctypes.c_int
-            getattr(lib, n).argtypes = [PP, P, I64, P, P, P]
+            getattr(lib, n).argtypes = [P, P, I64, P, P, P]
         lib.layer_norm_fwd.restype = ctypes.c_int
         lib.layer_norm_fwd.argtypes = [P, P, P, I64, I64, I64, I32, F, P, P, P, P]
         lib.layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
@@ -190,6 +191,17 @@ def _ptr(t):
 
 def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _raw_stream(t):
+    """The current stream of t's device as an integer handle, without the
+    stream object (a call that takes a few microseconds feels the object)."""
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _addr(t):
+    """Device address for a pointer argument (None: NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -402,20 +414,48 @@ def ssd_bwd(q, k, v, g, do, scale=1.0, segment_ids=None, initial_state=None, dht
 
 
 # ---- the recurrence token by token -------------------------------------------
+# glacore_problem as bytes: a call of a few microseconds feels a ctypes
+# structure filled field by field
+_PACK = struct.Struct("@6qiifi5PqPPN3q")
+assert _PACK.size == ctypes.sizeof(Problem)
+
+
+def _tokens(t):
+    """_rows, with the usual case first."""
+    if not t.is_cuda:
+        raise ValueError("glacore takes CUDA tensors")
+    return (t, 0) if t.is_contiguous() else _rows(t)
+
+
 def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
-    n_seqs = q.shape[0] if q.shape[1] else 0
-    p, keep = _problem(q, k, v, g, scale, None, None, 0, n_seqs, kind == "ssd")
-    dev = keep[0].device
+    B, T, Hqk, K = q.shape
+    H, V = v.shape[2:]
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt:
+        raise TypeError("q, k, v must share one dtype")
+    if k.shape != q.shape or v.shape[0] != B or v.shape[1] != T:
+        raise ValueError("shape mismatch between q, k, v")
+    if tuple(g.shape) != ((B, T, H, K) if kind == "gla" else (B, T, H)):
+        raise ValueError("gla_step's gate must be [B,T,H,K]" if kind == "gla" else "ssd_step's gate must be [B,T,H]")
+    (q, qs), (k, ks), (v, vs) = _tokens(q), _tokens(k), _tokens(v)
+    g = _contig(g, torch.float32)
     if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
-    if state.dim() != 4 or tuple(state.shape[1:]) != (p.H, p.K, p.V):
-        raise ValueError(f"state must be [n_slots,{p.H},{p.K},{p.V}]")
+    if state.dim() != 4 or tuple(state.shape[1:]) != (H, K, V):
+        raise ValueError(f"state must be [n_slots,{H},{K},{V}]")
     idx = _contig(state_indices, torch.int32)
-    if idx is not None and tuple(idx.shape) != (p.B,):
+    if idx is not None and (idx.dim() != 1 or idx.shape[0] != B):
         raise ValueError("state_indices must be [B]")
-    o = out if out is not None else _new(tuple(keep[2].shape), keep[0].dtype, dev, poison)
-    name = kind + "_step"
-    _check(getattr(load(), name)(ctypes.byref(p), _ptr(state), state.shape[0], _ptr(idx), _ptr(o), _stream(dev)), name)
+    o = out if out is not None else _new((B, T, H, V), dt, q.device, poison)
+    if scale is None:
+        scale = K ** -0.5
+    p = _PACK.pack(B, T, H, Hqk, K, V, _dtype_code(q), 0, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                   g.data_ptr(), 0, B if T else 0, 0, 0, 0, qs, ks, vs)
+    lib = _lib or load()
+    st = (lib.gla_step if kind == "gla" else lib.ssd_step)(p, state.data_ptr(), state.shape[0], _addr(idx),
+                                                           o.data_ptr(), _raw_stream(q))
+    if st:
+        _check(st, kind + "_step")
     return o
 
 
@@ -455,14 +495,16 @@ def layer_norm_fwd(x, w=None, b=None, eps=1e-5, out=None):
     Returns (y, mean, rstd), the row statistics fp32 with x's leading shape."""
     x, rows, D, xs = _rows2d(x, "x")
     w, b = _contig(w, torch.float32), _contig(b, torch.float32)
-    if (w is not None and tuple(w.shape) != (D,)) or (b is not None and tuple(b.shape) != (D,)):
+    if (w is not None and w.shape != (D,)) or (b is not None and b.shape != (D,)):
         raise ValueError("layer_norm: w and b must be [D]")
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    stats = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device)
-    mean, rstd = stats[0], stats[1]
-    st = load().layer_norm_fwd(_ptr(x), _ptr(w), _ptr(b), rows, D, xs, _dtype_code(x), eps, _ptr(y), _ptr(mean),
-                               _ptr(rstd), _stream(x.device))
-    _check(st, "layer_norm_fwd")
+    shape, dev = x.shape, x.device
+    y = out if out is not None else torch.empty(shape, dtype=x.dtype, device=dev)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    st = (_lib or load()).layer_norm_fwd(x.data_ptr(), _addr(w), _addr(b), rows, D, xs, _dtype_code(x), eps,
+                                         y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(x))
+    if st:
+        _check(st, "layer_norm_fwd")
     return y, mean, rstd
 
 
@@ -474,21 +516,22 @@ def layer_norm_bwd(x, w, mean, rstd, dy, outs=None, workspace=None):
     x, rows, D, xs = _rows2d(x, "x")
     dy, _, _, ys = _rows2d(dy, "dy")
     w, mean, rstd = _contig(w, torch.float32), _contig(mean, torch.float32), _contig(rstd, torch.float32)
-    if (w is not None and tuple(w.shape) != (D,)) or mean.numel() != rows or rstd.numel() != rows:
+    if (w is not None and w.shape != (D,)) or mean.numel() != rows or rstd.numel() != rows:
         raise ValueError("layer_norm: w must be [D], mean and rstd one value per row")
+    dev = x.device
     if outs is not None:
         dx, dw, db = outs
     else:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        grads = torch.empty((2, D), dtype=torch.float32, device=x.device)
-        dw, db = grads[0], grads[1]
-    lib = load()
-    need = lib.layer_norm_bwd_workspace_size(rows, D)
-    ws = workspace if workspace is not None and workspace.numel() >= need else torch.empty(
-        max(need, 256), dtype=torch.uint8, device=x.device)
-    st = lib.layer_norm_bwd(_ptr(x), _ptr(w), _ptr(mean), _ptr(rstd), _ptr(dy), rows, D, xs, ys, _dtype_code(x),
-                            _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel(), _stream(x.device))
-    _check(st, "layer_norm_bwd")
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        dw = torch.empty(D, dtype=torch.float32, device=dev)
+        db = torch.empty(D, dtype=torch.float32, device=dev)
+    lib = _lib or load()
+    ws = _scratch(lib.layer_norm_bwd_workspace_size(rows, D), dev, workspace)
+    st = lib.layer_norm_bwd(x.data_ptr(), _addr(w), mean.data_ptr(), rstd.data_ptr(), dy.data_ptr(), rows, D, xs, ys,
+                            _dtype_code(x), dx.data_ptr(), dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel(),
+                            _raw_stream(x))
+    if st:
+        _check(st, "layer_norm_bwd")
     return dx, dw, db
 
 
@@ -566,13 +609,14 @@ def linear_ce_fwd(x, w, target, outs=None, workspace=None):
     if outs is not None:
         loss, lse = outs
     else:
-        both = torch.empty((2, N), dtype=torch.float32, device=x.device)
-        loss, lse = both[0], both[1]
-    lib = load()
+        loss = torch.empty(N, dtype=torch.float32, device=x.device)
+        lse = torch.empty(N, dtype=torch.float32, device=x.device)
+    lib = _lib or load()
     ws = _scratch(lib.linear_ce_fwd_workspace_size(N, D, V, code), x.device, workspace)
-    st = lib.linear_ce_fwd(_ptr(x), _ptr(w), _ptr(target), N, D, V, xs, code, _ptr(loss), _ptr(lse), _ptr(ws),
-                           ws.numel(), _stream(x.device))
-    _check(st, "linear_ce_fwd")
+    st = lib.linear_ce_fwd(x.data_ptr(), w.data_ptr(), target.data_ptr(), N, D, V, xs, code, loss.data_ptr(),
+                           lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(x))
+    if st:
+        _check(st, "linear_ce_fwd")
     return loss, lse
 
 
@@ -590,11 +634,12 @@ def linear_ce_bwd(x, w, target, lse, dloss, outs=None, workspace=None):
     else:
         dx = torch.empty((N, D), dtype=x.dtype, device=x.device)
         dw = torch.empty((V, D), dtype=x.dtype, device=x.device)
-    lib = load()
+    lib = _lib or load()
     ws = _scratch(lib.linear_ce_bwd_workspace_size(N, D, V, code), x.device, workspace)
-    st = lib.linear_ce_bwd(_ptr(x), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), N, D, V, xs, code, _ptr(dx),
-                           _ptr(dw), _ptr(ws), ws.numel(), _stream(x.device))
-    _check(st, "linear_ce_bwd")
+    st = lib.linear_ce_bwd(x.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(), N, D, V,
+                           xs, code, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(x))
+    if st:
+        _check(st, "linear_ce_bwd")
     return dx, dw
 
 

@@ -7,16 +7,21 @@
 //
 // HBM-bound: the forward moves 2, the backward 3 rows of D values per token
 // and nothing is read twice.  A row lives in the registers of L threads
-// (column vectors t, t + L, t + 2L, ... of 16 bytes for thread t), so the
-// mean and the squared deviations from it are two exact passes over
-// registers; L <= 32 threads exchange sums by shuffles alone, L = 64 .. 256
-// through shared memory and a barrier of the row's own warps, so the rows of
-// a CTA never wait for one another.  Rows of more than MAX_COLS values are
-// walked in a loop by a whole CTA instead.  All arithmetic is fp32; bf16
-// outputs are rounded once.  The weight gradients are deterministic: column
-// sums in registers over the rows a thread sees, per-CTA partial sums in the
-// workspace, then one kernel that adds the partial rows in a fixed order.
+// (column vectors t, t + L, ... of 16 bytes for thread t), so the mean and the
+// squared deviations from it are two exact passes over registers.  A thread
+// keeps its columns for the whole kernel: their weights and the column sums of
+// the weight gradients stay in its registers (read for every row instead, w
+// and b took the L1 more time than the rows took the memory: 8192 x 2048 bf16
+// forward 22.5 us).  It takes up to two rows at a time and loads the next ones
+// before it reduces these.  L <= 32 threads exchange sums by shuffles alone, L
+// = 64 .. 256 through shared memory and a barrier of the row's own warps.
+// Rows of more than MAX_COLS values are walked in a loop by a whole CTA
+// instead.  All arithmetic is fp32; bf16 outputs are rounded once.  The weight
+// gradients are deterministic: per-CTA partial sums in the workspace, then one
+// kernel that adds the partial rows in a fixed order.
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "internal.cuh"
 #include "tc.cuh"
@@ -88,87 +93,126 @@ __device__ __forceinline__ void weights(const float *w, int64_t c, float otherwi
   }
 }
 
-// Sums over the L threads of a row, in every one of them.  Two buffers in
-// turn: one barrier per sum, since a thread writes a buffer again only after
-// a barrier that everyone reaches after reading it.
-struct RowSum {
-  float2 (*red)[THREADS / 32];
+// N sums over the L threads of a row group, in every one of them.  Two
+// buffers in turn: one barrier per call, since a thread writes a buffer again
+// only after a barrier that everyone reaches after reading it.
+template <int N> struct RowSum {
+  float (*red)[THREADS / 32][N];
   int L, buf;
-  __device__ __forceinline__ float2 operator()(float2 v) {
-    for (int m = 1; m < L && m < 32; m <<= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, m);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, m);
-    }
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    for (int m = 1; m < L && m < 32; m <<= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], m);
     if (L > 32) {
       const int warp = threadIdx.x >> 5, wpr = L >> 5, first = warp & ~(wpr - 1);
-      if ((threadIdx.x & 31) == 0) red[buf][warp] = v;
+      if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) red[buf][warp][i] = v[i];
       asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpr), "r"(L) : "memory");
-      v = make_float2(0.f, 0.f);
-      for (int i = 0; i < wpr; ++i) {
-        const float2 a = red[buf][first + i];
-        v.x += a.x;
-        v.y += a.y;
-      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 0.f;
+      for (int k = 0; k < wpr; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += red[buf][first + k][i];
       buf ^= 1;
     }
-    return v;
   }
 };
+
+// Rows a thread takes at a time, and whether the next ones are loaded early:
+// as far as registers allow.
+constexpr int rows_of(int vec, int nv) { return vec * nv <= 8 ? 2 : 1; }
+constexpr bool early(int vec, int nv) { return vec * nv * rows_of(vec, nv) <= 16; }
 
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(THREADS)
     layer_norm_fwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ b,
                           T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd, int64_t rows, int D,
                           int64_t xs, int lg, float eps) {
-  __shared__ float2 red[2][THREADS / 32];
-  const int L = 1 << lg, t = threadIdx.x & (L - 1), per = THREADS >> lg;
-  RowSum sum{red, L, 0};
+  constexpr int R = rows_of(VEC, NV);
+  __shared__ float red[2][THREADS / 32][R];
+  const int L = 1 << lg, t = threadIdx.x & (L - 1), per = (THREADS >> lg) * R;
+  RowSum<R> sum{red, L, 0};
   const float inv = 1.f / (float)D;
-  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += (int64_t)gridDim.x * per) {
-    const int64_t row = r0 + (threadIdx.x >> lg);
-    const bool live = row < rows;
-    Vec<T, VEC> xv[NV];
-    float s = 0.f;
+  float wv[NV][VEC], bv[NV][VEC];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (live && (j * L + t) * VEC < D) xv[j].load(x + row * xs + (j * L + t) * VEC);
+  for (int j = 0; j < NV; ++j)
+    if ((j * L + t) * VEC < D) {
+      weights<VEC>(w, (j * L + t) * VEC, 1.f, wv[j]);
+      weights<VEC>(b, (j * L + t) * VEC, 0.f, bv[j]);
+    }
+  Vec<T, VEC> xv[R][NV], next[R][NV];
+  auto fetch = [&](int64_t r0, Vec<T, VEC>(&v)[R][NV]) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (live && (j * L + t) * VEC < D) {
-        float v[VEC];
-        xv[j].get(v);
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = r0 + (threadIdx.x >> lg) * R + i;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) s += v[e];
+      for (int j = 0; j < NV; ++j)
+        if (row < rows && (j * L + t) * VEC < D) v[i][j].load(x + row * xs + (j * L + t) * VEC);
+    }
+  };
+  int64_t r0 = (int64_t)blockIdx.x * per;
+  const int64_t step = (int64_t)gridDim.x * per;
+  if (early(VEC, NV)) fetch(r0, xv);
+  for (; r0 < rows; r0 += step) {
+    if (early(VEC, NV))
+      fetch(r0 + step, next);
+    else
+      fetch(r0, xv);
+    const int64_t first = r0 + (threadIdx.x >> lg) * R;
+    float m[R], r[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      m[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (first + i < rows && (j * L + t) * VEC < D) {
+          float v[VEC];
+          xv[i][j].get(v);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) m[i] += v[e];
+        }
+    }
+    sum(m);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      m[i] *= inv;
+      r[i] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (first + i < rows && (j * L + t) * VEC < D) {
+          float v[VEC];
+          xv[i][j].get(v);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) r[i] += (v[e] - m[i]) * (v[e] - m[i]);
+        }
+    }
+    sum(r);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (first + i >= rows) continue;
+      r[i] = rsqrtf(r[i] * inv + eps);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * L + t) * VEC;
+        if (c < D) {
+          float v[VEC];
+          xv[i][j].get(v);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[e] = (v[e] - m[i]) * r[i] * wv[j][e] + bv[j][e];
+          Vec<T, VEC>::store(y + (first + i) * D + c, v);
+        }
       }
-    const float m = sum(make_float2(s, 0.f)).x * inv;
-    s = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (live && (j * L + t) * VEC < D) {
-        float v[VEC];
-        xv[j].get(v);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) s += (v[e] - m) * (v[e] - m);
-      }
-    const float r = rsqrtf(sum(make_float2(s, 0.f)).x * inv + eps);
-    if (!live) continue;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * L + t) * VEC;
-      if (c < D) {
-        float v[VEC], wv[VEC], bv[VEC];
-        xv[j].get(v);
-        weights<VEC>(w, c, 1.f, wv);
-        weights<VEC>(b, c, 0.f, bv);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = (v[e] - m) * r * wv[e] + bv[e];
-        Vec<T, VEC>::store(y + row * D + c, v);
+      if (t == 0 && mean) {
+        mean[first + i] = m[i];
+        rstd[first + i] = r[i];
       }
     }
-    if (t == 0 && mean) {
-      mean[row] = m;
-      rstd[row] = r;
-    }
+    if (early(VEC, NV))
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < NV; ++j) xv[i][j] = next[i][j];
   }
 }
 
@@ -178,66 +222,90 @@ __global__ void __launch_bounds__(THREADS)
     layer_norm_bwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ mean,
                           const float *__restrict__ rstd, const T *__restrict__ dy, T *__restrict__ dx,
                           float *__restrict__ part, int64_t rows, int D, int64_t xs, int64_t ys, int lg) {
-  __shared__ float2 red[2][THREADS / 32];
+  constexpr int R = rows_of(VEC, NV);
+  __shared__ float red[2][THREADS / 32][2 * R];
   __shared__ float cols[MAX_COLS];
-  const int L = 1 << lg, t = threadIdx.x & (L - 1), per = THREADS >> lg;
-  RowSum sum{red, L, 0};
+  const int L = 1 << lg, t = threadIdx.x & (L - 1), per = (THREADS >> lg) * R;
+  RowSum<2 * R> sum{red, L, 0};
   const float inv = 1.f / (float)D;
-  float dw[NV][VEC], db[NV][VEC];
+  float wv[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
+  for (int j = 0; j < NV; ++j) {
+    if ((j * L + t) * VEC < D) weights<VEC>(w, (j * L + t) * VEC, 1.f, wv[j]);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
-  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += (int64_t)gridDim.x * per) {
-    const int64_t row = r0 + (threadIdx.x >> lg);
-    const bool live = row < rows;
-    Vec<T, VEC> xv[NV], gv[NV];
+  }
+  struct Rows {
+    Vec<T, VEC> x[R][NV], g[R][NV];
+    float m[R], r[R];
+  } cur, next;
+  auto fetch = [&](int64_t r0, Rows &f) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if (live && (j * L + t) * VEC < D) {
-        xv[j].load(x + row * xs + (j * L + t) * VEC);
-        gv[j].load(dy + row * ys + (j * L + t) * VEC);
-      }
-    const float m = live ? mean[row] : 0.f, r = live ? rstd[row] : 0.f;
-    float2 s = make_float2(0.f, 0.f);
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = r0 + (threadIdx.x >> lg) * R + i;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * L + t) * VEC;
-      if (live && c < D) {
-        float v[VEC], g[VEC], wv[VEC];
-        xv[j].get(v);
-        gv[j].get(g);
-        weights<VEC>(w, c, 1.f, wv);
+      for (int j = 0; j < NV; ++j)
+        if (row < rows && (j * L + t) * VEC < D) {
+          f.x[i][j].load(x + row * xs + (j * L + t) * VEC);
+          f.g[i][j].load(dy + row * ys + (j * L + t) * VEC);
+        }
+      f.m[i] = row < rows ? mean[row] : 0.f;
+      f.r[i] = row < rows ? rstd[row] : 0.f;
+    }
+  };
+  int64_t r0 = (int64_t)blockIdx.x * per;
+  const int64_t step = (int64_t)gridDim.x * per;
+  if (early(VEC, NV)) fetch(r0, cur);
+  for (; r0 < rows; r0 += step) {
+    if (early(VEC, NV))
+      fetch(r0 + step, next);
+    else
+      fetch(r0, cur);
+    const int64_t first = r0 + (threadIdx.x >> lg) * R;
+    float s[2 * R];
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float n = (v[e] - m) * r, a = g[e] * wv[e];
-          dw[j][e] += g[e] * n;
-          db[j][e] += g[e];
-          s.x += a;
-          s.y += a * n;
+    for (int i = 0; i < R; ++i) {
+      s[2 * i] = s[2 * i + 1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (first + i < rows && (j * L + t) * VEC < D) {
+          float v[VEC], g[VEC];
+          cur.x[i][j].get(v);
+          cur.g[i][j].get(g);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float n = (v[e] - cur.m[i]) * cur.r[i], a = g[e] * wv[j][e];
+            dw[j][e] += g[e] * n;
+            db[j][e] += g[e];
+            s[2 * i] += a;
+            s[2 * i + 1] += a * n;
+          }
+        }
+    }
+    sum(s);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float c1 = s[2 * i] * inv, c2 = s[2 * i + 1] * inv;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * L + t) * VEC;
+        if (first + i < rows && c < D) {
+          float v[VEC], g[VEC];
+          cur.x[i][j].get(v);
+          cur.g[i][j].get(g);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            v[e] = cur.r[i] * (g[e] * wv[j][e] - c1 - (v[e] - cur.m[i]) * cur.r[i] * c2);
+          Vec<T, VEC>::store(dx + (first + i) * D + c, v);
         }
       }
     }
-    s = sum(s);
-    if (!live) continue;
-    const float c1 = s.x * inv, c2 = s.y * inv;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int c = (j * L + t) * VEC;
-      if (c < D) {
-        float v[VEC], g[VEC], wv[VEC];
-        xv[j].get(v);
-        gv[j].get(g);
-        weights<VEC>(w, c, 1.f, wv);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[e] = r * (g[e] * wv[e] - c1 - (v[e] - m) * r * c2);
-        Vec<T, VEC>::store(dx + row * D + c, v);
-      }
-    }
+    if (early(VEC, NV)) cur = next;
   }
   // Column sums of the CTA: rows that share a warp by shuffles, then the
   // warps one after another (in warp order) through shared memory.
-  const int warp = threadIdx.x >> 5, turn = L > 32 ? threadIdx.x >> lg : warp, turns = L > 32 ? per : THREADS / 32;
+  const int warp = threadIdx.x >> 5, turn = L > 32 ? threadIdx.x >> lg : warp,
+            turns = L > 32 ? THREADS >> lg : THREADS / 32;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     float(&acc)[NV][VEC] = which ? db : dw;
@@ -378,7 +446,7 @@ __global__ void __launch_bounds__(THREADS)
 // How a row is spread over threads: L threads (2^lg), nv vectors each.
 struct Plan {
   int vec, nv, lg;
-  int64_t ctas;  // of one row per L threads
+  int64_t ctas;  // that cover the rows once
 };
 
 inline int log2_up(int64_t v) {
@@ -387,98 +455,91 @@ inline int log2_up(int64_t v) {
   return lg;
 }
 
-// vec values per vector (1 where 16-byte accesses are ruled out).  Up to 32
-// threads take one vector of the row each; a longer row gives them more, up
-// to max_nv, before it takes more threads: a warp that holds a whole row
-// needs no barrier.  Few rows are spread wider, so that the row's loads are
-// in flight from more threads.
-inline Plan plan_of(int64_t rows, int64_t D, int vec, int max_nv) {
+// vec values per vector (1 where 16-byte accesses are ruled out).  Up to 256
+// threads share a row, one vector each, before a thread takes several.
+inline Plan plan_of(int64_t rows, int64_t D, int vec) {
   const int64_t need = (D + vec - 1) / vec;
   Plan p;
   p.vec = vec;
-  p.nv = 1;
-  while (p.nv < max_nv && need > 32 * p.nv) p.nv *= 2;
+  p.nv = vec == 1 ? 4 : 1;
+  while (need > (int64_t)THREADS * p.nv) p.nv *= 2;
   p.lg = log2_up((need + p.nv - 1) / p.nv);
-  while (p.nv > (vec == 1 ? 4 : 1) && p.lg < 8 && rows << std::max(0, p.lg - 5) < 8 * tc::sm_count()) {
-    p.nv /= 2;
-    p.lg = log2_up((need + p.nv - 1) / p.nv);
-  }
-  if (vec == 1 && p.nv < 4) {
-    p.nv = 4;
-    p.lg = log2_up((need + 3) / 4);
-  }
-  p.ctas = (rows + (THREADS >> p.lg) - 1) / (THREADS >> p.lg);
+  const int64_t per = (int64_t)(THREADS >> p.lg) * rows_of(vec, p.nv);
+  p.ctas = (rows + per - 1) / per;
   return p;
+}
+
+// CTAs of a persistent launch: what fits at once (looked up once per kernel).
+template <typename K> int64_t resident(K kernel, std::atomic<int> &cache) {
+  int n = cache.load(std::memory_order_relaxed);
+  if (n <= 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, THREADS, 0) != cudaSuccess || n <= 0) n = 1;
+    cache.store(n, std::memory_order_relaxed);
+  }
+  return n * tc::sm_count();
 }
 
 inline bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// CTAs of the backward: enough warps to cover the memory latency, few enough
-// that the partial sums stay small.
+// CTAs of the backward, at most: few enough that the partial sums stay small.
 inline int64_t bwd_ctas(int64_t ctas) { return std::max<int64_t>(1, std::min<int64_t>(ctas, 2 * tc::sm_count())); }
 inline int64_t long_chunks(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, 64)); }
+
+// Calls f with the number of vectors as a constant: up to 8192 values per row
+// over 256 threads.
+template <int VEC, typename F> void pick(int nv, F f) {
+  if constexpr (VEC == 1) {
+    switch (nv) {
+      case 4: f(std::integral_constant<int, 4>()); break;
+      case 8: f(std::integral_constant<int, 8>()); break;
+      case 16: f(std::integral_constant<int, 16>()); break;
+      default: f(std::integral_constant<int, 32>()); break;
+    }
+  } else {
+    switch (nv) {
+      case 1: f(std::integral_constant<int, 1>()); break;
+      case 2: f(std::integral_constant<int, 2>()); break;
+      default:
+        if constexpr (VEC == 4) {
+          if (nv == 8) {
+            f(std::integral_constant<int, 8>());
+            break;
+          }
+        }
+        f(std::integral_constant<int, 4>());
+    }
+  }
+}
 
 template <typename T, int VEC>
 cudaError_t fwd(const Plan &p, const void *x, const float *w, const float *b, void *y, float *mean, float *rstd,
                 int64_t rows, int64_t D, int64_t xs, float eps, cudaStream_t st) {
-  const unsigned grid = (unsigned)std::min<int64_t>(p.ctas, 8 * tc::sm_count());
-#define GLACORE_LN(NV)                                                                                      \
-  layer_norm_fwd_kernel<T, VEC, NV><<<grid, THREADS, 0, st>>>((const T *)x, w, b, (T *)y, mean, rstd, rows, \
-                                                              (int)D, xs, p.lg, eps)
-  if constexpr (VEC == 1) {
-    switch (p.nv) {
-      case 4: GLACORE_LN(4); break;
-      case 8: GLACORE_LN(8); break;
-      case 16: GLACORE_LN(16); break;
-      default: GLACORE_LN(32); break;
-    }
-  } else {
-    switch (p.nv) {
-      case 1: GLACORE_LN(1); break;
-      case 2: GLACORE_LN(2); break;
-      case 4: GLACORE_LN(4); break;
-      default: GLACORE_LN(8); break;
-    }
-  }
-#undef GLACORE_LN
+  auto go = [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    static std::atomic<int> cache;
+    auto *k = layer_norm_fwd_kernel<T, VEC, NV>;
+    const unsigned grid = (unsigned)std::min<int64_t>(p.ctas, resident(k, cache));
+    k<<<grid, THREADS, 0, st>>>((const T *)x, w, b, (T *)y, mean, rstd, rows, (int)D, xs, p.lg, eps);
+  };
+  pick<VEC>(p.nv, go);
   return cudaGetLastError();
 }
 
 template <typename T, int VEC>
-cudaError_t bwd(const Plan &p, int64_t ctas, const void *x, const float *w, const float *mean, const float *rstd,
+cudaError_t bwd(const Plan &p, int64_t &ctas, const void *x, const float *w, const float *mean, const float *rstd,
                 const void *dy, void *dx, float *part, int64_t rows, int64_t D, int64_t xs, int64_t ys,
                 cudaStream_t st) {
-#define GLACORE_LN(NV)                                                                                     \
-  layer_norm_bwd_kernel<T, VEC, NV><<<(unsigned)ctas, THREADS, 0, st>>>(                                   \
-      (const T *)x, w, mean, rstd, (const T *)dy, (T *)dx, part, rows, (int)D, xs, ys, p.lg)
-  if constexpr (VEC == 1) {
-    switch (p.nv) {
-      case 4: GLACORE_LN(4); break;
-      case 8: GLACORE_LN(8); break;
-      case 16: GLACORE_LN(16); break;
-      default: GLACORE_LN(32); break;
-    }
-  } else if constexpr (VEC == 4) {
-    switch (p.nv) {
-      case 1: GLACORE_LN(1); break;
-      case 2: GLACORE_LN(2); break;
-      case 4: GLACORE_LN(4); break;
-      default: GLACORE_LN(8); break;
-    }
-  } else {
-    switch (p.nv) {
-      case 1: GLACORE_LN(1); break;
-      case 2: GLACORE_LN(2); break;
-      default: GLACORE_LN(4); break;
-    }
-  }
-#undef GLACORE_LN
+  auto go = [&](auto nv) {
+    constexpr int NV = decltype(nv)::value;
+    static std::atomic<int> cache;
+    auto *k = layer_norm_bwd_kernel<T, VEC, NV>;
+    ctas = std::min(bwd_ctas(p.ctas), resident(k, cache));
+    k<<<(unsigned)ctas, THREADS, 0, st>>>((const T *)x, w, mean, rstd, (const T *)dy, (T *)dx, part, rows, (int)D, xs,
+                                          ys, p.lg);
+  };
+  pick<VEC>(p.nv, go);
   return cudaGetLastError();
 }
-
-// Most vectors a thread holds: 64 values of a row in the forward (packed as
-// they lie in memory), 32 in the backward beside their two column sums.
-inline int max_nv(int vec, bool backward) { return vec == 1 ? 32 : (vec == 4 || !backward) ? 8 : 4; }
 
 inline bool sizes_ok(int64_t rows, int64_t D, int64_t xs, int32_t dtype) {
   return rows >= 0 && D >= 1 && D < ((int64_t)1 << 31) && (xs == 0 || xs >= D) &&
@@ -515,7 +576,7 @@ glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int
   } else {
     const int full = bf ? 8 : 4;
     const bool wide = D % full == 0 && xs % full == 0 && al16(x) && al16(y) && al16(w) && al16(b);
-    const Plan p = plan_of(rows, D, wide ? full : 1, max_nv(wide ? full : 1, false));
+    const Plan p = plan_of(rows, D, wide ? full : 1);
     if (bf)
       e = wide ? fwd<__nv_bfloat16, 8>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st)
                : fwd<__nv_bfloat16, 1>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st);
@@ -574,8 +635,7 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean, 
   } else {
     const int full = bf ? 8 : 4;
     const bool wide = D % full == 0 && xs % full == 0 && ys % full == 0 && al16(x) && al16(dy) && al16(dx) && al16(w);
-    const Plan p = plan_of(rows, D, wide ? full : 1, max_nv(wide ? full : 1, true));
-    n = bwd_ctas(p.ctas);
+    const Plan p = plan_of(rows, D, wide ? full : 1);
     if (bf)
       e = wide ? bwd<__nv_bfloat16, 8>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st)
                : bwd<__nv_bfloat16, 1>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st);

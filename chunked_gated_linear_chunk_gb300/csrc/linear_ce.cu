@@ -60,7 +60,8 @@ using tc::WAIT_CYCLES;
 constexpr int THREADS = 320, EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;
 constexpr int BM = 256, BK = 64;   // rows of a pair's tile, K of a stage
 constexpr uint32_t A_BYTES = 128 * BK * 2;
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 12;
+constexpr int STAGE_SMEM = 221184;  // shared memory of the ring, at most (a KB is left for its alignment)
 constexpr int GROUP_M = 8;         // row tiles that share a walk over the columns (L2 reuse)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
@@ -72,6 +73,7 @@ struct Gemm {
   int64_t m, n;
   int32_t a_mn;             // A stored with its M axis contiguous (B: always its K axis)
   int32_t mt, nt, kb;       // tiles, k-blocks
+  int32_t a_box, b_box;     // rows of a K-major operand's load (fewer than a CTA's share where there are no more)
   int32_t splits, kb_split; // K cut into `splits` runs of kb_split blocks
   // PRODUCT: where C (C^T if `trans`) goes.  out_f32: fp32, split s at
   // out + s * m * n, added to what is there if `add`; otherwise the tensors'
@@ -83,7 +85,7 @@ struct Gemm {
 struct Args {
   Gemm g[2];
   int64_t units0, units;  // units of g[0], of both
-  int32_t bn;
+  int32_t bn, stages;
   int64_t N, V, v0;  // tokens, vocabulary, first column of the piece
   const int64_t *target;
   float2 *part;      // STATS: [2 * nt][N] (maximum * log2 e, sum)
@@ -119,7 +121,10 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
   return t;
 }
 
-constexpr int stages_of(int parts) { return parts == 1 ? 6 : 3; }
+constexpr int stage_bytes_of(int parts, int bn) { return parts * (int)(A_BYTES + bn * BK); }
+constexpr int stages_of(int parts, int bn) {
+  return STAGE_SMEM / stage_bytes_of(parts, bn) < MAX_STAGES ? STAGE_SMEM / stage_bytes_of(parts, bn) : MAX_STAGES;
+}
 // k-blocks whose products one accumulator sums
 constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 4 : kind == STATS ? 16 : 1 << 30; }
 
@@ -127,9 +132,23 @@ constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 4 : kind == ST
 // one (bf16 operands: the only one).
 __device__ constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
 
+// Bytes of one k-block (and part) that CTA `rank` loads for a tile.  What lies
+// wholly past the end of M or N is not loaded (a load of nothing but fill
+// takes longer than one of data): the operand rows left over from another tile
+// only reach accumulator rows and columns that nobody reads.
+__device__ __forceinline__ uint32_t load_bytes(const Gemm &g, const Tile &t, int bn, int rank) {
+  const int64_t am = t.m0 + rank * 128, bn0 = t.n0 + rank * (bn / 2);
+  uint32_t n = bn0 < g.n ? (uint32_t)g.b_box * (BK * 2) : 0;
+  if (g.a_mn)
+    n += (am < g.m ? 8192 : 0) + (am + 64 < g.m ? 8192 : 0);
+  else
+    n += am < g.m ? (uint32_t)g.a_box * (BK * 2) : 0;
+  return n;
+}
+
 template <int KIND, int PARTS>
 __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_constant__ Args a) {
-  constexpr int STAGES = stages_of(PARTS), CHUNK = chunk_of(KIND, PARTS);
+  constexpr int CHUNK = chunk_of(KIND, PARTS);
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_ptr;
@@ -141,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < a.stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -162,41 +181,58 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   tc_fence_after();
   const uint32_t tmem = tmem_ptr;
 
+  // Everything the two issuing threads use per k-block is in registers: a
+  // parameter read again behind each of their asm statements costs them more
+  // than the products take.
+  const uint32_t full0 = smem_u32(full), empty0 = smem_u32(empty);
+  const int stages = a.stages;
   if (warp == TMA_WARP) {
     if (lane == 0) {
       // ---- tile loads of this CTA; bytes complete on the leader's barrier
-      bool ok = true;
-      int64_t it = 0;
+      bool ok = true, wrapped = false;
+      int s = 0;
+      uint32_t phase = 0;  // of the ring's current turn
+      const uint32_t bar0 = mapa_shared(full0, 0);
       for (int64_t u = pair; u < a.units && ok; u += pairs) {
         const Tile t = tile_of(a, u);
         const Gemm &g = a.g[t.which];
+        const CUtensorMap *ma = &g.a, *mb = &g.b;
         const int am = (int)(t.m0 + rank * 128), bn0 = (int)(t.n0 + rank * (a.bn / 2));
-        for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-          const int s = (int)(it % STAGES);
-          if (!mbar_wait_cluster(&empty[s], (uint32_t)(it / STAGES + 1) & 1, WAIT_CYCLES)) {
+        const bool a_mn = g.a_mn, a0 = am < g.m, a1 = am + 64 < g.m, b0 = bn0 < g.n;
+        const uint32_t bytes = PARTS * (load_bytes(g, t, a.bn, 0) + load_bytes(g, t, a.bn, 1));
+        int k = t.kb0 * BK;
+        for (int n = t.kb1 - t.kb0; n > 0; --n, k += BK) {
+          if (!mbar_wait_at(empty0 + 8 * s, phase ^ 1, WAIT_CYCLES)) {
             set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(&full[s], 2 * stage_bytes);
-          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_expect_tx_at(full0 + 8 * s, bytes);
+          const uint32_t bar = bar0 + 8 * s;
           const uint32_t sa = smem + s * stage_bytes, sb = sa + PARTS * A_BYTES;
-          const int k = kb * BK;
+#pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            if (g.a_mn) {
-              for (int i = 0; i < 2; ++i) tma_load_3d_pair(sa + p * A_BYTES + i * 8192, &g.a, am + 64 * i, k, p, bar);
-            } else {
-              tma_load_3d_pair(sa + p * A_BYTES, &g.a, k, am, p, bar);
+            if (a_mn) {
+              if (a0) tma_load_3d_pair(sa + p * A_BYTES, ma, am, k, p, bar);
+              if (a1) tma_load_3d_pair(sa + p * A_BYTES + 8192, ma, am + 64, k, p, bar);
+            } else if (a0) {
+              tma_load_3d_pair(sa + p * A_BYTES, ma, k, am, p, bar);
             }
-            tma_load_3d_pair(sb + p * b_bytes, &g.b, k, bn0, p, bar);
+            if (b0) tma_load_3d_pair(sb + p * b_bytes, mb, k, bn0, p, bar);
+          }
+          if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+            wrapped = true;
           }
         }
       }
       // every load has landed, and every release has arrived, before the CTA ends
-      for (int64_t i = it > STAGES ? it - STAGES : 0; i < it; ++i) {
-        const int s = (int)(i % STAGES);
-        if (rank == 0) mbar_wait_cluster(&full[s], (uint32_t)(i / STAGES) & 1, WAIT_CYCLES);
-        if (ok) ok = mbar_wait_cluster(&empty[s], (uint32_t)(i / STAGES) & 1, WAIT_CYCLES);
+      for (int i = 0; i < stages; ++i) {
+        if (i >= s && !wrapped) break;  // never used
+        const uint32_t used = i < s ? phase : phase ^ 1;
+        if (rank == 0) mbar_wait_at(full0 + 8 * i, used, WAIT_CYCLES);
+        if (ok) ok = mbar_wait_at(empty0 + 8 * i, used, WAIT_CYCLES);
       }
     }
     __syncwarp();
@@ -204,51 +240,60 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     if (lane == 0 && rank == 0) {
       // ---- products of the pair
       bool ok = true;
-      int64_t it = 0, hand = 0;
+      int s = 0;
+      uint32_t phase = 0;
+      uint32_t hand = 0;
+      const uint32_t acc_full0 = smem_u32(acc_full);
       for (int64_t u = pair; u < a.units && ok; u += pairs) {
         const Tile t = tile_of(a, u);
-        const Gemm &g = a.g[t.which];
-        const uint32_t idesc = idesc_bf16(BM, a.bn, g.a_mn, false);
-        const uint32_t astep = g.a_mn ? 2048 : 32;  // bytes between 16-element steps of K
-        for (int kb = t.kb0; kb < t.kb1 && ok;) {
-          const int buf = (int)(hand & 1);
-          if (!mbar_wait_cluster(&acc_empty[buf], (uint32_t)(hand / 2 + 1) & 1, WAIT_CYCLES)) {
+        const bool a_mn = a.g[t.which].a_mn;
+        const uint32_t idesc = idesc_bf16(BM, a.bn, a_mn, false);
+        const uint32_t astep = a_mn ? 2048 : 32;  // bytes between 16-element steps of K
+        const SDesc ad0 = sdesc_sw128(smem, a_mn ? 8192 : 16, 1024);
+        const SDesc bd0 = sdesc_sw128(smem + PARTS * A_BYTES, 16, 1024);
+        for (int left = t.kb1 - t.kb0; left > 0 && ok; ++hand) {
+          const uint32_t buf = hand & 1;
+          if (!mbar_wait_cluster(&acc_empty[buf], (hand / 2 + 1) & 1, WAIT_CYCLES)) {
             set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
           }
           tc_fence_after();
-          const int end = min(t.kb1 - kb, CHUNK) + kb, kfirst = kb;
-          for (; kb < end; ++kb, ++it) {
-            const int s = (int)(it % STAGES);
-            if (!mbar_wait_cluster(&full[s], (uint32_t)(it / STAGES) & 1, WAIT_CYCLES)) {
+          const int run = min(left, CHUNK);
+          left -= run;
+          uint32_t more = 0;  // the run's first products overwrite the accumulator
+          for (int n = run; n > 0; --n) {
+            if (!mbar_wait_at(full0 + 8 * s, phase, WAIT_CYCLES)) {
               set_device_error(a.err, GLACORE_ERR_TIMEOUT);
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = smem + s * stage_bytes, sb = sa + PARTS * A_BYTES;
+            const SDesc as = ad0 + s * stage_bytes, bs = bd0 + s * stage_bytes;
 #pragma unroll
             for (int i = PARTS == 1 ? 5 : 0; i < 6; ++i) {
               const bool large = i == 5;
               const uint32_t d = tmem + buf * 256 + (large ? 0 : 128);
-              const SDesc ad = sdesc_sw128(sa + (PARTS == 1 ? 0 : PA[i] * A_BYTES), g.a_mn ? 8192 : 16, 1024);
-              const SDesc bd = sdesc_sw128(sb + (PARTS == 1 ? 0 : PB[i] * b_bytes), 16, 1024);
+              const SDesc ad = as + (PARTS == 1 ? 0 : PA[i] * A_BYTES);
+              const SDesc bd = bs + (PARTS == 1 ? 0 : PB[i] * b_bytes);
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc,
-                              !(kb == kfirst && k == 0 && (large || i == 0)));
+                mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc, more | (uint32_t)(k > 0 || !(large || i == 0)));
             }
-            mma_commit_pair(&empty[s]);
+            more = 1;
+            mma_commit_pair(empty0 + 8 * s);
+            if (++s == stages) {
+              s = 0;
+              phase ^= 1;
+            }
           }
-          if (ok) mma_commit_pair(&acc_full[buf]);
-          ++hand;
+          if (ok) mma_commit_pair(acc_full0 + 8 * buf);
         }
       }
-      mma_commit_pair(&drained);
+      mma_commit_pair(smem_u32(&drained));
     }
     // the products in flight end before TMEM and the operands of either CTA go
-    if (lane == 0) mbar_wait_cluster(&drained, 0, WAIT_CYCLES);
+    if (lane == 0) mbar_wait_at(smem_u32(&drained), 0, WAIT_CYCLES);
     __syncwarp();
   } else {
     // ---- epilogue: thread = row, half = which half of the tile's columns
@@ -286,14 +331,14 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       auto use = [&](int c, float (&v)[32]) {
         const int64_t col = c0 + c;
         if constexpr (KIND == STATS) {
-          const int64_t room = a.V - col;  // columns of the vocabulary here
+          const int64_t room = min(a.V - col, (int64_t)(cols - c));  // columns of the vocabulary, of this warp here
           if (room <= 0) return;
           if (room < 32) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (i >= room) v[i] = -INFINITY;
           }
-          if (tgt >= col && tgt < col + 32) {
+          if (tgt >= col && tgt < col + room) {
             float z = 0.f;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -400,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         }
       };
       if constexpr (PARTS == 1) {
-        // sums of the chunks before the last (bn = 256: 128 columns)
+        // sums of the chunks so far (up to 128 columns)
         float acc[KIND == STATS ? 4 : 1][32];
 #pragma unroll
         for (int j = 0; j < (KIND == STATS ? 4 : 1); ++j)
@@ -408,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
         for (int kb = t.kb0; kb < t.kb1; kb += min(t.kb1 - kb, CHUNK), ++hand) {
           const int buf = (int)(hand & 1);
-          if (!mbar_wait_cluster(&acc_full[buf], (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
+          if (!mbar_wait_at(smem_u32(&acc_full[buf]), (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
             if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
@@ -417,6 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           const bool last = t.kb1 - kb <= CHUNK;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
+            if (32 * c >= cols) break;
             if constexpr (KIND == STATS) {
 #pragma unroll
               for (int j = 0; j < 32; j += 16) {  // few registers beside the sums
@@ -426,13 +472,13 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < 16; ++i) acc[c][i + j] += __uint_as_float(r[i]);
               }
-              if (c == 3) release(buf);
+              if (32 * c + 32 >= cols) release(buf);
               if (last) use(32 * c, acc[c]);
             } else {
               uint32_t r[32];
               tmem_ld32(lanes + buf * 256 + 32 * c, r);
               tmem_ld_wait32(r);
-              if (c == 3) release(buf);
+              if (32 * c + 32 >= cols) release(buf);
               float v[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
@@ -449,7 +495,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
         for (int kb = t.kb0; kb < t.kb1; kb += CHUNK, ++hand) {
           const int buf = (int)(hand & 1);
-          if (!mbar_wait_cluster(&acc_full[buf], (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
+          if (!mbar_wait_at(smem_u32(&acc_full[buf]), (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
             if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
@@ -486,9 +532,9 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   }
 }
 
-// lse and loss of 32 rows from the tiles' (maximum, sum) pairs: 8 threads per
-// row take every 8th pair, then merge in order.
-constexpr int MERGE_ROWS = 32, MERGE_LANES = 8;
+// lse and loss of 32 rows from the tiles' (maximum, sum) pairs: 32 threads per
+// row take every 32nd pair, then merge in order.
+constexpr int MERGE_ROWS = 32, MERGE_LANES = 32;
 __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
     ce_merge_kernel(const float2 *__restrict__ part, int64_t slots, int64_t N, int64_t V,
                     const int64_t *__restrict__ target, const float *__restrict__ zt, float *__restrict__ loss,
@@ -501,8 +547,17 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
     s = s * exp2f(m - ref) + p.y * exp2f(p.x - ref);
     m = top;
   };
-  if (row < N)
-    for (int64_t i = threadIdx.y; i < slots; i += MERGE_LANES) merge(part[i * N + row]);
+  if (row < N) {
+    int64_t i = threadIdx.y;
+    for (; i + 3 * MERGE_LANES < slots; i += 4 * MERGE_LANES) {
+      float2 p[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = part[(i + k * MERGE_LANES) * N + row];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) merge(p[k]);
+    }
+    for (; i < slots; i += MERGE_LANES) merge(part[i * N + row]);
+  }
   red[threadIdx.y][threadIdx.x] = make_float2(m, s);
   __syncthreads();
   if (threadIdx.y || row >= N) return;
@@ -590,21 +645,20 @@ template <int PARTS, typename T>
 __global__ void __launch_bounds__(256)
     ce_pack_kernel(const T *__restrict__ src, int64_t rows, int64_t D, int64_t stride, int64_t pitch,
                    __nv_bfloat16 *__restrict__ dst) {
-  const int64_t n = rows * D;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / D, c = i - r * D;
-    if constexpr (PARTS == 1) {
-      dst[r * pitch + c] = src[r * stride + c];
-    } else {
-      float x = src[r * stride + c];
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = threadIdx.x; c < D; c += 256) {
+      if constexpr (PARTS == 1) {
+        dst[r * pitch + c] = src[r * stride + c];
+      } else {
+        float x = src[r * stride + c];
 #pragma unroll
-      for (int p = 0; p < PARTS; ++p) {
-        const float hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-        dst[(p * rows + r) * pitch + c] = __float2bfloat16_rn(hi);
-        x = isinf(hi) ? 0.f : x - hi;  // an infinity stays one, in the first part
+        for (int p = 0; p < PARTS; ++p) {
+          const float hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+          dst[(p * rows + r) * pitch + c] = __float2bfloat16_rn(hi);
+          x = isinf(hi) ? 0.f : x - hi;  // an infinity stays one, in the first part
+        }
       }
     }
-  }
 }
 
 // ---- host ------------------------------------------------------------------
@@ -616,7 +670,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Layout {
-  int parts, bn;
+  int parts, bn, bn_z;               // bn_z: tile width of the logits
   bool pack;                         // x and w are copied to rows TMA can address
   int64_t pitch, xt_pitch, piece, pieces, gpitch;
   int splits, run;  // dx's K axis: `splits` runs of `run` k-blocks (in the first, longest piece)
@@ -634,7 +688,7 @@ int64_t pair_count() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tc::sm_count() / 2 * 2));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = stages_of(1) * 2 * A_BYTES + 1024;
+    cfg.dynamicSmemBytes = STAGE_SMEM + 1024;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -681,6 +735,21 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
   memset(&L, 0, sizeof(L));
   L.parts = dtype == GLACORE_F32 ? 3 : 1;
   L.bn = L.parts == 3 ? 128 : 256;
+  L.bn_z = L.bn;
+  if (!backward && L.parts == 1) {
+    // The width that deals the vocabulary out most evenly: the fewest columns
+    // for the busiest pair, and about 32 columns' time for a tile's start and
+    // end.  It matters for few tokens, where the call is bound by reading w
+    // once (16 x 2048 x 32000: 36.4 us with 256, 34.8 us with 224).
+    int64_t least = -1;
+    for (int bn = 256; bn >= 128; bn -= 32) {
+      const int64_t cost = up(up(N, BM) * up(V, bn), pair_count()) * (bn + 32);
+      if (least < 0 || cost < least) {
+        least = cost;
+        L.bn_z = bn;
+      }
+    }
+  }
   L.pack = L.parts == 3 || D % 8 != 0;
   L.pitch = up(D, 8) * 8;
   size_t off = 0;
@@ -693,7 +762,7 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     take(L.off_w, (size_t)L.parts * V * L.pitch * 2);
   }
   if (!backward) {
-    take(L.off_part, (size_t)up(V, L.bn) * 2 * N * sizeof(float2));
+    take(L.off_part, (size_t)up(V, L.bn_z) * 2 * N * sizeof(float2));
     take(L.off_zt, (size_t)N * sizeof(float));
   } else {
     const int64_t most = std::max<int64_t>(2048, (int64_t)(G_BYTES / (2 * L.parts * (size_t)N)) / 256 * 256);
@@ -733,7 +802,7 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
-  const int smem = stages_of(PARTS) * PARTS * (int)(A_BYTES + a.bn * BK) + 1024;
+  const int smem = a.stages * stage_bytes_of(PARTS, a.bn) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -753,7 +822,12 @@ template <int KIND> cudaError_t launch(const Args &a, int parts, cudaStream_t st
   return parts == 3 ? launch<KIND, 3>(a, st) : launch<KIND, 1>(a, st);
 }
 
+// Rows of a K-major operand's load: a CTA's share, or what there is of it.
+int box_of(int64_t rows, int share) { return (int)std::min<int64_t>(share, up(rows, 8) * 8); }
+
 void whole_k(Gemm &g, int64_t m, int64_t n, int64_t k, int bn) {
+  g.a_box = box_of(m, 128);
+  g.b_box = box_of(n, bn / 2);
   g.m = m;
   g.n = n;
   g.mt = (int32_t)up(m, BM);
@@ -774,7 +848,7 @@ cudaError_t rows_of(const Layout &L, const void *x, int64_t xs, const void *w, i
     return cudaSuccess;
   }
   auto pack = [&](const void *src, int64_t rows, int64_t stride, size_t off) {
-    const unsigned grid = (unsigned)std::min<int64_t>(up(rows * D, 256), 16 * tc::sm_count());
+    const unsigned grid = (unsigned)std::min<int64_t>(rows, 32 * tc::sm_count());
     __nv_bfloat16 *dst = (__nv_bfloat16 *)(ws + off);
     if (L.parts == 3)
       ce_pack_kernel<3, float><<<grid, 256, 0, st>>>((const float *)src, rows, D, stride, L.pitch, dst);
@@ -833,11 +907,13 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   Args a;
   memset(&a, 0, sizeof(a));
   Gemm &g = a.g[0];
-  if (!make_map3(&g.a, r.x, D, N, L.parts, r.xp, N, 128) || !make_map3(&g.b, r.w, D, V, L.parts, r.wp, V, L.bn / 2))
+  if (!make_map3(&g.a, r.x, D, N, L.parts, r.xp, N, box_of(N, 128)) ||
+      !make_map3(&g.b, r.w, D, V, L.parts, r.wp, V, box_of(V, L.bn_z / 2)))
     return status_of(cudaErrorInvalidValue);
-  whole_k(g, N, V, D, L.bn);
+  whole_k(g, N, V, D, L.bn_z);
   a.units0 = a.units = (int64_t)g.mt * g.nt;
-  a.bn = L.bn;
+  a.bn = L.bn_z;
+  a.stages = stages_of(L.parts, a.bn);
   a.N = N;
   a.V = V;
   a.target = target;
@@ -847,8 +923,7 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   e = ce::launch<STATS>(a, L.parts, st);
   mark_launch("ce_stats", st);
   if (e != cudaSuccess) return status_of(e);
-  // pairs of column halves that hold part of the vocabulary
-  const int64_t slots = up(V, L.bn / 2);
+  const int64_t slots = up(V, L.bn_z / 2);  // tile halves that hold part of the vocabulary
   ce_merge_kernel<<<(unsigned)up(N, MERGE_ROWS), dim3(MERGE_ROWS, MERGE_LANES), 0, st>>>(a.part, slots, N, V, target,
                                                                                        a.zt, loss, lse, a.err);
   mark_launch("ce_merge", st);
@@ -895,7 +970,8 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     const char *wp = (const char *)r.w + (size_t)v0 * r.wp * 2;
     Args a;
     memset(&a, 0, sizeof(a));
-    a.bn = L.bn;
+    a.bn = L.bn_z;
+    a.stages = stages_of(L.parts, a.bn);
     a.N = N;
     a.V = V;
     a.v0 = v0;
@@ -912,17 +988,19 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     auto g_map = [&](CUtensorMap *m, int box_rows) {
       return make_map3(m, ws + L.off_g, cols, N, L.parts, L.gpitch, N, box_rows);
     };
-    if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, 128) || !w_map(&a.g[0].b, L.bn / 2))
+    if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, box_of(N, 128)) || !w_map(&a.g[0].b, box_of(cols, L.bn_z / 2)))
       return status_of(cudaErrorInvalidValue);
-    whole_k(a.g[0], N, cols, D, L.bn);
+    whole_k(a.g[0], N, cols, D, L.bn_z);
     a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
     e = ce::launch<GRAD>(a, L.parts, st);
     mark_launch("ce_grad", st);
     if (e != cudaSuccess) return status_of(e);
     // dx^T (K = the piece) and dw of the piece (K = the tokens)
+    a.bn = L.bn;
+    a.stages = stages_of(L.parts, a.bn);
     Gemm &gx = a.g[0], &gw = a.g[1];
-    if (!w_map(&gx.a, 64) || !g_map(&gx.b, L.bn / 2) || !g_map(&gw.a, 64) ||
-        !make_map3(&gw.b, xt, N, D, L.parts, L.xt_pitch, D, L.bn / 2))
+    if (!w_map(&gx.a, 64) || !g_map(&gx.b, box_of(N, L.bn / 2)) || !g_map(&gw.a, 64) ||
+        !make_map3(&gw.b, xt, N, D, L.parts, L.xt_pitch, D, box_of(D, L.bn / 2)))
       return status_of(cudaErrorInvalidValue);
     whole_k(gx, D, N, cols, L.bn);
     gx.a_mn = 1;

@@ -52,7 +52,7 @@ __device__ __forceinline__ void store(void *p, int bf16, int64_t i, float x) {
 // COLT threads side by side cover 4 COLT value columns; VEC: V is a multiple
 // of 4 and the pool 16-byte aligned.
 template <int COLT, int KR, bool VEC>
-__global__ void __launch_bounds__(THREADS) step_kernel(const Args a) {
+__global__ void __launch_bounds__(THREADS, KR <= 8 ? 4 : 2) step_kernel(const Args a) {
   constexpr int ROWT = THREADS / COLT, COLS = 4 * COLT;
   __shared__ float s_q[TOKENS][ROWT * KR], s_k[TOKENS][ROWT * KR], s_a[TOKENS][ROWT * KR];
   __shared__ float s_v[TOKENS][COLS];

@@ -42,12 +42,34 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, SDesc a, SDesc b,
 }
 // Arrives once on the barrier at this shared-memory offset in both CTAs when
 // every product issued so far by this thread has completed.
-__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          smem_u32(bar)),
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
+}
+// Barriers by shared address, for loops that keep their addresses in
+// registers.  The wait is bounded as mbar_wait's; the clock is read only once
+// the first try has failed.
+__device__ __forceinline__ void mbar_expect_tx_at(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"((uint32_t)GLACORE_WAIT_HINT_NS)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, long long max_cycles) {
+  if (mbar_try_wait_at(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait_at(bar, parity))
+    if (clock64() - t0 > max_cycles) return false;
+  return true;
 }
 // 2^x, flushing subnormal results.
 __device__ __forceinline__ float ex2(float x) {
