@@ -5,20 +5,22 @@
 //   backward, a = dy w:
 //     dx = r (a - mean(a) - n mean(a n)),  dw = sum_rows dy n,  db = sum_rows dy
 //
-// HBM-bound: the forward moves 2, the backward 3 rows of D values per token
-// and nothing is read twice.  A row lives in the registers of L threads
-// (column vectors t, t + L, ... of 16 bytes for thread t), so the mean and the
-// squared deviations from it are two exact passes over registers.  A thread
-// keeps its columns for the whole kernel: their weights and the column sums of
-// the weight gradients stay in its registers (read for every row instead, w
-// and b took the L1 more time than the rows took the memory: 8192 x 2048 bf16
-// forward 22.5 us).  It takes up to two rows at a time and loads the next ones
-// before it reduces these.  L <= 32 threads exchange sums by shuffles alone, L
-// = 64 .. 256 through shared memory and a barrier of the row's own warps.
-// Rows of more than MAX_COLS values are walked in a loop by a whole CTA
-// instead.  All arithmetic is fp32; bf16 outputs are rounded once.  The weight
-// gradients are deterministic: per-CTA partial sums in the workspace, then one
-// kernel that adds the partial rows in a fixed order.
+// HBM-bound, with the instruction issue close behind: the forward moves 2, the
+// backward 3 rows of D values per token and nothing is read twice.  A row
+// lives in the registers of L threads (column vectors t, t + L, ... of 16
+// bytes for thread t), so the mean and the squared deviations from it are two
+// exact passes over registers; the next row is loaded before this one is
+// reduced.  A sum over a row's threads costs some 30 instructions each, so a
+// thread holds as many values of a row as registers allow: in the forward up
+// to 64 (a warp holds a row of 2048 bf16 and needs no barrier; the weights
+// wait in shared memory), in the backward 16 to 32 beside the column sums of
+// the two weight gradients, with a barrier of the row's own warps.  (8 values
+// per thread ran the forward at 77% of all issue slots and 28% of the DRAM
+// rate.)  The arithmetic is fp32, two values per instruction; bf16 outputs are
+// rounded once.  Rows of more than MAX_COLS values are walked in a loop by a
+// whole CTA instead.  The weight gradients are deterministic: per-CTA partial
+// sums in the workspace, then one kernel that adds the partial rows in a fixed
+// order.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -75,6 +77,67 @@ template <typename T> struct Vec<T, 1> {
   static __device__ __forceinline__ void store(T *p, const float (&v)[1]) { *p = from_f32<T>(v[0]); }
 };
 
+// Two fp32 operations per instruction.
+__device__ __forceinline__ void fma2(float &x, float &y, float ax, float ay, float bx, float by, float cx, float cy) {
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by), "f"(cx), "f"(cy));
+}
+__device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "f"(ax), "f"(ay), "f"(x), "f"(y));
+}
+__device__ __forceinline__ void mul2(float &x, float &y, float ax, float ay, float bx, float by) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+// The same over N values: o = a b + c, o += a, o = a b (b and c may be one
+// number for all).
+struct All {
+  float v;
+  __device__ __forceinline__ float operator[](int) const { return v; }
+};
+template <int N, typename B, typename C>
+__device__ __forceinline__ void vfma(float (&o)[N], const float (&a)[N], const B &b, const C &c) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) fma2(o[i], o[i + 1], a[i], a[i + 1], b[i], b[i + 1], c[i], c[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = fmaf(a[i], b[i], c[i]);
+  }
+}
+template <int N> __device__ __forceinline__ void vadd(float (&o)[N], const float (&a)[N]) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) add2(o[i], o[i + 1], a[i], a[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] += a[i];
+  }
+}
+template <int N, typename B>
+__device__ __forceinline__ void vmul(float (&o)[N], const float (&a)[N], const B &b) {
+  if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) mul2(o[i], o[i + 1], a[i], a[i + 1], b[i], b[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = a[i] * b[i];
+  }
+}
+template <int N> __device__ __forceinline__ float total(const float (&a)[N]) {
+  float s = a[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) s += a[i];
+  return s;
+}
+
 // VEC consecutive weights (null: all `otherwise`).
 template <int VEC>
 __device__ __forceinline__ void weights(const float *w, int64_t c, float otherwise, float (&v)[VEC]) {
@@ -90,6 +153,24 @@ __device__ __forceinline__ void weights(const float *w, int64_t c, float otherwi
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) v[e] = __ldg(w + c + e);
+  }
+}
+
+// Shared-memory copy of D weights, 16-byte accesses of a warp free of bank
+// conflicts: of 8 consecutive weights the first four lie in one half of the
+// copy, the others in the other.
+template <int VEC> __device__ __forceinline__ int staged_at(int c, int D) {
+  return VEC == 8 ? ((c >> 2) & 1) * (D / 2) + (c >> 3) * 4 + (c & 3) : c;
+}
+template <int VEC> __device__ __forceinline__ void staged(const float *s, int c, int D, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = s[c];
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; e += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(s + staged_at<VEC>(c + e, D));
+      v[e] = f.x; v[e + 1] = f.y; v[e + 2] = f.z; v[e + 3] = f.w;
+    }
   }
 }
 
@@ -110,121 +191,147 @@ template <int N> struct RowSum {
         for (int i = 0; i < N; ++i) red[buf][warp][i] = v[i];
       asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / wpr), "r"(L) : "memory");
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = 0.f;
-      for (int k = 0; k < wpr; ++k)
+      for (int i = 0; i < N; ++i) v[i] = red[buf][first][i];
+      for (int k = 1; k < wpr; ++k)
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += red[buf][first + k][i];
       buf ^= 1;
     }
   }
+  __device__ __forceinline__ float operator()(float x) {
+    float v[1] = {x};
+    (*this)(v);
+    return v[0];
+  }
 };
 
-// Rows a thread takes at a time, and whether the next ones are loaded early:
-// as far as registers allow.
-constexpr int rows_of(int vec, int nv) { return vec * nv <= 8 ? 2 : 1; }
-constexpr bool early(int vec, int nv) { return vec * nv * rows_of(vec, nv) <= 16; }
+// Whether the forward loads a row's successor early: where registers allow.
+constexpr bool early(int bytes) { return bytes <= 128; }
 
-template <typename T, int VEC, int NV>
+// STAGED: w and b go through shared memory (worth it where a CTA takes several
+// rows).
+template <typename T, int VEC, int NV, bool STAGED>
 __global__ void __launch_bounds__(THREADS)
     layer_norm_fwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ b,
                           T *__restrict__ y, float *__restrict__ mean, float *__restrict__ rstd, int64_t rows, int D,
                           int64_t xs, int lg, float eps) {
-  constexpr int R = rows_of(VEC, NV);
-  __shared__ float red[2][THREADS / 32][R];
-  const int L = 1 << lg, t = threadIdx.x & (L - 1), per = (THREADS >> lg) * R;
-  RowSum<R> sum{red, L, 0};
+  constexpr bool EARLY = STAGED && early(NV * VEC * (int)sizeof(T));
+  extern __shared__ float4 smem[];
+  __shared__ float red[2][THREADS / 32][1];
+  const int L = 1 << lg, t = threadIdx.x & (L - 1), per = THREADS >> lg;
+  RowSum<1> sum{red, L, 0};
   const float inv = 1.f / (float)D;
-  float wv[NV][VEC], bv[NV][VEC];
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if ((j * L + t) * VEC < D) {
-      weights<VEC>(w, (j * L + t) * VEC, 1.f, wv[j]);
-      weights<VEC>(b, (j * L + t) * VEC, 0.f, bv[j]);
+  float *sw = reinterpret_cast<float *>(smem), *sb = sw + (D + 3) / 4 * 4;
+  if (STAGED) {
+    for (int c = threadIdx.x; c < D; c += THREADS) {
+      sw[staged_at<VEC>(c, D)] = w ? w[c] : 1.f;
+      sb[staged_at<VEC>(c, D)] = b ? b[c] : 0.f;
     }
-  Vec<T, VEC> xv[R][NV], next[R][NV];
-  auto fetch = [&](int64_t r0, Vec<T, VEC>(&v)[R][NV]) {
+    __syncthreads();
+  }
+  Vec<T, VEC> xv[NV], next[NV];
+  auto fetch = [&](int64_t row, Vec<T, VEC>(&v)[NV]) {
+    if (row >= rows) return;
+    const T *p = x + row * xs + t * VEC;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t row = r0 + (threadIdx.x >> lg) * R + i;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (row < rows && (j * L + t) * VEC < D) v[i][j].load(x + row * xs + (j * L + t) * VEC);
-    }
+    for (int j = 0; j < NV; ++j)
+      if ((j * L + t) * VEC < D) v[j].load(p + j * L * VEC);
   };
-  int64_t r0 = (int64_t)blockIdx.x * per;
+  int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> lg);
   const int64_t step = (int64_t)gridDim.x * per;
-  if (early(VEC, NV)) fetch(r0, xv);
-  for (; r0 < rows; r0 += step) {
-    if (early(VEC, NV))
-      fetch(r0 + step, next);
+  if (EARLY) fetch(row, xv);
+  // every thread of the CTA turns as often as its first row group (barriers)
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step) {
+    if (EARLY)
+      fetch(row + step, next);
     else
-      fetch(r0, xv);
-    const int64_t first = r0 + (threadIdx.x >> lg) * R;
-    float m[R], r[R];
+      fetch(row, xv);
+    const bool live = row < rows;
+    float acc[VEC];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      m[i] = 0.f;
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (first + i < rows && (j * L + t) * VEC < D) {
-          float v[VEC];
-          xv[i][j].get(v);
+    for (int j = 0; j < NV; ++j)
+      if (live && (j * L + t) * VEC < D) {
+        float v[VEC];
+        xv[j].get(v);
+        vadd(acc, v);
+      }
+    const float m = sum(total(acc)) * inv;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) m[i] += v[e];
-        }
-    }
-    sum(m);
+    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      m[i] *= inv;
-      r[i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (first + i < rows && (j * L + t) * VEC < D) {
-          float v[VEC];
-          xv[i][j].get(v);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) r[i] += (v[e] - m[i]) * (v[e] - m[i]);
-        }
-    }
-    sum(r);
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      if (first + i >= rows) continue;
-      r[i] = rsqrtf(r[i] * inv + eps);
+    for (int j = 0; j < NV; ++j)
+      if (live && (j * L + t) * VEC < D) {
+        float v[VEC], d[VEC];
+        xv[j].get(v);
+        vfma(d, v, All{1.f}, All{-m});
+        vfma(acc, d, d, acc);
+      }
+    const float r = rsqrtf(sum(total(acc)) * inv + eps);
+    if (live) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * L + t) * VEC;
         if (c < D) {
-          float v[VEC];
-          xv[i][j].get(v);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[e] = (v[e] - m[i]) * r[i] * wv[j][e] + bv[j][e];
-          Vec<T, VEC>::store(y + (first + i) * D + c, v);
+          float v[VEC], wv[VEC], bv[VEC];
+          xv[j].get(v);
+          if (STAGED) {
+            staged<VEC>(sw, c, D, wv);
+            staged<VEC>(sb, c, D, bv);
+          } else {
+            weights<VEC>(w, c, 1.f, wv);
+            weights<VEC>(b, c, 0.f, bv);
+          }
+          // the difference first: exact for x near m, however far off centre
+          vfma(v, v, All{1.f}, All{-m});
+          vmul(v, v, All{r});
+          vfma(v, v, wv, bv);
+          Vec<T, VEC>::store(y + row * D + c, v);
         }
       }
       if (t == 0 && mean) {
-        mean[first + i] = m[i];
-        rstd[first + i] = r[i];
+        mean[row] = m;
+        rstd[row] = r;
       }
     }
-    if (early(VEC, NV))
+    if (EARLY)
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < NV; ++j) xv[i][j] = next[i][j];
+      for (int j = 0; j < NV; ++j) xv[j] = next[j];
   }
 }
 
+// Copy of BYTES (4 or 16) to shared memory, in flight until its group is
+// waited for.
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(d), "l"(src) : "memory");
+}
+
+// The backward takes two rows at a time (one exchange of sums for both), and
+// copies them to shared memory AHEAD turns before theirs, each thread its own
+// columns (no barrier: a thread reads only what it copied).  In registers the
+// rows in flight would have to share the space with the column sums: 8192 x
+// 2048 bf16 ran with 32 KB in flight per SM and 35 us.  Rows of bf16 on odd
+// addresses cannot be copied so (4 bytes at least) and are read in place,
+// twice.
+constexpr int AHEAD = 2, SLOTS = AHEAD + 1;
+constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }  // by a thread's values of a row (shared memory)
+
 // part: [gridDim.x][2][D] partial dw, db of the rows each CTA walked.
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 2)
     layer_norm_bwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ mean,
                           const float *__restrict__ rstd, const T *__restrict__ dy, T *__restrict__ dx,
                           float *__restrict__ part, int64_t rows, int D, int64_t xs, int64_t ys, int lg) {
-  constexpr int R = rows_of(VEC, NV);
+  constexpr int BYTES = VEC * (int)sizeof(T);
+  constexpr bool ASYNC = BYTES >= 4;
+  constexpr int R = rows_at_once(NV * VEC);
+  extern __shared__ float4 smem[];
   __shared__ float red[2][THREADS / 32][2 * R];
-  __shared__ float cols[MAX_COLS];
   const int L = 1 << lg, t = threadIdx.x & (L - 1), per = (THREADS >> lg) * R;
   RowSum<2 * R> sum{red, L, 0};
   const float inv = 1.f / (float)D;
@@ -235,73 +342,108 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
   }
-  struct Rows {
-    Vec<T, VEC> x[R][NV], g[R][NV];
-    float m[R], r[R];
-  } cur, next;
-  auto fetch = [&](int64_t r0, Rows &f) {
+  // this thread's columns of its row group's slots: x, dy of each of R rows
+  const int pitch = (D * (int)sizeof(T) + 15) / 16 * 16;
+  char *slots = reinterpret_cast<char *>(smem) + (int64_t)(threadIdx.x >> lg) * SLOTS * R * 2 * pitch + t * BYTES;
+  auto fetch = [&](int64_t row, int slot) {
+    if constexpr (ASYNC) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t row = r0 + (threadIdx.x >> lg) * R + i;
+      for (int i = 0; i < R; ++i)
+        if (row + i < rows) {
+          const T *px = x + (row + i) * xs + t * VEC, *pg = dy + (row + i) * ys + t * VEC;
+          char *to = slots + (slot * R + i) * 2 * pitch;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (row < rows && (j * L + t) * VEC < D) {
-          f.x[i][j].load(x + row * xs + (j * L + t) * VEC);
-          f.g[i][j].load(dy + row * ys + (j * L + t) * VEC);
+          for (int j = 0; j < NV; ++j)
+            if ((j * L + t) * VEC < D) {
+              copy_async<BYTES>(to + j * L * BYTES, px + j * L * VEC);
+              copy_async<BYTES>(to + pitch + j * L * BYTES, pg + j * L * VEC);
+            }
         }
-      f.m[i] = row < rows ? mean[row] : 0.f;
-      f.r[i] = row < rows ? rstd[row] : 0.f;
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
   };
-  int64_t r0 = (int64_t)blockIdx.x * per;
+  int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> lg) * R;
   const int64_t step = (int64_t)gridDim.x * per;
-  if (early(VEC, NV)) fetch(r0, cur);
-  for (; r0 < rows; r0 += step) {
-    if (early(VEC, NV))
-      fetch(r0 + step, next);
-    else
-      fetch(r0, cur);
-    const int64_t first = r0 + (threadIdx.x >> lg) * R;
-    float s[2 * R];
+  float m_next[R], r_next[R];
+  auto stats = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (row + i < rows) {
+        m_next[i] = mean[row + i];
+        r_next[i] = rstd[row + i];
+      }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) fetch(row + i * step, i);
+  stats(row);
+  int slot = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step) {
+    fetch(row + AHEAD * step, slot == 0 ? SLOTS - 1 : slot - 1);
+    if (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+    float m[R], r[R], s[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      s[2 * i] = s[2 * i + 1] = 0.f;
+      m[i] = m_next[i];
+      r[i] = r_next[i];
+    }
+    stats(row + step);
+    auto get = [&](int i, int j, float(&v)[VEC], float(&g)[VEC]) {  // columns j of x and dy of row i
+      Vec<T, VEC> vx, vg;
+      if constexpr (ASYNC) {
+        const char *from = slots + (slot * R + i) * 2 * pitch + j * L * BYTES;
+        vx.load(reinterpret_cast<const T *>(from));
+        vg.load(reinterpret_cast<const T *>(from + pitch));
+      } else {
+        vx.load(x + (row + i) * xs + (j * L + t) * VEC);
+        vg.load(dy + (row + i) * ys + (j * L + t) * VEC);
+      }
+      vx.get(v);
+      vg.get(g);
+    };
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (first + i < rows && (j * L + t) * VEC < D) {
-          float v[VEC], g[VEC];
-          cur.x[i][j].get(v);
-          cur.g[i][j].get(g);
+    for (int i = 0; i < R; ++i) {
+      float s0[VEC], s1[VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float n = (v[e] - cur.m[i]) * cur.r[i], a = g[e] * wv[j][e];
-            dw[j][e] += g[e] * n;
-            db[j][e] += g[e];
-            s[2 * i] += a;
-            s[2 * i + 1] += a * n;
+      for (int e = 0; e < VEC; ++e) s0[e] = s1[e] = 0.f;
+      if (row + i < rows)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+          if ((j * L + t) * VEC < D) {
+            float n[VEC], g[VEC], a[VEC];
+            get(i, j, n, g);
+            vfma(n, n, All{1.f}, All{-m[i]});  // as in the forward
+            vmul(n, n, All{r[i]});
+            vmul(a, g, wv[j]);
+            vfma(dw[j], g, n, dw[j]);
+            vadd(db[j], g);
+            vadd(s0, a);
+            vfma(s1, a, n, s1);
           }
-        }
+      s[2 * i] = total(s0);
+      s[2 * i + 1] = total(s1);
     }
     sum(s);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const float c1 = s[2 * i] * inv, c2 = s[2 * i + 1] * inv;
+      if (row + i >= rows) continue;
+      // dx = r a - r mean(a) - r mean(a n) n = r a + kx x + k1
+      const float kn = -s[2 * i + 1] * inv * r[i], kx = kn * r[i], k1 = -s[2 * i] * inv * r[i] - kx * m[i];
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * L + t) * VEC;
-        if (first + i < rows && c < D) {
+        if (c < D) {
           float v[VEC], g[VEC];
-          cur.x[i][j].get(v);
-          cur.g[i][j].get(g);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e)
-            v[e] = cur.r[i] * (g[e] * wv[j][e] - c1 - (v[e] - cur.m[i]) * cur.r[i] * c2);
-          Vec<T, VEC>::store(dx + (first + i) * D + c, v);
+          get(i, j, v, g);
+          vmul(g, g, wv[j]);
+          vfma(v, v, All{kx}, All{k1});
+          vfma(v, g, All{r[i]}, v);
+          Vec<T, VEC>::store(dx + (row + i) * D + c, v);
         }
       }
     }
-    if (early(VEC, NV)) cur = next;
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
   }
+  float *cols = reinterpret_cast<float *>(smem);  // the slots are done with
   // Column sums of the CTA: rows that share a warp by shuffles, then the
   // warps one after another (in warp order) through shared memory.
   const int warp = threadIdx.x >> 5, turn = L > 32 ? threadIdx.x >> lg : warp,
@@ -455,39 +597,50 @@ inline int log2_up(int64_t v) {
   return lg;
 }
 
-// vec values per vector (1 where 16-byte accesses are ruled out).  Up to 256
-// threads share a row, one vector each, before a thread takes several.
-inline Plan plan_of(int64_t rows, int64_t D, int vec) {
+// vec values per vector (1 where 16-byte accesses are ruled out).  A thread
+// takes up to `most` values of a row before the row takes more threads than a
+// warp, and more than that only where 256 threads do not hold the row.  Few
+// rows are spread wider, so that more threads have loads in flight.
+inline Plan plan_of(int64_t rows, int64_t D, int vec, int most) {
   const int64_t need = (D + vec - 1) / vec;
+  const int least = vec == 1 ? 4 : 1;
   Plan p;
   p.vec = vec;
-  p.nv = vec == 1 ? 4 : 1;
+  p.nv = least;
+  while (p.nv * vec < most && need > 32 * p.nv) p.nv *= 2;
+  while (p.nv > least && need <= (int64_t)THREADS * p.nv / 2 &&
+         rows * ((need + 32 * p.nv - 1) / (32 * p.nv)) < 8 * tc::sm_count())
+    p.nv /= 2;
   while (need > (int64_t)THREADS * p.nv) p.nv *= 2;
   p.lg = log2_up((need + p.nv - 1) / p.nv);
-  const int64_t per = (int64_t)(THREADS >> p.lg) * rows_of(vec, p.nv);
-  p.ctas = (rows + per - 1) / per;
+  p.ctas = (rows + (THREADS >> p.lg) - 1) / (THREADS >> p.lg);
   return p;
 }
 
-// CTAs of a persistent launch: what fits at once (looked up once per kernel).
-template <typename K> int64_t resident(K kernel, std::atomic<int> &cache) {
+// CTAs of a persistent launch: what fits at once.  The part of it that hangs
+// on registers is looked up once per kernel.
+template <typename K> int64_t resident(K kernel, std::atomic<int> &cache, size_t smem = 0) {
   int n = cache.load(std::memory_order_relaxed);
   if (n <= 0) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, THREADS, 0) != cudaSuccess || n <= 0) n = 1;
     cache.store(n, std::memory_order_relaxed);
   }
-  return n * tc::sm_count();
+  return std::min<int64_t>(n, (227 << 10) / (smem + 2048)) * tc::sm_count();
 }
 
 inline bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// CTAs of the backward, at most: few enough that the partial sums stay small.
-inline int64_t bwd_ctas(int64_t ctas) { return std::max<int64_t>(1, std::min<int64_t>(ctas, 2 * tc::sm_count())); }
+// Shared memory of the backward's rows, at most.
+constexpr int RING_MAX = SLOTS * 2 * (int)MAX_COLS * 4;
+// CTAs of the backward: two per SM at most (registers), one where the rows in
+// flight take more than half the shared memory.
+inline int64_t bwd_ctas(int64_t ctas, size_t smem) {
+  return std::max<int64_t>(1, std::min<int64_t>(ctas, (smem <= (112u << 10) ? 2 : 1) * tc::sm_count()));
+}
 inline int64_t long_chunks(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, 64)); }
 
-// Calls f with the number of vectors as a constant: up to 8192 values per row
-// over 256 threads.
-template <int VEC, typename F> void pick(int nv, F f) {
+// Calls f with the number of vectors as a constant, up to MOST values.
+template <int VEC, int MOST, typename F> void pick(int nv, F f) {
   if constexpr (VEC == 1) {
     switch (nv) {
       case 4: f(std::integral_constant<int, 4>()); break;
@@ -500,7 +653,7 @@ template <int VEC, typename F> void pick(int nv, F f) {
       case 1: f(std::integral_constant<int, 1>()); break;
       case 2: f(std::integral_constant<int, 2>()); break;
       default:
-        if constexpr (VEC == 4) {
+        if constexpr (8 * VEC <= MOST) {
           if (nv == 8) {
             f(std::integral_constant<int, 8>());
             break;
@@ -514,31 +667,53 @@ template <int VEC, typename F> void pick(int nv, F f) {
 template <typename T, int VEC>
 cudaError_t fwd(const Plan &p, const void *x, const float *w, const float *b, void *y, float *mean, float *rstd,
                 int64_t rows, int64_t D, int64_t xs, float eps, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
-    static std::atomic<int> cache;
-    auto *k = layer_norm_fwd_kernel<T, VEC, NV>;
-    const unsigned grid = (unsigned)std::min<int64_t>(p.ctas, resident(k, cache));
-    k<<<grid, THREADS, 0, st>>>((const T *)x, w, b, (T *)y, mean, rstd, rows, (int)D, xs, p.lg, eps);
+    if (p.ctas < 4 * tc::sm_count()) {  // a row or two per CTA: w and b straight from memory
+      layer_norm_fwd_kernel<T, VEC, NV, false><<<(unsigned)p.ctas, THREADS, 0, st>>>(
+          (const T *)x, w, b, (T *)y, mean, rstd, rows, (int)D, xs, p.lg, eps);
+      return;
+    }
+    auto *k = layer_norm_fwd_kernel<T, VEC, NV, true>;
+    static std::atomic<int> ready, cache;
+    const size_t smem = 2 * (size_t)((D + 3) / 4 * 4) * sizeof(float);
+    if (!ready.load(std::memory_order_relaxed)) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (int)MAX_COLS * (int)sizeof(float));
+      if (e != cudaSuccess) return;
+      ready.store(1, std::memory_order_relaxed);
+    }
+    const unsigned grid = (unsigned)std::min<int64_t>(p.ctas, resident(k, cache, smem));
+    k<<<grid, THREADS, smem, st>>>((const T *)x, w, b, (T *)y, mean, rstd, rows, (int)D, xs, p.lg, eps);
   };
-  pick<VEC>(p.nv, go);
-  return cudaGetLastError();
+  pick<VEC, 64>(p.nv, go);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t bwd(const Plan &p, int64_t &ctas, const void *x, const float *w, const float *mean, const float *rstd,
                 const void *dy, void *dx, float *part, int64_t rows, int64_t D, int64_t xs, int64_t ys,
                 cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
   auto go = [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
-    static std::atomic<int> cache;
+    constexpr int R = rows_at_once(NV * VEC);
+    static std::atomic<int> ready;
     auto *k = layer_norm_bwd_kernel<T, VEC, NV>;
-    ctas = std::min(bwd_ctas(p.ctas), resident(k, cache));
-    k<<<(unsigned)ctas, THREADS, 0, st>>>((const T *)x, w, mean, rstd, (const T *)dy, (T *)dx, part, rows, (int)D, xs,
-                                          ys, p.lg);
+    const size_t row = (size_t)((D * (int64_t)sizeof(T) + 15) / 16 * 16);
+    const size_t ring = VEC * sizeof(T) >= 4 ? (size_t)(THREADS >> p.lg) * SLOTS * R * 2 * row : 0;
+    const size_t smem = std::max(ring, (size_t)D * sizeof(float));
+    if (!ready.load(std::memory_order_relaxed)) {
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_MAX);
+      if (e != cudaSuccess) return;
+      ready.store(1, std::memory_order_relaxed);
+    }
+    ctas = bwd_ctas((p.ctas + R - 1) / R, smem);
+    k<<<(unsigned)ctas, THREADS, smem, st>>>((const T *)x, w, mean, rstd, (const T *)dy, (T *)dx, part, rows, (int)D,
+                                             xs, ys, p.lg);
   };
-  pick<VEC>(p.nv, go);
-  return cudaGetLastError();
+  pick<VEC, 32>(p.nv, go);  // 8192 values over 256 threads
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 inline bool sizes_ok(int64_t rows, int64_t D, int64_t xs, int32_t dtype) {
@@ -576,7 +751,7 @@ glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int
   } else {
     const int full = bf ? 8 : 4;
     const bool wide = D % full == 0 && xs % full == 0 && al16(x) && al16(y) && al16(w) && al16(b);
-    const Plan p = plan_of(rows, D, wide ? full : 1);
+    const Plan p = plan_of(rows, D, wide ? full : 1, bf && wide ? 64 : 32);
     if (bf)
       e = wide ? fwd<__nv_bfloat16, 8>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st)
                : fwd<__nv_bfloat16, 1>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st);
@@ -592,7 +767,7 @@ glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int
 // pointers, which the query does not see).
 size_t layer_norm_bwd_workspace_size(int64_t rows, int64_t D) {
   if (rows < 0 || D < 1 || D >= ((int64_t)1 << 31)) return 0;
-  const int64_t n = D > MAX_COLS ? long_chunks(rows) : bwd_ctas(rows);
+  const int64_t n = D > MAX_COLS ? long_chunks(rows) : bwd_ctas(rows, 0);
   return (size_t)n * 2 * (size_t)D * sizeof(float);
 }
 
@@ -635,7 +810,7 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean, 
   } else {
     const int full = bf ? 8 : 4;
     const bool wide = D % full == 0 && xs % full == 0 && ys % full == 0 && al16(x) && al16(dy) && al16(dx) && al16(w);
-    const Plan p = plan_of(rows, D, wide ? full : 1);
+    const Plan p = plan_of(rows, D, wide ? full : 1, 16);
     if (bf)
       e = wide ? bwd<__nv_bfloat16, 8>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st)
                : bwd<__nv_bfloat16, 1>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st);
