@@ -421,10 +421,20 @@ assert _PACK.size == ctypes.sizeof(Problem)
 
 
 def _tokens(t):
-    """_rows, with the usual case first."""
+    """_rows for the few tokens of a step, with the usual cases first: a
+    [B, T, heads, D] tensor with contiguous heads whose tokens (over B, where T
+    is 1) are evenly spaced goes in place."""
     if not t.is_cuda:
         raise ValueError("glacore takes CUDA tensors")
-    return (t, 0) if t.is_contiguous() else _rows(t)
+    B, T, Hh, D = t.shape
+    s0, s1, s2, s3 = t.stride()
+    if s3 == 1 and (s2 == D or Hh == 1):
+        if T == 1:
+            if s0 >= Hh * D:
+                return t, s0
+        elif s1 >= Hh * D and (B == 1 or s0 == T * s1):
+            return t, s1
+    return t.contiguous(), 0
 
 
 def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):

@@ -36,8 +36,8 @@ constexpr int64_t MAX_COLS = 8192;  // a row in registers: at most 256 threads x
 constexpr int LONG_THREADS = 512;   // a CTA per longer row
 constexpr int RED_X = 32, RED_Y = 32;
 
-// VEC consecutive values of T as they lie in memory (16 bytes, or one value
-// where the row length or an address rules out 16-byte accesses).
+// VEC consecutive values of T as they lie in memory: 16 bytes, or 4 or one
+// bf16 where the row length or an address rules that out.
 template <typename T, int VEC> struct Vec;
 template <> struct Vec<__nv_bfloat16, 8> {
   uint4 u;
@@ -58,6 +58,17 @@ template <> struct Vec<__nv_bfloat16, 8> {
       w[i] = *reinterpret_cast<uint32_t *>(&h);
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <> struct Vec<__nv_bfloat16, 2> {
+  uint32_t u;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint32_t *>(p); }
+  __device__ __forceinline__ void get(float (&v)[2]) const {
+    v[0] = __uint_as_float(u << 16);
+    v[1] = __uint_as_float(u & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[2]) {
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(v[0], v[1]);
   }
 };
 template <> struct Vec<float, 4> {
@@ -163,8 +174,9 @@ template <int VEC> __device__ __forceinline__ int staged_at(int c, int D) {
   return VEC == 8 ? ((c >> 2) & 1) * (D / 2) + (c >> 3) * 4 + (c & 3) : c;
 }
 template <int VEC> __device__ __forceinline__ void staged(const float *s, int c, int D, float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    v[0] = s[c];
+  if constexpr (VEC < 4) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = s[c + e];
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; e += 4) {
@@ -315,11 +327,17 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const
 // copies them to shared memory AHEAD turns before theirs, each thread its own
 // columns (no barrier: a thread reads only what it copied).  In registers the
 // rows in flight would have to share the space with the column sums: 8192 x
-// 2048 bf16 ran with 32 KB in flight per SM and 35 us.  Rows of bf16 on odd
-// addresses cannot be copied so (4 bytes at least) and are read in place,
-// twice.
+// 2048 bf16 ran with 32 KB in flight per SM and 35 us.  Rows of bf16 that start
+// between two 4-byte words (the least that can be copied so) are copied as the
+// words that hold them, by their whole row group, with a barrier of the group
+// per turn (4554 x 1335: 66 us when they were read in place, WORDSUS so).
 constexpr int AHEAD = 2, SLOTS = AHEAD + 1;
 constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }  // by a thread's values of a row (shared memory)
+
+// Shared memory of one row, and of the words that hold it.
+__host__ __device__ inline int slot_bytes(int row_bytes, int vec_bytes) {
+  return (row_bytes + (vec_bytes < 4 ? 4 : 0) + 15) / 16 * 16;
+}
 
 // part: [gridDim.x][2][D] partial dw, db of the rows each CTA walked.
 template <typename T, int VEC, int NV>
@@ -328,7 +346,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                           const float *__restrict__ rstd, const T *__restrict__ dy, T *__restrict__ dx,
                           float *__restrict__ part, int64_t rows, int D, int64_t xs, int64_t ys, int lg) {
   constexpr int BYTES = VEC * (int)sizeof(T);
-  constexpr bool ASYNC = BYTES >= 4;
+  constexpr bool WORDS = BYTES < 4;
   constexpr int R = rows_at_once(NV * VEC);
   extern __shared__ float4 smem[];
   __shared__ float red[2][THREADS / 32][2 * R];
@@ -343,15 +361,24 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
   }
   // this thread's columns of its row group's slots: x, dy of each of R rows
-  const int pitch = (D * (int)sizeof(T) + 15) / 16 * 16;
+  const int pitch = slot_bytes(D * (int)sizeof(T), BYTES);
   char *slots = reinterpret_cast<char *>(smem) + (int64_t)(threadIdx.x >> lg) * SLOTS * R * 2 * pitch + t * BYTES;
   auto fetch = [&](int64_t row, int slot) {
-    if constexpr (ASYNC) {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (row + i < rows) {
-          const T *px = x + (row + i) * xs + t * VEC, *pg = dy + (row + i) * ys + t * VEC;
-          char *to = slots + (slot * R + i) * 2 * pitch;
+    for (int i = 0; i < R; ++i)
+      if (row + i < rows) {
+        const T *px = x + (row + i) * xs, *pg = dy + (row + i) * ys;
+        char *to = slots + (slot * R + i) * 2 * pitch;
+        if constexpr (WORDS) {
+          to += t * (4 - BYTES);
+          const char *wx = reinterpret_cast<const char *>((uintptr_t)px & ~(uintptr_t)3) + 4 * t;
+          const char *wg = reinterpret_cast<const char *>((uintptr_t)pg & ~(uintptr_t)3) + 4 * t;
+          const char *ex = reinterpret_cast<const char *>(px + D), *eg = reinterpret_cast<const char *>(pg + D);
+          for (int k = 0; wx + k < ex; k += 4 * L) copy_async<4>(to + k, wx + k);
+          for (int k = 0; wg + k < eg; k += 4 * L) copy_async<4>(to + pitch + k, wg + k);
+        } else {
+          px += t * VEC;
+          pg += t * VEC;
 #pragma unroll
           for (int j = 0; j < NV; ++j)
             if ((j * L + t) * VEC < D) {
@@ -359,8 +386,8 @@ __global__ void __launch_bounds__(THREADS, 2)
               copy_async<BYTES>(to + pitch + j * L * BYTES, pg + j * L * VEC);
             }
         }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> lg) * R;
   const int64_t step = (int64_t)gridDim.x * per;
@@ -378,8 +405,14 @@ __global__ void __launch_bounds__(THREADS, 2)
   stats(row);
   int slot = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD - 1) : "memory");
+    if constexpr (WORDS) {  // the group's copies are in, and it is done with the slot copied to next
+      if (L > 32)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + (threadIdx.x >> lg)), "r"(L) : "memory");
+      else
+        __syncwarp();
+    }
     fetch(row + AHEAD * step, slot == 0 ? SLOTS - 1 : slot - 1);
-    if (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
     float m[R], r[R], s[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -389,14 +422,13 @@ __global__ void __launch_bounds__(THREADS, 2)
     stats(row + step);
     auto get = [&](int i, int j, float(&v)[VEC], float(&g)[VEC]) {  // columns j of x and dy of row i
       Vec<T, VEC> vx, vg;
-      if constexpr (ASYNC) {
-        const char *from = slots + (slot * R + i) * 2 * pitch + j * L * BYTES;
-        vx.load(reinterpret_cast<const T *>(from));
-        vg.load(reinterpret_cast<const T *>(from + pitch));
-      } else {
-        vx.load(x + (row + i) * xs + (j * L + t) * VEC);
-        vg.load(dy + (row + i) * ys + (j * L + t) * VEC);
+      const char *fx = slots + (slot * R + i) * 2 * pitch + j * L * BYTES, *fg = fx + pitch;
+      if constexpr (WORDS) {  // where in its first word the row starts
+        fx += (uintptr_t)(x + (row + i) * xs) & 3;
+        fg += (uintptr_t)(dy + (row + i) * ys) & 3;
       }
+      vx.load(reinterpret_cast<const T *>(fx));
+      vg.load(reinterpret_cast<const T *>(fg));
       vx.get(v);
       vg.get(g);
     };
@@ -597,13 +629,16 @@ inline int log2_up(int64_t v) {
   return lg;
 }
 
-// vec values per vector (1 where 16-byte accesses are ruled out).  A thread
+// Fewest vectors a thread is built for.
+constexpr int least_nv(int vec) { return vec < 4 ? 4 / vec : 1; }
+
+// vec values per vector.  A thread
 // takes up to `most` values of a row before the row takes more threads than a
 // warp, and more than that only where 256 threads do not hold the row.  Few
 // rows are spread wider, so that more threads have loads in flight.
 inline Plan plan_of(int64_t rows, int64_t D, int vec, int most) {
   const int64_t need = (D + vec - 1) / vec;
-  const int least = vec == 1 ? 4 : 1;
+  const int least = least_nv(vec);
   Plan p;
   p.vec = vec;
   p.nv = least;
@@ -628,7 +663,14 @@ template <typename K> int64_t resident(K kernel, std::atomic<int> &cache, size_t
   return std::min<int64_t>(n, (227 << 10) / (smem + 2048)) * tc::sm_count();
 }
 
-inline bool al16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+// Values per access: 16 bytes, else 4, else one, as rows, strides (elements)
+// and addresses allow (weights: 16 bytes with the first only).
+inline int vec_of(bool bf, int64_t D, int64_t s0, int64_t s1, uintptr_t data, uintptr_t w) {
+  const int64_t all = D | s0 | s1;
+  const int full = bf ? 8 : 4;
+  if (all % full == 0 && ((data | w) & 15) == 0) return full;
+  return bf && all % 2 == 0 && (data & 3) == 0 ? 2 : 1;
+}
 
 // Shared memory of the backward's rows, at most.
 constexpr int RING_MAX = SLOTS * 2 * (int)MAX_COLS * 4;
@@ -639,28 +681,21 @@ inline int64_t bwd_ctas(int64_t ctas, size_t smem) {
 }
 inline int64_t long_chunks(int64_t rows) { return std::max<int64_t>(1, std::min<int64_t>(rows, 64)); }
 
-// Calls f with the number of vectors as a constant, up to MOST values.
+// Calls f with the number of vectors as a constant: 1, 2, 4 or 8 times the
+// least, up to MOST values.
 template <int VEC, int MOST, typename F> void pick(int nv, F f) {
-  if constexpr (VEC == 1) {
-    switch (nv) {
-      case 4: f(std::integral_constant<int, 4>()); break;
-      case 8: f(std::integral_constant<int, 8>()); break;
-      case 16: f(std::integral_constant<int, 16>()); break;
-      default: f(std::integral_constant<int, 32>()); break;
-    }
-  } else {
-    switch (nv) {
-      case 1: f(std::integral_constant<int, 1>()); break;
-      case 2: f(std::integral_constant<int, 2>()); break;
-      default:
-        if constexpr (8 * VEC <= MOST) {
-          if (nv == 8) {
-            f(std::integral_constant<int, 8>());
-            break;
-          }
+  constexpr int U = least_nv(VEC);
+  switch (nv / U) {
+    case 1: f(std::integral_constant<int, U>()); break;
+    case 2: f(std::integral_constant<int, 2 * U>()); break;
+    default:
+      if constexpr (8 * U * VEC <= MOST) {
+        if (nv == 8 * U) {
+          f(std::integral_constant<int, 8 * U>());
+          break;
         }
-        f(std::integral_constant<int, 4>());
-    }
+      }
+      f(std::integral_constant<int, 4 * U>());
   }
 }
 
@@ -700,8 +735,7 @@ cudaError_t bwd(const Plan &p, int64_t &ctas, const void *x, const float *w, con
     constexpr int R = rows_at_once(NV * VEC);
     static std::atomic<int> ready;
     auto *k = layer_norm_bwd_kernel<T, VEC, NV>;
-    const size_t row = (size_t)((D * (int64_t)sizeof(T) + 15) / 16 * 16);
-    const size_t ring = VEC * sizeof(T) >= 4 ? (size_t)(THREADS >> p.lg) * SLOTS * R * 2 * row : 0;
+    const size_t ring = (size_t)(THREADS >> p.lg) * SLOTS * R * 2 * slot_bytes((int)(D * sizeof(T)), VEC * sizeof(T));
     const size_t smem = std::max(ring, (size_t)D * sizeof(float));
     if (!ready.load(std::memory_order_relaxed)) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_MAX);
@@ -749,15 +783,11 @@ glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int
                                                                        rows, D, xs, eps);
     e = cudaGetLastError();
   } else {
-    const int full = bf ? 8 : 4;
-    const bool wide = D % full == 0 && xs % full == 0 && al16(x) && al16(y) && al16(w) && al16(b);
-    const Plan p = plan_of(rows, D, wide ? full : 1, bf && wide ? 64 : 32);
-    if (bf)
-      e = wide ? fwd<__nv_bfloat16, 8>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st)
-               : fwd<__nv_bfloat16, 1>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st);
-    else
-      e = wide ? fwd<float, 4>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st)
-               : fwd<float, 1>(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st);
+    const int vec = vec_of(bf, D, xs, xs, (uintptr_t)x | (uintptr_t)y, (uintptr_t)w | (uintptr_t)b);
+    const Plan p = plan_of(rows, D, vec, vec == 8 ? 64 : 32);
+    auto go = bf ? vec == 8 ? fwd<__nv_bfloat16, 8> : vec == 2 ? fwd<__nv_bfloat16, 2> : fwd<__nv_bfloat16, 1>
+              : vec == 4 ? fwd<float, 4> : fwd<float, 1>;
+    e = go(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st);
   }
   mark_launch("layer_norm_fwd", st);
   return status_of(e);
@@ -808,15 +838,11 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean, 
     }
     e = cudaGetLastError();
   } else {
-    const int full = bf ? 8 : 4;
-    const bool wide = D % full == 0 && xs % full == 0 && ys % full == 0 && al16(x) && al16(dy) && al16(dx) && al16(w);
-    const Plan p = plan_of(rows, D, wide ? full : 1, 16);
-    if (bf)
-      e = wide ? bwd<__nv_bfloat16, 8>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st)
-               : bwd<__nv_bfloat16, 1>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st);
-    else
-      e = wide ? bwd<float, 4>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st)
-               : bwd<float, 1>(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st);
+    const int vec = vec_of(bf, D, xs, ys, (uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx, (uintptr_t)w);
+    const Plan p = plan_of(rows, D, vec, 16);
+    auto go = bf ? vec == 8 ? bwd<__nv_bfloat16, 8> : vec == 2 ? bwd<__nv_bfloat16, 2> : bwd<__nv_bfloat16, 1>
+              : vec == 4 ? bwd<float, 4> : bwd<float, 1>;
+    e = go(p, n, x, w, mean, rstd, dy, dx, part, rows, D, xs, ys, st);
   }
   mark_launch("layer_norm_bwd", st);
   if (e != cudaSuccess) return status_of(e);
