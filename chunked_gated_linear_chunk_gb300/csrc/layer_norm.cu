@@ -330,7 +330,7 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const
 // 2048 bf16 ran with 32 KB in flight per SM and 35 us.  Rows of bf16 that start
 // between two 4-byte words (the least that can be copied so) are copied as the
 // words that hold them, by their whole row group, with a barrier of the group
-// per turn (4554 x 1335: 66 us when they were read in place, WORDSUS so).
+// per turn (4554 x 1335: 66 us when they were read in place, 28 us so).
 constexpr int AHEAD = 2, SLOTS = AHEAD + 1;
 constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }  // by a thread's values of a row (shared memory)
 
@@ -784,7 +784,7 @@ glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int
     e = cudaGetLastError();
   } else {
     const int vec = vec_of(bf, D, xs, xs, (uintptr_t)x | (uintptr_t)y, (uintptr_t)w | (uintptr_t)b);
-    const Plan p = plan_of(rows, D, vec, vec == 8 ? 64 : 32);
+    const Plan p = plan_of(rows, D, vec, vec == 8 ? 64 : vec == 1 ? 16 : 32);
     auto go = bf ? vec == 8 ? fwd<__nv_bfloat16, 8> : vec == 2 ? fwd<__nv_bfloat16, 2> : fwd<__nv_bfloat16, 1>
               : vec == 4 ? fwd<float, 4> : fwd<float, 1>;
     e = go(p, x, w, b, y, mean, rstd, rows, D, xs, eps, st);

@@ -58,18 +58,18 @@ using tc::tmem_ld_wait32;
 using tc::WAIT_CYCLES;
 
 constexpr int THREADS = 320, EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;
+enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
 constexpr int BM = 256, BK = 64;   // rows of a pair's tile, K of a stage
 constexpr uint32_t A_BYTES = 128 * BK * 2;
 constexpr int MAX_STAGES = 12;
-constexpr int STAGE_SMEM = 221184;  // shared memory of the ring, at most (a KB is left for its alignment)
+constexpr int SMEM = 231168;          // shared memory of ring and output staging, at most (a KB is left for alignment)
+constexpr uint32_t OUT_BYTES = 4096;  // output staging of a warp: 32 rows of 128 bytes
 constexpr int GROUP_M = 8;         // row tiles that share a walk over the columns (L2 reuse)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
-enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
-
 // One product C[m, n] = A B^T over k-blocks, tiles of BM x bn.
 struct Gemm {
-  CUtensorMap a, b;
+  CUtensorMap a, b, o;      // o: the output, where `tma_out`
   int64_t m, n;
   int32_t a_mn;             // A stored with its M axis contiguous (B: always its K axis)
   int32_t mt, nt, kb;       // tiles, k-blocks
@@ -79,12 +79,13 @@ struct Gemm {
   // out + s * m * n, added to what is there if `add`; otherwise the tensors'
   // dtype.
   void *out;
-  int32_t out_f32, add, trans;
+  int32_t out_f32, add, trans, tma_out;
 };
 
 struct Args {
   Gemm g[2];
   int64_t units0, units;  // units of g[0], of both
+  int32_t skip;           // rounds of g[1]'s units that the pairs with one unit of g[0] more sit out
   int32_t bn, stages;
   int64_t N, V, v0;  // tokens, vocabulary, first column of the piece
   const int64_t *target;
@@ -100,6 +101,32 @@ struct Args {
 struct Tile {
   int64_t m0, n0;
   int which, split, kb0, kb1, nt;
+};
+
+// The units of pair p of P: g[0]'s dealt out in turn, then g[1]'s, whose first
+// `skip` rounds pass over the first units0 % P pairs (they got a unit of g[0]
+// more, worth about so many of g[1]'s).
+struct Walk {
+  int64_t p, P, units0, units1, u0, i;
+  int32_t skip;
+  __device__ __forceinline__ Walk(const Args &a, int64_t pair, int64_t pairs)
+      : p(pair), P(pairs), units0(a.units0), units1(a.units - a.units0), u0(pair), i(0), skip(a.skip) {}
+  // the next unit (g[1]'s counted on from units0), or -1
+  __device__ __forceinline__ int64_t next() {
+    if (u0 < units0) {
+      const int64_t u = u0;
+      u0 += P;
+      return u;
+    }
+    const int64_t r = units0 % P, rest = P - r;
+    int64_t u;
+    if (p < r)
+      u = skip * rest + i * P + p;
+    else
+      u = i < skip ? i * rest + p - r : skip * rest + (i - skip) * P + p;
+    ++i;
+    return u < units1 ? units0 + u : -1;
+  }
 };
 
 __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
@@ -122,8 +149,14 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
 }
 
 constexpr int stage_bytes_of(int parts, int bn) { return parts * (int)(A_BYTES + bn * BK); }
-constexpr int stages_of(int parts, int bn) {
-  return STAGE_SMEM / stage_bytes_of(parts, bn) < MAX_STAGES ? STAGE_SMEM / stage_bytes_of(parts, bn) : MAX_STAGES;
+// G and dw of bf16 operands leave through shared memory and TMA: a warp's
+// direct stores of 32 rows touch 32 lines each, and a product over few k-blocks
+// is bound by them (backward of 16 x 2048 x 32000: 116 us with direct stores,
+// 110 us so).  Three parts leave no room for it.
+constexpr bool staged_out(int kind, int parts) { return kind != STATS && parts == 1; }
+constexpr int stages_of(int kind, int parts, int bn) {
+  const int n = (SMEM - (staged_out(kind, parts) ? EPI_WARPS * (int)OUT_BYTES : 0)) / stage_bytes_of(parts, bn);
+  return n < MAX_STAGES ? n : MAX_STAGES;
 }
 // k-blocks whose products one accumulator sums
 constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 4 : kind == STATS ? 16 : 1 << 30; }
@@ -193,7 +226,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       int s = 0;
       uint32_t phase = 0;  // of the ring's current turn
       const uint32_t bar0 = mapa_shared(full0, 0);
-      for (int64_t u = pair; u < a.units && ok; u += pairs) {
+      Walk walk(a, pair, pairs);
+      for (int64_t u; ok && (u = walk.next()) >= 0;) {
         const Tile t = tile_of(a, u);
         const Gemm &g = a.g[t.which];
         const CUtensorMap *ma = &g.a, *mb = &g.b;
@@ -244,7 +278,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       uint32_t phase = 0;
       uint32_t hand = 0;
       const uint32_t acc_full0 = smem_u32(acc_full);
-      for (int64_t u = pair; u < a.units && ok; u += pairs) {
+      Walk walk(a, pair, pairs);
+      for (int64_t u; ok && (u = walk.next()) >= 0;) {
         const Tile t = tile_of(a, u);
         const bool a_mn = a.g[t.which].a_mn;
         const uint32_t idesc = idesc_bf16(BM, a.bn, a_mn, false);
@@ -299,6 +334,23 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     // ---- epilogue: thread = row, half = which half of the tile's columns
     const int quarter = warp & 3, half = warp >> 2, cols = a.bn / 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * cols;
+    // The warp's staging: 32 rows of 128 bytes, 16-byte chunks swizzled by row.
+    const uint32_t stage = smem + stages * stage_bytes + warp * OUT_BYTES;
+    auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+      tc::st_shared_v4(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4), x, y, z, w);
+    };
+    auto begin_out = [&]() {  // the last store has read the staging
+      if (lane == 0) bulk_wait_read_all();
+      __syncwarp();
+    };
+    auto send_out = [&](const CUtensorMap *map, int x, int y, int z) {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_3d_at(map, stage, x, y, z);
+        bulk_commit();
+      }
+    };
     auto release = [&](int buf) {  // this warp has read the accumulator
       tc_fence_before();
       __syncwarp();
@@ -307,7 +359,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     const float unit = KIND != STATS && a.unit ? *a.unit : 1.f;
     int64_t hand = 0;
     bool ok = true;
-    for (int64_t u = pair; u < a.units && ok; u += pairs) {
+    Walk walk(a, pair, pairs);
+    for (int64_t u; ok && (u = walk.next()) >= 0;) {
       const Tile t = tile_of(a, u);
       const Gemm &g = a.g[t.which];
       const int64_t row = t.m0 + rank * 128 + quarter * 32 + lane;
@@ -372,33 +425,57 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           // a token that is not scored has no gradient, whatever its logits are
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = scored ? v[i] * dl : 0.f;
-          if (!live) return;
+          if constexpr (PARTS == 1) {
+            if (!(c & 32)) begin_out();
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            __nv_bfloat16 *out = a.G + ((int64_t)p * a.N + row) * a.gpitch + col;
+            for (int i = 0; i < 4; ++i)
+              put(i + (c & 32) / 8, pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                  pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+            if ((c & 32) && row - lane < g.m) send_out(&g.o, (int)col - 32, (int)(row - lane), 0);
+          } else {
+            if (!live) return;
 #pragma unroll
-            for (int i = 0; i < 32; i += 16) {
-              uint32_t w[8];
+            for (int p = 0; p < PARTS; ++p) {
+              __nv_bfloat16 *out = a.G + ((int64_t)p * a.N + row) * a.gpitch + col;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                float &x = v[i + 2 * j], &y = v[i + 2 * j + 1];
-                if (PARTS == 1) {
-                  w[j] = pack_bf16(x, y);
-                } else {  // the leading 8 bits of what is left, exactly
+              for (int i = 0; i < 32; i += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {  // the leading 8 bits of what is left, exactly
+                  float &x = v[i + 2 * j], &y = v[i + 2 * j + 1];
                   const uint32_t xb = __float_as_uint(x) & 0xffff0000u, yb = __float_as_uint(y) & 0xffff0000u;
                   w[j] = (xb >> 16) | yb;
                   x -= __uint_as_float(xb);
                   y -= __uint_as_float(yb);
                 }
+                st_global_v8(out + i, w);
               }
-              st_global_v8(out + i, w);
             }
           }
         } else {
-          if (!live || col >= g.n) return;
-          const int room = g.n - col < 32 ? (int)(g.n - col) : 32;
+          if (col - (c & 32) >= g.n || row - lane >= g.m) return;  // nothing of the warp's 64 columns is there
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= unit;
+          if (PARTS == 1 && g.tma_out) {  // what lies past the edges is not written
+            if (g.out_f32) {
+              begin_out();
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                put(i, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                    __float_as_uint(v[4 * i + 3]));
+              if (col < g.n) send_out(&g.o, (int)col, (int)(row - lane), t.split);
+            } else {
+              if (!(c & 32)) begin_out();
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                put(i + (c & 32) / 8, pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                    pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
+              if (c & 32) send_out(&g.o, (int)col - 32, (int)(row - lane), 0);
+            }
+            return;
+          }
+          if (!live || col >= g.n) return;
+          const int room = g.n - col < 32 ? (int)(g.n - col) : 32;
           if (g.trans) {  // the warp's 32 rows lie side by side
             const int64_t at = col * g.m + row;
             if (g.out_f32) {
@@ -419,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           }
           const bool whole = room == 32 && g.n % 8 == 0;
           if (g.out_f32) {
-            float *out = reinterpret_cast<float *>(g.out) + row * g.n + col;
+            float *out = reinterpret_cast<float *>(g.out) + ((int64_t)t.split * g.m + row) * g.n + col;
             if (whole) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
@@ -431,16 +508,9 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
             }
           } else if (PARTS == 1) {
             __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + row * g.n + col;
-            if (whole) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                tc::st_global_v4(out + i, pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
-                                 pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < room) out[i] = __float2bfloat16_rn(v[i]);
-            }
+            for (int i = 0; i < 32; ++i)
+              if (i < room) out[i] = __float2bfloat16_rn(v[i]);
           }
         }
       };
@@ -523,6 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         a.part[(int64_t)(2 * t.nt + half) * a.N + row] = make_float2(mx == -INFINITY ? mx : mx * LOG2E, sum);
     }
   }
+  if (staged_out(KIND, PARTS) && warp < EPI_WARPS && lane == 0) bulk_wait_all();
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -569,11 +640,11 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
   loss[row] = t < 0 || t >= V ? 0.f : l - zt[row];
 }
 
-// dx = the sum of its splits, in order, rounded to its type.  WIDE: n is a
-// multiple of 4 (every split then starts on 16 bytes).
+// A gradient from its splits' sums, added in order and rounded to its type.
+// WIDE: n is a multiple of 4 and dx 16-byte aligned.
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256)
-    ce_dx_kernel(const float *__restrict__ part, int splits, int64_t n, T *__restrict__ dx) {
+    ce_sum_kernel(const float *__restrict__ part, int splits, int64_t n, T *__restrict__ dx) {
   if constexpr (WIDE) {
     const float4 *p = reinterpret_cast<const float4 *>(part);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += (int64_t)gridDim.x * 256) {
@@ -597,46 +668,55 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The unit of G: the largest |dloss| of a scored token (1 if there is none).
-// With dloss one number for all tokens, the usual mean, G is then p - [v =
-// target] itself, and the -1 at the target of a token that is far from
-// foreseen, most of its gradient, is exact in bf16.
-__global__ void __launch_bounds__(1024)
-    ce_unit_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ target, int64_t N, int64_t V,
-                   float *__restrict__ unit) {
-  __shared__ float red[32];
-  float m = 0.f;
-  for (int64_t i = threadIdx.x; i < N; i += 1024) {
-    const int64_t t = target[i];
-    if (t >= 0 && t < V) m = fmaxf(m, fabsf(dloss[i]));
-  }
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    m = red[threadIdx.x];
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (threadIdx.x == 0) *unit = m > 0.f && isfinite(m) ? m : 1.f;
-  }
-}
-
-// dst [parts, cols, dpitch] = src [parts, rows, spitch] transposed, 64 x 64 at
-// a time through shared memory.
+// Before the products of the backward: dst [parts, cols, dpitch] = src [parts,
+// rows, spitch] transposed, 64 x 64 at a time through shared memory (pitches
+// are multiples of 8: two values per access); and, by one CTA beside them, the
+// unit of G (null: none wanted): the largest |dloss| of a scored token, 1 if
+// there is none.  With dloss one number for all tokens, the usual mean, G in
+// that unit is p - [v = target] itself, and the -1 at the target of a token
+// that is far from foreseen, most of its gradient, is exact in bf16.
 __global__ void __launch_bounds__(256)
-    ce_transpose_kernel(const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
-                        int64_t dpitch, __nv_bfloat16 *__restrict__ dst) {
-  __shared__ __nv_bfloat16 tile[64][66];
+    ce_prepare_kernel(const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
+                      int64_t dpitch, __nv_bfloat16 *__restrict__ dst, const float *__restrict__ dloss,
+                      const int64_t *__restrict__ target, int64_t V, float *__restrict__ unit) {
+  __shared__ __nv_bfloat162 tile[64][33];
+  __shared__ float red[8];
+  if (blockIdx.x == gridDim.x - 1) {
+    if (!unit || blockIdx.y || blockIdx.z) return;
+    float m = 0.f;
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < rows; i += 256) {
+      const int64_t t = target[i];
+      const float d = fabsf(dloss[i]);
+      if (t >= 0 && t < V) m = fmaxf(m, d);
+    }
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) m = fmaxf(m, red[i]);
+      *unit = m > 0.f && isfinite(m) ? m : 1.f;
+    }
+    return;
+  }
   src += blockIdx.z * rows * spitch;
   dst += blockIdx.z * cols * dpitch;
   const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   for (int i = y; i < 64; i += 8)
-    for (int j = x; j < 64; j += 32)
-      if (r0 + i < rows && c0 + j < cols) tile[i][j] = src[(r0 + i) * spitch + c0 + j];
+    if (r0 + i < rows && c0 + 2 * x < spitch)
+      tile[i][x] = *reinterpret_cast<const __nv_bfloat162 *>(src + (r0 + i) * spitch + c0 + 2 * x);
   __syncthreads();
-  for (int j = y; j < 64; j += 8)
-    for (int i = x; i < 64; i += 32)
-      if (r0 + i < rows && c0 + j < cols) dst[(c0 + j) * dpitch + r0 + i] = tile[i][j];
+  // columns c, c + 1 of rows 2x, 2x + 1
+  for (int j = y; j < 32; j += 8) {
+    const int64_t c = c0 + 2 * j;
+    if (r0 + 2 * x >= rows) continue;
+    const __nv_bfloat162 a = tile[2 * x][j], b = tile[2 * x + 1][j];
+    if (c < cols)
+      *reinterpret_cast<__nv_bfloat162 *>(dst + c * dpitch + r0 + 2 * x) = __halves2bfloat162(a.x, b.x);
+    if (c + 1 < cols)
+      *reinterpret_cast<__nv_bfloat162 *>(dst + (c + 1) * dpitch + r0 + 2 * x) = __halves2bfloat162(a.y, b.y);
+  }
 }
 
 // Rows of bf16 with a pitch that TMA can address: a copy of bf16 values
@@ -645,8 +725,10 @@ template <int PARTS, typename T>
 __global__ void __launch_bounds__(256)
     ce_pack_kernel(const T *__restrict__ src, int64_t rows, int64_t D, int64_t stride, int64_t pitch,
                    __nv_bfloat16 *__restrict__ dst) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < D; c += 256) {
+  const int lane = threadIdx.x & 31;
+  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8) {
+#pragma unroll 4
+    for (int64_t c = lane; c < D; c += 32) {
       if constexpr (PARTS == 1) {
         dst[r * pitch + c] = src[r * stride + c];
       } else {
@@ -659,12 +741,12 @@ __global__ void __launch_bounds__(256)
         }
       }
     }
+  }
 }
 
 // ---- host ------------------------------------------------------------------
 constexpr size_t G_BYTES = (size_t)512 << 20;   // G of one piece of the vocabulary, about
-constexpr size_t DX_BYTES = (size_t)512 << 20;  // dx's splits, at most
-constexpr int MAX_SPLITS = 32;
+constexpr size_t SUMS_BYTES = (size_t)512 << 20;  // fp32 sums of a gradient's splits, at most (if there are several)
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -674,8 +756,9 @@ struct Layout {
   bool pack;                         // x and w are copied to rows TMA can address
   int64_t pitch, xt_pitch, piece, pieces, gpitch;
   int splits, run;  // dx's K axis: `splits` runs of `run` k-blocks (in the first, longest piece)
-  bool dx_f32;
-  size_t off_x, off_w, off_part, off_zt, off_unit, off_xt, off_g, off_dx, total;
+  int splits_w, run_w;  // dw's
+  bool dx_f32, dw_sums;
+  size_t off_x, off_w, off_part, off_zt, off_unit, off_xt, off_g, off_dx, off_dw, total;
 };
 
 // Pairs of CTAs that run at once on the current device.
@@ -688,7 +771,7 @@ int64_t pair_count() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tc::sm_count() / 2 * 2));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = STAGE_SMEM + 1024;
+    cfg.dynamicSmemBytes = SMEM + 1024;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -707,27 +790,50 @@ int64_t pair_count() {
   return n;
 }
 
-// dx's K axis (a piece of the vocabulary) is cut so that the units of dx and
-// dw together load the pairs evenly: the cut with the shortest longest pair,
-// units dealt out in turn.
-int best_splits(int64_t tiles_x, int64_t kb_x, int64_t tiles_w, int64_t kb_w, int most) {
-  const int64_t pairs = pair_count();
-  int best = 1;
+// How the two gradients' units load the pairs: the time of the busiest pair,
+// in k-blocks of a tile (about 0.27 us), for units of run_x and run_w
+// k-blocks.  A unit takes no less than its epilogue, about EPI_KB of them, and
+// 4 for its start and end.
+constexpr int64_t EPI_KB = 8;
+struct Deal {
+  int64_t longest;
+  int32_t skip;
+};
+Deal deal(int64_t ux, int64_t run_x, int64_t uw, int64_t run_w) {
+  const int64_t P = pair_count(), cx = std::max<int64_t>(run_x, EPI_KB) + 4, cw = std::max<int64_t>(run_w, EPI_KB) + 4,
+                r = ux % P, nx = ux / P;
+  const int64_t skip = r ? std::min((cx + cw / 2) / cw, up(uw, P - r)) : 0;
+  const int64_t rem = std::max<int64_t>(0, uw - skip * (P - r)), rounds = rem / P, rest = rem % P;
+  const int64_t a = (nx + (r > 0)) * cx + (rounds + (rest > 0)) * cw;
+  const int64_t b = nx * cx + (skip + rounds + (rest > r)) * cw;
+  return Deal{r ? std::max(a, b) : b, (int32_t)skip};
+}
+
+// Cuts of the two gradients' K axes (dx: a piece of the vocabulary, dw: the
+// tokens) for the shortest busiest pair.  A cut costs its fp32 sums' way to
+// memory and back (1.8 MB per k-block's time) and a launch.
+void choose_splits(Layout &L, int64_t N, int64_t D, int64_t cols) {
+  static const int tries[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+  const int64_t tx = up(D, BM) * up(N, L.bn), tw = up(cols, BM) * up(D, L.bn), kx = up(cols, BK), kw = up(N, BK);
   int64_t least = -1;
-  for (int s = 1; s <= most && s <= kb_x; ++s) {
-    const int64_t run = up(kb_x, s), ux = tiles_x * up(kb_x, run);
-    int64_t longest = 0;
-    for (int64_t p = 0; p < pairs; ++p) {
-      const int64_t nx = ux > p ? (ux - p + pairs - 1) / pairs : 0;
-      const int64_t all = ux + tiles_w > p ? (ux + tiles_w - p + pairs - 1) / pairs : 0;
-      longest = std::max(longest, nx * (run + 4) + (all - nx) * (kb_w + 4));  // 4: a unit's start and end
-    }
-    if (least < 0 || longest < least) {
-      least = longest;
-      best = s;
+  for (int sx : tries) {
+    const int64_t rx = up(kx, sx), mx = up(kx, rx) * N * D * 4;
+    if (sx > 1 && (sx > kx || mx > (int64_t)SUMS_BYTES)) break;
+    for (int sw : tries) {
+      const int64_t rw = up(kw, sw), mw = up(kw, rw) * cols * D * 4;
+      if (sw > 1 && (sw > kw || mw > (int64_t)SUMS_BYTES)) break;
+      int64_t cost = deal(tx * up(kx, rx), rx, tw * up(kw, rw), rw).longest;
+      if (sx > 1 || L.pieces > 1) cost += 2 * mx / 1800000 + 8;
+      if (sw > 1) cost += 2 * mw / 1800000 + 8;
+      if (least < 0 || cost < least) {
+        least = cost;
+        L.run = (int)rx;
+        L.splits = (int)up(kx, rx);
+        L.run_w = (int)rw;
+        L.splits_w = (int)up(kw, rw);
+      }
     }
   }
-  return best;
 }
 
 Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
@@ -736,13 +842,13 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
   L.parts = dtype == GLACORE_F32 ? 3 : 1;
   L.bn = L.parts == 3 ? 128 : 256;
   L.bn_z = L.bn;
-  if (!backward && L.parts == 1) {
+  if (L.parts == 1) {
     // The width that deals the vocabulary out most evenly: the fewest columns
     // for the busiest pair, and about 32 columns' time for a tile's start and
     // end.  It matters for few tokens, where the call is bound by reading w
     // once (16 x 2048 x 32000: 36.4 us with 256, 34.8 us with 224).
     int64_t least = -1;
-    for (int bn = 256; bn >= 128; bn -= 32) {
+    for (int bn = 256; bn >= 128; bn -= backward ? 128 : 32) {  // G leaves 64 columns of a warp at a time
       const int64_t cost = up(up(N, BM) * up(V, bn), pair_count()) * (bn + 32);
       if (least < 0 || cost < least) {
         least = cost;
@@ -774,35 +880,37 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     take(L.off_unit, sizeof(float));
     take(L.off_xt, (size_t)L.parts * D * L.xt_pitch * 2);
     take(L.off_g, (size_t)L.parts * N * L.gpitch * 2);
-    const int cap = (int)std::max<int64_t>(1, std::min<int64_t>(MAX_SPLITS, DX_BYTES / (4 * N * D)));
-    const int64_t first = std::min(L.piece, V), kb = up(first, BK);
-    L.run = (int)up(kb, best_splits(up(D, BM) * up(N, L.bn), kb, up(first, BM) * up(D, L.bn), up(N, BK), cap));
-    L.splits = (int)up(kb, L.run);
+    choose_splits(L, N, D, std::min(L.piece, V));
     L.dx_f32 = L.splits > 1 || L.pieces > 1;
+    L.dw_sums = L.splits_w > 1;
     if (L.dx_f32) take(L.off_dx, (size_t)L.splits * N * D * sizeof(float));
+    if (L.dw_sums) take(L.off_dw, (size_t)L.splits_w * std::min(L.piece, V) * D * sizeof(float));
   }
   L.total = off;
   return L;
 }
 
-// [parts, rows, cols] bf16, `pitch` elements between rows, part_rows rows
-// between parts, box of 64 columns x box_rows.
+// [parts, rows, cols] bf16 (or fp32), `pitch` elements between rows, part_rows
+// rows between parts, box of 128 bytes x box_rows.
 bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t parts, int64_t pitch,
-               int64_t part_rows, int box_rows) {
+               int64_t part_rows, int box_rows, bool f32 = false) {
   tc::EncodeFn enc = tc::encoder();
   if (!enc) return false;
+  const int64_t es = f32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
-  cuuint64_t strides[2] = {(cuuint64_t)(pitch * 2), (cuuint64_t)(part_rows * pitch * 2)};
-  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  cuuint64_t strides[2] = {(cuuint64_t)(pitch * es), (cuuint64_t)(part_rows * pitch * es)};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / es), (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+  return enc(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base),
+             dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
-  const int smem = a.stages * stage_bytes_of(PARTS, a.bn) + 1024;
+  const int smem =
+      a.stages * stage_bytes_of(PARTS, a.bn) + (staged_out(KIND, PARTS) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -848,7 +956,7 @@ cudaError_t rows_of(const Layout &L, const void *x, int64_t xs, const void *w, i
     return cudaSuccess;
   }
   auto pack = [&](const void *src, int64_t rows, int64_t stride, size_t off) {
-    const unsigned grid = (unsigned)std::min<int64_t>(rows, 32 * tc::sm_count());
+    const unsigned grid = (unsigned)std::min<int64_t>(up(rows, 8), 8 * tc::sm_count());
     __nv_bfloat16 *dst = (__nv_bfloat16 *)(ws + off);
     if (L.parts == 3)
       ce_pack_kernel<3, float><<<grid, 256, 0, st>>>((const float *)src, rows, D, stride, L.pitch, dst);
@@ -862,9 +970,22 @@ cudaError_t rows_of(const Layout &L, const void *x, int64_t xs, const void *w, i
   return e != cudaSuccess ? e : pack(w, V, D, L.off_w);
 }
 
+cudaError_t add_splits(const float *part, int splits, int64_t n, int32_t dtype, void *out, cudaStream_t st) {
+  const unsigned grid = (unsigned)std::min<int64_t>(up(n, 1024), 16 * tc::sm_count());
+  const bool wide = n % 4 == 0 && ((uintptr_t)out & 15) == 0;
+  if (dtype == GLACORE_BF16)
+    wide ? ce_sum_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(part, splits, n, (__nv_bfloat16 *)out)
+         : ce_sum_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(part, splits, n, (__nv_bfloat16 *)out);
+  else
+    wide ? ce_sum_kernel<float, true><<<grid, 256, 0, st>>>(part, splits, n, (float *)out)
+         : ce_sum_kernel<float, false><<<grid, 256, 0, st>>>(part, splits, n, (float *)out);
+  mark_launch("ce_sum", st);
+  return cudaGetLastError();
+}
+
 glacore_status check(const void *x, const void *w, int64_t N, int64_t D, int64_t V, int64_t xs, int32_t dtype) {
   const int64_t lim = (int64_t)1 << 30;
-  if (N < 0 || D < 1 || V < 1 || N > lim || D > lim || V > lim || (xs != 0 && xs < D) ||
+  if (N < 0 || D < 1 || V < 1 || N > lim || D > (1 << 22) - 64 || V > lim || (xs != 0 && xs < D) ||
       (dtype != GLACORE_BF16 && dtype != GLACORE_F32))
     return GLACORE_ERR_INVALID_ARG;
   if (N == 0) return GLACORE_OK;
@@ -913,7 +1034,7 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   whole_k(g, N, V, D, L.bn_z);
   a.units0 = a.units = (int64_t)g.mt * g.nt;
   a.bn = L.bn_z;
-  a.stages = stages_of(L.parts, a.bn);
+  a.stages = stages_of(STATS, L.parts, a.bn);
   a.N = N;
   a.V = V;
   a.target = target;
@@ -949,21 +1070,12 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   if (e != cudaSuccess) return status_of(e);
   int *err = device_error_ptr();
   const __nv_bfloat16 *xt = (const __nv_bfloat16 *)(ws + L.off_xt);
-  const float *unit = nullptr;
-  {
-    const dim3 grid((unsigned)up(N, 64), (unsigned)up(D, 64), (unsigned)L.parts);
-    if (grid.y > 65535u) return GLACORE_ERR_UNSUPPORTED;
-    ce_transpose_kernel<<<grid, 256, 0, st>>>((const __nv_bfloat16 *)r.x, N, D, r.xp, L.xt_pitch,
-                                              (__nv_bfloat16 *)(ws + L.off_xt));
-    mark_launch("ce_transpose", st);
-    if ((e = cudaGetLastError()) != cudaSuccess) return status_of(e);
-    if (L.parts == 1) {  // three parts hold dloss as it is
-      unit = (const float *)(ws + L.off_unit);
-      ce_unit_kernel<<<1, 1024, 0, st>>>(dloss, target, N, V, (float *)(ws + L.off_unit));
-      mark_launch("ce_unit", st);
-      if ((e = cudaGetLastError()) != cudaSuccess) return status_of(e);
-    }
-  }
+  float *unit = L.parts == 1 ? (float *)(ws + L.off_unit) : nullptr;  // three parts hold dloss as it is
+  const dim3 grid((unsigned)up(N, 64) + 1, (unsigned)up(D, 64), (unsigned)L.parts);
+  ce_prepare_kernel<<<grid, 256, 0, st>>>((const __nv_bfloat16 *)r.x, N, D, r.xp, L.xt_pitch,
+                                          (__nv_bfloat16 *)(ws + L.off_xt), dloss, target, V, unit);
+  mark_launch("ce_prepare", st);
+  if ((e = cudaGetLastError()) != cudaSuccess) return status_of(e);
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, cols = std::min(L.piece, V - v0);
     // the piece's rows of w (its parts stay V rows apart)
@@ -971,7 +1083,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     Args a;
     memset(&a, 0, sizeof(a));
     a.bn = L.bn_z;
-    a.stages = stages_of(L.parts, a.bn);
+    a.stages = stages_of(GRAD, L.parts, a.bn);
     a.N = N;
     a.V = V;
     a.v0 = v0;
@@ -991,13 +1103,16 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, box_of(N, 128)) || !w_map(&a.g[0].b, box_of(cols, L.bn_z / 2)))
       return status_of(cudaErrorInvalidValue);
     whole_k(a.g[0], N, cols, D, L.bn_z);
+    // all of G's columns: the tiles' are written whole
+    if (L.parts == 1 && !make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, 1, L.gpitch, N, 32))
+      return status_of(cudaErrorInvalidValue);
     a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
     e = ce::launch<GRAD>(a, L.parts, st);
     mark_launch("ce_grad", st);
     if (e != cudaSuccess) return status_of(e);
     // dx^T (K = the piece) and dw of the piece (K = the tokens)
     a.bn = L.bn;
-    a.stages = stages_of(L.parts, a.bn);
+    a.stages = stages_of(PRODUCT, L.parts, a.bn);
     Gemm &gx = a.g[0], &gw = a.g[1];
     if (!w_map(&gx.a, 64) || !g_map(&gx.b, box_of(N, L.bn / 2)) || !g_map(&gw.a, 64) ||
         !make_map3(&gw.b, xt, N, D, L.parts, L.xt_pitch, D, box_of(D, L.bn / 2)))
@@ -1012,27 +1127,24 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     gx.out = L.dx_f32 ? (void *)(ws + L.off_dx) : dx;
     whole_k(gw, cols, D, N, L.bn);
     gw.a_mn = 1;
-    gw.out_f32 = dtype == GLACORE_F32;
-    gw.out = (char *)dw + (size_t)v0 * D * es;
+    gw.kb_split = L.run_w;
+    gw.splits = L.splits_w;
+    char *dw_piece = (char *)dw + (size_t)v0 * D * es;
+    gw.out_f32 = L.dw_sums || dtype == GLACORE_F32;
+    gw.out = L.dw_sums ? ws + L.off_dw : dw_piece;
+    gw.tma_out = L.parts == 1 && D % 8 == 0;
+    if (gw.tma_out && !make_map3(&gw.o, gw.out, D, cols, gw.splits, D, cols, 32, gw.out_f32))
+      return status_of(cudaErrorInvalidValue);
     a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
-    a.units = a.units0 + (int64_t)gw.mt * gw.nt;
+    a.units = a.units0 + (int64_t)gw.mt * gw.nt * gw.splits;
+    a.skip = deal(a.units0, gx.kb_split, a.units - a.units0, gw.kb_split).skip;
     e = ce::launch<PRODUCT>(a, L.parts, st);
     mark_launch("ce_product", st);
+    if (e == cudaSuccess && L.dw_sums)
+      e = add_splits((const float *)(ws + L.off_dw), gw.splits, cols * D, dtype, dw_piece, st);
     if (e != cudaSuccess) return status_of(e);
   }
-  if (L.dx_f32) {
-    const int64_t n = N * D;
-    const unsigned grid = (unsigned)std::min<int64_t>(up(n, 1024), 16 * tc::sm_count());
-    const float *p = (const float *)(ws + L.off_dx);
-    if (dtype == GLACORE_BF16)
-      n % 4 == 0 ? ce_dx_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(p, L.splits, n, (__nv_bfloat16 *)dx)
-                 : ce_dx_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(p, L.splits, n, (__nv_bfloat16 *)dx);
-    else
-      n % 4 == 0 ? ce_dx_kernel<float, true><<<grid, 256, 0, st>>>(p, L.splits, n, (float *)dx)
-                 : ce_dx_kernel<float, false><<<grid, 256, 0, st>>>(p, L.splits, n, (float *)dx);
-    mark_launch("ce_dx", st);
-    e = cudaGetLastError();
-  }
+  if (L.dx_f32) e = add_splits((const float *)(ws + L.off_dx), L.splits, N * D, dtype, dx, st);
   return status_of(e);
 }
 

@@ -49,12 +49,30 @@ __device__ __forceinline__ void store(void *p, int bf16, int64_t i, float x) {
     reinterpret_cast<float *>(p)[i] = x;
 }
 
+// Two fp32 operations per instruction: o = a b + c, and o = a b.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 o;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return o;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 o;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return o;
+}
+
 // COLT threads side by side cover 4 COLT value columns; VEC: V is a multiple
 // of 4 and the pool 16-byte aligned.
 template <int COLT, int KR, bool VEC>
-__global__ void __launch_bounds__(THREADS, KR <= 8 ? 4 : 2) step_kernel(const Args a) {
+__global__ void __launch_bounds__(THREADS, 4) step_kernel(const Args a) {
   constexpr int ROWT = THREADS / COLT, COLS = 4 * COLT;
-  __shared__ float s_q[TOKENS][ROWT * KR], s_k[TOKENS][ROWT * KR], s_a[TOKENS][ROWT * KR];
+  __shared__ float4 s_akq[TOKENS][ROWT * KR];  // decay, k, scale q of a key row
   __shared__ float s_v[TOKENS][COLS];
   __shared__ float s_o[TOKENS][WARPS][COLS];
   const int slice = blockIdx.x % a.slices;
@@ -73,25 +91,30 @@ __global__ void __launch_bounds__(THREADS, KR <= 8 ? 4 : 2) step_kernel(const Ar
     return;
   }
   float *S = a.state + (slot * a.H + h) * a.K * a.V;
-  float st[KR][4];
+  float2 st[KR][2];
 #pragma unroll
   for (int j = 0; j < KR; ++j) {
     const int c = row + j * ROWT;
     if (VEC) {
       float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
       if (c < a.K && v0 + 4 * col < a.V) f = *reinterpret_cast<const float4 *>(S + (int64_t)c * a.V + v0 + 4 * col);
-      st[j][0] = f.x; st[j][1] = f.y; st[j][2] = f.z; st[j][3] = f.w;
+      st[j][0] = make_float2(f.x, f.y);
+      st[j][1] = make_float2(f.z, f.w);
     } else {
+      float f[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int vc = v0 + col + e * COLT;
-        st[j][e] = c < a.K && vc < a.V ? S[(int64_t)c * a.V + vc] : 0.f;
+        f[e] = c < a.K && vc < a.V ? S[(int64_t)c * a.V + vc] : 0.f;
       }
+      st[j][0] = make_float2(f[0], f[1]);
+      st[j][1] = make_float2(f[2], f[3]);
     }
   }
   for (int64_t t0 = 0; t0 < a.T; t0 += TOKENS) {
     const int n = (int)(a.T - t0 < TOKENS ? a.T - t0 : TOKENS);
     if (t0) __syncthreads();  // the last tokens' rows have been used
+    bool forgets = false;
     for (int i = threadIdx.x; i < n * (ROWT * KR); i += THREADS) {
       const int t = i / (ROWT * KR), c = i % (ROWT * KR);
       const int64_t tok = b * a.T + t0 + t;
@@ -101,30 +124,35 @@ __global__ void __launch_bounds__(THREADS, KR <= 8 ? 4 : 2) step_kernel(const Ar
         k = load(a.k, a.bf16, tok * a.ks + (int64_t)hq * a.K + c);
         d = expf(a.head_gate ? a.g[tok * a.H + h] : a.g[(tok * a.H + h) * a.K + c]);
       }
-      s_q[t][c] = q;
-      s_k[t][c] = k;
-      s_a[t][c] = d;
+      forgets |= c < a.K && d == 0.f;
+      s_akq[t][c] = make_float4(d, k, q, 0.f);
     }
     for (int i = threadIdx.x; i < n * COLS; i += THREADS) {
       const int t = i / COLS, c = i % COLS;
       s_v[t][c] = v0 + c < a.V ? load(a.v, a.bf16, (b * a.T + t0 + t) * a.vs + (int64_t)h * a.V + v0 + c) : 0.f;
     }
-    __syncthreads();
+    forgets = __syncthreads_or(forgets);
     for (int t = 0; t < n; ++t) {
-      float v[4], o[4] = {0.f, 0.f, 0.f, 0.f};
+      if (forgets) {  // a decay of exactly 0 forgets whatever the slot held, NaN included
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = s_v[t][VEC ? 4 * col + e : col + e * COLT];
+        for (int j = 0; j < KR; ++j)
+          if (s_akq[t][row + j * ROWT].x == 0.f) st[j][0] = st[j][1] = make_float2(0.f, 0.f);
+      }
+      float2 v[2], acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        v[e] = make_float2(s_v[t][VEC ? 4 * col + 2 * e : col + 2 * e * COLT],
+                           s_v[t][VEC ? 4 * col + 2 * e + 1 : col + (2 * e + 1) * COLT]);
 #pragma unroll
       for (int j = 0; j < KR; ++j) {
-        const int c = row + j * ROWT;
-        const float d = s_a[t][c], k = s_k[t][c], q = s_q[t][c];
+        const float4 r = s_akq[t][row + j * ROWT];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          // a decay of exactly 0 forgets whatever the slot held, NaN included
-          st[j][e] = fmaf(k, v[e], d == 0.f ? 0.f : d * st[j][e]);
-          o[e] = fmaf(q, st[j][e], o[e]);
+        for (int e = 0; e < 2; ++e) {
+          st[j][e] = fma2(make_float2(r.y, r.y), v[e], mul2(make_float2(r.x, r.x), st[j][e]));
+          acc[e] = fma2(make_float2(r.z, r.z), st[j][e], acc[e]);
         }
       }
+      float o[4] = {acc[0].x, acc[0].y, acc[1].x, acc[1].y};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
 #pragma unroll
@@ -148,13 +176,14 @@ __global__ void __launch_bounds__(THREADS, KR <= 8 ? 4 : 2) step_kernel(const Ar
     const int c = row + j * ROWT;
     if (VEC) {
       if (c < a.K && v0 + 4 * col < a.V)
-        *reinterpret_cast<float4 *>(S + (int64_t)c * a.V + v0 + 4 * col) =
-            make_float4(st[j][0], st[j][1], st[j][2], st[j][3]);
+        __stcs(reinterpret_cast<float4 *>(S + (int64_t)c * a.V + v0 + 4 * col),  // not read again in this call
+               make_float4(st[j][0].x, st[j][0].y, st[j][1].x, st[j][1].y));
     } else {
+      const float f[4] = {st[j][0].x, st[j][0].y, st[j][1].x, st[j][1].y};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int vc = v0 + col + e * COLT;
-        if (c < a.K && vc < a.V) S[(int64_t)c * a.V + vc] = st[j][e];
+        if (c < a.K && vc < a.V) S[(int64_t)c * a.V + vc] = f[e];
       }
     }
   }
@@ -196,17 +225,19 @@ cudaError_t launch(const glacore_problem *p, bool head_gate, float *state, int64
   a.head_gate = head_gate;
   a.scale = p->scale;
   const bool vec = p->V % 4 == 0 && ((uintptr_t)state & 15) == 0;
-  // columns of a CTA by V, key rows of a thread by K
+  // Columns of a CTA by V: 64 where they waste no more than 32 would; key rows
+  // of a thread by K, no more than 8 (64 registers: four CTAs per SM).
+  const int64_t over64 = (p->V + 63) / 64 * 64, over32 = (p->V + 31) / 32 * 32;
   cudaError_t e;
-  if (p->V > 32)
-    e = p->K <= 64 ? launch_as<16, 4>(a, p->B, vec, st)
-                   : p->K <= 128 ? launch_as<16, 8>(a, p->B, vec, st) : launch_as<16, 16>(a, p->B, vec, st);
-  else if (p->V > 16)
-    e = p->K <= 64 ? launch_as<8, 2>(a, p->B, vec, st)
-                   : p->K <= 128 ? launch_as<8, 4>(a, p->B, vec, st) : launch_as<8, 8>(a, p->B, vec, st);
-  else
+  if (p->V <= 16)
     e = p->K <= 64 ? launch_as<4, 1>(a, p->B, vec, st)
                    : p->K <= 128 ? launch_as<4, 2>(a, p->B, vec, st) : launch_as<4, 4>(a, p->B, vec, st);
+  else if (p->K > 128)
+    e = launch_as<8, 8>(a, p->B, vec, st);
+  else if (over32 < over64)
+    e = p->K <= 64 ? launch_as<8, 2>(a, p->B, vec, st) : launch_as<8, 4>(a, p->B, vec, st);
+  else
+    e = p->K <= 64 ? launch_as<16, 4>(a, p->B, vec, st) : launch_as<16, 8>(a, p->B, vec, st);
   mark_launch(head_gate ? "ssd_step" : "gla_step", st);
   return e;
 }

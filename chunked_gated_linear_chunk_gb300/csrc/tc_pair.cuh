@@ -71,6 +71,14 @@ __device__ __forceinline__ bool mbar_wait_at(uint32_t bar, uint32_t parity, long
     if (clock64() - t0 > max_cycles) return false;
   return true;
 }
+// Tile store shared -> global by shared address (bulk group of the issuing
+// thread); what lies past the tensor's extent is not written.
+__device__ __forceinline__ void tma_store_3d_at(const CUtensorMap *m, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   (uint64_t)m),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 // 2^x, flushing subnormal results.
 __device__ __forceinline__ float ex2(float x) {
   float r;

@@ -358,7 +358,7 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean,
  *     scored),  dx = G w,  dw = G^T x
  *   dloss       [N] fp32
  *   dx          [N, D], dw [V, D] (dtype), contiguous, written
- * Any N >= 0, D, V up to 2^30.  x, w, dx and dw 16-byte aligned; for bf16
+ * Any N >= 0 and V up to 2^30, D up to 2^22 - 64.  x, w, dx and dw 16-byte aligned; for bf16
  * with D a multiple of 8, x_stride as well.  bf16 products run on the tensor
  * cores with fp32 sums, G rounded to bf16 for them; fp32 operands are split
  * exactly into three bf16 parts (results to fp32's accuracy).  x and w must be

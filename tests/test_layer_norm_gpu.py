@@ -50,6 +50,9 @@ CASES = [
     (8192, 2048, torch.bfloat16), (5000, 2048, torch.float32), (77, 1111, torch.float32),
     (2000, 1111, torch.bfloat16), (9, 4095, torch.bfloat16), (650, 4096, torch.float32), (3, 8192, torch.bfloat16),
     (40, 8191, torch.float32), (5, 8193, torch.float32), (70, 20000, torch.bfloat16), (2, 20001, torch.float32),
+    # rows on 4-byte addresses, and between them
+    (33, 30, torch.bfloat16), (400, 1334, torch.bfloat16), (3, 4098, torch.bfloat16), (7, 8190, torch.bfloat16),
+    (31, 4097, torch.bfloat16), (700, 8191, torch.bfloat16), (600, 1024, torch.float32), (2500, 17, torch.bfloat16),
 ]
 
 
@@ -82,7 +85,7 @@ def test_without_weights(cuda_ok, dtype):
     assert close(got[0], want[0]) and rel(got[1], want[1]) <= TOL_DW and rel(got[2], want[2]) <= TOL_DW
 
 
-@pytest.mark.parametrize("stride,offset", [(128, 0), (136, 8), (131, 0), (128, 3)])
+@pytest.mark.parametrize("stride,offset", [(128, 0), (136, 8), (131, 0), (128, 3), (130, 0), (130, 2), (130, 1)])
 def test_strided_and_misaligned_rows(cuda_ok, stride, offset):
     """x and dy as columns of a wider tensor: 16-byte aligned, or not."""
     wide, wide_dy, w, b = data(40, 160, torch.bfloat16, 6)

@@ -76,6 +76,8 @@ CASES = [
     (1, 8, 1, torch.float32), (5, 64, 100, torch.float32), (130, 77, 129, torch.float32),
     (256, 256, 384, torch.float32), (301, 520, 2000, torch.float32), (2, 1030, 700, torch.float32),
     (40, 16, 20011, torch.float32),
+    # many tokens, little else: dw's sum over the tokens is cut
+    (4655, 48, 423, torch.bfloat16), (3001, 33, 300, torch.bfloat16), (2600, 40, 301, torch.float32),
 ]
 
 
