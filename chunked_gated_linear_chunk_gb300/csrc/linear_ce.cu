@@ -34,13 +34,15 @@
 //
 // fp32 operands: each value is cut exactly into three bf16 parts (8 + 8 + 8
 // significant bits) and a product of two values is six of the nine products
-// of their parts (the rest is below 2^-24 of it).  The large product and the
-// five corrections have accumulators of their own.
+// of their parts (the rest is below 2^-24 of it).
 // Wherever a result is fp32 (the loss; everything of fp32 operands) the
 // accumulators are added up in fp32 registers every few k-blocks (chunk_of):
 // the tensor core's running sum is not rounded to nearest, and over hundreds
 // of steps that shows (loss of 8192 x 2048 x 32000: 1.2e-6 off with one sum
-// over K = 2048).
+// over K = 2048).  With fp32 operands that is every k-block, the small products
+// of its parts first, so that only the large one's four steps lose anything
+// (gradients of 1001 x 520 x 10007: 1.1e-6 off; 2.7e-6 with the small products
+// summed apart and all four k-blocks at a time, in 12% less time).
 #include <string.h>
 
 #include <algorithm>
@@ -93,8 +95,6 @@ struct Args {
   float *zt;         // STATS: [N] the target's logit
   const float *lse, *dloss;  // GRAD
   const float *unit;         // G is in units of *unit (null: 1)
-  __nv_bfloat16 *G;          // GRAD: [PARTS][N][gpitch]
-  int64_t gpitch;
   int *err;
 };
 
@@ -148,18 +148,20 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
   return t;
 }
 
+// Accumulators in TMEM: the epilogue of one runs under the products of the
+// others.  (fp32 operands: tiles of 128 columns, handed over every k-block.)
+constexpr int bufs_of(int parts) { return parts == 3 ? 4 : 2; }
 constexpr int stage_bytes_of(int parts, int bn) { return parts * (int)(A_BYTES + bn * BK); }
-// G and dw of bf16 operands leave through shared memory and TMA: a warp's
-// direct stores of 32 rows touch 32 lines each, and a product over few k-blocks
-// is bound by them (backward of 16 x 2048 x 32000: 116 us with direct stores,
-// 110 us so).  Three parts leave no room for it.
-constexpr bool staged_out(int kind, int parts) { return kind != STATS && parts == 1; }
+// G and dw leave through shared memory and TMA: a warp's direct stores of 32
+// rows touch 32 lines each, and a product over few k-blocks is bound by them
+// (backward of 16 x 2048 x 32000: 116 us with direct stores, 110 us so).
+constexpr bool staged_out(int kind) { return kind != STATS; }
 constexpr int stages_of(int kind, int parts, int bn) {
-  const int n = (SMEM - (staged_out(kind, parts) ? EPI_WARPS * (int)OUT_BYTES : 0)) / stage_bytes_of(parts, bn);
+  const int n = (SMEM - (staged_out(kind) ? EPI_WARPS * (int)OUT_BYTES : 0)) / stage_bytes_of(parts, bn);
   return n < MAX_STAGES ? n : MAX_STAGES;
 }
 // k-blocks whose products one accumulator sums
-constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 4 : kind == STATS ? 16 : 1 << 30; }
+constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 1 : kind == STATS ? 16 : 1 << 30; }
 
 // The six products of parts (a, b), small ones first; the last is the large
 // one (bf16 operands: the only one).
@@ -182,8 +184,10 @@ __device__ __forceinline__ uint32_t load_bytes(const Gemm &g, const Tile &t, int
 template <int KIND, int PARTS>
 __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_constant__ Args a) {
   constexpr int CHUNK = chunk_of(KIND, PARTS);
+  constexpr bool CHUNKED = KIND == STATS || PARTS == 3;
+  constexpr int BUFS = bufs_of(PARTS), BUF_COLS = 512 / BUFS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[2], acc_empty[2], drained;
+  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[BUFS], acc_empty[BUFS], drained;
   __shared__ uint32_t tmem_ptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < BUFS; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 2 * EPI_WARPS);
     }
@@ -287,8 +291,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         const SDesc ad0 = sdesc_sw128(smem, a_mn ? 8192 : 16, 1024);
         const SDesc bd0 = sdesc_sw128(smem + PARTS * A_BYTES, 16, 1024);
         for (int left = t.kb1 - t.kb0; left > 0 && ok; ++hand) {
-          const uint32_t buf = hand & 1;
-          if (!mbar_wait_cluster(&acc_empty[buf], (hand / 2 + 1) & 1, WAIT_CYCLES)) {
+          const uint32_t buf = hand % BUFS;
+          if (!mbar_wait_cluster(&acc_empty[buf], (hand / BUFS + 1) & 1, WAIT_CYCLES)) {
             set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
@@ -307,13 +311,12 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
             const SDesc as = ad0 + s * stage_bytes, bs = bd0 + s * stage_bytes;
 #pragma unroll
             for (int i = PARTS == 1 ? 5 : 0; i < 6; ++i) {
-              const bool large = i == 5;
-              const uint32_t d = tmem + buf * 256 + (large ? 0 : 128);
+              const uint32_t d = tmem + buf * BUF_COLS;
               const SDesc ad = as + (PARTS == 1 ? 0 : PA[i] * A_BYTES);
               const SDesc bd = bs + (PARTS == 1 ? 0 : PB[i] * b_bytes);
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
-                mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc, more | (uint32_t)(k > 0 || !(large || i == 0)));
+                mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc, more | (uint32_t)(k > 0 || i > (PARTS == 1 ? 5 : 0)));
             }
             more = 1;
             mma_commit_pair(empty0 + 8 * s);
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
     };
     const float unit = KIND != STATS && a.unit ? *a.unit : 1.f;
-    int64_t hand = 0;
+    uint32_t hand = 0;
     bool ok = true;
     Walk walk(a, pair, pairs);
     for (int64_t u; ok && (u = walk.next()) >= 0;) {
@@ -380,220 +383,184 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           dl = a.dloss[row] / unit;
         }
       }
-      // 32 columns c0 + c .. of the row
-      auto use = [&](int c, float (&v)[32]) {
+      // 64 columns c0 + c .. of the row
+      auto use = [&](int c, float (&v)[64]) {
         const int64_t col = c0 + c;
         if constexpr (KIND == STATS) {
           const int64_t room = min(a.V - col, (int64_t)(cols - c));  // columns of the vocabulary, of this warp here
           if (room <= 0) return;
-          if (room < 32) {
+          if (room < 64) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 64; ++i)
               if (i >= room) v[i] = -INFINITY;
           }
           if (tgt >= col && tgt < col + room) {
             float z = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 64; ++i)
               if (tgt == col + i) z = v[i];
             if (live) a.zt[row] = z;
           }
-          float top = mx;
+          float top[4] = {mx, v[0], v[1], v[2]};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+          for (int i = 3; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
+          const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           // a row of -inf so far: any finite reference gives sums of 0
-          const float ref = top == -INFINITY ? 0.f : top * LOG2E;
+          const float ref = peak == -INFINITY ? 0.f : peak * LOG2E;
           float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) s[i & 3] += ex2(fmaf(v[i], LOG2E, -ref));
+          for (int i = 0; i < 64; ++i) s[i & 3] += ex2(fmaf(v[i], LOG2E, -ref));
           const float old = mx == -INFINITY ? 0.f : sum * ex2(mx * LOG2E - ref);
           sum = old + ((s[0] + s[1]) + (s[2] + s[3]));
-          mx = top;
+          mx = peak;
         } else if constexpr (KIND == GRAD) {
+          if (c >= cols) return;
           const bool scored = tgt >= 0;
           const int64_t hit = tgt - a.v0 - col;
           // the difference first: a product of either with log2 e would round
           // by more than 1 at logits of some 10^4
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
+          for (int i = 0; i < 64; ++i)
             v[i] = PARTS == 1 ? ex2((v[i] - lse) * LOG2E) : expf(v[i] - lse);
-          if (hit >= 0 && hit < 32) {
+          if (hit >= 0 && hit < 64) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 64; ++i)
               if (hit == i) v[i] -= 1.f;
           }
           // a token that is not scored has no gradient, whatever its logits are
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = scored ? v[i] * dl : 0.f;
-          if constexpr (PARTS == 1) {
-            if (!(c & 32)) begin_out();
+          for (int i = 0; i < 64; ++i) v[i] = scored ? v[i] * dl : 0.f;
+          if (row - lane >= g.m) return;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              put(i + (c & 32) / 8, pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                  pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-            if ((c & 32) && row - lane < g.m) send_out(&g.o, (int)col - 32, (int)(row - lane), 0);
-          } else {
-            if (!live) return;
+          for (int p = 0; p < PARTS; ++p) {
+            begin_out();
 #pragma unroll
-            for (int p = 0; p < PARTS; ++p) {
-              __nv_bfloat16 *out = a.G + ((int64_t)p * a.N + row) * a.gpitch + col;
+            for (int i = 0; i < 8; ++i) {
+              uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 32; i += 16) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {  // the leading 8 bits of what is left, exactly
-                  float &x = v[i + 2 * j], &y = v[i + 2 * j + 1];
+              for (int j = 0; j < 4; ++j) {
+                float &x = v[8 * i + 2 * j], &y = v[8 * i + 2 * j + 1];
+                if (PARTS == 1) {
+                  w[j] = pack_bf16(x, y);
+                } else {  // the leading 8 bits of what is left, exactly
                   const uint32_t xb = __float_as_uint(x) & 0xffff0000u, yb = __float_as_uint(y) & 0xffff0000u;
                   w[j] = (xb >> 16) | yb;
                   x -= __uint_as_float(xb);
                   y -= __uint_as_float(yb);
                 }
-                st_global_v8(out + i, w);
               }
+              put(i, w[0], w[1], w[2], w[3]);
             }
+            send_out(&g.o, (int)col, (int)(row - lane), p);
           }
         } else {
-          if (col - (c & 32) >= g.n || row - lane >= g.m) return;  // nothing of the warp's 64 columns is there
+          if (c >= cols || col >= g.n || row - lane >= g.m) return;  // nothing of the warp's columns is there
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= unit;
-          if (PARTS == 1 && g.tma_out) {  // what lies past the edges is not written
+          for (int i = 0; i < 64; ++i) v[i] *= unit;
+          const int room = g.n - col < 64 ? (int)(g.n - col) : 64;
+          if (g.tma_out) {  // what lies past the edges is not written
             if (g.out_f32) {
+#pragma unroll
+              for (int h = 0; h < 64; h += 32) {
+                if (h >= room) break;
+                begin_out();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  put(i, __float_as_uint(v[h + 4 * i]), __float_as_uint(v[h + 4 * i + 1]),
+                      __float_as_uint(v[h + 4 * i + 2]), __float_as_uint(v[h + 4 * i + 3]));
+                send_out(&g.o, (int)col + h, (int)(row - lane), t.split);
+              }
+            } else {
               begin_out();
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                put(i, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                    __float_as_uint(v[4 * i + 3]));
-              if (col < g.n) send_out(&g.o, (int)col, (int)(row - lane), t.split);
-            } else {
-              if (!(c & 32)) begin_out();
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                put(i + (c & 32) / 8, pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
+                put(i, pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
                     pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-              if (c & 32) send_out(&g.o, (int)col - 32, (int)(row - lane), 0);
+              send_out(&g.o, (int)col, (int)(row - lane), 0);
             }
             return;
           }
-          if (!live || col >= g.n) return;
-          const int room = g.n - col < 32 ? (int)(g.n - col) : 32;
-          if (g.trans) {  // the warp's 32 rows lie side by side
-            const int64_t at = col * g.m + row;
-            if (g.out_f32) {
-              float *out = reinterpret_cast<float *>(g.out) + (int64_t)t.split * g.m * g.n + at;
-              float old[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) old[i] = g.add && i < room ? out[i * g.m] : 0.f;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < room) out[i * g.m] = v[i] + old[i];
-            } else if (PARTS == 1) {
-              __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + at;
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < room) out[i * g.m] = __float2bfloat16_rn(v[i]);
-            }
-            return;
-          }
-          const bool whole = room == 32 && g.n % 8 == 0;
+          if (!live) return;
+          // C^T: the warp's 32 rows lie side by side.  C: rows that TMA cannot
+          // address.
+          const int64_t step = g.trans ? g.m : 1;
+          const int64_t at = g.trans ? col * g.m + row : row * g.n + col;
           if (g.out_f32) {
-            float *out = reinterpret_cast<float *>(g.out) + ((int64_t)t.split * g.m + row) * g.n + col;
-            if (whole) {
+            float *out = reinterpret_cast<float *>(g.out) + (int64_t)t.split * g.m * g.n + at;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4 *>(out + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            } else {
+            for (int h = 0; h < 64; h += 16) {
+              float old[16];
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < room) out[i] = v[i];
+              for (int i = 0; i < 16; ++i) old[i] = g.add && h + i < room ? out[(h + i) * step] : 0.f;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (h + i < room) out[(h + i) * step] = v[h + i] + old[i];
             }
           } else if (PARTS == 1) {
-            __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + row * g.n + col;
+            __nv_bfloat16 *out = reinterpret_cast<__nv_bfloat16 *>(g.out) + at;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < room) out[i] = __float2bfloat16_rn(v[i]);
+            for (int i = 0; i < 64; ++i)
+              if (i < room) out[i * step] = __float2bfloat16_rn(v[i]);
           }
         }
       };
-      if constexpr (PARTS == 1) {
-        // sums of the chunks so far (up to 128 columns)
-        float acc[KIND == STATS ? 4 : 1][32];
+      constexpr int HALVES = PARTS == 3 ? 1 : 2;  // 64 columns each of a warp's, at most
+      constexpr int SUMS = CHUNKED ? HALVES : 1;
+      float acc[SUMS][64];  // the chunks so far
+      if (CHUNKED)
 #pragma unroll
-        for (int j = 0; j < (KIND == STATS ? 4 : 1); ++j)
+        for (int j = 0; j < SUMS; ++j)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) acc[j][i] = 0.f;
-        for (int kb = t.kb0; kb < t.kb1; kb += min(t.kb1 - kb, CHUNK), ++hand) {
-          const int buf = (int)(hand & 1);
-          if (!mbar_wait_at(smem_u32(&acc_full[buf]), (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
-            if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const bool last = t.kb1 - kb <= CHUNK;
+          for (int i = 0; i < 64; ++i) acc[j][i] = 0.f;
+      for (int kb = t.kb0; kb < t.kb1; kb += min(t.kb1 - kb, CHUNK), ++hand) {
+        const int buf = (int)(hand % BUFS);
+        if (!mbar_wait_at(smem_u32(&acc_full[buf]), (hand / BUFS) & 1, WAIT_CYCLES)) {
+          if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool last = t.kb1 - kb <= CHUNK;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (32 * c >= cols) break;
-            if constexpr (KIND == STATS) {
+        for (int j = 0; j < HALVES; ++j) {
+          if (64 * j >= cols) break;
+          float(&v)[64] = acc[CHUNKED ? j : 0];
+          if constexpr (SUMS == 2) {  // few registers beside the sums
 #pragma unroll
-              for (int j = 0; j < 32; j += 16) {  // few registers beside the sums
-                uint32_t r[16];
-                tmem_ld16(lanes + buf * 256 + 32 * c + j, r);
-                tmem_ld_wait(r);
+            for (int h = 0; h < 64; h += 16) {
+              uint32_t r[16];
+              tmem_ld16(lanes + buf * BUF_COLS + 64 * j + h, r);
+              tmem_ld_wait(r);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[c][i + j] += __uint_as_float(r[i]);
-              }
-              if (32 * c + 32 >= cols) release(buf);
-              if (last) use(32 * c, acc[c]);
-            } else {
-              uint32_t r[32];
-              tmem_ld32(lanes + buf * 256 + 32 * c, r);
-              tmem_ld_wait32(r);
-              if (32 * c + 32 >= cols) release(buf);
-              float v[32];
+              for (int i = 0; i < 16; ++i) v[h + i] += __uint_as_float(r[i]);
+            }
+          } else {
+            uint32_t r[32], q[32];
+            tmem_ld32(lanes + buf * BUF_COLS + 64 * j, r);
+            tmem_ld32(lanes + buf * BUF_COLS + 64 * j + 32, q);
+            tmem_ld_wait32(r);
+            tmem_ld_wait32(q);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-              use(32 * c, v);
+            for (int i = 0; i < 32; ++i) {
+              v[i] = (CHUNKED ? v[i] : 0.f) + __uint_as_float(r[i]);
+              v[32 + i] = (CHUNKED ? v[32 + i] : 0.f) + __uint_as_float(q[i]);
             }
           }
+          if (64 * j + 64 >= cols) release(buf);
+          if (!CHUNKED) use(64 * j, v);
         }
-        if (!ok) break;
-      } else {
-        float acc[2][32];  // bn = 128: 64 columns
+        if (CHUNKED && last) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
-        for (int kb = t.kb0; kb < t.kb1; kb += CHUNK, ++hand) {
-          const int buf = (int)(hand & 1);
-          if (!mbar_wait_at(smem_u32(&acc_full[buf]), (uint32_t)(hand / 2) & 1, WAIT_CYCLES)) {
-            if (lane == 0) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t r[32];
-            tmem_ld32(lanes + buf * 256 + 128 + 32 * c, r);
-            tmem_ld_wait32(r);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
-            tmem_ld32(lanes + buf * 256 + 32 * c, r);
-            tmem_ld_wait32(r);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c][i] += __uint_as_float(r[i]);
-          }
-          release(buf);
+          for (int j = 0; j < SUMS; ++j)
+            if (64 * j < cols) use(64 * j, acc[j]);
         }
-        if (!ok) break;
-        use(0, acc[0]);
-        use(32, acc[1]);
       }
+      if (!ok) break;
       if (KIND == STATS && live && c0 < a.V)
         a.part[(int64_t)(2 * t.nt + half) * a.N + row] = make_float2(mx == -INFINITY ? mx : mx * LOG2E, sum);
     }
   }
-  if (staged_out(KIND, PARTS) && warp < EPI_WARPS && lane == 0) bulk_wait_all();
+  if (staged_out(KIND) && warp < EPI_WARPS && lane == 0) bulk_wait_all();
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -910,7 +877,7 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
   const int smem =
-      a.stages * stage_bytes_of(PARTS, a.bn) + (staged_out(KIND, PARTS) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
+      a.stages * stage_bytes_of(PARTS, a.bn) + (staged_out(KIND) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1091,8 +1058,6 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     a.lse = lse;
     a.dloss = dloss;
     a.unit = unit;
-    a.G = (__nv_bfloat16 *)(ws + L.off_g);
-    a.gpitch = L.gpitch;
     a.err = err;
     auto w_map = [&](CUtensorMap *m, int box_rows) {
       return make_map3(m, wp, D, cols, L.parts, r.wp, V, box_rows);
@@ -1104,7 +1069,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
       return status_of(cudaErrorInvalidValue);
     whole_k(a.g[0], N, cols, D, L.bn_z);
     // all of G's columns: the tiles' are written whole
-    if (L.parts == 1 && !make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, 1, L.gpitch, N, 32))
+    if (!make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, L.parts, L.gpitch, N, 32))
       return status_of(cudaErrorInvalidValue);
     a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
     e = ce::launch<GRAD>(a, L.parts, st);
@@ -1132,7 +1097,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     char *dw_piece = (char *)dw + (size_t)v0 * D * es;
     gw.out_f32 = L.dw_sums || dtype == GLACORE_F32;
     gw.out = L.dw_sums ? ws + L.off_dw : dw_piece;
-    gw.tma_out = L.parts == 1 && D % 8 == 0;
+    gw.tma_out = D % (gw.out_f32 ? 4 : 8) == 0;
     if (gw.tma_out && !make_map3(&gw.o, gw.out, D, cols, gw.splits, D, cols, 32, gw.out_f32))
       return status_of(cudaErrorInvalidValue);
     a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
