@@ -168,6 +168,27 @@ cudaError_t sum_channels(int64_t rows, const float *x, float *dg, cudaStream_t s
 // be had); looked up once per device.
 int *device_error_ptr();
 
+// Launch of a kernel that reads what the kernel before it on the stream
+// wrote, without the gap between them: its CTAs may start while the earlier
+// kernel's last ones run, and wait (follow_wait, first thing in the kernel)
+// until that kernel is complete and its writes are visible.  The earlier kernel
+// allows it with follow_allow.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_follow(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void follow_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void follow_allow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Records the next caller-provided timing event (if any) after a launch.
 void mark_launch(const char *label, cudaStream_t st);
 // Maps a CUDA result to a status, remembering the CUDA error of this host

@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     layer_norm_bwd_kernel(const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ mean,
                           const float *__restrict__ rstd, const T *__restrict__ dy, T *__restrict__ dx,
                           float *__restrict__ part, int64_t rows, int D, int64_t xs, int64_t ys, int lg) {
+  follow_allow();
   constexpr int BYTES = VEC * (int)sizeof(T);
   constexpr bool WORDS = BYTES < 4;
   constexpr int R = rows_at_once(NV * VEC);
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(RED_X *RED_Y)
     layer_norm_dw_kernel(const float *__restrict__ part, int64_t n, int64_t D, float *__restrict__ dw,
                          float *__restrict__ db) {
   __shared__ float red[RED_Y][RED_X + 1];
+  follow_wait();
   const int64_t c = (int64_t)blockIdx.x * RED_X + threadIdx.x;
   float acc = 0.f;
   if (c < 2 * D) {
@@ -846,9 +848,10 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean, 
   }
   mark_launch("layer_norm_bwd", st);
   if (e != cudaSuccess) return status_of(e);
-  layer_norm_dw_kernel<<<(unsigned)((2 * D + RED_X - 1) / RED_X), dim3(RED_X, RED_Y), 0, st>>>(part, n, D, dw, db);
+  e = launch_follow(layer_norm_dw_kernel, dim3((unsigned)((2 * D + RED_X - 1) / RED_X)), dim3(RED_X, RED_Y), st,
+                    (const float *)part, n, D, dw, db);
   mark_launch("layer_norm_dw", st);
-  return status_of(cudaGetLastError());
+  return status_of(e);
 }
 
 }  // extern "C"

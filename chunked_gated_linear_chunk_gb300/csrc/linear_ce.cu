@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = tmem_ptr;
+  follow_wait();  // what came before is needed from here on
+  follow_allow();
 
   // Everything the two issuing threads use per k-block is in registers: a
   // parameter read again behind each of their asm statements costs them more
@@ -578,6 +580,7 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
                     const int64_t *__restrict__ target, const float *__restrict__ zt, float *__restrict__ loss,
                     float *__restrict__ lse, int *err) {
   __shared__ float2 red[MERGE_LANES][MERGE_ROWS];
+  follow_wait();
   const int64_t row = (int64_t)blockIdx.x * MERGE_ROWS + threadIdx.x;
   float m = -INFINITY, s = 0.f;
   auto merge = [&](float2 p) {
@@ -612,6 +615,8 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(256)
     ce_sum_kernel(const float *__restrict__ part, int splits, int64_t n, T *__restrict__ dx) {
+  follow_wait();
+  follow_allow();
   if constexpr (WIDE) {
     const float4 *p = reinterpret_cast<const float4 *>(part);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += (int64_t)gridDim.x * 256) {
@@ -648,6 +653,8 @@ __global__ void __launch_bounds__(256)
                       const int64_t *__restrict__ target, int64_t V, float *__restrict__ unit) {
   __shared__ __nv_bfloat162 tile[64][33];
   __shared__ float red[8];
+  follow_wait();
+  follow_allow();
   if (blockIdx.x == gridDim.x - 1) {
     if (!unit || blockIdx.y || blockIdx.z) return;
     float m = 0.f;
@@ -692,6 +699,8 @@ template <int PARTS, typename T>
 __global__ void __launch_bounds__(256)
     ce_pack_kernel(const T *__restrict__ src, int64_t rows, int64_t D, int64_t stride, int64_t pitch,
                    __nv_bfloat16 *__restrict__ dst) {
+  follow_wait();
+  follow_allow();
   const int lane = threadIdx.x & 31;
   for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8) {
 #pragma unroll 4
@@ -874,7 +883,8 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st) {
+// follows: the kernel before it on the stream is one of this call's.
+template <int KIND, int PARTS> cudaError_t launch(const Args &a, bool follows, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
   const int smem =
       a.stages * stage_bytes_of(PARTS, a.bn) + (staged_out(KIND) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
@@ -885,16 +895,18 @@ template <int KIND, int PARTS> cudaError_t launch(const Args &a, cudaStream_t st
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = follows;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
-template <int KIND> cudaError_t launch(const Args &a, int parts, cudaStream_t st) {
-  return parts == 3 ? launch<KIND, 3>(a, st) : launch<KIND, 1>(a, st);
+template <int KIND> cudaError_t launch(const Args &a, int parts, bool follows, cudaStream_t st) {
+  return parts == 3 ? launch<KIND, 3>(a, follows, st) : launch<KIND, 1>(a, follows, st);
 }
 
 // Rows of a K-major operand's load: a CTA's share, or what there is of it.
@@ -940,14 +952,15 @@ cudaError_t rows_of(const Layout &L, const void *x, int64_t xs, const void *w, i
 cudaError_t add_splits(const float *part, int splits, int64_t n, int32_t dtype, void *out, cudaStream_t st) {
   const unsigned grid = (unsigned)std::min<int64_t>(up(n, 1024), 16 * tc::sm_count());
   const bool wide = n % 4 == 0 && ((uintptr_t)out & 15) == 0;
+  cudaError_t e;
   if (dtype == GLACORE_BF16)
-    wide ? ce_sum_kernel<__nv_bfloat16, true><<<grid, 256, 0, st>>>(part, splits, n, (__nv_bfloat16 *)out)
-         : ce_sum_kernel<__nv_bfloat16, false><<<grid, 256, 0, st>>>(part, splits, n, (__nv_bfloat16 *)out);
+    e = launch_follow(wide ? ce_sum_kernel<__nv_bfloat16, true> : ce_sum_kernel<__nv_bfloat16, false>, dim3(grid),
+                      dim3(256), st, part, splits, n, (__nv_bfloat16 *)out);
   else
-    wide ? ce_sum_kernel<float, true><<<grid, 256, 0, st>>>(part, splits, n, (float *)out)
-         : ce_sum_kernel<float, false><<<grid, 256, 0, st>>>(part, splits, n, (float *)out);
+    e = launch_follow(wide ? ce_sum_kernel<float, true> : ce_sum_kernel<float, false>, dim3(grid), dim3(256), st, part,
+                      splits, n, (float *)out);
   mark_launch("ce_sum", st);
-  return cudaGetLastError();
+  return e;
 }
 
 glacore_status check(const void *x, const void *w, int64_t N, int64_t D, int64_t V, int64_t xs, int32_t dtype) {
@@ -1008,14 +1021,14 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   a.part = (float2 *)(ws + L.off_part);
   a.zt = (float *)(ws + L.off_zt);
   a.err = device_error_ptr();
-  e = ce::launch<STATS>(a, L.parts, st);
+  e = ce::launch<STATS>(a, L.parts, L.pack, st);
   mark_launch("ce_stats", st);
   if (e != cudaSuccess) return status_of(e);
   const int64_t slots = up(V, L.bn_z / 2);  // tile halves that hold part of the vocabulary
-  ce_merge_kernel<<<(unsigned)up(N, MERGE_ROWS), dim3(MERGE_ROWS, MERGE_LANES), 0, st>>>(a.part, slots, N, V, target,
-                                                                                       a.zt, loss, lse, a.err);
+  e = launch_follow(ce_merge_kernel, dim3((unsigned)up(N, MERGE_ROWS)), dim3(MERGE_ROWS, MERGE_LANES), st,
+                    (const float2 *)a.part, slots, N, V, target, (const float *)a.zt, loss, lse, a.err);
   mark_launch("ce_merge", st);
-  return status_of(cudaGetLastError());
+  return status_of(e);
 }
 
 glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target, const float *lse,
@@ -1072,7 +1085,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     if (!make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, L.parts, L.gpitch, N, 32))
       return status_of(cudaErrorInvalidValue);
     a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
-    e = ce::launch<GRAD>(a, L.parts, st);
+    e = ce::launch<GRAD>(a, L.parts, true, st);
     mark_launch("ce_grad", st);
     if (e != cudaSuccess) return status_of(e);
     // dx^T (K = the piece) and dw of the piece (K = the tokens)
@@ -1103,7 +1116,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
     a.units = a.units0 + (int64_t)gw.mt * gw.nt * gw.splits;
     a.skip = deal(a.units0, gx.kb_split, a.units - a.units0, gw.kb_split).skip;
-    e = ce::launch<PRODUCT>(a, L.parts, st);
+    e = ce::launch<PRODUCT>(a, L.parts, true, st);
     mark_launch("ce_product", st);
     if (e == cudaSuccess && L.dw_sums)
       e = add_splits((const float *)(ws + L.off_dw), gw.splits, cols * D, dtype, dw_piece, st);
