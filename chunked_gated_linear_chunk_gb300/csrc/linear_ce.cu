@@ -12,7 +12,7 @@
 // CTA loads half of either operand, so every byte brought to an SM feeds
 // twice the products a single CTA's tile would) with three epilogues:
 //   STATS    a tile of logits becomes, per row, its maximum and its sum of
-//            exponentials (one pass, the running maximum rescaled every 32
+//            exponentials (one pass, the running sum rescaled every 64
 //            columns) and the target's logit; the tiles' pairs are merged by
 //            ce_merge_kernel.  The logits leave TMEM and are gone.
 //   GRAD     a tile of logits becomes a tile of G in bf16 (its products with w
@@ -29,8 +29,11 @@
 // transposed once per call for dw's B.
 // Warps of a CTA (320 threads): 0..7 epilogue (a TMEM lane per thread, two
 // warps per lane quarter, each half of the tile's columns), 8 TMA, 9 MMA (of
-// the pair's leader).  Two accumulators in TMEM, so the epilogue of one tile
-// runs under the products of the next.
+// the pair's leader).  Two accumulators in TMEM (four with fp32 operands), so
+// the epilogue of one runs under the products of the next.
+// Measured (8192 x 2048 x 32000 bf16, cool card): forward 557 us, 1930 TFLOP/s;
+// backward 1690 us, 1900 TFLOP/s (kept busy, the card's power limit takes 5 to
+// 15% off both).
 //
 // fp32 operands: each value is cut exactly into three bf16 parts (8 + 8 + 8
 // significant bits) and a product of two values is six of the nine products
@@ -61,12 +64,12 @@ using tc::WAIT_CYCLES;
 
 constexpr int THREADS = 320, EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;
 enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
-constexpr int BM = 256, BK = 64;   // rows of a pair's tile, K of a stage
+constexpr int BM = 256, BK = 64;      // rows of a pair's tile, columns of a k-block
 constexpr uint32_t A_BYTES = 128 * BK * 2;
 constexpr int MAX_STAGES = 12;
 constexpr int SMEM = 231168;          // shared memory of ring and output staging, at most (a KB is left for alignment)
 constexpr uint32_t OUT_BYTES = 4096;  // output staging of a warp: 32 rows of 128 bytes
-constexpr int GROUP_M = 8;         // row tiles that share a walk over the columns (L2 reuse)
+constexpr int GROUP_M = 8;            // row tiles that share a walk over the columns (L2 reuse)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // One product C[m, n] = A B^T over k-blocks, tiles of BM x bn.
@@ -148,16 +151,21 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
   return t;
 }
 
-// Accumulators in TMEM: the epilogue of one runs under the products of the
-// others.  (fp32 operands: tiles of 128 columns, handed over every k-block.)
+// Accumulators in TMEM (fp32 operands: tiles of 128 columns, handed over every
+// k-block).
 constexpr int bufs_of(int parts) { return parts == 3 ? 4 : 2; }
 constexpr int stage_bytes_of(int parts, int bn) { return parts * (int)(A_BYTES + bn * BK); }
 // G and dw leave through shared memory and TMA: a warp's direct stores of 32
 // rows touch 32 lines each, and a product over few k-blocks is bound by them
 // (backward of 16 x 2048 x 32000: 116 us with direct stores, 110 us so).
 constexpr bool staged_out(int kind) { return kind != STATS; }
+// k-blocks of a stage.  Two for the logits: half the waits and commits (8192 x
+// 2048 x 32000 forward 571 -> 546 us on a cool card).  The gradients' products,
+// with an operand in 64-row boxes, ran 3% slower so.
+constexpr int join_of(int kind, int parts) { return parts == 1 && kind != PRODUCT ? 2 : 1; }
 constexpr int stages_of(int kind, int parts, int bn) {
-  const int n = (SMEM - (staged_out(kind) ? EPI_WARPS * (int)OUT_BYTES : 0)) / stage_bytes_of(parts, bn);
+  const int n = (SMEM - (staged_out(kind) ? EPI_WARPS * (int)OUT_BYTES : 0)) /
+                (join_of(kind, parts) * stage_bytes_of(parts, bn));
   return n < MAX_STAGES ? n : MAX_STAGES;
 }
 // k-blocks whose products one accumulator sums
@@ -168,9 +176,8 @@ constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 1 : kind == ST
 __device__ constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
 
 // Bytes of one k-block (and part) that CTA `rank` loads for a tile.  What lies
-// wholly past the end of M or N is not loaded (a load of nothing but fill
-// takes longer than one of data): the operand rows left over from another tile
-// only reach accumulator rows and columns that nobody reads.
+// wholly past the end of M or N is not loaded: whatever is in its place only
+// reaches accumulator rows and columns that nobody reads.
 __device__ __forceinline__ uint32_t load_bytes(const Gemm &g, const Tile &t, int bn, int rank) {
   const int64_t am = t.m0 + rank * 128, bn0 = t.n0 + rank * (bn / 2);
   uint32_t n = bn0 < g.n ? (uint32_t)g.b_box * (BK * 2) : 0;
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   const uint32_t rank = cluster_ctarank();
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t b_bytes = (uint32_t)a.bn * BK;  // bn / 2 rows of BK bf16
-  const uint32_t stage_bytes = PARTS * (A_BYTES + b_bytes);
+  const uint32_t block_bytes = PARTS * (A_BYTES + b_bytes), stage_bytes = join_of(KIND, PARTS) * block_bytes;
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -241,24 +248,28 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         const bool a_mn = g.a_mn, a0 = am < g.m, a1 = am + 64 < g.m, b0 = bn0 < g.n;
         const uint32_t bytes = PARTS * (load_bytes(g, t, a.bn, 0) + load_bytes(g, t, a.bn, 1));
         int k = t.kb0 * BK;
-        for (int n = t.kb1 - t.kb0; n > 0; --n, k += BK) {
+        for (int n = t.kb1 - t.kb0; n > 0; n -= join_of(KIND, PARTS)) {
           if (!mbar_wait_at(empty0 + 8 * s, phase ^ 1, WAIT_CYCLES)) {
             set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx_at(full0 + 8 * s, bytes);
+          if (rank == 0) mbar_expect_tx_at(full0 + 8 * s, bytes * (uint32_t)min(n, join_of(KIND, PARTS)));
           const uint32_t bar = bar0 + 8 * s;
-          const uint32_t sa = smem + s * stage_bytes, sb = sa + PARTS * A_BYTES;
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
-            if (a_mn) {
-              if (a0) tma_load_3d_pair(sa + p * A_BYTES, ma, am, k, p, bar);
-              if (a1) tma_load_3d_pair(sa + p * A_BYTES + 8192, ma, am + 64, k, p, bar);
-            } else if (a0) {
-              tma_load_3d_pair(sa + p * A_BYTES, ma, k, am, p, bar);
+          for (int q = 0; q < join_of(KIND, PARTS); ++q, k += BK) {
+            if (q >= n) break;
+            const uint32_t sa = smem + s * stage_bytes + q * block_bytes, sb = sa + PARTS * A_BYTES;
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) {
+              if (a_mn) {
+                if (a0) tma_load_3d_pair(sa + p * A_BYTES, ma, am, k, p, bar);
+                if (a1) tma_load_3d_pair(sa + p * A_BYTES + 8192, ma, am + 64, k, p, bar);
+              } else if (a0) {
+                tma_load_3d_pair(sa + p * A_BYTES, ma, k, am, p, bar);
+              }
+              if (b0) tma_load_3d_pair(sb + p * b_bytes, mb, k, bn0, p, bar);
             }
-            if (b0) tma_load_3d_pair(sb + p * b_bytes, mb, k, bn0, p, bar);
           }
           if (++s == stages) {
             s = 0;
@@ -303,24 +314,29 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           const int run = min(left, CHUNK);
           left -= run;
           uint32_t more = 0;  // the run's first products overwrite the accumulator
-          for (int n = run; n > 0; --n) {
+          for (int n = run; n > 0; n -= join_of(KIND, PARTS)) {
             if (!mbar_wait_at(full0 + 8 * s, phase, WAIT_CYCLES)) {
               set_device_error(a.err, GLACORE_ERR_TIMEOUT);
               ok = false;
               break;
             }
             tc_fence_after();
-            const SDesc as = ad0 + s * stage_bytes, bs = bd0 + s * stage_bytes;
 #pragma unroll
-            for (int i = PARTS == 1 ? 5 : 0; i < 6; ++i) {
-              const uint32_t d = tmem + buf * BUF_COLS;
-              const SDesc ad = as + (PARTS == 1 ? 0 : PA[i] * A_BYTES);
-              const SDesc bd = bs + (PARTS == 1 ? 0 : PB[i] * b_bytes);
+            for (int q = 0; q < join_of(KIND, PARTS); ++q) {
+              if (q >= n) break;
+              const uint32_t at = s * stage_bytes + q * block_bytes;
 #pragma unroll
-              for (int k = 0; k < BK / 16; ++k)
-                mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc, more | (uint32_t)(k > 0 || i > (PARTS == 1 ? 5 : 0)));
+              for (int i = PARTS == 1 ? 5 : 0; i < 6; ++i) {
+                const uint32_t d = tmem + buf * BUF_COLS;
+                const SDesc ad = ad0 + (at + (PARTS == 1 ? 0 : PA[i] * A_BYTES));
+                const SDesc bd = bd0 + (at + (PARTS == 1 ? 0 : PB[i] * b_bytes));
+#pragma unroll
+                for (int k = 0; k < BK / 16; ++k)
+                  mma_bf16_pair(d, ad + k * astep, bd + k * 32, idesc,
+                                more | (uint32_t)(k > 0 || i > (PARTS == 1 ? 5 : 0)));
+              }
+              more = 1;
             }
-            more = 1;
             mma_commit_pair(empty0 + 8 * s);
             if (++s == stages) {
               s = 0;
@@ -886,8 +902,8 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 // follows: the kernel before it on the stream is one of this call's.
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, bool follows, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
-  const int smem =
-      a.stages * stage_bytes_of(PARTS, a.bn) + (staged_out(KIND) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
+  const int ring = a.stages * join_of(KIND, PARTS) * stage_bytes_of(PARTS, a.bn);
+  const int smem = ring + (staged_out(KIND) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
