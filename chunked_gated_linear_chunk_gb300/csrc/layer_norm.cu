@@ -234,13 +234,6 @@ __global__ void __launch_bounds__(THREADS)
   RowSum<1> sum{red, L, 0};
   const float inv = 1.f / (float)D;
   float *sw = reinterpret_cast<float *>(smem), *sb = sw + (D + 3) / 4 * 4;
-  if (STAGED) {
-    for (int c = threadIdx.x; c < D; c += THREADS) {
-      sw[staged_at<VEC>(c, D)] = w ? w[c] : 1.f;
-      sb[staged_at<VEC>(c, D)] = b ? b[c] : 0.f;
-    }
-    __syncthreads();
-  }
   Vec<T, VEC> xv[NV], next[NV];
   auto fetch = [&](int64_t row, Vec<T, VEC>(&v)[NV]) {
     if (row >= rows) return;
@@ -251,7 +244,14 @@ __global__ void __launch_bounds__(THREADS)
   };
   int64_t row = (int64_t)blockIdx.x * per + (threadIdx.x >> lg);
   const int64_t step = (int64_t)gridDim.x * per;
-  if (EARLY) fetch(row, xv);
+  if (EARLY) fetch(row, xv);  // under way while the weights are staged
+  if (STAGED) {
+    for (int c = threadIdx.x; c < D; c += THREADS) {
+      sw[staged_at<VEC>(c, D)] = w ? w[c] : 1.f;
+      sb[staged_at<VEC>(c, D)] = b ? b[c] : 0.f;
+    }
+    __syncthreads();
+  }
   // every thread of the CTA turns as often as its first row group (barriers)
   for (int64_t r0 = (int64_t)blockIdx.x * per; r0 < rows; r0 += step, row += step) {
     if (EARLY)
@@ -332,7 +332,8 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const
 // words that hold them, by their whole row group, with a barrier of the group
 // per turn (4554 x 1335: 66 us when they were read in place, 28 us so).
 constexpr int AHEAD = 2, SLOTS = AHEAD + 1;
-constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }  // by a thread's values of a row (shared memory)
+// by a thread's values of a row (shared memory)
+constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }
 
 // Shared memory of one row, and of the words that hold it.
 __host__ __device__ inline int slot_bytes(int row_bytes, int vec_bytes) {

@@ -1094,7 +1094,8 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     auto g_map = [&](CUtensorMap *m, int box_rows) {
       return make_map3(m, ws + L.off_g, cols, N, L.parts, L.gpitch, N, box_rows);
     };
-    if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, box_of(N, 128)) || !w_map(&a.g[0].b, box_of(cols, L.bn_z / 2)))
+    if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, box_of(N, 128)) ||
+        !w_map(&a.g[0].b, box_of(cols, L.bn_z / 2)))
       return status_of(cudaErrorInvalidValue);
     whole_k(a.g[0], N, cols, D, L.bn_z);
     // all of G's columns: the tiles' are written whole
