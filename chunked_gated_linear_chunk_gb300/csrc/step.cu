@@ -14,6 +14,9 @@
 // call walk over registers.  The sum over key rows is a shuffle within a
 // warp and one pass over the warps' partial rows in shared memory, added in a
 // fixed order.  State arithmetic is fp32 throughout.
+// Measured: 256 sequences x 16 heads of 128 x 128 states, bf16, 85 us = 6.4 TB/s
+// (94% of the copy rate); 128 x 32 heads of 128 x 64, 44.5 us = 6.1 TB/s.  With
+// two CTAs per SM instead of four (registers): 121 us.
 #include <algorithm>
 
 #include "internal.cuh"
