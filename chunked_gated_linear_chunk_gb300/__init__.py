@@ -585,10 +585,6 @@ def norm_gate_bwd(o, z, w, dy, eps=1e-5, outs=None, workspace=None):
     return do, dz, dw
 
 
-def _aligned16(t):
-    return t if t.data_ptr() % 16 == 0 else t.clone()
-
-
 def _ce_args(x, w, target):
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
         raise ValueError("linear_ce: x must be [N, D] and w [V, D] of one dtype")
@@ -598,9 +594,12 @@ def _ce_args(x, w, target):
     if tuple(target.shape) != (x.shape[0],):
         raise ValueError("linear_ce: target must be [N]")
     x, N, D, xs = _rows2d(x, "x")
-    if x.dtype == torch.bfloat16 and D % 8 == 0 and xs % 8:
-        x, xs = x.contiguous(), 0
-    return _aligned16(x), _aligned16(_contig(w)), target, N, D, w.shape[0], xs
+    if x.data_ptr() % 16 or (x.dtype == torch.bfloat16 and D % 8 == 0 and xs % 8):
+        x, xs = x.clone(memory_format=torch.contiguous_format), 0
+    w = _contig(w)
+    if w.data_ptr() % 16:
+        w = w.clone()
+    return x, w, target, N, D, w.shape[0], xs
 
 
 def _scratch(need, device, workspace):

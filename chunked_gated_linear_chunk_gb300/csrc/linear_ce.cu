@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(256)
   const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   for (int i = y; i < 64; i += 8)
-    if (r0 + i < rows && c0 + 2 * x < spitch)
+    if (r0 + i < rows && c0 + 2 * x < cols)  // an odd number of columns has its padding beside it
       tile[i][x] = *reinterpret_cast<const __nv_bfloat162 *>(src + (r0 + i) * spitch + c0 + 2 * x);
   __syncthreads();
   // columns c, c + 1 of rows 2x, 2x + 1

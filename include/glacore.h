@@ -363,10 +363,13 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean,
  * cores with fp32 sums, G rounded to bf16 for them; fp32 operands are split
  * exactly into three bf16 parts (results to fp32's accuracy).  x and w must be
  * finite (an infinity in a row that is not scored still reaches dw as NaN).
- * The workspace (the *_workspace_size bytes, 256-byte aligned) holds row
- * statistics of the logits' tiles (forward), or G for one piece of the
- * vocabulary and dx in fp32 (backward): it does not grow with N * V beyond one
- * piece.  Results do not depend on the order in which CTAs run. */
+ * The workspace (the *_workspace_size bytes, 256-byte aligned) holds, forward,
+ * 16 bytes per token and tile of the vocabulary (at most 256 columns; a 64th of
+ * fp32 logits); backward, G for one piece of the vocabulary (512 MB, or 2048
+ * columns where those are more), x transposed, and fp32 sums of a gradient
+ * that is cut (512 MB each at most, or dx once).  Operands that TMA cannot
+ * address (bf16 with D no multiple of 8) and fp32 operands are copied there.
+ * Results do not depend on the order in which CTAs run. */
 size_t linear_ce_fwd_workspace_size(int64_t N, int64_t D, int64_t V,
                                     int32_t dtype);
 glacore_status linear_ce_fwd(const void *x, const void *w,

@@ -180,12 +180,14 @@ def test_strided_misaligned_x_and_other_stream(cuda_ok, dtype):
     x, w, t, dl = data(33, 64, 200, dtype, 9)
     wide = torch.zeros(33, 80, dtype=dtype, device="cuda")
     wide[:, 8:72] = x.cuda()
+    off = torch.zeros(33, 72, dtype=dtype, device="cuda")  # a row stride, and rows that start off 16 bytes
+    off[:, 1:65] = x.cuda()
     odd = torch.zeros(33 * 64 + 1, dtype=dtype, device="cuda")[1:].view(33, 64)
     odd.copy_(x)
     lse = check_fwd(x, w, t, glc.linear_ce_fwd(x.cuda(), w.cuda(), t.cuda()))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
-    for v in (wide[:, 8:72], odd):
+    for v in (wide[:, 8:72], off[:, 1:65], odd):
         with torch.cuda.stream(side):
             got = glc.linear_ce_fwd(v, w.cuda(), t.cuda())
             grads = glc.linear_ce_bwd(v, w.cuda(), t.cuda(), lse, dl.cuda())
