@@ -91,7 +91,7 @@ struct Args {
   Gemm g[2];
   int64_t units0, units;  // units of g[0], of both
   int32_t skip;           // rounds of g[1]'s units that the pairs with one unit of g[0] more sit out
-  int32_t bn, stages;
+  int32_t bn, stages, a_bytes;  // a_bytes: a CTA's rows of A in a k-block, as far as they are there
   int64_t N, V, v0;  // tokens, vocabulary, first column of the piece
   const int64_t *target;
   float2 *part;      // STATS: [2 * nt][N] (maximum * log2 e, sum)
@@ -154,7 +154,7 @@ __device__ __forceinline__ Tile tile_of(const Args &a, int64_t u) {
 // Accumulators in TMEM (fp32 operands: tiles of 128 columns, handed over every
 // k-block).
 constexpr int bufs_of(int parts) { return parts == 3 ? 4 : 2; }
-constexpr int stage_bytes_of(int parts, int bn) { return parts * (int)(A_BYTES + bn * BK); }
+constexpr int block_bytes_of(int parts, int a_bytes, int bn) { return parts * (a_bytes + bn * BK); }
 // G and dw leave through shared memory and TMA: a warp's direct stores of 32
 // rows touch 32 lines each, and a product over few k-blocks is bound by them
 // (backward of 16 x 2048 x 32000: 116 us with direct stores, 110 us so).
@@ -163,9 +163,13 @@ constexpr bool staged_out(int kind) { return kind != STATS; }
 // 2048 x 32000 forward 571 -> 546 us on a cool card).  The gradients' products,
 // with an operand in 64-row boxes, ran 3% slower so.
 constexpr int join_of(int kind, int parts) { return parts == 1 && kind != PRODUCT ? 2 : 1; }
-constexpr int stages_of(int kind, int parts, int bn) {
-  const int n = (SMEM - (staged_out(kind) ? EPI_WARPS * (int)OUT_BYTES : 0)) /
-                (join_of(kind, parts) * stage_bytes_of(parts, bn));
+// Shared memory of the output staging, and of the last stage's A rows that are
+// not there: a product reads 128 rows of A, whatever is in them.
+constexpr int extra_of(int kind, int a_bytes) {
+  return (staged_out(kind) ? EPI_WARPS * (int)OUT_BYTES : 0) + (int)A_BYTES - a_bytes;
+}
+constexpr int stages_of(int kind, int parts, int a_bytes, int bn) {
+  const int n = (SMEM - extra_of(kind, a_bytes)) / (join_of(kind, parts) * block_bytes_of(parts, a_bytes, bn));
   return n < MAX_STAGES ? n : MAX_STAGES;
 }
 // k-blocks whose products one accumulator sums
@@ -200,7 +204,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   const uint32_t rank = cluster_ctarank();
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t b_bytes = (uint32_t)a.bn * BK;  // bn / 2 rows of BK bf16
-  const uint32_t block_bytes = PARTS * (A_BYTES + b_bytes), stage_bytes = join_of(KIND, PARTS) * block_bytes;
+  const uint32_t a_bytes = a.a_bytes;
+  const uint32_t block_bytes = PARTS * (a_bytes + b_bytes), stage_bytes = join_of(KIND, PARTS) * block_bytes;
   const int64_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -259,14 +264,14 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
 #pragma unroll
           for (int q = 0; q < join_of(KIND, PARTS); ++q, k += BK) {
             if (q >= n) break;
-            const uint32_t sa = smem + s * stage_bytes + q * block_bytes, sb = sa + PARTS * A_BYTES;
+            const uint32_t sa = smem + s * stage_bytes + q * block_bytes, sb = sa + PARTS * a_bytes;
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
               if (a_mn) {
-                if (a0) tma_load_3d_pair(sa + p * A_BYTES, ma, am, k, p, bar);
-                if (a1) tma_load_3d_pair(sa + p * A_BYTES + 8192, ma, am + 64, k, p, bar);
+                if (a0) tma_load_3d_pair(sa + p * a_bytes, ma, am, k, p, bar);
+                if (a1) tma_load_3d_pair(sa + p * a_bytes + 8192, ma, am + 64, k, p, bar);
               } else if (a0) {
-                tma_load_3d_pair(sa + p * A_BYTES, ma, k, am, p, bar);
+                tma_load_3d_pair(sa + p * a_bytes, ma, k, am, p, bar);
               }
               if (b0) tma_load_3d_pair(sb + p * b_bytes, mb, k, bn0, p, bar);
             }
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         const uint32_t idesc = idesc_bf16(BM, a.bn, a_mn, false);
         const uint32_t astep = a_mn ? 2048 : 32;  // bytes between 16-element steps of K
         const SDesc ad0 = sdesc_sw128(smem, a_mn ? 8192 : 16, 1024);
-        const SDesc bd0 = sdesc_sw128(smem + PARTS * A_BYTES, 16, 1024);
+        const SDesc bd0 = sdesc_sw128(smem + PARTS * a_bytes, 16, 1024);
         for (int left = t.kb1 - t.kb0; left > 0 && ok; ++hand) {
           const uint32_t buf = hand % BUFS;
           if (!mbar_wait_cluster(&acc_empty[buf], (hand / BUFS + 1) & 1, WAIT_CYCLES)) {
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
 #pragma unroll
               for (int i = PARTS == 1 ? 5 : 0; i < 6; ++i) {
                 const uint32_t d = tmem + buf * BUF_COLS;
-                const SDesc ad = ad0 + (at + (PARTS == 1 ? 0 : PA[i] * A_BYTES));
+                const SDesc ad = ad0 + (at + (PARTS == 1 ? 0 : PA[i] * a_bytes));
                 const SDesc bd = bd0 + (at + (PARTS == 1 ? 0 : PB[i] * b_bytes));
 #pragma unroll
                 for (int k = 0; k < BK / 16; ++k)
@@ -838,7 +843,8 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     // The width that deals the vocabulary out most evenly: the fewest columns
     // for the busiest pair, and about 32 columns' time for a tile's start and
     // end.  It matters for few tokens, where the call is bound by reading w
-    // once (16 x 2048 x 32000: 36.4 us with 256, 34.8 us with 224).
+    // once (16 x 2048 x 32000: 36.4 us with 256, 34.8 us with 224, 33.6 us with
+    // the ring's stages no taller than the tokens).
     int64_t least = -1;
     for (int bn = 256; bn >= 128; bn -= backward ? 128 : 32) {  // G leaves 64 columns of a warp at a time
       const int64_t cost = up(up(N, BM) * up(V, bn), pair_count()) * (bn + 32);
@@ -902,8 +908,8 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 // follows: the kernel before it on the stream is one of this call's.
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, bool follows, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
-  const int ring = a.stages * join_of(KIND, PARTS) * stage_bytes_of(PARTS, a.bn);
-  const int smem = ring + (staged_out(KIND) ? EPI_WARPS * (int)OUT_BYTES : 0) + 1024;
+  const int ring = a.stages * join_of(KIND, PARTS) * block_bytes_of(PARTS, a.a_bytes, a.bn);
+  const int smem = ring + extra_of(KIND, a.a_bytes) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1030,7 +1036,8 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   whole_k(g, N, V, D, L.bn_z);
   a.units0 = a.units = (int64_t)g.mt * g.nt;
   a.bn = L.bn_z;
-  a.stages = stages_of(STATS, L.parts, a.bn);
+  a.a_bytes = box_of(N, 128) * BK * 2;
+  a.stages = stages_of(STATS, L.parts, a.a_bytes, a.bn);
   a.N = N;
   a.V = V;
   a.target = target;
@@ -1079,7 +1086,8 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     Args a;
     memset(&a, 0, sizeof(a));
     a.bn = L.bn_z;
-    a.stages = stages_of(GRAD, L.parts, a.bn);
+    a.a_bytes = box_of(N, 128) * BK * 2;
+    a.stages = stages_of(GRAD, L.parts, a.a_bytes, a.bn);
     a.N = N;
     a.V = V;
     a.v0 = v0;
@@ -1107,7 +1115,8 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     if (e != cudaSuccess) return status_of(e);
     // dx^T (K = the piece) and dw of the piece (K = the tokens)
     a.bn = L.bn;
-    a.stages = stages_of(PRODUCT, L.parts, a.bn);
+    a.a_bytes = (int)A_BYTES;
+    a.stages = stages_of(PRODUCT, L.parts, a.a_bytes, a.bn);
     Gemm &gx = a.g[0], &gw = a.g[1];
     if (!w_map(&gx.a, 64) || !g_map(&gx.b, box_of(N, L.bn / 2)) || !g_map(&gw.a, 64) ||
         !make_map3(&gw.b, xt, N, D, L.parts, L.xt_pitch, D, box_of(D, L.bn / 2)))
