@@ -433,7 +433,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 64; ++i) s[i & 3] += ex2(fmaf(v[i], LOG2E, -ref));
-          const float old = mx == -INFINITY ? 0.f : sum * ex2(mx * LOG2E - ref);
+          // no finite maximum yet: the sum is 0, or a NaN that stays
+          const float old = mx == -INFINITY ? sum : sum * ex2(mx * LOG2E - ref);
           sum = old + ((s[0] + s[1]) + (s[2] + s[3]));
           mx = peak;
         } else if constexpr (KIND == GRAD) {

@@ -159,6 +159,16 @@ def test_extreme_logits(cuda_ok, dtype):
     check_bwd(x, w, t, lse, torch.ones(3), glc.linear_ce_bwd(*c, lse, torch.ones(3, device="cuda")))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("first,count", [(0, 64), (64, 64), (300, 1), (0, 500)])
+def test_a_nan_among_the_logits_is_not_lost(cuda_ok, dtype, first, count):
+    """Also where it is all that an epilogue has seen of a row so far."""
+    x, w, t, _ = data(40, 64, 500, dtype, 11, skip=0)
+    w[first:first + count] = float("nan")
+    loss, lse = glc.linear_ce_fwd(x.cuda(), w.cuda(), t.cuda())
+    assert torch.isnan(loss).all() and torch.isnan(lse).all()
+
+
 def test_target_out_of_range_is_reported(cuda_ok):
     x, w, t, dl = data(20, 64, 300, torch.bfloat16, 8, skip=0)
     t[4] = 300
