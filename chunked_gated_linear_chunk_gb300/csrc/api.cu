@@ -485,7 +485,11 @@ glacore_status run_step(const glacore_problem *p, bool head_gate, float *state, 
   if (p->segment_ids || p->initial_state || p->chunk_size != 0) return GLACORE_ERR_INVALID_ARG;
   if (n_slots < 0 || (!slots && n_slots < p->B)) return GLACORE_ERR_INVALID_ARG;
   if (p->B * p->T == 0) return GLACORE_OK;
-  if (!o || (n_slots > 0 && !state) || ((uintptr_t)state & 3) || ((uintptr_t)slots & 3)) return GLACORE_ERR_INVALID_ARG;
+  // every pointer at a multiple of its elements' size
+  const uintptr_t data = (uintptr_t)p->q | (uintptr_t)p->k | (uintptr_t)p->v | (uintptr_t)o;
+  if (!o || (n_slots > 0 && !state) || (((uintptr_t)state | (uintptr_t)slots | (uintptr_t)p->g) & 3) ||
+      (data & (p->dtype == GLACORE_BF16 ? 1 : 3)))
+    return GLACORE_ERR_INVALID_ARG;
   int *err = device_error_ptr();
   if (!err) return GLACORE_ERR_CUDA;
   return status_of(step::launch(p, head_gate, state, n_slots, slots, o, err, st));

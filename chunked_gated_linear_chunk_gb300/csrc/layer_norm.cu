@@ -756,6 +756,11 @@ cudaError_t bwd(const Plan &p, int64_t &ctas, const void *x, const float *w, con
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// Every pointer at a multiple of its elements' size (null passes).
+inline bool natural(int32_t dtype, uintptr_t data, uintptr_t fp32) {
+  return (data & (dtype == GLACORE_BF16 ? 1 : 3)) == 0 && (fp32 & 3) == 0;
+}
+
 inline bool sizes_ok(int64_t rows, int64_t D, int64_t xs, int32_t dtype) {
   return rows >= 0 && D >= 1 && D < ((int64_t)1 << 31) && (xs == 0 || xs >= D) &&
          (dtype == GLACORE_BF16 || dtype == GLACORE_F32);
@@ -775,6 +780,8 @@ glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int
   if (!sizes_ok(rows, D, x_stride, dtype) || !(eps >= 0.f)) return GLACORE_ERR_INVALID_ARG;
   if (rows == 0) return GLACORE_OK;
   if (!x || !y || !mean != !rstd) return GLACORE_ERR_INVALID_ARG;
+  if (!natural(dtype, (uintptr_t)x | (uintptr_t)y, (uintptr_t)w | (uintptr_t)b | (uintptr_t)mean | (uintptr_t)rstd))
+    return GLACORE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   const int64_t xs = x_stride ? x_stride : D;
   const bool bf = dtype == GLACORE_BF16;
@@ -811,7 +818,9 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean, 
                               int64_t rows, int64_t D, int64_t x_stride, int64_t dy_stride, int32_t dtype, void *dx,
                               float *dw, float *db, void *workspace, size_t workspace_bytes,
                               glacore_stream_t stream) {
-  if (!sizes_ok(rows, D, x_stride, dtype) || (dy_stride != 0 && dy_stride < D) || !dw || !db)
+  if (!sizes_ok(rows, D, x_stride, dtype) || (dy_stride != 0 && dy_stride < D) || !dw || !db ||
+      !natural(dtype, (uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx,
+               (uintptr_t)w | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dw | (uintptr_t)db))
     return GLACORE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0) {

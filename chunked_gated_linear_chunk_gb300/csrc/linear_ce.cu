@@ -1019,7 +1019,8 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
                              size_t workspace_bytes, glacore_stream_t stream) {
   const glacore_status s = check(x, w, N, D, V, x_stride, dtype);
   if (s || N == 0) return s;
-  if (!target || !loss || !lse) return GLACORE_ERR_INVALID_ARG;
+  if (!target || !loss || !lse || ((uintptr_t)target & 7) || (((uintptr_t)loss | (uintptr_t)lse) & 3))
+    return GLACORE_ERR_INVALID_ARG;
   const ce::Layout L = ce::layout(N, D, V, dtype, false);
   if (!workspace || workspace_bytes < L.total || ((uintptr_t)workspace & 255)) return GLACORE_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
@@ -1064,7 +1065,8 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   if (!dw || ((uintptr_t)dw & 15) || ((uintptr_t)dx & 15)) return GLACORE_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
   if (N == 0) return status_of(cudaMemsetAsync(dw, 0, (size_t)V * D * es, st));
-  if (!target || !lse || !dloss || !dx) return GLACORE_ERR_INVALID_ARG;
+  if (!target || !lse || !dloss || !dx || ((uintptr_t)target & 7) || (((uintptr_t)lse | (uintptr_t)dloss) & 3))
+    return GLACORE_ERR_INVALID_ARG;
   const ce::Layout L = ce::layout(N, D, V, dtype, true);
   if (!workspace || workspace_bytes < L.total || ((uintptr_t)workspace & 255)) return GLACORE_ERR_WORKSPACE;
   if (const cudaError_t be = tc::bind_context()) return status_of(be);

@@ -185,7 +185,7 @@ glacore_status ssd_bwd(const glacore_problem *p, const void *do_,
  * its new tokens run by these give what one call over all tokens gives.
  *   p              B, T, H, Hqk, K, V, dtype, scale, q, k, v, g and the token
  *                  strides as in the chunked calls (any stride, no alignment
- *                  rule); n_seqs = B (0 if T = 0); segment_ids, initial_state
+ *                  but the elements' own); n_seqs = B (0 if T = 0); segment_ids, initial_state
  *                  NULL; chunk_size 0; no workspace
  *   state          [n_slots, H, K, V] fp32, contiguous, read and written
  *   state_indices  [B] int32 (device) or NULL (sequence b uses slot b;

@@ -142,3 +142,25 @@ def test_binding_refuses_cpu_tensors():
     q = torch.zeros(1, 1, 1, 8)
     with pytest.raises(ValueError):
         glc.gla_step(q, q, q, q, torch.zeros(1, 1, 8, 8))
+
+
+def off(n):
+    return ctypes.c_void_p(4096 + n)
+
+
+def test_pointers_between_elements_are_refused():
+    lib = glc.load()
+    for kw in (dict(x=off(1)), dict(y=off(1)), dict(w=off(2)), dict(b=off(2)), dict(mean=off(2)), dict(rstd=off(2)),
+               dict(x=off(2), dt=glc.F32), dict(y=off(2), dt=glc.F32)):
+        assert norm_fwd(lib, **kw) == glc.ERR_INVALID_ARG, kw
+    for kw in (dict(x=off(1)), dict(dy=off(1)), dict(dx=off(1)), dict(w=off(2)), dict(mean=off(2)), dict(rstd=off(2)),
+               dict(dw=off(2)), dict(db=off(2)), dict(dy=off(2), dt=glc.F32)):
+        assert norm_bwd(lib, **kw) == glc.ERR_INVALID_ARG, kw
+    for kw in (dict(t=off(4)), dict(lse=off(2))):
+        assert ce_fwd(lib, **kw) == glc.ERR_INVALID_ARG, kw
+        assert ce_bwd(lib, **kw) == glc.ERR_INVALID_ARG, kw
+    assert ce_fwd(lib, loss=off(2)) == ce_bwd(lib, dl=off(2)) == glc.ERR_INVALID_ARG
+    for over, o in ((dict(q=4098), A), (dict(g=4098), A), (dict(v=4097, dtype=glc.BF16), A), ({}, off(2)),
+                    (dict(dtype=glc.BF16), off(1))):
+        for call in (lib.gla_step, lib.ssd_step):
+            assert call(ctypes.byref(step_problem(**over)), A, 9, A, o, NULL) == glc.ERR_INVALID_ARG, over
