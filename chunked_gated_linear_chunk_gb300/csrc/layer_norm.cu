@@ -38,6 +38,7 @@ constexpr int THREADS = 256;
 constexpr int64_t MAX_COLS = 8192;  // a row in registers: at most 256 threads x 32 values
 constexpr int LONG_THREADS = 512;   // a CTA per longer row
 constexpr int RED_X = 32, RED_Y = 32;
+constexpr size_t SMEM_DEFAULT = 46 << 10;  // dynamic shared memory that needs no leave (48 KB with the static part)
 
 // VEC consecutive values of T as they lie in memory: 16 bytes, or 4 or one
 // bf16 where the row length or an address rules that out.
@@ -717,12 +718,11 @@ cudaError_t fwd(const Plan &p, const void *x, const float *w, const float *b, vo
       return;
     }
     auto *k = layer_norm_fwd_kernel<T, VEC, NV, true>;
-    static std::atomic<int> ready, cache;
+    static std::atomic<int> cache;
     const size_t smem = 2 * (size_t)((D + 3) / 4 * 4) * sizeof(float);
-    if (!ready.load(std::memory_order_relaxed)) {
+    if (smem > SMEM_DEFAULT) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (int)MAX_COLS * (int)sizeof(float));
       if (e != cudaSuccess) return;
-      ready.store(1, std::memory_order_relaxed);
     }
     const unsigned grid = (unsigned)std::min<int64_t>(p.ctas, resident(k, cache, smem));
     k<<<grid, THREADS, smem, st>>>((const T *)x, w, b, (T *)y, mean, rstd, rows, (int)D, xs, p.lg, eps);
@@ -739,14 +739,12 @@ cudaError_t bwd(const Plan &p, int64_t &ctas, const void *x, const float *w, con
   auto go = [&](auto nv) {
     constexpr int NV = decltype(nv)::value;
     constexpr int R = rows_at_once(NV * VEC);
-    static std::atomic<int> ready;
     auto *k = layer_norm_bwd_kernel<T, VEC, NV>;
     const size_t ring = (size_t)(THREADS >> p.lg) * SLOTS * R * 2 * slot_bytes((int)(D * sizeof(T)), VEC * sizeof(T));
     const size_t smem = std::max(ring, (size_t)D * sizeof(float));
-    if (!ready.load(std::memory_order_relaxed)) {
+    if (smem > SMEM_DEFAULT) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_MAX);
       if (e != cudaSuccess) return;
-      ready.store(1, std::memory_order_relaxed);
     }
     ctas = bwd_ctas((p.ctas + R - 1) / R, smem);
     k<<<(unsigned)ctas, THREADS, smem, st>>>((const T *)x, w, mean, rstd, (const T *)dy, (T *)dx, part, rows, (int)D,
