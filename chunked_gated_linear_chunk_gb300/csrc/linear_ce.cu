@@ -27,10 +27,14 @@
 // against 334 us), an A operand did not (334 against 326 us).  So dx is
 // computed transposed (A = w^T as it lies, B = G as it lies), and x is
 // transposed once per call for dw's B.
-// Warps of a CTA (320 threads): 0..7 epilogue (a TMEM lane per thread, two
-// warps per lane quarter, each half of the tile's columns), 8 TMA, 9 MMA (of
-// the pair's leader).  Two accumulators in TMEM (four with fp32 operands), so
-// the epilogue of one runs under the products of the next.
+// Warps of a CTA (352 threads): 0..7 epilogue (a TMEM lane per thread, two
+// warps per lane quarter, each half of the tile's columns), 8 TMA, 9 and 10 MMA
+// (of the pair's leader).  Two accumulators in TMEM (four with fp32 operands),
+// so the epilogue of one runs under the products of the next.  The two MMA
+// warps fill accumulators in turn: the queue of issued products covers some 500
+// cycles, less than one warp takes from its last product of an accumulator to
+// its first of the next (two commits and two waits; fp32 1000 x 1000 x 8000
+// forward: 116 us with one warp, 98 us with two).
 // Measured (8192 x 2048 x 32000 bf16, cool card): forward 557 us, 1930 TFLOP/s;
 // backward 1690 us, 1900 TFLOP/s (kept busy, the card's power limit takes 5 to
 // 15% off both).
@@ -65,7 +69,7 @@ using tc::tmem_ld32;
 using tc::tmem_ld_wait32;
 using tc::WAIT_CYCLES;
 
-constexpr int THREADS = 320, EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;
+constexpr int THREADS = 352, EPI_WARPS = 8, TMA_WARP = 8, MMA_WARP = 9;  // and MMA_WARP + 1
 enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
 constexpr int BM = 256, BK = 64;      // rows of a pair's tile, columns of a k-block
 constexpr uint32_t A_BYTES = 128 * BK * 2;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   constexpr bool CHUNKED = KIND == STATS || PARTS == 3;
   constexpr int BUFS = bufs_of(PARTS), BUF_COLS = 512 / BUFS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[BUFS], acc_empty[BUFS], drained;
+  __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[BUFS], acc_empty[BUFS], turn[2], drained;
   __shared__ uint32_t tmem_ptr;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -220,7 +224,9 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 2 * EPI_WARPS);
     }
-    mbar_init(&drained, 1);
+    mbar_init(&turn[0], 1);
+    mbar_init(&turn[1], 1);
+    mbar_init(&drained, 2);
     fence_mbar_init();
   }
   if (warp == MMA_WARP) {
@@ -295,13 +301,12 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       }
     }
     __syncwarp();
-  } else if (warp == MMA_WARP) {
+  } else if (warp >= MMA_WARP) {
     if (lane == 0 && rank == 0) {
-      // ---- products of the pair
+      // ---- products of the pair: every second accumulator's
       bool ok = true;
-      int s = 0;
-      uint32_t phase = 0;
-      uint32_t hand = 0;
+      const uint32_t side = warp - MMA_WARP;
+      uint32_t hand = 0, ring = 0;  // accumulators handed over, stages used (modulo two turns), by both
       const uint32_t acc_full0 = smem_u32(acc_full);
       Walk walk(a, pair, pairs);
       for (int64_t u; ok && (u = walk.next()) >= 0;) {
@@ -312,15 +317,27 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         const SDesc ad0 = sdesc_sw128(smem, a_mn ? 8192 : 16, 1024);
         const SDesc bd0 = sdesc_sw128(smem + PARTS * a_bytes, 16, 1024);
         for (int left = t.kb1 - t.kb0; left > 0 && ok; ++hand) {
+          const int run = min(left, CHUNK);
+          left -= run;
+          int s = ring;
+          uint32_t phase = 0;
+          ring = (ring + (run + join_of(KIND, PARTS) - 1) / join_of(KIND, PARTS)) % (2 * stages);
+          if ((hand & 1) != side) continue;
+          if (s >= stages) {
+            s -= stages;
+            phase = 1;
+          }
           const uint32_t buf = hand % BUFS;
-          if (!mbar_wait_cluster(&acc_empty[buf], (hand / BUFS + 1) & 1, WAIT_CYCLES)) {
+          // The accumulator has been read; and the other warp has seen all its
+          // stages arrive (a stage's barrier tells two turns of the ring apart,
+          // no more, so nobody waits for one further ahead).
+          if (!mbar_wait_at(smem_u32(&acc_empty[buf]), (hand / BUFS + 1) & 1, WAIT_CYCLES) ||
+              (hand > 0 && !mbar_wait_at(smem_u32(&turn[side]), ((hand - 1) >> 1) & 1, WAIT_CYCLES))) {
             set_device_error(a.err, GLACORE_ERR_TIMEOUT);
             ok = false;
             break;
           }
           tc_fence_after();
-          const int run = min(left, CHUNK);
-          left -= run;
           uint32_t more = 0;  // the run's first products overwrite the accumulator
           for (int n = run; n > 0; n -= join_of(KIND, PARTS)) {
             if (!mbar_wait_at(full0 + 8 * s, phase, WAIT_CYCLES)) {
@@ -328,6 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
               ok = false;
               break;
             }
+            if (n <= join_of(KIND, PARTS)) mbar_arrive(&turn[side ^ 1]);
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < join_of(KIND, PARTS); ++q) {
@@ -383,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     auto release = [&](int buf) {  // this warp has read the accumulator
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      if (lane == 0) mbar_arrive_pair(mapa_shared(smem_u32(&acc_empty[buf]), 0));
     };
     const float unit = KIND != STATS && a.unit ? *a.unit : 1.f;
     uint32_t hand = 0;
