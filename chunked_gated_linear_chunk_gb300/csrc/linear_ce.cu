@@ -75,13 +75,16 @@ constexpr int BM = 256, BK = 64;      // rows of a pair's tile, columns of a k-b
 constexpr uint32_t A_BYTES = 128 * BK * 2;
 constexpr int MAX_STAGES = 12;
 constexpr int SMEM = 231168;          // shared memory of ring and output staging, at most (a KB is left for alignment)
-constexpr uint32_t OUT_BYTES = 4096;  // output staging of a warp: 32 rows of 128 bytes
+// Output staging of a warp: 32 rows of 128 bytes, stored by TMA; with fp32
+// operands 8 rows at a time, stored by the warp, which leaves room for a third
+// stage of the ring (gradients of 1001 x 520 x 10007: 220 us with two, 187 us).
+constexpr int out_bytes_of(int parts) { return parts == 3 ? 1024 : 4096; }
 constexpr int GROUP_M = 8;            // row tiles that share a walk over the columns (L2 reuse)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // One product C[m, n] = A B^T over k-blocks, tiles of BM x bn.
 struct Gemm {
-  CUtensorMap a, b, o;      // o: the output, where `tma_out`
+  CUtensorMap a, b, o;      // o: the output, where bf16 operands' leaves by TMA
   int64_t m, n;
   int32_t a_mn;             // A stored with its M axis contiguous (B: always its K axis)
   int32_t mt, nt, kb;       // tiles, k-blocks
@@ -89,9 +92,11 @@ struct Gemm {
   int32_t splits, kb_split; // K cut into `splits` runs of kb_split blocks
   // PRODUCT: where C (C^T if `trans`) goes.  out_f32: fp32, split s at
   // out + s * m * n, added to what is there if `add`; otherwise the tensors'
-  // dtype.
+  // dtype.  wide_out: its rows start at 16-byte steps, and leave through shared
+  // memory.  GRAD of fp32 operands: G, out_pitch elements between rows.
   void *out;
-  int32_t out_f32, add, trans, tma_out;
+  int64_t out_pitch;
+  int32_t out_f32, add, trans, wide_out;
 };
 
 struct Args {
@@ -172,11 +177,11 @@ constexpr bool staged_out(int kind) { return kind != STATS; }
 constexpr int join_of(int kind, int parts) { return parts == 1 && kind != PRODUCT ? 2 : 1; }
 // Shared memory of the output staging, and of the last stage's A rows that are
 // not there: a product reads 128 rows of A, whatever is in them.
-constexpr int extra_of(int kind, int a_bytes) {
-  return (staged_out(kind) ? EPI_WARPS * (int)OUT_BYTES : 0) + (int)A_BYTES - a_bytes;
+constexpr int extra_of(int kind, int parts, int a_bytes) {
+  return (staged_out(kind) ? EPI_WARPS * out_bytes_of(parts) : 0) + (int)A_BYTES - a_bytes;
 }
 constexpr int stages_of(int kind, int parts, int a_bytes, int bn) {
-  const int n = (SMEM - extra_of(kind, a_bytes)) / (join_of(kind, parts) * block_bytes_of(parts, a_bytes, bn));
+  const int n = (SMEM - extra_of(kind, parts, a_bytes)) / (join_of(kind, parts) * block_bytes_of(parts, a_bytes, bn));
   return n < MAX_STAGES ? n : MAX_STAGES;
 }
 // k-blocks whose products one accumulator sums
@@ -381,8 +386,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
     // ---- epilogue: thread = row, half = which half of the tile's columns
     const int quarter = warp & 3, half = warp >> 2, cols = a.bn / 2;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * cols;
-    // The warp's staging: 32 rows of 128 bytes, 16-byte chunks swizzled by row.
-    const uint32_t stage = smem + stages * stage_bytes + warp * OUT_BYTES;
+    // The warp's staging: rows of 128 bytes, 16-byte chunks swizzled by row.
+    const uint32_t stage = smem + stages * stage_bytes + warp * out_bytes_of(PARTS);
     auto put = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
       tc::st_shared_v4(stage + lane * 128 + ((chunk ^ (lane & 7)) << 4), x, y, z, w);
     };
@@ -396,6 +401,25 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       if (lane == 0) {
         tma_store_3d_at(map, stage, x, y, z);
         bulk_commit();
+      }
+    };
+    // `w`: 128 bytes of this lane's row; rows `pitch` bytes apart from `to` on,
+    // of which the first `rows` are there, and the first `bytes` of each.
+    auto store_rows = [&](const uint4 (&w)[8], char *to, int64_t pitch, int64_t rows, int bytes) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if ((lane >> 3) == r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            tc::st_shared_v4(stage + (lane & 7) * 128 + ((i ^ (lane & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+          const int y = (lane >> 3) + h, c = lane & 7;
+          const uint4 f = ld_shared_v4(stage + y * 128 + ((c ^ y) << 4));
+          if (8 * r + y < rows && 16 * c < bytes) *reinterpret_cast<uint4 *>(to + (8 * r + y) * pitch + 16 * c) = f;
+        }
+        __syncwarp();
       }
     };
     auto release = [&](int buf) {  // this warp has read the accumulator
@@ -478,35 +502,52 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           if (row - lane >= g.m) return;
 #pragma unroll
           for (int p = 0; p < PARTS; ++p) {
-            begin_out();
+            uint4 w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              uint32_t w[4];
+              uint32_t u[4];
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 float &x = v[8 * i + 2 * j], &y = v[8 * i + 2 * j + 1];
-                if (PARTS == 1) {
-                  w[j] = pack_bf16(x, y);
-                } else {  // the bf16 nearest to what is left, and exactly what is left then
-                  w[j] = pack_bf16(x, y);
-                  x -= __uint_as_float(w[j] << 16);
-                  y -= __uint_as_float(w[j] & 0xffff0000u);
+                u[j] = pack_bf16(x, y);
+                if (PARTS == 3) {  // the bf16 nearest to what is left, and exactly what is left then
+                  x -= __uint_as_float(u[j] << 16);
+                  y -= __uint_as_float(u[j] & 0xffff0000u);
                 }
               }
-              put(i, w[0], w[1], w[2], w[3]);
+              w[i] = make_uint4(u[0], u[1], u[2], u[3]);
             }
-            send_out(&g.o, (int)col, (int)(row - lane), p);
+            if constexpr (PARTS == 3) {
+              store_rows(w, reinterpret_cast<char *>(g.out) + ((p * a.N + row - lane) * g.out_pitch + col) * 2,
+                         g.out_pitch * 2, g.m - (row - lane), 128);
+            } else {
+              begin_out();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) put(i, w[i].x, w[i].y, w[i].z, w[i].w);
+              send_out(&g.o, (int)col, (int)(row - lane), p);
+            }
           }
         } else {
           if (c >= cols || col >= g.n || row - lane >= g.m) return;  // nothing of the warp's columns is there
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] *= unit;
           const int room = g.n - col < 64 ? (int)(g.n - col) : 64;
-          if (g.tma_out) {  // what lies past the edges is not written
+          if (g.wide_out) {  // what lies past the edges is not written
             if (g.out_f32) {
 #pragma unroll
               for (int h = 0; h < 64; h += 32) {
                 if (h >= room) break;
+                if constexpr (PARTS == 3) {
+                  uint4 w[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i)
+                    w[i] = make_uint4(__float_as_uint(v[h + 4 * i]), __float_as_uint(v[h + 4 * i + 1]),
+                                      __float_as_uint(v[h + 4 * i + 2]), __float_as_uint(v[h + 4 * i + 3]));
+                  store_rows(w, reinterpret_cast<char *>(g.out) +
+                                    (((int64_t)t.split * g.m + row - lane) * g.n + col + h) * 4,
+                             g.n * 4, g.m - (row - lane), 4 * (room - h));
+                  continue;
+                }
                 begin_out();
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -931,7 +972,7 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 template <int KIND, int PARTS> cudaError_t launch(const Args &a, bool follows, cudaStream_t st) {
   auto *k = ce_product_kernel<KIND, PARTS>;
   const int ring = a.stages * join_of(KIND, PARTS) * block_bytes_of(PARTS, a.a_bytes, a.bn);
-  const int smem = ring + extra_of(KIND, a.a_bytes) + 1024;
+  const int smem = ring + extra_of(KIND, PARTS, a.a_bytes) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1131,8 +1172,10 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
       return status_of(cudaErrorInvalidValue);
     whole_k(a.g[0], N, cols, D, L.bn_z);
     // all of G's columns: the tiles' are written whole
-    if (!make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, L.parts, L.gpitch, N, 32))
+    if (L.parts == 1 && !make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, L.parts, L.gpitch, N, 32))
       return status_of(cudaErrorInvalidValue);
+    a.g[0].out = ws + L.off_g;
+    a.g[0].out_pitch = L.gpitch;
     a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
     e = ce::launch<GRAD>(a, L.parts, true, st);
     mark_launch("ce_grad", st);
@@ -1160,8 +1203,8 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     char *dw_piece = (char *)dw + (size_t)v0 * D * es;
     gw.out_f32 = L.dw_sums || dtype == GLACORE_F32;
     gw.out = L.dw_sums ? ws + L.off_dw : dw_piece;
-    gw.tma_out = D % (gw.out_f32 ? 4 : 8) == 0;
-    if (gw.tma_out && !make_map3(&gw.o, gw.out, D, cols, gw.splits, D, cols, 32, gw.out_f32))
+    gw.wide_out = D % (gw.out_f32 ? 4 : 8) == 0;
+    if (L.parts == 1 && gw.wide_out && !make_map3(&gw.o, gw.out, D, cols, gw.splits, D, cols, 32, gw.out_f32))
       return status_of(cudaErrorInvalidValue);
     a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
     a.units = a.units0 + (int64_t)gw.mt * gw.nt * gw.splits;

@@ -87,6 +87,14 @@ __device__ __forceinline__ void tma_store_3d_at(const CUtensorMap *m, uint32_t s
                "r"(src), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
 // 2^x, flushing subnormal results.
 __device__ __forceinline__ float ex2(float x) {
   float r;
