@@ -23,7 +23,7 @@
 // order.
 // Measured: 8192 x 2048 bf16 forward 15.2 us (4.4 TB/s), backward 25.4 us (4.0
 // TB/s; 3.5 us of it the sum of the partial rows); 4099 x 1111 fp32 backward
-// 26.6 us.
+// 23.8 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -331,17 +331,18 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const
 // copies them to shared memory AHEAD turns before theirs, each thread its own
 // columns (no barrier: a thread reads only what it copied).  In registers the
 // rows in flight would have to share the space with the column sums: 8192 x
-// 2048 bf16 ran with 32 KB in flight per SM and 35 us.  Rows of bf16 that start
-// between two 4-byte words (the least that can be copied so) are copied as the
-// words that hold them, by their whole row group, with a barrier of the group
-// per turn (4554 x 1335: 66 us when they were read in place, 28 us so).
+// 2048 bf16 ran with 32 KB in flight per SM and 35 us.  Rows that start between
+// two vectors (odd lengths) are copied as the 16-byte words that hold them, by
+// their whole row group, with a barrier of the group per turn (4554 x 1335 bf16:
+// 66 us when they were read in place, 24.4 us so; 4099 x 1111 fp32: 26.6 us when
+// they were copied value by value, 23.8 us so).
 constexpr int AHEAD = 2, SLOTS = AHEAD + 1;
 // by a thread's values of a row (shared memory)
 constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }
 
-// Shared memory of one row, and of the words that hold it.
-__host__ __device__ inline int slot_bytes(int row_bytes, int vec_bytes) {
-  return (row_bytes + (vec_bytes < 4 ? 4 : 0) + 15) / 16 * 16;
+// Shared memory of one row, or of the words that hold it (single values).
+__host__ __device__ inline int slot_bytes(int row_bytes, int vec) {
+  return (row_bytes + (vec == 1 ? 15 : 0) + 15) / 16 * 16;
 }
 
 // part: [gridDim.x][2][D] partial dw, db of the rows each CTA walked.
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                           float *__restrict__ part, int64_t rows, int D, int64_t xs, int64_t ys, int lg) {
   follow_allow();
   constexpr int BYTES = VEC * (int)sizeof(T);
-  constexpr bool WORDS = BYTES < 4;
+  constexpr bool WORDS = VEC == 1;
   constexpr int R = rows_at_once(NV * VEC);
   extern __shared__ float4 smem[];
   __shared__ float red[2][THREADS / 32][2 * R];
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, 2)
     for (int e = 0; e < VEC; ++e) dw[j][e] = db[j][e] = 0.f;
   }
   // this thread's columns of its row group's slots: x, dy of each of R rows
-  const int pitch = slot_bytes(D * (int)sizeof(T), BYTES);
+  const int pitch = slot_bytes(D * (int)sizeof(T), VEC);
   char *slots = reinterpret_cast<char *>(smem) + (int64_t)(threadIdx.x >> lg) * SLOTS * R * 2 * pitch + t * BYTES;
   auto fetch = [&](int64_t row, int slot) {
 #pragma unroll
@@ -376,12 +377,12 @@ __global__ void __launch_bounds__(THREADS, 2)
         const T *px = x + (row + i) * xs, *pg = dy + (row + i) * ys;
         char *to = slots + (slot * R + i) * 2 * pitch;
         if constexpr (WORDS) {
-          to += t * (4 - BYTES);
-          const char *wx = reinterpret_cast<const char *>((uintptr_t)px & ~(uintptr_t)3) + 4 * t;
-          const char *wg = reinterpret_cast<const char *>((uintptr_t)pg & ~(uintptr_t)3) + 4 * t;
+          to += t * (16 - BYTES);
+          const char *wx = reinterpret_cast<const char *>((uintptr_t)px & ~(uintptr_t)15) + 16 * t;
+          const char *wg = reinterpret_cast<const char *>((uintptr_t)pg & ~(uintptr_t)15) + 16 * t;
           const char *ex = reinterpret_cast<const char *>(px + D), *eg = reinterpret_cast<const char *>(pg + D);
-          for (int k = 0; wx + k < ex; k += 4 * L) copy_async<4>(to + k, wx + k);
-          for (int k = 0; wg + k < eg; k += 4 * L) copy_async<4>(to + pitch + k, wg + k);
+          for (int k = 0; wx + k < ex; k += 16 * L) copy_async<16>(to + k, wx + k);
+          for (int k = 0; wg + k < eg; k += 16 * L) copy_async<16>(to + pitch + k, wg + k);
         } else {
           px += t * VEC;
           pg += t * VEC;
@@ -430,8 +431,8 @@ __global__ void __launch_bounds__(THREADS, 2)
       Vec<T, VEC> vx, vg;
       const char *fx = slots + (slot * R + i) * 2 * pitch + j * L * BYTES, *fg = fx + pitch;
       if constexpr (WORDS) {  // where in its first word the row starts
-        fx += (uintptr_t)(x + (row + i) * xs) & 3;
-        fg += (uintptr_t)(dy + (row + i) * ys) & 3;
+        fx += (uintptr_t)(x + (row + i) * xs) & 15;
+        fg += (uintptr_t)(dy + (row + i) * ys) & 15;
       }
       vx.load(reinterpret_cast<const T *>(fx));
       vg.load(reinterpret_cast<const T *>(fg));
@@ -446,7 +447,9 @@ __global__ void __launch_bounds__(THREADS, 2)
       if (row + i < rows)
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-          if ((j * L + t) * VEC < D) {
+          if (VEC == 1 && j * L >= D) {  // no thread of the row has this one: jump, do not predicate
+            break;
+          } else if ((j * L + t) * VEC < D) {
             float n[VEC], g[VEC], a[VEC];
             get(i, j, n, g);
             vfma(n, n, All{1.f}, All{-m[i]});  // as in the forward
@@ -469,6 +472,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int c = (j * L + t) * VEC;
+        if (VEC == 1 && j * L >= D) break;
         if (c < D) {
           float v[VEC], g[VEC];
           get(i, j, v, g);
@@ -679,8 +683,9 @@ inline int vec_of(bool bf, int64_t D, int64_t s0, int64_t s1, uintptr_t data, ui
   return bf && all % 2 == 0 && (data & 3) == 0 ? 2 : 1;
 }
 
-// Shared memory of the backward's rows, at most.
-constexpr int RING_MAX = SLOTS * 2 * (int)MAX_COLS * 4;
+// Shared memory of the backward's rows, at most: 12 slots of each of 8 rows of
+// 511 fp32 in the words that hold them are 198144 bytes, no other spread has more.
+constexpr int RING_MAX = 12 * 8 * 2064;
 // CTAs of the backward: two per SM at most (registers), one where the rows in
 // flight take more than half the shared memory.
 inline int64_t bwd_ctas(int64_t ctas, size_t smem) {
@@ -740,7 +745,7 @@ cudaError_t bwd(const Plan &p, int64_t &ctas, const void *x, const float *w, con
     constexpr int NV = decltype(nv)::value;
     constexpr int R = rows_at_once(NV * VEC);
     auto *k = layer_norm_bwd_kernel<T, VEC, NV>;
-    const size_t ring = (size_t)(THREADS >> p.lg) * SLOTS * R * 2 * slot_bytes((int)(D * sizeof(T)), VEC * sizeof(T));
+    const size_t ring = (size_t)(THREADS >> p.lg) * SLOTS * R * 2 * slot_bytes((int)(D * sizeof(T)), VEC);
     const size_t smem = std::max(ring, (size_t)D * sizeof(float));
     if (smem > SMEM_DEFAULT) {
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_MAX);
