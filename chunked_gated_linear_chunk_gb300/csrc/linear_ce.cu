@@ -776,29 +776,34 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Rows of bf16 with a pitch that TMA can address: a copy of bf16 values
-// (PARTS = 1), or the three exact parts of fp32 values.
+// Rows of x, then of w, as bf16 with a pitch that TMA can address: a copy of
+// bf16 values (PARTS = 1), or the three exact parts of fp32 values.
 template <int PARTS, typename T>
 __global__ void __launch_bounds__(256)
-    ce_pack_kernel(const T *__restrict__ src, int64_t rows, int64_t D, int64_t stride, int64_t pitch,
-                   __nv_bfloat16 *__restrict__ dst) {
-  follow_wait();
+    ce_pack_kernel(const T *__restrict__ x, int64_t N, int64_t xs, __nv_bfloat16 *__restrict__ xp,
+                   const T *__restrict__ w, int64_t V, __nv_bfloat16 *__restrict__ wp, int64_t D, int64_t pitch) {
   follow_allow();
   const int lane = threadIdx.x & 31;
-  for (int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.x * 8) {
+  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < N + V; i += (int64_t)gridDim.x * 8) {
+    const int64_t r = i < N ? i : i - N, rows = i < N ? N : V;
+    const T *src = i < N ? x + r * xs : w + r * D;
+    __nv_bfloat16 *dst = i < N ? xp : wp;
 #pragma unroll 4
-    for (int64_t c = lane; c < D; c += 32) {
-      if constexpr (PARTS == 1) {
-        dst[r * pitch + c] = src[r * stride + c];
-      } else {
-        float x = src[r * stride + c];
+    for (int64_t c = 2 * lane; c < D; c += 64) {  // two values per store (an odd row's last with a zero)
+      float a = to_f32(src[c]), b = c + 1 < D ? to_f32(src[c + 1]) : 0.f;
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) {
-          float hi = __bfloat162float(__float2bfloat16_rn(x));
-          if (isinf(hi)) hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);  // above bf16's largest value
-          dst[(p * rows + r) * pitch + c] = __float2bfloat16_rn(hi);
-          x = isinf(hi) ? 0.f : x - hi;  // an infinity stays one, in the first part
+      for (int p = 0; p < PARTS; ++p) {
+        uint32_t u = pack_bf16(a, b);
+        if (PARTS == 3) {
+          float ha = __uint_as_float(u << 16), hb = __uint_as_float(u & 0xffff0000u);
+          // above bf16's largest value the nearest is cut off instead
+          if (isinf(ha)) ha = __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+          if (isinf(hb)) hb = __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+          u = pack_bf16(ha, hb);
+          a = isinf(ha) ? 0.f : a - ha;  // an infinity stays one, in the first part
+          b = isinf(hb) ? 0.f : b - hb;
         }
+        *reinterpret_cast<uint32_t *>(dst + (p * rows + r) * pitch + c) = u;
       }
     }
   }
@@ -1019,19 +1024,16 @@ cudaError_t rows_of(const Layout &L, const void *x, int64_t xs, const void *w, i
     r = Rows{x, w, xs, D};
     return cudaSuccess;
   }
-  auto pack = [&](const void *src, int64_t rows, int64_t stride, size_t off) {
-    const unsigned grid = (unsigned)std::min<int64_t>(up(rows, 8), 8 * tc::sm_count());
-    __nv_bfloat16 *dst = (__nv_bfloat16 *)(ws + off);
-    if (L.parts == 3)
-      ce_pack_kernel<3, float><<<grid, 256, 0, st>>>((const float *)src, rows, D, stride, L.pitch, dst);
-    else
-      ce_pack_kernel<1, __nv_bfloat16><<<grid, 256, 0, st>>>((const __nv_bfloat16 *)src, rows, D, stride, L.pitch, dst);
-    mark_launch("ce_pack", st);
-    return cudaGetLastError();
-  };
-  r = Rows{ws + L.off_x, ws + L.off_w, L.pitch, L.pitch};
-  const cudaError_t e = pack(x, N, xs, L.off_x);
-  return e != cudaSuccess ? e : pack(w, V, D, L.off_w);
+  const unsigned grid = (unsigned)std::min<int64_t>(up(N + V, 8), 8 * tc::sm_count());
+  __nv_bfloat16 *xp = (__nv_bfloat16 *)(ws + L.off_x), *wp = (__nv_bfloat16 *)(ws + L.off_w);
+  if (L.parts == 3)
+    ce_pack_kernel<3, float><<<grid, 256, 0, st>>>((const float *)x, N, xs, xp, (const float *)w, V, wp, D, L.pitch);
+  else
+    ce_pack_kernel<1, __nv_bfloat16><<<grid, 256, 0, st>>>((const __nv_bfloat16 *)x, N, xs, xp,
+                                                           (const __nv_bfloat16 *)w, V, wp, D, L.pitch);
+  mark_launch("ce_pack", st);
+  r = Rows{xp, wp, L.pitch, L.pitch};
+  return cudaGetLastError();
 }
 
 cudaError_t add_splits(const float *part, int splits, int64_t n, int32_t dtype, void *out, cudaStream_t st) {
@@ -1140,10 +1142,16 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   const __nv_bfloat16 *xt = (const __nv_bfloat16 *)(ws + L.off_xt);
   float *unit = L.parts == 1 ? (float *)(ws + L.off_unit) : nullptr;  // three parts hold dloss as it is
   const dim3 grid((unsigned)up(N, 64) + 1, (unsigned)up(D, 64), (unsigned)L.parts);
-  ce_prepare_kernel<<<grid, 256, 0, st>>>((const __nv_bfloat16 *)r.x, N, D, r.xp, L.xt_pitch,
-                                          (__nv_bfloat16 *)(ws + L.off_xt), dloss, target, V, unit);
+  __nv_bfloat16 *to = (__nv_bfloat16 *)(ws + L.off_xt);
+  const __nv_bfloat16 *rows = (const __nv_bfloat16 *)r.x;
+  if (L.pack)
+    e = launch_follow(ce_prepare_kernel, grid, dim3(256), st, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
+  else {
+    ce_prepare_kernel<<<grid, 256, 0, st>>>(rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
+    e = cudaGetLastError();
+  }
   mark_launch("ce_prepare", st);
-  if ((e = cudaGetLastError()) != cudaSuccess) return status_of(e);
+  if (e != cudaSuccess) return status_of(e);
   for (int64_t i = 0; i < L.pieces; ++i) {
     const int64_t v0 = i * L.piece, cols = std::min(L.piece, V - v0);
     // the piece's rows of w (its parts stay V rows apart)
