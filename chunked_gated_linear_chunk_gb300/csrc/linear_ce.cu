@@ -34,9 +34,9 @@
 // warps fill accumulators in turn: the queue of issued products covers some 500
 // cycles, less than one warp takes from its last product of an accumulator to
 // its first of the next (two commits and two waits; fp32 1000 x 1000 x 8000
-// forward: 116 us with one warp, 98 us with two).
-// Measured (8192 x 2048 x 32000 bf16, cool card): forward 557 us, 1930 TFLOP/s;
-// backward 1690 us, 1900 TFLOP/s (kept busy, the card's power limit takes 5 to
+// forward: 18 us more with one warp).
+// Measured (8192 x 2048 x 32000 bf16, cool card): forward 549 us, 1960 TFLOP/s;
+// backward 1680 us, 1920 TFLOP/s (kept busy, the card's power limit takes 5 to
 // 15% off both).
 //
 // fp32 operands: each value is cut exactly into three bf16 parts (the nearest
@@ -77,7 +77,7 @@ constexpr int MAX_STAGES = 12;
 constexpr int SMEM = 231168;          // shared memory of ring and output staging, at most (a KB is left for alignment)
 // Output staging of a warp: 32 rows of 128 bytes, stored by TMA; with fp32
 // operands 8 rows at a time, stored by the warp, which leaves room for a third
-// stage of the ring (gradients of 1001 x 520 x 10007: 220 us with two, 187 us).
+// stage of the ring (gradients of 1001 x 520 x 10007: 33 us more with two stages).
 constexpr int out_bytes_of(int parts) { return parts == 3 ? 1024 : 4096; }
 constexpr int GROUP_M = 8;            // row tiles that share a walk over the columns (L2 reuse)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
