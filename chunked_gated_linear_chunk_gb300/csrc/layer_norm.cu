@@ -336,6 +336,8 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const
 // their whole row group, with a barrier of the group per turn (4554 x 1335 bf16:
 // 66 us when they were read in place, 24.4 us so; 4099 x 1111 fp32: 26.6 us when
 // they were copied value by value, 23.8 us so).
+// Such a word may hold up to 15 bytes beside the row: they are in the same aligned
+// 16 bytes as a value of it, so never on another page, and nothing uses them.
 constexpr int AHEAD = 2, SLOTS = AHEAD + 1;
 // by a thread's values of a row (shared memory)
 constexpr int rows_at_once(int values) { return values <= 16 ? 2 : 1; }
