@@ -17,7 +17,8 @@
 //            ce_merge_kernel.  The logits leave TMEM and are gone.
 //   GRAD     a tile of logits becomes a tile of G in bf16 (its products with w
 //            and x are bf16 tensor-core products), for one piece of the
-//            vocabulary at a time, so G takes a bounded workspace.
+//            vocabulary at a time, so G takes a bounded workspace.  Of few
+//            tokens in two bf16 parts (FEW_TOKENS).
 //   PRODUCT  dx^T += w_piece^T G_piece^T and dw_piece = G_piece^T x as one
 //            list of units: dw's fill the last wave that dx's would leave
 //            open.  dx is summed over pieces and splits of the vocabulary in
@@ -57,6 +58,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "tc_pair.cuh"
 
@@ -110,6 +112,7 @@ struct Args {
   float *zt;         // STATS: [N] the target's logit
   const float *lse, *dloss;  // GRAD
   const float *unit;         // G is in units of *unit (null: 1)
+  const float *at_target;    // GRAD of few tokens: [N] p - 1 at the target
   int *err;
 };
 
@@ -194,8 +197,9 @@ __device__ constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
 // Bytes of one k-block (and part) that CTA `rank` loads for a tile.  What lies
 // wholly past the end of M or N is not loaded: whatever is in its place only
 // reaches accumulator rows and columns that nobody reads.
-__device__ __forceinline__ uint32_t load_bytes(const Gemm &g, const Tile &t, int bn, int rank) {
-  const int64_t am = t.m0 + rank * 128, bn0 = t.n0 + rank * (bn / 2);
+// `beside`: B is two parts of the same rows side by side, one for each CTA.
+__device__ __forceinline__ uint32_t load_bytes(const Gemm &g, const Tile &t, int bn, int rank, bool beside) {
+  const int64_t am = t.m0 + rank * 128, bn0 = t.n0 + (beside ? 0 : rank * (bn / 2));
   uint32_t n = bn0 < g.n ? (uint32_t)g.b_box * (BK * 2) : 0;
   if (g.a_mn)
     n += (am < g.m ? 8192 : 0) + (am + 64 < g.m ? 8192 : 0);
@@ -204,8 +208,16 @@ __device__ __forceinline__ uint32_t load_bytes(const Gemm &g, const Tile &t, int
   return n;
 }
 
-template <int KIND, int PARTS>
+// Parts of G (FEW: few tokens).  Two bf16 parts: GRAD writes them; of PRODUCT's
+// sums dx has them side by side along its N axis (the tokens fill less than half
+// a tile, so they cost it nothing) and leaves each as a split of its own, dw one
+// after the other along K.
+constexpr int g_parts_of(int parts, bool few) { return parts == 3 ? 3 : few ? 2 : 1; }
+
+template <int KIND, int PARTS, bool FEW>
 __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_constant__ Args a) {
+  constexpr int G_PARTS = g_parts_of(PARTS, FEW);
+  constexpr bool TWO = KIND == PRODUCT && PARTS == 1 && G_PARTS == 2;
   constexpr int CHUNK = chunk_of(KIND, PARTS);
   constexpr bool CHUNKED = KIND == STATS || PARTS == 3;
   constexpr int BUFS = bufs_of(PARTS), BUF_COLS = 512 / BUFS;
@@ -263,10 +275,13 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
         const Tile t = tile_of(a, u);
         const Gemm &g = a.g[t.which];
         const CUtensorMap *ma = &g.a, *mb = &g.b;
-        const int am = (int)(t.m0 + rank * 128), bn0 = (int)(t.n0 + rank * (a.bn / 2));
+        const int am = (int)(t.m0 + rank * 128), bn0 = TWO && !t.which ? 0 : (int)(t.n0 + rank * (a.bn / 2));
         const bool a_mn = g.a_mn, a0 = am < g.m, a1 = am + 64 < g.m, b0 = bn0 < g.n;
-        const uint32_t bytes = PARTS * (load_bytes(g, t, a.bn, 0) + load_bytes(g, t, a.bn, 1));
-        int k = t.kb0 * BK;
+        const bool beside = TWO && !t.which;
+        const uint32_t bytes = PARTS * (load_bytes(g, t, a.bn, 0, beside) + load_bytes(g, t, a.bn, 1, beside));
+        const bool behind = TWO && t.which;
+        int k = behind ? t.kb0 / 2 * BK : t.kb0 * BK, za = behind ? t.kb0 % 2 : 0;
+        const int zb = beside ? (int)rank : 0;
         for (int n = t.kb1 - t.kb0; n > 0; n -= join_of(KIND, PARTS)) {
           if (!mbar_wait_at(empty0 + 8 * s, phase ^ 1, WAIT_CYCLES)) {
             set_device_error(a.err, GLACORE_ERR_TIMEOUT);
@@ -276,18 +291,24 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           if (rank == 0) mbar_expect_tx_at(full0 + 8 * s, bytes * (uint32_t)min(n, join_of(KIND, PARTS)));
           const uint32_t bar = bar0 + 8 * s;
 #pragma unroll
-          for (int q = 0; q < join_of(KIND, PARTS); ++q, k += BK) {
+          for (int q = 0; q < join_of(KIND, PARTS); ++q) {
             if (q >= n) break;
             const uint32_t sa = smem + s * stage_bytes + q * block_bytes, sb = sa + PARTS * a_bytes;
 #pragma unroll
             for (int p = 0; p < PARTS; ++p) {
               if (a_mn) {
-                if (a0) tma_load_3d_pair(sa + p * a_bytes, ma, am, k, p, bar);
-                if (a1) tma_load_3d_pair(sa + p * a_bytes + 8192, ma, am + 64, k, p, bar);
+                if (a0) tma_load_3d_pair(sa + p * a_bytes, ma, am, k, p + za, bar);
+                if (a1) tma_load_3d_pair(sa + p * a_bytes + 8192, ma, am + 64, k, p + za, bar);
               } else if (a0) {
                 tma_load_3d_pair(sa + p * a_bytes, ma, k, am, p, bar);
               }
-              if (b0) tma_load_3d_pair(sb + p * b_bytes, mb, k, bn0, p, bar);
+              if (b0) tma_load_3d_pair(sb + p * b_bytes, mb, k, bn0, p + zb, bar);
+            }
+            if (behind && za == 0) {
+              za = 1;
+            } else {
+              za = 0;
+              k += BK;
             }
           }
           if (++s == stages) {
@@ -436,7 +457,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       const Gemm &g = a.g[t.which];
       const int64_t row = t.m0 + rank * 128 + quarter * 32 + lane;
       const bool live = row < g.m;
-      const int64_t c0 = t.n0 + half * cols;  // first column of this warp (in the piece)
+      const bool beside = TWO && !t.which;
+      const int64_t c0 = beside ? 0 : t.n0 + half * cols;  // first column of this warp (in the piece)
       // per-row state of the epilogue
       float mx = -INFINITY, sum = 0.f, lse = 0.f, dl = 0.f;
       int64_t tgt = -1;
@@ -492,16 +514,17 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           for (int i = 0; i < 64; ++i)
             v[i] = PARTS == 1 ? ex2((v[i] - lse) * LOG2E) : expf(v[i] - lse);
           if (hit >= 0 && hit < 64) {
+            const float at = FEW ? a.at_target[row] : 0.f;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (hit == i) v[i] -= 1.f;
+              if (hit == i) v[i] = FEW ? at : v[i] - 1.f;
           }
           // a token that is not scored has no gradient, whatever its logits are
 #pragma unroll
           for (int i = 0; i < 64; ++i) v[i] = scored ? v[i] * dl : 0.f;
           if (row - lane >= g.m) return;
 #pragma unroll
-          for (int p = 0; p < PARTS; ++p) {
+          for (int p = 0; p < G_PARTS; ++p) {
             uint4 w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
               for (int j = 0; j < 4; ++j) {
                 float &x = v[8 * i + 2 * j], &y = v[8 * i + 2 * j + 1];
                 u[j] = pack_bf16(x, y);
-                if (PARTS == 3) {  // the bf16 nearest to what is left, and exactly what is left then
+                if (p + 1 < G_PARTS) {  // the bf16 nearest to what is left, and exactly what is left then
                   x -= __uint_as_float(u[j] << 16);
                   y -= __uint_as_float(u[j] & 0xffff0000u);
                 }
@@ -571,7 +594,8 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           const int64_t step = g.trans ? g.m : 1;
           const int64_t at = g.trans ? col * g.m + row : row * g.n + col;
           if (g.out_f32) {
-            float *out = reinterpret_cast<float *>(g.out) + (int64_t)t.split * g.m * g.n + at;
+            const int64_t split = beside ? 2 * t.split + half : t.split;
+            float *out = reinterpret_cast<float *>(g.out) + split * g.m * g.n + at;
 #pragma unroll
             for (int h = 0; h < 64; h += 16) {
               float old[16];
@@ -723,22 +747,58 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// p - 1 at the target of each of few tokens, from its logit summed in 64 bits: a
+// tile's logit comes from the tensor core's truncated sum, and where p is near 1
+// its error is a large part of what is left of p - 1.
+template <typename T> struct Targets {
+  const T *x, *w;  // as the caller has them
+  int64_t xs;
+  const float *lse;
+  float *at_target;  // null: not wanted
+};
+// One token by the CTA.
+template <typename T>
+__device__ __forceinline__ void at_target(const Targets<T> &g, int64_t n, int64_t D, const int64_t *target, int64_t V) {
+  __shared__ double part[8];
+  const int64_t t = target[n];
+  if (t < 0 || t >= V) return;  // not scored: nobody reads it
+  double s = 0.;
+#pragma unroll 8
+  for (int64_t c = threadIdx.x; c < D; c += 256)
+    s += (double)to_f32(g.x[n * g.xs + c]) * (double)to_f32(g.w[t * D + c]);
+  for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) s += part[i];
+    g.at_target[n] = expm1f((float)(s - (double)g.lse[n]));
+  }
+}
+
 // Before the products of the backward: dst [parts, cols, dpitch] = src [parts,
 // rows, spitch] transposed, 64 x 64 at a time through shared memory (pitches
 // are multiples of 8: two values per access); and, by one CTA beside them, the
 // unit of G (null: none wanted): the largest |dloss| of a scored token, 1 if
 // there is none.  With dloss one number for all tokens, the usual mean, G in
 // that unit is p - [v = target] itself, and the -1 at the target of a token
-// that is far from foreseen, most of its gradient, is exact in bf16.
+// that is far from foreseen, most of its gradient, is exact in bf16.  Further
+// CTAs take a token each of `targets`.
+template <typename T>
 __global__ void __launch_bounds__(256)
-    ce_prepare_kernel(const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
+    ce_prepare_kernel(const Targets<T> targets, const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
                       int64_t dpitch, __nv_bfloat16 *__restrict__ dst, const float *__restrict__ dloss,
                       const int64_t *__restrict__ target, int64_t V, float *__restrict__ unit) {
   __shared__ __nv_bfloat162 tile[64][33];
   __shared__ float red[8];
   follow_wait();
   follow_allow();
-  if (blockIdx.x == gridDim.x - 1) {
+  const int64_t beyond = (int64_t)blockIdx.x - (rows + 63) / 64;
+  if (beyond > 0) {
+    const int64_t n = (beyond - 1) * gridDim.y + blockIdx.y;
+    if (blockIdx.z == 0 && n < rows) at_target(targets, n, cols, target, V);
+    return;
+  }
+  if (beyond == 0) {
     if (!unit || blockIdx.y || blockIdx.z) return;
     float m = 0.f;
 #pragma unroll 4
@@ -811,6 +871,13 @@ __global__ void __launch_bounds__(256)
 
 // ---- host ------------------------------------------------------------------
 constexpr size_t G_BYTES = (size_t)512 << 20;   // G of one piece of the vocabulary, about
+// Tokens up to which the gradients take G in two bf16 parts (of bf16 operands) and
+// its entry at the target from a logit in 64 bits.  A handful of tokens has no
+// others that average an entry's error out: gradients of single tokens were up
+// to 1.6e-2 off (2-norm) with neither, where rounding the result to bf16 alone
+// gives 1.7e-3.  With 16 tokens of 2048 x 32000 it costs 7 of 99 us.  With 128 it
+// would be 14 of 110 us, for 1.65e-3 instead of 1.9e-3: left as one bf16 there.
+constexpr int64_t FEW_TOKENS = 64;
 constexpr size_t SUMS_BYTES = (size_t)512 << 20;  // fp32 sums of a gradient's splits, at most (if there are several)
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -818,12 +885,15 @@ inline int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Layout {
   int parts, bn, bn_z;               // bn_z: tile width of the logits
+  bool few;                          // no more than FEW_TOKENS
+  int g_parts;                       // of G
   bool pack;                         // x and w are copied to rows TMA can address
   int64_t pitch, xt_pitch, piece, pieces, gpitch;
   int splits, run;  // dx's K axis: `splits` runs of `run` k-blocks (in the first, longest piece)
   int splits_w, run_w;  // dw's
   bool dx_f32, dw_sums;
-  size_t off_x, off_w, off_part, off_zt, off_unit, off_xt, off_g, off_dx, off_dw, total;
+  int sums;  // of dx, for each of its splits
+  size_t off_x, off_w, off_part, off_zt, off_unit, off_at, off_xt, off_g, off_dx, off_dw, total;
 };
 
 // Pairs of CTAs that run at once on the current device.
@@ -843,7 +913,7 @@ int64_t pair_count() {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto *k = ce_product_kernel<STATS, 1>;
+    auto *k = ce_product_kernel<STATS, 1, false>;
     if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n <= 0) {
@@ -879,16 +949,17 @@ Deal deal(int64_t ux, int64_t run_x, int64_t uw, int64_t run_w) {
 // memory and back (1.8 MB per k-block's time) and a launch.
 void choose_splits(Layout &L, int64_t N, int64_t D, int64_t cols) {
   static const int tries[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
-  const int64_t tx = up(D, BM) * up(N, L.bn), tw = up(cols, BM) * up(D, L.bn), kx = up(cols, BK), kw = up(N, BK);
+  const int64_t tx = up(D, BM) * up(N, L.bn), tw = up(cols, BM) * up(D, L.bn), kx = up(cols, BK),
+                kw = up(N, BK) * L.sums;
   int64_t least = -1;
   for (int sx : tries) {
-    const int64_t rx = up(kx, sx), mx = up(kx, rx) * N * D * 4;
+    const int64_t rx = up(kx, sx), mx = up(kx, rx) * L.sums * N * D * 4;
     if (sx > 1 && (sx > kx || mx > (int64_t)SUMS_BYTES)) break;
     for (int sw : tries) {
       const int64_t rw = up(kw, sw), mw = up(kw, rw) * cols * D * 4;
       if (sw > 1 && (sw > kw || mw > (int64_t)SUMS_BYTES)) break;
       int64_t cost = deal(tx * up(kx, rx), rx, tw * up(kw, rw), rw).longest;
-      if (sx > 1 || L.pieces > 1) cost += 2 * mx / 1800000 + 8;
+      if (sx > 1 || L.pieces > 1 || L.sums > 1) cost += 2 * mx / 1800000 + 8;
       if (sw > 1) cost += 2 * mw / 1800000 + 8;
       if (least < 0 || cost < least) {
         least = cost;
@@ -937,19 +1008,23 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     take(L.off_part, (size_t)up(V, L.bn_z) * 2 * N * sizeof(float2));
     take(L.off_zt, (size_t)N * sizeof(float));
   } else {
-    const int64_t most = std::max<int64_t>(2048, (int64_t)(G_BYTES / (2 * L.parts * (size_t)N)) / 256 * 256);
+    L.few = N <= FEW_TOKENS;
+    L.g_parts = g_parts_of(L.parts, L.few);
+    L.sums = L.g_parts == 2 ? 2 : 1;
+    const int64_t most = std::max<int64_t>(2048, (int64_t)(G_BYTES / (2 * L.g_parts * (size_t)N)) / 256 * 256);
     L.pieces = up(V, most);
     L.piece = up(up(V, L.pieces), 256) * 256;
     L.pieces = up(V, L.piece);
     L.gpitch = L.piece;
     L.xt_pitch = up(N, 8) * 8;
     take(L.off_unit, sizeof(float));
+    if (L.few) take(L.off_at, (size_t)N * sizeof(float));
     take(L.off_xt, (size_t)L.parts * D * L.xt_pitch * 2);
-    take(L.off_g, (size_t)L.parts * N * L.gpitch * 2);
+    take(L.off_g, (size_t)L.g_parts * N * L.gpitch * 2);
     choose_splits(L, N, D, std::min(L.piece, V));
-    L.dx_f32 = L.splits > 1 || L.pieces > 1;
+    L.dx_f32 = L.splits > 1 || L.pieces > 1 || L.sums > 1;
     L.dw_sums = L.splits_w > 1;
-    if (L.dx_f32) take(L.off_dx, (size_t)L.splits * N * D * sizeof(float));
+    if (L.dx_f32) take(L.off_dx, (size_t)L.splits * L.sums * N * D * sizeof(float));
     if (L.dw_sums) take(L.off_dw, (size_t)L.splits_w * std::min(L.piece, V) * D * sizeof(float));
   }
   L.total = off;
@@ -974,8 +1049,8 @@ bool make_map3(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int
 }
 
 // follows: the kernel before it on the stream is one of this call's.
-template <int KIND, int PARTS> cudaError_t launch(const Args &a, bool follows, cudaStream_t st) {
-  auto *k = ce_product_kernel<KIND, PARTS>;
+template <int KIND, int PARTS, bool FEW> cudaError_t launch(const Args &a, bool follows, cudaStream_t st) {
+  auto *k = ce_product_kernel<KIND, PARTS, FEW>;
   const int ring = a.stages * join_of(KIND, PARTS) * block_bytes_of(PARTS, a.a_bytes, a.bn);
   const int smem = ring + extra_of(KIND, PARTS, a.a_bytes) + 1024;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -995,21 +1070,30 @@ template <int KIND, int PARTS> cudaError_t launch(const Args &a, bool follows, c
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
-template <int KIND> cudaError_t launch(const Args &a, int parts, bool follows, cudaStream_t st) {
-  return parts == 3 ? launch<KIND, 3>(a, follows, st) : launch<KIND, 1>(a, follows, st);
+// fp32 products have G's three parts whatever the tokens.
+template <int KIND> cudaError_t launch(const Args &a, int parts, bool few, bool follows, cudaStream_t st) {
+  if constexpr (KIND == STATS)
+    return parts == 3 ? launch<KIND, 3, false>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
+  else if constexpr (KIND == PRODUCT)
+    return parts == 3 ? launch<KIND, 3, false>(a, follows, st)
+                      : few ? launch<KIND, 1, true>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
+  else if (few)
+    return parts == 3 ? launch<KIND, 3, true>(a, follows, st) : launch<KIND, 1, true>(a, follows, st);
+  else
+    return parts == 3 ? launch<KIND, 3, false>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
 }
 
 // Rows of a K-major operand's load: a CTA's share, or what there is of it.
 int box_of(int64_t rows, int share) { return (int)std::min<int64_t>(share, up(rows, 8) * 8); }
 
-void whole_k(Gemm &g, int64_t m, int64_t n, int64_t k, int bn) {
+void whole_k(Gemm &g, int64_t m, int64_t n, int64_t k, int bn, int runs = 1) {
   g.a_box = box_of(m, 128);
   g.b_box = box_of(n, bn / 2);
   g.m = m;
   g.n = n;
   g.mt = (int32_t)up(m, BM);
   g.nt = (int32_t)up(n, bn);
-  g.kb = g.kb_split = (int32_t)up(k, BK);
+  g.kb = g.kb_split = (int32_t)up(k, BK) * runs;
   g.splits = 1;
 }
 
@@ -1110,7 +1194,7 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   a.part = (float2 *)(ws + L.off_part);
   a.zt = (float *)(ws + L.off_zt);
   a.err = device_error_ptr();
-  e = ce::launch<STATS>(a, L.parts, L.pack, st);
+  e = ce::launch<STATS>(a, L.parts, false, L.pack, st);
   mark_launch("ce_stats", st);
   if (e != cudaSuccess) return status_of(e);
   const int64_t slots = up(V, L.bn_z / 2);  // tile halves that hold part of the vocabulary
@@ -1141,15 +1225,21 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   int *err = device_error_ptr();
   const __nv_bfloat16 *xt = (const __nv_bfloat16 *)(ws + L.off_xt);
   float *unit = L.parts == 1 ? (float *)(ws + L.off_unit) : nullptr;  // three parts hold dloss as it is
-  const dim3 grid((unsigned)up(N, 64) + 1, (unsigned)up(D, 64), (unsigned)L.parts);
+  float *at = L.few ? (float *)(ws + L.off_at) : nullptr;
+  const int64_t gy = up(D, 64), xs = x_stride ? x_stride : D;
+  const dim3 grid((unsigned)(up(N, 64) + 1 + (L.few ? up(N, gy) : 0)), (unsigned)gy, (unsigned)L.parts);
   __nv_bfloat16 *to = (__nv_bfloat16 *)(ws + L.off_xt);
   const __nv_bfloat16 *rows = (const __nv_bfloat16 *)r.x;
-  if (L.pack)
-    e = launch_follow(ce_prepare_kernel, grid, dim3(256), st, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
-  else {
-    ce_prepare_kernel<<<grid, 256, 0, st>>>(rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
-    e = cudaGetLastError();
-  }
+  auto prepare = [&](auto *typed) {
+    typedef std::remove_const_t<std::remove_pointer_t<decltype(typed)>> T;
+    const Targets<T> targets = {typed, (const T *)w, xs, lse, at};
+    if (L.pack)
+      return launch_follow(ce_prepare_kernel<T>, grid, dim3(256), st, targets, rows, N, D, r.xp, L.xt_pitch, to, dloss,
+                           target, V, unit);
+    ce_prepare_kernel<T><<<grid, 256, 0, st>>>(targets, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
+    return cudaGetLastError();
+  };
+  e = dtype == GLACORE_F32 ? prepare((const float *)x) : prepare((const __nv_bfloat16 *)x);
   mark_launch("ce_prepare", st);
   if (e != cudaSuccess) return status_of(e);
   for (int64_t i = 0; i < L.pieces; ++i) {
@@ -1168,24 +1258,25 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     a.lse = lse;
     a.dloss = dloss;
     a.unit = unit;
+    a.at_target = at;
     a.err = err;
     auto w_map = [&](CUtensorMap *m, int box_rows) {
       return make_map3(m, wp, D, cols, L.parts, r.wp, V, box_rows);
     };
     auto g_map = [&](CUtensorMap *m, int box_rows) {
-      return make_map3(m, ws + L.off_g, cols, N, L.parts, L.gpitch, N, box_rows);
+      return make_map3(m, ws + L.off_g, cols, N, L.g_parts, L.gpitch, N, box_rows);
     };
     if (!make_map3(&a.g[0].a, r.x, D, N, L.parts, r.xp, N, box_of(N, 128)) ||
         !w_map(&a.g[0].b, box_of(cols, L.bn_z / 2)))
       return status_of(cudaErrorInvalidValue);
     whole_k(a.g[0], N, cols, D, L.bn_z);
     // all of G's columns: the tiles' are written whole
-    if (L.parts == 1 && !make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, L.parts, L.gpitch, N, 32))
+    if (L.parts == 1 && !make_map3(&a.g[0].o, ws + L.off_g, L.gpitch, N, L.g_parts, L.gpitch, N, 32))
       return status_of(cudaErrorInvalidValue);
     a.g[0].out = ws + L.off_g;
     a.g[0].out_pitch = L.gpitch;
     a.units0 = a.units = (int64_t)a.g[0].mt * a.g[0].nt;
-    e = ce::launch<GRAD>(a, L.parts, true, st);
+    e = ce::launch<GRAD>(a, L.parts, L.few, true, st);
     mark_launch("ce_grad", st);
     if (e != cudaSuccess) return status_of(e);
     // dx^T (K = the piece) and dw of the piece (K = the tokens)
@@ -1204,7 +1295,7 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     gx.add = i > 0;
     gx.trans = 1;
     gx.out = L.dx_f32 ? (void *)(ws + L.off_dx) : dx;
-    whole_k(gw, cols, D, N, L.bn);
+    whole_k(gw, cols, D, N, L.bn, L.sums);  // two parts of G: one after the other
     gw.a_mn = 1;
     gw.kb_split = L.run_w;
     gw.splits = L.splits_w;
@@ -1217,13 +1308,13 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     a.units0 = (int64_t)gx.mt * gx.nt * gx.splits;
     a.units = a.units0 + (int64_t)gw.mt * gw.nt * gw.splits;
     a.skip = deal(a.units0, gx.kb_split, a.units - a.units0, gw.kb_split).skip;
-    e = ce::launch<PRODUCT>(a, L.parts, true, st);
+    e = ce::launch<PRODUCT>(a, L.parts, L.few, true, st);
     mark_launch("ce_product", st);
     if (e == cudaSuccess && L.dw_sums)
       e = add_splits((const float *)(ws + L.off_dw), gw.splits, cols * D, dtype, dw_piece, st);
     if (e != cudaSuccess) return status_of(e);
   }
-  if (L.dx_f32) e = add_splits((const float *)(ws + L.off_dx), L.splits, N * D, dtype, dx, st);
+  if (L.dx_f32) e = add_splits((const float *)(ws + L.off_dx), L.splits * L.sums, N * D, dtype, dx, st);
   return status_of(e);
 }
 
