@@ -82,7 +82,7 @@ constexpr int SMEM = 231168;          // shared memory of ring and output stagin
 // stage of the ring (gradients of 1001 x 520 x 10007: 33 us more with two stages).
 constexpr int out_bytes_of(int parts) { return parts == 3 ? 1024 : 4096; }
 constexpr int GROUP_M = 8;            // row tiles that share a walk over the columns (L2 reuse)
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.4426950408889634f;
 
 // One product C[m, n] = A B^T over k-blocks, tiles of BM x bn.
 struct Gemm {
@@ -108,7 +108,7 @@ struct Args {
   int32_t bn, stages, a_bytes;  // a_bytes: a CTA's rows of A in a k-block, as far as they are there
   int64_t N, V, v0;  // tokens, vocabulary, first column of the piece
   const int64_t *target;
-  float2 *part;      // STATS: [2 * nt][N] (maximum * log2 e, sum)
+  float2 *part;      // STATS: [2 * nt][N] (maximum, sum of exponentials of the differences from it), the target left out
   float *zt;         // STATS: [N] the target's logit
   const float *lse, *dloss;  // GRAD
   const float *unit;         // G is in units of *unit (null: 1)
@@ -193,6 +193,16 @@ constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 1 : kind == ST
 // The six products of parts (a, b), small ones first; the last is the large
 // one (bf16 operands: the only one).
 __device__ constexpr int PA[6] = {2, 0, 1, 1, 0, 0}, PB[6] = {0, 2, 1, 0, 1, 0};
+
+// (x - r) f and (y - r) f, two operations at once.
+__device__ __forceinline__ float2 scaled_difference(float x, float y, float r, float f) {
+  float2 o;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 b, {%5, %5};\n mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(x), "f"(y), "f"(-r), "f"(f));
+  return o;
+}
 
 // Bytes of one k-block (and part) that CTA `rank` loads for a tile.  What lies
 // wholly past the end of M or N is not loaded: whatever is in its place only
@@ -488,7 +498,10 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
             float z = 0.f;
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (tgt == col + i) z = v[i];
+              if (tgt == col + i) {
+                z = v[i];
+                v[i] = -INFINITY;
+              }
             if (live) a.zt[row] = z;
           }
           float top[4] = {mx, v[0], v[1], v[2]};
@@ -496,12 +509,18 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
           for (int i = 3; i < 64; ++i) top[i & 3] = fmaxf(top[i & 3], v[i]);
           const float peak = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           // a row of -inf so far: any finite reference gives sums of 0
-          const float ref = peak == -INFINITY ? 0.f : peak * LOG2E;
+          const float ref = peak == -INFINITY ? 0.f : peak;
+          // The difference first, as for G: a product of either with log2 e is
+          // rounded at the size of the logit.
           float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 64; ++i) s[i & 3] += ex2(fmaf(v[i], LOG2E, -ref));
+          for (int i = 0; i < 64; i += 2) {
+            const float2 d = scaled_difference(v[i], v[i + 1], ref, LOG2E);
+            s[i & 3] += ex2(d.x);
+            s[(i & 3) + 1] += ex2(d.y);
+          }
           // no finite maximum yet: the sum is 0, or a NaN that stays
-          const float old = mx == -INFINITY ? sum : sum * ex2(mx * LOG2E - ref);
+          const float old = mx == -INFINITY ? sum : sum * ex2((mx - ref) * LOG2E);
           sum = old + ((s[0] + s[1]) + (s[2] + s[3]));
           mx = peak;
         } else if constexpr (KIND == GRAD) {
@@ -666,7 +685,7 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
       }
       if (!ok) break;
       if (KIND == STATS && live && c0 < a.V)
-        a.part[(int64_t)(2 * t.nt + half) * a.N + row] = make_float2(mx == -INFINITY ? mx : mx * LOG2E, sum);
+        a.part[(int64_t)(2 * t.nt + half) * a.N + row] = make_float2(mx, sum);
     }
   }
   if (staged_out(KIND) && warp < EPI_WARPS && lane == 0) bulk_wait_all();
@@ -680,7 +699,10 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
 }
 
 // lse and loss of 32 rows from the tiles' (maximum, sum) pairs: 32 threads per
-// row take every 32nd pair, then merge in order.
+// row take every 32nd pair, then merge in order.  The pairs are of the other
+// tokens: beside the target's own 1 the sum of a well foreseen token would lose
+// its digits, and its loss is nothing else.  No term of the loss is rounded at
+// the size of a logit, and it is never negative.
 constexpr int MERGE_ROWS = 32, MERGE_LANES = 32;
 __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
     ce_merge_kernel(const float2 *__restrict__ part, int64_t slots, int64_t N, int64_t V,
@@ -692,7 +714,7 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
   float m = -INFINITY, s = 0.f;
   auto merge = [&](float2 p) {
     const float top = fmaxf(m, p.x), ref = top == -INFINITY ? 0.f : top;
-    s = s * exp2f(m - ref) + p.y * exp2f(p.x - ref);
+    s = s * exp2f((m - ref) * LOG2E) + p.y * exp2f((p.x - ref) * LOG2E);
     m = top;
   };
   if (row < N) {
@@ -710,11 +732,23 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
   __syncthreads();
   if (threadIdx.y || row >= N) return;
   for (int i = 1; i < MERGE_LANES; ++i) merge(red[i][threadIdx.x]);
-  const float l = (m + log2f(s)) * LN2;
-  lse[row] = l;
   const int64_t t = target[row];
   if (t >= V) set_device_error(err, GLACORE_ERR_INDEX);
-  loss[row] = t < 0 || t >= V ? 0.f : l - zt[row];
+  if (t < 0 || t >= V) {
+    lse[row] = m + logf(s);
+    loss[row] = 0.f;
+    return;
+  }
+  const float z = zt[row];
+  if (m > z) {
+    const float l = logf(s + exp2f((z - m) * LOG2E));
+    lse[row] = m + l;
+    loss[row] = (m - z) + l;
+  } else {  // the target's logit is the largest (or a NaN, or infinite: z - z)
+    const float l = log1pf(s * exp2f((m - z) * LOG2E)) + (z - z);
+    lse[row] = z + l;
+    loss[row] = l;
+  }
 }
 
 // A gradient from its splits' sums, added in order and rounded to its type.
