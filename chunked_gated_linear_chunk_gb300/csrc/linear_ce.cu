@@ -187,8 +187,14 @@ constexpr int stages_of(int kind, int parts, int a_bytes, int bn) {
   const int n = (SMEM - extra_of(kind, parts, a_bytes)) / (join_of(kind, parts) * block_bytes_of(parts, a_bytes, bn));
   return n < MAX_STAGES ? n : MAX_STAGES;
 }
-// k-blocks whose products one accumulator sums
-constexpr int chunk_of(int kind, int parts) { return parts == 3 ? 1 : kind == STATS ? 16 : 1 << 30; }
+// k-blocks whose products one accumulator sums.  The logits of bf16 operands (8192
+// x 2048 x 32000, loss): 16 k-blocks 5.4e-7 off in 544 us, 8 2.5e-7 in 549, 4
+// 1.3e-7 in 596.  Of few tokens, where w's way from memory bounds the call (16
+// tokens): 8 in 32.6 us, 4 in 34.9; with 8 a single token's loss was up to 2e-6
+// off, where sums in fp32 rounded to nearest give 5e-7.
+constexpr int chunk_of(int kind, int parts, bool few) {
+  return parts == 3 ? 1 : kind != STATS ? 1 << 30 : few ? 4 : 8;
+}
 
 // The six products of parts (a, b), small ones first; the last is the large
 // one (bf16 operands: the only one).
@@ -228,8 +234,9 @@ template <int KIND, int PARTS, bool FEW>
 __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_constant__ Args a) {
   constexpr int G_PARTS = g_parts_of(PARTS, FEW);
   constexpr bool TWO = KIND == PRODUCT && PARTS == 1 && G_PARTS == 2;
-  constexpr int CHUNK = chunk_of(KIND, PARTS);
+  constexpr int CHUNK = chunk_of(KIND, PARTS, FEW);
   constexpr bool CHUNKED = KIND == STATS || PARTS == 3;
+  static_assert(CHUNK % join_of(KIND, PARTS) == 0);  // an accumulator's k-blocks fill whole stages
   constexpr int BUFS = bufs_of(PARTS), BUF_COLS = 512 / BUFS;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[MAX_STAGES], empty[MAX_STAGES], acc_full[BUFS], acc_empty[BUFS], turn[2], drained;
@@ -698,17 +705,52 @@ __global__ void __launch_bounds__(THREADS, 1) ce_product_kernel(const __grid_con
   }
 }
 
+// The logit at the target of each of few tokens, from the caller's own x and w: a
+// tile's logit comes from the tensor core's truncated sum, and where p is near 1
+// its error is a large part of the loss and of p - 1.
+template <typename T> struct Targets {
+  const T *x, *w;
+  int64_t xs, D;
+  // A warp's share of token n's logit at t: every `threads`-th product from
+  // `first` on.  A thread's are added in A, the threads' in 64 bits.
+  template <typename A> __device__ __forceinline__ double part(int64_t n, int64_t t, int first, int threads) const {
+    const T *xr = x + n * xs, *wr = w + t * D;
+    A f[4] = {A(0), A(0), A(0), A(0)};
+    int64_t c = first;
+    for (; c + 15 * threads < D; c += 16 * threads)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i & 3] = fma((A)to_f32(xr[c + i * threads]), (A)to_f32(wr[c + i * threads]), f[i & 3]);
+    for (; c < D; c += threads) f[0] = fma((A)to_f32(xr[c]), (A)to_f32(wr[c]), f[0]);
+    double s = ((double)f[0] + (double)f[1]) + ((double)f[2] + (double)f[3]);
+    for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    return s;
+  }
+};
+
 // lse and loss of 32 rows from the tiles' (maximum, sum) pairs: 32 threads per
 // row take every 32nd pair, then merge in order.  The pairs are of the other
 // tokens: beside the target's own 1 the sum of a well foreseen token would lose
 // its digits, and its loss is nothing else.  No term of the loss is rounded at
-// the size of a logit, and it is never negative.
+// the size of a logit, and it is never negative.  FEW: the target's logit comes
+// from `targets`, a row per warp, before the wait for the tiles: x, w and target
+// were there before the call's first kernel.
 constexpr int MERGE_ROWS = 32, MERGE_LANES = 32;
+template <typename T, bool FEW>
 __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
-    ce_merge_kernel(const float2 *__restrict__ part, int64_t slots, int64_t N, int64_t V,
+    ce_merge_kernel(const Targets<T> targets, const float2 *__restrict__ part, int64_t slots, int64_t N, int64_t V,
                     const int64_t *__restrict__ target, const float *__restrict__ zt, float *__restrict__ loss,
                     float *__restrict__ lse, int *err) {
   __shared__ float2 red[MERGE_LANES][MERGE_ROWS];
+  __shared__ float at_target[FEW ? MERGE_ROWS : 1];
+  if constexpr (FEW) {
+    const int64_t n = (int64_t)blockIdx.x * MERGE_ROWS + threadIdx.y, t = n < N ? target[n] : -1;
+    if (t >= 0 && t < V) {
+      // shares in fp32, each rounded at a small part of the logit's size: an SM's
+      // few 64-bit units took 16 tokens of D = 2048 18 us longer
+      const double z = targets.template part<float>(n, t, threadIdx.x, 32);
+      if (threadIdx.x == 0) at_target[threadIdx.y] = (float)z;
+    }
+  }
   follow_wait();
   const int64_t row = (int64_t)blockIdx.x * MERGE_ROWS + threadIdx.x;
   float m = -INFINITY, s = 0.f;
@@ -739,7 +781,7 @@ __global__ void __launch_bounds__(MERGE_ROWS *MERGE_LANES)
     loss[row] = 0.f;
     return;
   }
-  const float z = zt[row];
+  const float z = FEW ? at_target[threadIdx.x] : zt[row];
   if (m > z) {
     const float l = logf(s + exp2f((z - m) * LOG2E));
     lse[row] = m + l;
@@ -781,31 +823,19 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// p - 1 at the target of each of few tokens, from its logit summed in 64 bits: a
-// tile's logit comes from the tensor core's truncated sum, and where p is near 1
-// its error is a large part of what is left of p - 1.
-template <typename T> struct Targets {
-  const T *x, *w;  // as the caller has them
-  int64_t xs;
-  const float *lse;
-  float *at_target;  // null: not wanted
-};
-// One token by the CTA.
+// p - 1 at token n's target, by the CTA.
 template <typename T>
-__device__ __forceinline__ void at_target(const Targets<T> &g, int64_t n, int64_t D, const int64_t *target, int64_t V) {
+__device__ __forceinline__ void find_at_target(const Targets<T> &g, int64_t n, const int64_t *target, int64_t V,
+                                               const float *lse, float *at_target) {
   __shared__ double part[8];
   const int64_t t = target[n];
   if (t < 0 || t >= V) return;  // not scored: nobody reads it
-  double s = 0.;
-#pragma unroll 8
-  for (int64_t c = threadIdx.x; c < D; c += 256)
-    s += (double)to_f32(g.x[n * g.xs + c]) * (double)to_f32(g.w[t * D + c]);
-  for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+  double s = g.template part<double>(n, t, threadIdx.x, 256);  // p - 1 of fp32 operands needs them all
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int i = 1; i < 8; ++i) s += part[i];
-    g.at_target[n] = expm1f((float)(s - (double)g.lse[n]));
+    at_target[n] = expm1f((float)(s - (double)lse[n]));
   }
 }
 
@@ -816,10 +846,11 @@ __device__ __forceinline__ void at_target(const Targets<T> &g, int64_t n, int64_
 // there is none.  With dloss one number for all tokens, the usual mean, G in
 // that unit is p - [v = target] itself, and the -1 at the target of a token
 // that is far from foreseen, most of its gradient, is exact in bf16.  Further
-// CTAs take a token each of `targets`.
+// CTAs take a token each for at_target.
 template <typename T>
 __global__ void __launch_bounds__(256)
-    ce_prepare_kernel(const Targets<T> targets, const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
+    ce_prepare_kernel(const Targets<T> targets, const float *__restrict__ lse, float *__restrict__ at_target,
+                      const __nv_bfloat16 *__restrict__ src, int64_t rows, int64_t cols, int64_t spitch,
                       int64_t dpitch, __nv_bfloat16 *__restrict__ dst, const float *__restrict__ dloss,
                       const int64_t *__restrict__ target, int64_t V, float *__restrict__ unit) {
   __shared__ __nv_bfloat162 tile[64][33];
@@ -829,7 +860,7 @@ __global__ void __launch_bounds__(256)
   const int64_t beyond = (int64_t)blockIdx.x - (rows + 63) / 64;
   if (beyond > 0) {
     const int64_t n = (beyond - 1) * gridDim.y + blockIdx.y;
-    if (blockIdx.z == 0 && n < rows) at_target(targets, n, cols, target, V);
+    if (blockIdx.z == 0 && n < rows) find_at_target(targets, n, target, V, lse, at_target);
     return;
   }
   if (beyond == 0) {
@@ -905,8 +936,8 @@ __global__ void __launch_bounds__(256)
 
 // ---- host ------------------------------------------------------------------
 constexpr size_t G_BYTES = (size_t)512 << 20;   // G of one piece of the vocabulary, about
-// Tokens up to which the gradients take G in two bf16 parts (of bf16 operands) and
-// its entry at the target from a logit in 64 bits.  A handful of tokens has no
+// Tokens up to which the target's logit is summed apart (Targets), and the gradients
+// take G in two bf16 parts (of bf16 operands).  A handful of tokens has no
 // others that average an entry's error out: gradients of single tokens were up
 // to 1.6e-2 off (2-norm) with neither, where rounding the result to bf16 alone
 // gives 1.7e-3.  With 16 tokens of 2048 x 32000 it costs 7 of 99 us.  With 128 it
@@ -1028,6 +1059,7 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     }
   }
   L.pack = L.parts == 3 || D % 8 != 0;
+  L.few = N <= FEW_TOKENS;
   L.pitch = up(D, 8) * 8;
   size_t off = 0;
   auto take = [&](size_t &o, size_t bytes) {
@@ -1042,7 +1074,6 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     take(L.off_part, (size_t)up(V, L.bn_z) * 2 * N * sizeof(float2));
     take(L.off_zt, (size_t)N * sizeof(float));
   } else {
-    L.few = N <= FEW_TOKENS;
     L.g_parts = g_parts_of(L.parts, L.few);
     L.sums = L.g_parts == 2 ? 2 : 1;
     const int64_t most = std::max<int64_t>(2048, (int64_t)(G_BYTES / (2 * L.g_parts * (size_t)N)) / 256 * 256);
@@ -1104,17 +1135,12 @@ template <int KIND, int PARTS, bool FEW> cudaError_t launch(const Args &a, bool 
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, k, a);
 }
-// fp32 products have G's three parts whatever the tokens.
 template <int KIND> cudaError_t launch(const Args &a, int parts, bool few, bool follows, cudaStream_t st) {
-  if constexpr (KIND == STATS)
-    return parts == 3 ? launch<KIND, 3, false>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
-  else if constexpr (KIND == PRODUCT)
-    return parts == 3 ? launch<KIND, 3, false>(a, follows, st)
-                      : few ? launch<KIND, 1, true>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
-  else if (few)
-    return parts == 3 ? launch<KIND, 3, true>(a, follows, st) : launch<KIND, 1, true>(a, follows, st);
-  else
-    return parts == 3 ? launch<KIND, 3, false>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
+  // fp32 operands: only G's entry at the target differs
+  if (parts == 3)
+    return KIND == GRAD && few ? launch<KIND, 3, KIND == GRAD>(a, follows, st)
+                               : launch<KIND, 3, false>(a, follows, st);
+  return few ? launch<KIND, 1, true>(a, follows, st) : launch<KIND, 1, false>(a, follows, st);
 }
 
 // Rows of a K-major operand's load: a CTA's share, or what there is of it.
@@ -1228,12 +1254,24 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
   a.part = (float2 *)(ws + L.off_part);
   a.zt = (float *)(ws + L.off_zt);
   a.err = device_error_ptr();
-  e = ce::launch<STATS>(a, L.parts, false, L.pack, st);
+  e = ce::launch<STATS>(a, L.parts, L.few, L.pack, st);
   mark_launch("ce_stats", st);
   if (e != cudaSuccess) return status_of(e);
   const int64_t slots = up(V, L.bn_z / 2);  // tile halves that hold part of the vocabulary
-  e = launch_follow(ce_merge_kernel, dim3((unsigned)up(N, MERGE_ROWS)), dim3(MERGE_ROWS, MERGE_LANES), st,
-                    (const float2 *)a.part, slots, N, V, target, (const float *)a.zt, loss, lse, a.err);
+  auto merge = [&](auto *typed, auto few) {
+    typedef std::remove_const_t<std::remove_pointer_t<decltype(typed)>> T;
+    const Targets<T> targets = {typed, (const T *)w, x_stride ? x_stride : D, D};
+    return launch_follow(ce_merge_kernel<T, decltype(few)::value>, dim3((unsigned)up(N, MERGE_ROWS)),
+                         dim3(MERGE_ROWS, MERGE_LANES), st, targets, (const float2 *)a.part, slots, N, V, target,
+                         (const float *)a.zt, loss, lse, a.err);
+  };
+  const auto *xb = (const __nv_bfloat16 *)x;
+  if (!L.few)
+    e = merge(xb, std::false_type());  // reads no x
+  else if (dtype == GLACORE_F32)
+    e = merge((const float *)x, std::true_type());
+  else
+    e = merge(xb, std::true_type());
   mark_launch("ce_merge", st);
   return status_of(e);
 }
@@ -1266,11 +1304,11 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
   const __nv_bfloat16 *rows = (const __nv_bfloat16 *)r.x;
   auto prepare = [&](auto *typed) {
     typedef std::remove_const_t<std::remove_pointer_t<decltype(typed)>> T;
-    const Targets<T> targets = {typed, (const T *)w, xs, lse, at};
+    const Targets<T> targets = {typed, (const T *)w, xs, D};
     if (L.pack)
-      return launch_follow(ce_prepare_kernel<T>, grid, dim3(256), st, targets, rows, N, D, r.xp, L.xt_pitch, to, dloss,
+      return launch_follow(ce_prepare_kernel<T>, grid, dim3(256), st, targets, lse, at, rows, N, D, r.xp, L.xt_pitch, to, dloss,
                            target, V, unit);
-    ce_prepare_kernel<T><<<grid, 256, 0, st>>>(targets, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
+    ce_prepare_kernel<T><<<grid, 256, 0, st>>>(targets, lse, at, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
     return cudaGetLastError();
   };
   e = dtype == GLACORE_F32 ? prepare((const float *)x) : prepare((const __nv_bfloat16 *)x);

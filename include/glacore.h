@@ -361,8 +361,7 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean,
  * Any N >= 0 and V up to 2^30, D up to 2^22 - 64.  x, w, dx and dw 16-byte aligned; for bf16
  * with D a multiple of 8, x_stride as well.  bf16 products run on the tensor
  * cores with fp32 sums, G rounded to bf16 for them (up to 64 tokens: to two bf16
- * parts, and its entry at the target comes from a logit summed in 64 bits);
- * fp32 operands are split exactly into three bf16 parts (results to fp32's accuracy).  x and w must be
+ * parts; their targets' logits are summed apart, rounded to nearest); fp32 operands are split exactly into three bf16 parts (results to fp32's accuracy).  x and w must be
  * finite (an infinity in a row that is not scored still reaches dw as NaN).
  * The workspace (the *_workspace_size bytes, 256-byte aligned) holds, forward,
  * 16 bytes per token and tile of the vocabulary (at most 256 columns; a 64th of

@@ -1,5 +1,5 @@
-"""The gradient of a handful of tokens, where no other token's error averages a
-rounding of G out, against 64 bits.
+"""The loss and the gradient of a handful of tokens, where no other token's error
+averages one out, against 64 bits.
 
 Tolerances, element by element, with S = sum |G| |w| (dx) or sum |G| |x| (dw) of
 the definition's own G = (p - [v = target]) dloss: the entry at the target keeps
@@ -58,3 +58,31 @@ def test_gradients_of_few_tokens(cuda_ok, N, D, V, dtype, pull):
     assert torch.all(dx[t < 0] == 0)
     again = glc.linear_ce_bwd(x, w, t, lse, dl)
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,D,V", [(1, 1072, 17911), (1, 80, 1618), (2, 1384, 143), (3, 33, 300), (2, 888, 1050),
+                                   (16, 520, 2000), (40, 64, 1003), (64, 2100, 500)])
+@pytest.mark.parametrize("pull", [0.0, 7.0, 14.0])
+def test_losses_of_few_tokens(cuda_ok, N, D, V, dtype, pull):
+    """An error of the logits moves the loss by (1 - p) of itself: the target's own
+    logit is within 2^-24 of itself, the others' sums are chunks of 32 truncated
+    steps, 32 * 2^-23 of the largest logit, joined by up to 5 rounded ones.  With
+    the exponentials' own 3e-6 that is (1 - p) (5e-6 top + 3e-6), and a few
+    roundings of the loss itself."""
+    x, w, t, _ = data(N, D, V, dtype, N + D + V, pull)
+    if N > 2:
+        t[1] = -100
+    loss, lse = glc.linear_ce_fwd(x, w, t)
+    z = x.double() @ w.double().T
+    top = z.abs().amax(1)
+    at = t.clamp(min=0)[:, None]
+    zt = z.gather(1, at)[:, 0]
+    others = torch.logsumexp(z.scatter(1, at, -float("inf")), 1)
+    want = torch.where(t < 0, 0.0, torch.nn.functional.softplus(others - zt, threshold=1000))
+    rest = torch.sigmoid(others - zt)  # 1 - p
+    assert bool(((loss.double() - want).abs() <= rest * (5e-6 * top + 3e-6) + 2.0 ** -22 * want).all())
+    exact = torch.logsumexp(z, 1)
+    share = torch.where(t < 0, 1.0, rest)
+    assert bool(((lse.double() - exact).abs() <= share * (5e-6 * top + 3e-6) + 2.0 ** -22 * (1 + top)).all())
+    assert torch.all(loss[t < 0] == 0)
