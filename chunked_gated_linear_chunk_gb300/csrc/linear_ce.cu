@@ -76,7 +76,8 @@ enum Kind { STATS = 0, GRAD = 1, PRODUCT = 2 };
 constexpr int BM = 256, BK = 64;      // rows of a pair's tile, columns of a k-block
 constexpr uint32_t A_BYTES = 128 * BK * 2;
 constexpr int MAX_STAGES = 12;
-constexpr int SMEM = 231168;          // shared memory of ring and output staging, at most (a KB is left for alignment)
+constexpr int SMEM = 231040;          // shared memory of ring and output staging, at most
+constexpr int SMEM_LEAVE = SMEM + 1024;  // with a KB for alignment; 227 KB less the barriers' own
 // Output staging of a warp: 32 rows of 128 bytes, stored by TMA; with fp32
 // operands 8 rows at a time, stored by the warp, which leaves room for a third
 // stage of the ring (gradients of 1001 x 520 x 10007: 33 us more with two stages).
@@ -971,7 +972,7 @@ int64_t pair_count() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tc::sm_count() / 2 * 2));
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = SMEM + 1024;
+    cfg.dynamicSmemBytes = SMEM_LEAVE;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1118,7 +1119,9 @@ template <int KIND, int PARTS, bool FEW> cudaError_t launch(const Args &a, bool 
   auto *k = ce_product_kernel<KIND, PARTS, FEW>;
   const int ring = a.stages * join_of(KIND, PARTS) * block_bytes_of(PARTS, a.a_bytes, a.bn);
   const int smem = ring + extra_of(KIND, PARTS, a.a_bytes) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The leave is the kernel's on this device, for every host thread: one value for
+  // all calls, so that none takes it from another's launch.
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LEAVE);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(a.units, pair_count())));
