@@ -316,7 +316,8 @@ static cudaError_t fwd_as(const Prob &p, const Docs &docs, void *o, float *ht, f
   dim3 grid((unsigned)docs.n, (unsigned)p.H, (unsigned)((p.V + SV - 1) / SV));
   const size_t smem = fwd_smem(p.K, SC);
   auto k = fwd_kernel<T, SC>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // one leave for all calls: it is the kernel's on this device, for every host thread
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
   k<<<grid, 256, smem, st>>>(p, docs, (T *)o, ht, ws_states);
   mark_launch(o ? "simt_fwd" : "simt_state_pass", st);
@@ -349,7 +350,7 @@ static cudaError_t bwd_as(const Prob &p, const Docs &docs, const void *dO, const
   dim3 grid((unsigned)docs.n, (unsigned)p.H);
   const size_t smem = bwd_smem(p.K, p.V, SC);
   auto k = bwd_kernel<T, SC>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem);
   if (e != cudaSuccess) return e;
   k<<<grid, 256, smem, st>>>(p, docs, (const T *)dO, dht, ws_states, ws_final, (T *)dq, (T *)dk, dq_acc,
                              dk_acc, (T *)dv, dg, dh0);

@@ -2,6 +2,7 @@
 its own: what a launch may take of shared memory is a property of the kernel on
 the device, which the threads share, so no call may leave it at less than
 another's launch needs.  ctypes releases the interpreter's lock during a call."""
+import ctypes
 import threading
 
 import pytest
@@ -70,3 +71,36 @@ def test_layer_norms_of_different_sizes(cuda_ok):
         return lambda: (*glc.layer_norm_fwd(x, w), *glc.layer_norm_bwd(x, w, mean, rstd, x))
 
     run_together([call(1500, D, torch.float32) for D in (511, 64, 2048, 8191)], 200)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_recurrences_of_different_sizes(cuda_ok, dtype):
+    """The kernels of head sizes other than the tensor-core ones.  The C entry
+    itself, in a tight loop: there is little between two launches."""
+    lib, keep, statuses = glc.load(), [], []
+
+    def problem(K, V):
+        r = lambda *s: torch.randn(*s, device="cuda")
+        q, k, v = r(1, 16, 1, K).to(dtype), r(1, 16, 1, K).to(dtype), r(1, 16, 1, V).to(dtype)
+        p, args = glc._problem(q, k, v, -r(1, 16, 1, K).abs() / 16, 1.0, None, None, 16, None, False)
+        ws = glc._workspace(p, "gla_fwd", q.device, None)
+        o, stream = torch.empty_like(v), torch.cuda.Stream()
+        keep.append((args, ws, o, stream))
+        torch.cuda.synchronize()
+        return ctypes.byref(p), glc._ptr(o), ctypes.c_void_p(stream.cuda_stream)
+
+    problems = [problem(K, V) for K, V in ((16, 16), (112, 40), (48, 24), (120, 80))]
+    start = threading.Barrier(len(problems))
+
+    def work(p, o, stream):
+        start.wait()
+        statuses.append({lib.gla_fwd(p, o, None, stream) for _ in range(5000)})
+
+    threads = [threading.Thread(target=work, args=a) for a in problems]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert statuses == [{glc.OK}] * len(problems)
+    glc.get_device_error()
