@@ -222,6 +222,23 @@ def _contig(t, dtype=None):
     return t if t.is_contiguous() else t.contiguous()
 
 
+def _same_device(device, **tensors):
+    """Refuses a tensor (None: not given) that is not on `device`, the call's."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+
+
+def _given(t, name, shape, dtype, device):
+    """A caller's own output tensor, as the kernels write it: of this shape and
+    type, contiguous, on the call's device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}")
+    return t
+
+
 def _new(shape, dtype, device, poison):
     if poison:
         return torch.full(shape, float("nan"), dtype=dtype, device=device)
@@ -449,6 +466,10 @@ def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
         raise ValueError("gla_step's gate must be [B,T,H,K]" if kind == "gla" else "ssd_step's gate must be [B,T,H]")
     (q, qs), (k, ks), (v, vs) = _tokens(q), _tokens(k), _tokens(v)
     g = _contig(g, torch.float32)
+    dev = q.get_device()
+    if not (k.get_device() == v.get_device() == g.get_device() == state.get_device() == dev) or (
+            state_indices is not None and state_indices.get_device() != dev):
+        _same_device(q.device, k=k, v=v, g=g, state=state, state_indices=state_indices)
     if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
     if state.dim() != 4 or tuple(state.shape[1:]) != (H, K, V):
@@ -456,7 +477,7 @@ def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
     idx = _contig(state_indices, torch.int32)
     if idx is not None and (idx.dim() != 1 or idx.shape[0] != B):
         raise ValueError("state_indices must be [B]")
-    o = out if out is not None else _new((B, T, H, V), dt, q.device, poison)
+    o = _given(out, "out", (B, T, H, V), dt, q.device) if out is not None else _new((B, T, H, V), dt, q.device, poison)
     if scale is None:
         scale = K ** -0.5
     p = _PACK.pack(B, T, H, Hqk, K, V, _dtype_code(q), 0, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -508,7 +529,10 @@ def layer_norm_fwd(x, w=None, b=None, eps=1e-5, out=None):
     if (w is not None and w.shape != (D,)) or (b is not None and b.shape != (D,)):
         raise ValueError("layer_norm: w and b must be [D]")
     shape, dev = x.shape, x.device
-    y = out if out is not None else torch.empty(shape, dtype=x.dtype, device=dev)
+    at = x.get_device()
+    if (w is not None and w.get_device() != at) or (b is not None and b.get_device() != at):
+        _same_device(dev, w=w, b=b)
+    y = _given(out, "out", shape, x.dtype, dev) if out is not None else torch.empty(shape, dtype=x.dtype, device=dev)
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
     st = (_lib or load()).layer_norm_fwd(x.data_ptr(), _addr(w), _addr(b), rows, D, xs, _dtype_code(x), eps,
@@ -529,8 +553,12 @@ def layer_norm_bwd(x, w, mean, rstd, dy, outs=None, workspace=None):
     if (w is not None and w.shape != (D,)) or mean.numel() != rows or rstd.numel() != rows:
         raise ValueError("layer_norm: w must be [D], mean and rstd one value per row")
     dev = x.device
+    _same_device(dev, w=w, mean=mean, rstd=rstd, dy=dy)
     if outs is not None:
         dx, dw, db = outs
+        _given(dx, "dx", x.shape, x.dtype, dev)
+        _given(dw, "dw", (D,), torch.float32, dev)
+        _given(db, "db", (D,), torch.float32, dev)
     else:
         dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
         dw = torch.empty(D, dtype=torch.float32, device=dev)
@@ -603,6 +631,7 @@ def _ce_args(x, w, target):
 
 
 def _scratch(need, device, workspace):
+    _same_device(device, workspace=workspace)
     if workspace is not None and workspace.numel() >= need and workspace.data_ptr() % 256 == 0:
         return workspace
     return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
@@ -616,7 +645,7 @@ def linear_ce_fwd(x, w, target, outs=None, workspace=None):
     x, w, target, N, D, V, xs = _ce_args(x, w, target)
     code = _dtype_code(x)
     if outs is not None:
-        loss, lse = outs
+        loss, lse = (_given(o, n, (N,), torch.float32, x.device) for o, n in zip(outs, ("loss", "lse")))
     else:
         loss = torch.empty(N, dtype=torch.float32, device=x.device)
         lse = torch.empty(N, dtype=torch.float32, device=x.device)
@@ -637,9 +666,12 @@ def linear_ce_bwd(x, w, target, lse, dloss, outs=None, workspace=None):
     lse, dloss = _contig(lse, torch.float32), _contig(dloss, torch.float32)
     if tuple(lse.shape) != (N,) or tuple(dloss.shape) != (N,):
         raise ValueError("linear_ce: lse and dloss must be [N]")
+    _same_device(x.device, lse=lse, dloss=dloss)
     code = _dtype_code(x)
     if outs is not None:
         dx, dw = outs
+        _given(dx, "dx", (N, D), x.dtype, x.device)
+        _given(dw, "dw", (V, D), x.dtype, x.device)
     else:
         dx = torch.empty((N, D), dtype=x.dtype, device=x.device)
         dw = torch.empty((V, D), dtype=x.dtype, device=x.device)
