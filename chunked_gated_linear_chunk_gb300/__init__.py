@@ -331,6 +331,7 @@ def _problem(q, k, v, g, scale, segment_ids, initial_state, chunk_size, n_seqs, 
     h0 = _contig(initial_state, torch.float32) if initial_state is not None else None
     if h0 is not None and tuple(h0.shape) != (n, H, K, V):
         raise ValueError(f"initial_state must be [{n},{H},{K},{V}]")
+    _same_device(q.device, k=k, v=v, g=g, segment_ids=seg, initial_state=h0)
     if scale is None:
         scale = K ** -0.5 if not head_gate else 1.0
     p = Problem(B=B, T=T, H=H, Hqk=Hqk, K=K, V=V, dtype=_dtype_code(q), chunk_size=int(chunk_size),
@@ -350,6 +351,7 @@ def _workspace(p, kind, device, workspace):
     need = workspace_size(p, kind)
     if need == 0:
         return None
+    _same_device(device, workspace=workspace)
     if workspace is not None and workspace.numel() >= need and workspace.data_ptr() % 256 == 0:
         ws = workspace
     else:
@@ -366,10 +368,12 @@ def _fwd(kind, q, k, v, g, scale=None, segment_ids=None, initial_state=None,
     p, keep = _problem(q, k, v, g, scale, segment_ids, initial_state, chunk_size, n_seqs, head_gate)
     dev = keep[0].device
     o = out if out is not None else _new(tuple(keep[2].shape), keep[0].dtype, dev, poison)
+    _given(o, "out", keep[2].shape, keep[0].dtype, dev)
     ht = None
     if output_final_state:
         ht = final_out if final_out is not None else _new((p.n_seqs, p.H, p.K, p.V), torch.float32, dev,
                                                           poison)
+        _given(ht, "final_out", (p.n_seqs, p.H, p.K, p.V), torch.float32, dev)
     ws = _workspace(p, kind + "_fwd", dev, workspace)
     st = getattr(load(), kind + "_fwd")(ctypes.byref(p), _ptr(o), _ptr(ht), _stream(dev))
     _check(st, kind + "_fwd")
@@ -388,8 +392,13 @@ def _bwd(kind, q, k, v, g, do, scale=None, segment_ids=None, initial_state=None,
         raise ValueError("do must match v")
     if dht is not None and tuple(dht.shape) != (p.n_seqs, p.H, p.K, p.V):
         raise ValueError("dht must be [n_seqs,H,K,V]")
+    _same_device(dev, do=do, dht=dht)
     if outs is not None:
         dq, dk, dv, dg, dh0 = outs
+        for t, name, like in ((dq, "dq", keep[0]), (dk, "dk", keep[1]), (dv, "dv", keep[2]), (dg, "dg", keep[3])):
+            _given(t, name, like.shape, like.dtype, dev)
+        if dh0 is not None:
+            _given(dh0, "dh0", (p.n_seqs, p.H, p.K, p.V), torch.float32, dev)
     else:
         dq = _new(tuple(keep[0].shape), keep[0].dtype, dev, poison)
         dk = _new(tuple(keep[1].shape), keep[0].dtype, dev, poison)
@@ -583,7 +592,8 @@ def norm_gate_fwd(o, z, w, eps=1e-5, out=None):
         raise ValueError("norm_gate: o and z must match and w must be [V]")
     V = o.shape[-1]
     rows = o.numel() // V if V else 0
-    y = out if out is not None else torch.empty_like(o)
+    _same_device(o.device, z=z, w=w)
+    y = _given(out, "out", o.shape, o.dtype, o.device) if out is not None else torch.empty_like(o)
     st = load().norm_gate_fwd(_ptr(o), _ptr(z), _ptr(w), rows, V, _dtype_code(o), float(eps), _ptr(y),
                               _stream(o.device))
     _check(st, "norm_gate_fwd")
@@ -596,10 +606,14 @@ def norm_gate_bwd(o, z, w, dy, eps=1e-5, outs=None, workspace=None):
     w = _contig(w, torch.float32)
     if not (o.shape == z.shape == dy.shape) or not (o.dtype == z.dtype == dy.dtype):
         raise ValueError("norm_gate: o, z and dy must match")
+    _same_device(o.device, z=z, w=w, dy=dy, workspace=workspace)
     V = o.shape[-1]
     rows = o.numel() // V if V else 0
     if outs is not None:
         do, dz, dw = outs
+        _given(do, "do", o.shape, o.dtype, o.device)
+        _given(dz, "dz", o.shape, o.dtype, o.device)
+        _given(dw, "dw", (V,), torch.float32, o.device)
     else:
         do, dz = torch.empty_like(o), torch.empty_like(z)
         dw = torch.empty(V, dtype=torch.float32, device=o.device)
@@ -696,7 +710,8 @@ def short_conv_fwd(x, w, b=None, segment_ids=None, activation=True, out=None):
     Kc = w.shape[0]
     if tuple(w.shape) != (Kc, D) or (b is not None and tuple(b.shape) != (D,)):
         raise ValueError("short_conv: w must be [Kc, D] and b [D]")
-    y = out if out is not None else torch.empty_like(x)
+    _same_device(x.device, w=w, b=b, segment_ids=seg)
+    y = _given(out, "out", x.shape, x.dtype, x.device) if out is not None else torch.empty_like(x)
     st = load().short_conv_fwd(_ptr(x), _ptr(w), _ptr(b), _ptr(seg), B, T, D, Kc, _dtype_code(x),
                                1 if activation else 0, _ptr(y), _stream(x.device))
     _check(st, "short_conv_fwd")
@@ -711,8 +726,12 @@ def short_conv_bwd(x, w, b, dy, segment_ids=None, activation=True, outs=None, wo
     seg = _contig(segment_ids, torch.int32) if segment_ids is not None else None
     B, T, D = x.shape
     Kc = w.shape[0]
+    _same_device(x.device, w=w, b=b, dy=dy, segment_ids=seg, workspace=workspace)
     if outs is not None:
         dx, dw, db = outs
+        _given(dx, "dx", x.shape, x.dtype, x.device)
+        _given(dw, "dw", (Kc, D), torch.float32, x.device)
+        _given(db, "db", (D,), torch.float32, x.device)
     else:
         dx = torch.empty_like(x)
         dw = torch.empty(Kc, D, dtype=torch.float32, device=x.device)

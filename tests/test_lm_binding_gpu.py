@@ -1,5 +1,4 @@
-"""What the binding of the layer norm, the steps and the linear cross entropy
-refuses before it hands an address to the library: operands on another device
+"""What the binding refuses before it hands an address to the library: operands on another device
 than the call's, and output tensors that the kernels would not fill as they are."""
 import pytest
 import torch
@@ -41,10 +40,18 @@ def calls():
         "ssd_step": (dict(step, g=g[..., 0].contiguous()), "out", [z(2, 1, 4, 8)]),
         "linear_ce_fwd": (dict(x=h, w=head, target=t), "outs", [z(5), z(5)]),
         "linear_ce_bwd": (dict(x=h, w=head, target=t, lse=z(5), dloss=z(5)), "outs", [z(5, 16), z(9, 16)]),
+        "gla_fwd": (dict(q=q, k=q, v=v, g=g), "out", [z(2, 1, 4, 8)]),
+        "gla_bwd": (dict(q=q, k=q, v=v, g=g, do=v), "outs", [z(2, 1, 2, 8), z(2, 1, 2, 8), z(2, 1, 4, 8), z(2, 1, 4, 8)]),
+        "norm_gate_fwd": (dict(o=x, z=x, w=w), "out", [z(6, 16)]),
+        "norm_gate_bwd": (dict(o=x, z=x, w=w, dy=x), "outs", [z(6, 16), z(6, 16), z(16)]),
+        "short_conv_fwd": (dict(x=z(2, 3, 16), w=z(4, 16), b=b), "out", [z(2, 3, 16)]),
+        "short_conv_bwd": (dict(x=z(2, 3, 16), w=z(4, 16), b=b, dy=z(2, 3, 16)), "outs",
+                           [z(2, 3, 16), z(4, 16), z(16)]),
     }
 
 
-NAMES = ["layer_norm_fwd", "layer_norm_bwd", "gla_step", "ssd_step", "linear_ce_fwd", "linear_ce_bwd"]
+NAMES = ["layer_norm_fwd", "layer_norm_bwd", "gla_step", "ssd_step", "linear_ce_fwd", "linear_ce_bwd", "gla_fwd",
+         "gla_bwd", "norm_gate_fwd", "norm_gate_bwd", "short_conv_fwd", "short_conv_bwd"]
 
 
 @pytest.mark.parametrize("name", NAMES)
@@ -63,7 +70,8 @@ def test_operands_on_another_device(cuda_ok, name):
 def test_outputs_that_do_not_fit(cuda_ok, name):
     args, key, outs = calls()[name]
     call = getattr(glc, name)
-    given = lambda o: {key: o[0] if key == "out" else tuple(o)}
+    more = (None,) if name == "gla_bwd" else ()  # no dh0
+    given = lambda o: {key: o[0] if key == "out" else tuple(o) + more}
     got = call(**args, **given(outs))
     got = got[:len(outs)] if isinstance(got, tuple) else (got,)
     assert all(a is b for a, b in zip(got, outs))
@@ -74,7 +82,8 @@ def test_outputs_that_do_not_fit(cuda_ok, name):
                 call(**args, **given(outs[:i] + [bad] + outs[i + 1:]))
 
 
-@pytest.mark.parametrize("name", ["layer_norm_bwd", "linear_ce_fwd", "linear_ce_bwd"])
+@pytest.mark.parametrize("name", ["layer_norm_bwd", "linear_ce_fwd", "linear_ce_bwd", "gla_bwd", "norm_gate_bwd",
+                                  "short_conv_bwd"])
 def test_workspace_on_another_device(cuda_ok, name):
     args, _, _ = calls()[name]
     ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
