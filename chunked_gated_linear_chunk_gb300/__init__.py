@@ -258,7 +258,7 @@ class LaunchTimer:
     """Per-kernel CUDA-event timing through the library's measurement hook.
 
     ``with LaunchTimer(n) as t: gla_fwd(...)`` records one event after each
-    kernel launch of the call; ``t.labels`` names the kernels and
+    kernel launch of the call (of several: the last one's); ``t.labels`` names the kernels and
     ``t.events`` holds the torch events (elapsed times are read after a
     synchronize)."""
 

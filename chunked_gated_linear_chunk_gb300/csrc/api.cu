@@ -31,6 +31,8 @@ glacore_status status_of(cudaError_t e) {
   return GLACORE_ERR_CUDA;
 }
 
+void begin_marks() { t_used = 0; }
+
 void mark_launch(const char *label, cudaStream_t st) {
   if (t_events && t_used < t_nev) {
     cudaEventRecord(t_events[t_used], st);
@@ -514,33 +516,33 @@ size_t ssd_bwd_workspace_size(const glacore_problem *p) { return ws_size(p, true
 
 glacore_status gla_fwd(const glacore_problem *p, void *o, float *final_state,
                        glacore_stream_t stream) {
-  t_used = 0;
+  begin_marks();
   return run_fwd(p, false, o, final_state, (cudaStream_t)stream);
 }
 glacore_status ssd_fwd(const glacore_problem *p, void *o, float *final_state,
                        glacore_stream_t stream) {
-  t_used = 0;
+  begin_marks();
   return run_fwd(p, true, o, final_state, (cudaStream_t)stream);
 }
 glacore_status gla_bwd(const glacore_problem *p, const void *do_, const float *dht, void *dq,
                        void *dk, void *dv, float *dg, float *dh0, glacore_stream_t stream) {
-  t_used = 0;
+  begin_marks();
   return run_bwd(p, false, do_, dht, dq, dk, dv, dg, dh0, (cudaStream_t)stream);
 }
 glacore_status ssd_bwd(const glacore_problem *p, const void *do_, const float *dht, void *dq,
                        void *dk, void *dv, float *dg, float *dh0, glacore_stream_t stream) {
-  t_used = 0;
+  begin_marks();
   return run_bwd(p, true, do_, dht, dq, dk, dv, dg, dh0, (cudaStream_t)stream);
 }
 
 glacore_status gla_step(const glacore_problem *p, float *state, int64_t n_slots, const int32_t *state_indices,
                         void *o, glacore_stream_t stream) {
-  t_used = 0;
+  begin_marks();
   return run_step(p, false, state, n_slots, state_indices, o, (cudaStream_t)stream);
 }
 glacore_status ssd_step(const glacore_problem *p, float *state, int64_t n_slots, const int32_t *state_indices,
                         void *o, glacore_stream_t stream) {
-  t_used = 0;
+  begin_marks();
   return run_step(p, true, state, n_slots, state_indices, o, (cudaStream_t)stream);
 }
 
@@ -576,7 +578,7 @@ glacore_status gla_fwd_state(const glacore_problem *p, float *L, float *D, glaco
   if (!(aligned16(p->q) && aligned16(p->k) && aligned16(p->v) && aligned16(p->g) && aligned16(L) && aligned16(D)))
     return GLACORE_ERR_INVALID_ARG;
   if (p->B * p->T == 0) return GLACORE_OK;
-  t_used = 0;
+  begin_marks();
   Layout Lo;
   memset(&Lo, 0, sizeof(Lo));
   Lo.chunk = tc::C;
@@ -594,7 +596,7 @@ glacore_status gla_bwd_state(const glacore_problem *p, const void *do_, float *L
         aligned16(D) && aligned16(do_)))
     return GLACORE_ERR_INVALID_ARG;
   if (p->B * p->T == 0) return GLACORE_OK;
-  t_used = 0;
+  begin_marks();
   Layout Lo;
   memset(&Lo, 0, sizeof(Lo));
   Lo.chunk = tc::C;
@@ -605,6 +607,7 @@ glacore_status gla_bwd_state(const glacore_problem *p, const void *do_, float *L
 glacore_status glacore_state_scan(const float *L, const float *D, int64_t R, int64_t mats, int64_t K, int64_t V,
                                   const float *seed, int64_t r, int32_t reverse, float *out,
                                   glacore_stream_t stream) {
+  begin_marks();
   if (R < 1 || mats < 0 || K < 1 || V < 1 || r < 0 || r >= R || (reverse != 0 && reverse != 1))
     return GLACORE_ERR_INVALID_ARG;
   if (mats == 0) return GLACORE_OK;

@@ -513,6 +513,7 @@ size_t norm_gate_bwd_workspace_size(int64_t rows, int64_t V) {
 
 glacore_status norm_gate_fwd(const void *o, const void *z, const float *w, int64_t rows, int64_t V, int32_t dtype,
                              float eps, void *y, glacore_stream_t stream) {
+  begin_marks();
   const int lg = log2_lanes(V);
   if (rows < 0 || lg < 0 || (dtype != GLACORE_BF16 && dtype != GLACORE_F32) || !(eps >= 0.f))
     return GLACORE_ERR_INVALID_ARG;
@@ -533,6 +534,7 @@ glacore_status norm_gate_fwd(const void *o, const void *z, const float *w, int64
 glacore_status norm_gate_bwd(const void *o, const void *z, const float *w, const void *dy, int64_t rows, int64_t V,
                              int32_t dtype, float eps, void *do_, void *dz, float *dw, void *workspace,
                              size_t workspace_bytes, glacore_stream_t stream) {
+  begin_marks();
   const int lg = log2_lanes(V);
   if (rows < 0 || lg < 0 || (dtype != GLACORE_BF16 && dtype != GLACORE_F32) || !(eps >= 0.f) || !dw)
     return GLACORE_ERR_INVALID_ARG;
@@ -569,6 +571,7 @@ size_t short_conv_bwd_workspace_size(int64_t B, int64_t T, int64_t D, int32_t Kc
 glacore_status short_conv_fwd(const void *x, const float *w, const float *b, const int32_t *segment_ids, int64_t B,
                               int64_t T, int64_t D, int32_t Kc, int32_t dtype, int32_t activation, void *y,
                               glacore_stream_t stream) {
+  begin_marks();
   if (B < 1 || T < 0 || D < 8 || (D & 7) || Kc < 1 || Kc > 4 || (activation != 0 && activation != 1) ||
       (dtype != GLACORE_BF16 && dtype != GLACORE_F32) || B > 65535)
     return GLACORE_ERR_INVALID_ARG;
@@ -605,6 +608,7 @@ glacore_status short_conv_bwd(const void *x, const float *w, const float *b, con
                               const void *dy, int64_t B, int64_t T, int64_t D, int32_t Kc, int32_t dtype,
                               int32_t activation, void *dx, float *dw, float *db, void *workspace,
                               size_t workspace_bytes, glacore_stream_t stream) {
+  begin_marks();
   if (B < 1 || T < 0 || D < 8 || (D & 7) || Kc < 1 || Kc > 4 || (activation != 0 && activation != 1) ||
       (dtype != GLACORE_BF16 && dtype != GLACORE_F32) || B > 65535 || !dw || !db)
     return GLACORE_ERR_INVALID_ARG;

@@ -189,6 +189,8 @@ inline cudaError_t launch_follow(void (*kernel)(Params...), dim3 grid, dim3 bloc
 __device__ __forceinline__ void follow_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void follow_allow() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// An entry call begins: its launches record from the first timing event on.
+void begin_marks();
 // Records the next caller-provided timing event (if any) after a launch.
 void mark_launch(const char *label, cudaStream_t st);
 // Maps a CUDA result to a status, remembering the CUDA error of this host

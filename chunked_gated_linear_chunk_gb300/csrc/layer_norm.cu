@@ -785,6 +785,7 @@ extern "C" {
 glacore_status layer_norm_fwd(const void *x, const float *w, const float *b, int64_t rows, int64_t D,
                               int64_t x_stride, int32_t dtype, float eps, void *y, float *mean, float *rstd,
                               glacore_stream_t stream) {
+  begin_marks();
   if (!sizes_ok(rows, D, x_stride, dtype) || !(eps >= 0.f)) return GLACORE_ERR_INVALID_ARG;
   if (rows == 0) return GLACORE_OK;
   if (!x || !y || !mean != !rstd) return GLACORE_ERR_INVALID_ARG;
@@ -826,6 +827,7 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean, 
                               int64_t rows, int64_t D, int64_t x_stride, int64_t dy_stride, int32_t dtype, void *dx,
                               float *dw, float *db, void *workspace, size_t workspace_bytes,
                               glacore_stream_t stream) {
+  begin_marks();
   if (!sizes_ok(rows, D, x_stride, dtype) || (dy_stride != 0 && dy_stride < D) || !dw || !db ||
       !natural(dtype, (uintptr_t)x | (uintptr_t)dy | (uintptr_t)dx,
                (uintptr_t)w | (uintptr_t)mean | (uintptr_t)rstd | (uintptr_t)dw | (uintptr_t)db))

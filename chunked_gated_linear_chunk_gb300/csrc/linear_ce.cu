@@ -1228,6 +1228,7 @@ size_t linear_ce_bwd_workspace_size(int64_t N, int64_t D, int64_t V, int32_t dty
 glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target, int64_t N, int64_t D, int64_t V,
                              int64_t x_stride, int32_t dtype, float *loss, float *lse, void *workspace,
                              size_t workspace_bytes, glacore_stream_t stream) {
+  begin_marks();
   const glacore_status s = check(x, w, N, D, V, x_stride, dtype);
   if (s || N == 0) return s;
   if (!target || !loss || !lse || ((uintptr_t)target & 7) || (((uintptr_t)loss | (uintptr_t)lse) & 3))
@@ -1282,6 +1283,7 @@ glacore_status linear_ce_fwd(const void *x, const void *w, const int64_t *target
 glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target, const float *lse,
                              const float *dloss, int64_t N, int64_t D, int64_t V, int64_t x_stride, int32_t dtype,
                              void *dx, void *dw, void *workspace, size_t workspace_bytes, glacore_stream_t stream) {
+  begin_marks();
   const glacore_status s = check(x, w, N, D, V, x_stride, dtype);
   if (s) return s;
   const size_t es = dtype == GLACORE_F32 ? 4 : 2;

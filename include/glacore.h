@@ -420,7 +420,7 @@ const char *glacore_status_string(glacore_status s);
 int glacore_version(void);
 
 /* Measurement hook.  After this call, every kernel launch made by the next
- * gla_ / ssd_ entry call on this host thread is followed by a record of the
+ * entry call on this host thread is followed by a record of the
  * next event of `events` (cudaEvent_t[n_events], created by the caller) on
  * the call's stream, so the caller can time each kernel with
  * cudaEventElapsedTime.  Each entry call restarts at events[0].  Pass NULL
