@@ -14,6 +14,8 @@ pytestmark = pytest.mark.gpu
     (3000, 2048, 12000, torch.bfloat16), (2100, 1000, 9000, torch.float32),
     (63, 256, 700, torch.bfloat16), (64, 256, 700, torch.bfloat16), (65, 256, 700, torch.bfloat16),
     (64, 31, 20000, torch.bfloat16), (64, 31, 2000, torch.float32), (65, 31, 2000, torch.float32),
+    # few tokens of a vocabulary in two pieces, the last one ragged
+    (64, 16, 2200001, torch.bfloat16), (64, 16, 1500001, torch.float32),
     (17, 4100, 257, torch.bfloat16), (33, 8, 1, torch.bfloat16), (33, 8, 1, torch.float32),
 ])
 def test_against_definition(cuda_ok, N, D, V, dtype):
