@@ -486,7 +486,8 @@ def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
     idx = _contig(state_indices, torch.int32)
     if idx is not None and (idx.dim() != 1 or idx.shape[0] != B):
         raise ValueError("state_indices must be [B]")
-    o = _given(out, "out", (B, T, H, V), dt, q.device) if out is not None else _new((B, T, H, V), dt, q.device, poison)
+    shape = (B, T, H, V)
+    o = _given(out, "out", shape, dt, q.device) if out is not None else _new(shape, dt, q.device, poison)
     if scale is None:
         scale = K ** -0.5
     p = _PACK.pack(B, T, H, Hqk, K, V, _dtype_code(q), 0, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),

@@ -12,8 +12,8 @@
 // CTA loads half of either operand, so every byte brought to an SM feeds
 // twice the products a single CTA's tile would) with three epilogues:
 //   STATS    a tile of logits becomes, per row, its maximum and its sum of
-//            exponentials (one pass, the running sum rescaled every 64
-//            columns) and the target's logit; the tiles' pairs are merged by
+//            exponentials, the target left out (one pass, the running sum
+//            rescaled every 64 columns), and the target's logit; the tiles' pairs are merged by
 //            ce_merge_kernel.  The logits leave TMEM and are gone.
 //   GRAD     a tile of logits becomes a tile of G in bf16 (its products with w
 //            and x are bf16 tensor-core products), for one piece of the
@@ -109,7 +109,7 @@ struct Args {
   int32_t bn, stages, a_bytes;  // a_bytes: a CTA's rows of A in a k-block, as far as they are there
   int64_t N, V, v0;  // tokens, vocabulary, first column of the piece
   const int64_t *target;
-  float2 *part;      // STATS: [2 * nt][N] (maximum, sum of exponentials of the differences from it), the target left out
+  float2 *part;      // STATS: [2 * nt][N] (maximum, sum of e^(z - maximum)), the target left out
   float *zt;         // STATS: [N] the target's logit
   const float *lse, *dloss;  // GRAD
   const float *unit;         // G is in units of *unit (null: 1)
@@ -720,7 +720,10 @@ template <typename T> struct Targets {
     int64_t c = first;
     for (; c + 15 * threads < D; c += 16 * threads)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i & 3] = fma((A)to_f32(xr[c + i * threads]), (A)to_f32(wr[c + i * threads]), f[i & 3]);
+      for (int i = 0; i < 16; ++i) {
+        const int64_t at = c + i * threads;
+        f[i & 3] = fma((A)to_f32(xr[at]), (A)to_f32(wr[at]), f[i & 3]);
+      }
     for (; c < D; c += threads) f[0] = fma((A)to_f32(xr[c]), (A)to_f32(wr[c]), f[0]);
     double s = ((double)f[0] + (double)f[1]) + ((double)f[2] + (double)f[3]);
     for (int m = 16; m; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
@@ -1048,8 +1051,9 @@ Layout layout(int64_t N, int64_t D, int64_t V, int32_t dtype, bool backward) {
     // The width that deals the vocabulary out most evenly: the fewest columns
     // for the busiest pair, and about 32 columns' time for a tile's start and
     // end.  It matters for few tokens, where the call is bound by reading w
-    // once (16 x 2048 x 32000: 36.4 us with 256, 34.8 us with 224, 33.6 us with
-    // the ring's stages no taller than the tokens).
+    // once (16 x 2048 x 32000: 36.4 us with 256, 34.8 us with 224, 33.1 us with
+    // the ring's stages no taller than the tokens, and 34.9 us now that its sums
+    // are handed over every four k-blocks).
     int64_t least = -1;
     for (int bn = 256; bn >= 128; bn -= backward ? 128 : 32) {  // G leaves 64 columns of a warp at a time
       const int64_t cost = up(up(N, BM) * up(V, bn), pair_count()) * (bn + 32);
@@ -1311,9 +1315,10 @@ glacore_status linear_ce_bwd(const void *x, const void *w, const int64_t *target
     typedef std::remove_const_t<std::remove_pointer_t<decltype(typed)>> T;
     const Targets<T> targets = {typed, (const T *)w, xs, D};
     if (L.pack)
-      return launch_follow(ce_prepare_kernel<T>, grid, dim3(256), st, targets, lse, at, rows, N, D, r.xp, L.xt_pitch, to, dloss,
-                           target, V, unit);
-    ce_prepare_kernel<T><<<grid, 256, 0, st>>>(targets, lse, at, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V, unit);
+      return launch_follow(ce_prepare_kernel<T>, grid, dim3(256), st, targets, lse, at, rows, N, D, r.xp, L.xt_pitch, to,
+                           dloss, target, V, unit);
+    ce_prepare_kernel<T><<<grid, 256, 0, st>>>(targets, lse, at, rows, N, D, r.xp, L.xt_pitch, to, dloss, target, V,
+                                               unit);
     return cudaGetLastError();
   };
   e = dtype == GLACORE_F32 ? prepare((const float *)x) : prepare((const __nv_bfloat16 *)x);

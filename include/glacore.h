@@ -324,7 +324,8 @@ glacore_status short_conv_bwd(const void *x, const float *w, const float *b,
  *   mean, rstd  [rows] fp32: m and r, written; both NULL if not wanted
  *   D           1 .. 2^31 - 1, any; rows of up to 8192 values with D, the
  *               strides and the addresses multiples of 16 bytes are the fast
- *               case.  eps >= 0
+ *               case (longer rows and odd ones take 1.5 to 3 times as long
+ *               for each value).  eps >= 0
  * Backward (from mean and rstd of the forward), with n = (x - m) r and
  * a = dy w:
  *     dx = r (a - mean(a) - n mean(a n)),  dw = sum dy n,  db = sum dy
@@ -361,13 +362,16 @@ glacore_status layer_norm_bwd(const void *x, const float *w, const float *mean,
  * Any N >= 0 and V up to 2^30, D up to 2^22 - 64.  x, w, dx and dw 16-byte aligned; for bf16
  * with D a multiple of 8, x_stride as well.  bf16 products run on the tensor
  * cores with fp32 sums, G rounded to bf16 for them (up to 64 tokens: to two bf16
- * parts; their targets' logits are summed apart, rounded to nearest); fp32 operands are split exactly into three bf16 parts (results to fp32's accuracy).  x and w must be
- * finite (an infinity in a row that is not scored still reaches dw as NaN).
+ * parts; their targets' logits are summed apart, rounded to nearest); fp32
+ * operands are split exactly into three bf16 parts (results to fp32's
+ * accuracy).  A loss is never negative.  x and w must be finite (an infinity in
+ * a row that is not scored still reaches dw as NaN).
  * The workspace (the *_workspace_size bytes, 256-byte aligned) holds, forward,
- * 16 bytes per token and tile of the vocabulary (at most 256 columns; a 64th of
- * fp32 logits); backward, G for one piece of the vocabulary (512 MB, or 2048
- * columns where those are more), x transposed, and fp32 sums of a gradient
- * that is cut (512 MB each at most, or dx once).  Operands that TMA cannot
+ * 16 bytes per token and tile of the vocabulary (128 to 256 columns, fp32
+ * operands 128: a 64th to a 32nd of fp32 logits); backward, G for one piece of
+ * the vocabulary (512 MB, or 2048 columns where those are more), x transposed,
+ * and fp32 sums of a gradient that is cut (512 MB each at most, or dx once, of
+ * up to 64 tokens twice).  Operands that TMA cannot
  * address (bf16 with D no multiple of 8) and fp32 operands are copied there.
  * Results do not depend on the order in which CTAs run. */
 size_t linear_ce_fwd_workspace_size(int64_t N, int64_t D, int64_t V,
