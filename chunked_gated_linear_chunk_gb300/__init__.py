@@ -23,6 +23,7 @@ Layouts: q, k [B,T,Hqk,K]; v, o, do [B,T,H,V]; g [B,T,H,K] (GLA) or
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 import threading
@@ -230,12 +231,12 @@ def _same_device(device, **tensors):
 
 
 def _given(t, name, shape, dtype, device):
-    """A caller's own output tensor, as the kernels write it: of this shape and
-    type, contiguous, on the call's device."""
+    """A caller's own output tensor, as the kernels write it: of this type and
+    as many values (whatever axes it has), contiguous, on the call's device."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor on {device}")
+    if t.device != device or t.numel() != math.prod(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of the values of {list(shape)} on {device}")
     return t
 
 
