@@ -11,7 +11,9 @@ Entry points (same names as the C ABI):
     gla_fwd(q, k, v, g, ...)            -> (o, final_state)
     gla_bwd(q, k, v, g, do, ...)        -> (dq, dk, dv, dg, dh0)
     ssd_fwd / ssd_bwd                   (scalar per-head gate, g [B,T,H])
-    gla_step / ssd_step                 -> o (new tokens on a pool of states)
+    delta_fwd / delta_bwd               (gated delta rule, g and beta [B,T,H])
+    gla_step / ssd_step / delta_step    -> o (new tokens on a pool of states)
+    qk_norm_fwd / qk_norm_bwd           -> (q, k) / (dq, dk, dwq, dwk)
     layer_norm_fwd / layer_norm_bwd     -> (y, mean, rstd) / (dx, dw, db)
     linear_ce_fwd / linear_ce_bwd       -> (loss, lse) / (dx, dw)
     count_docs(segment_ids)             -> int
@@ -35,6 +37,7 @@ __all__ = [
     "get_device_error", "workspace_size", "Problem", "selftest_wait", "norm_gate_fwd", "norm_gate_bwd",
     "short_conv_fwd", "short_conv_bwd", "gla_fwd_state", "gla_bwd_state", "state_scan",
     "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd", "linear_ce_fwd", "linear_ce_bwd",
+    "delta_fwd", "delta_bwd", "delta_step", "qk_norm_fwd", "qk_norm_bwd",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -53,6 +56,8 @@ EXPORTS = (
     "gla_fwd_state", "gla_bwd_state", "glacore_state_scan", "glacore_last_cuda_error",
     "gla_step", "ssd_step", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_bwd_workspace_size",
     "linear_ce_fwd", "linear_ce_bwd", "linear_ce_fwd_workspace_size", "linear_ce_bwd_workspace_size",
+    "delta_fwd", "delta_bwd", "delta_step", "delta_fwd_workspace_size", "delta_bwd_workspace_size",
+    "qk_norm_fwd", "qk_norm_bwd", "qk_norm_bwd_workspace_size",
 )
 
 
@@ -81,6 +86,21 @@ class Problem(ctypes.Structure):
         ("initial_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t),
         ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+    ]
+
+
+class QkNorm(ctypes.Structure):
+    """Mirror of ``glacore_qk_norm`` in include/glacore.h."""
+
+    _fields_ = [
+        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+        ("D", ctypes.c_int64), ("R", ctypes.c_int64),
+        ("dtype", ctypes.c_int32), ("l2", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("reserved0", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("wq", ctypes.c_void_p), ("wk", ctypes.c_void_p),
+        ("cos_table", ctypes.c_void_p), ("sin_table", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("n_positions", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -169,6 +189,14 @@ def load(path: str | None = None):
             getattr(lib, n).restype = ctypes.c_int
         lib.linear_ce_fwd.argtypes = [P, P, P, I64, I64, I64, I64, I32, P, P, P, ctypes.c_size_t, P]
         lib.linear_ce_bwd.argtypes = [P, P, P, P, P, I64, I64, I64, I64, I32, P, P, P, ctypes.c_size_t, P]
+        for n in ("delta_fwd_workspace_size", "delta_bwd_workspace_size", "qk_norm_bwd_workspace_size"):
+            getattr(lib, n).restype = ctypes.c_size_t
+            getattr(lib, n).argtypes = [P]
+        for n, args in (("delta_fwd", 5), ("delta_bwd", 11), ("qk_norm_fwd", 4), ("qk_norm_bwd", 8)):
+            getattr(lib, n).restype = ctypes.c_int
+            getattr(lib, n).argtypes = [P] * args
+        lib.delta_step.restype = ctypes.c_int
+        lib.delta_step.argtypes = [P, P, P, I64, P, P, P]
         if path is None:
             _lib = lib
         return lib
@@ -464,7 +492,7 @@ def _tokens(t):
     return t.contiguous(), 0
 
 
-def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
+def _step(kind, q, k, v, g, state, state_indices, scale, out, poison, beta=None):
     B, T, Hqk, K = q.shape
     H, V = v.shape[2:]
     dt = q.dtype
@@ -473,13 +501,16 @@ def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
     if k.shape != q.shape or v.shape[0] != B or v.shape[1] != T:
         raise ValueError("shape mismatch between q, k, v")
     if tuple(g.shape) != ((B, T, H, K) if kind == "gla" else (B, T, H)):
-        raise ValueError("gla_step's gate must be [B,T,H,K]" if kind == "gla" else "ssd_step's gate must be [B,T,H]")
+        raise ValueError("gla_step's gate must be [B,T,H,K]" if kind == "gla" else f"{kind}_step's gate must be [B,T,H]")
+    if beta is not None and beta.shape != g.shape:
+        raise ValueError("delta_step's beta must be [B,T,H]")
     (q, qs), (k, ks), (v, vs) = _tokens(q), _tokens(k), _tokens(v)
-    g = _contig(g, torch.float32)
+    g, beta = _contig(g, torch.float32), _contig(beta, torch.float32)
     dev = q.get_device()
     if not (k.get_device() == v.get_device() == g.get_device() == state.get_device() == dev) or (
-            state_indices is not None and state_indices.get_device() != dev):
-        _same_device(q.device, k=k, v=v, g=g, state=state, state_indices=state_indices)
+            state_indices is not None and state_indices.get_device() != dev) or (
+            beta is not None and beta.get_device() != dev):
+        _same_device(q.device, k=k, v=v, g=g, beta=beta, state=state, state_indices=state_indices)
     if not state.is_cuda or state.dtype != torch.float32 or not state.is_contiguous():
         raise ValueError("state must be a contiguous float32 CUDA tensor (it is updated in place)")
     if state.dim() != 4 or tuple(state.shape[1:]) != (H, K, V):
@@ -494,8 +525,12 @@ def _step(kind, q, k, v, g, state, state_indices, scale, out, poison):
     p = _PACK.pack(B, T, H, Hqk, K, V, _dtype_code(q), 0, scale, 0, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                    g.data_ptr(), 0, B if T else 0, 0, 0, 0, qs, ks, vs)
     lib = _lib or load()
-    st = (lib.gla_step if kind == "gla" else lib.ssd_step)(p, state.data_ptr(), state.shape[0], _addr(idx),
-                                                           o.data_ptr(), _raw_stream(q))
+    if kind == "delta":
+        st = lib.delta_step(p, beta.data_ptr(), state.data_ptr(), state.shape[0], _addr(idx), o.data_ptr(),
+                            _raw_stream(q))
+    else:
+        st = (lib.gla_step if kind == "gla" else lib.ssd_step)(p, state.data_ptr(), state.shape[0], _addr(idx),
+                                                               o.data_ptr(), _raw_stream(q))
     if st:
         _check(st, kind + "_step")
     return o
@@ -514,7 +549,173 @@ def ssd_step(q, k, v, g, state, state_indices=None, scale=1.0, out=None, poison=
     return _step("ssd", q, k, v, g, state, state_indices, scale, out, poison)
 
 
+# ---- the gated delta rule ------------------------------------------------------
+def _delta_beta(beta, g, device):
+    beta = _contig(beta, torch.float32)
+    if beta.shape != g.shape:
+        raise ValueError("beta must be [B,T,H]")
+    _same_device(device, beta=beta)
+    return beta
+
+
+def delta_fwd(q, k, v, g, beta, scale=None, segment_ids=None, initial_state=None, output_final_state=False,
+              n_seqs=None, out=None, final_out=None, workspace=None, poison=False):
+    """Gated delta rule over whole sequences:
+        u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),  S_t = exp(g_t) S_{t-1} + k_t u_t^T,  o_t = scale S_t^T q_t
+    q, k [B,T,Hqk,K] (k of unit length: qk_norm_fwd), v [B,T,H,V], g (log
+    decay) and beta [B,T,H] fp32; scale K^-1/2 unless given.  segment_ids,
+    initial_state and n_seqs as in ssd_fwd.  Returns (o, final_state or None)."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    p, keep = _problem(q, k, v, g, scale, segment_ids, initial_state, 0, n_seqs, True)
+    dev, dt = keep[0].device, keep[0].dtype
+    beta = _delta_beta(beta, keep[3], dev)
+    o = _given(out, "out", keep[2].shape, dt, dev) if out is not None else _new(tuple(keep[2].shape), dt, dev, poison)
+    ht = None
+    if output_final_state:
+        shape = (p.n_seqs, p.H, p.K, p.V)
+        ht = (_given(final_out, "final_out", shape, torch.float32, dev) if final_out is not None
+              else _new(shape, torch.float32, dev, poison))
+    ws = _workspace(p, "delta_fwd", dev, workspace)
+    _check(load().delta_fwd(ctypes.byref(p), _ptr(beta), _ptr(o), _ptr(ht), _stream(dev)), "delta_fwd")
+    del ws, keep
+    return o, ht
+
+
+def delta_bwd(q, k, v, g, beta, do, scale=None, segment_ids=None, initial_state=None, dht=None, n_seqs=None, outs=None,
+              workspace=None, poison=False):
+    """Gradients of delta_fwd.  do [B,T,H,V] and dht [n_seqs,H,K,V] (or None)
+    are those of o and the final state.  Returns (dq, dk, dv, dg, dbeta, dh0
+    or None)."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    p, keep = _problem(q, k, v, g, scale, segment_ids, initial_state, 0, n_seqs, True)
+    dev, dt = keep[0].device, keep[0].dtype
+    beta = _delta_beta(beta, keep[3], dev)
+    do = _contig(do, dt)
+    dht = _contig(dht, torch.float32)
+    if do.shape != keep[2].shape:
+        raise ValueError("do must match v")
+    states = (p.n_seqs, p.H, p.K, p.V)
+    if dht is not None and tuple(dht.shape) != states:
+        raise ValueError("dht must be [n_seqs,H,K,V]")
+    _same_device(dev, do=do, dht=dht)
+    if outs is not None:
+        dq, dk, dv, dg, dbeta, dh0 = outs
+        for t, name, like in ((dq, "dq", keep[0]), (dk, "dk", keep[1]), (dv, "dv", keep[2]), (dg, "dg", keep[3]),
+                              (dbeta, "dbeta", beta)):
+            _given(t, name, like.shape, like.dtype, dev)
+        if dh0 is not None:
+            _given(dh0, "dh0", states, torch.float32, dev)
+    else:
+        dq, dk, dv, dg, dbeta = (_new(tuple(x.shape), x.dtype, dev, poison) for x in (*keep[:4], beta))
+        dh0 = _new(states, torch.float32, dev, poison) if initial_state is not None else None
+    ws = _workspace(p, "delta_bwd", dev, workspace)
+    st = load().delta_bwd(ctypes.byref(p), _ptr(beta), _ptr(do), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+                          _ptr(dbeta), _ptr(dh0), _stream(dev))
+    _check(st, "delta_bwd")
+    del ws, keep
+    return dq, dk, dv, dg, dbeta, dh0
+
+
+def delta_step(q, k, v, g, beta, state, state_indices=None, scale=None, out=None, poison=False):
+    """New tokens of B sequences by the gated delta rule, on a pool of states
+    as in gla_step; g and beta [B,T,H]."""
+    return _step("delta", q, k, v, g, state, state_indices, scale, out, poison, beta)
+
+
 # ---- operations around the recurrence ---------------------------------------
+# glacore_qk_norm as bytes (see _PACK)
+_QK_PACK = struct.Struct("@6q3if8P3qPN")
+assert _QK_PACK.size == ctypes.sizeof(QkNorm)
+
+
+def _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved):
+    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+        raise ValueError("qk_norm: q must be [B, T, Hq, D] and k [B, T, Hk, D]")
+    if q.dtype != k.dtype:
+        raise TypeError("qk_norm: q and k must share one dtype")
+    if norm not in ("rms", "l2"):
+        raise ValueError("qk_norm: norm must be 'rms' or 'l2'")
+    if (cos is None) != (sin is None) or (cos is None and positions is not None):
+        raise ValueError("qk_norm: cos, sin and positions go together")
+    B, T, Hq, D = q.shape
+    (q, qs), (k, ks) = _tokens(q), _tokens(k)
+    wq, wk, cos, sin = (_contig(t, torch.float32) for t in (wq, wk, cos, sin))
+    positions = _contig(positions, torch.int32)
+    if (wq is not None and wq.shape != (D,)) or (wk is not None and wk.shape != (D,)):
+        raise ValueError("qk_norm: wq and wk must be [D]")
+    R = P = 0
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape or 2 * cos.shape[1] > D:
+            raise ValueError("qk_norm: cos and sin must be [n_positions, R] with 2 R <= D")
+        P, R = cos.shape
+        if positions is None and T > P:
+            raise ValueError("qk_norm: more tokens than positions in the tables")
+        if positions is not None and positions.shape != (B, T):
+            raise ValueError("qk_norm: positions must be [B, T]")
+    dev = q.get_device()
+    for t in (k, wq, wk, cos, sin, positions):
+        if t is not None and t.get_device() != dev:
+            _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, positions=positions)
+
+    def pack(ws=0, size=0):
+        return _QK_PACK.pack(B, T, Hq, k.shape[2], D, R, _dtype_code(q), int(norm == "l2"), int(bool(interleaved)), eps,
+                             0, q.data_ptr(), k.data_ptr(), _addr(wq) or 0, _addr(wk) or 0, _addr(cos) or 0,
+                             _addr(sin) or 0, _addr(positions) or 0, P, qs, ks, ws, size)
+
+    return q, k, pack, (wq, wk, cos, sin, positions)
+
+
+def qk_norm_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, eps=1e-6, norm="rms", interleaved=False,
+                outs=None):
+    """Norm of every query and key head and the rotation by position in one
+    pass: per row of D channels x * (mean(x^2) + eps)^-1/2 * w ("l2": the sum
+    in the mean's place), then its first R pairs of channels, (i, i + R) or
+    interleaved (2 i, 2 i + 1), rotated by the angle whose cos and sin
+    [n_positions, R] fp32 hold at the token's position.  q [B,T,Hq,D], k
+    [B,T,Hk,D] (bf16 or fp32; views of one projection go in place), wq, wk [D]
+    fp32 or None, positions [B,T] int32 or None (0 .. T - 1).  Returns (q, k)."""
+    q, k, pack, keep = _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved)
+    dt, dev = q.dtype, q.device
+    if outs is not None:
+        qo, ko = _given(outs[0], "q out", q.shape, dt, dev), _given(outs[1], "k out", k.shape, dt, dev)
+    else:
+        qo, ko = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+    st = (_lib or load()).qk_norm_fwd(pack(), qo.data_ptr(), ko.data_ptr(), _raw_stream(q))
+    if st:
+        _check(st, "qk_norm_fwd")
+    return qo, ko
+
+
+def qk_norm_bwd(q, k, dqo, dko, wq=None, wk=None, cos=None, sin=None, positions=None, eps=1e-6, norm="rms",
+                interleaved=False, outs=None, workspace=None):
+    """Gradients of qk_norm_fwd from those of its outputs: (dq, dk, dwq, dwk),
+    the last two [D] fp32 (also without weights)."""
+    q, k, pack, keep = _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved)
+    dt, dev = q.dtype, q.device
+    if dqo.shape != q.shape or dko.shape != k.shape:
+        raise ValueError("qk_norm: dqo and dko must match q and k")
+    dqo, dko = _contig(dqo, dt), _contig(dko, dt)
+    _same_device(dev, dqo=dqo, dko=dko)
+    D = q.shape[3]
+    if outs is not None:
+        dq, dk, dwq, dwk = outs
+        for t, name, shape, ty in ((dq, "dq", q.shape, dt), (dk, "dk", k.shape, dt), (dwq, "dwq", (D,), torch.float32),
+                                   (dwk, "dwk", (D,), torch.float32)):
+            _given(t, name, shape, ty, dev)
+    else:
+        dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
+        dwq, dwk = (torch.empty(D, dtype=torch.float32, device=dev) for _ in range(2))
+    lib = _lib or load()
+    ws = _scratch(lib.qk_norm_bwd_workspace_size(pack()), dev, workspace)
+    st = lib.qk_norm_bwd(pack(ws.data_ptr(), ws.numel()), dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                         dwq.data_ptr(), dwk.data_ptr(), _raw_stream(q))
+    if st:
+        _check(st, "qk_norm_bwd")
+    return dq, dk, dwq, dwk
+
+
 def _rows2d(t, name):
     """(tensor, rows, D, row stride) of a [..., D] tensor seen as rows of D
     values: evenly spaced rows are passed in place, anything else is copied."""

@@ -177,23 +177,6 @@ __global__ void state_scan_kernel(const float *L, const float *D, int64_t R, int
 
 // ---- argument checks ----------------------------------------------------
 
-namespace {
-
-struct Layout {
-  bool ssd;            // SSD tensor-core kernels (one gate per head, V = 64)
-  bool tc;             // tensor-core path
-  bool ssdx;           // SSD through the GLA tensor-core kernels (states padded in the workspace)
-  int chunk;           // chunk length of the state workspace / doc table
-  size_t off_start, off_cbase;  // doc tables (segments only)
-  size_t off_states, off_final, off_acc_q, off_acc_k, off_tc;
-  // ssdx: the GLA problem's tensors ([B*T, H, 128]) and states ([n, H, 128, 128])
-  size_t off_xh0, off_xht, off_xdht, off_xdq, off_xdk, off_xdg, off_xdh0;
-  size_t total;
-};
-
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
-inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
-
 glacore_status check_problem(const glacore_problem *p, bool head_gate) {
   if (!p) return GLACORE_ERR_INVALID_ARG;
   if (p->B < 1 || p->T < 0 || p->H < 1 || p->Hqk < 1 || p->K < 1 || p->V < 1)
@@ -223,6 +206,44 @@ glacore_status check_problem(const glacore_problem *p, bool head_gate) {
   (void)head_gate;
   return GLACORE_OK;
 }
+
+Prob make_prob(const glacore_problem *p, bool head_gate) {
+  Prob q;
+  q.BT = p->B * p->T;
+  q.H = p->H;
+  q.Hqk = p->Hqk;
+  q.K = p->K;
+  q.V = p->V;
+  q.gate_head = head_gate ? 1 : 0;
+  q.scale = p->scale;
+  q.q = p->q;
+  q.k = p->k;
+  q.v = p->v;
+  q.qs = p->q_stride ? p->q_stride : p->Hqk * p->K;
+  q.ks = p->k_stride ? p->k_stride : p->Hqk * p->K;
+  q.vs = p->v_stride ? p->v_stride : p->H * p->V;
+  q.g = p->g;
+  q.h0 = p->initial_state;
+  q.err = device_error_ptr();
+  return q;
+}
+
+namespace {
+
+struct Layout {
+  bool ssd;            // SSD tensor-core kernels (one gate per head, V = 64)
+  bool tc;             // tensor-core path
+  bool ssdx;           // SSD through the GLA tensor-core kernels (states padded in the workspace)
+  int chunk;           // chunk length of the state workspace / doc table
+  size_t off_start, off_cbase;  // doc tables (segments only)
+  size_t off_states, off_final, off_acc_q, off_acc_k, off_tc;
+  // ssdx: the GLA problem's tensors ([B*T, H, 128]) and states ([n, H, 128, 128])
+  size_t off_xh0, off_xht, off_xdht, off_xdq, off_xdk, off_xdg, off_xdh0;
+  size_t total;
+};
+
+inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
 // The CUDA-core kernels take any K, V up to 128 at chunk 16 (chunk_size 0
 // or 16), and chunks of 32 or 64 where their shared memory fits.
@@ -323,27 +344,6 @@ glacore_status check_ws(const glacore_problem *p, const Layout &L) {
   if (!p->workspace || p->workspace_bytes < L.total) return GLACORE_ERR_WORKSPACE;
   if ((uintptr_t)p->workspace & 255) return GLACORE_ERR_WORKSPACE;
   return GLACORE_OK;
-}
-
-Prob make_prob(const glacore_problem *p, bool head_gate) {
-  Prob q;
-  q.BT = p->B * p->T;
-  q.H = p->H;
-  q.Hqk = p->Hqk;
-  q.K = p->K;
-  q.V = p->V;
-  q.gate_head = head_gate ? 1 : 0;
-  q.scale = p->scale;
-  q.q = p->q;
-  q.k = p->k;
-  q.v = p->v;
-  q.qs = p->q_stride ? p->q_stride : p->Hqk * p->K;
-  q.ks = p->k_stride ? p->k_stride : p->Hqk * p->K;
-  q.vs = p->v_stride ? p->v_stride : p->H * p->V;
-  q.g = p->g;
-  q.h0 = p->initial_state;
-  q.err = device_error_ptr();
-  return q;
 }
 
 glacore_status cuda_status(cudaError_t e) { return status_of(e); }
@@ -643,7 +643,7 @@ const char *glacore_status_string(glacore_status s) {
     case GLACORE_ERR_RANGE:
       return "a chunk's summed log-decay is below the kernels' range (-80 per chunk; chunk_size 16 "
              "covers stronger decay)";
-    case GLACORE_ERR_INDEX: return "a state slot or a target token id is out of range";
+    case GLACORE_ERR_INDEX: return "a state slot, a target token id or a position is out of range";
   }
   return "unknown status";
 }

@@ -1,0 +1,63 @@
+// delta.cuh -- the gated delta rule (delta*.cu): declarations shared by its
+// host side and kernels.  Notation of the chunk form, for the C tokens of a
+// chunk of one (document, value head), S0 the state before it, S1 after it:
+//     G_t = sum of g from the chunk's start,  D_ts = exp(G_t - G_s) (s <= t)
+//     N = strict lower part of D (.) K K^T,   Z = -(I + N diag(b))^-1 N
+//     Y = V - e^G (.) K S0,  E = Y + Z (b Y),  U = b E
+//     O = scale (e^G (.) Q S0 + P U),  P = lower part of D (.) Q K^T
+//     S1 = e^{G_C} S0 + K^T (e^{G_C - G} (.) U)
+// E_t = v_t - e^{g_t} S_{t-1}^T k_t is the error of token t's own prediction.
+// Backward, with dS1 the gradient of S1:
+//     dU = scale P^T dO + e^{G_C - G} (.) K dS1,  dE = b dU
+//     dR = dU + Z^T (b dU),  dY = b dR = dV,  db = rowsum(E (.) dR)
+//     dS0 = e^{G_C} dS1 + Q^T (scale e^G (.) dO) - K^T (e^G (.) dY)
+//     dPd = scale D (.) lower(dO U^T),  dA = -D (.) strict lower(dY U^T)
+//     dQ = scale e^G (.) dO S0^T + dPd K
+//     dK = -e^G (.) dY S0^T + e^{G_C - G} (.) U dS1^T + dPd^T Q + (dA + dA^T) K
+// and dg_t, the gradient of everything that g_t decays: the pairs r >= t > s
+// of W = dPd (.) Q K^T + dA (.) K K^T, what the tokens r >= t read of S0, what
+// the tokens s < t left in S1, and e^{G_C} <S0, dS1>.
+#pragma once
+
+#include "internal.cuh"
+
+namespace glacore {
+namespace delta {
+
+constexpr int C = 64;  // tokens of a chunk
+
+struct Call {
+  Prob p;
+  Docs docs;         // tables for chunks of C tokens
+  int64_t slots;     // chunk slots (of all documents)
+  int dtype;
+  const float *beta;  // [BT, H]
+  cudaStream_t st;
+};
+
+// Scratch of the backward, all fp32: states before and state gradients after
+// every chunk [slots, H, K, V], E and dR of every token [BT, H, V].
+struct Saved {
+  float *s0, *ds1, *e, *dr;
+};
+
+// ---- CUDA-core kernels (delta_simt.cu): any K, V up to 256, both types ----
+// Token by token.  Forward: o (may be null), ht (may be null), and with
+// `saved` the states before the chunks and E.
+cudaError_t simt_scan(const Call &c, void *o, float *ht, const Saved *saved);
+// Backwards in time: dv, dR, the state gradients after the chunks, dh0.
+cudaError_t simt_scan_back(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved);
+// dq, dk, dg, dbeta from what the two passes saved, every chunk by itself.
+// dq and dk: [BT, H, K] fp32 per value head where heads share q and k (to be
+// summed by reduce_heads), [BT, H, K] dtype otherwise.
+cudaError_t simt_grads(const Call &c, const void *dO, const Saved &saved, void *dq, void *dk, bool per_head, float *dg,
+                       float *dbeta);
+// out [BT, Hqk, K] dtype = sums of x [BT, H, K] fp32 over the heads of a group.
+cudaError_t reduce_heads(const Call &c, const float *x, void *out);
+
+// ---- token by token on a pool of states (delta_step.cu) -------------------
+cudaError_t launch_step(const glacore_problem *p, const float *beta, float *state, int64_t n_slots,
+                        const int32_t *slots, void *o, int *err, cudaStream_t st);
+
+}  // namespace delta
+}  // namespace glacore

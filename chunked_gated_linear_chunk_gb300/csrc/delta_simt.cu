@@ -1,0 +1,643 @@
+// delta_simt.cu -- the gated delta rule on the CUDA cores, in fp32, for any
+// K and V up to 256 and both types (formulas in delta.cuh).
+//
+// The forward and the two passes of the backward that carry a state run token
+// by token: a state's value columns do not see each other, so a warp owns 8
+// columns of one (document, head), each thread KR key rows of two of them in
+// registers (two columns are one packed fp32 operation), and one exchange
+// over the 8 lanes of a column pair gives S^T k and S^T q of a token at once:
+//     o_t = scale (e^g S^T q + (q . k) u),  u = b (v - e^g S^T k)
+// (both on the state before the token).  The other half of the block's warps
+// converts the next 16 tokens' q, k, v into shared memory meanwhile.  Bound by
+// the latency of that dependence, about 230 cycles per token; any decay is
+// exact here.  The gradients of q, k, g and beta then take every chunk of 64 tokens
+// by itself (simt_grads), as products of 64 x 64 tiles.
+#include <algorithm>
+
+#include "delta.cuh"
+
+namespace glacore {
+namespace delta {
+
+namespace {
+
+constexpr int LK = 8;          // lanes along the key rows
+constexpr int TT = 16;         // tokens staged at once
+constexpr int COLS = 32;       // value columns of a block (4 warps x 8)
+constexpr int THREADS = 256;   // 4 warps that compute, 4 that stage
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 o;
+  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return o;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 o;
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return o;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+enum Mode { FWD, STATES, BACK };
+
+template <typename T>
+struct ScanArgs {
+  const T *q, *k, *v;  // v: do in BACK
+  const float *g, *beta, *seed;  // seed: initial state / gradient of the final state, or null
+  float *last;                   // final state / gradient of the initial state, or null
+  T *out;                        // o / null / dv
+  float *states;                 // states before / gradients after every chunk (STATES, BACK)
+  float *rows;                   // E / dR
+  Docs docs;
+  int64_t qs, ks, vs;
+  int H, share, K, V, slices;
+  float scale;
+};
+
+template <int KR>
+struct alignas(16) Tile {
+  float q[TT][LK * KR], k[TT][LK * KR];
+  float v[TT][COLS];
+  float a[TT], b[TT], qk[TT];
+};
+
+template <typename T, int KR, int MODE>
+__global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  Tile<KR> *tiles = reinterpret_cast<Tile<KR> *>(smem);  // two
+  constexpr int KP = LK * KR;
+  constexpr bool NEEDQ = MODE != STATES;
+  const int slice = (int)(blockIdx.x % a.slices);
+  const int64_t dh = blockIdx.x / a.slices;
+  const int h = (int)(dh % a.H);
+  const int64_t d = dh / a.H;
+  const int hq = h / a.share, v0 = slice * COLS;
+  int64_t s0, s1;
+  a.docs.range(d, s0, s1);
+  const int64_t n = s1 - s0;
+  const int ntile = (int)((n + TT - 1) / TT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool stages = warp >= 4;
+  const int64_t slot0 = a.docs.chunk_base(d);
+
+  // tile i of the pass covers the tokens tile_of(i) * TT ... of the document
+  auto tile_of = [&](int i) { return MODE == BACK ? ntile - 1 - i : i; };
+  auto stage = [&](int i) {
+    Tile<KR> &t = tiles[i & 1];
+    const int64_t t0 = (int64_t)tile_of(i) * TT;
+    const int len = (int)min((int64_t)TT, n - t0);
+    for (int r = warp - 4; r < len; r += 4) {
+      const int64_t tok = s0 + t0 + r;
+      const T *qr = a.q + tok * a.qs + (int64_t)hq * a.K, *kr = a.k + tok * a.ks + (int64_t)hq * a.K;
+      float dot = 0.f, kx[KP / 32], qx[KP / 32];
+#pragma unroll
+      for (int e = 0; e < KP / 32; ++e) {
+        const int c = lane + 32 * e;
+        kx[e] = c < a.K ? to_f32(kr[c]) : 0.f;
+        qx[e] = NEEDQ && c < a.K ? to_f32(qr[c]) : 0.f;
+      }
+      const float vx = v0 + lane < a.V ? to_f32(a.v[tok * a.vs + (int64_t)h * a.V + v0 + lane]) : 0.f;
+      const float gx = a.g[tok * a.H + h], bx = a.beta[tok * a.H + h];
+#pragma unroll
+      for (int e = 0; e < KP / 32; ++e) {
+        t.k[r][lane + 32 * e] = kx[e];
+        if (NEEDQ) t.q[r][lane + 32 * e] = qx[e];
+        dot = fmaf(kx[e], qx[e], dot);
+      }
+      t.v[r][lane] = vx;
+      if (NEEDQ)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) {
+        t.a[r] = expf(gx);
+        t.b[r] = bx;
+        t.qk[r] = dot;
+      }
+    }
+  };
+
+  // thread (lk, c): rows 4 lk + 32 i + 0..3 of columns v0 + 8 warp + 2 c + 0..1
+  const int lk = lane & 7, cl = (warp & 3) * 8 + 2 * (lane >> 3), col = v0 + cl;
+  const bool in0 = col < a.V, in1 = col + 1 < a.V;
+  float2 S[KR];
+  const int64_t mat = (d * a.H + h) * a.K * a.V;
+  auto put_state = [&](float *dst) {
+#pragma unroll
+    for (int j = 0; j < KR; ++j) {
+      const int row = 4 * lk + 32 * (j >> 2) + (j & 3);
+      if (row < a.K) {
+        if (in0) dst[(int64_t)row * a.V + col] = S[j].x;
+        if (in1) dst[(int64_t)row * a.V + col + 1] = S[j].y;
+      }
+    }
+  };
+  if (!stages) {
+#pragma unroll
+    for (int j = 0; j < KR; ++j) {
+      const int row = 4 * lk + 32 * (j >> 2) + (j & 3);
+      S[j] = both(0.f);
+      if (a.seed && row < a.K) {
+        if (in0) S[j].x = a.seed[mat + (int64_t)row * a.V + col];
+        if (in1) S[j].y = a.seed[mat + (int64_t)row * a.V + col + 1];
+      }
+    }
+  } else if (ntile > 0) {
+    stage(0);
+  }
+  __syncthreads();
+  for (int i = 0; i < ntile; ++i) {
+    if (stages) {
+      if (i + 1 < ntile) stage(i + 1);
+    } else {
+      const Tile<KR> &t = tiles[i & 1];
+      const int64_t t0 = (int64_t)tile_of(i) * TT;
+      const int len = (int)min((int64_t)TT, n - t0);
+      // the states before a chunk; the gradients after one (its last tile, or the document's)
+      if (MODE == STATES && t0 % C == 0) put_state(a.states + ((slot0 + t0 / C) * a.H + h) * a.K * a.V);
+      if (MODE == BACK && ((t0 + TT) % C == 0 || i == 0))
+        put_state(a.states + ((slot0 + t0 / C) * a.H + h) * a.K * a.V);
+      for (int rr = 0; rr < len; ++rr) {
+        const int r = MODE == BACK ? len - 1 - rr : rr;
+        float2 xk = both(0.f), xq = both(0.f);
+        float4 kv[KR / 4], qv[KR / 4];
+#pragma unroll
+        for (int j = 0; j < KR / 4; ++j) {
+          kv[j] = *reinterpret_cast<const float4 *>(&t.k[r][4 * lk + 32 * j]);
+          if (NEEDQ) qv[j] = *reinterpret_cast<const float4 *>(&t.q[r][4 * lk + 32 * j]);
+        }
+        const float *kp = reinterpret_cast<const float *>(kv), *qp = reinterpret_cast<const float *>(qv);
+        float2 xk2 = both(0.f);
+#pragma unroll
+        for (int j = 0; j < KR; j += 2) {
+          xk = fma2(both(kp[j]), S[j], xk);
+          xk2 = fma2(both(kp[j + 1]), S[j + 1], xk2);
+        }
+        xk.x += xk2.x;
+        xk.y += xk2.y;
+        if (MODE == FWD) {
+#pragma unroll
+          for (int j = 0; j < KR; ++j) xq = fma2(both(qp[j]), S[j], xq);
+        }
+#pragma unroll
+        for (int o = 1; o < LK; o <<= 1) {
+          xk.x += __shfl_xor_sync(0xffffffffu, xk.x, o);
+          xk.y += __shfl_xor_sync(0xffffffffu, xk.y, o);
+          if (MODE == FWD) {
+            xq.x += __shfl_xor_sync(0xffffffffu, xq.x, o);
+            xq.y += __shfl_xor_sync(0xffffffffu, xq.y, o);
+          }
+        }
+        const float2 v = *reinterpret_cast<const float2 *>(&t.v[r][cl]);
+        const float dec = t.a[r], b = t.b[r];
+        const int64_t at = ((s0 + t0 + r) * a.H + h) * a.V + col;
+        if (MODE != BACK) {
+          const float2 e = make_float2(v.x - dec * xk.x, v.y - dec * xk.y);
+          const float2 u = make_float2(b * e.x, b * e.y);
+#pragma unroll
+          for (int j = 0; j < KR; ++j) S[j] = fma2(both(kp[j]), u, mul2(both(dec), S[j]));
+          if (MODE == FWD) {
+            if (a.out && lk == 0) {
+              const float qk = t.qk[r];
+              if (in0) a.out[at] = from_f32<T>(a.scale * fmaf(qk, u.x, dec * xq.x));
+              if (in1) a.out[at + 1] = from_f32<T>(a.scale * fmaf(qk, u.y, dec * xq.y));
+            }
+          } else if (lk == 0) {
+            if (in0) a.rows[at] = e.x;
+            if (in1) a.rows[at + 1] = e.y;
+          }
+        } else {
+          const float sqk = a.scale * t.qk[r];
+          const float2 du = make_float2(fmaf(sqk, v.x, xk.x), fmaf(sqk, v.y, xk.y));
+          const float2 dy = make_float2(b * du.x, b * du.y), w = make_float2(a.scale * v.x, a.scale * v.y);
+#pragma unroll
+          for (int j = 0; j < KR; ++j)
+            S[j] = mul2(both(dec), fma2(both(-kp[j]), dy, fma2(both(qp[j]), w, S[j])));
+          if (lk == 0) {
+            if (in0) a.rows[at] = du.x, a.out[at] = from_f32<T>(dy.x);
+            if (in1) a.rows[at + 1] = du.y, a.out[at + 1] = from_f32<T>(dy.y);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (!stages && a.last) put_state(a.last + mat);
+}
+
+template <typename T, int MODE>
+cudaError_t scan_as(const Call &c, const void *v, int64_t vs, const float *seed, float *last, void *out, float *states,
+                    float *rows) {
+  ScanArgs<T> a;
+  a.q = (const T *)c.p.q;
+  a.k = (const T *)c.p.k;
+  a.v = (const T *)v;
+  a.g = c.p.g;
+  a.beta = c.beta;
+  a.seed = seed;
+  a.last = last;
+  a.out = (T *)out;
+  a.states = states;
+  a.rows = rows;
+  a.docs = c.docs;
+  a.qs = c.p.qs;
+  a.ks = c.p.ks;
+  a.vs = vs;
+  a.H = (int)c.p.H;
+  a.share = (int)(c.p.H / c.p.Hqk);
+  a.K = (int)c.p.K;
+  a.V = (int)c.p.V;
+  a.slices = (a.V + COLS - 1) / COLS;
+  a.scale = c.p.scale;
+  const int64_t ctas = c.docs.n * c.p.H * a.slices;
+  if (ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  auto go = [&](auto kernel, size_t smem) -> cudaError_t {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)ctas, THREADS, smem, c.st>>>(a);
+    return cudaGetLastError();
+  };
+  cudaError_t e;
+  if (a.K <= 32)
+    e = go(scan_kernel<T, 4, MODE>, 2 * sizeof(Tile<4>));
+  else if (a.K <= 64)
+    e = go(scan_kernel<T, 8, MODE>, 2 * sizeof(Tile<8>));
+  else if (a.K <= 128)
+    e = go(scan_kernel<T, 16, MODE>, 2 * sizeof(Tile<16>));
+  else
+    e = go(scan_kernel<T, 32, MODE>, 2 * sizeof(Tile<32>));
+  mark_launch(MODE == FWD ? "delta_scan" : MODE == STATES ? "delta_scan_states" : "delta_scan_back", c.st);
+  return e;
+}
+
+// ---- gradients of q, k, g, beta ---------------------------------------------
+//
+// One block per (chunk, head), 256 threads; thread (tx, ty) owns the 4 x 4
+// entries (ty + 16 i, tx + 16 j) of a 64 x 64 result (rows and columns 16
+// apart, so that its shared-memory reads are free of bank conflicts at a row pitch of PITCH).
+constexpr int W = 32;      // columns of a staged slice of the contraction
+constexpr int PITCH = 33;  // its row pitch
+constexpr int CP = C + 1;  // pitch of the C x C matrices
+
+template <typename T>
+struct GradArgs {
+  const T *q, *k, *dO;
+  const float *g, *beta;
+  Saved s;
+  Docs docs;
+  int64_t qs, ks;
+  int H, share, K, V;
+  float scale;
+  void *dq, *dk;
+  int per_head;  // dq, dk fp32 (to be summed), else T
+  float *dg, *dbeta;
+};
+
+struct GradSmem {
+  float x[5][C][PITCH];  // staged slices
+  float dP[C][CP], dA[C][CP];
+  float kt[C][C + 1], qt[C][C + 1];  // 64 channels of k and q
+  double G[C];
+  float into[C], outof[C], beta[C];
+  float gq[C], gk[C], gadd[C], db[C], pair[C];
+  float red[32];
+};
+
+// acc[i][j] += sum over the slice of a[ty + 16 i][.] b[tx + 16 j][.]
+__device__ __forceinline__ void slice_product(float (&acc)[4][4], const float (*a)[PITCH], const float (*b)[PITCH],
+                                              int tx, int ty) {
+#pragma unroll 8
+  for (int w = 0; w < W; ++w) {
+    float x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = a[ty + 16 * i][w];
+      y[i] = b[tx + 16 * i][w];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+  }
+}
+__device__ __forceinline__ void zero(float (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  GradSmem &s = *reinterpret_cast<GradSmem *>(smem_raw);
+  const int h = (int)(blockIdx.x % a.H);
+  const int64_t slot = blockIdx.x / a.H;
+  // the document of the chunk slot
+  int64_t d, j;
+  if (a.docs.cbase) {
+    if (slot >= a.docs.cbase[a.docs.n]) return;
+    int64_t lo = 0, hi = a.docs.n;  // cbase[lo] <= slot < cbase[hi]
+    while (hi - lo > 1) {
+      const int64_t m = (lo + hi) >> 1;
+      if (a.docs.cbase[m] <= slot) lo = m; else hi = m;
+    }
+    d = lo;
+    j = slot - a.docs.cbase[d];
+  } else {
+    const int64_t per = (a.docs.T + C - 1) / C;
+    d = slot / per;
+    j = slot - d * per;
+  }
+  int64_t s0, s1;
+  a.docs.range(d, s0, s1);
+  const int64_t tok0 = s0 + j * C;
+  const int L = (int)min((int64_t)C, s1 - tok0);
+  const int hq = h / a.share;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const T *q = a.q + (int64_t)hq * a.K, *k = a.k + (int64_t)hq * a.K;
+
+  if (tid < C) {
+    s.G[tid] = tid < L ? (double)fmaxf(a.g[(tok0 + tid) * a.H + h], -1e4f) : 0.0;  // exp of less is 0 as well
+    s.beta[tid] = tid < L ? a.beta[(tok0 + tid) * a.H + h] : 0.f;
+    s.gq[tid] = s.gk[tid] = s.gadd[tid] = s.db[tid] = 0.f;
+  }
+  __syncthreads();
+  if (tid == 0)
+    for (int t = 1; t < C; ++t) s.G[t] += s.G[t - 1];
+  __syncthreads();
+  if (tid < C) {
+    s.into[tid] = expf((float)s.G[tid]);
+    s.outof[tid] = expf((float)(s.G[L - 1] - s.G[tid]));
+  }
+  const float over = expf((float)s.G[L - 1]);
+
+  // token rows [tok0, tok0 + L) x columns [c0, c0 + W) of a per-head fp32 or T tensor
+  auto stage_rows = [&](float (*dst)[PITCH], auto *src, int64_t stride, int c0, int width) {
+    for (int i = tid; i < C * W; i += 256) {
+      const int r = i / W, c = i % W;
+      dst[r][c] = r < L && c0 + c < width ? to_f32(src[(tok0 + r) * stride + c0 + c]) : 0.f;
+    }
+  };
+  const int64_t hv = (int64_t)a.H * a.V;
+  const float *e = a.s.e + (int64_t)h * a.V, *dr = a.s.dr + (int64_t)h * a.V;
+  const T *dO = a.dO + (int64_t)h * a.V;
+
+  // C x C products over the value columns, then over the key channels
+  float b1[4][4], b2[4][4];
+  zero(b1);
+  zero(b2);
+  for (int c0 = 0; c0 < a.V; c0 += W) {
+    __syncthreads();
+    stage_rows(s.x[0], dO, hv, c0, a.V);
+    stage_rows(s.x[1], dr, hv, c0, a.V);
+    stage_rows(s.x[2], e, hv, c0, a.V);
+    __syncthreads();
+    slice_product(b1, s.x[0], s.x[2], tx, ty);
+    slice_product(b2, s.x[1], s.x[2], tx, ty);
+    if (tid < C) {
+      float x = 0.f;
+      for (int c = 0; c < W; ++c) x = fmaf(s.x[1][tid][c], s.x[2][tid][c], x);
+      s.db[tid] += x;
+    }
+  }
+  float qk[4][4], kk[4][4];
+  zero(qk);
+  zero(kk);
+  for (int c0 = 0; c0 < a.K; c0 += W) {
+    __syncthreads();
+    stage_rows(s.x[0], q, a.qs, c0, a.K);
+    stage_rows(s.x[1], k, a.ks, c0, a.K);
+    __syncthreads();
+    slice_product(qk, s.x[0], s.x[1], tx, ty);
+    slice_product(kk, s.x[1], s.x[1], tx, ty);
+  }
+  // dPd and dA; W_rs of the pairs r > s, kept in the staging area
+  float (*Wm)[CP] = reinterpret_cast<float (*)[CP]>(&s.x[0][0][0]);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const int t = ty + 16 * i, r = tx + 16 * jj;
+      float dp = 0.f, da = 0.f;
+      if (r <= t && t < L) {
+        const float D = expf((float)(s.G[t] - s.G[r])) * s.beta[r];  // U = beta E
+        dp = a.scale * D * b1[i][jj];
+        if (r < t) da = -D * s.beta[t] * b2[i][jj];
+      }
+      s.dP[t][r] = dp;
+      s.dA[t][r] = da;
+      Wm[t][r] = r < t ? fmaf(dp, qk[i][jj], da * kk[i][jj]) : 0.f;
+    }
+  __syncthreads();
+  // pair[t] = sum over r >= t > s of W_rs: first every column's sums from below, then along each row
+  if (tid < C) {
+    float x = 0.f;
+    for (int r = C - 1; r >= 0; --r) {
+      x += Wm[r][tid];
+      Wm[r][tid] = x;
+    }
+  }
+  __syncthreads();
+  if (tid < C) {
+    float x = 0.f;
+    for (int c = 0; c < tid; ++c) x += Wm[tid][c];
+    s.pair[tid] = x;
+  }
+
+  // dq, dk for 64 channels at a time; <S0, dS1> on the way
+  const float *S0 = a.s.s0 + (slot * a.H + h) * (int64_t)a.K * a.V, *S1 = a.s.ds1 + (slot * a.H + h) * (int64_t)a.K * a.V;
+  float sd = 0.f;
+  for (int k0 = 0; k0 < a.K; k0 += 64) {
+    float m1[4][4], m2[4][4], m3[4][4];
+    zero(m1);
+    zero(m2);
+    zero(m3);
+    for (int c0 = 0; c0 < a.V; c0 += W) {
+      __syncthreads();
+      stage_rows(s.x[0], dO, hv, c0, a.V);
+      stage_rows(s.x[1], dr, hv, c0, a.V);
+      stage_rows(s.x[2], e, hv, c0, a.V);
+      for (int i = tid; i < C * W; i += 256) {
+        const int r = i / W, c = i % W;
+        const bool in = k0 + r < a.K && c0 + c < a.V;
+        const float x = in ? S0[(int64_t)(k0 + r) * a.V + c0 + c] : 0.f, y = in ? S1[(int64_t)(k0 + r) * a.V + c0 + c] : 0.f;
+        s.x[3][r][c] = x;
+        s.x[4][r][c] = y;
+        sd = fmaf(x, y, sd);
+      }
+      __syncthreads();
+      slice_product(m1, s.x[0], s.x[3], tx, ty);
+      slice_product(m2, s.x[1], s.x[3], tx, ty);
+      slice_product(m3, s.x[2], s.x[4], tx, ty);
+    }
+    __syncthreads();
+    for (int i = tid; i < C * 64; i += 256) {
+      const int r = i / 64, c = i % 64;
+      const bool in = r < L && k0 + c < a.K;
+      s.kt[r][c] = in ? to_f32(k[(tok0 + r) * a.ks + k0 + c]) : 0.f;
+      s.qt[r][c] = in ? to_f32(q[(tok0 + r) * a.qs + k0 + c]) : 0.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = ty + 16 * i;
+      float rq = 0.f, rk = 0.f, ra = 0.f;
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int c = tx + 16 * jj;
+        m1[i][jj] *= a.scale * s.into[t];
+        m2[i][jj] *= -s.into[t] * s.beta[t];
+        m3[i][jj] *= s.outof[t] * s.beta[t];
+        rq = fmaf(s.qt[t][c], m1[i][jj], rq);
+        rk = fmaf(s.kt[t][c], m2[i][jj], rk);
+        ra = fmaf(s.kt[t][c], m3[i][jj], ra);
+        m2[i][jj] += m3[i][jj];
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) {
+        rq += __shfl_xor_sync(0xffffffffu, rq, o);
+        rk += __shfl_xor_sync(0xffffffffu, rk, o);
+        ra += __shfl_xor_sync(0xffffffffu, ra, o);
+      }
+      if (tx == 0) {
+        s.gq[t] += rq;
+        s.gk[t] += rk;
+        s.gadd[t] += ra;
+      }
+    }
+    for (int r = 0; r < L; ++r) {
+      float kx[4], qx[4], pr[4], ar[4], pc[4], ac[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        kx[i] = s.kt[r][tx + 16 * i];
+        qx[i] = s.qt[r][tx + 16 * i];
+        pr[i] = s.dP[ty + 16 * i][r];
+        ar[i] = s.dA[ty + 16 * i][r];
+        pc[i] = s.dP[r][ty + 16 * i];
+        ac[i] = s.dA[r][ty + 16 * i];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          m1[i][jj] = fmaf(pr[i], kx[jj], m1[i][jj]);
+          m2[i][jj] = fmaf(pc[i], qx[jj], fmaf(ar[i] + ac[i], kx[jj], m2[i][jj]));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int t = ty + 16 * i, c = k0 + tx + 16 * jj;
+        if (t < L && c < a.K) {
+          const int64_t at = ((tok0 + t) * a.H + h) * a.K + c;
+          if (a.per_head) {
+            ((float *)a.dq)[at] = m1[i][jj];
+            ((float *)a.dk)[at] = m2[i][jj];
+          } else {
+            ((T *)a.dq)[at] = from_f32<T>(m1[i][jj]);
+            ((T *)a.dk)[at] = from_f32<T>(m2[i][jj]);
+          }
+        }
+      }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
+  if ((tid & 31) == 0) s.red[tid >> 5] = sd;
+  __syncthreads();
+  if (tid < L) {
+    float x = s.pair[tid], sum = 0.f;
+    for (int r = tid; r < L; ++r) x += s.gq[r] + s.gk[r];
+    for (int r = 0; r < tid; ++r) x += s.gadd[r];
+    for (int w = 0; w < 8; ++w) sum += s.red[w];
+    a.dg[(tok0 + tid) * a.H + h] = fmaf(over, sum, x);
+    a.dbeta[(tok0 + tid) * a.H + h] = s.db[tid];
+  }
+}
+
+template <typename T>
+cudaError_t grads_as(const Call &c, const void *dO, const Saved &saved, void *dq, void *dk, bool per_head, float *dg,
+                     float *dbeta) {
+  GradArgs<T> a;
+  a.q = (const T *)c.p.q;
+  a.k = (const T *)c.p.k;
+  a.dO = (const T *)dO;
+  a.g = c.p.g;
+  a.beta = c.beta;
+  a.s = saved;
+  a.docs = c.docs;
+  a.qs = c.p.qs;
+  a.ks = c.p.ks;
+  a.H = (int)c.p.H;
+  a.share = (int)(c.p.H / c.p.Hqk);
+  a.K = (int)c.p.K;
+  a.V = (int)c.p.V;
+  a.scale = c.p.scale;
+  a.dq = dq;
+  a.dk = dk;
+  a.per_head = per_head;
+  a.dg = dg;
+  a.dbeta = dbeta;
+  const int64_t ctas = c.slots * c.p.H;
+  if (ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(grads_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(GradSmem));
+  if (e != cudaSuccess) return e;
+  grads_kernel<T><<<(unsigned)ctas, 256, sizeof(GradSmem), c.st>>>(a);
+  mark_launch("delta_grads", c.st);
+  return cudaGetLastError();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) reduce_heads_kernel(const float *x, T *out, int64_t n, int64_t K, int share) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const float *src = x + (i / K) * share * K + i % K;
+    float s = 0.f;
+    for (int e = 0; e < share; ++e) s += src[e * K];
+    out[i] = from_f32<T>(s);
+  }
+}
+
+}  // namespace
+
+cudaError_t simt_scan(const Call &c, void *o, float *ht, const Saved *saved) {
+  if (saved)
+    return c.dtype == GLACORE_BF16
+               ? scan_as<__nv_bfloat16, STATES>(c, c.p.v, c.p.vs, c.p.h0, ht, nullptr, saved->s0, saved->e)
+               : scan_as<float, STATES>(c, c.p.v, c.p.vs, c.p.h0, ht, nullptr, saved->s0, saved->e);
+  return c.dtype == GLACORE_BF16 ? scan_as<__nv_bfloat16, FWD>(c, c.p.v, c.p.vs, c.p.h0, ht, o, nullptr, nullptr)
+                                 : scan_as<float, FWD>(c, c.p.v, c.p.vs, c.p.h0, ht, o, nullptr, nullptr);
+}
+
+cudaError_t simt_scan_back(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved) {
+  const int64_t vs = c.p.H * c.p.V;
+  return c.dtype == GLACORE_BF16 ? scan_as<__nv_bfloat16, BACK>(c, dO, vs, dht, dh0, dv, saved.ds1, saved.dr)
+                                 : scan_as<float, BACK>(c, dO, vs, dht, dh0, dv, saved.ds1, saved.dr);
+}
+
+cudaError_t simt_grads(const Call &c, const void *dO, const Saved &saved, void *dq, void *dk, bool per_head, float *dg,
+                       float *dbeta) {
+  return c.dtype == GLACORE_BF16 ? grads_as<__nv_bfloat16>(c, dO, saved, dq, dk, per_head, dg, dbeta)
+                                 : grads_as<float>(c, dO, saved, dq, dk, per_head, dg, dbeta);
+}
+
+cudaError_t reduce_heads(const Call &c, const float *x, void *out) {
+  const int64_t n = c.p.BT * c.p.Hqk * c.p.K;
+  const int blocks = (int)std::min<int64_t>((n + 255) / 256, 152 * 16);
+  const int share = (int)(c.p.H / c.p.Hqk);
+  if (c.dtype == GLACORE_BF16)
+    reduce_heads_kernel<<<blocks, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, n, c.p.K, share);
+  else
+    reduce_heads_kernel<<<blocks, 256, 0, c.st>>>(x, (float *)out, n, c.p.K, share);
+  mark_launch("delta_reduce_heads", c.st);
+  return cudaGetLastError();
+}
+
+}  // namespace delta
+}  // namespace glacore

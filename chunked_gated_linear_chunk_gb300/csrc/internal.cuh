@@ -197,6 +197,11 @@ void mark_launch(const char *label, cudaStream_t st);
 // thread's last failing call (glacore_last_cuda_error).
 glacore_status status_of(cudaError_t e);
 
+// Checks of a problem's own fields, before any launch (api.cu).
+glacore_status check_problem(const glacore_problem *p, bool head_gate);
+// The problem as the kernels see it.
+Prob make_prob(const glacore_problem *p, bool head_gate);
+
 // ---- segment prep ------------------------------------------------------
 cudaError_t launch_prep(const int32_t *seg, int64_t B, int64_t T, int64_t n_seqs, int chunk,
                         int64_t *start, int64_t *cbase, int *err, cudaStream_t st);

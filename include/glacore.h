@@ -80,7 +80,7 @@ typedef enum {
   GLACORE_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than *_workspace_size */
   GLACORE_ERR_DOCS = 6,        /* device: document count != n_seqs */
   GLACORE_ERR_RANGE = 7,       /* device: a chunk's decay is outside the kernels' range (below) */
-  GLACORE_ERR_INDEX = 8        /* device: a state slot or a target token id is out of range */
+  GLACORE_ERR_INDEX = 8        /* device: a state slot, a target token id or a position is out of range */
 } glacore_status;
 
 typedef enum { GLACORE_F32 = 0, GLACORE_BF16 = 1 } glacore_dtype;
@@ -205,6 +205,40 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
                         int64_t n_slots, const int32_t *state_indices,
                         void *o, glacore_stream_t stream);
 
+/* ---- the gated delta rule -----------------------------------------------
+ * The recurrence whose tokens correct what the state already holds for their
+ * key, with one log-decay and one writing strength per value head:
+ *     u_t = beta_t (v_t - e^{g_t} S_{t-1}^T k_t)
+ *     S_t = e^{g_t} S_{t-1} + k_t u_t^T,     o_t = scale * S_t^T q_t
+ * (that is, S_t = e^{g_t} (1 - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T;
+ * the plain delta rule is g = 0).  Problem, layouts, token strides, head
+ * sharing, documents, states and workspaces are those of ssd_fwd / ssd_bwd:
+ *   p            g [B,T,H] fp32, g <= 0; chunk_size 0 or 64; K and V up to 256
+ *   beta         [B,T,H] fp32.  With keys of unit length (qk_norm_fwd) any
+ *                beta in [0, 2] keeps the state bounded.
+ *   o, final_state, do_, dht, dq, dk, dv, dg, dh0   as in ssd_fwd / ssd_bwd
+ *   dbeta        [B,T,H] fp32, written
+ * Any decay is exact (g below -10^4 counts as -10^4: e^g is 0 either way).
+ * No alignment but the elements' own is asked for.
+ * The backward keeps in its workspace the states before and the state
+ * gradients after every 64 tokens, 8 K V bytes per head, and 8 V bytes per
+ * token and head. */
+size_t delta_fwd_workspace_size(const glacore_problem *p);
+size_t delta_bwd_workspace_size(const glacore_problem *p);
+glacore_status delta_fwd(const glacore_problem *p, const float *beta, void *o,
+                         float *final_state, glacore_stream_t stream);
+glacore_status delta_bwd(const glacore_problem *p, const float *beta,
+                         const void *do_, const float *dht, void *dq, void *dk,
+                         void *dv, float *dg, float *dbeta, float *dh0,
+                         glacore_stream_t stream);
+/* The T newest tokens of each of B sequences on a pool of states: gla_step's
+ * arguments and rules (pool, slots, idle rows, forgetting at g = -inf), with g
+ * and beta [B,T,H]. */
+glacore_status delta_step(const glacore_problem *p, const float *beta,
+                          float *state, int64_t n_slots,
+                          const int32_t *state_indices, void *o,
+                          glacore_stream_t stream);
+
 /* gla_bwd without a workspace, for callers that cannot allocate device
  * memory when they call the backward (for example a host framework that
  * owns all device memory and gives its plugins no allocator, or a training
@@ -314,6 +348,53 @@ glacore_status short_conv_bwd(const void *x, const float *w, const float *b,
                               int32_t dtype, int32_t activation, void *dx,
                               float *dw, float *db, void *workspace,
                               size_t workspace_bytes, glacore_stream_t stream);
+
+/* Norm of every query and key head and the rotation by position, in one pass,
+ * before the recurrence (the delta rule wants keys of unit length).  Over each
+ * row x of D channels (one token, one head), w the weights of queries or keys:
+ *     n = x r w,  r = (mean(x^2) + eps)^(-1/2),  l2: (sum(x^2) + eps)^(-1/2)
+ *     (n_i, n_j) -> (n_i c - n_j s, n_j c + n_i s)
+ * for the R pairs (i, i + R), interleaved: (2 i, 2 i + 1), with c and s entry
+ * (position, i) of the two tables; channels from 2 R on are not rotated.
+ *   q, k        [B, T, Hq, D], [B, T, Hk, D] (dtype), token strides as in
+ *               glacore_problem (0: contiguous), so that both are read in place
+ *               from one projection; D up to 256, any
+ *   wq, wk      [D] fp32 or NULL (1)
+ *   cos_table, sin_table  [n_positions, R] fp32, or NULL with R = 0
+ *   positions   [B, T] int32 or NULL (token t of a row is at position t).  A
+ *               position outside the tables leaves its token unrotated and
+ *               sets GLACORE_ERR_INDEX in the device error word.
+ *   l2, interleaved  0 or 1;  eps >= 0 (0: a row of zeros becomes NaN)
+ *   qo, ko      [B, T, Hq, D], [B, T, Hk, D] (dtype), contiguous, written; no
+ *               output may overlap an input
+ * Backward, of the same problem: dqo and dko the outputs' gradients
+ * (contiguous); dq, dk (contiguous, dtype) and dwq, dwk [D] fp32 written (also
+ * without weights), the latter reduced deterministically through the workspace
+ * (at least qk_norm_bwd_workspace_size bytes, 256-byte aligned).
+ * D and R multiples of 8 (interleaved: R of 4) with 16-byte aligned addresses
+ * and strides are the fast case (others take about 3 times as long). */
+typedef struct glacore_qk_norm {
+  int64_t B, T, Hq, Hk, D, R;
+  int32_t dtype;
+  int32_t l2;
+  int32_t interleaved;
+  float eps;
+  int64_t reserved0; /* must be 0 */
+  const void *q, *k;
+  const float *wq, *wk;
+  const float *cos_table, *sin_table;
+  const int32_t *positions;
+  int64_t n_positions;
+  int64_t q_stride, k_stride;
+  void *workspace;
+  size_t workspace_bytes;
+} glacore_qk_norm;
+glacore_status qk_norm_fwd(const glacore_qk_norm *p, void *qo, void *ko,
+                           glacore_stream_t stream);
+size_t qk_norm_bwd_workspace_size(const glacore_qk_norm *p);
+glacore_status qk_norm_bwd(const glacore_qk_norm *p, const void *dqo,
+                           const void *dko, void *dq, void *dk, float *dwq,
+                           float *dwk, glacore_stream_t stream);
 
 /* Layer norm over rows of D values (the norm in front of a layer and before
  * the output projection):
