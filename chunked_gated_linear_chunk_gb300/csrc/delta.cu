@@ -17,8 +17,10 @@ struct Layout {
   size_t start, cbase;          // document tables (segment_ids only)
   size_t s0, ds1, e, dr;        // backward
   size_t dq, dk;                // backward, shared q / k heads: per value head, fp32
+  size_t tc;                    // the tensor-core kernels' own
   size_t total;
   int64_t slots;
+  bool on_tc;
 };
 
 Layout layout(const glacore_problem *p, bool backward) {
@@ -36,6 +38,8 @@ Layout layout(const glacore_problem *p, bool backward) {
   }
   // a document's last chunk may be short: at most one more than its tokens fill
   L.slots = p->segment_ids ? std::min(BT, BT / C + n) : p->B * ((p->T + C - 1) / C);
+  L.on_tc = tc_supported(p);
+  if (L.on_tc && !backward) take(L.tc, tc_workspace(L.slots, p->H, false));
   if (backward) {
     const size_t states = sizeof(float) * (size_t)L.slots * p->H * p->K * p->V;
     const size_t rows = sizeof(float) * (size_t)BT * p->H * p->V;
@@ -104,6 +108,7 @@ glacore_status run_fwd(const glacore_problem *p, const float *beta, void *o, flo
   if (BT == 0) return GLACORE_OK;
   Call c;
   if ((s = begin(p, beta, L, st, c))) return s;
+  if (L.on_tc && !((uintptr_t)o & 15)) return status_of(tc_fwd(c, o, ht, (char *)p->workspace + L.tc));
   return status_of(simt_scan(c, o, ht, nullptr));
 }
 

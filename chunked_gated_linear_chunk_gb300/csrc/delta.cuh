@@ -35,6 +35,31 @@ struct Call {
   cudaStream_t st;
 };
 
+// The chunk in a slot: its document d and tokens [tok, tok + len).  False: an
+// unused slot (behind the last document's).
+__device__ __forceinline__ bool chunk_in_slot(const Docs &docs, int64_t slot, int64_t &tok, int &len) {
+  int64_t d, j;
+  if (docs.cbase) {
+    if (slot >= docs.cbase[docs.n]) return false;
+    int64_t lo = 0, hi = docs.n;  // cbase[lo] <= slot < cbase[hi]
+    while (hi - lo > 1) {
+      const int64_t m = (lo + hi) >> 1;
+      if (docs.cbase[m] <= slot) lo = m; else hi = m;
+    }
+    d = lo;
+    j = slot - docs.cbase[d];
+  } else {
+    const int64_t per = (docs.T + C - 1) / C;
+    d = slot / per;
+    j = slot - d * per;
+  }
+  int64_t s0, s1;
+  docs.range(d, s0, s1);
+  tok = s0 + j * C;
+  len = (int)min((int64_t)C, s1 - tok);
+  return true;
+}
+
 // Scratch of the backward, all fp32: states before and state gradients after
 // every chunk [slots, H, K, V], E and dR of every token [BT, H, V].
 struct Saved {
@@ -54,6 +79,11 @@ cudaError_t simt_grads(const Call &c, const void *dO, const Saved &saved, void *
                        float *dbeta);
 // out [BT, Hqk, K] dtype = sums of x [BT, H, K] fp32 over the heads of a group.
 cudaError_t reduce_heads(const Call &c, const float *x, void *out);
+
+// ---- tensor-core kernels (delta_tc.cu): bf16, K and V multiples of 8 up to 128 ----
+bool tc_supported(const glacore_problem *p);  // sizes, strides and addresses of q, k, v
+size_t tc_workspace(int64_t slots, int64_t H, bool backward);
+cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws);
 
 // ---- token by token on a pool of states (delta_step.cu) -------------------
 cudaError_t launch_step(const glacore_problem *p, const float *beta, float *state, int64_t n_slots,

@@ -338,26 +338,9 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
   GradSmem &s = *reinterpret_cast<GradSmem *>(smem_raw);
   const int h = (int)(blockIdx.x % a.H);
   const int64_t slot = blockIdx.x / a.H;
-  // the document of the chunk slot
-  int64_t d, j;
-  if (a.docs.cbase) {
-    if (slot >= a.docs.cbase[a.docs.n]) return;
-    int64_t lo = 0, hi = a.docs.n;  // cbase[lo] <= slot < cbase[hi]
-    while (hi - lo > 1) {
-      const int64_t m = (lo + hi) >> 1;
-      if (a.docs.cbase[m] <= slot) lo = m; else hi = m;
-    }
-    d = lo;
-    j = slot - a.docs.cbase[d];
-  } else {
-    const int64_t per = (a.docs.T + C - 1) / C;
-    d = slot / per;
-    j = slot - d * per;
-  }
-  int64_t s0, s1;
-  a.docs.range(d, s0, s1);
-  const int64_t tok0 = s0 + j * C;
-  const int L = (int)min((int64_t)C, s1 - tok0);
+  int64_t tok0;
+  int L;
+  if (!chunk_in_slot(a.docs, slot, tok0, L)) return;
   const int hq = h / a.share;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const T *q = a.q + (int64_t)hq * a.K, *k = a.k + (int64_t)hq * a.K;
