@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
 #pragma unroll
       for (int c0 = 0; c0 < 32; c0 += 8) {
         uint32_t hi[4], lo[4];
-        float z[8];
+        alignas(16) float z[8];
         *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(&s.Z[row][c1 + c0]);
         *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(&s.Z[row][c1 + c0 + 4]);
 #pragma unroll
@@ -315,20 +315,34 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
 // transposed, value column v in lane v of tensor memory, so that every
 // elementwise step belongs to one thread and no operand that the chain makes
 // goes through shared memory:
-//     X^T  = S^T k^T             A: S^T (hi, lo), B: k    -> Y = v - e^G X, R = b Y
-//     E^T  = Y^T + R^T Z^T       A: R^T (hi, lo), B: Z    -> U = b E, U' = e^{G_C - G} U
+//     X^T  = S^T k^T                 A: S^T (hi, lo), B: k    -> Y = v - e^G X, R = b Y
+//     E^T  = Y^T + R^T Z^T           A: R^T (hi, lo), B: Z    -> U = b E, U' = e^{G_C - G} U
 //     S'^T = e^{G_C} S^T + U'^T k    A: U'^T (hi, lo), B: k (as rows of the contraction)
 //     O^T  = scale e^G (S^T q^T) + U^T P^T
-// 256 threads of 8 warps compute: thread (lane v, half w) holds 64 of the
-// state's key rows of its column and 32 of the chunk's tokens; one thread of a ninth warp issues
-// copies and products.  Three exchanges per chunk are in sequence (X, E, S');
-// S^T q^T runs while R is made, U^T P^T while the state is updated, and o is
-// stored while the next X runs.
-// TMEM columns: [0, 128) S^T as hi / lo of rows 0..63, hi / lo of rows 64..127;
-// the same columns take U'^T k, once X and S^T q^T have read S.
+// Three products and three elementwise steps per chunk are in sequence, and
+// the kernel is bound by that sequence: one block per (document, head), about
+// half of a chunk's time in the products (a product of N <= 128 columns takes
+// the tensor core the time of 128).  So S^T q^T shares X's instructions (B: [k; q], 128
+// rows), U^T P^T runs where the sequence leaves the tensor core idle, and the
+// output has warps of its own.
+//   warps 0..15  the chain: lanes of quarter w % 4, group w / 4 holds 32 of the
+//                state's key rows and 16 of the chunk's tokens (of its column v)
+//   warps 16..19 the output (STATES: one thread that stores images)
+//   warp 20      copies and products, one thread
+// TMEM columns: [0, 128) S^T, per group of 32 rows 16 columns of hi and 16 of
+// lo; the same columns take U'^T k once X and S^T q^T have read S.  [128, 384)
+// [X | S^T q^T] of even and odd chunks; E^T and then U^T P^T take X's place.  [384, 448)
+// R, then U'; [448, 512) U.
+// STATES (the backward's first pass) has no q, P and o; it saves the state before
+// every chunk and E as the images that delta_grads_kernel multiplies with.
 // ---------------------------------------------------------------------------
-constexpr uint32_t T_S = 0, T_X = 128, T_QS = 192, T_R = 256, T_U2 = 320, T_U = 384, T_PU = 448;
-constexpr uint32_t T_R3 = T_U2;  // R's third part, until U' is made
+constexpr uint32_t T_S = 0, T_XQ = 128, T_R = 384, T_U = 448;
+constexpr uint32_t T_R3 = T_S;  // R's third part, between X and the new state
+
+// Images: rows of a value column v, 64 columns (channels of a block, or
+// tokens) to a row of 128 bytes, 128-byte swizzle.
+constexpr uint32_t S_IMAGE = 4 * 16384;  // [hi, lo][two blocks of 64 channels][128 rows]
+constexpr uint32_t E_IMAGE = 2 * 16384;  // [hi, lo][128 rows]
 
 struct ChainMaps {
   CUtensorMap q, k, v;
@@ -342,23 +356,64 @@ struct ChainArgs {
   __nv_bfloat16 *o;
   const char *tiles;
   const float *gates;
+  char *s_images, *e_images;  // STATES
   int *err;
 };
-namespace cs {  // shared memory: two stages, the output tile
-constexpr uint32_t KQ = 0, V = 32768, ZP = 49152, GT = 90112, STAGE = 91136;  // GT: 1 KB
-constexpr uint32_t STAGES = 2;
-constexpr uint32_t O = STAGES * STAGE;  // 16 KB
-constexpr uint32_t BYTES = O + 16384 + 1024;
-}  // namespace cs
-static_assert(cs::STAGE % 1024 == 0 && cs::O % 1024 == 0, "tiles are 1024-byte aligned");
-constexpr int CHAIN_THREADS = 288;
 
+// Shared memory: two stages of k, (q), v, Z, gates; three of P; the output
+// tile, or the two images.
+template <bool STATES>
+struct ChainSmem {
+  static constexpr uint32_t KQ = 0, V = STATES ? 16384 : 32768, Z = V + 16384, GT = Z + 3 * TILE, STAGE = GT + 1024;
+  static constexpr uint32_t P = 2 * STAGE, OUT = P + (STATES ? 0 : 3 * 2 * TILE);
+  static constexpr uint32_t BYTES = OUT + (STATES ? S_IMAGE + E_IMAGE : 16384) + 1024;
+  static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BYTES <= 227 * 1024, "");
+};
+constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = 672;
+
+__device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// A warp's arrival, after what its lanes did (with their fences) is done: one
+// arrival instead of 32 that would queue for the barrier.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+// columns of K-step ks of S^T's hi part; lo: 16 further
+__device__ __forceinline__ uint32_t s_col(uint32_t tb, int ks) {
+  return tb + T_S + (uint32_t)(ks >> 1) * 32u + (uint32_t)(ks & 1) * 8u;
+}
+// 32 values of a column as hi and lo parts, into tensor memory and, with IMG,
+// into the image row `row` (at `img`, lo a half further) from column c0 on.
+template <bool IMG>
+__device__ __forceinline__ void put_state(uint32_t at, const float (&S)[32], uint8_t *img, int row, int c0) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) split2(S[2 * i], S[2 * i + 1], hi[i], lo[i]);
+  tmem_st16(at, hi);
+  tmem_st16(at + 16, lo);
+  if (IMG) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t o = smem_u32(img) + sw128_off(row, c0 + 8 * i, 128);
+      st_shared_v4(o, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      st_shared_v4(o + S_IMAGE / 2, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+    }
+  }
+}
+
+template <bool STATES>
 __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __grid_constant__ ChainMaps maps,
                                                                        const ChainArgs a) {
-  using namespace cs;
+  using L_ = ChainSmem<STATES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[STAGES], s_ready, x_full, r_ready, e_full, u_ready, s_full, pu_full, o_free, drain;
+  __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, pu_full[2], o_free[2], drain;
+  __shared__ uint64_t si_ready, si_free, ei_ready, ei_free;
+  __shared__ alignas(16) float o_into[2][CH];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -371,22 +426,19 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
   auto chunk_tok = [&](int j) -> int64_t { return s0 + (int64_t)j * CH; };
   auto chunk_len = [&](int j) -> int { return (int)min((int64_t)CH, s1 - chunk_tok(j)); };
 
-  if (warp == 8) {
+  if (warp == 20) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (uint32_t i = 0; i < STAGES; ++i) mbar_init(&full[i], 1);
-    mbar_init(&x_full, 1);
-    mbar_init(&e_full, 1);
-    mbar_init(&s_full, 1);
-    mbar_init(&pu_full, 1);
-    mbar_init(&drain, 1);
-    mbar_init(&s_ready, 256);
-    mbar_init(&r_ready, 256);
-    mbar_init(&u_ready, 256);
-    mbar_init(&o_free, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&pu_full[i], 1);
+      mbar_init(&o_free[i], 4);
+    }
+    for (uint64_t *b : {&x_full, &e_full, &s_full, &drain, &si_free, &ei_free}) mbar_init(b, 1);
+    for (uint64_t *b : {&s_ready, &r_ready, &u_ready, &si_ready, &ei_ready}) mbar_init(b, CHAIN_WARPS);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -394,8 +446,10 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
   tc_fence_after();
   const uint32_t tb = tmem_base;
   const uint32_t sb = smem_u32(sm);
+  auto stage = [&](int j) -> uint32_t { return (uint32_t)(j & 1) * L_::STAGE; };
+  auto wait_full = [&](int j) -> bool { return mbar_wait(&full[j & 1], (uint32_t)(j >> 1) & 1u, WAIT_CYCLES); };
 
-  if (warp == 8) {
+  if (warp == 20) {
     if (lane == 0) {
       const int hq = h / a.share;
       tma_prefetch_desc(&maps.q);
@@ -406,268 +460,332 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
       auto wide_of = [&](int j) -> float { return j < nch ? ldg_early(a.gates + ((slot0 + j) * a.H + h) * GATES + G_WIDE) : 0.f; };
       float wide_next = wide_of(0);
       auto load = [&](int j) {
-        const uint32_t st = (uint32_t)j % STAGES;
-        uint8_t *p = sm + st * STAGE;
+        uint8_t *p = sm + stage(j);
+        uint64_t *bar = &full[j & 1];
         const int tok = (int)chunk_tok(j);
         const bool wide = wide_next != 0.f;
         wide_next = wide_of(j + 1);
-        mbar_expect_tx(&full[st], wide ? STAGE : STAGE - TILE);
-        tma_load_3d(p + KQ, &maps.k, 0, hq, tok, &full[st]);
-        tma_load_3d(p + KQ + 8192, &maps.q, 0, hq, tok, &full[st]);
-        tma_load_3d(p + KQ + 16384, &maps.k, 64, hq, tok, &full[st]);
-        tma_load_3d(p + KQ + 24576, &maps.q, 64, hq, tok, &full[st]);
-        tma_load_3d(p + V, &maps.v, 0, h, tok, &full[st]);
-        tma_load_3d(p + V + 8192, &maps.v, 64, h, tok, &full[st]);
+        mbar_expect_tx(bar, (STATES ? 2 : 3) * 16384 + (STATES ? 2 : 4) * TILE + (wide ? TILE : 0) + GATES * 4);
+        if (STATES) {
+          tma_load_3d(p + L_::KQ, &maps.k, 0, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 8192, &maps.k, 64, hq, tok, bar);
+        } else {
+          tma_load_3d(p + L_::KQ, &maps.k, 0, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 8192, &maps.q, 0, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 16384, &maps.k, 64, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 24576, &maps.q, 64, hq, tok, bar);
+        }
+        tma_load_3d(p + L_::V, &maps.v, 0, h, tok, bar);
+        tma_load_3d(p + L_::V + 8192, &maps.v, 64, h, tok, bar);
         const int64_t sh = (slot0 + j) * a.H + h;
-        bulk_load(p + ZP, a.tiles + sh * TILES, wide ? TILES : 4 * TILE, &full[st]);
-        bulk_load(p + GT, a.gates + sh * GATES, GATES * 4, &full[st]);
+        bulk_load(p + L_::Z, a.tiles + sh * TILES, 2 * TILE, bar);
+        if (wide) bulk_load(p + L_::Z + 2 * TILE, a.tiles + sh * TILES + 4 * TILE, TILE, bar);
+        if (!STATES) bulk_load(sm + L_::P + (uint32_t)(j % 3) * 2 * TILE, a.tiles + sh * TILES + 2 * TILE, 2 * TILE, bar);
+        bulk_load(p + L_::GT, a.gates + sh * GATES, GATES * 4, bar);
         loaded = j + 1;
       };
-      constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), idS = idesc_bf16(128, 128, false, true);
-      // columns of K-step ks of S^T (hi), of a 64-token operand
-      auto sA = [&](int ks) { return tb + T_S + (uint32_t)(ks >> 2) * 64u + (uint32_t)(ks & 3) * 8u; };
+      constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), id128 = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, true);
+      constexpr uint32_t KROWS = STATES ? 64 : 128;  // rows of a 64-channel block of [k; q]
+      // U^T P^T of chunk j: hi hi, then the rest
+      auto pu = [&](int j, bool rest) {
+        const uint32_t D = tb + T_XQ + (uint32_t)(j & 1) * 128u, p = sb + L_::P + (uint32_t)(j % 3) * 2 * TILE;
+        if (!rest) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_U + 8u * ks, kdesc(p, ks, 64), id64, ks);
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_U + 32u + 8u * ks, kdesc(p, ks, 64), id64, 1);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_U + 8u * ks, kdesc(p + TILE, ks, 64), id64, 1);
+          mma_commit(&pu_full[j & 1]);
+        }
+      };
       bool ok = true;
-      for (int j = 0; j < nch && j < (int)STAGES - 1; ++j) load(j);
-      for (int j = 0; ok && j < nch; ++j) {
-        const uint32_t st = (uint32_t)j % STAGES, ph = (uint32_t)j & 1u;
-        const uint32_t k = sb + st * STAGE + KQ, q = k + 8192, z = sb + st * STAGE + ZP, p = z + 2 * TILE;
-        ok = ok && mbar_wait(&full[st], (uint32_t)(j / (int)STAGES) & 1u, WAIT_CYCLES) &&
-             mbar_wait(&s_ready, ph, WAIT_CYCLES);
+      if (nch > 0) load(0);
+      for (int j = 0; j < nch; ++j) {
+        const uint32_t ph = (uint32_t)j & 1u, D = tb + T_XQ + ph * 128u;
+        const uint32_t k = sb + stage(j) + L_::KQ, z = sb + stage(j) + L_::Z;
+        ok = wait_full(j) && mbar_wait(&s_ready, ph, WAIT_CYCLES);
+        // the output has read this buffer's last values
+        if (ok && !STATES && j >= 2) ok = mbar_wait(&o_free[ph], (uint32_t)((j - 2) >> 1) & 1u, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + T_X, sA(ks), kdesc(k, ks, 128), id64, ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(D, s_col(tb, ks), kdesc(k, ks, KROWS), STATES ? id64 : id128, ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + T_X, sA(ks) + 32u, kdesc(k, ks, 128), id64, 1);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(D, s_col(tb, ks) + 16u, kdesc(k, ks, KROWS), STATES ? id64 : id128, 1);
         mma_commit(&x_full);
-        // chunk j - 1 is done with its stage and with S^T q^T and U^T P^T
-        if (j >= 1) ok = mbar_wait(&o_free, (uint32_t)(j - 1) & 1u, WAIT_CYCLES);
-        if (!ok) break;
-        tc_fence_after();
+        // chunk j - 1 is through with its stage (its last product with k before s_ready), j - 2 with its P
         if (j + 1 < nch) load(j + 1);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + T_QS, sA(ks), kdesc(q, ks, 128), id64, ks);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + T_QS, sA(ks) + 32u, kdesc(q, ks, 128), id64, 1);
+        if (!STATES && j >= 1) pu(j - 1, true);
         ok = mbar_wait(&r_ready, ph, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_X, tb + T_R + 8u * ks, kdesc(z, ks, 64), id64, ks);
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_R + 8u * ks, kdesc(z, ks, 64), id64, ks);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_X, tb + T_R + 32u + 8u * ks, kdesc(z, ks, 64), id64, 1);
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_R + 32u + 8u * ks, kdesc(z, ks, 64), id64, 1);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_X, tb + T_R + 8u * ks, kdesc(z + TILE, ks, 64), id64, 1);
-        if (lds_f1(sb + st * STAGE + GT + 4u * G_WIDE) != 0.f) {
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_R + 8u * ks, kdesc(z + TILE, ks, 64), id64, 1);
+        if (lds_f1(sb + stage(j) + L_::GT + 4u * G_WIDE) != 0.f) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_bf16_ta(tb + T_X, tb + T_R + 32u + 8u * ks, kdesc(z + TILE, ks, 64), id64, 1);
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_R + 32u + 8u * ks, kdesc(z + TILE, ks, 64), id64, 1);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_X, tb + T_R3 + 8u * ks, kdesc(z, ks, 64), id64, 1);
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_R3 + 8u * ks, kdesc(z, ks, 64), id64, 1);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_X, tb + T_R + 8u * ks, kdesc(z + 4 * TILE, ks, 64), id64, 1);
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(D, tb + T_R + 8u * ks, kdesc(z + 2 * TILE, ks, 64), id64, 1);
         }
         mma_commit(&e_full);
         ok = mbar_wait(&u_ready, ph, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_S, tb + T_U2 + 8u * ks, mdesc(k, ks, 16384), idS, ks);
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_ta(tb + T_S, tb + T_R + 8u * ks, mdesc(k, ks, KROWS * 128u), idS, ks);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_S, tb + T_U2 + 32u + 8u * ks, mdesc(k, ks, 16384), idS, 1);
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_ta(tb + T_S, tb + T_R + 32u + 8u * ks, mdesc(k, ks, KROWS * 128u), idS, 1);
         mma_commit(&s_full);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_PU, tb + T_U + 8u * ks, kdesc(p, ks, 64), id64, ks);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_PU, tb + T_U + 32u + 8u * ks, kdesc(p, ks, 64), id64, 1);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + T_PU, tb + T_U + 8u * ks, kdesc(p + TILE, ks, 64), id64, 1);
-        mma_commit(&pu_full);
+        if (!STATES) pu(j, false);
       }
+      if (!STATES && ok && nch > 0) pu(nch - 1, true);
       // no copy or product of this block is in flight when it leaves
-      for (int j = max(0, loaded - (int)STAGES); j < loaded; ++j)
-        if (!mbar_wait(&full[j % (int)STAGES], (uint32_t)(j / (int)STAGES) & 1u, WAIT_CYCLES)) ok = false;
+      for (int j = max(0, loaded - 2); j < loaded; ++j)
+        if (!wait_full(j)) ok = false;
       mma_commit(&drain);
       if (!mbar_wait(&drain, 0, WAIT_CYCLES)) ok = false;
       if (!ok) atomicExch(&abort_flag, 1);
     }
     __syncwarp();
-  } else {
-    const int w = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
-    const uint32_t lo = (uint32_t)(qw * 32) << 16;  // this warp's lanes of tensor memory
+  } else if (warp < CHAIN_WARPS) {
+    const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;  // this warp's lanes of tensor memory
     const bool in = v < a.V;
-    float S[64];
+    uint8_t *s_img = sm + L_::OUT, *e_img = sm + L_::OUT + S_IMAGE;
+    float S[32];
     {
-      const float *src = a.h0 && in ? a.h0 + ((d * a.H + h) * a.K + 64 * w) * (int64_t)a.V + v : nullptr;
+      const int64_t at = ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
 #pragma unroll
-      for (int i = 0; i < 64; ++i) S[i] = src && 64 * w + i < a.K ? src[(int64_t)i * a.V] : 0.f;
+      for (int i = 0; i < 32; ++i) S[i] = a.h0 && in && 32 * grp + i < a.K ? a.h0[at + (int64_t)i * a.V] : 0.f;
     }
-    // S^T's hi and lo parts into tensor memory
-    auto put_state = [&]() {
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t hi[16], l[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) split2(S[c + 2 * i], S[c + 2 * i + 1], hi[i], l[i]);
-        tmem_st16(tb + lo + T_S + 64u * w + c / 2, hi);
-        tmem_st16(tb + lo + T_S + 64u * w + 32u + c / 2, l);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-    };
     // Rows past the document's end hold other tokens: as zeros, nothing in them reaches a sum.
     auto clear_rows = [&](int j) -> bool {
       const int L = chunk_len(j);
       if (L == CH) return true;
-      const uint32_t st = (uint32_t)j % STAGES;
-      if (!mbar_wait(&full[st], (uint32_t)(j / (int)STAGES) & 1u, WAIT_CYCLES)) return false;
-      const int tid = threadIdx.x;
-      for (int i = tid; i < (CH - L) * 48; i += 256) {  // rows of k, q (two blocks each) and v (two)
-        const int r = L + i / 48, c = i % 48, b = c / 8;
-        const uint32_t base = sb + st * STAGE + (b < 4 ? KQ + b * 8192u : V + (b - 4) * 8192u);
-        st_shared_v4(base + r * 128u + (c % 8) * 16u, 0u, 0u, 0u, 0u);
+      if (!wait_full(j)) return false;
+      constexpr int BLOCKS = STATES ? 4 : 6;  // tiles of 64 rows: k, (q), v
+      for (int i = threadIdx.x; i < (CH - L) * BLOCKS * 8; i += 32 * CHAIN_WARPS) {
+        const int c = i % 8, b = i / 8 % BLOCKS, r = L + i / (8 * BLOCKS);
+        st_shared_v4(sb + stage(j) + b * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
       }
       fence_async_smem();
       return true;
     };
-    put_state();
-    bool ok = nch == 0 || clear_rows(0);
-    mbar_arrive(&s_ready);
-    for (int j = 0; j < nch; ++j) {
-      const uint32_t st = (uint32_t)j % STAGES, ph = (uint32_t)j & 1u;
-      const uint8_t *sp = sm + st * STAGE;
-      const float *gs = reinterpret_cast<const float *>(sp + GT);
-      float Y[32];
-      ok = ok && mbar_wait(&full[st], (uint32_t)(j / (int)STAGES) & 1u, WAIT_CYCLES);
-      {
-        const ColBf16 col(smem_u32(sp + V), 32 * w, v);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) Y[i] = bf16_bits_to_f32(lds_u16(col.at(i)));
+    bool ok = true;
+    // the state before chunk j, handed to the products
+    auto hand_state = [&](int j) {
+      if (STATES && j >= 1) ok = ok && mbar_wait(&si_free, (uint32_t)(j - 1) & 1u, WAIT_CYCLES);
+      put_state<STATES>(tb + lanes + T_S + 32u * grp, S, s_img, v, 32 * grp);
+      tmem_st_wait();
+      tc_fence_before();
+      ok = ok && clear_rows(j);
+      warp_arrive(&s_ready);
+      if (STATES) {
+        fence_async_smem();
+        warp_arrive(&si_ready);
       }
+    };
+    if (nch > 0) hand_state(0);
+    for (int j = 0; j < nch; ++j) {
+      const uint32_t ph = (uint32_t)j & 1u, D = tb + lanes + T_XQ + ph * 128u + 16u * grp;
+      const float *gates = reinterpret_cast<const float *>(sm + stage(j) + L_::GT);
+      const float4 *into = reinterpret_cast<const float4 *>(gates + G_INTO + 16 * grp);
+      const float4 *out = reinterpret_cast<const float4 *>(gates + G_OUT + 16 * grp);
+      const float4 *beta = reinterpret_cast<const float4 *>(gates + G_BETA + 16 * grp);
+      float Y[16];
+      ok = ok && wait_full(j);
+      {
+        const ColBf16 col(sb + stage(j) + L_::V, 16 * grp, v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) Y[i] = bf16_bits_to_f32(lds_u16(col.at(i)));
+      }
+      const bool wide = gates[G_WIDE] != 0.f;
       ok = ok && mbar_wait(&x_full, ph, WAIT_CYCLES);
       tc_fence_after();
       {
-        uint32_t x[32];
-        tmem_ld32(tb + lo + T_X + 32u * w, x);
-        tmem_ld_wait32(x);
-        uint32_t hi[16], l[16];
+        uint32_t x[16];
+        tmem_ld16(D, x);
+        tmem_ld_wait(x);
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 e = lds_f4(smem_u32(gs + G_INTO + 32 * w + i)), b = lds_f4(smem_u32(gs + G_BETA + 32 * w + i));
+        for (int i = 0; i < 16; i += 4) {
+          const float4 e = into[i / 4], b = beta[i / 4];
           Y[i] = fmaf(-e.x, __uint_as_float(x[i]), Y[i]);
           Y[i + 1] = fmaf(-e.y, __uint_as_float(x[i + 1]), Y[i + 1]);
           Y[i + 2] = fmaf(-e.z, __uint_as_float(x[i + 2]), Y[i + 2]);
           Y[i + 3] = fmaf(-e.w, __uint_as_float(x[i + 3]), Y[i + 3]);
-          split2(b.x * Y[i], b.y * Y[i + 1], hi[i / 2], l[i / 2]);
-          split2(b.z * Y[i + 2], b.w * Y[i + 3], hi[i / 2 + 1], l[i / 2 + 1]);
+          split2(b.x * Y[i], b.y * Y[i + 1], hi[i / 2], lo[i / 2]);
+          split2(b.z * Y[i + 2], b.w * Y[i + 3], hi[i / 2 + 1], lo[i / 2 + 1]);
         }
-        tmem_st16(tb + lo + T_R + 16u * w, hi);
-        tmem_st16(tb + lo + T_R + 32u + 16u * w, l);
-        if (lds_f1(smem_u32(gs + G_WIDE)) != 0.f) {
-          uint32_t l3[16];
+        tmem_st8(tb + lanes + T_R + 8u * grp, hi);
+        tmem_st8(tb + lanes + T_R + 32u + 8u * grp, lo);
+        if (wide) {
+          uint32_t l3[8];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float b0 = lds_f1(smem_u32(gs + G_BETA + 32 * w + i)), b1 = lds_f1(smem_u32(gs + G_BETA + 32 * w + i + 1));
-            l3[i / 2] = split3(b0 * Y[i], b1 * Y[i + 1], hi[i / 2], l[i / 2]);
+          for (int i = 0; i < 16; i += 4) {
+            const float4 b = beta[i / 4];
+            l3[i / 2] = split3(b.x * Y[i], b.y * Y[i + 1], hi[i / 2], lo[i / 2]);
+            l3[i / 2 + 1] = split3(b.z * Y[i + 2], b.w * Y[i + 3], hi[i / 2 + 1], lo[i / 2 + 1]);
           }
-          tmem_st16(tb + lo + T_R3 + 16u * w, l3);
+          tmem_st8(tb + lanes + T_R3 + 8u * grp, l3);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&r_ready);
+        warp_arrive(&r_ready);
       }
       ok = ok && mbar_wait(&e_full, ph, WAIT_CYCLES);
       tc_fence_after();
       {
-        uint32_t x[32];
-        tmem_ld32(tb + lo + T_X + 32u * w, x);
-        tmem_ld_wait32(x);
-        uint32_t hi[16], l[16], hi2[16], l2[16];
+        uint32_t x[16];
+        tmem_ld16(D, x);
+        tmem_ld_wait(x);
+        uint32_t hi[8], lo[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 b = lds_f4(smem_u32(gs + G_BETA + 32 * w + i)), r = lds_f4(smem_u32(gs + G_OUT + 32 * w + i));
-          const float u0 = b.x * (Y[i] + __uint_as_float(x[i])), u1 = b.y * (Y[i + 1] + __uint_as_float(x[i + 1]));
-          const float u2 = b.z * (Y[i + 2] + __uint_as_float(x[i + 2])), u3 = b.w * (Y[i + 3] + __uint_as_float(x[i + 3]));
-          split2(u0, u1, hi[i / 2], l[i / 2]);
-          split2(u2, u3, hi[i / 2 + 1], l[i / 2 + 1]);
-          split2(r.x * u0, r.y * u1, hi2[i / 2], l2[i / 2]);
-          split2(r.z * u2, r.w * u3, hi2[i / 2 + 1], l2[i / 2 + 1]);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 b = beta[i / 4], r = out[i / 4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) Y[i + n] += __uint_as_float(x[i + n]);
+          split2(r.x * (b.x * Y[i]), r.y * (b.y * Y[i + 1]), hi[i / 2], lo[i / 2]);
+          split2(r.z * (b.z * Y[i + 2]), r.w * (b.w * Y[i + 3]), hi[i / 2 + 1], lo[i / 2 + 1]);
         }
-        tmem_st16(tb + lo + T_U2 + 16u * w, hi2);
-        tmem_st16(tb + lo + T_U2 + 32u + 16u * w, l2);
-        tmem_st16(tb + lo + T_U + 16u * w, hi);
-        tmem_st16(tb + lo + T_U + 32u + 16u * w, l);
+        tmem_st8(tb + lanes + T_R + 8u * grp, hi);
+        tmem_st8(tb + lanes + T_R + 32u + 8u * grp, lo);
+        if (!STATES) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 b = beta[i / 4];
+            split2(b.x * Y[i], b.y * Y[i + 1], hi[i / 2], lo[i / 2]);
+            split2(b.z * Y[i + 2], b.w * Y[i + 3], hi[i / 2 + 1], lo[i / 2 + 1]);
+          }
+          tmem_st8(tb + lanes + T_U + 8u * grp, hi);
+          tmem_st8(tb + lanes + T_U + 32u + 8u * grp, lo);
+        }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&u_ready);
+        warp_arrive(&u_ready);
+        if (STATES) {  // E
+          if (j >= 1) ok = ok && mbar_wait(&ei_free, (uint32_t)(j - 1) & 1u, WAIT_CYCLES);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) split2(Y[i], Y[i + 1], hi[i / 2], lo[i / 2]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t o = smem_u32(e_img) + sw128_off(v, 16 * grp + 8 * i, 128);
+            st_shared_v4(o, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            st_shared_v4(o + E_IMAGE / 2, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          }
+          fence_async_smem();
+          warp_arrive(&ei_ready);
+        }
       }
+      const float over = gates[G_OVER];
       ok = ok && mbar_wait(&s_full, ph, WAIT_CYCLES);
       tc_fence_after();
       {
-        const float over = lds_f1(smem_u32(gs + G_OVER));
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          uint32_t x[32];
-          tmem_ld32(tb + lo + T_S + 64u * w + c, x);
-          tmem_ld_wait32(x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) S[c + i] = fmaf(over, S[c + i], __uint_as_float(x[i]));
-        }
-        if (j + 1 < nch) {
-          put_state();
-          ok = ok && clear_rows(j + 1);
-          mbar_arrive(&s_ready);
-        }
-      }
-      // o of the chunk, while the next X runs
-      ok = ok && mbar_wait(&pu_full, ph, WAIT_CYCLES);
-      tc_fence_after();
-      {
-        uint32_t x[32], p[32];
-        tmem_ld32(tb + lo + T_QS + 32u * w, x);
-        tmem_ld32(tb + lo + T_PU + 32u * w, p);
+        uint32_t x[32];
+        tmem_ld32(tb + lanes + T_S + 32u * grp, x);
         tmem_ld_wait32(x);
-        tmem_ld_wait32(p);
-        const ColBf16 col(smem_u32(sm + O), 32 * w, v);
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const float4 e = lds_f4(smem_u32(gs + G_INTO + 32 * w + i));
-          const float f[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-            sts_u16(col.at(i + n),
-                    f32_to_bf16_bits(fmaf(a.scale * f[n], __uint_as_float(x[i + n]), __uint_as_float(p[i + n]))));
-        }
-        tc_fence_before();
-        mbar_arrive(&o_free);
+        for (int i = 0; i < 32; ++i) S[i] = fmaf(over, S[i], __uint_as_float(x[i]));
       }
-      // the 256 threads leave together: the barrier tells everyone of a wait that ran out
-      if (named_bar_any(1, 256, !ok)) {
+      if (j + 1 < nch) hand_state(j + 1);
+    }
+    if (!ok) atomicExch(&abort_flag, 1);
+    if (a.ht && in && ok) {
+      float *dst = a.ht + ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
+    }
+  } else if (STATES) {
+    if (warp == CHAIN_WARPS && lane == 0) {  // the images leave, the state's and E's in turn
+      bool ok = true;
+      for (int j = 0; j < nch && ok; ++j) {
+        const uint32_t ph = (uint32_t)j & 1u;
+        const int64_t sh = (slot0 + j) * a.H + h;
+        ok = mbar_wait(&si_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        bulk_store(a.s_images + sh * S_IMAGE, sm + L_::OUT, S_IMAGE);
+        bulk_commit();
+        if (j >= 1) {  // E of the chunk before has been read
+          bulk_wait_read_all_but_one();
+          mbar_arrive(&ei_free);
+        }
+        ok = mbar_wait(&ei_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        bulk_store(a.e_images + sh * E_IMAGE, sm + L_::OUT + S_IMAGE, E_IMAGE);
+        bulk_commit();
+        bulk_wait_read_all_but_one();
+        mbar_arrive(&si_free);
+      }
+      bulk_wait_all();
+      if (!ok) atomicExch(&abort_flag, 1);
+    }
+    __syncwarp();
+  } else {
+    const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    bool ok = true;
+    for (int j = 0; j < nch; ++j) {
+      const uint32_t ph = (uint32_t)j & 1u, D = tb + lanes + T_XQ + ph * 128u;
+      // e^G of the chunk, kept past its stage (which is full: s_ready of this chunk
+      // waits for nothing of ours, and the next load into it for its own state)
+      ok = ok && wait_full(j);
+      if (tid < CH) o_into[ph][tid] = a.scale * lds_f1(sb + stage(j) + L_::GT + 4u * (G_INTO + tid));
+      ok = ok && mbar_wait(&pu_full[ph], (uint32_t)(j >> 1) & 1u, WAIT_CYCLES);
+      tc_fence_after();
+      // the factors are there, the last tile has been read; everyone hears of a wait that ran out
+      if (named_bar_any(1, 128, !ok)) {
         ok = false;
         break;
       }
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        uint32_t x[16], p[16];
+        tmem_ld16(D + 64u + c, x);
+        tmem_ld16(D + c, p);
+        tmem_ld_wait(x);
+        tmem_ld_wait(p);
+        const ColBf16 col(smem_u32(sm + L_::OUT), c, v);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 e = lds_f4(smem_u32(&o_into[ph][c + i]));
+          const float f[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+          for (int n = 0; n < 4; ++n)
+            sts_u16(col.at(i + n), f32_to_bf16_bits(fmaf(f[n], __uint_as_float(x[i + n]), __uint_as_float(p[i + n]))));
+        }
+      }
+      tc_fence_before();
+      warp_arrive(&o_free[ph]);
+      named_bar(2, 128);
       const int L = chunk_len(j);
       __nv_bfloat16 *dst = a.o + (chunk_tok(j) * a.H + h) * (int64_t)a.V;
-      for (int i = threadIdx.x; i < CH * 16; i += 256) {
-        const int r = i >> 4, c = (i & 15) * 8;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int i = tid + 128 * n, r = i >> 4, c = (i & 15) * 8;
         if (r < L && c < a.V) {
-          const uint4 x = lds_u4(smem_u32(sm + O) + sw128_off(r, c, 64));
+          const uint4 x = lds_u4(smem_u32(sm + L_::OUT) + sw128_off(r, c, 64));
           st_global_v4(dst + (int64_t)r * a.H * a.V + c, x.x, x.y, x.z, x.w);
         }
       }
     }
     if (!ok) atomicExch(&abort_flag, 1);
-    if (a.ht && in && ok) {
-      float *dst = a.ht + ((d * a.H + h) * a.K + 64 * w) * (int64_t)a.V + v;
-#pragma unroll
-      for (int i = 0; i < 64; ++i)
-        if (64 * w + i < a.K) dst[(int64_t)i * a.V] = S[i];
-    }
   }
   tc_fence_before();
   __syncthreads();
   if (threadIdx.x == 0 && *(volatile int *)&abort_flag) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
-  if (warp == 8) {
+  if (warp == 20) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
@@ -737,9 +855,11 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
   a.tiles = tiles;
   a.gates = gates;
   a.err = c.p.err;
-  e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, cs::BYTES);
+  a.s_images = a.e_images = nullptr;
+  constexpr uint32_t smem = ChainSmem<false>::BYTES;
+  e = cudaFuncSetAttribute(delta_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  delta_chain_kernel<<<(unsigned)units, CHAIN_THREADS, cs::BYTES, c.st>>>(maps, a);
+  delta_chain_kernel<false><<<(unsigned)units, CHAIN_THREADS, smem, c.st>>>(maps, a);
   mark_launch("delta_chain", c.st);
   return cudaGetLastError();
 }
