@@ -41,10 +41,16 @@ constexpr int G_WIDE = 193;                     // 1: Z (b Y) is to be taken in 
 constexpr float WIDE = 16.f;
 constexpr int NP = 68;                          // row pitch of the fp32 64 x 64 matrices
 
-// hi and lo parts of two neighbours, packed
+// hi and lo parts of two neighbours, packed.  What hi leaves is a product with
+// -1 of the packed half itself, added to the fp32 value.
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  float ra, rb;
   hi = pack_bf16(a, b);
-  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
+  asm("{\n .reg .b16 x, y, m;\n mov.b32 {x, y}, %2;\n mov.b16 m, 0xBF80;\n fma.rn.f32.bf16 %0, x, m, %3;\n"
+      " fma.rn.f32.bf16 %1, y, m, %4;\n}\n"
+      : "=f"(ra), "=f"(rb)
+      : "r"(hi), "f"(a), "f"(b));
+  lo = pack_bf16(ra, rb);
 }
 // what hi and lo leave of them
 __device__ __forceinline__ uint32_t split3(float a, float b, uint32_t hi, uint32_t lo) {
