@@ -39,14 +39,17 @@ Layout layout(const glacore_problem *p, bool backward) {
   // a document's last chunk may be short: at most one more than its tokens fill
   L.slots = p->segment_ids ? std::min(BT, BT / C + n) : p->B * ((p->T + C - 1) / C);
   L.on_tc = tc_supported(p);
-  if (L.on_tc && !backward) take(L.tc, tc_workspace(L.slots, p->H, false));
+  // the scratch of one call serves either family: the addresses of the outputs decide (run_fwd, run_bwd)
+  if (L.on_tc) take(L.tc, tc_workspace(L.slots, p->H, backward));
   if (backward) {
+    if (L.on_tc) off = L.tc;
     const size_t states = sizeof(float) * (size_t)L.slots * p->H * p->K * p->V;
     const size_t rows = sizeof(float) * (size_t)BT * p->H * p->V;
     take(L.s0, states);
     take(L.ds1, states);
     take(L.e, rows);
     take(L.dr, rows);
+    if (L.on_tc) off = std::max(off, L.tc + align256(tc_workspace(L.slots, p->H, true)));
     if (p->Hqk != p->H) {
       take(L.dq, sizeof(float) * (size_t)BT * p->H * p->K);
       take(L.dk, sizeof(float) * (size_t)BT * p->H * p->K);
@@ -128,9 +131,14 @@ glacore_status run_bwd(const glacore_problem *p, const float *beta, const void *
   const Saved saved = {(float *)(ws + L.s0), (float *)(ws + L.ds1), (float *)(ws + L.e), (float *)(ws + L.dr)};
   const bool shared = p->Hqk != p->H;
   void *hq = shared ? (void *)(ws + L.dq) : dq, *hk = shared ? (void *)(ws + L.dk) : dk;
-  cudaError_t e = simt_scan(c, nullptr, nullptr, &saved);
-  if (e == cudaSuccess) e = simt_scan_back(c, dO, dht, dv, dh0, saved);
-  if (e == cudaSuccess) e = simt_grads(c, dO, saved, hq, hk, shared, dg, dbeta);
+  cudaError_t e;
+  if (L.on_tc && !(((uintptr_t)dO | (uintptr_t)dv) & 15)) {
+    e = tc_bwd(c, dO, dht, hq, hk, shared, dv, dg, dbeta, dh0, ws + L.tc);
+  } else {
+    e = simt_scan(c, nullptr, nullptr, &saved);
+    if (e == cudaSuccess) e = simt_scan_back(c, dO, dht, dv, dh0, saved);
+    if (e == cudaSuccess) e = simt_grads(c, dO, saved, hq, hk, shared, dg, dbeta);
+  }
   if (e == cudaSuccess && shared) e = reduce_heads(c, (const float *)hq, dq);
   if (e == cudaSuccess && shared) e = reduce_heads(c, (const float *)hk, dk);
   return status_of(e);

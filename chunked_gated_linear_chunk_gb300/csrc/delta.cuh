@@ -84,6 +84,9 @@ cudaError_t reduce_heads(const Call &c, const float *x, void *out);
 bool tc_supported(const glacore_problem *p);  // sizes, strides and addresses of q, k, v
 size_t tc_workspace(int64_t slots, int64_t H, bool backward);
 cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws);
+// dq and dk as in simt_grads
+cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, void *dk, bool per_head, void *dv, float *dg,
+                   float *dbeta, float *dh0, char *ws);
 
 // ---- token by token on a pool of states (delta_step.cu) -------------------
 cudaError_t launch_step(const glacore_problem *p, const float *beta, float *state, int64_t n_slots,

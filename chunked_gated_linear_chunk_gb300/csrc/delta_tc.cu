@@ -797,26 +797,779 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
   }
 }
 
-inline size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+// ---------------------------------------------------------------------------
+// The same walk backwards, with the gradient of the state: value column v in
+// lane v, per chunk
+//     dU^T  = dO^T (P) + e^{G_C - G} (dS1^T k^T)       A: dO (rows of the contraction), dS1^T; B: P, k
+//     dR^T  = dU^T + (b dU)^T Z                        -> dY = b dR (= dV), dX = -e^G dY
+//     dS0^T = e^{G_C} dS1^T + (scale e^G dO)^T q + dX^T k
+// dO^T P and the product with q do not wait for the chain.  Saved for
+// delta_grads_kernel: dS1 of every chunk (an image as S0's), dR (as rows of a
+// token, [hi, lo][two blocks of 64 columns][64 rows]) and e^{G_C} <S0, dS1>.
+//   warps 0..15  the chain, as in the forward
+//   warps 16..19 scale e^G dO as an operand, dv and dR on their way out
+//   warp 20      copies and products, one thread
+// TMEM columns: [0, 128) dS1^T (hi, lo); [128, 192) dS1^T k^T, then (b dU)^T Z;
+// [192, 256) dO^T P; [256, 320) b dU, then dX; [320, 384) scale e^G dO;
+// [384, 512) the new part of dS0^T.
+// ---------------------------------------------------------------------------
+constexpr uint32_t B_D1 = 128, B_PDO = 192, B_R = 256, B_DO = 320, B_DS = 384;
+constexpr uint32_t R_IMAGE = 2 * 16384;
 
-cudaError_t prep(const Call &c, const PrepMaps &maps, char *tiles, float *gates) {
-  PrepArgs a;
-  a.g = c.p.g;
-  a.beta = c.beta;
-  a.docs = c.docs;
-  a.H = (int)c.p.H;
-  a.Hqk = (int)c.p.Hqk;
-  a.share = a.H / a.Hqk;
-  a.scale = c.p.scale;
-  a.tiles = tiles;
-  a.gates = gates;
-  a.err = c.p.err;
-  cudaError_t e = cudaFuncSetAttribute(delta_prep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PREP_BYTES);
-  if (e != cudaSuccess) return e;
-  delta_prep_kernel<<<(unsigned)(c.slots * c.p.Hqk), 128, PREP_BYTES, c.st>>>(maps, a);
-  mark_launch("delta_prep", c.st);
-  return cudaGetLastError();
+struct BackMaps {
+  CUtensorMap q, k, dO;
+};
+struct BackArgs {
+  Docs docs;
+  int H, share, K, V;
+  float scale;
+  const float *dht;
+  float *dh0;
+  __nv_bfloat16 *dv;
+  const char *tiles;
+  const float *gates;
+  const char *s_images;
+  char *ds_images, *r_images;
+  float *sdot;  // [slot, H]
+  int *err;
+};
+struct BackSmem {
+  static constexpr uint32_t K = 0, Q = 16384, DO = 32768, Z = 49152, P = Z + 2 * TILE, Z3 = P + 2 * TILE, GT = Z3 + TILE,
+                            STAGE = GT + 1024;
+  static constexpr uint32_t R = 2 * STAGE, BYTES = R + R_IMAGE + 1024;
+};
+static_assert(BackSmem::STAGE % 1024 == 0 && BackSmem::BYTES <= 226 * 1024, "");
+
+__global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __grid_constant__ BackMaps maps,
+                                                                      const BackArgs a) {
+  using L_ = BackSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, do_ready, dr_ready, dr_free, drain;
+  __shared__ float w_beta[3][CH], w_dot[2][CHAIN_WARPS];  // of three steps: read behind the next step's barrier
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (int)(blockIdx.x % a.H);
+  const int64_t d = blockIdx.x / a.H;
+  int64_t s0, s1;
+  a.docs.range(d, s0, s1);
+  const int nch = (int)((s1 - s0 + CH - 1) / CH);
+  const int64_t slot0 = a.docs.chunk_base(d);
+  // step i of the walk takes chunk nch - 1 - i
+  auto chunk_tok = [&](int i) -> int64_t { return s0 + (int64_t)(nch - 1 - i) * CH; };
+  auto chunk_len = [&](int i) -> int { return (int)min((int64_t)CH, s1 - chunk_tok(i)); };
+  auto chunk_sh = [&](int i) -> int64_t { return (slot0 + nch - 1 - i) * a.H + h; };
+
+  if (warp == 20) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (uint64_t *b : {&full[0], &full[1], &x_full, &e_full, &s_full, &drain}) mbar_init(b, 1);
+    for (uint64_t *b : {&s_ready, &r_ready, &u_ready, &dr_ready}) mbar_init(b, CHAIN_WARPS);
+    for (uint64_t *b : {&do_ready, &dr_free}) mbar_init(b, 4);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = tmem_base;
+  const uint32_t sb = smem_u32(sm);
+  auto stage = [&](int i) -> uint32_t { return (uint32_t)(i & 1) * L_::STAGE; };
+  auto wait_full = [&](int i) -> bool { return mbar_wait(&full[i & 1], (uint32_t)(i >> 1) & 1u, WAIT_CYCLES); };
+
+  if (warp == 20) {
+    if (lane == 0) {
+      const int hq = h / a.share;
+      tma_prefetch_desc(&maps.q);
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.dO);
+      int loaded = 0;
+      auto wide_of = [&](int i) -> float { return i < nch ? ldg_early(a.gates + chunk_sh(i) * GATES + G_WIDE) : 0.f; };
+      float wide_next = wide_of(0);
+      auto load = [&](int i) {
+        uint8_t *p = sm + stage(i);
+        uint64_t *bar = &full[i & 1];
+        const int tok = (int)chunk_tok(i);
+        const bool wide = wide_next != 0.f;
+        wide_next = wide_of(i + 1);
+        mbar_expect_tx(bar, 3 * 16384 + 4 * TILE + (wide ? TILE : 0) + GATES * 4);
+        tma_load_3d(p + L_::K, &maps.k, 0, hq, tok, bar);
+        tma_load_3d(p + L_::K + 8192, &maps.k, 64, hq, tok, bar);
+        tma_load_3d(p + L_::DO, &maps.dO, 0, h, tok, bar);
+        tma_load_3d(p + L_::DO + 8192, &maps.dO, 64, h, tok, bar);
+        tma_load_3d(p + L_::Q, &maps.q, 0, hq, tok, bar);
+        tma_load_3d(p + L_::Q + 8192, &maps.q, 64, hq, tok, bar);
+        const char *tiles = a.tiles + chunk_sh(i) * TILES;
+        bulk_load(p + L_::Z, tiles, (wide ? 5 : 4) * TILE, bar);  // Z, P, Z's third part
+        bulk_load(p + L_::GT, a.gates + chunk_sh(i) * GATES, GATES * 4, bar);
+        loaded = i + 1;
+      };
+      constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), id64n = idesc_bf16(128, 64, false, true);
+      constexpr uint32_t idP = idesc_bf16(128, 64, true, true), idS = idesc_bf16(128, 128, false, true);
+      bool ok = true;
+      if (nch > 0) load(0);
+      for (int i = 0; i < nch; ++i) {
+        const uint32_t ph = (uint32_t)i & 1u;
+        const uint32_t st = sb + stage(i), k = st + L_::K, q = st + L_::Q, dO = st + L_::DO, z = st + L_::Z, p = st + L_::P;
+        // every row of the chunk is what it should be (rows past the end cleared) with the state of the step
+        ok = wait_full(i) && mbar_wait(&s_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + B_D1, s_col(tb, ks), kdesc(k, ks, 64), id64, ks);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + B_D1, s_col(tb, ks) + 16u, kdesc(k, ks, 64), id64, 1);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + B_PDO, mdesc(dO, ks, 8192), mdesc(p, ks, 8192), idP, ks);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + B_PDO, mdesc(dO, ks, 8192), mdesc(p + TILE, ks, 8192), idP, 1);
+        mma_commit(&x_full);
+        // step i - 1 is through with its stage (its last product before s_ready, dO's copy in TMEM, gates copied)
+        if (i + 1 < nch) load(i + 1);
+        ok = mbar_wait(&do_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 8u * ks, mdesc(q, ks, 8192), idS, ks);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 32u + 8u * ks, mdesc(q, ks, 8192), idS, 1);
+        ok = mbar_wait(&r_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + B_R + 8u * ks, mdesc(z, ks, 8192), id64n, ks);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + B_R + 32u + 8u * ks, mdesc(z, ks, 8192), id64n, 1);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + B_R + 8u * ks, mdesc(z + TILE, ks, 8192), id64n, 1);
+        if (lds_f1(st + L_::GT + 4u * G_WIDE) != 0.f) {
+          const uint32_t z3 = st + L_::Z3;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + B_R + 32u + 8u * ks, mdesc(z + TILE, ks, 8192), id64n, 1);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + T_R3 + 8u * ks, mdesc(z, ks, 8192), id64n, 1);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + B_R + 8u * ks, mdesc(z3, ks, 8192), id64n, 1);
+        }
+        mma_commit(&e_full);
+        ok = mbar_wait(&u_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_R + 8u * ks, mdesc(k, ks, 8192), idS, 1);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_R + 32u + 8u * ks, mdesc(k, ks, 8192), idS, 1);
+        mma_commit(&s_full);
+      }
+      // no copy or product of this block is in flight when it leaves
+      for (int i = max(0, loaded - 2); i < loaded; ++i)
+        if (!wait_full(i)) ok = false;
+      mma_commit(&drain);
+      if (!mbar_wait(&drain, 0, WAIT_CYCLES)) ok = false;
+      if (!ok) atomicExch(&abort_flag, 1);
+    }
+    __syncwarp();
+  } else if (warp < CHAIN_WARPS) {
+    const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    const bool in = v < a.V;
+    float S[32];
+    {
+      const int64_t at = ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) S[i] = a.dht && in && 32 * grp + i < a.K ? a.dht[at + (int64_t)i * a.V] : 0.f;
+    }
+    auto clear_rows = [&](int i) -> bool {
+      const int L = chunk_len(i);
+      if (L == CH) return true;
+      if (!wait_full(i)) return false;
+      for (int n = threadIdx.x; n < (CH - L) * 6 * 8; n += 32 * CHAIN_WARPS) {  // k, q, dO: six tiles of 64 rows
+        const int c = n % 8, b = n / 8 % 6, r = L + n / 48;
+        st_shared_v4(sb + stage(i) + b * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+      return true;
+    };
+    // where a row of this thread's lies in an image of the state: 64 bytes of hi, as many S_IMAGE / 2 further
+    const uint32_t img0 = (uint32_t)(grp >> 1) * 16384u + (uint32_t)v * 128u;
+    auto img_chunk = [&](int n) -> uint32_t { return img0 + ((((uint32_t)(grp & 1) * 4u + n) ^ ((uint32_t)v & 7u)) << 4); };
+    bool ok = true;
+    // the gradient behind the chunk of step i, handed to the products and to the grads kernel
+    auto hand_state = [&](int i) {
+      uint32_t hi[16], lo[16];
+#pragma unroll
+      for (int n = 0; n < 16; ++n) split2(S[2 * n], S[2 * n + 1], hi[n], lo[n]);
+      tmem_st16(tb + lanes + T_S + 32u * grp, hi);
+      tmem_st16(tb + lanes + T_S + 32u * grp + 16u, lo);
+      tmem_st_wait();
+      tc_fence_before();
+      ok = ok && clear_rows(i);
+      warp_arrive(&s_ready);
+      char *img = a.ds_images + chunk_sh(i) * S_IMAGE;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        st_global_v4(img + img_chunk(n), hi[4 * n], hi[4 * n + 1], hi[4 * n + 2], hi[4 * n + 3]);
+        st_global_v4(img + S_IMAGE / 2 + img_chunk(n), lo[4 * n], lo[4 * n + 1], lo[4 * n + 2], lo[4 * n + 3]);
+      }
+    };
+    if (nch > 0) hand_state(0);
+    for (int i = 0; i < nch; ++i) {
+      const uint32_t ph = (uint32_t)i & 1u, D = tb + lanes + 16u * grp;
+      const float *gates = reinterpret_cast<const float *>(sm + stage(i) + L_::GT);
+      const float4 *into = reinterpret_cast<const float4 *>(gates + G_INTO + 16 * grp);
+      const float4 *out = reinterpret_cast<const float4 *>(gates + G_OUT + 16 * grp);
+      const float4 *beta = reinterpret_cast<const float4 *>(gates + G_BETA + 16 * grp);
+      float Y[16];
+      ok = ok && wait_full(i);
+      const bool wide = gates[G_WIDE] != 0.f;
+      ok = ok && mbar_wait(&x_full, ph, WAIT_CYCLES);
+      tc_fence_after();
+      {
+        uint32_t x[16], p[16], hi[8], lo[8];
+        tmem_ld16(D + B_D1, x);
+        tmem_ld16(D + B_PDO, p);
+        tmem_ld_wait(x);
+        tmem_tie(p);
+#pragma unroll
+        for (int n = 0; n < 16; n += 4) {
+          const float4 r = out[n / 4], b = beta[n / 4];
+          Y[n] = fmaf(r.x, __uint_as_float(x[n]), __uint_as_float(p[n]));
+          Y[n + 1] = fmaf(r.y, __uint_as_float(x[n + 1]), __uint_as_float(p[n + 1]));
+          Y[n + 2] = fmaf(r.z, __uint_as_float(x[n + 2]), __uint_as_float(p[n + 2]));
+          Y[n + 3] = fmaf(r.w, __uint_as_float(x[n + 3]), __uint_as_float(p[n + 3]));
+          split2(b.x * Y[n], b.y * Y[n + 1], hi[n / 2], lo[n / 2]);
+          split2(b.z * Y[n + 2], b.w * Y[n + 3], hi[n / 2 + 1], lo[n / 2 + 1]);
+        }
+        tmem_st8(tb + lanes + B_R + 8u * grp, hi);
+        tmem_st8(tb + lanes + B_R + 32u + 8u * grp, lo);
+        if (wide) {
+          uint32_t l3[8];
+#pragma unroll
+          for (int n = 0; n < 16; n += 4) {
+            const float4 b = beta[n / 4];
+            l3[n / 2] = split3(b.x * Y[n], b.y * Y[n + 1], hi[n / 2], lo[n / 2]);
+            l3[n / 2 + 1] = split3(b.z * Y[n + 2], b.w * Y[n + 3], hi[n / 2 + 1], lo[n / 2 + 1]);
+          }
+          tmem_st8(tb + lanes + T_R3 + 8u * grp, l3);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&r_ready);
+      }
+      ok = ok && mbar_wait(&e_full, ph, WAIT_CYCLES);
+      tc_fence_after();
+      {
+        uint32_t x[16], hi[8], lo[8];
+        tmem_ld16(D + B_D1, x);
+        tmem_ld_wait(x);
+#pragma unroll
+        for (int n = 0; n < 16; n += 4) {
+          const float4 b = beta[n / 4], e = into[n / 4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) Y[n + m] += __uint_as_float(x[n + m]);
+          split2(-e.x * (b.x * Y[n]), -e.y * (b.y * Y[n + 1]), hi[n / 2], lo[n / 2]);
+          split2(-e.z * (b.z * Y[n + 2]), -e.w * (b.w * Y[n + 3]), hi[n / 2 + 1], lo[n / 2 + 1]);
+        }
+        tmem_st8(tb + lanes + B_R + 8u * grp, hi);
+        tmem_st8(tb + lanes + B_R + 32u + 8u * grp, lo);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&u_ready);
+      }
+      // dR, a column of the tile
+      if (i >= 1) ok = ok && mbar_wait(&dr_free, (uint32_t)(i - 1) & 1u, WAIT_CYCLES);
+      {
+        const ColBf16 col(sb + L_::R, 16 * grp, v);
+#pragma unroll
+        for (int n = 0; n < 16; n += 2) {
+          uint32_t hi, lo;
+          split2(Y[n], Y[n + 1], hi, lo);
+          sts_u16(col.at(n), (uint16_t)hi);
+          sts_u16(col.at(n + 1), (uint16_t)(hi >> 16));
+          sts_u16(col.at(n) + 16384u, (uint16_t)lo);
+          sts_u16(col.at(n + 1) + 16384u, (uint16_t)(lo >> 16));
+        }
+        fence_async_smem();
+        warp_arrive(&dr_ready);
+      }
+      // this thread's part of <S0, dS1>
+      {
+        const char *img = a.s_images + chunk_sh(i) * S_IMAGE;
+        float dot = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(img + img_chunk(n)));
+          const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(img + S_IMAGE / 2 + img_chunk(n)));
+          const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16), S[8 * n + 2 * m], dot);
+            dot = fmaf(__uint_as_float(x[m] & 0xffff0000u) + __uint_as_float(y[m] & 0xffff0000u), S[8 * n + 2 * m + 1], dot);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) w_dot[ph][warp] = dot;  // read by the output warps after the next dr_ready
+      }
+      const float over = gates[G_OVER];
+      ok = ok && mbar_wait(&s_full, ph, WAIT_CYCLES);
+      tc_fence_after();
+      {
+        uint32_t x[32];
+        tmem_ld32(tb + lanes + B_DS + 32u * grp, x);
+        tmem_ld_wait32(x);
+#pragma unroll
+        for (int n = 0; n < 32; ++n) S[n] = fmaf(over, S[n], __uint_as_float(x[n]));
+      }
+      if (i + 1 < nch) hand_state(i + 1);
+    }
+    // the last step's dot products
+    if (nch > 0) {
+      if (ok) ok = mbar_wait(&dr_free, (uint32_t)(nch - 1) & 1u, WAIT_CYCLES);
+      warp_arrive(&dr_ready);
+    }
+    if (!ok) atomicExch(&abort_flag, 1);
+    if (a.dh0 && in && ok) {
+      float *dst = a.dh0 + ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
+    }
+  } else {
+    const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    bool ok = true;
+    // scale e^G dO of step i into tensor memory (the product that read the last one is done)
+    auto put_do = [&](int i) {
+      ok = ok && wait_full(i);
+      const float *gates = reinterpret_cast<const float *>(sm + stage(i) + L_::GT);
+      const int L = chunk_len(i);
+      if (tid < CH) w_beta[i % 3][tid] = gates[G_BETA + tid];
+#pragma unroll
+      for (int c = 0; c < 64; c += 16) {
+        const ColBf16 col(sb + stage(i) + L_::DO, c, v);
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int n = 0; n < 16; n += 2) {
+          // rows past the end may be cleared or not yet
+          const float x = c + n < L ? bf16_bits_to_f32(lds_u16(col.at(n))) * (a.scale * gates[G_INTO + c + n]) : 0.f;
+          const float y = c + n + 1 < L ? bf16_bits_to_f32(lds_u16(col.at(n + 1))) * (a.scale * gates[G_INTO + c + n + 1]) : 0.f;
+          split2(x, y, hi[n / 2], lo[n / 2]);
+        }
+        tmem_st8(tb + lanes + B_DO + c / 2, hi);
+        tmem_st8(tb + lanes + B_DO + 32u + c / 2, lo);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&do_ready);
+    };
+    auto put_dot = [&](int i) {  // of step i
+      if (tid == 0) {
+        float x = 0.f;
+        for (int w = 0; w < CHAIN_WARPS; ++w) x += w_dot[i & 1][w];
+        a.sdot[chunk_sh(i)] = x;
+      }
+    };
+    if (nch > 0) put_do(0);
+    for (int i = 0; i < nch; ++i) {
+      const uint32_t ph = (uint32_t)i & 1u;
+      ok = ok && mbar_wait(&e_full, ph, WAIT_CYCLES);  // the product with q of step i before it
+      tc_fence_after();
+      if (i + 1 < nch) put_do(i + 1);
+      ok = ok && mbar_wait(&dr_ready, ph, WAIT_CYCLES);
+      // w_beta is there; everyone hears of a wait that ran out
+      if (named_bar_any(1, 128, !ok)) {
+        ok = false;
+        break;
+      }
+      if (i >= 1) put_dot(i - 1);
+      if (tid == 0) {
+        bulk_store(a.r_images + chunk_sh(i) * R_IMAGE, sm + L_::R, R_IMAGE);
+        bulk_commit();
+      }
+      const int L = chunk_len(i);
+      __nv_bfloat16 *dst = a.dv + (chunk_tok(i) * a.H + h) * (int64_t)a.V;
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        const int e = tid + 128 * n, r = e >> 4, c = (e & 15) * 8;
+        if (r < L && c < a.V) {
+          const uint32_t o = sb + L_::R + sw128_off(r, c, 64);
+          const uint4 x = lds_u4(o), y = lds_u4(o + 16384u);
+          const float b = w_beta[i % 3][r];
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+          uint32_t w[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            w[m] = pack_bf16(b * (__uint_as_float(xs[m] << 16) + __uint_as_float(ys[m] << 16)),
+                             b * (__uint_as_float(xs[m] & 0xffff0000u) + __uint_as_float(ys[m] & 0xffff0000u)));
+          st_global_v4(dst + (int64_t)r * a.H * a.V + c, w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (tid == 0) bulk_wait_read_all();
+      warp_arrive(&dr_free);
+    }
+    if (ok && nch > 0) {
+      ok = mbar_wait(&dr_ready, (uint32_t)nch & 1u, WAIT_CYCLES);
+      if (ok) put_dot(nch - 1);
+    }
+    if (tid == 0) bulk_wait_all();
+    if (!ok) atomicExch(&abort_flag, 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *(volatile int *)&abort_flag) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+  if (warp == 20) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
 }
+
+// ---------------------------------------------------------------------------
+// Gradients of q, k, g and beta, every chunk of a head by itself.  Key channel
+// in lane (128 of them), tokens in columns:
+//     B1 = dO E^T, B2 = dR E^T (token in lane: the stacked [dO; dR], twice over for
+//     the two parts of dR, so that rows of dO come out doubled)
+//     dPd = scale D (.) B1 diag(b), dA = -D (.) diag(b) B2 diag(b), db = diag(B2)
+//     dQ^T = scale e^G (S0 dO^T) + K^T dPd^T
+//     dK^T = -e^G b (S0 dR^T) + e^{G_C - G} b (dS1 E^T) + Q^T dPd + K^T (dA + dA^T)
+// One block per (chunk, head), 256 threads, phase after phase; the images of S0
+// and dS1 follow one another through the same 64 KB.
+// ---------------------------------------------------------------------------
+constexpr uint32_t Q_QK = 0, Q_B = 64, Q_1 = 192, Q_2 = 256, Q_3 = 320, Q_4 = 384, Q_5 = 448;
+
+struct GradMaps {
+  CUtensorMap q, k, dO;
+};
+struct GradArgs {
+  Docs docs;
+  int H, share, K;
+  float scale;
+  const float *g, *beta;
+  const char *s_images, *ds_images, *e_images, *r_images;
+  const float *sdot;
+  void *dq, *dk;  // bf16, or per value head in fp32
+  int per_head;
+  float *dg, *dbeta;
+  int *err;
+};
+struct GradSmem {
+  // S: S0's image, then dS1's; X1, X2: per 64 columns 64 rows of dO, 64 of dR (hi, lo); QK: of q and k;
+  // T: dPd hi, lo, dA hi, lo, W: pair weights, in X1's and X2's places once the products have read them
+  static constexpr uint32_t S = 0, X1 = S + S_IMAGE, X2 = X1 + 32768, E = X2 + 32768, QK = E + E_IMAGE,
+                            BYTES = QK + 32768 + 1024;
+  static constexpr uint32_t T = X1, W = X2;
+};
+static_assert(4 * TILE <= 32768 && CH * (CH + 1) * 4 <= 32768, "");
+
+__global__ void __launch_bounds__(256, 1) delta_grads_kernel(const __grid_constant__ GradMaps maps, const GradArgs a) {
+  using L_ = GradSmem;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  __shared__ uint64_t full, full_ds, g1, g2, g3;
+  __shared__ uint32_t tmem_base;
+  __shared__ alignas(16) float2 s_g[CH];
+  __shared__ float s_into[CH], s_out[CH], s_beta[CH], s_db[CH], s_pair[CH], s_red[2][2][4][32];
+  __shared__ double warp0_total;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = (int)(blockIdx.x % a.H);
+  const int64_t slot = blockIdx.x / a.H, sh = slot * a.H + h;
+  int64_t tok;
+  int L;
+  if (!chunk_in_slot(a.docs, slot, tok, L)) return;
+  const int hq = h / a.share;
+  if (warp == 0) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (uint64_t *b : {&full, &full_ds, &g1, &g2, &g3}) mbar_init(b, 1);
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb = tmem_base, sb = smem_u32(sm);
+  bool ok = true;
+  if (tid == 0) {
+    mbar_expect_tx(&full, S_IMAGE + 2 * 32768 + E_IMAGE + 32768);
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb) {
+      tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full);
+      tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
+      tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
+      tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
+      bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + cb * 8192, 8192, &full);
+      bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + 16384 + cb * 8192, 8192, &full);
+    }
+    bulk_load(sm + L_::E, a.e_images + sh * E_IMAGE, E_IMAGE, &full);
+    bulk_load(sm + L_::S, a.s_images + sh * S_IMAGE, S_IMAGE, &full);
+  }
+  // decays meanwhile
+  double G = 0.0;
+  float b = 0.f;
+  if (tid < 64) {
+    if (tid < L) {
+      G = (double)fmaxf(a.g[(tok + tid) * a.H + h], -1e4f);
+      b = a.beta[(tok + tid) * a.H + h];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, G, o);
+      if (lane >= o) G += y;
+    }
+    if (tid == 31) warp0_total = G;
+  }
+  __syncthreads();
+  if (tid < 64) {
+    if (warp == 1) G += warp0_total;
+    const float gh = (float)G;
+    s_g[tid] = make_float2(gh, (float)(G - (double)gh));
+    s_beta[tid] = b;
+  }
+  __syncthreads();
+  if (tid < 64) {
+    const float2 x = s_g[tid], e = s_g[63];
+    s_into[tid] = expf(x.x + x.y);
+    s_out[tid] = expf((e.x - x.x) + (e.y - x.y));
+  }
+  ok = mbar_wait(&full, 0, WAIT_CYCLES);
+  if (L < CH && ok) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
+    for (int n = tid; n < (CH - L) * 4 * 8; n += 256) {
+      const int c = n % 8, t = n / 8 % 4, r = L + n / 32;
+      st_shared_v4(sb + L_::QK + t * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+    }
+    fence_async_smem();
+  }
+  ok = !__syncthreads_or(!ok);
+  if (ok) {
+    const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S;
+    constexpr uint32_t idQK = idesc_bf16(128, 64, false, false), idB = idesc_bf16(128, 128, false, true);
+    constexpr uint32_t idKN = idesc_bf16(128, 64, true, false), idMN = idesc_bf16(128, 64, true, true);
+    if (tid == 0) {
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_QK, kdesc(q, ks, 128), kdesc(k, ks, 128), idQK, ks);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x1, ks, 128), mdesc(e, ks, 16384), idB, ks);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x2, ks, 128), mdesc(e, ks, 16384), idB, 1);
+      mma_commit(&g1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16(tb + Q_1, mdesc(si + p * (S_IMAGE / 2), ks, 16384), kdesc(x1, ks, 128), idKN, p | ks);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16(tb + Q_2, mdesc(si + p * (S_IMAGE / 2), ks, 16384), kdesc(x1 + 8192, ks, 128), idKN, p | ks);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, mdesc(si, ks, 16384), kdesc(x2 + 8192, ks, 128), idKN, 1);
+      mma_commit(&g2);
+    }
+    __syncwarp();
+    // thread (row of the stack: lane of tensor memory, half of the columns)
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane, t = row & 63, c0 = 32 * half;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const bool isA = row >= 64;
+    ok = mbar_wait(&g1, 0, WAIT_CYCLES);
+    tc_fence_after();
+    float w[32];
+    {
+      uint32_t x[32], y[32];
+      tmem_ld32(tb + lanes + Q_B + c0, x);
+      tmem_ld32(tb + lanes + Q_B + 64u + c0, y);
+      tmem_ld_wait32(x);
+      tmem_ld_wait32(y);
+      const float2 gt = s_g[t];
+      const float f = isA ? -s_beta[t] : 0.5f * a.scale;
+      const int last = t < L ? (isA ? t - 1 : t) : -1;
+#pragma unroll
+      for (int n = 0; n < 32; ++n) {
+        const int c = c0 + n;
+        const float B = __uint_as_float(x[n]) + __uint_as_float(y[n]);
+        if (isA && c == t) s_db[t] = B;
+        const float2 gc = s_g[c];
+        w[n] = c <= last ? f * s_beta[c] * expf((gt.x - gc.x) + (gt.y - gc.y)) * B : 0.f;
+      }
+      ok = mbar_wait(&g2, 0, WAIT_CYCLES) && ok;  // S0's image and the stacks have been read
+      const uint32_t tile = sb + L_::T + (isA ? 2 * TILE : 0);
+#pragma unroll
+      for (int n = 0; n < 32; n += 8) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) split2(w[n + 2 * m], w[n + 2 * m + 1], hi[m], lo[m]);
+        const uint32_t o = tile + sw128_off(t, c0 + n, 64);
+        st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
+      }
+      tmem_ld32(tb + lanes + Q_QK + c0, x);
+      tmem_ld_wait32(x);
+#pragma unroll
+      for (int n = 0; n < 32; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
+    }
+    fence_async_smem();
+    tc_fence_before();
+    ok = !__syncthreads_or(!ok);
+    tc_fence_after();
+    if (ok && tid == 0) {
+      mbar_expect_tx(&full_ds, S_IMAGE);
+      bulk_load(sm + L_::S, a.ds_images + sh * S_IMAGE, S_IMAGE, &full_ds);
+      const uint32_t dp = sb + L_::T, da = dp + 2 * TILE;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_4, mdesc(k, ks, 16384), kdesc(dp + p * TILE, ks, 64), idKN, p | ks);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(q, ks, 16384), mdesc(dp + p * TILE, ks, 8192), idMN, p | ks);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), mdesc(da + p * TILE, ks, 8192), idMN, 1);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), kdesc(da + p * TILE, ks, 64), idKN, 1);
+    }
+    __syncwarp();
+    // sums of the pairs r >= t > s: rows of dA's part, rows of dPd's added, prefix sums along them, then down the columns
+    float *W = reinterpret_cast<float *>(sm + L_::W);
+    constexpr int WP = CH + 1;
+    if (isA)
+#pragma unroll
+      for (int n = 0; n < 32; ++n) W[t * WP + c0 + n] = w[n];
+    __syncthreads();
+    if (!isA) {
+      float x = 0.f;
+#pragma unroll
+      for (int n = 0; n < 32; ++n) {
+        x += w[n] + W[t * WP + c0 + n];
+        W[t * WP + c0 + n] = x;
+      }
+    }
+    __syncthreads();
+    if (tid < CH) {
+      float x = 0.f;
+      if (tid > 0)
+        for (int r = tid; r < CH; ++r) x += W[r * WP + tid - 1] + (tid > 32 ? W[r * WP + 31] : 0.f);
+      s_pair[tid] = x;
+    }
+    if (ok && tid == 0) {
+      ok = mbar_wait(&full_ds, 0, WAIT_CYCLES);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16(tb + Q_3, mdesc(si + p * (S_IMAGE / 2), ks, 16384), mdesc(e, ks, 16384), idMN, p | ks);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, mdesc(si, ks, 16384), mdesc(e + 16384, ks, 16384), idMN, 1);
+      mma_commit(&g3);
+    }
+    __syncwarp();
+    ok = mbar_wait(&g3, 0, WAIT_CYCLES) && ok;
+    ok = !__syncthreads_or(!ok);
+    tc_fence_after();
+    if (ok) {
+      // lane: key channel; tokens c0 .. c0 + 31
+      const int ch = row;
+      const bool in = ch < a.K;
+      float rd[32], ad[32];  // what token t's query and key read of S0, what its key left in S1, of this channel
+      const ColBf16 cq(q, c0, ch, 16384u), ck(k, c0, ch, 16384u);
+#pragma unroll
+      for (int n0 = 0; n0 < 32; n0 += 16) {
+        uint32_t x[16], y[16];
+        tmem_ld16(tb + lanes + Q_1 + c0 + n0, x);
+        tmem_ld16(tb + lanes + Q_4 + c0 + n0, y);
+        tmem_ld_wait(x);
+        tmem_ld_wait(y);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int tt = c0 + n0 + n;
+          const float qi = a.scale * s_into[tt] * __uint_as_float(x[n]);
+          rd[n0 + n] = qi * bf16_bits_to_f32(lds_u16(cq.at(n0 + n)));
+          const float dq = qi + __uint_as_float(y[n]);
+          if (in && tt < L) {
+            const int64_t at = ((tok + tt) * a.H + h) * (int64_t)a.K + ch;
+            if (a.per_head)
+              ((float *)a.dq)[at] = dq;
+            else
+              ((__nv_bfloat16 *)a.dq)[at] = __float2bfloat16_rn(dq);
+          }
+        }
+      }
+#pragma unroll
+      for (int n0 = 0; n0 < 32; n0 += 16) {
+        uint32_t x[16], y[16], z[16];
+        tmem_ld16(tb + lanes + Q_2 + c0 + n0, x);
+        tmem_ld16(tb + lanes + Q_3 + c0 + n0, y);
+        tmem_ld16(tb + lanes + Q_5 + c0 + n0, z);
+        tmem_ld_wait(x);
+        tmem_ld_wait(y);
+        tmem_ld_wait(z);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          const int tt = c0 + n0 + n;
+          const float ki = -s_into[tt] * s_beta[tt] * __uint_as_float(x[n]);
+          const float ko = s_out[tt] * s_beta[tt] * __uint_as_float(y[n]);
+          const float kx = bf16_bits_to_f32(lds_u16(ck.at(n0 + n)));
+          rd[n0 + n] = fmaf(kx, ki, rd[n0 + n]);
+          ad[n0 + n] = kx * ko;
+          const float dk = ki + ko + __uint_as_float(z[n]);
+          if (in && tt < L) {
+            const int64_t at = ((tok + tt) * a.H + h) * (int64_t)a.K + ch;
+            if (a.per_head)
+              ((float *)a.dk)[at] = dk;
+            else
+              ((__nv_bfloat16 *)a.dk)[at] = __float2bfloat16_rn(dk);
+          }
+        }
+      }
+      // summed over the warp's channels: lane n gets token c0 + n
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        const bool up = (lane & o) != 0;
+#pragma unroll
+        for (int n = 0; n < o; ++n) {
+          const float s1 = __shfl_xor_sync(0xffffffffu, up ? rd[n] : rd[n + o], o);
+          const float s2 = __shfl_xor_sync(0xffffffffu, up ? ad[n] : ad[n + o], o);
+          rd[n] = (up ? rd[n + o] : rd[n]) + s1;
+          ad[n] = (up ? ad[n + o] : ad[n]) + s2;
+        }
+      }
+      s_red[half][0][warp & 3][lane] = rd[0];
+      s_red[half][1][warp & 3][lane] = ad[0];
+    }
+    __syncthreads();
+    float *reads = W, *adds = W + CH;
+    if (ok && tid < CH) {
+      const int hf = tid >> 5, n = tid & 31;
+      reads[tid] = (s_red[hf][0][0][n] + s_red[hf][0][1][n]) + (s_red[hf][0][2][n] + s_red[hf][0][3][n]);
+      adds[tid] = (s_red[hf][1][0][n] + s_red[hf][1][1][n]) + (s_red[hf][1][2][n] + s_red[hf][1][3][n]);
+    }
+    __syncthreads();
+    if (ok && tid < L) {
+      float x = s_pair[tid];
+      for (int r = tid; r < L; ++r) x += reads[r];
+      for (int r = 0; r < tid; ++r) x += adds[r];
+      a.dg[(tok + tid) * a.H + h] = fmaf(s_into[63], a.sdot[sh], x);
+      a.dbeta[(tok + tid) * a.H + h] = s_db[tid];
+    }
+  }
+  if (tid == 0 && !ok) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tb, 512);
+  }
+}
+
+inline size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 }  // namespace
 
@@ -826,29 +1579,71 @@ bool tc_supported(const glacore_problem *p) {
          !(((uintptr_t)p->q | (uintptr_t)p->k | (uintptr_t)p->v) & 15);
 }
 
-size_t tc_workspace(int64_t slots, int64_t H, bool backward) {
-  (void)backward;
-  return al256((size_t)slots * H * TILES) + al256((size_t)slots * H * GATES * sizeof(float));
+// Scratch (byte offsets): tiles and gates of every chunk and head, the backward's images.
+namespace {
+struct TcLayout {
+  size_t tiles, gates, s, ds, e, r, sdot, total;
+};
+TcLayout tc_layout(int64_t slots, int64_t H, bool backward) {
+  TcLayout l;
+  memset(&l, 0, sizeof(l));
+  size_t off = 0;
+  auto take = [&](size_t &at, size_t each) {
+    at = off;
+    off = al256(off + (size_t)slots * H * each);
+  };
+  take(l.tiles, TILES);
+  take(l.gates, GATES * sizeof(float));
+  if (backward) {
+    take(l.s, S_IMAGE);
+    take(l.ds, S_IMAGE);
+    take(l.e, E_IMAGE);
+    take(l.r, R_IMAGE);
+    take(l.sdot, sizeof(float));
+  }
+  l.total = off;
+  return l;
 }
 
-cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
-  if (const cudaError_t be = bind_context()) return be;
-  const int64_t units = c.docs.n * c.p.H;
-  if (units >= ((int64_t)1 << 31) || c.slots * c.p.Hqk >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  ChainMaps maps;
-  memset(&maps, 0, sizeof(maps));
-  if (!make_map(&maps.q, c.p.q, true, c.p.K, c.p.Hqk, c.p.BT, 64, c.p.qs) ||
-      !make_map(&maps.k, c.p.k, true, c.p.K, c.p.Hqk, c.p.BT, 64, c.p.ks) ||
-      !make_map(&maps.v, c.p.v, true, c.p.V, c.p.H, c.p.BT, 64, c.p.vs))
-    return cudaErrorInvalidValue;
-  PrepMaps pm;
-  pm.q = maps.q;
-  pm.k = maps.k;
-  char *tiles = ws;
-  float *gates = (float *)(ws + al256((size_t)c.slots * c.p.H * TILES));
-  cudaError_t e = prep(c, pm, tiles, gates);
+struct Maps {
+  CUtensorMap q, k, v, dO;
+};
+cudaError_t make_maps(const Call &c, const void *dO, Maps &m) {
+  if (const cudaError_t e = bind_context()) return e;
+  memset(&m, 0, sizeof(m));
+  const bool ok = make_map(&m.q, c.p.q, true, c.p.K, c.p.Hqk, c.p.BT, 64, c.p.qs) &&
+                  make_map(&m.k, c.p.k, true, c.p.K, c.p.Hqk, c.p.BT, 64, c.p.ks) &&
+                  make_map(&m.v, c.p.v, true, c.p.V, c.p.H, c.p.BT, 64, c.p.vs) &&
+                  (!dO || make_map(&m.dO, dO, true, c.p.V, c.p.H, c.p.BT, 64));
+  return ok ? cudaSuccess : cudaErrorInvalidValue;
+}
+template <typename K, typename M, typename A>
+cudaError_t launch(K kernel, int64_t blocks, int threads, uint32_t smem, const Call &c, const M &maps, const A &a,
+                   const char *label) {
+  if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)blocks, threads, smem, c.st>>>(maps, a);
+  mark_launch(label, c.st);
+  return cudaGetLastError();
+}
+cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
+  PrepArgs a;
+  a.g = c.p.g;
+  a.beta = c.beta;
+  a.docs = c.docs;
+  a.H = (int)c.p.H;
+  a.Hqk = (int)c.p.Hqk;
+  a.share = a.H / a.Hqk;
+  a.scale = c.p.scale;
+  a.tiles = ws + l.tiles;
+  a.gates = (float *)(ws + l.gates);
+  a.err = c.p.err;
+  return launch(delta_prep_kernel, c.slots * c.p.Hqk, 128, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep");
+}
+ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   ChainArgs a;
+  memset(&a, 0, sizeof(a));
   a.docs = c.docs;
   a.H = (int)c.p.H;
   a.share = (int)(c.p.H / c.p.Hqk);
@@ -856,18 +1651,81 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
   a.V = (int)c.p.V;
   a.scale = c.p.scale;
   a.h0 = c.p.h0;
-  a.ht = ht;
-  a.o = (__nv_bfloat16 *)o;
-  a.tiles = tiles;
-  a.gates = gates;
+  a.tiles = ws + l.tiles;
+  a.gates = (const float *)(ws + l.gates);
   a.err = c.p.err;
-  a.s_images = a.e_images = nullptr;
-  constexpr uint32_t smem = ChainSmem<false>::BYTES;
-  e = cudaFuncSetAttribute(delta_chain_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return a;
+}
+}  // namespace
+
+size_t tc_workspace(int64_t slots, int64_t H, bool backward) { return tc_layout(slots, H, backward).total; }
+
+cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
+  const TcLayout l = tc_layout(c.slots, c.p.H, false);
+  Maps m;
+  cudaError_t e = make_maps(c, nullptr, m);
+  if (e == cudaSuccess) e = prep(c, m, ws, l);
   if (e != cudaSuccess) return e;
-  delta_chain_kernel<false><<<(unsigned)units, CHAIN_THREADS, smem, c.st>>>(maps, a);
-  mark_launch("delta_chain", c.st);
-  return cudaGetLastError();
+  ChainArgs a = chain_args(c, ws, l);
+  a.o = (__nv_bfloat16 *)o;
+  a.ht = ht;
+  return launch(delta_chain_kernel<false>, c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
+                ChainMaps{m.q, m.k, m.v}, a, "delta_chain");
+}
+
+cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, void *dk, bool per_head, void *dv, float *dg,
+                   float *dbeta, float *dh0, char *ws) {
+  const TcLayout l = tc_layout(c.slots, c.p.H, true);
+  Maps m;
+  cudaError_t e = make_maps(c, dO, m);
+  if (e == cudaSuccess) e = prep(c, m, ws, l);
+  if (e != cudaSuccess) return e;
+  ChainArgs a = chain_args(c, ws, l);
+  a.s_images = ws + l.s;
+  a.e_images = ws + l.e;
+  e = launch(delta_chain_kernel<true>, c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<true>::BYTES, c,
+             ChainMaps{m.q, m.k, m.v}, a, "delta_chain_states");
+  if (e != cudaSuccess) return e;
+  BackArgs b;
+  b.docs = a.docs;
+  b.H = a.H;
+  b.share = a.share;
+  b.K = a.K;
+  b.V = a.V;
+  b.scale = a.scale;
+  b.dht = dht;
+  b.dh0 = dh0;
+  b.dv = (__nv_bfloat16 *)dv;
+  b.tiles = a.tiles;
+  b.gates = a.gates;
+  b.s_images = a.s_images;
+  b.ds_images = ws + l.ds;
+  b.r_images = ws + l.r;
+  b.sdot = (float *)(ws + l.sdot);
+  b.err = a.err;
+  e = launch(delta_back_kernel, c.docs.n * c.p.H, CHAIN_THREADS, BackSmem::BYTES, c, BackMaps{m.q, m.k, m.dO}, b,
+             "delta_back");
+  if (e != cudaSuccess) return e;
+  GradArgs g;
+  g.docs = a.docs;
+  g.H = a.H;
+  g.share = a.share;
+  g.K = a.K;
+  g.scale = a.scale;
+  g.g = c.p.g;
+  g.beta = c.beta;
+  g.s_images = a.s_images;
+  g.ds_images = b.ds_images;
+  g.e_images = a.e_images;
+  g.r_images = b.r_images;
+  g.sdot = b.sdot;
+  g.dq = dq;
+  g.dk = dk;
+  g.per_head = per_head;
+  g.dg = dg;
+  g.dbeta = dbeta;
+  g.err = a.err;
+  return launch(delta_grads_kernel, c.slots * c.p.H, 256, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g, "delta_grads");
 }
 
 }  // namespace delta
