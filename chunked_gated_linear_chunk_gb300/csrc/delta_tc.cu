@@ -62,11 +62,14 @@ __device__ __forceinline__ uint32_t split3(float a, float b, uint32_t hi, uint32
 // One block per (chunk, q / k head): Q K^T and K K^T as one product of the
 // stacked tiles [q; k] (128 rows) with k, then for each value head of the group
 // P and N with the decays, and Z = -(I + N diag(b))^-1 N.  Z is made by
-// blocks of 32: the diagonal ones by forward substitution, a thread per column in
-// registers, and with (I + N b)^-1 = I + Z b
+// blocks: those of 16 on the diagonal by forward substitution, a thread per
+// column in registers, then twice the block below a pair of them, with
+// (I + N b)^-1 = I + Z b,
 //     Z21 = W + Z22 (b W),   W = -(N21 + N21 (b Z11)).
-// Decays are e^{G_t - G_s} of the difference itself, G kept in two fp32 parts, so that
-// neither a strong decay nor a long chunk costs digits.
+// (Substitution over the whole chunk is a sequence four times as long, and most
+// of this kernel's time.)  Decays are e^{G_t - G_s} of the difference itself, G (in units
+// of log 2) kept in two fp32 parts, so that neither a strong decay nor a long
+// chunk costs digits.
 // ---------------------------------------------------------------------------
 struct PrepArgs {
   const float *g, *beta;
@@ -82,7 +85,8 @@ struct PrepMaps {
 };
 struct PrepSmem {
   float N[CH][NP], Z[CH][NP], W[32][36];
-  float Gh[CH], Gl[CH], beta[CH];
+  float2 G[CH];  // two parts of the decay exponent
+  float beta[CH];
 };
 constexpr uint32_t PREP_BYTES = 32768 + sizeof(PrepSmem) + 1024;
 
@@ -120,6 +124,42 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
       tma_load_3d(sm + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full);
       tma_load_3d(sm + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
     }
+  }
+  const int t = tid & 63;
+  // gates of head e of the group, loaded a head ahead; then their prefix sums
+  float g_next = 0.f, b_next = 0.f;
+  auto fetch = [&](int e) {
+    g_next = b_next = 0.f;
+    if (tid < L && tid < CH && e < a.share) {
+      const int64_t at = (tok + tid) * a.H + hq * a.share + e;
+      g_next = a.g[at];
+      b_next = a.beta[at];
+    }
+  };
+  auto scan = [&]() {  // ends with a barrier of the block
+    double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;  // e^g of less is 0 as well
+    const float b = b_next;
+    if (tid < CH) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, G, o);
+        if (lane >= o) G += y;
+      }
+      if (tid == 31) warp0_total = G;
+    }
+    __syncthreads();
+    if (tid < CH) {
+      if (warp == 1) G += warp0_total;
+      const float gh = (float)G;
+      s.G[t] = make_float2(gh, (float)(G - (double)gh));
+      s.beta[t] = b;
+    }
+    __syncthreads();
+  };
+  fetch(0);
+  scan();
+  fetch(1);
+  if (tid == 0) {
     ok = mbar_wait(&full, 0, WAIT_CYCLES);
     const uint32_t base = smem_u32(sm);
     if (ok) {
@@ -129,6 +169,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
     }
     mma_commit(&done);
   }
+  __syncwarp();
   ok = mbar_wait(&done, 0, WAIT_CYCLES) && ok;
   ok = !__syncthreads_or(!ok);
   if (ok) {
@@ -140,59 +181,41 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
     tmem_ld32(at + 32, r1);
     tmem_ld_wait32(r0);
     tmem_ld_wait32(r1);
-    const int t = tid & 63;
     for (int e = 0; e < a.share; ++e) {
       const int h = hq * a.share + e;
       const int64_t sh = slot * a.H + h;
-      if (e) {  // the tiles of the last head have left shared memory
-        if (tid == 0) bulk_wait_read_all();
-        __syncthreads();
+      if (e) {
+        if (tid == 0) bulk_wait_read_all();  // the tiles of the last head have left shared memory
+        scan();
+        fetch(e + 1);
       }
-      double G = 0.0;
-      float b = 0.f;
-      if (tid < 64) {
-        if (t < L) {
-          G = (double)fmaxf(a.g[(tok + t) * a.H + h], -1e4f);  // e^g of less is 0 as well
-          b = a.beta[(tok + t) * a.H + h];
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const double y = __shfl_up_sync(0xffffffffu, G, o);
-          if (lane >= o) G += y;
-        }
-        if (tid == 31) warp0_total = G;
-      }
-      __syncthreads();
-      if (tid < 64) {
-        if (warp == 1) G += warp0_total;
-        s.Gh[t] = (float)G;
-        s.Gl[t] = (float)(G - (double)(float)G);
-        s.beta[t] = b;
-      }
-      __syncthreads();
-      const float gh = s.Gh[t], gl = s.Gl[t];
-      if (tid < 64) {
+      const float2 gt = s.G[t];
+      if (tid < CH) {
+        const float2 last = s.G[63];
         float *gs = a.gates + sh * GATES;
-        gs[G_INTO + t] = expf(gh + gl);
-        gs[G_OUT + t] = expf((s.Gh[63] - gh) + (s.Gl[63] - gl));  // tokens past the end add no decay
-        gs[G_BETA + t] = b;
-        if (t == 0) gs[G_OVER] = expf(s.Gh[63] + s.Gl[63]);
+        gs[G_INTO + t] = exp2f(gt.x + gt.y);
+        gs[G_OUT + t] = exp2f((last.x - gt.x) + (last.y - gt.y));  // tokens past the end add no decay
+        gs[G_BETA + t] = s.beta[t];
+        if (t == 0) gs[G_OVER] = exp2f(last.x + last.y);
       }
       // row t, columns s <= t (P) or s < t (N): scale D (.) QK^T, D (.) KK^T
-      const int last = t < L ? (tid < 64 ? t : t - 1) : -1;
-      const float f = tid < 64 ? a.scale : 1.f;
+      const int last = t < L ? (tid < CH ? t : t - 1) : -1;
+      const float f = tid < CH ? a.scale : 1.f;
 #pragma unroll
       for (int c0 = 0; c0 < 64; c0 += 8) {
-        float x[8];
-        const bool some = c0 <= (t | 31);  // for the warp: one of its rows reaches these columns
+        alignas(16) float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (c0 <= (t | 31)) {  // for the warp: one of its rows reaches these columns
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = c0 + i;
-          x[i] = 0.f;
-          if (some && c <= last)
-            x[i] = f * expf((gh - s.Gh[c]) + (gl - s.Gl[c])) * __uint_as_float(c < 32 ? r0[c & 31] : r1[c & 31]);
+          for (int i = 0; i < 8; i += 2) {
+            const int c = c0 + i;
+            const float4 gc = *reinterpret_cast<const float4 *>(&s.G[c]);
+            const float m0 = __uint_as_float(c < 32 ? r0[c & 31] : r1[c & 31]);
+            const float m1 = __uint_as_float(c < 32 ? r0[(c + 1) & 31] : r1[(c + 1) & 31]);
+            x[i] = c <= last ? f * exp2f((gt.x - gc.x) + (gt.y - gc.y)) * m0 : 0.f;
+            x[i + 1] = c + 1 <= last ? f * exp2f((gt.x - gc.z) + (gt.y - gc.w)) * m1 : 0.f;
+          }
         }
-        if (tid < 64) {
+        if (tid < CH) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
@@ -204,13 +227,13 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
           *reinterpret_cast<float4 *>(&s.N[t][c0 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
         }
       }
-      if (warp >= 2) {  // Z of the diagonal blocks: warp 2 the first, warp 3 the second
+      if (warp >= 2) {  // Z of the four diagonal blocks, two by a warp, a column by a thread
         named_bar(1, 64);
-        const int r = (warp - 2) * 32;
-        float zb[32];
+        const int r = (warp - 2) * 32 + (lane & 16), j = lane & 15;
+        float zb[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float z0 = -s.N[r + i][r + lane], z1 = 0.f;
+        for (int i = 0; i < 16; ++i) {
+          float z0 = -s.N[r + i][r + j], z1 = 0.f;
 #pragma unroll
           for (int c = 0; c < i; c += 4) {
             const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + i][r + c]);
@@ -220,8 +243,46 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
             if (c + 3 < i) z1 = fmaf(-n.w, zb[c + 3], z1);
           }
           const float z = z0 + z1;
-          s.Z[r + i][r + lane] = z;
+          s.Z[r + i][r + j] = z;
           zb[i] = z * s.beta[r + i];
+        }
+      }
+      __syncthreads();
+      // the block below each pair of them: warps 0, 1 the first pair, four rows of a column by a thread
+      {
+        const int r = (warp >> 1) * 32, j = lane & 15, i0 = 8 * (warp & 1) + 4 * (lane >> 4);
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = -s.N[r + 16 + i0 + i][r + j];
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          float z[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) z[x] = s.beta[r + c + x] * s.Z[r + c + x][r + j];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + 16 + i0 + i][r + c]);
+            w[i] = fmaf(-n.x, z[0], fmaf(-n.y, z[1], fmaf(-n.z, z[2], fmaf(-n.w, z[3], w[i]))));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.W[i0 + i][(warp >> 1) * 16 + j] = w[i];
+        named_bar(2 + (warp >> 1), 64);
+#pragma unroll
+        for (int c = 0; c < 16; c += 4) {
+          float z[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) z[x] = s.beta[r + 16 + c + x] * s.W[c + x][(warp >> 1) * 16 + j];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 n = *reinterpret_cast<const float4 *>(&s.Z[r + 16 + i0 + i][r + 16 + c]);
+            w[i] = fmaf(n.x, z[0], fmaf(n.y, z[1], fmaf(n.z, z[2], fmaf(n.w, z[3], w[i]))));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s.Z[r + 16 + i0 + i][r + j] = w[i];
+          s.Z[r + i0 + i][r + 16 + j] = 0.f;
         }
       }
       __syncthreads();
@@ -243,12 +304,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) s.W[i0 + i][j] = w[i];
-      }
-      __syncthreads();
-      {
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = s.W[i0 + i][j];
+        __syncthreads();
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           float z[4];
@@ -905,6 +961,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         const char *tiles = a.tiles + chunk_sh(i) * TILES;
         bulk_load(p + L_::Z, tiles, (wide ? 5 : 4) * TILE, bar);  // Z, P, Z's third part
         bulk_load(p + L_::GT, a.gates + chunk_sh(i) * GATES, GATES * 4, bar);
+        bulk_prefetch_l2(a.s_images + chunk_sh(i) * S_IMAGE, S_IMAGE);
         loaded = i + 1;
       };
       constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), id64n = idesc_bf16(128, 64, false, true);
@@ -1014,6 +1071,23 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         st_global_v4(img + img_chunk(n), hi[4 * n], hi[4 * n + 1], hi[4 * n + 2], hi[4 * n + 3]);
         st_global_v4(img + S_IMAGE / 2 + img_chunk(n), lo[4 * n], lo[4 * n + 1], lo[4 * n + 2], lo[4 * n + 3]);
       }
+      // this thread's part of <S0, dS1>, while the products run (S0's image is on its way to L2 since the last step)
+      const char *s0i = a.s_images + chunk_sh(i) * S_IMAGE;
+      float dot = 0.f;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const uint4 h4 = __ldg(reinterpret_cast<const uint4 *>(s0i + img_chunk(n)));
+        const uint4 l4 = __ldg(reinterpret_cast<const uint4 *>(s0i + S_IMAGE / 2 + img_chunk(n)));
+        const uint32_t x[4] = {h4.x, h4.y, h4.z, h4.w}, y[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16), S[8 * n + 2 * m], dot);
+          dot = fmaf(__uint_as_float(x[m] & 0xffff0000u) + __uint_as_float(y[m] & 0xffff0000u), S[8 * n + 2 * m + 1], dot);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      if (lane == 0) w_dot[i & 1][warp] = dot;  // read by the output warps behind this step's dr_ready
     };
     if (nch > 0) hand_state(0);
     for (int i = 0; i < nch; ++i) {
@@ -1095,25 +1169,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         fence_async_smem();
         warp_arrive(&dr_ready);
       }
-      // this thread's part of <S0, dS1>
-      {
-        const char *img = a.s_images + chunk_sh(i) * S_IMAGE;
-        float dot = 0.f;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint4 hi = __ldg(reinterpret_cast<const uint4 *>(img + img_chunk(n)));
-          const uint4 lo = __ldg(reinterpret_cast<const uint4 *>(img + S_IMAGE / 2 + img_chunk(n)));
-          const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16), S[8 * n + 2 * m], dot);
-            dot = fmaf(__uint_as_float(x[m] & 0xffff0000u) + __uint_as_float(y[m] & 0xffff0000u), S[8 * n + 2 * m + 1], dot);
-          }
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) w_dot[ph][warp] = dot;  // read by the output warps after the next dr_ready
-      }
       const float over = gates[G_OVER];
       ok = ok && mbar_wait(&s_full, ph, WAIT_CYCLES);
       tc_fence_after();
@@ -1125,11 +1180,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         for (int n = 0; n < 32; ++n) S[n] = fmaf(over, S[n], __uint_as_float(x[n]));
       }
       if (i + 1 < nch) hand_state(i + 1);
-    }
-    // the last step's dot products
-    if (nch > 0) {
-      if (ok) ok = mbar_wait(&dr_free, (uint32_t)(nch - 1) & 1u, WAIT_CYCLES);
-      warp_arrive(&dr_ready);
     }
     if (!ok) atomicExch(&abort_flag, 1);
     if (a.dh0 && in && ok) {
@@ -1166,13 +1216,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
       tc_fence_before();
       warp_arrive(&do_ready);
     };
-    auto put_dot = [&](int i) {  // of step i
-      if (tid == 0) {
-        float x = 0.f;
-        for (int w = 0; w < CHAIN_WARPS; ++w) x += w_dot[i & 1][w];
-        a.sdot[chunk_sh(i)] = x;
-      }
-    };
     if (nch > 0) put_do(0);
     for (int i = 0; i < nch; ++i) {
       const uint32_t ph = (uint32_t)i & 1u;
@@ -1185,8 +1228,10 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         ok = false;
         break;
       }
-      if (i >= 1) put_dot(i - 1);
       if (tid == 0) {
+        float x = 0.f;
+        for (int w = 0; w < CHAIN_WARPS; ++w) x += w_dot[ph][w];
+        a.sdot[chunk_sh(i)] = x;
         bulk_store(a.r_images + chunk_sh(i) * R_IMAGE, sm + L_::R, R_IMAGE);
         bulk_commit();
       }
@@ -1211,10 +1256,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
       if (tid == 0) bulk_wait_read_all();
       warp_arrive(&dr_free);
     }
-    if (ok && nch > 0) {
-      ok = mbar_wait(&dr_ready, (uint32_t)nch & 1u, WAIT_CYCLES);
-      if (ok) put_dot(nch - 1);
-    }
     if (tid == 0) bulk_wait_all();
     if (!ok) atomicExch(&abort_flag, 1);
   }
@@ -1235,10 +1276,16 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
 //     dPd = scale D (.) B1 diag(b), dA = -D (.) diag(b) B2 diag(b), db = diag(B2)
 //     dQ^T = scale e^G (S0 dO^T) + K^T dPd^T
 //     dK^T = -e^G b (S0 dR^T) + e^{G_C - G} b (dS1 E^T) + Q^T dPd + K^T (dA + dA^T)
-// One block per (chunk, head), 256 threads, phase after phase; the images of S0
-// and dS1 follow one another through the same 64 KB.
+// One block per (chunk, head): 16 warps of elementwise work, one that copies
+// and multiplies.  The images of S0 and dS1 follow one another through the same 64 KB; the
+// products with two parts of a matrix put both into one operand of 128 columns
+// where tensor memory has room for the two results (a product of 64 columns
+// is bound by its other operand's way through shared memory).
+// TMEM columns: [0, 64) [q; k] k^T, [64, 192) B1, B2 of E's two parts, later [0, 128)
+// the pairs' part of dK^T (two halves); [192, 320) S0 dO^T, S0 dR^T; [320, 384)
+// K^T dPd^T; [384, 512) dS1 E^T (two halves).
 // ---------------------------------------------------------------------------
-constexpr uint32_t Q_QK = 0, Q_B = 64, Q_1 = 192, Q_2 = 256, Q_3 = 320, Q_4 = 384, Q_5 = 448;
+constexpr uint32_t Q_QK = 0, Q_B = 64, Q_1 = 192, Q_2 = 256, Q_4 = 320, Q_3 = 384, Q_5 = 0;
 
 struct GradMaps {
   CUtensorMap q, k, dO;
@@ -1262,16 +1309,21 @@ struct GradSmem {
                             BYTES = QK + 32768 + 1024;
   static constexpr uint32_t T = X1, W = X2;
 };
-static_assert(4 * TILE <= 32768 && CH * (CH + 1) * 4 <= 32768, "");
+constexpr int WP = CH + 1;  // pitch of W
+static_assert(4 * TILE <= 32768 && CH * WP * 4 <= 32768, "");
+constexpr int GRAD_WARPS = 16, GRAD_THREADS = 544;
 
-__global__ void __launch_bounds__(256, 1) delta_grads_kernel(const __grid_constant__ GradMaps maps, const GradArgs a) {
+__global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __grid_constant__ GradMaps maps,
+                                                                      const GradArgs a) {
   using L_ = GradSmem;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full, full_ds, g1, g2, g3;
+  __shared__ uint64_t full, full_ds, cleared, g1, g2, tiles, g3;
   __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
   __shared__ alignas(16) float2 s_g[CH];
-  __shared__ float s_into[CH], s_out[CH], s_beta[CH], s_db[CH], s_pair[CH], s_red[2][2][4][32];
+  __shared__ alignas(16) float s_into[CH], s_ki[CH], s_ko[CH], s_beta[CH];  // scale e^G, -e^G b, e^{G_C - G} b, b
+  __shared__ float s_db[CH], s_pair[8][CH], s_red[2][4][CH], s_over;
   __shared__ double warp0_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = (int)(blockIdx.x % a.H);
@@ -1280,125 +1332,169 @@ __global__ void __launch_bounds__(256, 1) delta_grads_kernel(const __grid_consta
   int L;
   if (!chunk_in_slot(a.docs, slot, tok, L)) return;
   const int hq = h / a.share;
-  if (warp == 0) {
+  if (warp == GRAD_WARPS) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
+    abort_flag = 0;
     for (uint64_t *b : {&full, &full_ds, &g1, &g2, &g3}) mbar_init(b, 1);
+    for (uint64_t *b : {&cleared, &tiles}) mbar_init(b, GRAD_WARPS);
     fence_mbar_init();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = tmem_base, sb = smem_u32(sm);
+  const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S;
   bool ok = true;
-  if (tid == 0) {
-    mbar_expect_tx(&full, S_IMAGE + 2 * 32768 + E_IMAGE + 32768);
+  if (warp == GRAD_WARPS) {
+    if (lane == 0) {
+      mbar_expect_tx(&full, S_IMAGE + 2 * 32768 + E_IMAGE + 32768);
 #pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full);
-      tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
-      tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
-      tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
-      bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + cb * 8192, 8192, &full);
-      bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + 16384 + cb * 8192, 8192, &full);
-    }
-    bulk_load(sm + L_::E, a.e_images + sh * E_IMAGE, E_IMAGE, &full);
-    bulk_load(sm + L_::S, a.s_images + sh * S_IMAGE, S_IMAGE, &full);
-  }
-  // decays meanwhile
-  double G = 0.0;
-  float b = 0.f;
-  if (tid < 64) {
-    if (tid < L) {
-      G = (double)fmaxf(a.g[(tok + tid) * a.H + h], -1e4f);
-      b = a.beta[(tok + tid) * a.H + h];
-    }
+      for (int cb = 0; cb < 2; ++cb) {
+        tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full);
+        tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
+        tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
+        tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
+        bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + cb * 8192, 8192, &full);
+        bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + 16384 + cb * 8192, 8192, &full);
+      }
+      bulk_load(sm + L_::E, a.e_images + sh * E_IMAGE, E_IMAGE, &full);
+      bulk_load(sm + L_::S, a.s_images + sh * S_IMAGE, S_IMAGE, &full);
+      bulk_prefetch_l2(a.ds_images + sh * S_IMAGE, S_IMAGE);
+      constexpr uint32_t idQK = idesc_bf16(128, 64, false, false), idB = idesc_bf16(128, 128, false, true);
+      constexpr uint32_t idKN = idesc_bf16(128, 64, true, false), idMN = idesc_bf16(128, 64, true, true);
+      constexpr uint32_t idKN2 = idesc_bf16(128, 128, true, false), idMN2 = idesc_bf16(128, 128, true, true);
+      const uint32_t dp = sb + L_::T, da = dp + 2 * TILE;
+      bool issued_ds = false;
+      do {
+        ok = mbar_wait(&full, 0, WAIT_CYCLES) && mbar_wait(&cleared, 0, WAIT_CYCLES);
+        if (!ok) break;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double y = __shfl_up_sync(0xffffffffu, G, o);
-      if (lane >= o) G += y;
-    }
-    if (tid == 31) warp0_total = G;
-  }
-  __syncthreads();
-  if (tid < 64) {
-    if (warp == 1) G += warp0_total;
-    const float gh = (float)G;
-    s_g[tid] = make_float2(gh, (float)(G - (double)gh));
-    s_beta[tid] = b;
-  }
-  __syncthreads();
-  if (tid < 64) {
-    const float2 x = s_g[tid], e = s_g[63];
-    s_into[tid] = expf(x.x + x.y);
-    s_out[tid] = expf((e.x - x.x) + (e.y - x.y));
-  }
-  ok = mbar_wait(&full, 0, WAIT_CYCLES);
-  if (L < CH && ok) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
-    for (int n = tid; n < (CH - L) * 4 * 8; n += 256) {
-      const int c = n % 8, t = n / 8 % 4, r = L + n / 32;
-      st_shared_v4(sb + L_::QK + t * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
-    }
-    fence_async_smem();
-  }
-  ok = !__syncthreads_or(!ok);
-  if (ok) {
-    const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S;
-    constexpr uint32_t idQK = idesc_bf16(128, 64, false, false), idB = idesc_bf16(128, 128, false, true);
-    constexpr uint32_t idKN = idesc_bf16(128, 64, true, false), idMN = idesc_bf16(128, 64, true, true);
-    if (tid == 0) {
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_QK, kdesc(q, ks, 128), kdesc(k, ks, 128), idQK, ks);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_QK, kdesc(q, ks, 128), kdesc(k, ks, 128), idQK, ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x1, ks, 128), mdesc(e, ks, 16384), idB, ks);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x1, ks, 128), mdesc(e, ks, 16384), idB, ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x2, ks, 128), mdesc(e, ks, 16384), idB, 1);
+        mma_commit(&g1);
+        // S0 (hi, lo) [dO | dR hi], S0 hi dR lo
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x2, ks, 128), mdesc(e, ks, 16384), idB, 1);
-      mma_commit(&g1);
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16(tb + Q_1, mdesc(si + p * (S_IMAGE / 2), ks, 16384), kdesc(x1, ks, 128), idKN2, p | ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16(tb + Q_1, mdesc(si + p * (S_IMAGE / 2), ks, 16384), kdesc(x1, ks, 128), idKN, p | ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, mdesc(si, ks, 16384), kdesc(x2 + 8192, ks, 128), idKN, 1);
+        mma_commit(&g2);
+        if (!(ok = mbar_wait(&g2, 0, WAIT_CYCLES))) break;
+        mbar_expect_tx(&full_ds, S_IMAGE);
+        bulk_load(sm + L_::S, a.ds_images + sh * S_IMAGE, S_IMAGE, &full_ds);
+        issued_ds = true;
+        if (!(ok = mbar_wait(&tiles, 0, WAIT_CYCLES))) break;
+        tc_fence_after();
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16(tb + Q_2, mdesc(si + p * (S_IMAGE / 2), ks, 16384), kdesc(x1 + 8192, ks, 128), idKN, p | ks);
+          for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_4, mdesc(k, ks, 16384), kdesc(dp + p * TILE, ks, 64), idKN, p | ks);
 #pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, mdesc(si, ks, 16384), kdesc(x2 + 8192, ks, 128), idKN, 1);
-      mma_commit(&g2);
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(q, ks, 16384), mdesc(dp, ks, TILE), idMN2, ks);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), mdesc(da, ks, TILE), idMN2, 1);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), kdesc(da, ks, 128), idKN2, 1);
+        if (!(ok = mbar_wait(&full_ds, 0, WAIT_CYCLES))) break;
+        // dS1 hi [E hi | E lo], dS1 lo E hi
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, mdesc(si, ks, 16384), mdesc(e, ks, 16384), idMN2, ks);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, mdesc(si + S_IMAGE / 2, ks, 16384), mdesc(e, ks, 16384), idMN, 1);
+        mma_commit(&g3);
+        ok = mbar_wait(&g3, 0, WAIT_CYCLES);
+      } while (false);
+      if (!ok) {  // nothing of this block's is in flight when it leaves
+        mbar_wait(&full, 0, WAIT_CYCLES);
+        if (issued_ds) mbar_wait(&full_ds, 0, WAIT_CYCLES);
+        mma_commit(&g3);
+        mbar_wait(&g3, 0, WAIT_CYCLES);
+        atomicExch(&abort_flag, 1);
+      }
     }
     __syncwarp();
-    // thread (row of the stack: lane of tensor memory, half of the columns)
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane, t = row & 63, c0 = 32 * half;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const bool isA = row >= 64;
-    ok = mbar_wait(&g1, 0, WAIT_CYCLES);
+  } else {
+    // decays, while the copies run
+    const float over = a.sdot[sh];
+    double G = 0.0;
+    float b = 0.f;
+    if (tid < CH) {
+      if (tid < L) {
+        G = (double)fmaxf(a.g[(tok + tid) * a.H + h], -1e4f);
+        b = a.beta[(tok + tid) * a.H + h];
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, G, o);
+        if (lane >= o) G += y;
+      }
+      if (tid == 31) warp0_total = G;
+    }
+    named_bar(1, 32 * GRAD_WARPS);
+    if (tid < CH) {
+      if (warp == 1) G += warp0_total;
+      const float gh = (float)G;
+      s_g[tid] = make_float2(gh, (float)(G - (double)gh));
+      s_beta[tid] = b;
+    }
+    named_bar(1, 32 * GRAD_WARPS);
+    if (tid < CH) {
+      const float2 x = s_g[tid], z = s_g[63];
+      const float into = expf(x.x + x.y), out = expf((z.x - x.x) + (z.y - x.y));
+      s_into[tid] = a.scale * into;
+      s_ki[tid] = -into * b;
+      s_ko[tid] = out * b;
+      if (tid == 63) s_over = into * over;
+    }
+    if (L < CH) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
+      ok = mbar_wait(&full, 0, WAIT_CYCLES);
+      for (int n = tid; n < (CH - L) * 4 * 8; n += 32 * GRAD_WARPS) {
+        const int c = n % 8, t = n / 8 % 4, r = L + n / 32;
+        st_shared_v4(sb + L_::QK + t * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+      }
+      fence_async_smem();
+    }
+    warp_arrive(&cleared);
+    // thread (row of the stack: lane of tensor memory, 16 of the columns)
+    const int grp = warp >> 2, qw = warp & 3, row = qw * 32 + lane, t = row & 63, c0 = 16 * grp;
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    const bool isA = qw >= 2;
+    float *W = reinterpret_cast<float *>(sm + L_::W);
+    ok = mbar_wait(&g1, 0, WAIT_CYCLES) && ok;
     tc_fence_after();
-    float w[32];
+    float w[16];
     {
-      uint32_t x[32], y[32];
-      tmem_ld32(tb + lanes + Q_B + c0, x);
-      tmem_ld32(tb + lanes + Q_B + 64u + c0, y);
-      tmem_ld_wait32(x);
-      tmem_ld_wait32(y);
+      uint32_t x[16], y[16];
+      tmem_ld16(tb + lanes + Q_B + c0, x);
+      tmem_ld16(tb + lanes + Q_B + 64u + c0, y);
+      tmem_ld_wait(x);
+      tmem_tie(y);
       const float2 gt = s_g[t];
       const float f = isA ? -s_beta[t] : 0.5f * a.scale;
       const int last = t < L ? (isA ? t - 1 : t) : -1;
 #pragma unroll
-      for (int n = 0; n < 32; ++n) {
+      for (int n = 0; n < 16; ++n) {
         const int c = c0 + n;
         const float B = __uint_as_float(x[n]) + __uint_as_float(y[n]);
         if (isA && c == t) s_db[t] = B;
         const float2 gc = s_g[c];
         w[n] = c <= last ? f * s_beta[c] * expf((gt.x - gc.x) + (gt.y - gc.y)) * B : 0.f;
       }
-      ok = mbar_wait(&g2, 0, WAIT_CYCLES) && ok;  // S0's image and the stacks have been read
+      tmem_ld16(tb + lanes + Q_QK + c0, x);
+      tmem_ld_wait(x);
+      tc_fence_before();
+      ok = mbar_wait(&g2, 0, WAIT_CYCLES) && ok;  // the stacks have been read
       const uint32_t tile = sb + L_::T + (isA ? 2 * TILE : 0);
 #pragma unroll
-      for (int n = 0; n < 32; n += 8) {
+      for (int n = 0; n < 16; n += 8) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) split2(w[n + 2 * m], w[n + 2 * m + 1], hi[m], lo[m]);
@@ -1406,164 +1502,162 @@ __global__ void __launch_bounds__(256, 1) delta_grads_kernel(const __grid_consta
         st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
       }
-      tmem_ld32(tb + lanes + Q_QK + c0, x);
-      tmem_ld_wait32(x);
+      fence_async_smem();
+      warp_arrive(&tiles);
 #pragma unroll
-      for (int n = 0; n < 32; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
+      for (int n = 0; n < 16; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
     }
-    fence_async_smem();
-    tc_fence_before();
-    ok = !__syncthreads_or(!ok);
-    tc_fence_after();
-    if (ok && tid == 0) {
-      mbar_expect_tx(&full_ds, S_IMAGE);
-      bulk_load(sm + L_::S, a.ds_images + sh * S_IMAGE, S_IMAGE, &full_ds);
-      const uint32_t dp = sb + L_::T, da = dp + 2 * TILE;
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_4, mdesc(k, ks, 16384), kdesc(dp + p * TILE, ks, 64), idKN, p | ks);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(q, ks, 16384), mdesc(dp + p * TILE, ks, 8192), idMN, p | ks);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), mdesc(da + p * TILE, ks, 8192), idMN, 1);
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), kdesc(da + p * TILE, ks, 64), idKN, 1);
-    }
-    __syncwarp();
-    // sums of the pairs r >= t > s: rows of dA's part, rows of dPd's added, prefix sums along them, then down the columns
-    float *W = reinterpret_cast<float *>(sm + L_::W);
-    constexpr int WP = CH + 1;
+    // sums of the pairs r >= t > s: rows of dA's part, dPd's added to them, summed along the rows, then down the columns
     if (isA)
 #pragma unroll
-      for (int n = 0; n < 32; ++n) W[t * WP + c0 + n] = w[n];
-    __syncthreads();
-    if (!isA) {
-      float x = 0.f;
+      for (int n = 0; n < 16; ++n) W[t * WP + c0 + n] = w[n];
+    named_bar(1, 32 * GRAD_WARPS);
+    if (!isA)
 #pragma unroll
-      for (int n = 0; n < 32; ++n) {
-        x += w[n] + W[t * WP + c0 + n];
-        W[t * WP + c0 + n] = x;
-      }
-    }
-    __syncthreads();
+      for (int n = 0; n < 16; ++n) W[t * WP + c0 + n] += w[n];
+    named_bar(1, 32 * GRAD_WARPS);
     if (tid < CH) {
       float x = 0.f;
-      if (tid > 0)
-        for (int r = tid; r < CH; ++r) x += W[r * WP + tid - 1] + (tid > 32 ? W[r * WP + 31] : 0.f);
-      s_pair[tid] = x;
+#pragma unroll 16
+      for (int n = 0; n < CH; ++n) {
+        x += W[tid * WP + n];
+        W[tid * WP + n] = x;
+      }
     }
-    if (ok && tid == 0) {
-      ok = mbar_wait(&full_ds, 0, WAIT_CYCLES);
+    named_bar(1, 32 * GRAD_WARPS);
+    {
+      const int c = tid & 63, r0 = (tid >> 6) * 8;  // 8 rows of a column
+      float x = 0.f;
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16(tb + Q_3, mdesc(si + p * (S_IMAGE / 2), ks, 16384), mdesc(e, ks, 16384), idMN, p | ks);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, mdesc(si, ks, 16384), mdesc(e + 16384, ks, 16384), idMN, 1);
-      mma_commit(&g3);
+      for (int r = r0; r < r0 + 8; ++r) x += c > 0 && r >= c ? W[r * WP + c - 1] : 0.f;
+      s_pair[tid >> 6][c] = x;
     }
-    __syncwarp();
     ok = mbar_wait(&g3, 0, WAIT_CYCLES) && ok;
-    ok = !__syncthreads_or(!ok);
     tc_fence_after();
-    if (ok) {
-      // lane: key channel; tokens c0 .. c0 + 31
+    if (!__any_sync(0xffffffffu, !ok)) {
+      // lane: key channel; tokens c0 .. c0 + 15
       const int ch = row;
       const bool in = ch < a.K;
-      float rd[32], ad[32];  // what token t's query and key read of S0, what its key left in S1, of this channel
+      float rd[16], ad[16];  // what token t's query and key read of S0, what its key left in S1, of this channel
       const ColBf16 cq(q, c0, ch, 16384u), ck(k, c0, ch, 16384u);
-#pragma unroll
-      for (int n0 = 0; n0 < 32; n0 += 16) {
+      const int64_t at0 = ((tok + c0) * a.H + h) * (int64_t)a.K + ch, step = (int64_t)a.H * a.K;
+      {
         uint32_t x[16], y[16];
-        tmem_ld16(tb + lanes + Q_1 + c0 + n0, x);
-        tmem_ld16(tb + lanes + Q_4 + c0 + n0, y);
+        tmem_ld16(tb + lanes + Q_1 + c0, x);
+        tmem_ld16(tb + lanes + Q_4 + c0, y);
         tmem_ld_wait(x);
-        tmem_ld_wait(y);
+        tmem_tie(y);
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const int tt = c0 + n0 + n;
-          const float qi = a.scale * s_into[tt] * __uint_as_float(x[n]);
-          rd[n0 + n] = qi * bf16_bits_to_f32(lds_u16(cq.at(n0 + n)));
+          const float qi = s_into[c0 + n] * __uint_as_float(x[n]);
+          rd[n] = qi * bf16_bits_to_f32(lds_u16(cq.at(n)));
           const float dq = qi + __uint_as_float(y[n]);
-          if (in && tt < L) {
-            const int64_t at = ((tok + tt) * a.H + h) * (int64_t)a.K + ch;
+          if (in && c0 + n < L) {
             if (a.per_head)
-              ((float *)a.dq)[at] = dq;
+              ((float *)a.dq)[at0 + n * step] = dq;
             else
-              ((__nv_bfloat16 *)a.dq)[at] = __float2bfloat16_rn(dq);
+              ((__nv_bfloat16 *)a.dq)[at0 + n * step] = __float2bfloat16_rn(dq);
           }
         }
       }
-#pragma unroll
-      for (int n0 = 0; n0 < 32; n0 += 16) {
+      {
         uint32_t x[16], y[16], z[16];
-        tmem_ld16(tb + lanes + Q_2 + c0 + n0, x);
-        tmem_ld16(tb + lanes + Q_3 + c0 + n0, y);
-        tmem_ld16(tb + lanes + Q_5 + c0 + n0, z);
+        float ko[16];
+        tmem_ld16(tb + lanes + Q_3 + c0, x);
+        tmem_ld16(tb + lanes + Q_3 + 64u + c0, y);
         tmem_ld_wait(x);
-        tmem_ld_wait(y);
-        tmem_ld_wait(z);
+        tmem_tie(y);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) ko[n] = s_ko[c0 + n] * (__uint_as_float(x[n]) + __uint_as_float(y[n]));
+        tmem_ld16(tb + lanes + Q_2 + c0, x);
+        tmem_ld16(tb + lanes + Q_5 + c0, y);
+        tmem_ld16(tb + lanes + Q_5 + 64u + c0, z);
+        tmem_ld_wait(x);
+        tmem_tie(y);
+        tmem_tie(z);
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const int tt = c0 + n0 + n;
-          const float ki = -s_into[tt] * s_beta[tt] * __uint_as_float(x[n]);
-          const float ko = s_out[tt] * s_beta[tt] * __uint_as_float(y[n]);
-          const float kx = bf16_bits_to_f32(lds_u16(ck.at(n0 + n)));
-          rd[n0 + n] = fmaf(kx, ki, rd[n0 + n]);
-          ad[n0 + n] = kx * ko;
-          const float dk = ki + ko + __uint_as_float(z[n]);
-          if (in && tt < L) {
-            const int64_t at = ((tok + tt) * a.H + h) * (int64_t)a.K + ch;
+          const float ki = s_ki[c0 + n] * __uint_as_float(x[n]);
+          const float kx = bf16_bits_to_f32(lds_u16(ck.at(n)));
+          rd[n] = fmaf(kx, ki, rd[n]);
+          ad[n] = kx * ko[n];
+          const float dk = (ki + ko[n]) + (__uint_as_float(y[n]) + __uint_as_float(z[n]));
+          if (in && c0 + n < L) {
             if (a.per_head)
-              ((float *)a.dk)[at] = dk;
+              ((float *)a.dk)[at0 + n * step] = dk;
             else
-              ((__nv_bfloat16 *)a.dk)[at] = __float2bfloat16_rn(dk);
+              ((__nv_bfloat16 *)a.dk)[at0 + n * step] = __float2bfloat16_rn(dk);
           }
         }
       }
-      // summed over the warp's channels: lane n gets token c0 + n
+      // summed over the warp's channels: lanes n and n + 16 get token c0 + n
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
+      for (int n = 0; n < 16; ++n) {
+        rd[n] += __shfl_xor_sync(0xffffffffu, rd[n], 16);
+        ad[n] += __shfl_xor_sync(0xffffffffu, ad[n], 16);
+      }
+#pragma unroll
+      for (int o = 8; o; o >>= 1) {
         const bool up = (lane & o) != 0;
 #pragma unroll
         for (int n = 0; n < o; ++n) {
-          const float s1 = __shfl_xor_sync(0xffffffffu, up ? rd[n] : rd[n + o], o);
-          const float s2 = __shfl_xor_sync(0xffffffffu, up ? ad[n] : ad[n + o], o);
-          rd[n] = (up ? rd[n + o] : rd[n]) + s1;
-          ad[n] = (up ? ad[n + o] : ad[n]) + s2;
+          const float r1 = __shfl_xor_sync(0xffffffffu, up ? rd[n] : rd[n + o], o);
+          const float r2 = __shfl_xor_sync(0xffffffffu, up ? ad[n] : ad[n + o], o);
+          rd[n] = (up ? rd[n + o] : rd[n]) + r1;
+          ad[n] = (up ? ad[n + o] : ad[n]) + r2;
         }
       }
-      s_red[half][0][warp & 3][lane] = rd[0];
-      s_red[half][1][warp & 3][lane] = ad[0];
+      if (lane < 16) {
+        s_red[0][qw][c0 + lane] = rd[0];
+        s_red[1][qw][c0 + lane] = ad[0];
+      }
+    } else {
+      ok = false;
     }
-    __syncthreads();
-    float *reads = W, *adds = W + CH;
-    if (ok && tid < CH) {
-      const int hf = tid >> 5, n = tid & 31;
-      reads[tid] = (s_red[hf][0][0][n] + s_red[hf][0][1][n]) + (s_red[hf][0][2][n] + s_red[hf][0][3][n]);
-      adds[tid] = (s_red[hf][1][0][n] + s_red[hf][1][1][n]) + (s_red[hf][1][2][n] + s_red[hf][1][3][n]);
-    }
-    __syncthreads();
-    if (ok && tid < L) {
-      float x = s_pair[tid];
-      for (int r = tid; r < L; ++r) x += reads[r];
-      for (int r = 0; r < tid; ++r) x += adds[r];
-      a.dg[(tok + tid) * a.H + h] = fmaf(s_into[63], a.sdot[sh], x);
-      a.dbeta[(tok + tid) * a.H + h] = s_db[tid];
+    if (!ok) atomicExch(&abort_flag, 1);
+    named_bar(1, 32 * GRAD_WARPS);
+    if (warp == 0) {
+      // tokens lane and lane + 32: sums over the tokens from them on of what is read, over those before of what is left
+      float r0 = 0.f, r1 = 0.f, d0 = 0.f, d1 = 0.f, p0 = 0.f, p1 = 0.f;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        r0 += s_red[0][n][lane];
+        r1 += s_red[0][n][lane + 32];
+        d0 += s_red[1][n][lane];
+        d1 += s_red[1][n][lane + 32];
+      }
+#pragma unroll
+      for (int n = 0; n < 8; ++n) {
+        p0 += s_pair[n][lane];
+        p1 += s_pair[n][lane + 32];
+      }
+      const float own0 = d0, own1 = d1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float a0 = __shfl_down_sync(0xffffffffu, r0, o), a1 = __shfl_down_sync(0xffffffffu, r1, o);
+        const float b0 = __shfl_up_sync(0xffffffffu, d0, o), b1 = __shfl_up_sync(0xffffffffu, d1, o);
+        if (lane + o < 32) r0 += a0, r1 += a1;
+        if (lane >= o) d0 += b0, d1 += b1;
+      }
+      r0 += __shfl_sync(0xffffffffu, r1, 0);
+      d1 += __shfl_sync(0xffffffffu, d0, 31);
+      const float o_ = s_over;
+      if (*(volatile int *)&abort_flag == 0) {
+        if (lane < L) {
+          a.dg[(tok + lane) * a.H + h] = (p0 + o_) + (r0 + (d0 - own0));
+          a.dbeta[(tok + lane) * a.H + h] = s_db[lane];
+        }
+        if (lane + 32 < L) {
+          a.dg[(tok + lane + 32) * a.H + h] = (p1 + o_) + (r1 + (d1 - own1));
+          a.dbeta[(tok + lane + 32) * a.H + h] = s_db[lane + 32];
+        }
+      }
     }
   }
-  if (tid == 0 && !ok) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (tid == 0 && *(volatile int *)&abort_flag) set_device_error(a.err, GLACORE_ERR_TIMEOUT);
+  if (warp == GRAD_WARPS) {
     tc_fence_after();
     tmem_dealloc(tb, 512);
   }
@@ -1725,7 +1819,7 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   g.dg = dg;
   g.dbeta = dbeta;
   g.err = a.err;
-  return launch(delta_grads_kernel, c.slots * c.p.H, 256, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g, "delta_grads");
+  return launch(delta_grads_kernel, c.slots * c.p.H, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g, "delta_grads");
 }
 
 }  // namespace delta
