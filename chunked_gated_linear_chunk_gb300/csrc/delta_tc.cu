@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
 // output has warps of its own.
 //   warps 0..15  the chain: lanes of quarter w % 4, group w / 4 holds 32 of the
 //                state's key rows and 16 of the chunk's tokens (of its column v)
-//   warps 16..19 the output (STATES: one thread that stores images)
+//   warps 16..19 the output (none in STATES)
 //   warp 20      copies and products, one thread
 // TMEM columns: [0, 128) S^T, per group of 32 rows 16 columns of hi and 16 of
 // lo; the same columns take U'^T k once X and S^T q^T have read S.  [128, 384)
@@ -401,10 +401,17 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
 constexpr uint32_t T_S = 0, T_XQ = 128, T_R = 384, T_U = 448;
 constexpr uint32_t T_R3 = T_S;  // R's third part, between X and the new state
 
-// Images: rows of a value column v, 64 columns (channels of a block, or
-// tokens) to a row of 128 bytes, 128-byte swizzle.
-constexpr uint32_t S_IMAGE = 4 * 16384;  // [hi, lo][two blocks of 64 channels][128 rows]
-constexpr uint32_t E_IMAGE = 2 * 16384;  // [hi, lo][128 rows]
+// Images: units of 16 bytes, 8 channels (tokens) of a value column, the 128
+// columns of a unit one after another: lanes write and read whole lines, and it
+// is an operand with the value columns along the contraction.  (Rows of 128 swizzled
+// bytes, a row to a lane, took 5000 cycles a chunk to write.)
+constexpr uint32_t UNITS = 128 * 16;         // the columns of a unit
+constexpr uint32_t S_IMAGE = 2 * 16 * UNITS;  // [hi, lo][16 units of 8 channels][128 columns]
+constexpr uint32_t E_IMAGE = 2 * 8 * UNITS;   // [hi, lo][8 units of 8 tokens][128 columns]
+// K-step ks (16 value columns) of an image
+__device__ __forceinline__ SDesc image_desc(uint32_t base, int ks) {
+  return sdesc_mn16(base, 128, UNITS) + (uint32_t)ks * 256u;
+}
 
 struct ChainMaps {
   CUtensorMap q, k, v;
@@ -423,13 +430,13 @@ struct ChainArgs {
 };
 
 // Shared memory: two stages of k, (q), v, Z, gates; three of P; the output
-// tile, or the two images.
+// tile.
 template <bool STATES>
 struct ChainSmem {
   static constexpr uint32_t KQ = 0, V = STATES ? 16384 : 32768, Z = V + 16384, GT = Z + 3 * TILE, STAGE = GT + 1024;
   static constexpr uint32_t P = 2 * STAGE, OUT = P + (STATES ? 0 : 3 * 2 * TILE);
-  static constexpr uint32_t BYTES = OUT + (STATES ? S_IMAGE + E_IMAGE : 16384) + 1024;
-  static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BYTES <= 227 * 1024, "");
+  static constexpr uint32_t BYTES = OUT + (STATES ? 0 : 16384) + 1024;
+  static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BYTES <= 226 * 1024, "");
 };
 constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = 672;
 
@@ -448,21 +455,23 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
 __device__ __forceinline__ uint32_t s_col(uint32_t tb, int ks) {
   return tb + T_S + (uint32_t)(ks >> 1) * 32u + (uint32_t)(ks & 1) * 8u;
 }
-// 32 values of a column as hi and lo parts, into tensor memory and, with IMG,
-// into the image row `row` (at `img`, lo a half further) from column c0 on.
-template <bool IMG>
-__device__ __forceinline__ void put_state(uint32_t at, const float (&S)[32], uint8_t *img, int row, int c0) {
+// 32 values of a column as hi and lo parts, into tensor memory; with IMG into
+// an image as well, behind `arrive`.
+template <bool IMG, typename F>
+__device__ __forceinline__ void put_state(uint32_t at, const float (&S)[32], char *img, F arrive) {
   uint32_t hi[16], lo[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) split2(S[2 * i], S[2 * i + 1], hi[i], lo[i]);
   tmem_st16(at, hi);
   tmem_st16(at + 16, lo);
+  tmem_st_wait();
+  tc_fence_before();
+  arrive();
   if (IMG) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t o = smem_u32(img) + sw128_off(row, c0 + 8 * i, 128);
-      st_shared_v4(o, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-      st_shared_v4(o + S_IMAGE / 2, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+      st_global_v4(img + i * UNITS, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      st_global_v4(img + S_IMAGE / 2 + i * UNITS, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
     }
   }
 }
@@ -474,7 +483,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, pu_full[2], o_free[2], drain;
-  __shared__ uint64_t si_ready, si_free, ei_ready, ei_free;
   __shared__ alignas(16) float o_into[2][CH];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -499,8 +507,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
       mbar_init(&pu_full[i], 1);
       mbar_init(&o_free[i], 4);
     }
-    for (uint64_t *b : {&x_full, &e_full, &s_full, &drain, &si_free, &ei_free}) mbar_init(b, 1);
-    for (uint64_t *b : {&s_ready, &r_ready, &u_ready, &si_ready, &ei_ready}) mbar_init(b, CHAIN_WARPS);
+    for (uint64_t *b : {&x_full, &e_full, &s_full, &drain}) mbar_init(b, 1);
+    for (uint64_t *b : {&s_ready, &r_ready, &u_ready}) mbar_init(b, CHAIN_WARPS);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -624,7 +632,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
     const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;  // this warp's lanes of tensor memory
     const bool in = v < a.V;
-    uint8_t *s_img = sm + L_::OUT, *e_img = sm + L_::OUT + S_IMAGE;
     float S[32];
     {
       const int64_t at = ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
@@ -647,16 +654,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
     bool ok = true;
     // the state before chunk j, handed to the products
     auto hand_state = [&](int j) {
-      if (STATES && j >= 1) ok = ok && mbar_wait(&si_free, (uint32_t)(j - 1) & 1u, WAIT_CYCLES);
-      put_state<STATES>(tb + lanes + T_S + 32u * grp, S, s_img, v, 32 * grp);
-      tmem_st_wait();
-      tc_fence_before();
-      ok = ok && clear_rows(j);
-      warp_arrive(&s_ready);
-      if (STATES) {
-        fence_async_smem();
-        warp_arrive(&si_ready);
-      }
+      put_state<STATES>(tb + lanes + T_S + 32u * grp, S,
+                        a.s_images + ((slot0 + j) * a.H + h) * S_IMAGE + 4 * grp * UNITS + v * 16, [&] {
+                          ok = ok && clear_rows(j);
+                          warp_arrive(&s_ready);
+                        });
     };
     if (nch > 0) hand_state(0);
     for (int j = 0; j < nch; ++j) {
@@ -737,17 +739,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
         tc_fence_before();
         warp_arrive(&u_ready);
         if (STATES) {  // E
-          if (j >= 1) ok = ok && mbar_wait(&ei_free, (uint32_t)(j - 1) & 1u, WAIT_CYCLES);
+          char *img = a.e_images + ((slot0 + j) * a.H + h) * E_IMAGE + 2 * grp * UNITS + v * 16;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) split2(Y[i], Y[i + 1], hi[i / 2], lo[i / 2]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t o = smem_u32(e_img) + sw128_off(v, 16 * grp + 8 * i, 128);
-            st_shared_v4(o, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-            st_shared_v4(o + E_IMAGE / 2, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+            st_global_v4(img + i * UNITS, hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+            st_global_v4(img + E_IMAGE / 2 + i * UNITS, lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
           }
-          fence_async_smem();
-          warp_arrive(&ei_ready);
         }
       }
       const float over = gates[G_OVER];
@@ -769,32 +768,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
       for (int i = 0; i < 32; ++i)
         if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
     }
-  } else if (STATES) {
-    if (warp == CHAIN_WARPS && lane == 0) {  // the images leave, the state's and E's in turn
-      bool ok = true;
-      for (int j = 0; j < nch && ok; ++j) {
-        const uint32_t ph = (uint32_t)j & 1u;
-        const int64_t sh = (slot0 + j) * a.H + h;
-        ok = mbar_wait(&si_ready, ph, WAIT_CYCLES);
-        if (!ok) break;
-        bulk_store(a.s_images + sh * S_IMAGE, sm + L_::OUT, S_IMAGE);
-        bulk_commit();
-        if (j >= 1) {  // E of the chunk before has been read
-          bulk_wait_read_all_but_one();
-          mbar_arrive(&ei_free);
-        }
-        ok = mbar_wait(&ei_ready, ph, WAIT_CYCLES);
-        if (!ok) break;
-        bulk_store(a.e_images + sh * E_IMAGE, sm + L_::OUT + S_IMAGE, E_IMAGE);
-        bulk_commit();
-        bulk_wait_read_all_but_one();
-        mbar_arrive(&si_free);
-      }
-      bulk_wait_all();
-      if (!ok) atomicExch(&abort_flag, 1);
-    }
-    __syncwarp();
-  } else {
+  } else if (!STATES) {
     const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     bool ok = true;
@@ -1050,34 +1024,21 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
       fence_async_smem();
       return true;
     };
-    // where a row of this thread's lies in an image of the state: 64 bytes of hi, as many S_IMAGE / 2 further
-    const uint32_t img0 = (uint32_t)(grp >> 1) * 16384u + (uint32_t)v * 128u;
-    auto img_chunk = [&](int n) -> uint32_t { return img0 + ((((uint32_t)(grp & 1) * 4u + n) ^ ((uint32_t)v & 7u)) << 4); };
+    const uint32_t img0 = 4 * grp * UNITS + v * 16;  // this thread's units in an image of the state
     bool ok = true;
     // the gradient behind the chunk of step i, handed to the products and to the grads kernel
     auto hand_state = [&](int i) {
-      uint32_t hi[16], lo[16];
-#pragma unroll
-      for (int n = 0; n < 16; ++n) split2(S[2 * n], S[2 * n + 1], hi[n], lo[n]);
-      tmem_st16(tb + lanes + T_S + 32u * grp, hi);
-      tmem_st16(tb + lanes + T_S + 32u * grp + 16u, lo);
-      tmem_st_wait();
-      tc_fence_before();
-      ok = ok && clear_rows(i);
-      warp_arrive(&s_ready);
-      char *img = a.ds_images + chunk_sh(i) * S_IMAGE;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        st_global_v4(img + img_chunk(n), hi[4 * n], hi[4 * n + 1], hi[4 * n + 2], hi[4 * n + 3]);
-        st_global_v4(img + S_IMAGE / 2 + img_chunk(n), lo[4 * n], lo[4 * n + 1], lo[4 * n + 2], lo[4 * n + 3]);
-      }
+      put_state<true>(tb + lanes + T_S + 32u * grp, S, a.ds_images + chunk_sh(i) * S_IMAGE + img0, [&] {
+        ok = ok && clear_rows(i);
+        warp_arrive(&s_ready);
+      });
       // this thread's part of <S0, dS1>, while the products run (S0's image is on its way to L2 since the last step)
-      const char *s0i = a.s_images + chunk_sh(i) * S_IMAGE;
+      const char *s0i = a.s_images + chunk_sh(i) * S_IMAGE + img0;
       float dot = 0.f;
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
-        const uint4 h4 = __ldg(reinterpret_cast<const uint4 *>(s0i + img_chunk(n)));
-        const uint4 l4 = __ldg(reinterpret_cast<const uint4 *>(s0i + S_IMAGE / 2 + img_chunk(n)));
+        const uint4 h4 = __ldg(reinterpret_cast<const uint4 *>(s0i + n * UNITS));
+        const uint4 l4 = __ldg(reinterpret_cast<const uint4 *>(s0i + S_IMAGE / 2 + n * UNITS));
         const uint32_t x[4] = {h4.x, h4.y, h4.z, h4.w}, y[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
@@ -1374,18 +1335,18 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_QK, kdesc(q, ks, 128), kdesc(k, ks, 128), idQK, ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x1, ks, 128), mdesc(e, ks, 16384), idB, ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x1, ks, 128), image_desc(e, ks), idB, ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x2, ks, 128), mdesc(e, ks, 16384), idB, 1);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x2, ks, 128), image_desc(e, ks), idB, 1);
         mma_commit(&g1);
         // S0 (hi, lo) [dO | dR hi], S0 hi dR lo
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_bf16(tb + Q_1, mdesc(si + p * (S_IMAGE / 2), ks, 16384), kdesc(x1, ks, 128), idKN2, p | ks);
+            mma_bf16(tb + Q_1, image_desc(si + p * (S_IMAGE / 2), ks), kdesc(x1, ks, 128), idKN2, p | ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, mdesc(si, ks, 16384), kdesc(x2 + 8192, ks, 128), idKN, 1);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, image_desc(si, ks), kdesc(x2 + 8192, ks, 128), idKN, 1);
         mma_commit(&g2);
         if (!(ok = mbar_wait(&g2, 0, WAIT_CYCLES))) break;
         mbar_expect_tx(&full_ds, S_IMAGE);
@@ -1406,9 +1367,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         if (!(ok = mbar_wait(&full_ds, 0, WAIT_CYCLES))) break;
         // dS1 hi [E hi | E lo], dS1 lo E hi
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, mdesc(si, ks, 16384), mdesc(e, ks, 16384), idMN2, ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(si, ks), image_desc(e, ks), idMN2, ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, mdesc(si + S_IMAGE / 2, ks, 16384), mdesc(e, ks, 16384), idMN, 1);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(si + S_IMAGE / 2, ks), image_desc(e, ks), idMN, 1);
         mma_commit(&g3);
         ok = mbar_wait(&g3, 0, WAIT_CYCLES);
       } while (false);

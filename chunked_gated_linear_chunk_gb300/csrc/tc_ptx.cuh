@@ -307,6 +307,15 @@ __device__ __forceinline__ SDesc sdesc_sw128(uint32_t saddr, uint32_t lbo, uint3
          | (2u << 29);                       // bits 61-63: 128-byte swizzle
   return d;
 }
+// The same without a swizzle, MN-major: units of 16 bytes (8 elements along
+// M/N), 8 rows along K of them contiguous (128 bytes); lbo = distance between
+// 8-row groups along K, sbo = distance between 8-element blocks along M/N.
+__device__ __forceinline__ SDesc sdesc_mn16(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  SDesc d;
+  d.lo = ((saddr & 0x3FFFFu) >> 4) | (((lbo >> 4) & 0x3FFFu) << 16);
+  d.hi = ((sbo >> 4) & 0x3FFFu) | (1u << 14);
+  return d;
+}
 __device__ __forceinline__ SDesc operator+(SDesc d, uint32_t bytes) {
   d.lo += bytes >> 4;
   return d;
