@@ -132,7 +132,7 @@ glacore_status run_bwd(const glacore_problem *p, const float *beta, const void *
   const bool shared = p->Hqk != p->H;
   void *hq = shared ? (void *)(ws + L.dq) : dq, *hk = shared ? (void *)(ws + L.dk) : dk;
   cudaError_t e;
-  if (L.on_tc && !(((uintptr_t)dO | (uintptr_t)dv) & 15)) {
+  if (L.on_tc && !(((uintptr_t)dO | (uintptr_t)dv | (uintptr_t)hq | (uintptr_t)hk) & 15)) {
     e = tc_bwd(c, dO, dht, hq, hk, shared, dv, dg, dbeta, dh0, ws + L.tc);
   } else {
     e = simt_scan(c, nullptr, nullptr, &saved);

@@ -834,8 +834,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
 //     dR^T  = dU^T + (b dU)^T Z                        -> dY = b dR (= dV), dX = -e^G dY
 //     dS0^T = e^{G_C} dS1^T + (scale e^G dO)^T q + dX^T k
 // dO^T P and the product with q do not wait for the chain.  Saved for
-// delta_grads_kernel: dS1 of every chunk (an image as S0's), dR (as rows of a
-// token, [hi, lo][two blocks of 64 columns][64 rows]) and e^{G_C} <S0, dS1>.
+// delta_grads_kernel: dS1 of every chunk (an image as S0's) and dR (as rows of a
+// token, [hi, lo][two blocks of 64 columns][64 rows]).
 //   warps 0..15  the chain, as in the forward
 //   warps 16..19 scale e^G dO as an operand, dv and dR on their way out
 //   warp 20      copies and products, one thread
@@ -858,9 +858,7 @@ struct BackArgs {
   __nv_bfloat16 *dv;
   const char *tiles;
   const float *gates;
-  const char *s_images;
   char *ds_images, *r_images;
-  float *sdot;  // [slot, H]
   int *err;
 };
 struct BackSmem {
@@ -875,8 +873,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
   using L_ = BackSmem;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, do_ready, dr_ready, dr_free, drain;
-  __shared__ float w_beta[3][CH], w_dot[2][CHAIN_WARPS];  // of three steps: read behind the next step's barrier
+  __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, q_full, do_ready, dr_ready, dr_free, drain;
+  __shared__ float w_beta[3][CH];  // of three steps: read behind the next step's barrier
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -897,7 +895,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
   }
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (uint64_t *b : {&full[0], &full[1], &x_full, &e_full, &s_full, &drain}) mbar_init(b, 1);
+    for (uint64_t *b : {&full[0], &full[1], &x_full, &e_full, &s_full, &q_full, &drain}) mbar_init(b, 1);
     for (uint64_t *b : {&s_ready, &r_ready, &u_ready, &dr_ready}) mbar_init(b, CHAIN_WARPS);
     for (uint64_t *b : {&do_ready, &dr_free}) mbar_init(b, 4);
     fence_mbar_init();
@@ -935,16 +933,22 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         const char *tiles = a.tiles + chunk_sh(i) * TILES;
         bulk_load(p + L_::Z, tiles, (wide ? 5 : 4) * TILE, bar);  // Z, P, Z's third part
         bulk_load(p + L_::GT, a.gates + chunk_sh(i) * GATES, GATES * 4, bar);
-        bulk_prefetch_l2(a.s_images + chunk_sh(i) * S_IMAGE, S_IMAGE);
         loaded = i + 1;
       };
       constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), id64n = idesc_bf16(128, 64, false, true);
       constexpr uint32_t idP = idesc_bf16(128, 64, true, true), idS = idesc_bf16(128, 128, false, true);
+      auto pdo = [&](int i) {  // dO^T P
+        const uint32_t dO = sb + stage(i) + L_::DO, p = sb + stage(i) + L_::P;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + B_PDO, mdesc(dO, ks, 8192), mdesc(p, ks, 8192), idP, ks);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + B_PDO, mdesc(dO, ks, 8192), mdesc(p + TILE, ks, 8192), idP, 1);
+      };
       bool ok = true;
       if (nch > 0) load(0);
       for (int i = 0; i < nch; ++i) {
         const uint32_t ph = (uint32_t)i & 1u;
-        const uint32_t st = sb + stage(i), k = st + L_::K, q = st + L_::Q, dO = st + L_::DO, z = st + L_::Z, p = st + L_::P;
+        const uint32_t st = sb + stage(i), k = st + L_::K, q = st + L_::Q, z = st + L_::Z;
         // every row of the chunk is what it should be (rows past the end cleared) with the state of the step
         ok = wait_full(i) && mbar_wait(&s_ready, ph, WAIT_CYCLES);
         if (!ok) break;
@@ -953,10 +957,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + B_D1, s_col(tb, ks), kdesc(k, ks, 64), id64, ks);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tb + B_D1, s_col(tb, ks) + 16u, kdesc(k, ks, 64), id64, 1);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + B_PDO, mdesc(dO, ks, 8192), mdesc(p, ks, 8192), idP, ks);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + B_PDO, mdesc(dO, ks, 8192), mdesc(p + TILE, ks, 8192), idP, 1);
+        if (i == 0) pdo(0);
         mma_commit(&x_full);
         // step i - 1 is through with its stage (its last product before s_ready, dO's copy in TMEM, gates copied)
         if (i + 1 < nch) load(i + 1);
@@ -967,6 +968,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 8u * ks, mdesc(q, ks, 8192), idS, ks);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 32u + 8u * ks, mdesc(q, ks, 8192), idS, 1);
+        mma_commit(&q_full);
         ok = mbar_wait(&r_ready, ph, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
@@ -994,6 +996,10 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_R + 32u + 8u * ks, mdesc(k, ks, 8192), idS, 1);
         mma_commit(&s_full);
+        if (i + 1 < nch) {  // a whole chunk, no rows to be cleared
+          if (!(ok = wait_full(i + 1))) break;
+          pdo(i + 1);
+        }
       }
       // no copy or product of this block is in flight when it leaves
       for (int i = max(0, loaded - 2); i < loaded; ++i)
@@ -1032,23 +1038,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         ok = ok && clear_rows(i);
         warp_arrive(&s_ready);
       });
-      // this thread's part of <S0, dS1>, while the products run (S0's image is on its way to L2 since the last step)
-      const char *s0i = a.s_images + chunk_sh(i) * S_IMAGE + img0;
-      float dot = 0.f;
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const uint4 h4 = __ldg(reinterpret_cast<const uint4 *>(s0i + n * UNITS));
-        const uint4 l4 = __ldg(reinterpret_cast<const uint4 *>(s0i + S_IMAGE / 2 + n * UNITS));
-        const uint32_t x[4] = {h4.x, h4.y, h4.z, h4.w}, y[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16), S[8 * n + 2 * m], dot);
-          dot = fmaf(__uint_as_float(x[m] & 0xffff0000u) + __uint_as_float(y[m] & 0xffff0000u), S[8 * n + 2 * m + 1], dot);
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      if (lane == 0) w_dot[i & 1][warp] = dot;  // read by the output warps behind this step's dr_ready
     };
     if (nch > 0) hand_state(0);
     for (int i = 0; i < nch; ++i) {
@@ -1163,12 +1152,21 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
       for (int c = 0; c < 64; c += 16) {
         const ColBf16 col(sb + stage(i) + L_::DO, c, v);
         uint32_t hi[8], lo[8];
+        uint16_t x[16];
 #pragma unroll
-        for (int n = 0; n < 16; n += 2) {
-          // rows past the end may be cleared or not yet
-          const float x = c + n < L ? bf16_bits_to_f32(lds_u16(col.at(n))) * (a.scale * gates[G_INTO + c + n]) : 0.f;
-          const float y = c + n + 1 < L ? bf16_bits_to_f32(lds_u16(col.at(n + 1))) * (a.scale * gates[G_INTO + c + n + 1]) : 0.f;
-          split2(x, y, hi[n / 2], lo[n / 2]);
+        for (int n = 0; n < 16; ++n) x[n] = lds_u16(col.at(n));
+#pragma unroll
+        for (int n = 0; n < 16; n += 4) {
+          const float4 e = *reinterpret_cast<const float4 *>(gates + G_INTO + c + n);
+          const float f[4] = {e.x, e.y, e.z, e.w};
+          float y[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) y[m] = bf16_bits_to_f32(x[n + m]) * (a.scale * f[m]);
+          if (L < CH)  // rows past the end may be cleared or not yet
+#pragma unroll
+            for (int m = 0; m < 4; ++m) y[m] = c + n + m < L ? y[m] : 0.f;
+          split2(y[0], y[1], hi[n / 2], lo[n / 2]);
+          split2(y[2], y[3], hi[n / 2 + 1], lo[n / 2 + 1]);
         }
         tmem_st8(tb + lanes + B_DO + c / 2, hi);
         tmem_st8(tb + lanes + B_DO + 32u + c / 2, lo);
@@ -1180,7 +1178,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
     if (nch > 0) put_do(0);
     for (int i = 0; i < nch; ++i) {
       const uint32_t ph = (uint32_t)i & 1u;
-      ok = ok && mbar_wait(&e_full, ph, WAIT_CYCLES);  // the product with q of step i before it
+      ok = ok && mbar_wait(&q_full, ph, WAIT_CYCLES);
       tc_fence_after();
       if (i + 1 < nch) put_do(i + 1);
       ok = ok && mbar_wait(&dr_ready, ph, WAIT_CYCLES);
@@ -1190,9 +1188,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         break;
       }
       if (tid == 0) {
-        float x = 0.f;
-        for (int w = 0; w < CHAIN_WARPS; ++w) x += w_dot[ph][w];
-        a.sdot[chunk_sh(i)] = x;
         bulk_store(a.r_images + chunk_sh(i) * R_IMAGE, sm + L_::R, R_IMAGE);
         bulk_commit();
       }
@@ -1237,11 +1232,12 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
 //     dPd = scale D (.) B1 diag(b), dA = -D (.) diag(b) B2 diag(b), db = diag(B2)
 //     dQ^T = scale e^G (S0 dO^T) + K^T dPd^T
 //     dK^T = -e^G b (S0 dR^T) + e^{G_C - G} b (dS1 E^T) + Q^T dPd + K^T (dA + dA^T)
-// One block per (chunk, head): 16 warps of elementwise work, one that copies
-// and multiplies.  The images of S0 and dS1 follow one another through the same 64 KB; the
-// products with two parts of a matrix put both into one operand of 128 columns
-// where tensor memory has room for the two results (a product of 64 columns
-// is bound by its other operand's way through shared memory).
+// One block per SM walks over (chunk, head) pairs: 16 warps of elementwise
+// work, one that copies and multiplies.  The images of S0 and dS1 follow one another
+// through the same 64 KB; the next pair's S0 and E are on their way while this
+// one's gradients leave.  Products with two parts of a matrix put both into one operand of
+// 128 columns where tensor memory has room for the two results (a product of 64
+// columns is bound by its other operand's way through shared memory).
 // TMEM columns: [0, 64) [q; k] k^T, [64, 192) B1, B2 of E's two parts, later [0, 128)
 // the pairs' part of dK^T (two halves); [192, 320) S0 dO^T, S0 dR^T; [320, 384)
 // K^T dPd^T; [384, 512) dS1 E^T (two halves).
@@ -1253,19 +1249,18 @@ struct GradMaps {
 };
 struct GradArgs {
   Docs docs;
+  int64_t units;  // slots x H
   int H, share, K;
   float scale;
   const float *g, *beta;
   const char *s_images, *ds_images, *e_images, *r_images;
-  const float *sdot;
   void *dq, *dk;  // bf16, or per value head in fp32
-  int per_head;
   float *dg, *dbeta;
   int *err;
 };
 struct GradSmem {
-  // S: S0's image, then dS1's; X1, X2: per 64 columns 64 rows of dO, 64 of dR (hi, lo); QK: of q and k;
-  // T: dPd hi, lo, dA hi, lo, W: pair weights, in X1's and X2's places once the products have read them
+  // S: S0's image, then dS1's; X1, X2: per 64 columns 64 rows of dO, 64 of dR (hi, lo); QK: of q and k.
+  // Once the products have read X1 and X2, T: dPd hi, lo, dA hi, lo; then dq and dk; W: pair weights
   static constexpr uint32_t S = 0, X1 = S + S_IMAGE, X2 = X1 + 32768, E = X2 + 32768, QK = E + E_IMAGE,
                             BYTES = QK + 32768 + 1024;
   static constexpr uint32_t T = X1, W = X2;
@@ -1274,33 +1269,29 @@ constexpr int WP = CH + 1;  // pitch of W
 static_assert(4 * TILE <= 32768 && CH * WP * 4 <= 32768, "");
 constexpr int GRAD_WARPS = 16, GRAD_THREADS = 544;
 
+template <bool PER_HEAD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __grid_constant__ GradMaps maps,
                                                                       const GradArgs a) {
   using L_ = GradSmem;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full, full_ds, cleared, g1, g2, tiles, g3;
+  __shared__ uint64_t full_a, full_b, full_ds, cleared, s0_read, g1, g2, tiles, g3, left, drain;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ alignas(16) float2 s_g[CH];
-  __shared__ alignas(16) float s_into[CH], s_ki[CH], s_ko[CH], s_beta[CH];  // scale e^G, -e^G b, e^{G_C - G} b, b
-  __shared__ float s_db[CH], s_pair[8][CH], s_red[2][4][CH], s_over;
+  __shared__ alignas(16) float4 s_g[CH];  // two parts of G (in units of log 2), b
+  __shared__ alignas(16) float s_into[CH], s_ki[CH], s_ko[CH];  // scale e^G, -e^G b, e^{G_C - G} b
+  __shared__ alignas(16) float s_tot[CH][4];
+  __shared__ float s_db[CH], s_pair[2][CH], s_red[2][4][CH], s_over, s_dot[GRAD_WARPS];
   __shared__ double warp0_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = (int)(blockIdx.x % a.H);
-  const int64_t slot = blockIdx.x / a.H, sh = slot * a.H + h;
-  int64_t tok;
-  int L;
-  if (!chunk_in_slot(a.docs, slot, tok, L)) return;
-  const int hq = h / a.share;
   if (warp == GRAD_WARPS) {
     tmem_alloc(&tmem_base, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     abort_flag = 0;
-    for (uint64_t *b : {&full, &full_ds, &g1, &g2, &g3}) mbar_init(b, 1);
-    for (uint64_t *b : {&cleared, &tiles}) mbar_init(b, GRAD_WARPS);
+    for (uint64_t *b : {&full_a, &full_b, &full_ds, &g1, &g2, &g3, &drain}) mbar_init(b, 1);
+    for (uint64_t *b : {&cleared, &s0_read, &tiles, &left}) mbar_init(b, GRAD_WARPS);
     fence_mbar_init();
   }
   tc_fence_before();
@@ -1308,30 +1299,56 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   tc_fence_after();
   const uint32_t tb = tmem_base, sb = smem_u32(sm);
   const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S;
+  // the first used unit from u on (units of unused slots are passed over)
+  auto find = [&](int64_t u, int64_t &tok, int &L) -> int64_t {
+    while (u < a.units && !chunk_in_slot(a.docs, u / a.H, tok, L)) u += gridDim.x;
+    return u;
+  };
   bool ok = true;
+  int64_t tok = 0;
+  int L = 0;
   if (warp == GRAD_WARPS) {
     if (lane == 0) {
-      mbar_expect_tx(&full, S_IMAGE + 2 * 32768 + E_IMAGE + 32768);
+      tma_prefetch_desc(&maps.q);
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.dO);
+      int loads_a = 0, loads_b = 0, loads_ds = 0;
+      auto load_a = [&](int64_t u) {
+        mbar_expect_tx(&full_a, S_IMAGE + E_IMAGE);
+        bulk_load(sm + L_::E, a.e_images + u * E_IMAGE, E_IMAGE, &full_a);
+        bulk_load(sm + L_::S, a.s_images + u * S_IMAGE, S_IMAGE, &full_a);
+        bulk_prefetch_l2(a.ds_images + u * S_IMAGE, S_IMAGE);
+        bulk_prefetch_l2(a.r_images + u * R_IMAGE, R_IMAGE);
+        ++loads_a;
+      };
+      auto load_b = [&](int64_t u) {
+        const int h = (int)(u % a.H), hq = h / a.share;
+        mbar_expect_tx(&full_b, 3 * 32768);
 #pragma unroll
-      for (int cb = 0; cb < 2; ++cb) {
-        tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full);
-        tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
-        tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
-        tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full);
-        bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + cb * 8192, 8192, &full);
-        bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + sh * R_IMAGE + 16384 + cb * 8192, 8192, &full);
-      }
-      bulk_load(sm + L_::E, a.e_images + sh * E_IMAGE, E_IMAGE, &full);
-      bulk_load(sm + L_::S, a.s_images + sh * S_IMAGE, S_IMAGE, &full);
-      bulk_prefetch_l2(a.ds_images + sh * S_IMAGE, S_IMAGE);
+        for (int cb = 0; cb < 2; ++cb) {
+          tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full_b);
+          tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full_b);
+          tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full_b);
+          tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full_b);
+          bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + u * R_IMAGE + cb * 8192, 8192, &full_b);
+          bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + u * R_IMAGE + 16384 + cb * 8192, 8192, &full_b);
+        }
+        ++loads_b;
+      };
       constexpr uint32_t idQK = idesc_bf16(128, 64, false, false), idB = idesc_bf16(128, 128, false, true);
       constexpr uint32_t idKN = idesc_bf16(128, 64, true, false), idMN = idesc_bf16(128, 64, true, true);
       constexpr uint32_t idKN2 = idesc_bf16(128, 128, true, false), idMN2 = idesc_bf16(128, 128, true, true);
       const uint32_t dp = sb + L_::T, da = dp + 2 * TILE;
-      bool issued_ds = false;
-      do {
-        ok = mbar_wait(&full, 0, WAIT_CYCLES) && mbar_wait(&cleared, 0, WAIT_CYCLES);
+      int64_t u = find(blockIdx.x, tok, L);
+      if (u < a.units) load_a(u);
+      for (int it = 0; u < a.units; ++it) {
+        const uint32_t ph = (uint32_t)it & 1u;
+        // the last unit's gradients have left (q, k, the stacks and tensor memory are free)
+        if (it >= 1 && !(ok = mbar_wait(&left, ph ^ 1u, WAIT_CYCLES))) break;
+        load_b(u);
+        ok = mbar_wait(&full_a, ph, WAIT_CYCLES) && mbar_wait(&full_b, ph, WAIT_CYCLES) && mbar_wait(&cleared, ph, WAIT_CYCLES);
         if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_QK, kdesc(q, ks, 128), kdesc(k, ks, 128), idQK, ks);
 #pragma unroll
@@ -1348,11 +1365,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, image_desc(si, ks), kdesc(x2 + 8192, ks, 128), idKN, 1);
         mma_commit(&g2);
-        if (!(ok = mbar_wait(&g2, 0, WAIT_CYCLES))) break;
+        if (!(ok = mbar_wait(&g2, ph, WAIT_CYCLES) && mbar_wait(&s0_read, ph, WAIT_CYCLES))) break;
         mbar_expect_tx(&full_ds, S_IMAGE);
-        bulk_load(sm + L_::S, a.ds_images + sh * S_IMAGE, S_IMAGE, &full_ds);
-        issued_ds = true;
-        if (!(ok = mbar_wait(&tiles, 0, WAIT_CYCLES))) break;
+        bulk_load(sm + L_::S, a.ds_images + u * S_IMAGE, S_IMAGE, &full_ds);
+        ++loads_ds;
+        if (!(ok = mbar_wait(&tiles, ph, WAIT_CYCLES))) break;
         tc_fence_after();
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -1364,256 +1381,336 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), mdesc(da, ks, TILE), idMN2, 1);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), kdesc(da, ks, 128), idKN2, 1);
-        if (!(ok = mbar_wait(&full_ds, 0, WAIT_CYCLES))) break;
+        if (!(ok = mbar_wait(&full_ds, ph, WAIT_CYCLES))) break;
         // dS1 hi [E hi | E lo], dS1 lo E hi
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(si, ks), image_desc(e, ks), idMN2, ks);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(si + S_IMAGE / 2, ks), image_desc(e, ks), idMN, 1);
         mma_commit(&g3);
-        ok = mbar_wait(&g3, 0, WAIT_CYCLES);
-      } while (false);
+        u = find(u + gridDim.x, tok, L);
+        if (!(ok = mbar_wait(&g3, ph, WAIT_CYCLES))) break;
+        if (u < a.units) load_a(u);
+      }
       if (!ok) {  // nothing of this block's is in flight when it leaves
-        mbar_wait(&full, 0, WAIT_CYCLES);
-        if (issued_ds) mbar_wait(&full_ds, 0, WAIT_CYCLES);
-        mma_commit(&g3);
-        mbar_wait(&g3, 0, WAIT_CYCLES);
+        if (loads_a) mbar_wait(&full_a, (uint32_t)(loads_a - 1) & 1u, WAIT_CYCLES);
+        if (loads_b) mbar_wait(&full_b, (uint32_t)(loads_b - 1) & 1u, WAIT_CYCLES);
+        if (loads_ds) mbar_wait(&full_ds, (uint32_t)(loads_ds - 1) & 1u, WAIT_CYCLES);
+        mma_commit(&drain);
+        mbar_wait(&drain, 0, WAIT_CYCLES);
         atomicExch(&abort_flag, 1);
       }
     }
     __syncwarp();
   } else {
-    // decays, while the copies run
-    const float over = a.sdot[sh];
-    double G = 0.0;
-    float b = 0.f;
-    if (tid < CH) {
-      if (tid < L) {
-        G = (double)fmaxf(a.g[(tok + tid) * a.H + h], -1e4f);
-        b = a.beta[(tok + tid) * a.H + h];
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, G, o);
-        if (lane >= o) G += y;
-      }
-      if (tid == 31) warp0_total = G;
-    }
-    named_bar(1, 32 * GRAD_WARPS);
-    if (tid < CH) {
-      if (warp == 1) G += warp0_total;
-      const float gh = (float)G;
-      s_g[tid] = make_float2(gh, (float)(G - (double)gh));
-      s_beta[tid] = b;
-    }
-    named_bar(1, 32 * GRAD_WARPS);
-    if (tid < CH) {
-      const float2 x = s_g[tid], z = s_g[63];
-      const float into = expf(x.x + x.y), out = expf((z.x - x.x) + (z.y - x.y));
-      s_into[tid] = a.scale * into;
-      s_ki[tid] = -into * b;
-      s_ko[tid] = out * b;
-      if (tid == 63) s_over = into * over;
-    }
-    if (L < CH) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
-      ok = mbar_wait(&full, 0, WAIT_CYCLES);
-      for (int n = tid; n < (CH - L) * 4 * 8; n += 32 * GRAD_WARPS) {
-        const int c = n % 8, t = n / 8 % 4, r = L + n / 32;
-        st_shared_v4(sb + L_::QK + t * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
-      }
-      fence_async_smem();
-    }
-    warp_arrive(&cleared);
-    // thread (row of the stack: lane of tensor memory, 16 of the columns)
+    // thread (row of the stack, later key channel: lane of tensor memory; 16 of the columns, tokens)
     const int grp = warp >> 2, qw = warp & 3, row = qw * 32 + lane, t = row & 63, c0 = 16 * grp;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     const bool isA = qw >= 2;
     float *W = reinterpret_cast<float *>(sm + L_::W);
-    ok = mbar_wait(&g1, 0, WAIT_CYCLES) && ok;
-    tc_fence_after();
-    float w[16];
-    {
-      uint32_t x[16], y[16];
-      tmem_ld16(tb + lanes + Q_B + c0, x);
-      tmem_ld16(tb + lanes + Q_B + 64u + c0, y);
-      tmem_ld_wait(x);
-      tmem_tie(y);
-      const float2 gt = s_g[t];
-      const float f = isA ? -s_beta[t] : 0.5f * a.scale;
-      const int last = t < L ? (isA ? t - 1 : t) : -1;
+    int64_t u = find(blockIdx.x, tok, L);
+    for (int it = 0; u < a.units; ++it) {
+      const uint32_t ph = (uint32_t)it & 1u;
+      const int h = (int)(u % a.H);
+      // decays, while the copies run
+      double G = 0.0;
+      float b = 0.f;
+      if (tid < CH) {
+        if (tid < L) {
+          G = (double)fmaxf(a.g[(tok + tid) * a.H + h], -1e4f) * 1.4426950408889634;
+          b = a.beta[(tok + tid) * a.H + h];
+        }
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        const int c = c0 + n;
-        const float B = __uint_as_float(x[n]) + __uint_as_float(y[n]);
-        if (isA && c == t) s_db[t] = B;
-        const float2 gc = s_g[c];
-        w[n] = c <= last ? f * s_beta[c] * expf((gt.x - gc.x) + (gt.y - gc.y)) * B : 0.f;
+        for (int o = 1; o < 32; o <<= 1) {
+          const double y = __shfl_up_sync(0xffffffffu, G, o);
+          if (lane >= o) G += y;
+        }
+        if (tid == 31) warp0_total = G;
       }
-      tmem_ld16(tb + lanes + Q_QK + c0, x);
-      tmem_ld_wait(x);
-      tc_fence_before();
-      ok = mbar_wait(&g2, 0, WAIT_CYCLES) && ok;  // the stacks have been read
-      const uint32_t tile = sb + L_::T + (isA ? 2 * TILE : 0);
-#pragma unroll
-      for (int n = 0; n < 16; n += 8) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int m = 0; m < 4; ++m) split2(w[n + 2 * m], w[n + 2 * m + 1], hi[m], lo[m]);
-        const uint32_t o = tile + sw128_off(t, c0 + n, 64);
-        st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
-        st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
+      named_bar(1, 32 * GRAD_WARPS);  // warp 0 is through with the last unit as well
+      if (tid < CH) {
+        if (warp == 1) G += warp0_total;
+        const float gh = (float)G;
+        s_g[tid] = make_float4(gh, (float)(G - (double)gh), b, 0.f);
       }
-      fence_async_smem();
-      warp_arrive(&tiles);
-#pragma unroll
-      for (int n = 0; n < 16; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
-    }
-    // sums of the pairs r >= t > s: rows of dA's part, dPd's added to them, summed along the rows, then down the columns
-    if (isA)
-#pragma unroll
-      for (int n = 0; n < 16; ++n) W[t * WP + c0 + n] = w[n];
-    named_bar(1, 32 * GRAD_WARPS);
-    if (!isA)
-#pragma unroll
-      for (int n = 0; n < 16; ++n) W[t * WP + c0 + n] += w[n];
-    named_bar(1, 32 * GRAD_WARPS);
-    if (tid < CH) {
-      float x = 0.f;
-#pragma unroll 16
-      for (int n = 0; n < CH; ++n) {
-        x += W[tid * WP + n];
-        W[tid * WP + n] = x;
+      named_bar(1, 32 * GRAD_WARPS);
+      if (tid < CH) {
+        const float4 x = s_g[tid], z = s_g[63];
+        const float into = exp2f(x.x + x.y), out = exp2f((z.x - x.x) + (z.y - x.y));
+        s_into[tid] = a.scale * into;
+        s_ki[tid] = -into * b;
+        s_ko[tid] = out * b;
+        if (tid == 63) s_over = into;
       }
-    }
-    named_bar(1, 32 * GRAD_WARPS);
-    {
-      const int c = tid & 63, r0 = (tid >> 6) * 8;  // 8 rows of a column
-      float x = 0.f;
+      if (L < CH) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
+        ok = ok && mbar_wait(&full_b, ph, WAIT_CYCLES);
+        for (int n = tid; n < (CH - L) * 4 * 8; n += 32 * GRAD_WARPS) {
+          const int c = n % 8, x = n / 8 % 4, r = L + n / 32;
+          st_shared_v4(sb + L_::QK + x * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+        }
+        fence_async_smem();
+      }
+      warp_arrive(&cleared);
+      {  // <S0, dS1>, while the first products run
+        const char *img = a.ds_images + u * S_IMAGE + tid * 16;
+        ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES);
+        float dot = 0.f;
 #pragma unroll
-      for (int r = r0; r < r0 + 8; ++r) x += c > 0 && r >= c ? W[r * WP + c - 1] : 0.f;
-      s_pair[tid >> 6][c] = x;
-    }
-    ok = mbar_wait(&g3, 0, WAIT_CYCLES) && ok;
-    tc_fence_after();
-    if (!__any_sync(0xffffffffu, !ok)) {
-      // lane: key channel; tokens c0 .. c0 + 15
-      const int ch = row;
-      const bool in = ch < a.K;
-      float rd[16], ad[16];  // what token t's query and key read of S0, what its key left in S1, of this channel
-      const ColBf16 cq(q, c0, ch, 16384u), ck(k, c0, ch, 16384u);
-      const int64_t at0 = ((tok + c0) * a.H + h) * (int64_t)a.K + ch, step = (int64_t)a.H * a.K;
+        for (int n = 0; n < 4; ++n) {
+          const uint4 dh = __ldg(reinterpret_cast<const uint4 *>(img + n * 8192));
+          const uint4 dl = __ldg(reinterpret_cast<const uint4 *>(img + S_IMAGE / 2 + n * 8192));
+          const uint4 hi = lds_u4(si + tid * 16 + n * 8192), lo = lds_u4(si + S_IMAGE / 2 + tid * 16 + n * 8192);
+          const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w};
+          const uint32_t v[4] = {dh.x, dh.y, dh.z, dh.w}, z[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16),
+                       __uint_as_float(v[m] << 16) + __uint_as_float(z[m] << 16), dot);
+            dot = fmaf(__uint_as_float(x[m] & 0xffff0000u) + __uint_as_float(y[m] & 0xffff0000u),
+                       __uint_as_float(v[m] & 0xffff0000u) + __uint_as_float(z[m] & 0xffff0000u), dot);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) s_dot[warp] = dot;
+        warp_arrive(&s0_read);
+      }
+      ok = ok && mbar_wait(&g1, ph, WAIT_CYCLES);
+      tc_fence_after();
+      float w[16];
       {
         uint32_t x[16], y[16];
-        tmem_ld16(tb + lanes + Q_1 + c0, x);
-        tmem_ld16(tb + lanes + Q_4 + c0, y);
+        tmem_ld16(tb + lanes + Q_B + c0, x);
+        tmem_ld16(tb + lanes + Q_B + 64u + c0, y);
         tmem_ld_wait(x);
         tmem_tie(y);
+        const float4 gt = s_g[t];
+        const float f = isA ? -gt.z : 0.5f * a.scale;
+        const int last = t < L ? (isA ? t - 1 : t) : -1;
+        if (c0 <= (t | 31)) {  // for the warp: one of its rows reaches these columns
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const int c = c0 + n;
+            const float B = __uint_as_float(x[n]) + __uint_as_float(y[n]);
+            if (isA && c == t) s_db[t] = B;
+            const float4 gc = s_g[c];
+            w[n] = c <= last ? f * gc.z * exp2f((gt.x - gc.x) + (gt.y - gc.y)) * B : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < 16; ++n) w[n] = 0.f;
+        }
+        tmem_ld16(tb + lanes + Q_QK + c0, x);
+        tmem_ld_wait(x);
+        tc_fence_before();
+        ok = ok && mbar_wait(&g2, ph, WAIT_CYCLES);  // the stacks have been read
+        const uint32_t tile = sb + L_::T + (isA ? 2 * TILE : 0);
+#pragma unroll
+        for (int n = 0; n < 16; n += 8) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) split2(w[n + 2 * m], w[n + 2 * m + 1], hi[m], lo[m]);
+          const uint32_t o = tile + sw128_off(t, c0 + n, 64);
+          st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
+          st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_async_smem();
+        warp_arrive(&tiles);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
+      }
+      // sums of the pairs r >= t > s: dPd's part and dA's of a row added, summed along the row, then down the columns
+      if (isA)
+#pragma unroll
+        for (int n = 0; n < 16; ++n) W[t * WP + c0 + n] = w[n];
+      named_bar(1, 32 * GRAD_WARPS);
+      if (!isA) {
+        float x = 0.f;
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const float qi = s_into[c0 + n] * __uint_as_float(x[n]);
-          rd[n] = qi * bf16_bits_to_f32(lds_u16(cq.at(n)));
-          const float dq = qi + __uint_as_float(y[n]);
-          if (in && c0 + n < L) {
-            if (a.per_head)
-              ((float *)a.dq)[at0 + n * step] = dq;
-            else
-              ((__nv_bfloat16 *)a.dq)[at0 + n * step] = __float2bfloat16_rn(dq);
+          x += w[n] + W[t * WP + c0 + n];
+          w[n] = x;
+        }
+        s_tot[t][grp] = x;
+      }
+      named_bar(1, 32 * GRAD_WARPS);
+      if (!isA) {
+        const float4 tot = *reinterpret_cast<const float4 *>(s_tot[t]);
+        const float before = (grp > 0 ? tot.x : 0.f) + (grp > 1 ? tot.y : 0.f) + (grp > 2 ? tot.z : 0.f);
+        // token c + 1 takes the sums up to column c of the rows from it on
+#pragma unroll
+        for (int n = 0; n < 16; ++n) w[n] = t > c0 + n ? w[n] + before : 0.f;
+#pragma unroll
+        for (int n = 0; n < 16; ++n) w[n] += __shfl_xor_sync(0xffffffffu, w[n], 16);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+          const bool up = (lane & o) != 0;
+#pragma unroll
+          for (int n = 0; n < o; ++n) {
+            const float y = __shfl_xor_sync(0xffffffffu, up ? w[n] : w[n + o], o);
+            w[n] = (up ? w[n + o] : w[n]) + y;
           }
         }
+        if (lane < 16 && c0 + lane + 1 < CH) s_pair[qw][c0 + lane + 1] = w[0];
+        if (lane == 0 && grp == 0) s_pair[qw][0] = 0.f;
       }
+      ok = ok && mbar_wait(&g3, ph, WAIT_CYCLES) && mbar_wait(&full_b, ph, WAIT_CYCLES);
+      tc_fence_after();
       {
-        uint32_t x[16], y[16], z[16];
-        float ko[16];
-        tmem_ld16(tb + lanes + Q_3 + c0, x);
-        tmem_ld16(tb + lanes + Q_3 + 64u + c0, y);
-        tmem_ld_wait(x);
-        tmem_tie(y);
+        // lane: key channel; tokens c0 .. c0 + 15
+        const int ch = row;
+        float rd[16], ad[16];  // what token t's query and key read of S0, what its key left in S1, of this channel
+        const ColBf16 cq(q, c0, ch, 16384u), ck(k, c0, ch, 16384u), oq(sb + L_::X1, c0, ch), ok_(sb + L_::X1 + 16384, c0, ch);
+        float *fq = (float *)a.dq + ((tok + c0) * a.H + h) * (int64_t)a.K + ch;
+        float *fk = (float *)a.dk + ((tok + c0) * a.H + h) * (int64_t)a.K + ch;
+        const int64_t step = (int64_t)a.H * a.K;
+        const int rows = PER_HEAD && ch < a.K ? L - c0 : 0;
+        {
+          uint32_t x[16], y[16];
+          uint16_t qv[16];
+          tmem_ld16(tb + lanes + Q_1 + c0, x);
+          tmem_ld16(tb + lanes + Q_4 + c0, y);
 #pragma unroll
-        for (int n = 0; n < 16; ++n) ko[n] = s_ko[c0 + n] * (__uint_as_float(x[n]) + __uint_as_float(y[n]));
-        tmem_ld16(tb + lanes + Q_2 + c0, x);
-        tmem_ld16(tb + lanes + Q_5 + c0, y);
-        tmem_ld16(tb + lanes + Q_5 + 64u + c0, z);
-        tmem_ld_wait(x);
-        tmem_tie(y);
-        tmem_tie(z);
+          for (int n = 0; n < 16; ++n) qv[n] = lds_u16(cq.at(n));
+          tmem_ld_wait(x);
+          tmem_tie(y);
+#pragma unroll
+          for (int n = 0; n < 16; n += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(s_into + c0 + n);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const float qi = f[m] * __uint_as_float(x[n + m]);
+              rd[n + m] = qi * bf16_bits_to_f32(qv[n + m]);
+              const float dq = qi + __uint_as_float(y[n + m]);
+              if (PER_HEAD) {
+                if (n + m < rows) fq[(n + m) * step] = dq;
+              } else {
+                sts_u16(oq.at(n + m), f32_to_bf16_bits(dq));
+              }
+            }
+          }
+        }
+        {
+          uint32_t x[16], y[16], z[16];
+          float ko[16];
+          uint16_t kv[16];
+          tmem_ld16(tb + lanes + Q_3 + c0, x);
+          tmem_ld16(tb + lanes + Q_3 + 64u + c0, y);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) kv[n] = lds_u16(ck.at(n));
+          tmem_ld_wait(x);
+          tmem_tie(y);
+#pragma unroll
+          for (int n = 0; n < 16; n += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(s_ko + c0 + n);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) ko[n + m] = f[m] * (__uint_as_float(x[n + m]) + __uint_as_float(y[n + m]));
+          }
+          tmem_ld16(tb + lanes + Q_2 + c0, x);
+          tmem_ld16(tb + lanes + Q_5 + c0, y);
+          tmem_ld16(tb + lanes + Q_5 + 64u + c0, z);
+          tmem_ld_wait(x);
+          tmem_tie(y);
+          tmem_tie(z);
+#pragma unroll
+          for (int n = 0; n < 16; n += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(s_ki + c0 + n);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              const int r = n + m;
+              const float ki = f[m] * __uint_as_float(x[r]), kx = bf16_bits_to_f32(kv[r]);
+              rd[r] = fmaf(kx, ki, rd[r]);
+              ad[r] = kx * ko[r];
+              const float dk = (ki + ko[r]) + (__uint_as_float(y[r]) + __uint_as_float(z[r]));
+              if (PER_HEAD) {
+                if (r < rows) fk[r * step] = dk;
+              } else {
+                sts_u16(ok_.at(r), f32_to_bf16_bits(dk));
+              }
+            }
+          }
+        }
+        // summed over the warp's channels: lanes n and n + 16 get token c0 + n
 #pragma unroll
         for (int n = 0; n < 16; ++n) {
-          const float ki = s_ki[c0 + n] * __uint_as_float(x[n]);
-          const float kx = bf16_bits_to_f32(lds_u16(ck.at(n)));
-          rd[n] = fmaf(kx, ki, rd[n]);
-          ad[n] = kx * ko[n];
-          const float dk = (ki + ko[n]) + (__uint_as_float(y[n]) + __uint_as_float(z[n]));
-          if (in && c0 + n < L) {
-            if (a.per_head)
-              ((float *)a.dk)[at0 + n * step] = dk;
-            else
-              ((__nv_bfloat16 *)a.dk)[at0 + n * step] = __float2bfloat16_rn(dk);
+          rd[n] += __shfl_xor_sync(0xffffffffu, rd[n], 16);
+          ad[n] += __shfl_xor_sync(0xffffffffu, ad[n], 16);
+        }
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+          const bool up = (lane & o) != 0;
+#pragma unroll
+          for (int n = 0; n < o; ++n) {
+            const float r1 = __shfl_xor_sync(0xffffffffu, up ? rd[n] : rd[n + o], o);
+            const float r2 = __shfl_xor_sync(0xffffffffu, up ? ad[n] : ad[n + o], o);
+            rd[n] = (up ? rd[n + o] : rd[n]) + r1;
+            ad[n] = (up ? ad[n + o] : ad[n]) + r2;
+          }
+        }
+        if (lane < 16) {
+          s_red[0][qw][c0 + lane] = rd[0];
+          s_red[1][qw][c0 + lane] = ad[0];
+        }
+      }
+      tc_fence_before();
+      // the gradients are in shared memory; everyone hears of a wait that ran out
+      if (named_bar_any(1, 32 * GRAD_WARPS, !ok)) {
+        ok = false;
+        break;
+      }
+      if (!PER_HEAD) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int i = tid + 512 * (n & 1), r = i >> 4, c = (i & 15) * 8;
+          if (r < L && c < a.K) {
+            const uint4 x = lds_u4(sb + L_::X1 + (n >> 1) * 16384 + sw128_off(r, c, 64));
+            __nv_bfloat16 *dst = (__nv_bfloat16 *)(n >> 1 ? a.dk : a.dq) + ((tok + r) * a.H + h) * (int64_t)a.K + c;
+            st_global_v4(dst, x.x, x.y, x.z, x.w);
           }
         }
       }
-      // summed over the warp's channels: lanes n and n + 16 get token c0 + n
+      fence_async_smem();
+      warp_arrive(&left);
+      if (warp == 0) {
+        // tokens lane and lane + 32: sums over the tokens from them on of what is read, over those before of what is left
+        float r0 = 0.f, r1 = 0.f, d0 = 0.f, d1 = 0.f;
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        rd[n] += __shfl_xor_sync(0xffffffffu, rd[n], 16);
-        ad[n] += __shfl_xor_sync(0xffffffffu, ad[n], 16);
-      }
-#pragma unroll
-      for (int o = 8; o; o >>= 1) {
-        const bool up = (lane & o) != 0;
-#pragma unroll
-        for (int n = 0; n < o; ++n) {
-          const float r1 = __shfl_xor_sync(0xffffffffu, up ? rd[n] : rd[n + o], o);
-          const float r2 = __shfl_xor_sync(0xffffffffu, up ? ad[n] : ad[n + o], o);
-          rd[n] = (up ? rd[n + o] : rd[n]) + r1;
-          ad[n] = (up ? ad[n + o] : ad[n]) + r2;
+        for (int n = 0; n < 4; ++n) {
+          r0 += s_red[0][n][lane];
+          r1 += s_red[0][n][lane + 32];
+          d0 += s_red[1][n][lane];
+          d1 += s_red[1][n][lane + 32];
         }
-      }
-      if (lane < 16) {
-        s_red[0][qw][c0 + lane] = rd[0];
-        s_red[1][qw][c0 + lane] = ad[0];
-      }
-    } else {
-      ok = false;
-    }
-    if (!ok) atomicExch(&abort_flag, 1);
-    named_bar(1, 32 * GRAD_WARPS);
-    if (warp == 0) {
-      // tokens lane and lane + 32: sums over the tokens from them on of what is read, over those before of what is left
-      float r0 = 0.f, r1 = 0.f, d0 = 0.f, d1 = 0.f, p0 = 0.f, p1 = 0.f;
+        const float p0 = s_pair[0][lane] + s_pair[1][lane], p1 = s_pair[0][lane + 32] + s_pair[1][lane + 32];
+        const float own0 = d0, own1 = d1;
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        r0 += s_red[0][n][lane];
-        r1 += s_red[0][n][lane + 32];
-        d0 += s_red[1][n][lane];
-        d1 += s_red[1][n][lane + 32];
-      }
+        for (int o = 1; o < 32; o <<= 1) {
+          const float a0 = __shfl_down_sync(0xffffffffu, r0, o), a1 = __shfl_down_sync(0xffffffffu, r1, o);
+          const float b0 = __shfl_up_sync(0xffffffffu, d0, o), b1 = __shfl_up_sync(0xffffffffu, d1, o);
+          if (lane + o < 32) r0 += a0, r1 += a1;
+          if (lane >= o) d0 += b0, d1 += b1;
+        }
+        r0 += __shfl_sync(0xffffffffu, r1, 0);
+        d1 += __shfl_sync(0xffffffffu, d0, 31);
+        float over = 0.f;
 #pragma unroll
-      for (int n = 0; n < 8; ++n) {
-        p0 += s_pair[n][lane];
-        p1 += s_pair[n][lane + 32];
-      }
-      const float own0 = d0, own1 = d1;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float a0 = __shfl_down_sync(0xffffffffu, r0, o), a1 = __shfl_down_sync(0xffffffffu, r1, o);
-        const float b0 = __shfl_up_sync(0xffffffffu, d0, o), b1 = __shfl_up_sync(0xffffffffu, d1, o);
-        if (lane + o < 32) r0 += a0, r1 += a1;
-        if (lane >= o) d0 += b0, d1 += b1;
-      }
-      r0 += __shfl_sync(0xffffffffu, r1, 0);
-      d1 += __shfl_sync(0xffffffffu, d0, 31);
-      const float o_ = s_over;
-      if (*(volatile int *)&abort_flag == 0) {
+        for (int n = 0; n < GRAD_WARPS; ++n) over += s_dot[n];
+        over *= s_over;
         if (lane < L) {
-          a.dg[(tok + lane) * a.H + h] = (p0 + o_) + (r0 + (d0 - own0));
+          a.dg[(tok + lane) * a.H + h] = (p0 + over) + (r0 + (d0 - own0));
           a.dbeta[(tok + lane) * a.H + h] = s_db[lane];
         }
         if (lane + 32 < L) {
-          a.dg[(tok + lane + 32) * a.H + h] = (p1 + o_) + (r1 + (d1 - own1));
+          a.dg[(tok + lane + 32) * a.H + h] = (p1 + over) + (r1 + (d1 - own1));
           a.dbeta[(tok + lane + 32) * a.H + h] = s_db[lane + 32];
         }
       }
+      u = find(u + gridDim.x, tok, L);
     }
+    if (!ok) atomicExch(&abort_flag, 1);
   }
   tc_fence_before();
   __syncthreads();
@@ -1637,7 +1734,7 @@ bool tc_supported(const glacore_problem *p) {
 // Scratch (byte offsets): tiles and gates of every chunk and head, the backward's images.
 namespace {
 struct TcLayout {
-  size_t tiles, gates, s, ds, e, r, sdot, total;
+  size_t tiles, gates, s, ds, e, r, total;
 };
 TcLayout tc_layout(int64_t slots, int64_t H, bool backward) {
   TcLayout l;
@@ -1654,7 +1751,6 @@ TcLayout tc_layout(int64_t slots, int64_t H, bool backward) {
     take(l.ds, S_IMAGE);
     take(l.e, E_IMAGE);
     take(l.r, R_IMAGE);
-    take(l.sdot, sizeof(float));
   }
   l.total = off;
   return l;
@@ -1753,10 +1849,8 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   b.dv = (__nv_bfloat16 *)dv;
   b.tiles = a.tiles;
   b.gates = a.gates;
-  b.s_images = a.s_images;
   b.ds_images = ws + l.ds;
   b.r_images = ws + l.r;
-  b.sdot = (float *)(ws + l.sdot);
   b.err = a.err;
   e = launch(delta_back_kernel, c.docs.n * c.p.H, CHAIN_THREADS, BackSmem::BYTES, c, BackMaps{m.q, m.k, m.dO}, b,
              "delta_back");
@@ -1773,14 +1867,17 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   g.ds_images = b.ds_images;
   g.e_images = a.e_images;
   g.r_images = b.r_images;
-  g.sdot = b.sdot;
   g.dq = dq;
   g.dk = dk;
-  g.per_head = per_head;
   g.dg = dg;
   g.dbeta = dbeta;
   g.err = a.err;
-  return launch(delta_grads_kernel, c.slots * c.p.H, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g, "delta_grads");
+  g.units = c.slots * c.p.H;
+  const int64_t blocks = std::min(g.units, tc::sm_count());
+  return per_head ? launch(delta_grads_kernel<true>, blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
+                           "delta_grads")
+                  : launch(delta_grads_kernel<false>, blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
+                           "delta_grads");
 }
 
 }  // namespace delta
