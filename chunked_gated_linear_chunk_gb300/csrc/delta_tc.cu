@@ -961,14 +961,6 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         mma_commit(&x_full);
         // step i - 1 is through with its stage (its last product before s_ready, dO's copy in TMEM, gates copied)
         if (i + 1 < nch) load(i + 1);
-        ok = mbar_wait(&do_ready, ph, WAIT_CYCLES);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 8u * ks, mdesc(q, ks, 8192), idS, ks);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 32u + 8u * ks, mdesc(q, ks, 8192), idS, 1);
-        mma_commit(&q_full);
         ok = mbar_wait(&r_ready, ph, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
@@ -988,6 +980,14 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
           for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_D1, tb + B_R + 8u * ks, mdesc(z3, ks, 8192), id64n, 1);
         }
         mma_commit(&e_full);
+        ok = mbar_wait(&do_ready, ph, WAIT_CYCLES);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 8u * ks, mdesc(q, ks, 8192), idS, ks);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) mma_bf16_ta(tb + B_DS, tb + B_DO + 32u + 8u * ks, mdesc(q, ks, 8192), idS, 1);
+        mma_commit(&q_full);
         ok = mbar_wait(&u_ready, ph, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
@@ -1154,7 +1154,7 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
         uint32_t hi[8], lo[8];
         uint16_t x[16];
 #pragma unroll
-        for (int n = 0; n < 16; ++n) x[n] = lds_u16(col.at(n));
+        for (int n = 0; n < 16; ++n) x[n] = ld_u16(sm + (col.at(n) - sb));
 #pragma unroll
         for (int n = 0; n < 16; n += 4) {
           const float4 e = *reinterpret_cast<const float4 *>(gates + G_INTO + c + n);
@@ -1197,8 +1197,8 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_back_kernel(const __gr
       for (int n = 0; n < 8; ++n) {
         const int e = tid + 128 * n, r = e >> 4, c = (e & 15) * 8;
         if (r < L && c < a.V) {
-          const uint32_t o = sb + L_::R + sw128_off(r, c, 64);
-          const uint4 x = lds_u4(o), y = lds_u4(o + 16384u);
+          const uint32_t o = L_::R + sw128_off(r, c, 64);
+          const uint4 x = *reinterpret_cast<const uint4 *>(sm + o), y = *reinterpret_cast<const uint4 *>(sm + o + 16384u);
           const float b = w_beta[i % 3][r];
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
           uint32_t w[4];
@@ -1408,18 +1408,39 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     const bool isA = qw >= 2;
     float *W = reinterpret_cast<float *>(sm + L_::W);
-    int64_t u = find(blockIdx.x, tok, L);
-    for (int it = 0; u < a.units; ++it) {
+    // the next unit, its tokens and gates, looked up while this one is worked on
+    int64_t next = 0, tok_next = 0;
+    int L_next = 0;
+    float g_next = 0.f, b_next = 0.f;
+    auto look = [&](int64_t from) {
+      next = find(from, tok_next, L_next);
+      g_next = b_next = 0.f;
+      if (next < a.units && tid < CH && tid < L_next) {
+        const int64_t at = (tok_next + tid) * a.H + next % a.H;
+        g_next = a.g[at];
+        b_next = a.beta[at];
+      }
+    };
+    look(blockIdx.x);
+    for (int it = 0; next < a.units; ++it) {
       const uint32_t ph = (uint32_t)it & 1u;
+      const int64_t u = next;
       const int h = (int)(u % a.H);
-      // decays, while the copies run
-      double G = 0.0;
-      float b = 0.f;
-      if (tid < CH) {
-        if (tid < L) {
-          G = (double)fmaxf(a.g[(tok + tid) * a.H + h], -1e4f) * 1.4426950408889634;
-          b = a.beta[(tok + tid) * a.H + h];
+      tok = tok_next;
+      L = L_next;
+      uint4 dh[4], dl[4];  // of dS1's image, for <S0, dS1>
+      {
+        const char *img = a.ds_images + u * S_IMAGE + tid * 16;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          dh[n] = __ldg(reinterpret_cast<const uint4 *>(img + n * 8192));
+          dl[n] = __ldg(reinterpret_cast<const uint4 *>(img + S_IMAGE / 2 + n * 8192));
         }
+      }
+      // decays, while the copies run
+      double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;
+      const float b = b_next;
+      if (tid < CH) {
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const double y = __shfl_up_sync(0xffffffffu, G, o);
@@ -1452,16 +1473,13 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       }
       warp_arrive(&cleared);
       {  // <S0, dS1>, while the first products run
-        const char *img = a.ds_images + u * S_IMAGE + tid * 16;
         ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES);
         float dot = 0.f;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-          const uint4 dh = __ldg(reinterpret_cast<const uint4 *>(img + n * 8192));
-          const uint4 dl = __ldg(reinterpret_cast<const uint4 *>(img + S_IMAGE / 2 + n * 8192));
           const uint4 hi = lds_u4(si + tid * 16 + n * 8192), lo = lds_u4(si + S_IMAGE / 2 + tid * 16 + n * 8192);
           const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w};
-          const uint32_t v[4] = {dh.x, dh.y, dh.z, dh.w}, z[4] = {dl.x, dl.y, dl.z, dl.w};
+          const uint32_t v[4] = {dh[n].x, dh[n].y, dh[n].z, dh[n].w}, z[4] = {dl[n].x, dl[n].y, dl[n].z, dl[n].w};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16),
@@ -1519,6 +1537,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
 #pragma unroll
         for (int n = 0; n < 16; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
       }
+      look(u + gridDim.x);
       // sums of the pairs r >= t > s: dPd's part and dA's of a row added, summed along the row, then down the columns
       if (isA)
 #pragma unroll
@@ -1708,7 +1727,6 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
           a.dbeta[(tok + lane + 32) * a.H + h] = s_db[lane + 32];
         }
       }
-      u = find(u + gridDim.x, tok, L);
     }
     if (!ok) atomicExch(&abort_flag, 1);
   }
