@@ -84,16 +84,68 @@ struct PrepMaps {
   CUtensorMap q, k;
 };
 struct PrepSmem {
-  float N[CH][NP], Z[CH][NP], W[32][36];
-  float2 G[CH];  // two parts of the decay exponent
+  float N[CH][NP];  // N, block by block replaced by Z
+  float2 G[CH];     // two parts of the decay exponent
   float beta[CH];
 };
+constexpr int WPITCH = 36;  // of W, in the place of Z's tiles until those are made
 constexpr uint32_t PREP_BYTES = 32768 + sizeof(PrepSmem) + 1024;
+constexpr int PREP_THREADS = 256;
 
-__global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__ PrepMaps maps, const PrepArgs a) {
+__device__ __forceinline__ void tmem_ld8(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+               :
+               : "memory");
+}
+
+// ROWS rows of a column of the block below a pair of diagonal ones (rows and
+// columns r .. r + M - 1 and r + M .. r + 2 M - 1): W, a barrier, then Z21.
+template <int M, int ROWS, typename B>
+__device__ __forceinline__ void below(PrepSmem &s, float *W, int r, int j, int i0, B barrier) {
+  float w[ROWS];
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) w[i] = -s.N[r + M + i0 + i][r + j];
+#pragma unroll
+  for (int c = 0; c < M; c += 4) {
+    const float4 b = *reinterpret_cast<const float4 *>(&s.beta[r + c]);
+    const float z[4] = {b.x * s.N[r + c][r + j], b.y * s.N[r + c + 1][r + j], b.z * s.N[r + c + 2][r + j],
+                        b.w * s.N[r + c + 3][r + j]};
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + M + i0 + i][r + c]);
+      w[i] = fmaf(-n.x, z[0], fmaf(-n.y, z[1], fmaf(-n.z, z[2], fmaf(-n.w, z[3], w[i]))));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) W[(i0 + i) * WPITCH + j] = w[i];
+  barrier();
+#pragma unroll
+  for (int c = 0; c < M; c += 4) {
+    const float4 b = *reinterpret_cast<const float4 *>(&s.beta[r + M + c]);
+    const float z[4] = {b.x * W[c * WPITCH + j], b.y * W[(c + 1) * WPITCH + j], b.z * W[(c + 2) * WPITCH + j],
+                        b.w * W[(c + 3) * WPITCH + j]};
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + M + i0 + i][r + M + c]);
+      w[i] = fmaf(n.x, z[0], fmaf(n.y, z[1], fmaf(n.z, z[2], fmaf(n.w, z[3], w[i]))));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) s.N[r + M + i0 + i][r + j] = w[i];
+}
+
+__global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __grid_constant__ PrepMaps maps,
+                                                                     const PrepArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // [q; k] tiles, then Z and P
   PrepSmem &s = *reinterpret_cast<PrepSmem *>(sm + 32768);
+  float *W = reinterpret_cast<float *>(sm);
   __shared__ uint64_t full, done;
   __shared__ uint32_t tmem_base;
   __shared__ double warp0_total;
@@ -103,21 +155,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
   int64_t tok;
   int L;
   if (!chunk_in_slot(a.docs, slot, tok, L)) return;
-  if (warp == 0) {
-    tmem_alloc(&tmem_base, 64);
-    tmem_relinquish();
-  }
   if (tid == 0) {
     mbar_init(&full, 1);
     mbar_init(&done, 1);
     fence_mbar_init();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tb = tmem_base;
-  bool ok = true;
-  if (tid == 0) {
     mbar_expect_tx(&full, 32768);
 #pragma unroll
     for (int cb = 0; cb < 2; ++cb) {  // 64 channels: 64 rows of q, then 64 of k
@@ -125,7 +166,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
       tma_load_3d(sm + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
     }
   }
-  const int t = tid & 63;
+  if (warp == 1) {
+    tmem_alloc(&tmem_base, 64);
+    tmem_relinquish();
+  }
   // gates of head e of the group, loaded a head ahead; then their prefix sums
   float g_next = 0.f, b_next = 0.f;
   auto fetch = [&](int e) {
@@ -136,7 +180,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
       b_next = a.beta[at];
     }
   };
-  auto scan = [&]() {  // ends with a barrier of the block
+  auto scan = [&]() {  // begins and ends with a barrier of the block
     double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;  // e^g of less is 0 as well
     const float b = b_next;
     if (tid < CH) {
@@ -151,14 +195,18 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
     if (tid < CH) {
       if (warp == 1) G += warp0_total;
       const float gh = (float)G;
-      s.G[t] = make_float2(gh, (float)(G - (double)gh));
-      s.beta[t] = b;
+      s.G[tid] = make_float2(gh, (float)(G - (double)gh));
+      s.beta[tid] = b;
     }
     __syncthreads();
   };
   fetch(0);
+  tc_fence_before();
   scan();
+  tc_fence_after();
+  const uint32_t tb = tmem_base;
   fetch(1);
+  bool ok = true;
   if (tid == 0) {
     ok = mbar_wait(&full, 0, WAIT_CYCLES);
     const uint32_t base = smem_u32(sm);
@@ -174,13 +222,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
   ok = !__syncthreads_or(!ok);
   if (ok) {
     tc_fence_after();
-    // thread tid < 64: row tid of Q K^T; else row tid - 64 of K K^T
-    uint32_t r0[32], r1[32];
-    const uint32_t at = tb + ((uint32_t)(warp * 32) << 16);
-    tmem_ld32(at, r0);
-    tmem_ld32(at + 32, r1);
-    tmem_ld_wait32(r0);
-    tmem_ld_wait32(r1);
+    // thread (row of the stack, half of the columns): rows < 64 of Q K^T, the others of K K^T
+    const int row = (warp & 3) * 32 + lane, t = row & 63, half = warp >> 2;
+    const bool isP = (warp & 3) < 2;
+    const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16);
     for (int e = 0; e < a.share; ++e) {
       const int h = hq * a.share + e;
       const int64_t sh = slot * a.H + h;
@@ -190,7 +235,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
         fetch(e + 1);
       }
       const float2 gt = s.G[t];
-      if (tid < CH) {
+      if (isP && half == 0) {
         const float2 last = s.G[63];
         float *gs = a.gates + sh * GATES;
         gs[G_INTO + t] = exp2f(gt.x + gt.y);
@@ -199,23 +244,24 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
         if (t == 0) gs[G_OVER] = exp2f(last.x + last.y);
       }
       // row t, columns s <= t (P) or s < t (N): scale D (.) QK^T, D (.) KK^T
-      const int last = t < L ? (tid < CH ? t : t - 1) : -1;
-      const float f = tid < CH ? a.scale : 1.f;
+      const int last = t < L ? (isP ? t : t - 1) : -1;
+      const float f = isP ? a.scale : 1.f;
 #pragma unroll
-      for (int c0 = 0; c0 < 64; c0 += 8) {
-        alignas(16) float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < 32; n += 8) {
+        const int c0 = 32 * half + n;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if (c0 <= (t | 31)) {  // for the warp: one of its rows reaches these columns
+          uint32_t m[8];
+          tmem_ld8(at + c0, m);
+          tmem_ld_wait8(m);
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
-            const int c = c0 + i;
-            const float4 gc = *reinterpret_cast<const float4 *>(&s.G[c]);
-            const float m0 = __uint_as_float(c < 32 ? r0[c & 31] : r1[c & 31]);
-            const float m1 = __uint_as_float(c < 32 ? r0[(c + 1) & 31] : r1[(c + 1) & 31]);
-            x[i] = c <= last ? f * exp2f((gt.x - gc.x) + (gt.y - gc.y)) * m0 : 0.f;
-            x[i + 1] = c + 1 <= last ? f * exp2f((gt.x - gc.z) + (gt.y - gc.w)) * m1 : 0.f;
+            const float4 gc = *reinterpret_cast<const float4 *>(&s.G[c0 + i]);
+            x[i] = c0 + i <= last ? f * exp2f((gt.x - gc.x) + (gt.y - gc.y)) * __uint_as_float(m[i]) : 0.f;
+            x[i + 1] = c0 + i + 1 <= last ? f * exp2f((gt.x - gc.z) + (gt.y - gc.w)) * __uint_as_float(m[i + 1]) : 0.f;
           }
         }
-        if (tid < CH) {
+        if (isP) {
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
@@ -227,128 +273,63 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
           *reinterpret_cast<float4 *>(&s.N[t][c0 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
         }
       }
-      if (warp >= 2) {  // Z of the four diagonal blocks, two by a warp, a column by a thread
-        named_bar(1, 64);
-        const int r = (warp - 2) * 32 + (lane & 16), j = lane & 15;
-        float zb[16];
+      if (!isP) {
+        named_bar(1, 128);
+        if (half == 0) {  // Z of the four diagonal blocks, two by a warp, a column by a thread, in N's place
+          const int r = (warp - 2) * 32 + (lane & 16), j = lane & 15;
+          float zb[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float z0 = -s.N[r + i][r + j], z1 = 0.f;
+          for (int i = 0; i < 16; ++i) {
+            float z0 = -s.N[r + i][r + j], z1 = 0.f;
 #pragma unroll
-          for (int c = 0; c < i; c += 4) {
-            const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + i][r + c]);
-            z0 = fmaf(-n.x, zb[c], z0);
-            if (c + 1 < i) z1 = fmaf(-n.y, zb[c + 1], z1);
-            if (c + 2 < i) z0 = fmaf(-n.z, zb[c + 2], z0);
-            if (c + 3 < i) z1 = fmaf(-n.w, zb[c + 3], z1);
+            for (int c = 0; c < i; c += 4) {
+              const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + i][r + c]);
+              z0 = fmaf(-n.x, zb[c], z0);
+              if (c + 1 < i) z1 = fmaf(-n.y, zb[c + 1], z1);
+              if (c + 2 < i) z0 = fmaf(-n.z, zb[c + 2], z0);
+              if (c + 3 < i) z1 = fmaf(-n.w, zb[c + 3], z1);
+            }
+            const float z = z0 + z1;
+            zb[i] = z * s.beta[r + i];
+            __syncwarp();
+            s.N[r + i][r + j] = z;
           }
-          const float z = z0 + z1;
-          s.Z[r + i][r + j] = z;
-          zb[i] = z * s.beta[r + i];
         }
       }
       __syncthreads();
-      // the block below each pair of them: warps 0, 1 the first pair, four rows of a column by a thread
-      {
-        const int r = (warp >> 1) * 32, j = lane & 15, i0 = 8 * (warp & 1) + 4 * (lane >> 4);
-        float w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = -s.N[r + 16 + i0 + i][r + j];
-#pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          float z[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) z[x] = s.beta[r + c + x] * s.Z[r + c + x][r + j];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + 16 + i0 + i][r + c]);
-            w[i] = fmaf(-n.x, z[0], fmaf(-n.y, z[1], fmaf(-n.z, z[2], fmaf(-n.w, z[3], w[i]))));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s.W[i0 + i][(warp >> 1) * 16 + j] = w[i];
-        named_bar(2 + (warp >> 1), 64);
-#pragma unroll
-        for (int c = 0; c < 16; c += 4) {
-          float z[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) z[x] = s.beta[r + 16 + c + x] * s.W[c + x][(warp >> 1) * 16 + j];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 n = *reinterpret_cast<const float4 *>(&s.Z[r + 16 + i0 + i][r + 16 + c]);
-            w[i] = fmaf(n.x, z[0], fmaf(n.y, z[1], fmaf(n.z, z[2], fmaf(n.w, z[3], w[i]))));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s.Z[r + 16 + i0 + i][r + j] = w[i];
-          s.Z[r + i0 + i][r + 16 + j] = 0.f;
-        }
-      }
+      // the block below each pair of them, then the one below both
+      below<16, 2>(s, W + half * 16 * WPITCH, half * 32, lane & 15, 4 * (warp & 3) + 2 * (lane >> 4),
+                   [&] { named_bar(2 + half, 128); });
       __syncthreads();
-      const int j = lane, i0 = warp * 8;
-      {
-        float w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = -s.N[32 + i0 + i][j];
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          float z[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) z[x] = s.beta[c + x] * s.Z[c + x][j];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 n = *reinterpret_cast<const float4 *>(&s.N[32 + i0 + i][c]);
-            w[i] = fmaf(-n.x, z[0], fmaf(-n.y, z[1], fmaf(-n.z, z[2], fmaf(-n.w, z[3], w[i]))));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s.W[i0 + i][j] = w[i];
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          float z[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) z[x] = s.beta[32 + c + x] * s.W[c + x][j];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 n = *reinterpret_cast<const float4 *>(&s.Z[32 + i0 + i][32 + c]);
-            w[i] = fmaf(n.x, z[0], fmaf(n.y, z[1], fmaf(n.z, z[2], fmaf(n.w, z[3], w[i]))));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s.Z[32 + i0 + i][j] = w[i];
-          s.Z[i0 + i][32 + j] = 0.f;
-        }
-      }
+      below<32, 4>(s, W, 0, lane, 4 * warp, [] { __syncthreads(); });
       __syncthreads();
+      const int zr = tid >> 2, z0 = (tid & 3) * 16;
       float sum = 0.f;
-      uint32_t third[16];
-      const int row = tid >> 1, c1 = (tid & 1) * 32;
+      uint32_t third[8];
 #pragma unroll
-      for (int c0 = 0; c0 < 32; c0 += 8) {
+      for (int n = 0; n < 16; n += 8) {
         uint32_t hi[4], lo[4];
         alignas(16) float z[8];
-        *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(&s.Z[row][c1 + c0]);
-        *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(&s.Z[row][c1 + c0 + 4]);
+        *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(&s.N[zr][z0 + n]);
+        *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(&s.N[zr][z0 + n + 4]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(fabsf(z[i]), fabsf(s.beta[c1 + c0 + i]), sum);
+        for (int i = 0; i < 8; ++i) sum = fmaf(fabsf(z[i]), fabsf(s.beta[z0 + n + i]), sum);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           split2(z[2 * i], z[2 * i + 1], hi[i], lo[i]);
-          third[c0 / 2 + i] = split3(z[2 * i], z[2 * i + 1], hi[i], lo[i]);
+          third[n / 2 + i] = split3(z[2 * i], z[2 * i + 1], hi[i], lo[i]);
         }
-        const uint32_t o = smem_u32(sm) + sw128_off(row, c1 + c0, 64);
+        const uint32_t o = smem_u32(sm) + sw128_off(zr, z0 + n, 64);
         st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const bool wide = __syncthreads_or(!(sum <= WIDE));
-      if (wide) {  // the third part takes N's place
+      if (wide) {  // the third part takes Z's place
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          st_shared_v4(smem_u32(&s.N[0][0]) + sw128_off(row, c1 + 8 * i, 64), third[4 * i], third[4 * i + 1],
+        for (int i = 0; i < 2; ++i)
+          st_shared_v4(smem_u32(&s.N[0][0]) + sw128_off(zr, z0 + 8 * i, 64), third[4 * i], third[4 * i + 1],
                        third[4 * i + 2], third[4 * i + 3]);
       }
       fence_async_smem();
@@ -362,11 +343,12 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const __grid_constant__
     }
     if (tid == 0) bulk_wait_all();
   } else if (tid == 0) {
+    mbar_wait(&full, 0, WAIT_CYCLES);
     set_device_error(a.err, GLACORE_ERR_TIMEOUT);
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tb, 64);
   }
@@ -1830,7 +1812,7 @@ cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
   a.tiles = ws + l.tiles;
   a.gates = (float *)(ws + l.gates);
   a.err = c.p.err;
-  return launch(delta_prep_kernel, c.slots * c.p.Hqk, 128, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep");
+  return launch(delta_prep_kernel, c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep");
 }
 ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   ChainArgs a;
