@@ -36,7 +36,7 @@ struct Call {
 };
 
 // The chunk in a slot: its document d and tokens [tok, tok + len).  False: an
-// unused slot (behind the last document's).
+// unused slot (behind the last document's).  There are fewer than 2^31 slots.
 __device__ __forceinline__ bool chunk_in_slot(const Docs &docs, int64_t slot, int64_t &tok, int &len) {
   int64_t d, j;
   if (docs.cbase) {
@@ -49,9 +49,9 @@ __device__ __forceinline__ bool chunk_in_slot(const Docs &docs, int64_t slot, in
     d = lo;
     j = slot - docs.cbase[d];
   } else {
-    const int64_t per = (docs.T + C - 1) / C;
-    d = slot / per;
-    j = slot - d * per;
+    const uint32_t per = (uint32_t)((docs.T + C - 1) / C), r = (uint32_t)slot / per;
+    d = r;
+    j = slot - (int64_t)r * per;
   }
   int64_t s0, s1;
   docs.range(d, s0, s1);

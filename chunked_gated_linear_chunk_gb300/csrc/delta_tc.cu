@@ -52,6 +52,20 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t 
       : "r"(hi), "f"(a), "f"(b));
   lo = pack_bf16(ra, rb);
 }
+// c + a b for both halves of two packed pairs
+__device__ __forceinline__ float fma_pairs(uint32_t a, uint32_t b, float c) {
+  asm("{\n .reg .b16 x, y, u, v;\n mov.b32 {x, y}, %1;\n mov.b32 {u, v}, %2;\n fma.rn.f32.bf16 %0, x, u, %0;\n"
+      " fma.rn.f32.bf16 %0, y, v, %0;\n}\n"
+      : "+f"(c)
+      : "r"(a), "r"(b));
+  return c;
+}
+// 2^x to 2 ulp; results below 2^-126 become 0
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // what hi and lo leave of them
 __device__ __forceinline__ uint32_t split3(float a, float b, uint32_t hi, uint32_t lo) {
   return pack_bf16((a - __uint_as_float(hi << 16)) - __uint_as_float(lo << 16),
@@ -238,10 +252,10 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
       if (isP && half == 0) {
         const float2 last = s.G[63];
         float *gs = a.gates + sh * GATES;
-        gs[G_INTO + t] = exp2f(gt.x + gt.y);
-        gs[G_OUT + t] = exp2f((last.x - gt.x) + (last.y - gt.y));  // tokens past the end add no decay
+        gs[G_INTO + t] = pow2(gt.x + gt.y);
+        gs[G_OUT + t] = pow2((last.x - gt.x) + (last.y - gt.y));  // tokens past the end add no decay
         gs[G_BETA + t] = s.beta[t];
-        if (t == 0) gs[G_OVER] = exp2f(last.x + last.y);
+        if (t == 0) gs[G_OVER] = pow2(last.x + last.y);
       }
       // row t, columns s <= t (P) or s < t (N): scale D (.) QK^T, D (.) KK^T
       const int last = t < L ? (isP ? t : t - 1) : -1;
@@ -257,8 +271,8 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
             const float4 gc = *reinterpret_cast<const float4 *>(&s.G[c0 + i]);
-            x[i] = c0 + i <= last ? f * exp2f((gt.x - gc.x) + (gt.y - gc.y)) * __uint_as_float(m[i]) : 0.f;
-            x[i + 1] = c0 + i + 1 <= last ? f * exp2f((gt.x - gc.z) + (gt.y - gc.w)) * __uint_as_float(m[i + 1]) : 0.f;
+            x[i] = c0 + i <= last ? f * pow2((gt.x - gc.x) + (gt.y - gc.y)) * __uint_as_float(m[i]) : 0.f;
+            x[i + 1] = c0 + i + 1 <= last ? f * pow2((gt.x - gc.z) + (gt.y - gc.w)) * __uint_as_float(m[i + 1]) : 0.f;
           }
         }
         if (isP) {
@@ -1304,8 +1318,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   const uint32_t tb = tmem_base, sb = smem_u32(sm);
   const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S;
   // the first used unit from u on (units of unused slots are passed over)
-  auto find = [&](int64_t u, int64_t &tok, int &L) -> int64_t {
-    while (u < a.units && !chunk_in_slot(a.docs, u / a.H, tok, L)) u += gridDim.x;
+  const uint32_t H = (uint32_t)a.H, units = (uint32_t)a.units;
+  auto find = [&](uint32_t u, int64_t &tok, int &L) -> uint32_t {
+    while (u < units && !chunk_in_slot(a.docs, u / H, tok, L)) u += gridDim.x;
     return u;
   };
   bool ok = true;
@@ -1317,7 +1332,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       tma_prefetch_desc(&maps.k);
       tma_prefetch_desc(&maps.dO);
       int loads_a = 0, loads_b = 0, loads_ds = 0;
-      auto load_a = [&](int64_t u) {
+      auto load_a = [&](uint32_t unit) {
+        const int64_t u = unit;
         mbar_expect_tx(&full_a, S_IMAGE + E_IMAGE);
         bulk_load(sm + L_::E, a.e_images + u * E_IMAGE, E_IMAGE, &full_a);
         bulk_load(sm + L_::S, a.s_images + u * S_IMAGE, S_IMAGE, &full_a);
@@ -1325,8 +1341,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         bulk_prefetch_l2(a.r_images + u * R_IMAGE, R_IMAGE);
         ++loads_a;
       };
-      auto load_b = [&](int64_t u) {
-        const int h = (int)(u % a.H), hq = h / a.share;
+      auto load_b = [&](uint32_t unit) {
+        const int64_t u = unit;
+        const int h = (int)(unit % H), hq = h / a.share;
         mbar_expect_tx(&full_b, 3 * 32768);
 #pragma unroll
         for (int cb = 0; cb < 2; ++cb) {
@@ -1343,9 +1360,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       constexpr uint32_t idKN = idesc_bf16(128, 64, true, false), idMN = idesc_bf16(128, 64, true, true);
       constexpr uint32_t idKN2 = idesc_bf16(128, 128, true, false), idMN2 = idesc_bf16(128, 128, true, true);
       const uint32_t dp = sb + L_::T, da = dp + 2 * TILE;
-      int64_t u = find(blockIdx.x, tok, L);
-      if (u < a.units) load_a(u);
-      for (int it = 0; u < a.units; ++it) {
+      uint32_t u = find(blockIdx.x, tok, L);
+      if (u < units) load_a(u);
+      for (int it = 0; u < units; ++it) {
         const uint32_t ph = (uint32_t)it & 1u;
         // the last unit's gradients have left (q, k, the stacks and tensor memory are free)
         if (it >= 1 && !(ok = mbar_wait(&left, ph ^ 1u, WAIT_CYCLES))) break;
@@ -1371,7 +1388,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         mma_commit(&g2);
         if (!(ok = mbar_wait(&g2, ph, WAIT_CYCLES) && mbar_wait(&s0_read, ph, WAIT_CYCLES))) break;
         mbar_expect_tx(&full_ds, S_IMAGE);
-        bulk_load(sm + L_::S, a.ds_images + u * S_IMAGE, S_IMAGE, &full_ds);
+        bulk_load(sm + L_::S, a.ds_images + (int64_t)u * S_IMAGE, S_IMAGE, &full_ds);
         ++loads_ds;
         if (!(ok = mbar_wait(&tiles, ph, WAIT_CYCLES))) break;
         tc_fence_after();
@@ -1394,7 +1411,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         mma_commit(&g3);
         u = find(u + gridDim.x, tok, L);
         if (!(ok = mbar_wait(&g3, ph, WAIT_CYCLES))) break;
-        if (u < a.units) load_a(u);
+        if (u < units) load_a(u);
       }
       if (!ok) {  // nothing of this block's is in flight when it leaves
         if (loads_a) mbar_wait(&full_a, (uint32_t)(loads_a - 1) & 1u, WAIT_CYCLES);
@@ -1413,28 +1430,28 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
     const bool isA = qw >= 2;
     float *W = reinterpret_cast<float *>(sm + L_::W);
     // the next unit, its tokens and gates, looked up while this one is worked on
-    int64_t next = 0, tok_next = 0;
+    uint32_t next = 0;
+    int64_t tok_next = 0;
     int L_next = 0;
     float g_next = 0.f, b_next = 0.f;
-    auto look = [&](int64_t from) {
+    auto look = [&](uint32_t from) {
       next = find(from, tok_next, L_next);
       g_next = b_next = 0.f;
-      if (next < a.units && tid < CH && tid < L_next) {
-        const int64_t at = (tok_next + tid) * a.H + next % a.H;
+      if (next < units && tid < CH && tid < L_next) {
+        const int64_t at = (tok_next + tid) * a.H + next % H;
         g_next = a.g[at];
         b_next = a.beta[at];
       }
     };
     look(blockIdx.x);
-    for (int it = 0; next < a.units; ++it) {
-      const uint32_t ph = (uint32_t)it & 1u;
-      const int64_t u = next;
-      const int h = (int)(u % a.H);
+    for (int it = 0; next < units; ++it) {
+      const uint32_t ph = (uint32_t)it & 1u, u = next;
+      const int h = (int)(u % H);
       tok = tok_next;
       L = L_next;
       uint4 dh[4], dl[4];  // of dS1's image, for <S0, dS1>
       {
-        const char *img = a.ds_images + u * S_IMAGE + tid * 16;
+        const char *img = a.ds_images + (int64_t)u * S_IMAGE + tid * 16;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           dh[n] = __ldg(reinterpret_cast<const uint4 *>(img + n * 8192));
@@ -1461,7 +1478,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       named_bar(1, 32 * GRAD_WARPS);
       if (tid < CH) {
         const float4 x = s_g[tid], z = s_g[63];
-        const float into = exp2f(x.x + x.y), out = exp2f((z.x - x.x) + (z.y - x.y));
+        const float into = pow2(x.x + x.y), out = pow2((z.x - x.x) + (z.y - x.y));
         s_into[tid] = a.scale * into;
         s_ki[tid] = -into * b;
         s_ko[tid] = out * b;
@@ -1478,7 +1495,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       warp_arrive(&cleared);
       {  // <S0, dS1>, while the first products run
         ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES);
-        float dot = 0.f;
+        float dot = 0.f, low = 0.f;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
           const uint4 hi = lds_u4(si + tid * 16 + n * 8192), lo = lds_u4(si + S_IMAGE / 2 + tid * 16 + n * 8192);
@@ -1486,12 +1503,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
           const uint32_t v[4] = {dh[n].x, dh[n].y, dh[n].z, dh[n].w}, z[4] = {dl[n].x, dl[n].y, dl[n].z, dl[n].w};
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
-            dot = fmaf(__uint_as_float(x[m] << 16) + __uint_as_float(y[m] << 16),
-                       __uint_as_float(v[m] << 16) + __uint_as_float(z[m] << 16), dot);
-            dot = fmaf(__uint_as_float(x[m] & 0xffff0000u) + __uint_as_float(y[m] & 0xffff0000u),
-                       __uint_as_float(v[m] & 0xffff0000u) + __uint_as_float(z[m] & 0xffff0000u), dot);
+            dot = fma_pairs(x[m], v[m], dot);
+            low = fma_pairs(x[m], z[m], fma_pairs(y[m], v[m], low));
           }
         }
+        dot += low;
 #pragma unroll
         for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
         if (lane == 0) s_dot[warp] = dot;
@@ -1516,7 +1532,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
             const float B = __uint_as_float(x[n]) + __uint_as_float(y[n]);
             if (isA && c == t) s_db[t] = B;
             const float4 gc = s_g[c];
-            w[n] = c <= last ? f * gc.z * exp2f((gt.x - gc.x) + (gt.y - gc.y)) * B : 0.f;
+            w[n] = c <= last ? f * gc.z * pow2((gt.x - gc.x) + (gt.y - gc.y)) * B : 0.f;
           }
         } else {
 #pragma unroll
