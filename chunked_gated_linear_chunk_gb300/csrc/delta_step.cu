@@ -54,10 +54,11 @@ __device__ __forceinline__ void store(void *p, int bf16, int64_t i, float x) {
 // of 4 and the pool 16-byte aligned.
 template <int COLT, int KR, bool VEC>
 __global__ void __launch_bounds__(THREADS, 4) delta_step_kernel(const StepArgs a) {
-  constexpr int ROWT = THREADS / COLT, COLS = 4 * COLT;
-  __shared__ float2 s_kq[TOKENS][ROWT * KR];  // k, q of a key row
+  constexpr int ROWT = THREADS / COLT, COLS = 4 * COLT, ROWS = ROWT * KR;
+  static_assert(ROWS % 32 == 0, "");
+  __shared__ float2 s_kq[TOKENS][ROWS];  // k, q of a key row
   __shared__ float s_v[TOKENS][COLS];
-  __shared__ float s_gate[TOKENS], s_beta[TOKENS], s_qk[TOKENS];
+  __shared__ float s_gate[TOKENS], s_beta[TOKENS], s_qk[TOKENS][ROWS / 32];
   __shared__ float4 s_x[2][WARPS][COLT][2];  // partial sums of S^T k and S^T q, two tokens' worth
   const int slice = blockIdx.x % a.slices;
   const int64_t bh = blockIdx.x / a.slices;
@@ -95,26 +96,25 @@ __global__ void __launch_bounds__(THREADS, 4) delta_step_kernel(const StepArgs a
   for (int64_t t0 = 0; t0 < a.T; t0 += TOKENS) {
     const int n = (int)(a.T - t0 < TOKENS ? a.T - t0 : TOKENS);
     if (t0) __syncthreads();  // the last tokens' rows have been used
-    // warp w stages token t0 + w (TOKENS == WARPS): its q, k, q . k, gate and beta
-    if (warp < n) {
-      const int64_t tok = b * a.T + t0 + warp;
-      float dot = 0.f;
-      for (int c = lane; c < ROWT * KR; c += 32) {
-        float q = 0.f, k = 0.f;
-        if (c < a.K) {
-          q = load(a.q, a.bf16, tok * a.qs + (int64_t)hq * a.K + c);
-          k = load(a.k, a.bf16, tok * a.ks + (int64_t)hq * a.K + c);
-        }
-        s_kq[warp][c] = make_float2(k, q);
-        dot = fmaf(q, k, dot);
+    // q, k and, of every 32 channels (a warp's), q . k; whole warps take part or none
+    for (int i = threadIdx.x; i < n * ROWS; i += THREADS) {
+      const int t = i / ROWS, c = i % ROWS;
+      const int64_t tok = b * a.T + t0 + t;
+      float q = 0.f, k = 0.f;
+      if (c < a.K) {
+        q = load(a.q, a.bf16, tok * a.qs + (int64_t)hq * a.K + c);
+        k = load(a.k, a.bf16, tok * a.ks + (int64_t)hq * a.K + c);
       }
+      s_kq[t][c] = make_float2(k, q);
+      float dot = q * k;
 #pragma unroll
       for (int m = 16; m; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-      if (lane == 0) {
-        s_qk[warp] = dot;
-        s_gate[warp] = expf(a.g[tok * a.H + h]);
-        s_beta[warp] = a.beta[tok * a.H + h];
-      }
+      if (lane == 0) s_qk[t][c / 32] = dot;
+    }
+    if (threadIdx.x < n) {
+      const int64_t at = (b * a.T + t0 + threadIdx.x) * a.H + h;
+      s_gate[threadIdx.x] = expf(a.g[at]);
+      s_beta[threadIdx.x] = a.beta[at];
     }
     for (int i = threadIdx.x; i < n * COLS; i += THREADS) {
       const int t = i / COLS, c = i % COLS;
@@ -168,10 +168,13 @@ __global__ void __launch_bounds__(THREADS, 4) delta_step_kernel(const StepArgs a
           sq.x += p.x, sq.y += p.y, sq.z += p.z, sq.w += p.w;
         }
         const float tq[4] = {sq.x, sq.y, sq.z, sq.w};
+        float qk = 0.f;
+#pragma unroll
+        for (int i = 0; i < ROWS / 32; ++i) qk += s_qk[t][i];
         const int64_t at = ((b * a.T + t0 + t) * a.H + h) * a.V + v0;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (v0 + column(e) < a.V) store(a.o, a.bf16, at + column(e), a.scale * fmaf(s_qk[t], u[e], d * tq[e]));
+          if (v0 + column(e) < a.V) store(a.o, a.bf16, at + column(e), a.scale * fmaf(qk, u[e], d * tq[e]));
       }
 #pragma unroll
       for (int j = 0; j < KR; ++j) {

@@ -40,7 +40,7 @@ struct Args {
   int *err;
   int64_t tokens, T, P, xs[2];
   int H[2], D, R, mean, inter;
-  int group[2], parts[2];  // forward: heads of a warp, warps per token
+  int group[2], parts[2];  // heads of a warp, warps per token
   float eps;
 };
 
@@ -62,6 +62,15 @@ template <> struct Vec<__nv_bfloat16> {
       v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
   }
+  // another lane's channels
+  __device__ __forceinline__ Vec of(int lane) const {
+    Vec o;
+    o.a.x = __shfl_sync(0xffffffffu, a.x, lane);
+    o.a.y = __shfl_sync(0xffffffffu, a.y, lane);
+    o.a.z = __shfl_sync(0xffffffffu, a.z, lane);
+    o.a.w = __shfl_sync(0xffffffffu, a.w, lane);
+    return o;
+  }
   static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
     uint32_t u[4];
 #pragma unroll
@@ -81,6 +90,18 @@ template <> struct Vec<float> {
   __device__ __forceinline__ void clear() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ Vec of(int lane) const {
+    Vec o;
+    o.a.x = __shfl_sync(0xffffffffu, a.x, lane);
+    o.a.y = __shfl_sync(0xffffffffu, a.y, lane);
+    o.a.z = __shfl_sync(0xffffffffu, a.z, lane);
+    o.a.w = __shfl_sync(0xffffffffu, a.w, lane);
+    o.b.x = __shfl_sync(0xffffffffu, b.x, lane);
+    o.b.y = __shfl_sync(0xffffffffu, b.y, lane);
+    o.b.z = __shfl_sync(0xffffffffu, b.z, lane);
+    o.b.w = __shfl_sync(0xffffffffu, b.w, lane);
+    return o;
   }
   static __device__ __forceinline__ void store(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -139,19 +160,16 @@ __device__ __forceinline__ void make_turn(const Args &a, int64_t token, int li, 
     }
   }
 }
-// v rotated (back: the other way).  All lanes of the warp call it.
-__device__ __forceinline__ void turn(const Args &a, const Turn &t, float (&v)[8], float dir) {
-  if (a.R == 0) return;
-  float o[8];
+// The 8 channels that a lane's are paired with, as they are in the row
+// (interleaved: its own, neighbours swapped).  All lanes of the warp call it.
+template <typename T>
+__device__ __forceinline__ void paired(const Args &a, const Turn &t, const Vec<T> &x, const float (&f)[8], float (&o)[8]) {
   if (a.inter) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = v[e ^ 1];
+    for (int e = 0; e < 8; ++e) o[e] = f[e ^ 1];
   } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, v[e], t.other);
+    x.of(t.other).get(o);
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = fmaf(dir * t.s[e], o[e], t.c[e] * v[e]);
 }
 
 __device__ __forceinline__ void weights(const float *w, int c0, bool in, float (&v)[8]) {
@@ -159,17 +177,16 @@ __device__ __forceinline__ void weights(const float *w, int c0, bool in, float (
   for (int e = 0; e < 8; ++e) v[e] = w && in ? __ldg(w + c0 + e) : 1.f;
 }
 
-template <typename T, int LPR>
-__global__ void __launch_bounds__(THREADS) fwd_kernel(const Args a) {
-  constexpr int RPP = 32 / LPR, UNROLL = 4;  // rows of a pass, passes in flight
+// With a row's rotation y_i = r (x_i w_i c + x_j w_j s) (s with its sign), c w
+// and the pair's s w are made once for a token, and the pair's raw channels
+// fetched while the row is summed.
+template <typename T, int LPR, bool TURN>
+__global__ void __launch_bounds__(THREADS, 4) fwd_kernel(const Args a) {
+  constexpr int RPP = 32 / LPR, UNROLL = 2;  // rows of a pass, passes in flight
   const int lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
-  const int64_t unit = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
-  const int per = a.parts[0] + a.parts[1];
-  const int64_t token = unit / per;
+  const int64_t token = (int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5);
   if (token >= a.tokens) return;
-  int part = (int)(unit % per);
-  const int z = part >= a.parts[0];
-  if (z) part -= a.parts[0];
+  const int z = (int)blockIdx.y >= a.parts[0], part = (int)blockIdx.y - (z ? a.parts[0] : 0);
   const int h0 = part * a.group[z], h1 = min(h0 + a.group[z], a.H[z]);
   const int c0 = 8 * li;
   const bool in = c0 < a.D;
@@ -185,28 +202,38 @@ __global__ void __launch_bounds__(THREADS) fwd_kernel(const Args a) {
     }
   };
   fetch(h0);
+  float cw[8], sw[8];
+  weights(a.w[z], c0, in, cw);
   Turn t;
-  make_turn<LPR>(a, token, li, t);
-  float w[8];
-  weights(a.w[z], c0, in, w);
-  for (int h = h0; h < h1; h += UNROLL * RPP) {
-    float f[UNROLL][8], ss[UNROLL];
+  if (TURN) {
+    make_turn<LPR>(a, token, li, t);
+    // the weights of the paired channels
+    float ow[8];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      v[u].get(f[u]);
-      ss[u] = 0.f;
+    for (int e = 0; e < 8; ++e) ow[e] = a.inter ? cw[e ^ 1] : __shfl_sync(0xffffffffu, cw[e], t.other);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss[u] = fmaf(f[u][e], f[u][e], ss[u]);
+    for (int e = 0; e < 8; ++e) {
+      cw[e] *= t.c[e];
+      sw[e] = ow[e] * t.s[e];
     }
+  }
+  for (int h = h0; h < h1; h += UNROLL * RPP) {
+    Vec<T> w[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) w[u] = v[u];
     fetch(h + UNROLL * RPP);
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
-      const float r = rsqrtf(fmaf(row_sum<LPR>(ss[u]), inv, a.eps));
+      float f[8], o[8], ss = 0.f;
+      w[u].get(f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[u][e] = f[u][e] * r * w[e];
-      turn(a, t, f[u], 1.f);
+      for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
+      if (TURN) paired(a, t, w[u], f, o);
+      const float r = rsqrtf(fmaf(row_sum<LPR>(ss), inv, a.eps));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = r * (TURN ? fmaf(o[e], sw[e], f[e] * cw[e]) : f[e] * cw[e]);
       const int hh = h + u * RPP + sub;
-      if (in && hh < h1) Vec<T>::store(y + (int64_t)hh * a.D, f[u]);
+      if (in && hh < h1) Vec<T>::store(y + (int64_t)hh * a.D, f);
     }
   }
 }
@@ -222,76 +249,76 @@ __device__ __forceinline__ void block_dw(const Args &a, const float *sums /* [ro
   }
 }
 
-template <typename T, int LPR>
-__global__ void __launch_bounds__(THREADS) bwd_kernel(const Args a) {
-  constexpr int RPP = 32 / LPR, UNROLL = 2;
+template <typename T, int LPR, bool TURN>
+__global__ void __launch_bounds__(THREADS, 3) bwd_kernel(const Args a) {
+  constexpr int RPP = 32 / LPR;
   extern __shared__ float sums[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
   const int c0 = 8 * li;
   const bool in = c0 < a.D;
   const float inv = a.mean ? 1.f / (float)a.D : 1.f;
-  float w[2][8], dw[2][8];
-#pragma unroll
   for (int z = 0; z < 2; ++z) {
-    weights(a.w[z], c0, in, w[z]);
+    float w[8], dw[8];
+    weights(a.w[z], c0, in, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[z][e] = 0.f;
-  }
-  for (int64_t token = (int64_t)blockIdx.x * WARPS + warp; token < a.tokens; token += (int64_t)gridDim.x * WARPS) {
-    Turn t;
-    make_turn<LPR>(a, token, li, t);
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
+    for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+    // (query, key) x token x part of the heads, dealt to the warps of the grid in turn
+    const int64_t all = (int64_t)gridDim.x * WARPS, mine = (int64_t)blockIdx.x * WARPS + warp;
+    const int64_t skip = z ? a.tokens * a.parts[0] % all : 0;
+    for (int64_t unit = (mine - skip + all) % all; unit < a.tokens * a.parts[z]; unit += all) {
+      const int64_t token = a.parts[z] == 1 ? unit : unit >> 1;
+      const int first = a.parts[z] == 1 ? 0 : (int)(unit & 1) * a.group[z], end = min(first + a.group[z], a.H[z]);
+      Turn t;
+      if (TURN) make_turn<LPR>(a, token, li, t);
       const T *x = (const T *)a.x[z] + token * a.xs[z] + c0;
       const T *dy = (const T *)a.dy[z] + token * a.H[z] * a.D + c0;
       T *dx = (T *)a.y[z] + token * a.H[z] * a.D + c0;
-      for (int h = 0; h < a.H[z]; h += UNROLL * RPP) {
-        Vec<T> vx[UNROLL], vd[UNROLL];
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-          const int hh = h + u * RPP + sub;
-          if (in && hh < a.H[z]) {
-            vx[u].load(x + (int64_t)hh * a.D);
-            vd[u].load(dy + (int64_t)hh * a.D);
-          } else {
-            vx[u].clear();
-            vd[u].clear();
-          }
+      Vec<T> nx, nd;  // the next row
+      auto fetch = [&](int h) {
+        if (in && h < end) {
+          nx.load(x + (int64_t)h * a.D);
+          nd.load(dy + (int64_t)h * a.D);
+        } else {
+          nx.clear();
+          nd.clear();
         }
-#pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-          float f[8], d[8], ss = 0.f, sa = 0.f;
-          vx[u].get(f);
-          vd[u].get(d);
-          turn(a, t, d, -1.f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            ss = fmaf(f[e], f[e], ss);
-            sa = fmaf(d[e] * w[z][e], f[e], sa);
-          }
-          ss = row_sum<LPR>(ss);
-          sa = row_sum<LPR>(sa);
-          const float r = rsqrtf(fmaf(ss, inv, a.eps));
-          const int hh = h + u * RPP + sub;
-          const bool live = in && hh < a.H[z];
-          const float m = sa * r * inv;  // mean (sum) of a w n
+      };
+      fetch(first + sub);
+      for (int h = first + sub; h < end + sub; h += RPP) {  // all lanes as often
+        const Vec<T> vx = nx, vd = nd;
+        fetch(h + RPP);
+        float f[8], d[8], g[8], ss = 0.f, sa = 0.f;
+        vx.get(f);
+        vd.get(d);
+        if (TURN) {  // the gradient rotated back
           float o[8];
+          paired(a, t, vd, d, o);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float n = f[e] * r;
-            o[e] = r * fmaf(-n, m, d[e] * w[z][e]);
-            if (live) dw[z][e] = fmaf(d[e], n, dw[z][e]);
-          }
-          if (live) Vec<T>::store(dx + (int64_t)hh * a.D, o);
+          for (int e = 0; e < 8; ++e) d[e] = fmaf(-t.s[e], o[e], t.c[e] * d[e]);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          g[e] = d[e] * f[e];
+          ss = fmaf(f[e], f[e], ss);
+          sa = fmaf(g[e], w[e], sa);
+        }
+        ss = row_sum<LPR>(ss);
+        sa = row_sum<LPR>(sa);
+        const float r = rsqrtf(fmaf(ss, inv, a.eps));
+        const float m = sa * r * r * r * inv;  // r m(a w n), for x itself
+        const bool live = in && h < end;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dw[e] = fmaf(g[e], live ? r : 0.f, dw[e]);
+          d[e] = fmaf(-f[e], m, r * (d[e] * w[e]));
+        }
+        if (live) Vec<T>::store(dx + (int64_t)h * a.D, d);
       }
     }
-  }
-#pragma unroll
-  for (int z = 0; z < 2; ++z)
     if (in)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sums[((warp * RPP + sub) * 2 + z) * a.D + c0 + e] = dw[z][e];
+      for (int e = 0; e < 8; ++e) sums[((warp * RPP + sub) * 2 + z) * a.D + c0 + e] = dw[e];
+  }
   __syncthreads();
   block_dw(a, sums, WARPS * RPP);
   follow_allow();
@@ -385,6 +412,7 @@ __global__ void __launch_bounds__(512) sum_dw_kernel(const float *part, int bloc
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
   float x = 0.f;
   if (c < 2 * D)
+#pragma unroll 8
     for (int b = warp; b < blocks; b += 16) x += part[(int64_t)b * 2 * D + c];
   s[warp][threadIdx.x & 31] = x;
   __syncthreads();
@@ -396,13 +424,14 @@ __global__ void __launch_bounds__(512) sum_dw_kernel(const float *part, int bloc
   }
 }
 
-constexpr int64_t BWD_BLOCKS = 152 * 4;  // blocks of the backward at most (resident at once)
+constexpr int64_t BWD_BLOCKS = 152 * 3;  // blocks of the backward at most (resident at once)
 
 int64_t bwd_blocks(int64_t tokens) { return std::max<int64_t>(1, std::min<int64_t>((tokens + WARPS - 1) / WARPS, BWD_BLOCKS)); }
 
 glacore_status check(const glacore_qk_norm *p) {
   if (!p || p->B < 1 || p->T < 0 || p->Hq < 1 || p->Hk < 1 || p->Hq > 65535 || p->Hk > 65535 || p->D < 1 ||
-      p->D > MAXD || p->R < 0 || 2 * p->R > p->D || p->B > (int64_t)1 << 31 || p->T > (int64_t)1 << 31)
+      p->D > MAXD || p->R < 0 || 2 * p->R > p->D || p->B > (int64_t)1 << 31 || p->T > (int64_t)1 << 31 ||
+      p->B * p->T > (int64_t)1 << 33)
     return GLACORE_ERR_INVALID_ARG;
   if (p->dtype != GLACORE_F32 && p->dtype != GLACORE_BF16) return GLACORE_ERR_INVALID_ARG;
   if ((p->l2 != 0 && p->l2 != 1) || (p->interleaved != 0 && p->interleaved != 1) || !(p->eps >= 0.f) || p->reserved0)
@@ -469,32 +498,40 @@ cudaError_t run_fwd(const glacore_qk_norm *p, Args &a, cudaStream_t st) {
   for (int z = 0; z < 2; ++z) {
     int g = a.H[z];
     while (g > least && a.tokens * 2 * ((a.H[z] + g - 1) / g) < 152 * 16) g = (g + 1) / 2;
+    g = std::max(g, (a.H[z] + 16383) / 16384);  // the second axis of a grid has 65535 places
     a.group[z] = (g + least - 1) / least * least;
     a.parts[z] = (a.H[z] + a.group[z] - 1) / a.group[z];
   }
-  const int64_t units = a.tokens * (a.parts[0] + a.parts[1]), blocks = (units + WARPS - 1) / WARPS;
-  if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)((a.tokens + WARPS - 1) / WARPS), a.parts[0] + a.parts[1]);
+  auto go = [&](auto kernel) { kernel<<<grid, THREADS, 0, st>>>(a); };
   if (lpr == 8)
-    fwd_kernel<T, 8><<<(unsigned)blocks, THREADS, 0, st>>>(a);
+    a.R ? go(fwd_kernel<T, 8, true>) : go(fwd_kernel<T, 8, false>);
   else if (lpr == 16)
-    fwd_kernel<T, 16><<<(unsigned)blocks, THREADS, 0, st>>>(a);
+    a.R ? go(fwd_kernel<T, 16, true>) : go(fwd_kernel<T, 16, false>);
   else
-    fwd_kernel<T, 32><<<(unsigned)blocks, THREADS, 0, st>>>(a);
+    a.R ? go(fwd_kernel<T, 32, true>) : go(fwd_kernel<T, 32, false>);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t run_bwd(const glacore_qk_norm *p, const Args &a, float *dwq, float *dwk, cudaStream_t st) {
+cudaError_t run_bwd(const glacore_qk_norm *p, Args &a, float *dwq, float *dwk, cudaStream_t st) {
+  for (int z = 0; z < 2; ++z) {  // two warps to the heads of a token where there are enough: the last round is shorter
+    a.parts[z] = a.H[z] >= 8 ? 2 : 1;
+    a.group[z] = (a.H[z] + a.parts[z] - 1) / a.parts[z];
+  }
   const int64_t blocks = bwd_blocks(a.tokens);
   const size_t row = 2 * sizeof(float) * a.D;
   if (!vectors(p, a)) {
     rows_kernel<T, true><<<(unsigned)blocks, THREADS, WARPS * row, st>>>(a);
-  } else if (p->D <= 64) {
-    bwd_kernel<T, 8><<<(unsigned)blocks, THREADS, WARPS * 4 * row, st>>>(a);
-  } else if (p->D <= 128) {
-    bwd_kernel<T, 16><<<(unsigned)blocks, THREADS, WARPS * 2 * row, st>>>(a);
   } else {
-    bwd_kernel<T, 32><<<(unsigned)blocks, THREADS, WARPS * row, st>>>(a);
+    const int lpr = p->D <= 64 ? 8 : p->D <= 128 ? 16 : 32;
+    auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, THREADS, WARPS * (32 / lpr) * row, st>>>(a); };
+    if (lpr == 8)
+      a.R ? go(bwd_kernel<T, 8, true>) : go(bwd_kernel<T, 8, false>);
+    else if (lpr == 16)
+      a.R ? go(bwd_kernel<T, 16, true>) : go(bwd_kernel<T, 16, false>);
+    else
+      a.R ? go(bwd_kernel<T, 32, true>) : go(bwd_kernel<T, 32, false>);
   }
   cudaError_t e = cudaGetLastError();
   mark_launch("qk_norm_bwd", st);
