@@ -355,6 +355,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
         bulk_commit();
       }
     }
+    follow_allow();
     if (tid == 0) bulk_wait_all();
   } else if (tid == 0) {
     mbar_wait(&full, 0, WAIT_CYCLES);
@@ -506,6 +507,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
     for (uint64_t *b : {&s_ready, &r_ready, &u_ready}) mbar_init(b, CHAIN_WARPS);
     fence_mbar_init();
   }
+  follow_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -894,6 +896,7 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
     for (uint64_t *b : {&do_ready, &dr_free}) mbar_init(b, 4);
     fence_mbar_init();
   }
+  follow_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1312,6 +1315,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
     for (uint64_t *b : {&cleared, &s0_read, &tiles, &left}) mbar_init(b, GRAD_WARPS);
     fence_mbar_init();
   }
+  follow_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1806,15 +1810,26 @@ cudaError_t make_maps(const Call &c, const void *dO, Maps &m) {
                   (!dO || make_map(&m.dO, dO, true, c.p.V, c.p.H, c.p.BT, 64));
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
+// `follow`: the kernel begins while the last one ends, and waits for it (follow_wait).
 template <typename K, typename M, typename A>
 cudaError_t launch(K kernel, int64_t blocks, int threads, uint32_t smem, const Call &c, const M &maps, const A &a,
-                   const char *label) {
+                   const char *label, bool follow) {
   if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)blocks, threads, smem, c.st>>>(maps, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = follow ? 1 : 0;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, maps, a);
   mark_launch(label, c.st);
-  return cudaGetLastError();
+  return r;
 }
 cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
   PrepArgs a;
@@ -1828,7 +1843,7 @@ cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
   a.tiles = ws + l.tiles;
   a.gates = (float *)(ws + l.gates);
   a.err = c.p.err;
-  return launch(delta_prep_kernel, c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep");
+  return launch(delta_prep_kernel, c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep", false);
 }
 ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   ChainArgs a;
@@ -1859,7 +1874,7 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
   a.o = (__nv_bfloat16 *)o;
   a.ht = ht;
   return launch(delta_chain_kernel, c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
-                ChainMaps{m.q, m.k, m.v}, a, "delta_chain");
+                ChainMaps{m.q, m.k, m.v}, a, "delta_chain", true);
 }
 
 cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, void *dk, bool per_head, void *dv, float *dg,
@@ -1889,7 +1904,7 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   b.err = a.err;
   const int64_t units = c.docs.n * c.p.H;
   e = launch(delta_walks_kernel, 2 * units, CHAIN_THREADS, std::max(ChainSmem<true>::BYTES, BackSmem::BYTES), c,
-             WalkMaps{{m.q, m.k, m.v}, {m.q, m.k, m.dO}}, WalkArgs{a, b, units}, "delta_walks");
+             WalkMaps{{m.q, m.k, m.v}, {m.q, m.k, m.dO}}, WalkArgs{a, b, units}, "delta_walks", true);
   if (e != cudaSuccess) return e;
   GradArgs g;
   g.docs = a.docs;
@@ -1911,9 +1926,9 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   g.units = c.slots * c.p.H;
   const int64_t blocks = std::min(g.units, tc::sm_count());
   return per_head ? launch(delta_grads_kernel<true>, blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
-                           "delta_grads")
+                           "delta_grads", true)
                   : launch(delta_grads_kernel<false>, blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
-                           "delta_grads");
+                           "delta_grads", true);
 }
 
 }  // namespace delta
