@@ -435,7 +435,11 @@ struct ChainSmem {
   static constexpr uint32_t BYTES = OUT + (STATES ? 0 : 16384) + 1024;
   static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BYTES <= 226 * 1024, "");
 };
-constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = 672;
+// 24 warps of 80 registers at launch (the last three of them idle), dealt out again by
+// warpgroup: 512 x 96 + 128 x 64 + 128 x 32 = 768 x 80.
+constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = 768;
+template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ void tmem_st8(uint32_t at, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
@@ -516,8 +520,9 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
   auto stage = [&](int j) -> uint32_t { return (uint32_t)(j & 1) * L_::STAGE; };
   auto wait_full = [&](int j) -> bool { return mbar_wait(&full[j & 1], (uint32_t)(j >> 1) & 1u, WAIT_CYCLES); };
 
-  if (warp == 20) {
-    if (lane == 0) {
+  if (warp >= 20) {
+    fewer_registers<48>();
+    if (warp == 20 && lane == 0) {
       const int hq = h / a.share;
       tma_prefetch_desc(&maps.q);
       tma_prefetch_desc(&maps.k);
@@ -626,6 +631,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
     }
     __syncwarp();
   } else if (warp < CHAIN_WARPS) {
+    more_registers<88>();
     const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;  // this warp's lanes of tensor memory
     const bool in = v < a.V;
@@ -765,11 +771,12 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
       for (int i = 0; i < 32; ++i)
         if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
     }
-  } else if (!STATES) {
+  } else {
+    fewer_registers<80>();
     const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     bool ok = true;
-    for (int j = 0; j < nch; ++j) {
+    for (int j = 0; !STATES && j < nch; ++j) {
       const uint32_t ph = (uint32_t)j & 1u, D = tb + lanes + T_XQ + ph * 128u;
       // e^G of the chunk, kept past its stage (which is full: s_ready of this chunk
       // waits for nothing of ours, and the next load into it for its own state)
@@ -905,8 +912,9 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
   auto stage = [&](int i) -> uint32_t { return (uint32_t)(i & 1) * L_::STAGE; };
   auto wait_full = [&](int i) -> bool { return mbar_wait(&full[i & 1], (uint32_t)(i >> 1) & 1u, WAIT_CYCLES); };
 
-  if (warp == 20) {
-    if (lane == 0) {
+  if (warp >= 20) {
+    fewer_registers<48>();
+    if (warp == 20 && lane == 0) {
       const int hq = h / a.share;
       tma_prefetch_desc(&maps.q);
       tma_prefetch_desc(&maps.k);
@@ -1007,6 +1015,7 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
     }
     __syncwarp();
   } else if (warp < CHAIN_WARPS) {
+    more_registers<88>();
     const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     const bool in = v < a.V;
@@ -1136,6 +1145,7 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
         if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
     }
   } else {
+    fewer_registers<80>();
     const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     bool ok = true;
