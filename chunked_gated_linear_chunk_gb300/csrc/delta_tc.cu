@@ -1291,14 +1291,14 @@ struct GradArgs {
 };
 struct GradSmem {
   // S: S0's image, then dS1's; X1, X2: per 64 columns 64 rows of dO, 64 of dR (hi, lo); QK: of q and k.
-  // Once the products have read X1 and X2, T: dPd hi, lo, dA hi, lo; then dq and dk; W: pair weights
+  // Once the products have read X1, T: dPd hi, lo, dA hi, lo; then dq and dk
   static constexpr uint32_t S = 0, X1 = S + S_IMAGE, X2 = X1 + 32768, E = X2 + 32768, QK = E + E_IMAGE,
                             BYTES = QK + 32768 + 1024;
-  static constexpr uint32_t T = X1, W = X2;
+  static constexpr uint32_t T = X1;
 };
-constexpr int WP = CH + 1;  // pitch of W
-static_assert(4 * TILE <= 32768 && CH * WP * 4 <= 32768, "");
-constexpr int GRAD_WARPS = 16, GRAD_THREADS = 544;
+// 20 warps of 96 registers at launch (the last three of them idle), dealt out again by warpgroup:
+// 512 x 104 + 128 x 64 = 640 x 96.  (Nothing may spill: shared memory leaves the first-level cache a few KB.)
+constexpr int GRAD_WARPS = 16, GRAD_THREADS = 640;
 
 template <bool PER_HEAD>
 __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __grid_constant__ GradMaps maps,
@@ -1311,8 +1311,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   __shared__ int abort_flag;
   __shared__ alignas(16) float4 s_g[CH];  // two parts of G (in units of log 2), b
   __shared__ alignas(16) float s_into[CH], s_ki[CH], s_ko[CH];  // scale e^G, -e^G b, e^{G_C - G} b
-  __shared__ alignas(16) float s_tot[CH][4];
-  __shared__ float s_db[CH], s_pair[2][CH], s_red[2][4][CH], s_over, s_dot[GRAD_WARPS];
+  __shared__ alignas(16) float s_tot[2 * CH][4];
+  // s_over, s_dot: of two units, the last one's are read while the next is begun
+  __shared__ float s_db[CH], s_pair[4][CH], s_red[2][4][CH], s_over[2], s_dot[2][GRAD_WARPS];
   __shared__ double warp0_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (warp == GRAD_WARPS) {
@@ -1340,8 +1341,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   bool ok = true;
   int64_t tok = 0;
   int L = 0;
-  if (warp == GRAD_WARPS) {
-    if (lane == 0) {
+  if (warp >= GRAD_WARPS) {
+    fewer_registers<64>();
+    if (warp == GRAD_WARPS && lane == 0) {
       tma_prefetch_desc(&maps.q);
       tma_prefetch_desc(&maps.k);
       tma_prefetch_desc(&maps.dO);
@@ -1353,6 +1355,13 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         bulk_load(sm + L_::S, a.s_images + u * S_IMAGE, S_IMAGE, &full_a);
         bulk_prefetch_l2(a.ds_images + u * S_IMAGE, S_IMAGE);
         bulk_prefetch_l2(a.r_images + u * R_IMAGE, R_IMAGE);
+        const int h = (int)(unit % H), hq = h / a.share;
+#pragma unroll
+        for (int cb = 0; cb < 2; ++cb) {
+          tma_prefetch_3d(&maps.q, cb * 64, hq, (int)tok);
+          tma_prefetch_3d(&maps.k, cb * 64, hq, (int)tok);
+          tma_prefetch_3d(&maps.dO, cb * 64, h, (int)tok);
+        }
         ++loads_a;
       };
       auto load_b = [&](uint32_t unit) {
@@ -1438,11 +1447,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
     }
     __syncwarp();
   } else {
+    more_registers<104>();
     // thread (row of the stack, later key channel: lane of tensor memory; 16 of the columns, tokens)
     const int grp = warp >> 2, qw = warp & 3, row = qw * 32 + lane, t = row & 63, c0 = 16 * grp;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     const bool isA = qw >= 2;
-    float *W = reinterpret_cast<float *>(sm + L_::W);
     // the next unit, its tokens and gates, looked up while this one is worked on
     uint32_t next = 0;
     int64_t tok_next = 0;
@@ -1483,20 +1492,18 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         }
         if (tid == 31) warp0_total = G;
       }
-      named_bar(1, 32 * GRAD_WARPS);  // warp 0 is through with the last unit as well
       if (tid < CH) {
+        named_bar(3, CH);
         if (warp == 1) G += warp0_total;
         const float gh = (float)G;
         s_g[tid] = make_float4(gh, (float)(G - (double)gh), b, 0.f);
-      }
-      named_bar(1, 32 * GRAD_WARPS);
-      if (tid < CH) {
+        named_bar(3, CH);
         const float4 x = s_g[tid], z = s_g[63];
         const float into = pow2(x.x + x.y), out = pow2((z.x - x.x) + (z.y - x.y));
         s_into[tid] = a.scale * into;
         s_ki[tid] = -into * b;
         s_ko[tid] = out * b;
-        if (tid == 63) s_over = into;
+        if (tid == 63) s_over[ph] = into;
       }
       if (L < CH) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
         ok = ok && mbar_wait(&full_b, ph, WAIT_CYCLES);
@@ -1524,9 +1531,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         dot += low;
 #pragma unroll
         for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) s_dot[warp] = dot;
+        if (lane == 0) s_dot[ph][warp] = dot;
         warp_arrive(&s0_read);
       }
+      named_bar(1, 32 * GRAD_WARPS);  // the decays are there, the last unit's sums have been read
       ok = ok && mbar_wait(&g1, ph, WAIT_CYCLES);
       tc_fence_after();
       float w[16];
@@ -1572,23 +1580,13 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         for (int n = 0; n < 16; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
       }
       look(u + gridDim.x);
-      // sums of the pairs r >= t > s: dPd's part and dA's of a row added, summed along the row, then down the columns
-      if (isA)
+      // sums of the pairs r >= t > s, dPd's part and dA's each by itself: along the row, then down the columns
 #pragma unroll
-        for (int n = 0; n < 16; ++n) W[t * WP + c0 + n] = w[n];
+      for (int n = 1; n < 16; ++n) w[n] += w[n - 1];
+      s_tot[row][grp] = w[15];
       named_bar(1, 32 * GRAD_WARPS);
-      if (!isA) {
-        float x = 0.f;
-#pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          x += w[n] + W[t * WP + c0 + n];
-          w[n] = x;
-        }
-        s_tot[t][grp] = x;
-      }
-      named_bar(1, 32 * GRAD_WARPS);
-      if (!isA) {
-        const float4 tot = *reinterpret_cast<const float4 *>(s_tot[t]);
+      {
+        const float4 tot = *reinterpret_cast<const float4 *>(s_tot[row]);
         const float before = (grp > 0 ? tot.x : 0.f) + (grp > 1 ? tot.y : 0.f) + (grp > 2 ? tot.z : 0.f);
         // token c + 1 takes the sums up to column c of the rows from it on
 #pragma unroll
@@ -1644,40 +1642,41 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
             }
           }
         }
-        {
-          uint32_t x[16], y[16], z[16];
-          float ko[16];
-          uint16_t kv[16];
-          tmem_ld16(tb + lanes + Q_3 + c0, x);
-          tmem_ld16(tb + lanes + Q_3 + 64u + c0, y);
 #pragma unroll
-          for (int n = 0; n < 16; ++n) kv[n] = lds_u16(ck.at(n));
-          tmem_ld_wait(x);
-          tmem_tie(y);
+        for (int n0 = 0; n0 < 16; n0 += 8) {
+          uint32_t x[8], y[8], z[8];
+          float ko[8];
+          uint16_t kv[8];
+          tmem_ld8(tb + lanes + Q_3 + c0 + n0, x);
+          tmem_ld8(tb + lanes + Q_3 + 64u + c0 + n0, y);
 #pragma unroll
-          for (int n = 0; n < 16; n += 4) {
-            const float4 f4 = *reinterpret_cast<const float4 *>(s_ko + c0 + n);
+          for (int n = 0; n < 8; ++n) kv[n] = lds_u16(ck.at(n0 + n));
+          tmem_ld_wait8(x);
+          tmem_ld_wait8(y);
+#pragma unroll
+          for (int n = 0; n < 8; n += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(s_ko + c0 + n0 + n);
             const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m) ko[n + m] = f[m] * (__uint_as_float(x[n + m]) + __uint_as_float(y[n + m]));
           }
-          tmem_ld16(tb + lanes + Q_2 + c0, x);
-          tmem_ld16(tb + lanes + Q_5 + c0, y);
-          tmem_ld16(tb + lanes + Q_5 + 64u + c0, z);
-          tmem_ld_wait(x);
-          tmem_tie(y);
-          tmem_tie(z);
+          tmem_ld8(tb + lanes + Q_2 + c0 + n0, x);
+          tmem_ld8(tb + lanes + Q_5 + c0 + n0, y);
+          tmem_ld8(tb + lanes + Q_5 + 64u + c0 + n0, z);
+          tmem_ld_wait8(x);
+          tmem_ld_wait8(y);
+          tmem_ld_wait8(z);
 #pragma unroll
-          for (int n = 0; n < 16; n += 4) {
-            const float4 f4 = *reinterpret_cast<const float4 *>(s_ki + c0 + n);
+          for (int n = 0; n < 8; n += 4) {
+            const float4 f4 = *reinterpret_cast<const float4 *>(s_ki + c0 + n0 + n);
             const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              const int r = n + m;
-              const float ki = f[m] * __uint_as_float(x[r]), kx = bf16_bits_to_f32(kv[r]);
+              const int r = n0 + n + m;
+              const float ki = f[m] * __uint_as_float(x[n + m]), kx = bf16_bits_to_f32(kv[n + m]);
               rd[r] = fmaf(kx, ki, rd[r]);
-              ad[r] = kx * ko[r];
-              const float dk = (ki + ko[r]) + (__uint_as_float(y[r]) + __uint_as_float(z[r]));
+              ad[r] = kx * ko[n + m];
+              const float dk = (ki + ko[n + m]) + (__uint_as_float(y[n + m]) + __uint_as_float(z[n + m]));
               if (PER_HEAD) {
                 if (r < rows) fk[r * step] = dk;
               } else {
@@ -1727,7 +1726,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       }
       fence_async_smem();
       warp_arrive(&left);
-      if (warp == 0) {
+      if (warp == GRAD_WARPS - 1) {  // not one of those that begin the next unit
         // tokens lane and lane + 32: sums over the tokens from them on of what is read, over those before of what is left
         float r0 = 0.f, r1 = 0.f, d0 = 0.f, d1 = 0.f;
 #pragma unroll
@@ -1737,7 +1736,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
           d0 += s_red[1][n][lane];
           d1 += s_red[1][n][lane + 32];
         }
-        const float p0 = s_pair[0][lane] + s_pair[1][lane], p1 = s_pair[0][lane + 32] + s_pair[1][lane + 32];
+        const float p0 = (s_pair[0][lane] + s_pair[1][lane]) + (s_pair[2][lane] + s_pair[3][lane]);
+        const float p1 = (s_pair[0][lane + 32] + s_pair[1][lane + 32]) + (s_pair[2][lane + 32] + s_pair[3][lane + 32]);
         const float own0 = d0, own1 = d1;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1750,8 +1750,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         d1 += __shfl_sync(0xffffffffu, d0, 31);
         float over = 0.f;
 #pragma unroll
-        for (int n = 0; n < GRAD_WARPS; ++n) over += s_dot[n];
-        over *= s_over;
+        for (int n = 0; n < GRAD_WARPS; ++n) over += s_dot[ph][n];
+        over *= s_over[ph];
         if (lane < L) {
           a.dg[(tok + lane) * a.H + h] = (p0 + over) + (r0 + (d0 - own0));
           a.dbeta[(tok + lane) * a.H + h] = s_db[lane];
