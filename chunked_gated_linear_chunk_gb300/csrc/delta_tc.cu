@@ -1264,9 +1264,11 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_walks_kernel(const __g
 //     dQ^T = scale e^G (S0 dO^T) + K^T dPd^T
 //     dK^T = -e^G b (S0 dR^T) + e^{G_C - G} b (dS1 E^T) + Q^T dPd + K^T (dA + dA^T)
 // One block per SM walks over (chunk, head) pairs: 16 warps of elementwise
-// work, one that copies and multiplies.  The images of S0 and dS1 follow one another
-// through the same 64 KB; the next pair's S0 and E are on their way while this
-// one's gradients leave.  Products with two parts of a matrix put both into one operand of
+// work, one that copies and multiplies.  dS1's image takes the place of the
+// stacks once those have been multiplied, beside S0's, in whose place the masked
+// tiles come when <S0, dS1> has been summed and dq and dk when all is multiplied.  The
+// next pair's operands are on their way while this one's gradients leave (S0's low
+// part behind them, and the products with it last).  Products with two parts of a matrix put both into one operand of
 // 128 columns where tensor memory has room for the two results (a product of 64
 // columns is bound by its other operand's way through shared memory).
 // TMEM columns: [0, 64) [q; k] k^T, [64, 192) B1, B2 of E's two parts, later [0, 128)
@@ -1290,11 +1292,12 @@ struct GradArgs {
   int *err;
 };
 struct GradSmem {
-  // S: S0's image, then dS1's; X1, X2: per 64 columns 64 rows of dO, 64 of dR (hi, lo); QK: of q and k.
-  // Once the products have read X1, T: dPd hi, lo, dA hi, lo; then dq and dk
+  // S: S0's image, then T: dPd hi, lo, dA hi, lo, and OUT: dq, dk; X1, X2: per 64 columns 64 rows of dO, 64 of dR
+  // (hi, lo), then DS: dS1's image; QK: per 64 channels 64 rows of q, 64 of k
   static constexpr uint32_t S = 0, X1 = S + S_IMAGE, X2 = X1 + 32768, E = X2 + 32768, QK = E + E_IMAGE,
                             BYTES = QK + 32768 + 1024;
-  static constexpr uint32_t T = X1;
+  static constexpr uint32_t T = S, OUT = S + S_IMAGE / 2, DS = X1;
+  static_assert(4 * TILE == S_IMAGE / 2 && S_IMAGE == 2 * 32768, "");
 };
 // 20 warps of 96 registers at launch (the last three of them idle), dealt out again by warpgroup:
 // 512 x 104 + 128 x 64 = 640 x 96.  (Nothing may spill: shared memory leaves the first-level cache a few KB.)
@@ -1306,7 +1309,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   using L_ = GradSmem;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full_a, full_b, full_ds, cleared, s0_read, g1, g2, tiles, g3, left, drain;
+  __shared__ uint64_t full_a, full_b, full_ds, cleared, qk_read, g1, g2, tiles, g3, left, drain;
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ alignas(16) float4 s_g[CH];  // two parts of G (in units of log 2), b
@@ -1323,7 +1326,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   if (tid == 0) {
     abort_flag = 0;
     for (uint64_t *b : {&full_a, &full_b, &full_ds, &g1, &g2, &g3, &drain}) mbar_init(b, 1);
-    for (uint64_t *b : {&cleared, &s0_read, &tiles, &left}) mbar_init(b, GRAD_WARPS);
+    for (uint64_t *b : {&cleared, &qk_read, &tiles, &left}) mbar_init(b, GRAD_WARPS);
     fence_mbar_init();
   }
   follow_wait();
@@ -1331,7 +1334,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = tmem_base, sb = smem_u32(sm);
-  const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S;
+  const uint32_t q = sb + L_::QK, k = q + 8192, x1 = sb + L_::X1, x2 = sb + L_::X2, e = sb + L_::E, si = sb + L_::S, ds = sb + L_::DS;
   // the first used unit from u on (units of unused slots are passed over)
   const uint32_t H = (uint32_t)a.H, units = (uint32_t)a.units;
   auto find = [&](uint32_t u, int64_t &tok, int &L) -> uint32_t {
@@ -1348,35 +1351,28 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       tma_prefetch_desc(&maps.k);
       tma_prefetch_desc(&maps.dO);
       int loads_a = 0, loads_b = 0, loads_ds = 0;
-      auto load_a = [&](uint32_t unit) {
+      auto load_a = [&](uint32_t unit) {  // all but the low part of S0
         const int64_t u = unit;
-        mbar_expect_tx(&full_a, S_IMAGE + E_IMAGE);
-        bulk_load(sm + L_::E, a.e_images + u * E_IMAGE, E_IMAGE, &full_a);
-        bulk_load(sm + L_::S, a.s_images + u * S_IMAGE, S_IMAGE, &full_a);
-        bulk_prefetch_l2(a.ds_images + u * S_IMAGE, S_IMAGE);
-        bulk_prefetch_l2(a.r_images + u * R_IMAGE, R_IMAGE);
         const int h = (int)(unit % H), hq = h / a.share;
+        mbar_expect_tx(&full_a, E_IMAGE + S_IMAGE / 2 + 3 * 32768);
+        bulk_load(sm + L_::E, a.e_images + u * E_IMAGE, E_IMAGE, &full_a);
 #pragma unroll
         for (int cb = 0; cb < 2; ++cb) {
-          tma_prefetch_3d(&maps.q, cb * 64, hq, (int)tok);
-          tma_prefetch_3d(&maps.k, cb * 64, hq, (int)tok);
-          tma_prefetch_3d(&maps.dO, cb * 64, h, (int)tok);
+          tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full_a);
+          tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full_a);
+          tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full_a);
+          tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full_a);
+          bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + u * R_IMAGE + cb * 8192, 8192, &full_a);
+          bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + u * R_IMAGE + 16384 + cb * 8192, 8192, &full_a);
         }
+        bulk_load(sm + L_::S, a.s_images + u * S_IMAGE, S_IMAGE / 2, &full_a);
+        bulk_prefetch_l2(a.s_images + u * S_IMAGE + S_IMAGE / 2, S_IMAGE / 2);
+        bulk_prefetch_l2(a.ds_images + u * S_IMAGE, S_IMAGE);
         ++loads_a;
       };
       auto load_b = [&](uint32_t unit) {
-        const int64_t u = unit;
-        const int h = (int)(unit % H), hq = h / a.share;
-        mbar_expect_tx(&full_b, 3 * 32768);
-#pragma unroll
-        for (int cb = 0; cb < 2; ++cb) {
-          tma_load_3d(sm + L_::QK + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full_b);
-          tma_load_3d(sm + L_::QK + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full_b);
-          tma_load_3d(sm + L_::X1 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full_b);
-          tma_load_3d(sm + L_::X2 + cb * 16384, &maps.dO, cb * 64, h, (int)tok, &full_b);
-          bulk_load(sm + L_::X1 + cb * 16384 + 8192, a.r_images + u * R_IMAGE + cb * 8192, 8192, &full_b);
-          bulk_load(sm + L_::X2 + cb * 16384 + 8192, a.r_images + u * R_IMAGE + 16384 + cb * 8192, 8192, &full_b);
-        }
+        mbar_expect_tx(&full_b, S_IMAGE / 2);
+        bulk_load(sm + L_::S + S_IMAGE / 2, a.s_images + (int64_t)unit * S_IMAGE + S_IMAGE / 2, S_IMAGE / 2, &full_b);
         ++loads_b;
       };
       constexpr uint32_t idQK = idesc_bf16(128, 64, false, false), idB = idesc_bf16(128, 128, false, true);
@@ -1387,10 +1383,10 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       if (u < units) load_a(u);
       for (int it = 0; u < units; ++it) {
         const uint32_t ph = (uint32_t)it & 1u;
-        // the last unit's gradients have left (q, k, the stacks and tensor memory are free)
+        // the last unit's gradients have left (S0's low part and tensor memory are free)
         if (it >= 1 && !(ok = mbar_wait(&left, ph ^ 1u, WAIT_CYCLES))) break;
         load_b(u);
-        ok = mbar_wait(&full_a, ph, WAIT_CYCLES) && mbar_wait(&full_b, ph, WAIT_CYCLES) && mbar_wait(&cleared, ph, WAIT_CYCLES);
+        ok = mbar_wait(&full_a, ph, WAIT_CYCLES) && mbar_wait(&cleared, ph, WAIT_CYCLES);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
@@ -1400,20 +1396,20 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_B, kdesc(x2, ks, 128), image_desc(e, ks), idB, 1);
         mma_commit(&g1);
-        // S0 (hi, lo) [dO | dR hi], S0 hi dR lo
+        // S0 hi [dO | dR hi], S0 hi dR lo, S0 lo [dO | dR hi]
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16(tb + Q_1, image_desc(si + p * (S_IMAGE / 2), ks), kdesc(x1, ks, 128), idKN2, p | ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_1, image_desc(si, ks), kdesc(x1, ks, 128), idKN2, ks);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_2, image_desc(si, ks), kdesc(x2 + 8192, ks, 128), idKN, 1);
+        if (!(ok = mbar_wait(&full_b, ph, WAIT_CYCLES))) break;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_1, image_desc(si + S_IMAGE / 2, ks), kdesc(x1, ks, 128), idKN2, 1);
         mma_commit(&g2);
-        if (!(ok = mbar_wait(&g2, ph, WAIT_CYCLES) && mbar_wait(&s0_read, ph, WAIT_CYCLES))) break;
+        if (!(ok = mbar_wait(&g2, ph, WAIT_CYCLES))) break;
         mbar_expect_tx(&full_ds, S_IMAGE);
-        bulk_load(sm + L_::S, a.ds_images + (int64_t)u * S_IMAGE, S_IMAGE, &full_ds);
+        bulk_load(sm + L_::DS, a.ds_images + (int64_t)u * S_IMAGE, S_IMAGE, &full_ds);
         ++loads_ds;
-        if (!(ok = mbar_wait(&tiles, ph, WAIT_CYCLES))) break;
+        if (!(ok = mbar_wait(&full_ds, ph, WAIT_CYCLES) && mbar_wait(&tiles, ph, WAIT_CYCLES))) break;
         tc_fence_after();
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -1425,15 +1421,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), mdesc(da, ks, TILE), idMN2, 1);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) mma_bf16(tb + Q_5, mdesc(k, ks, 16384), kdesc(da, ks, 128), idKN2, 1);
-        if (!(ok = mbar_wait(&full_ds, ph, WAIT_CYCLES))) break;
-        // dS1 hi [E hi | E lo], dS1 lo E hi
+        // dS1 (there when the tiles are) hi [E hi | E lo], dS1 lo E hi
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(si, ks), image_desc(e, ks), idMN2, ks);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(ds, ks), image_desc(e, ks), idMN2, ks);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(si + S_IMAGE / 2, ks), image_desc(e, ks), idMN, 1);
+        for (int ks = 0; ks < 8; ++ks) mma_bf16(tb + Q_3, image_desc(ds + S_IMAGE / 2, ks), image_desc(e, ks), idMN, 1);
         mma_commit(&g3);
         u = find(u + gridDim.x, tok, L);
-        if (!(ok = mbar_wait(&g3, ph, WAIT_CYCLES))) break;
+        if (!(ok = mbar_wait(&g3, ph, WAIT_CYCLES) && mbar_wait(&qk_read, ph, WAIT_CYCLES))) break;
         if (u < units) load_a(u);
       }
       if (!ok) {  // nothing of this block's is in flight when it leaves
@@ -1472,15 +1467,6 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       const int h = (int)(u % H);
       tok = tok_next;
       L = L_next;
-      uint4 dh[4], dl[4];  // of dS1's image, for <S0, dS1>
-      {
-        const char *img = a.ds_images + (int64_t)u * S_IMAGE + tid * 16;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          dh[n] = __ldg(reinterpret_cast<const uint4 *>(img + n * 8192));
-          dl[n] = __ldg(reinterpret_cast<const uint4 *>(img + S_IMAGE / 2 + n * 8192));
-        }
-      }
       // decays, while the copies run
       double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;
       const float b = b_next;
@@ -1506,7 +1492,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         if (tid == 63) s_over[ph] = into;
       }
       if (L < CH) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
-        ok = ok && mbar_wait(&full_b, ph, WAIT_CYCLES);
+        ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES);
         for (int n = tid; n < (CH - L) * 4 * 8; n += 32 * GRAD_WARPS) {
           const int c = n % 8, x = n / 8 % 4, r = L + n / 32;
           st_shared_v4(sb + L_::QK + x * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
@@ -1514,30 +1500,11 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         fence_async_smem();
       }
       warp_arrive(&cleared);
-      {  // <S0, dS1>, while the first products run
-        ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES);
-        float dot = 0.f, low = 0.f;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const uint4 hi = lds_u4(si + tid * 16 + n * 8192), lo = lds_u4(si + S_IMAGE / 2 + tid * 16 + n * 8192);
-          const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, y[4] = {lo.x, lo.y, lo.z, lo.w};
-          const uint32_t v[4] = {dh[n].x, dh[n].y, dh[n].z, dh[n].w}, z[4] = {dl[n].x, dl[n].y, dl[n].z, dl[n].w};
-#pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            dot = fma_pairs(x[m], v[m], dot);
-            low = fma_pairs(x[m], z[m], fma_pairs(y[m], v[m], low));
-          }
-        }
-        dot += low;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        if (lane == 0) s_dot[ph][warp] = dot;
-        warp_arrive(&s0_read);
-      }
       named_bar(1, 32 * GRAD_WARPS);  // the decays are there, the last unit's sums have been read
       ok = ok && mbar_wait(&g1, ph, WAIT_CYCLES);
       tc_fence_after();
       float w[16];
+      uint32_t hi[8], lo[8];
       {
         uint32_t x[16], y[16];
         tmem_ld16(tb + lanes + Q_B + c0, x);
@@ -1563,19 +1530,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         tmem_ld16(tb + lanes + Q_QK + c0, x);
         tmem_ld_wait(x);
         tc_fence_before();
-        ok = ok && mbar_wait(&g2, ph, WAIT_CYCLES);  // the stacks have been read
-        const uint32_t tile = sb + L_::T + (isA ? 2 * TILE : 0);
 #pragma unroll
-        for (int n = 0; n < 16; n += 8) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int m = 0; m < 4; ++m) split2(w[n + 2 * m], w[n + 2 * m + 1], hi[m], lo[m]);
-          const uint32_t o = tile + sw128_off(t, c0 + n, 64);
-          st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
-          st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
-        }
-        fence_async_smem();
-        warp_arrive(&tiles);
+        for (int n = 0; n < 8; ++n) split2(w[2 * n], w[2 * n + 1], hi[n], lo[n]);
 #pragma unroll
         for (int n = 0; n < 16; ++n) w[n] = c0 + n < t ? w[n] * __uint_as_float(x[n]) : 0.f;
       }
@@ -1605,24 +1561,65 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         if (lane < 16 && c0 + lane + 1 < CH) s_pair[qw][c0 + lane + 1] = w[0];
         if (lane == 0 && grp == 0) s_pair[qw][0] = 0.f;
       }
-      ok = ok && mbar_wait(&g3, ph, WAIT_CYCLES) && mbar_wait(&full_b, ph, WAIT_CYCLES);
+      {  // <S0, dS1>; then the tiles in S0's place
+        ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES) && mbar_wait(&full_b, ph, WAIT_CYCLES) &&
+             mbar_wait(&full_ds, ph, WAIT_CYCLES);
+        float dot = 0.f, low = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const uint32_t at = tid * 16 + n * 8192;
+          const uint4 sh = lds_u4(si + at), sl = lds_u4(si + S_IMAGE / 2 + at);
+          const uint4 dh = lds_u4(ds + at), dl = lds_u4(ds + S_IMAGE / 2 + at);
+          const uint32_t x[4] = {sh.x, sh.y, sh.z, sh.w}, y[4] = {sl.x, sl.y, sl.z, sl.w};
+          const uint32_t v[4] = {dh.x, dh.y, dh.z, dh.w}, z[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            dot = fma_pairs(x[m], v[m], dot);
+            low = fma_pairs(x[m], z[m], fma_pairs(y[m], v[m], low));
+          }
+        }
+        named_bar(1, 32 * GRAD_WARPS);  // everyone has read S0
+        const uint32_t tile = sb + L_::T + (isA ? 2 * TILE : 0);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint32_t o = tile + sw128_off(t, c0 + 8 * n, 64);
+          st_shared_v4(o, hi[4 * n], hi[4 * n + 1], hi[4 * n + 2], hi[4 * n + 3]);
+          st_shared_v4(o + TILE, lo[4 * n], lo[4 * n + 1], lo[4 * n + 2], lo[4 * n + 3]);
+        }
+        fence_async_smem();
+        warp_arrive(&tiles);
+        dot += low;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (lane == 0) s_dot[ph][warp] = dot;
+      }
+      // q and k of the thread's channel and tokens, before the next unit's take their place
+      uint32_t qv[8], kv[8];
+      {
+        const ColBf16 cq(q, c0, row, 16384u), ck(k, c0, row, 16384u);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+          qv[n] = (uint32_t)lds_u16(cq.at(2 * n)) | (uint32_t)lds_u16(cq.at(2 * n + 1)) << 16;
+          kv[n] = (uint32_t)lds_u16(ck.at(2 * n)) | (uint32_t)lds_u16(ck.at(2 * n + 1)) << 16;
+        }
+        warp_arrive(&qk_read);
+      }
+      auto half_of = [](uint32_t x, int n) { return __uint_as_float(n & 1 ? x & 0xffff0000u : x << 16); };
+      ok = ok && mbar_wait(&g3, ph, WAIT_CYCLES);
       tc_fence_after();
       {
         // lane: key channel; tokens c0 .. c0 + 15
         const int ch = row;
         float rd[16], ad[16];  // what token t's query and key read of S0, what its key left in S1, of this channel
-        const ColBf16 cq(q, c0, ch, 16384u), ck(k, c0, ch, 16384u), oq(sb + L_::X1, c0, ch), ok_(sb + L_::X1 + 16384, c0, ch);
+        const ColBf16 oq(sb + L_::OUT, c0, ch), ok_(sb + L_::OUT + 16384, c0, ch);
         float *fq = (float *)a.dq + ((tok + c0) * a.H + h) * (int64_t)a.K + ch;
         float *fk = (float *)a.dk + ((tok + c0) * a.H + h) * (int64_t)a.K + ch;
         const int64_t step = (int64_t)a.H * a.K;
         const int rows = PER_HEAD && ch < a.K ? L - c0 : 0;
         {
           uint32_t x[16], y[16];
-          uint16_t qv[16];
           tmem_ld16(tb + lanes + Q_1 + c0, x);
           tmem_ld16(tb + lanes + Q_4 + c0, y);
-#pragma unroll
-          for (int n = 0; n < 16; ++n) qv[n] = lds_u16(cq.at(n));
           tmem_ld_wait(x);
           tmem_tie(y);
 #pragma unroll
@@ -1632,7 +1629,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const float qi = f[m] * __uint_as_float(x[n + m]);
-              rd[n + m] = qi * bf16_bits_to_f32(qv[n + m]);
+              rd[n + m] = qi * half_of(qv[(n + m) / 2], m);
               const float dq = qi + __uint_as_float(y[n + m]);
               if (PER_HEAD) {
                 if (n + m < rows) fq[(n + m) * step] = dq;
@@ -1646,11 +1643,8 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         for (int n0 = 0; n0 < 16; n0 += 8) {
           uint32_t x[8], y[8], z[8];
           float ko[8];
-          uint16_t kv[8];
           tmem_ld8(tb + lanes + Q_3 + c0 + n0, x);
           tmem_ld8(tb + lanes + Q_3 + 64u + c0 + n0, y);
-#pragma unroll
-          for (int n = 0; n < 8; ++n) kv[n] = lds_u16(ck.at(n0 + n));
           tmem_ld_wait8(x);
           tmem_ld_wait8(y);
 #pragma unroll
@@ -1673,7 +1667,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               const int r = n0 + n + m;
-              const float ki = f[m] * __uint_as_float(x[n + m]), kx = bf16_bits_to_f32(kv[n + m]);
+              const float ki = f[m] * __uint_as_float(x[n + m]), kx = half_of(kv[r / 2], m);
               rd[r] = fmaf(kx, ki, rd[r]);
               ad[r] = kx * ko[n + m];
               const float dk = (ki + ko[n + m]) + (__uint_as_float(y[n + m]) + __uint_as_float(z[n + m]));
@@ -1718,7 +1712,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
         for (int n = 0; n < 4; ++n) {
           const int i = tid + 512 * (n & 1), r = i >> 4, c = (i & 15) * 8;
           if (r < L && c < a.K) {
-            const uint4 x = lds_u4(sb + L_::X1 + (n >> 1) * 16384 + sw128_off(r, c, 64));
+            const uint4 x = lds_u4(sb + L_::OUT + (n >> 1) * 16384 + sw128_off(r, c, 64));
             __nv_bfloat16 *dst = (__nv_bfloat16 *)(n >> 1 ? a.dk : a.dq) + ((tok + r) * a.H + h) * (int64_t)a.K + c;
             st_global_v4(dst, x.x, x.y, x.z, x.w);
           }
