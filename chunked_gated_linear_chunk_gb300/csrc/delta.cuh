@@ -67,11 +67,10 @@ struct Saved {
 };
 
 // ---- CUDA-core kernels (delta_simt.cu): any K, V up to 256, both types ----
-// Token by token.  Forward: o (may be null), ht (may be null), and with
-// `saved` the states before the chunks and E.
-cudaError_t simt_scan(const Call &c, void *o, float *ht, const Saved *saved);
-// Backwards in time: dv, dR, the state gradients after the chunks, dh0.
-cudaError_t simt_scan_back(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved);
+// Token by token: o, ht (may be null).
+cudaError_t simt_fwd(const Call &c, void *o, float *ht);
+// The backward's passes forwards and backwards in time: what `saved` holds, dv, dh0 (may be null).
+cudaError_t simt_scans(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved);
 // dq, dk, dg, dbeta from what the two passes saved, every chunk by itself.
 // dq and dk: [BT, H, K] fp32 per value head where heads share q and k (to be
 // summed by reduce_heads), [BT, H, K] dtype otherwise.

@@ -4,13 +4,12 @@
 // The forward and the two passes of the backward that carry a state run token
 // by token: a state's value columns do not see each other, so a warp owns 8
 // columns of one (document, head), each thread KR key rows of two of them in
-// registers (two columns are one packed fp32 operation), and one exchange
+// registers, and one exchange
 // over the 8 lanes of a column pair gives S^T k and S^T q of a token at once:
 //     o_t = scale (e^g S^T q + (q . k) u),  u = b (v - e^g S^T k)
 // (both on the state before the token).  The other half of the block's warps
 // converts the next 16 tokens' q, k, v into shared memory meanwhile.  Bound by
-// the latency of that dependence, about 230 cycles per token; any decay is
-// exact here.  The gradients of q, k, g and beta then take every chunk of 64 tokens
+// the latency of that dependence; any decay is exact here.  The gradients of q, k, g and beta then take every chunk of 64 tokens
 // by itself (simt_grads), as products of 64 x 64 tiles.
 #include <algorithm>
 
@@ -26,22 +25,12 @@ constexpr int TT = 16;         // tokens staged at once
 constexpr int COLS = 32;       // value columns of a block (4 warps x 8)
 constexpr int THREADS = 256;   // 4 warps that compute, 4 that stage
 
+// Two columns at a time, as single operations: the packed ones take two cycles
+// each and want the key's channel twice in a register pair.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 o;
-  asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 c, a, b, c;\n mov.b64 {%0, %1}, c;\n}\n"
-      : "=f"(o.x), "=f"(o.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return o;
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 o;
-  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " mul.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
-      : "=f"(o.x), "=f"(o.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return o;
-}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 enum Mode { FWD, STATES, BACK };
@@ -68,13 +57,13 @@ struct alignas(16) Tile {
 };
 
 template <typename T, int KR, int MODE>
-__global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
+__device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
   extern __shared__ __align__(16) uint8_t smem[];
   Tile<KR> *tiles = reinterpret_cast<Tile<KR> *>(smem);  // two
   constexpr int KP = LK * KR;
   constexpr bool NEEDQ = MODE != STATES;
-  const int slice = (int)(blockIdx.x % a.slices);
-  const int64_t dh = blockIdx.x / a.slices;
+  const int slice = (int)(block % a.slices);
+  const uint32_t dh = block / a.slices;
   const int h = (int)(dh % a.H);
   const int64_t d = dh / a.H;
   const int hq = h / a.share, v0 = slice * COLS;
@@ -92,31 +81,41 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
     Tile<KR> &t = tiles[i & 1];
     const int64_t t0 = (int64_t)tile_of(i) * TT;
     const int len = (int)min((int64_t)TT, n - t0);
-    for (int r = warp - 4; r < len; r += 4) {
-      const int64_t tok = s0 + t0 + r;
+    // a warp's four tokens at once: their loads are all in flight before the first is used
+    constexpr int N = TT / 4;
+    float kx[N][KP / 32], qx[N][KP / 32], vx[N], gx[N], bx[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int r = warp - 4 + 4 * n;
+      const int64_t tok = s0 + t0 + (r < len ? r : 0);
       const T *qr = a.q + tok * a.qs + (int64_t)hq * a.K, *kr = a.k + tok * a.ks + (int64_t)hq * a.K;
-      float dot = 0.f, kx[KP / 32], qx[KP / 32];
 #pragma unroll
       for (int e = 0; e < KP / 32; ++e) {
         const int c = lane + 32 * e;
-        kx[e] = c < a.K ? to_f32(kr[c]) : 0.f;
-        qx[e] = NEEDQ && c < a.K ? to_f32(qr[c]) : 0.f;
+        kx[n][e] = c < a.K ? to_f32(kr[c]) : 0.f;
+        qx[n][e] = NEEDQ && c < a.K ? to_f32(qr[c]) : 0.f;
       }
-      const float vx = v0 + lane < a.V ? to_f32(a.v[tok * a.vs + (int64_t)h * a.V + v0 + lane]) : 0.f;
-      const float gx = a.g[tok * a.H + h], bx = a.beta[tok * a.H + h];
+      vx[n] = v0 + lane < a.V ? to_f32(a.v[tok * a.vs + (int64_t)h * a.V + v0 + lane]) : 0.f;
+      gx[n] = a.g[tok * a.H + h];
+      bx[n] = a.beta[tok * a.H + h];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int r = warp - 4 + 4 * n;
+      float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < KP / 32; ++e) {
-        t.k[r][lane + 32 * e] = kx[e];
-        if (NEEDQ) t.q[r][lane + 32 * e] = qx[e];
-        dot = fmaf(kx[e], qx[e], dot);
+        t.k[r][lane + 32 * e] = kx[n][e];
+        if (NEEDQ) t.q[r][lane + 32 * e] = qx[n][e];
+        dot = fmaf(kx[n][e], qx[n][e], dot);
       }
-      t.v[r][lane] = vx;
+      t.v[r][lane] = vx[n];
       if (NEEDQ)
 #pragma unroll
         for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
       if (lane == 0) {
-        t.a[r] = expf(gx);
-        t.b[r] = bx;
+        t.a[r] = expf(gx[n]);
+        t.b[r] = bx[n];
         t.qk[r] = dot;
       }
     }
@@ -162,6 +161,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
       if (MODE == STATES && t0 % C == 0) put_state(a.states + ((slot0 + t0 / C) * a.H + h) * a.K * a.V);
       if (MODE == BACK && ((t0 + TT) % C == 0 || i == 0))
         put_state(a.states + ((slot0 + t0 / C) * a.H + h) * a.K * a.V);
+      const int64_t at0 = ((s0 + t0) * a.H + h) * a.V + col, step = (int64_t)a.H * a.V;
       for (int rr = 0; rr < len; ++rr) {
         const int r = MODE == BACK ? len - 1 - rr : rr;
         float2 xk = both(0.f), xq = both(0.f);
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
         }
         const float2 v = *reinterpret_cast<const float2 *>(&t.v[r][cl]);
         const float dec = t.a[r], b = t.b[r];
-        const int64_t at = ((s0 + t0 + r) * a.H + h) * a.V + col;
+        const int64_t at = at0 + r * step;
         if (MODE != BACK) {
           const float2 e = make_float2(v.x - dec * xk.x, v.y - dec * xk.y);
           const float2 u = make_float2(b * e.x, b * e.y);
@@ -230,9 +230,23 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
   if (!stages && a.last) put_state(a.last + mat);
 }
 
-template <typename T, int MODE>
-cudaError_t scan_as(const Call &c, const void *v, int64_t vs, const float *seed, float *last, void *out, float *states,
-                    float *rows) {
+template <typename T, int KR>
+__global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
+  scan<T, KR, FWD>(a, blockIdx.x);
+}
+// The backward's two passes do not need one another: the first half of the
+// blocks goes backwards in time, the second forwards.
+template <typename T, int KR>
+__global__ void __launch_bounds__(THREADS) scans_kernel(const ScanArgs<T> back, const ScanArgs<T> states, uint32_t half) {
+  if (blockIdx.x < half)
+    scan<T, KR, BACK>(back, blockIdx.x);
+  else
+    scan<T, KR, STATES>(states, blockIdx.x - half);
+}
+
+template <typename T>
+ScanArgs<T> scan_args(const Call &c, const void *v, int64_t vs, const float *seed, float *last, void *out, float *states,
+                      float *rows) {
   ScanArgs<T> a;
   a.q = (const T *)c.p.q;
   a.k = (const T *)c.p.k;
@@ -254,24 +268,49 @@ cudaError_t scan_as(const Call &c, const void *v, int64_t vs, const float *seed,
   a.V = (int)c.p.V;
   a.slices = (a.V + COLS - 1) / COLS;
   a.scale = c.p.scale;
+  return a;
+}
+
+// go(kernel, bytes of shared memory) with the kernel for K's rows
+template <template <int> class Kernel, typename F>
+cudaError_t by_rows(int64_t K, F go) {
+  if (K <= 32) return go(Kernel<4>::get(), 2 * sizeof(Tile<4>));
+  if (K <= 64) return go(Kernel<8>::get(), 2 * sizeof(Tile<8>));
+  if (K <= 128) return go(Kernel<16>::get(), 2 * sizeof(Tile<16>));
+  return go(Kernel<32>::get(), 2 * sizeof(Tile<32>));
+}
+template <typename T> struct Scan {
+  template <int KR> struct One { static auto get() { return scan_kernel<T, KR>; } };
+  template <int KR> struct Two { static auto get() { return scans_kernel<T, KR>; } };
+};
+
+template <typename T>
+cudaError_t scan_fwd(const Call &c, void *o, float *ht) {
+  const ScanArgs<T> a = scan_args<T>(c, c.p.v, c.p.vs, c.p.h0, ht, o, nullptr, nullptr);
   const int64_t ctas = c.docs.n * c.p.H * a.slices;
   if (ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  auto go = [&](auto kernel, size_t smem) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = by_rows<Scan<T>::template One>(c.p.K, [&](auto kernel, size_t smem) -> cudaError_t {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)ctas, THREADS, smem, c.st>>>(a);
     return cudaGetLastError();
-  };
-  cudaError_t e;
-  if (a.K <= 32)
-    e = go(scan_kernel<T, 4, MODE>, 2 * sizeof(Tile<4>));
-  else if (a.K <= 64)
-    e = go(scan_kernel<T, 8, MODE>, 2 * sizeof(Tile<8>));
-  else if (a.K <= 128)
-    e = go(scan_kernel<T, 16, MODE>, 2 * sizeof(Tile<16>));
-  else
-    e = go(scan_kernel<T, 32, MODE>, 2 * sizeof(Tile<32>));
-  mark_launch(MODE == FWD ? "delta_scan" : MODE == STATES ? "delta_scan_states" : "delta_scan_back", c.st);
+  });
+  mark_launch("delta_scan", c.st);
+  return e;
+}
+template <typename T>
+cudaError_t scans_bwd(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved) {
+  const ScanArgs<T> st = scan_args<T>(c, c.p.v, c.p.vs, c.p.h0, nullptr, nullptr, saved.s0, saved.e);
+  const ScanArgs<T> bk = scan_args<T>(c, dO, c.p.H * c.p.V, dht, dh0, dv, saved.ds1, saved.dr);
+  const int64_t ctas = c.docs.n * c.p.H * st.slices;
+  if (2 * ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = by_rows<Scan<T>::template Two>(c.p.K, [&](auto kernel, size_t smem) -> cudaError_t {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)(2 * ctas), THREADS, smem, c.st>>>(bk, st, (uint32_t)ctas);
+    return cudaGetLastError();
+  });
+  mark_launch("delta_scans", c.st);
   return e;
 }
 
@@ -589,19 +628,13 @@ __global__ void __launch_bounds__(256) reduce_heads_kernel(const float *x, T *ou
 
 }  // namespace
 
-cudaError_t simt_scan(const Call &c, void *o, float *ht, const Saved *saved) {
-  if (saved)
-    return c.dtype == GLACORE_BF16
-               ? scan_as<__nv_bfloat16, STATES>(c, c.p.v, c.p.vs, c.p.h0, ht, nullptr, saved->s0, saved->e)
-               : scan_as<float, STATES>(c, c.p.v, c.p.vs, c.p.h0, ht, nullptr, saved->s0, saved->e);
-  return c.dtype == GLACORE_BF16 ? scan_as<__nv_bfloat16, FWD>(c, c.p.v, c.p.vs, c.p.h0, ht, o, nullptr, nullptr)
-                                 : scan_as<float, FWD>(c, c.p.v, c.p.vs, c.p.h0, ht, o, nullptr, nullptr);
+cudaError_t simt_fwd(const Call &c, void *o, float *ht) {
+  return c.dtype == GLACORE_BF16 ? scan_fwd<__nv_bfloat16>(c, o, ht) : scan_fwd<float>(c, o, ht);
 }
 
-cudaError_t simt_scan_back(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved) {
-  const int64_t vs = c.p.H * c.p.V;
-  return c.dtype == GLACORE_BF16 ? scan_as<__nv_bfloat16, BACK>(c, dO, vs, dht, dh0, dv, saved.ds1, saved.dr)
-                                 : scan_as<float, BACK>(c, dO, vs, dht, dh0, dv, saved.ds1, saved.dr);
+cudaError_t simt_scans(const Call &c, const void *dO, const float *dht, void *dv, float *dh0, const Saved &saved) {
+  return c.dtype == GLACORE_BF16 ? scans_bwd<__nv_bfloat16>(c, dO, dht, dv, dh0, saved)
+                                 : scans_bwd<float>(c, dO, dht, dv, dh0, saved);
 }
 
 cudaError_t simt_grads(const Call &c, const void *dO, const Saved &saved, void *dq, void *dk, bool per_head, float *dg,
