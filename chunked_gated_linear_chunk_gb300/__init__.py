@@ -228,6 +228,14 @@ def _raw_stream(t):
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
+def _call(fn, t, *args):
+    """fn(*args, stream): on t's device and its current stream."""
+    if torch._C._cuda_getDevice() == t.get_device():
+        return fn(*args, _raw_stream(t))
+    with torch.cuda.device(t.device):
+        return fn(*args, _raw_stream(t))
+
+
 def _addr(t):
     """Device address for a pointer argument (None: NULL)."""
     return None if t is None else t.data_ptr()
@@ -526,8 +534,7 @@ def _step(kind, q, k, v, g, state, state_indices, scale, out, poison, beta=None)
                    g.data_ptr(), 0, B if T else 0, 0, 0, 0, qs, ks, vs)
     lib = _lib or load()
     if kind == "delta":
-        st = lib.delta_step(p, beta.data_ptr(), state.data_ptr(), state.shape[0], _addr(idx), o.data_ptr(),
-                            _raw_stream(q))
+        st = _call(lib.delta_step, q, p, beta.data_ptr(), state.data_ptr(), state.shape[0], _addr(idx), o.data_ptr())
     else:
         st = (lib.gla_step if kind == "gla" else lib.ssd_step)(p, state.data_ptr(), state.shape[0], _addr(idx),
                                                                o.data_ptr(), _raw_stream(q))
@@ -550,12 +557,52 @@ def ssd_step(q, k, v, g, state, state_indices=None, scale=1.0, out=None, poison=
 
 
 # ---- the gated delta rule ------------------------------------------------------
-def _delta_beta(beta, g, device):
-    beta = _contig(beta, torch.float32)
-    if beta.shape != g.shape:
-        raise ValueError("beta must be [B,T,H]")
-    _same_device(device, beta=beta)
-    return beta
+class _DeltaProblem:
+    """Checked operands of delta_fwd / delta_bwd and their glacore_problem as bytes."""
+
+    __slots__ = ("q", "k", "v", "g", "beta", "seg", "h0", "n", "dtype", "device", "states", "fields")
+
+    def __init__(self, q, k, v, g, beta, scale, segment_ids, initial_state, n_seqs):
+        (q, qs), (k, ks), (v, vs) = _tokens(q), _tokens(k), _tokens(v)
+        g, beta = _contig(g, torch.float32), _contig(beta, torch.float32)
+        if not (q.dtype == k.dtype == v.dtype):
+            raise TypeError("q, k, v must share one dtype")
+        B, T, Hqk, K = q.shape
+        H, V = v.shape[2:]
+        if k.shape != q.shape or v.shape[0] != B or v.shape[1] != T:
+            raise ValueError("shape mismatch between q, k, v")
+        if tuple(g.shape) != (B, T, H) or beta.shape != g.shape:
+            raise ValueError("the gate and beta must be [B,T,H]")
+        seg, h0 = _contig(segment_ids, torch.int32), _contig(initial_state, torch.float32)
+        if seg is not None and tuple(seg.shape) != (B, T):
+            raise ValueError("segment_ids must be [B,T]")
+        at = q.get_device()
+        for t in (k, v, g, beta, seg, h0):
+            if t is not None and t.get_device() != at:
+                _same_device(q.device, k=k, v=v, g=g, beta=beta, segment_ids=seg, initial_state=h0)
+        if seg is None:
+            n = B if T > 0 else 0
+        else:
+            n = n_seqs if n_seqs is not None else count_docs(seg)
+        self.states = (n, H, K, V)
+        if h0 is not None and tuple(h0.shape) != self.states:
+            raise ValueError(f"initial_state must be [{n},{H},{K},{V}]")
+        self.q, self.k, self.v, self.g, self.beta, self.seg, self.h0, self.n = q, k, v, g, beta, seg, h0, n
+        self.dtype, self.device = q.dtype, q.device
+        self.fields = (B, T, H, Hqk, K, V, _dtype_code(q), 0, K ** -0.5 if scale is None else scale, 0, q.data_ptr(),
+                       k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(seg) or 0, n, _addr(h0) or 0), (qs, ks, vs)
+
+    def pack(self, ws=0, size=0):
+        return _PACK.pack(*self.fields[0], ws, size, *self.fields[1])
+
+    def scratch(self, kind, workspace):
+        """(workspace or None, the problem's bytes with it)."""
+        p = self.pack()
+        need = getattr(_lib or load(), kind)(p)
+        if not need:
+            return None, p
+        ws = _scratch(need, self.device, workspace)
+        return ws, self.pack(ws.data_ptr(), ws.numel())
 
 
 def delta_fwd(q, k, v, g, beta, scale=None, segment_ids=None, initial_state=None, output_final_state=False,
@@ -565,20 +612,17 @@ def delta_fwd(q, k, v, g, beta, scale=None, segment_ids=None, initial_state=None
     q, k [B,T,Hqk,K] (k of unit length: qk_norm_fwd), v [B,T,H,V], g (log
     decay) and beta [B,T,H] fp32; scale K^-1/2 unless given.  segment_ids,
     initial_state and n_seqs as in ssd_fwd.  Returns (o, final_state or None)."""
-    if scale is None:
-        scale = q.shape[-1] ** -0.5
-    p, keep = _problem(q, k, v, g, scale, segment_ids, initial_state, 0, n_seqs, True)
-    dev, dt = keep[0].device, keep[0].dtype
-    beta = _delta_beta(beta, keep[3], dev)
-    o = _given(out, "out", keep[2].shape, dt, dev) if out is not None else _new(tuple(keep[2].shape), dt, dev, poison)
+    p = _DeltaProblem(q, k, v, g, beta, scale, segment_ids, initial_state, n_seqs)
+    dev, dt, shape = p.device, p.dtype, p.v.shape
+    o = _given(out, "out", shape, dt, dev) if out is not None else _new(tuple(shape), dt, dev, poison)
     ht = None
     if output_final_state:
-        shape = (p.n_seqs, p.H, p.K, p.V)
-        ht = (_given(final_out, "final_out", shape, torch.float32, dev) if final_out is not None
-              else _new(shape, torch.float32, dev, poison))
-    ws = _workspace(p, "delta_fwd", dev, workspace)
-    _check(load().delta_fwd(ctypes.byref(p), _ptr(beta), _ptr(o), _ptr(ht), _stream(dev)), "delta_fwd")
-    del ws, keep
+        ht = (_given(final_out, "final_out", p.states, torch.float32, dev) if final_out is not None
+              else _new(p.states, torch.float32, dev, poison))
+    ws, packed = p.scratch("delta_fwd_workspace_size", workspace)
+    st = _call((_lib or load()).delta_fwd, p.q, packed, p.beta.data_ptr(), o.data_ptr(), _addr(ht))
+    if st:
+        _check(st, "delta_fwd")
     return o, ht
 
 
@@ -587,34 +631,29 @@ def delta_bwd(q, k, v, g, beta, do, scale=None, segment_ids=None, initial_state=
     """Gradients of delta_fwd.  do [B,T,H,V] and dht [n_seqs,H,K,V] (or None)
     are those of o and the final state.  Returns (dq, dk, dv, dg, dbeta, dh0
     or None)."""
-    if scale is None:
-        scale = q.shape[-1] ** -0.5
-    p, keep = _problem(q, k, v, g, scale, segment_ids, initial_state, 0, n_seqs, True)
-    dev, dt = keep[0].device, keep[0].dtype
-    beta = _delta_beta(beta, keep[3], dev)
-    do = _contig(do, dt)
-    dht = _contig(dht, torch.float32)
-    if do.shape != keep[2].shape:
+    p = _DeltaProblem(q, k, v, g, beta, scale, segment_ids, initial_state, n_seqs)
+    dev, dt = p.device, p.dtype
+    do, dht = _contig(do, dt), _contig(dht, torch.float32)
+    if do.shape != p.v.shape:
         raise ValueError("do must match v")
-    states = (p.n_seqs, p.H, p.K, p.V)
-    if dht is not None and tuple(dht.shape) != states:
+    if dht is not None and tuple(dht.shape) != p.states:
         raise ValueError("dht must be [n_seqs,H,K,V]")
     _same_device(dev, do=do, dht=dht)
+    like = (p.q, p.k, p.v, p.g, p.beta)
     if outs is not None:
         dq, dk, dv, dg, dbeta, dh0 = outs
-        for t, name, like in ((dq, "dq", keep[0]), (dk, "dk", keep[1]), (dv, "dv", keep[2]), (dg, "dg", keep[3]),
-                              (dbeta, "dbeta", beta)):
-            _given(t, name, like.shape, like.dtype, dev)
+        for t, name, x in zip((dq, dk, dv, dg, dbeta), ("dq", "dk", "dv", "dg", "dbeta"), like):
+            _given(t, name, x.shape, x.dtype, dev)
         if dh0 is not None:
-            _given(dh0, "dh0", states, torch.float32, dev)
+            _given(dh0, "dh0", p.states, torch.float32, dev)
     else:
-        dq, dk, dv, dg, dbeta = (_new(tuple(x.shape), x.dtype, dev, poison) for x in (*keep[:4], beta))
-        dh0 = _new(states, torch.float32, dev, poison) if initial_state is not None else None
-    ws = _workspace(p, "delta_bwd", dev, workspace)
-    st = load().delta_bwd(ctypes.byref(p), _ptr(beta), _ptr(do), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
-                          _ptr(dbeta), _ptr(dh0), _stream(dev))
-    _check(st, "delta_bwd")
-    del ws, keep
+        dq, dk, dv, dg, dbeta = (_new(tuple(x.shape), x.dtype, dev, poison) for x in like)
+        dh0 = _new(p.states, torch.float32, dev, poison) if initial_state is not None else None
+    ws, packed = p.scratch("delta_bwd_workspace_size", workspace)
+    st = _call((_lib or load()).delta_bwd, p.q, packed, p.beta.data_ptr(), do.data_ptr(), _addr(dht), dq.data_ptr(),
+               dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dh0))
+    if st:
+        _check(st, "delta_bwd")
     return dq, dk, dv, dg, dbeta, dh0
 
 
@@ -682,7 +721,7 @@ def qk_norm_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, eps=
         qo, ko = _given(outs[0], "q out", q.shape, dt, dev), _given(outs[1], "k out", k.shape, dt, dev)
     else:
         qo, ko = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
-    st = (_lib or load()).qk_norm_fwd(pack(), qo.data_ptr(), ko.data_ptr(), _raw_stream(q))
+    st = _call((_lib or load()).qk_norm_fwd, q, pack(), qo.data_ptr(), ko.data_ptr())
     if st:
         _check(st, "qk_norm_fwd")
     return qo, ko
@@ -709,8 +748,8 @@ def qk_norm_bwd(q, k, dqo, dko, wq=None, wk=None, cos=None, sin=None, positions=
         dwq, dwk = (torch.empty(D, dtype=torch.float32, device=dev) for _ in range(2))
     lib = _lib or load()
     ws = _scratch(lib.qk_norm_bwd_workspace_size(pack()), dev, workspace)
-    st = lib.qk_norm_bwd(pack(ws.data_ptr(), ws.numel()), dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                         dwq.data_ptr(), dwk.data_ptr(), _raw_stream(q))
+    st = _call(lib.qk_norm_bwd, q, pack(ws.data_ptr(), ws.numel()), dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(),
+               dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr())
     if st:
         _check(st, "qk_norm_bwd")
     return dq, dk, dwq, dwk

@@ -38,7 +38,7 @@ Layout layout(const glacore_problem *p, bool backward) {
   }
   // a document's last chunk may be short: at most one more than its tokens fill
   L.slots = p->segment_ids ? std::min(BT, BT / C + n) : p->B * ((p->T + C - 1) / C);
-  L.on_tc = tc_supported(p);
+  L.on_tc = tc_supported(p) && L.slots * p->H < ((int64_t)1 << 30) && n * p->H < ((int64_t)1 << 30);  // units in 32 bits
   // the scratch of one call serves either family: the addresses of the outputs decide (run_fwd, run_bwd)
   if (L.on_tc) take(L.tc, tc_workspace(L.slots, p->H, backward));
   if (backward) {

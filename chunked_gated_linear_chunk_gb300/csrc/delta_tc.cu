@@ -20,6 +20,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "delta.cuh"
 #include "tc_common.cuh"
@@ -512,6 +513,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
     fence_mbar_init();
   }
   follow_wait();
+  fence_async_all();  // what the kernel before wrote with plain stores is read by copies here
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -707,6 +709,9 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
           }
           tmem_st8(tb + lanes + T_R3 + 8u * grp, l3);
         }
+        // scale e^G for the output, which outlives the stage; X of this chunk began behind o_free of the one
+        // before the last, whose factors were here
+        if (!STATES && qw == 0 && lane < 16) o_into[ph][16 * grp + lane] = a.scale * gates[G_INTO + 16 * grp + lane];
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&r_ready);
@@ -778,13 +783,9 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
     bool ok = true;
     for (int j = 0; !STATES && j < nch; ++j) {
       const uint32_t ph = (uint32_t)j & 1u, D = tb + lanes + T_XQ + ph * 128u;
-      // e^G of the chunk, kept past its stage (which is full: s_ready of this chunk
-      // waits for nothing of ours, and the next load into it for its own state)
-      ok = ok && wait_full(j);
-      if (tid < CH) o_into[ph][tid] = a.scale * lds_f1(sb + stage(j) + L_::GT + 4u * (G_INTO + tid));
       ok = ok && mbar_wait(&pu_full[ph], (uint32_t)(j >> 1) & 1u, WAIT_CYCLES);
       tc_fence_after();
-      // the factors are there, the last tile has been read; everyone hears of a wait that ran out
+      // the last tile has been read; everyone hears of a wait that ran out
       if (named_bar_any(1, 128, !ok)) {
         ok = false;
         break;
@@ -904,6 +905,7 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
     fence_mbar_init();
   }
   follow_wait();
+  fence_async_all();  // what the kernel before wrote with plain stores is read by copies here
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1330,6 +1332,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
     fence_mbar_init();
   }
   follow_wait();
+  fence_async_all();  // what the kernel before wrote with plain stores is read by copies here
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1815,12 +1818,21 @@ cudaError_t make_maps(const Call &c, const void *dO, Maps &m) {
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
 // `follow`: the kernel begins while the last one ends, and waits for it (follow_wait).
-template <typename K, typename M, typename A>
-cudaError_t launch(K kernel, int64_t blocks, int threads, uint32_t smem, const Call &c, const M &maps, const A &a,
+template <auto kernel, typename M, typename A>
+cudaError_t launch(int64_t blocks, int threads, uint32_t smem, const Call &c, const M &maps, const A &a,
                    const char *label, bool follow) {
   if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // shared memory is asked for once per kernel and device (the answer is the same for every call)
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_release);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(threads);
@@ -1847,7 +1859,7 @@ cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
   a.tiles = ws + l.tiles;
   a.gates = (float *)(ws + l.gates);
   a.err = c.p.err;
-  return launch(delta_prep_kernel, c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep", false);
+  return launch<delta_prep_kernel>(c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep", false);
 }
 ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   ChainArgs a;
@@ -1877,7 +1889,7 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
   ChainArgs a = chain_args(c, ws, l);
   a.o = (__nv_bfloat16 *)o;
   a.ht = ht;
-  return launch(delta_chain_kernel, c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
+  return launch<delta_chain_kernel>(c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
                 ChainMaps{m.q, m.k, m.v}, a, "delta_chain", true);
 }
 
@@ -1907,7 +1919,7 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   b.r_images = ws + l.r;
   b.err = a.err;
   const int64_t units = c.docs.n * c.p.H;
-  e = launch(delta_walks_kernel, 2 * units, CHAIN_THREADS, std::max(ChainSmem<true>::BYTES, BackSmem::BYTES), c,
+  e = launch<delta_walks_kernel>(2 * units, CHAIN_THREADS, std::max(ChainSmem<true>::BYTES, BackSmem::BYTES), c,
              WalkMaps{{m.q, m.k, m.v}, {m.q, m.k, m.dO}}, WalkArgs{a, b, units}, "delta_walks", true);
   if (e != cudaSuccess) return e;
   GradArgs g;
@@ -1929,9 +1941,9 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   g.err = a.err;
   g.units = c.slots * c.p.H;
   const int64_t blocks = std::min(g.units, tc::sm_count());
-  return per_head ? launch(delta_grads_kernel<true>, blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
+  return per_head ? launch<delta_grads_kernel<true>>(blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
                            "delta_grads", true)
-                  : launch(delta_grads_kernel<false>, blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
+                  : launch<delta_grads_kernel<false>>(blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
                            "delta_grads", true);
 }
 

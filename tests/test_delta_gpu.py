@@ -405,3 +405,39 @@ def test_no_tokens_and_refusals(cuda_ok):
     p.chunk_size = 32
     assert glc.load().delta_fwd(ctypes.byref(p), glc._ptr(g), glc._ptr(v), None, None) == glc.ERR_UNSUPPORTED
     del keep
+
+
+@pytest.mark.parametrize("B,T,H,Hqk,V,docs", [(4, 2048, 16, 16, 128, 1), (1, 8192, 16, 8, 128, 9), (2, 3001, 16, 4, 64, 5)])
+def test_many_chunks_against_the_other_kernels(cuda_ok, B, T, H, Hqk, V, docs):
+    """Dozens of chunks on every SM at once: the tensor-core kernels, ten times the same bits, against the token by
+    token ones (which take operands at odd addresses).  Both are within half an ulp and TOL of the same values."""
+    gen = torch.Generator("cuda")
+    gen.manual_seed(B + T)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    norm = torch.nn.functional.normalize
+    q, k = (norm(r(B, T, Hqk, 128), dim=-1).to(BF) for _ in range(2))
+    v, do, g, b = r(B, T, H, V).to(BF), r(B, T, H, V).to(BF), -r(B, T, H).abs() / 8, r(B, T, H).sigmoid()
+    seg = None
+    if docs > 1:
+        seg = torch.zeros(B, T, dtype=torch.int32, device="cuda")
+        for i in range(B):
+            seg[i, torch.randperm(T - 1, generator=gen, device="cuda")[:docs - 1] + 1] = 1
+        seg = seg.cumsum(1).to(torch.int32)
+
+    def odd(t):
+        x = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        return x.copy_(t)
+
+    def call(q):
+        o, ht = glc.delta_fwd(q, k, v, g, b, segment_ids=seg, output_final_state=True, n_seqs=B * docs, poison=True)
+        return (o, ht, *glc.delta_bwd(q, k, v, g, b, do, segment_ids=seg, n_seqs=B * docs, poison=True)[:5])
+
+    want = call(odd(q))
+    first = call(q)
+    for _ in range(9):
+        assert all(torch.equal(x, y) for x, y in zip(first, call(q)))
+    for name, x, y in zip(("o", "ht", *NAMES), first, want):
+        x, y = x.double(), y.double()
+        bound = 2 * (4 if name == "dg" else 1) * TOL * y.abs().max() + (2 * ULP[BF] * y.abs() if first[0].dtype == BF else 0)
+        assert bool(((x - y).abs() <= bound).all()), (name, float((x - y).abs().max()), float(y.abs().max()))
+    glc.get_device_error()
