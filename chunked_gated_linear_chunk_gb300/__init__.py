@@ -592,17 +592,15 @@ class _DeltaProblem:
         self.fields = (B, T, H, Hqk, K, V, _dtype_code(q), 0, K ** -0.5 if scale is None else scale, 0, q.data_ptr(),
                        k.data_ptr(), v.data_ptr(), g.data_ptr(), _addr(seg) or 0, n, _addr(h0) or 0), (qs, ks, vs)
 
-    def pack(self, ws=0, size=0):
-        return _PACK.pack(*self.fields[0], ws, size, *self.fields[1])
-
-    def scratch(self, kind, workspace):
+    def scratch(self, need_of, workspace):
         """(workspace or None, the problem's bytes with it)."""
-        p = self.pack()
-        need = getattr(_lib or load(), kind)(p)
+        first, strides = self.fields
+        p = _PACK.pack(*first, 0, 0, *strides)
+        need = need_of(p)
         if not need:
             return None, p
         ws = _scratch(need, self.device, workspace)
-        return ws, self.pack(ws.data_ptr(), ws.numel())
+        return ws, _PACK.pack(*first, ws.data_ptr(), ws.numel(), *strides)
 
 
 def delta_fwd(q, k, v, g, beta, scale=None, segment_ids=None, initial_state=None, output_final_state=False,
@@ -619,8 +617,9 @@ def delta_fwd(q, k, v, g, beta, scale=None, segment_ids=None, initial_state=None
     if output_final_state:
         ht = (_given(final_out, "final_out", p.states, torch.float32, dev) if final_out is not None
               else _new(p.states, torch.float32, dev, poison))
-    ws, packed = p.scratch("delta_fwd_workspace_size", workspace)
-    st = _call((_lib or load()).delta_fwd, p.q, packed, p.beta.data_ptr(), o.data_ptr(), _addr(ht))
+    lib = _lib or load()
+    ws, packed = p.scratch(lib.delta_fwd_workspace_size, workspace)
+    st = _call(lib.delta_fwd, p.q, packed, p.beta.data_ptr(), o.data_ptr(), _addr(ht))
     if st:
         _check(st, "delta_fwd")
     return o, ht
@@ -649,8 +648,9 @@ def delta_bwd(q, k, v, g, beta, do, scale=None, segment_ids=None, initial_state=
     else:
         dq, dk, dv, dg, dbeta = (_new(tuple(x.shape), x.dtype, dev, poison) for x in like)
         dh0 = _new(p.states, torch.float32, dev, poison) if initial_state is not None else None
-    ws, packed = p.scratch("delta_bwd_workspace_size", workspace)
-    st = _call((_lib or load()).delta_bwd, p.q, packed, p.beta.data_ptr(), do.data_ptr(), _addr(dht), dq.data_ptr(),
+    lib = _lib or load()
+    ws, packed = p.scratch(lib.delta_bwd_workspace_size, workspace)
+    st = _call(lib.delta_bwd, p.q, packed, p.beta.data_ptr(), do.data_ptr(), _addr(dht), dq.data_ptr(),
                dk.data_ptr(), dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _addr(dh0))
     if st:
         _check(st, "delta_bwd")
@@ -666,6 +666,7 @@ def delta_step(q, k, v, g, beta, state, state_indices=None, scale=None, out=None
 # ---- operations around the recurrence ---------------------------------------
 # glacore_qk_norm as bytes (see _PACK)
 _QK_PACK = struct.Struct("@6q3if8P3qPN")
+_WS_PACK = struct.Struct("@PN")  # its last two fields
 assert _QK_PACK.size == ctypes.sizeof(QkNorm)
 
 
@@ -698,12 +699,10 @@ def _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved):
         if t is not None and t.get_device() != dev:
             _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, positions=positions)
 
-    def pack(ws=0, size=0):
-        return _QK_PACK.pack(B, T, Hq, k.shape[2], D, R, _dtype_code(q), int(norm == "l2"), int(bool(interleaved)), eps,
-                             0, q.data_ptr(), k.data_ptr(), _addr(wq) or 0, _addr(wk) or 0, _addr(cos) or 0,
-                             _addr(sin) or 0, _addr(positions) or 0, P, qs, ks, ws, size)
-
-    return q, k, pack, (wq, wk, cos, sin, positions)
+    p = _QK_PACK.pack(B, T, Hq, k.shape[2], D, R, _dtype_code(q), int(norm == "l2"), int(bool(interleaved)), eps, 0,
+                      q.data_ptr(), k.data_ptr(), _addr(wq) or 0, _addr(wk) or 0, _addr(cos) or 0, _addr(sin) or 0,
+                      _addr(positions) or 0, P, qs, ks, 0, 0)
+    return q, k, p, (wq, wk, cos, sin, positions)
 
 
 def qk_norm_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, eps=1e-6, norm="rms", interleaved=False,
@@ -715,13 +714,13 @@ def qk_norm_fwd(q, k, wq=None, wk=None, cos=None, sin=None, positions=None, eps=
     [n_positions, R] fp32 hold at the token's position.  q [B,T,Hq,D], k
     [B,T,Hk,D] (bf16 or fp32; views of one projection go in place), wq, wk [D]
     fp32 or None, positions [B,T] int32 or None (0 .. T - 1).  Returns (q, k)."""
-    q, k, pack, keep = _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved)
+    q, k, p, keep = _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved)
     dt, dev = q.dtype, q.device
     if outs is not None:
         qo, ko = _given(outs[0], "q out", q.shape, dt, dev), _given(outs[1], "k out", k.shape, dt, dev)
     else:
         qo, ko = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
-    st = _call((_lib or load()).qk_norm_fwd, q, pack(), qo.data_ptr(), ko.data_ptr())
+    st = _call((_lib or load()).qk_norm_fwd, q, p, qo.data_ptr(), ko.data_ptr())
     if st:
         _check(st, "qk_norm_fwd")
     return qo, ko
@@ -731,12 +730,13 @@ def qk_norm_bwd(q, k, dqo, dko, wq=None, wk=None, cos=None, sin=None, positions=
                 interleaved=False, outs=None, workspace=None):
     """Gradients of qk_norm_fwd from those of its outputs: (dq, dk, dwq, dwk),
     the last two [D] fp32 (also without weights)."""
-    q, k, pack, keep = _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved)
+    q, k, p, keep = _qk_args(q, k, wq, wk, cos, sin, positions, eps, norm, interleaved)
     dt, dev = q.dtype, q.device
     if dqo.shape != q.shape or dko.shape != k.shape:
         raise ValueError("qk_norm: dqo and dko must match q and k")
     dqo, dko = _contig(dqo, dt), _contig(dko, dt)
-    _same_device(dev, dqo=dqo, dko=dko)
+    if not dqo.get_device() == dko.get_device() == q.get_device():
+        _same_device(dev, dqo=dqo, dko=dko)
     D = q.shape[3]
     if outs is not None:
         dq, dk, dwq, dwk = outs
@@ -747,8 +747,9 @@ def qk_norm_bwd(q, k, dqo, dko, wq=None, wk=None, cos=None, sin=None, positions=
         dq, dk = torch.empty(q.shape, dtype=dt, device=dev), torch.empty(k.shape, dtype=dt, device=dev)
         dwq, dwk = (torch.empty(D, dtype=torch.float32, device=dev) for _ in range(2))
     lib = _lib or load()
-    ws = _scratch(lib.qk_norm_bwd_workspace_size(pack()), dev, workspace)
-    st = _call(lib.qk_norm_bwd, q, pack(ws.data_ptr(), ws.numel()), dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(),
+    ws = _scratch(lib.qk_norm_bwd_workspace_size(p), dev, workspace)
+    p = p[:-16] + _WS_PACK.pack(ws.data_ptr(), ws.numel())
+    st = _call(lib.qk_norm_bwd, q, p, dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(),
                dk.data_ptr(), dwq.data_ptr(), dwk.data_ptr())
     if st:
         _check(st, "qk_norm_bwd")

@@ -40,7 +40,7 @@ Layout layout(const glacore_problem *p, bool backward) {
   L.slots = p->segment_ids ? std::min(BT, BT / C + n) : p->B * ((p->T + C - 1) / C);
   L.on_tc = tc_supported(p) && L.slots * p->H < ((int64_t)1 << 30) && n * p->H < ((int64_t)1 << 30);  // units in 32 bits
   // the scratch of one call serves either family: the addresses of the outputs decide (run_fwd, run_bwd)
-  if (L.on_tc) take(L.tc, tc_workspace(L.slots, p->H, backward));
+  if (L.on_tc) take(L.tc, tc_workspace(n, L.slots, p->H, backward));
   if (backward) {
     if (L.on_tc) off = L.tc;
     const size_t states = sizeof(float) * (size_t)L.slots * p->H * p->K * p->V;
@@ -49,7 +49,7 @@ Layout layout(const glacore_problem *p, bool backward) {
     take(L.ds1, states);
     take(L.e, rows);
     take(L.dr, rows);
-    if (L.on_tc) off = std::max(off, L.tc + align256(tc_workspace(L.slots, p->H, true)));
+    if (L.on_tc) off = std::max(off, L.tc + align256(tc_workspace(n, L.slots, p->H, true)));
     if (p->Hqk != p->H) {
       take(L.dq, sizeof(float) * (size_t)BT * p->H * p->K);
       take(L.dk, sizeof(float) * (size_t)BT * p->H * p->K);

@@ -81,7 +81,7 @@ cudaError_t reduce_heads(const Call &c, const float *x, void *out);
 
 // ---- tensor-core kernels (delta_tc.cu): bf16, K and V multiples of 8 up to 128 ----
 bool tc_supported(const glacore_problem *p);  // sizes, strides and addresses of q, k, v
-size_t tc_workspace(int64_t slots, int64_t H, bool backward);
+size_t tc_workspace(int64_t docs, int64_t slots, int64_t H, bool backward);
 cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws);
 // dq and dk as in simt_grads
 cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, void *dk, bool per_head, void *dv, float *dg,

@@ -416,6 +416,7 @@ struct ChainMaps {
 };
 struct ChainArgs {
   Docs docs;
+  const int32_t *order;  // documents, longest first, or null
   int H, share, K, V;
   float scale;
   const float *h0;
@@ -488,8 +489,9 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = (int)(unit % a.H);
-  const int64_t d = unit / a.H;
+  const int h = (int)((uint32_t)unit % (uint32_t)a.H);
+  const uint32_t rank = (uint32_t)unit / (uint32_t)a.H;
+  const int64_t d = a.order ? a.order[rank] : (int64_t)rank;
   int64_t s0, s1;
   a.docs.range(d, s0, s1);
   const int nch = (int)((s1 - s0 + CH - 1) / CH);
@@ -856,6 +858,7 @@ struct BackMaps {
 };
 struct BackArgs {
   Docs docs;
+  const int32_t *order;
   int H, share, K, V;
   float scale;
   const float *dht;
@@ -882,8 +885,9 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = (int)(unit % a.H);
-  const int64_t d = unit / a.H;
+  const int h = (int)((uint32_t)unit % (uint32_t)a.H);
+  const uint32_t rank = (uint32_t)unit / (uint32_t)a.H;
+  const int64_t d = a.order ? a.order[rank] : (int64_t)rank;
   int64_t s0, s1;
   a.docs.range(d, s0, s1);
   const int nch = (int)((s1 - s0 + CH - 1) / CH);
@@ -1783,12 +1787,12 @@ bool tc_supported(const glacore_problem *p) {
 // Scratch (byte offsets): tiles and gates of every chunk and head, the backward's images.
 namespace {
 struct TcLayout {
-  size_t tiles, gates, s, ds, e, r, total;
+  size_t order, tiles, gates, s, ds, e, r, total;
 };
-TcLayout tc_layout(int64_t slots, int64_t H, bool backward) {
+TcLayout tc_layout(int64_t docs, int64_t slots, int64_t H, bool backward) {
   TcLayout l;
   memset(&l, 0, sizeof(l));
-  size_t off = 0;
+  size_t off = al256((size_t)docs * sizeof(int32_t));
   auto take = [&](size_t &at, size_t each) {
     at = off;
     off = al256(off + (size_t)slots * H * each);
@@ -1861,6 +1865,16 @@ cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
   a.err = c.p.err;
   return launch<delta_prep_kernel>(c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep", false);
 }
+// Packed documents that do not all run at once: the longest first, so that none
+// of them is begun when the others are done.
+cudaError_t launch_order(const Call &c, int64_t blocks, char *ws, const int32_t *&order) {
+  if (!c.docs.start || blocks <= tc::sm_count()) return cudaSuccess;
+  Units u;
+  memset(&u, 0, sizeof(u));
+  u.docs = c.docs;
+  order = (const int32_t *)ws;
+  return tc::launch_order_units(u, c.docs.n, (int32_t *)ws, c.st);
+}
 ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   ChainArgs a;
   memset(&a, 0, sizeof(a));
@@ -1878,15 +1892,20 @@ ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
 }
 }  // namespace
 
-size_t tc_workspace(int64_t slots, int64_t H, bool backward) { return tc_layout(slots, H, backward).total; }
+size_t tc_workspace(int64_t docs, int64_t slots, int64_t H, bool backward) {
+  return tc_layout(docs, slots, H, backward).total;
+}
 
 cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
-  const TcLayout l = tc_layout(c.slots, c.p.H, false);
+  const TcLayout l = tc_layout(c.docs.n, c.slots, c.p.H, false);
   Maps m;
+  const int32_t *order = nullptr;
   cudaError_t e = make_maps(c, nullptr, m);
+  if (e == cudaSuccess) e = launch_order(c, c.docs.n * c.p.H, ws + l.order, order);
   if (e == cudaSuccess) e = prep(c, m, ws, l);
   if (e != cudaSuccess) return e;
   ChainArgs a = chain_args(c, ws, l);
+  a.order = order;
   a.o = (__nv_bfloat16 *)o;
   a.ht = ht;
   return launch<delta_chain_kernel>(c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
@@ -1895,16 +1914,20 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
 
 cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, void *dk, bool per_head, void *dv, float *dg,
                    float *dbeta, float *dh0, char *ws) {
-  const TcLayout l = tc_layout(c.slots, c.p.H, true);
+  const TcLayout l = tc_layout(c.docs.n, c.slots, c.p.H, true);
   Maps m;
+  const int32_t *order = nullptr;
   cudaError_t e = make_maps(c, dO, m);
+  if (e == cudaSuccess) e = launch_order(c, 2 * c.docs.n * c.p.H, ws + l.order, order);
   if (e == cudaSuccess) e = prep(c, m, ws, l);
   if (e != cudaSuccess) return e;
   ChainArgs a = chain_args(c, ws, l);
+  a.order = order;
   a.s_images = ws + l.s;
   a.e_images = ws + l.e;
   BackArgs b;
   b.docs = a.docs;
+  b.order = order;
   b.H = a.H;
   b.share = a.share;
   b.K = a.K;
