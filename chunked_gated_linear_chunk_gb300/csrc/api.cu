@@ -648,7 +648,7 @@ const char *glacore_status_string(glacore_status s) {
   return "unknown status";
 }
 
-int glacore_version(void) { return 300; }
+int glacore_version(void) { return 400; }
 
 void glacore_set_timing_events(void *events, int n_events) {
   t_events = (cudaEvent_t *)events;

@@ -1500,9 +1500,9 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       }
       if (L < CH) {  // rows past the end hold other tokens: as zeros, nothing in them reaches a sum
         ok = ok && mbar_wait(&full_a, ph, WAIT_CYCLES);
-        for (int n = tid; n < (CH - L) * 4 * 8; n += 32 * GRAD_WARPS) {
-          const int c = n % 8, x = n / 8 % 4, r = L + n / 32;
-          st_shared_v4(sb + L_::QK + x * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
+        for (int n = tid; n < (CH - L) * 8 * 8; n += 32 * GRAD_WARPS) {  // q, k (four tiles), dO (twice two)
+          const int c = n % 8, x = n / 8 % 8, r = L + n / 64;
+          st_shared_v4(sb + (x < 4 ? L_::QK + x * 8192u : L_::X1 + (x - 4) * 16384u) + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
         }
         fence_async_smem();
       }
