@@ -7,11 +7,11 @@
 // two bf16 parts, x = hi + lo to 2^-17 of x, and a product of two such matrices
 // as hi hi + hi lo + lo hi; sums and the state itself are fp32.  With one part
 // the outputs are off by 3e-3, twice what rounding them to bf16 costs,
-// with two by 5e-6.  Where Z's rows are long (sum of |Z_ts| b_s above WIDE: keys
-// that nearly coincide, written with b near 2), Y + Z (b Y) cancels and what Z
-// and b Y are off by counts that much more: in such a chunk that product takes
-// both in three parts (exact to 2^-25).  Chunks of unit keys that differ and b up to 1
-// stay below 10.
+// with two by 5e-6.  Where Z's rows are long (sum of |Z_ts| b_s above WIDE in a
+// quarter of a row: keys that nearly coincide, written with b near 2), Y + Z (b Y)
+// cancels and what Z and b Y are off by counts that much more: in such a chunk
+// that product takes both in three parts (exact to 2^-25).  Chunks of unit keys that
+// differ and b up to 1 stay below 3.
 //
 // delta_prep_kernel makes of every chunk by itself what the recurrence over
 // chunks needs: Z and P (two 64 x 64 tiles each, laid out as the matrix
@@ -39,7 +39,7 @@ constexpr uint32_t TILES = 5 * TILE;            // Z hi, Z lo, P hi, P lo; of a 
 constexpr int GATES = 256;                      // floats of a chunk's gate slot:
 constexpr int G_INTO = 0, G_OUT = 64, G_BETA = 128, G_OVER = 192;  // e^G, e^{G_C - G}, b, e^{G_C}
 constexpr int G_WIDE = 193;                     // 1: Z (b Y) is to be taken in three parts
-constexpr float WIDE = 16.f;
+constexpr float WIDE = 4.f;
 constexpr int NP = 68;                          // row pitch of the fp32 64 x 64 matrices
 
 // hi and lo parts of two neighbours, packed.  What hi leaves is a product with
@@ -119,40 +119,60 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
                : "memory");
 }
 
-// ROWS rows of a column of the block below a pair of diagonal ones (rows and
-// columns r .. r + M - 1 and r + M .. r + 2 M - 1): W, a barrier, then Z21.
-template <int M, int ROWS, typename B>
+// ROWS rows of COLS columns of the block below a pair of diagonal ones (rows
+// and columns r .. r + M - 1 and r + M .. r + 2 M - 1): W, a barrier, then Z21.
+// Bound by shared-memory reads: a row's four entries serve all columns, a
+// column pair's entry all rows.
+template <int M, int ROWS, int COLS, typename B>
 __device__ __forceinline__ void below(PrepSmem &s, float *W, int r, int j, int i0, B barrier) {
-  float w[ROWS];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) w[i] = -s.N[r + M + i0 + i][r + j];
-#pragma unroll
-  for (int c = 0; c < M; c += 4) {
-    const float4 b = *reinterpret_cast<const float4 *>(&s.beta[r + c]);
-    const float z[4] = {b.x * s.N[r + c][r + j], b.y * s.N[r + c + 1][r + j], b.z * s.N[r + c + 2][r + j],
-                        b.w * s.N[r + c + 3][r + j]};
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + M + i0 + i][r + c]);
-      w[i] = fmaf(-n.x, z[0], fmaf(-n.y, z[1], fmaf(-n.z, z[2], fmaf(-n.w, z[3], w[i]))));
+  auto pair = [](const float *p, float (&v)[COLS]) {
+    if (COLS == 2) {
+      const float2 x = *reinterpret_cast<const float2 *>(p);
+      v[0] = x.x;
+      v[COLS - 1] = x.y;
+    } else {
+      v[0] = *p;
     }
-  }
+  };
+  float w[ROWS][COLS];
+  auto product = [&](const float *left, const float *right, int pitch, const float *beta, float sign) {
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) W[(i0 + i) * WPITCH + j] = w[i];
+    for (int c = 0; c < M; c += 4) {
+      const float4 b4 = *reinterpret_cast<const float4 *>(beta + c);
+      const float b[4] = {b4.x, b4.y, b4.z, b4.w};
+      float z[4][COLS];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        pair(right + (c + x) * pitch, z[x]);
+#pragma unroll
+        for (int y = 0; y < COLS; ++y) z[x][y] *= sign * b[x];
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const float4 n = *reinterpret_cast<const float4 *>(left + i * NP + c);
+#pragma unroll
+        for (int y = 0; y < COLS; ++y)
+          w[i][y] = fmaf(n.x, z[0][y], fmaf(n.y, z[1][y], fmaf(n.z, z[2][y], fmaf(n.w, z[3][y], w[i][y]))));
+      }
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    pair(&s.N[r + M + i0 + i][r + j], w[i]);
+#pragma unroll
+    for (int y = 0; y < COLS; ++y) w[i][y] = -w[i][y];
+  }
+  product(&s.N[r + M + i0][r], &s.N[r][r + j], NP, &s.beta[r], -1.f);
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+    for (int y = 0; y < COLS; ++y) W[(i0 + i) * WPITCH + j + y] = w[i][y];
   barrier();
+  product(&s.N[r + M + i0][r + M], W + j, WPITCH, &s.beta[r + M], 1.f);
 #pragma unroll
-  for (int c = 0; c < M; c += 4) {
-    const float4 b = *reinterpret_cast<const float4 *>(&s.beta[r + M + c]);
-    const float z[4] = {b.x * W[c * WPITCH + j], b.y * W[(c + 1) * WPITCH + j], b.z * W[(c + 2) * WPITCH + j],
-                        b.w * W[(c + 3) * WPITCH + j]};
+  for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const float4 n = *reinterpret_cast<const float4 *>(&s.N[r + M + i0 + i][r + M + c]);
-      w[i] = fmaf(n.x, z[0], fmaf(n.y, z[1], fmaf(n.z, z[2], fmaf(n.w, z[3], w[i]))));
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) s.N[r + M + i0 + i][r + j] = w[i];
+    for (int y = 0; y < COLS; ++y) s.N[r + M + i0 + i][r + j + y] = w[i][y];
 }
 
 __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __grid_constant__ PrepMaps maps,
@@ -313,12 +333,13 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
       }
       __syncthreads();
       // the block below each pair of them, then the one below both
-      below<16, 2>(s, W + half * 16 * WPITCH, half * 32, lane & 15, 4 * (warp & 3) + 2 * (lane >> 4),
-                   [&] { named_bar(2 + half, 128); });
+      if ((warp & 3) < 2)
+        below<16, 2, 2>(s, W + half * 16 * WPITCH, half * 32, 2 * (lane & 7), 8 * (warp & 1) + 2 * (lane >> 3),
+                        [&] { named_bar(2 + half, 64); });
       __syncthreads();
-      below<32, 4>(s, W, 0, lane, 4 * warp, [] { __syncthreads(); });
+      if (warp < 4) below<32, 4, 2>(s, W, 0, 2 * (lane & 15), 8 * warp + 4 * (lane >> 4), [] { named_bar(1, 128); });
       __syncthreads();
-      const int zr = tid >> 2, z0 = (tid & 3) * 16;
+      const int zr = tid & 63, z0 = (tid >> 6) * 16;
       float sum = 0.f;
       uint32_t third[8];
 #pragma unroll
@@ -328,7 +349,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
         *reinterpret_cast<float4 *>(z) = *reinterpret_cast<const float4 *>(&s.N[zr][z0 + n]);
         *reinterpret_cast<float4 *>(z + 4) = *reinterpret_cast<const float4 *>(&s.N[zr][z0 + n + 4]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(fabsf(z[i]), fabsf(s.beta[z0 + n + i]), sum);
+        for (int i = 0; i < 8; ++i) sum = fmaf(fabsf(z[i]), fabsf(s.beta[z0 + n + i]), sum);  // a quarter of the row
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           split2(z[2 * i], z[2 * i + 1], hi[i], lo[i]);
@@ -338,8 +359,6 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
         st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       const bool wide = __syncthreads_or(!(sum <= WIDE));
       if (wide) {  // the third part takes Z's place
 #pragma unroll
