@@ -16,7 +16,8 @@
 // delta_prep_kernel makes of every chunk by itself what the recurrence over
 // chunks needs: Z and P (two 64 x 64 tiles each, laid out as the matrix
 // operands that they become) and the chunk's decays.  delta_chain_kernel walks
-// the chunks of one (document, head) with the state on chip.
+// the chunks of one (document, head) with the state on chip; delta_overlap_kernel
+// does both at once where few sequences leave SMs over.
 #include <string.h>
 
 #include <algorithm>
@@ -119,6 +120,17 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8]) {
                : "memory");
 }
 
+// A flag per chunk and head, for blocks of the same kernel.
+constexpr uint32_t READY = 1, READY_WIDE = 3;
+__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_relaxed(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // ROWS rows of COLS columns of the block below a pair of diagonal ones (rows
 // and columns r .. r + M - 1 and r + M .. r + 2 M - 1): W, a barrier, then Z21.
 // Bound by shared-memory reads: a row's four entries serve all columns, a
@@ -175,47 +187,44 @@ __device__ __forceinline__ void below(PrepSmem &s, float *W, int r, int j, int i
     for (int y = 0; y < COLS; ++y) s.N[r + M + i0 + i][r + j + y] = w[i][y];
 }
 
-__global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __grid_constant__ PrepMaps maps,
-                                                                     const PrepArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);  // [q; k] tiles, then Z and P
+// What a team of PREP_THREADS threads works with: its shared memory, barriers
+// `bar` .. `bar` + 3 of the block, 64 columns of tensor memory.
+struct PrepTeam {
+  uint8_t *sm;  // [q; k] tiles, then Z and P; behind them PrepSmem
+  uint64_t *full, *done;
+  uint32_t *tmem;
+  double *warp0_total;
+  int tid, bar;
+};
+__device__ __forceinline__ void prep_load(const PrepMaps &maps, const PrepTeam &w, int hq, int64_t tok) {
+  mbar_expect_tx(w.full, 32768);
+#pragma unroll
+  for (int cb = 0; cb < 2; ++cb) {  // 64 channels: 64 rows of q, then 64 of k
+    tma_load_3d(w.sm + cb * 16384, &maps.q, cb * 64, hq, (int)tok, w.full);
+    tma_load_3d(w.sm + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, w.full);
+  }
+}
+// The chunk in `slot`, whose tiles prep_load has asked for; `phase` of the
+// barriers.  `flags`: told of each head when its results are in memory.
+template <bool FLAGS>
+__device__ __forceinline__ bool prep_chunk(const PrepArgs &a, const PrepTeam &w, int64_t slot, int h0, int heads, int64_t tok,
+                                           int L, uint32_t phase, uint32_t *flags) {
+  uint8_t *sm = w.sm;
   PrepSmem &s = *reinterpret_cast<PrepSmem *>(sm + 32768);
   float *W = reinterpret_cast<float *>(sm);
-  __shared__ uint64_t full, done;
-  __shared__ uint32_t tmem_base;
-  __shared__ double warp0_total;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int hq = (int)(blockIdx.x % a.Hqk);
-  const int64_t slot = blockIdx.x / a.Hqk;
-  int64_t tok;
-  int L;
-  if (!chunk_in_slot(a.docs, slot, tok, L)) return;
-  if (tid == 0) {
-    mbar_init(&full, 1);
-    mbar_init(&done, 1);
-    fence_mbar_init();
-    mbar_expect_tx(&full, 32768);
-#pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {  // 64 channels: 64 rows of q, then 64 of k
-      tma_load_3d(sm + cb * 16384, &maps.q, cb * 64, hq, (int)tok, &full);
-      tma_load_3d(sm + cb * 16384 + 8192, &maps.k, cb * 64, hq, (int)tok, &full);
-    }
-  }
-  if (warp == 1) {
-    tmem_alloc(&tmem_base, 64);
-    tmem_relinquish();
-  }
+  const int tid = w.tid, warp = tid >> 5, lane = tid & 31;
+  auto team = [&] { named_bar(w.bar, PREP_THREADS); };
   // gates of head e of the group, loaded a head ahead; then their prefix sums
   float g_next = 0.f, b_next = 0.f;
   auto fetch = [&](int e) {
     g_next = b_next = 0.f;
-    if (tid < L && tid < CH && e < a.share) {
-      const int64_t at = (tok + tid) * a.H + hq * a.share + e;
+    if (tid < L && tid < CH && e < heads) {
+      const int64_t at = (tok + tid) * a.H + h0 + e;
       g_next = a.g[at];
       b_next = a.beta[at];
     }
   };
-  auto scan = [&]() {  // begins and ends with a barrier of the block
+  auto scan = [&]() {  // begins and ends with a barrier of the team
     double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;  // e^g of less is 0 as well
     const float b = b_next;
     if (tid < CH) {
@@ -224,48 +233,58 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
         const double y = __shfl_up_sync(0xffffffffu, G, o);
         if (lane >= o) G += y;
       }
-      if (tid == 31) warp0_total = G;
+      if (tid == 31) *w.warp0_total = G;
     }
-    __syncthreads();
+    team();
     if (tid < CH) {
-      if (warp == 1) G += warp0_total;
+      if (warp == 1) G += *w.warp0_total;
       const float gh = (float)G;
       s.G[tid] = make_float2(gh, (float)(G - (double)gh));
       s.beta[tid] = b;
     }
-    __syncthreads();
+    team();
   };
   fetch(0);
   tc_fence_before();
   scan();
   tc_fence_after();
-  const uint32_t tb = tmem_base;
+  const uint32_t tb = *w.tmem;
   fetch(1);
   bool ok = true;
   if (tid == 0) {
-    ok = mbar_wait(&full, 0, WAIT_CYCLES);
+    ok = mbar_wait(w.full, phase, WAIT_CYCLES);
     const uint32_t base = smem_u32(sm);
     if (ok) {
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks)
         mma_bf16(tb, kdesc(base, ks, 128), kdesc(base + 8192, ks, 128), idesc_bf16(128, 64, false, false), ks);
     }
-    mma_commit(&done);
+    mma_commit(w.done);
   }
   __syncwarp();
-  ok = mbar_wait(&done, 0, WAIT_CYCLES) && ok;
-  ok = !__syncthreads_or(!ok);
+  ok = mbar_wait(w.done, phase, WAIT_CYCLES) && ok;
+  ok = !named_bar_any(w.bar, PREP_THREADS, !ok);
+  uint32_t kind = 0;  // thread 0: of the last head
+  auto publish = [&](int64_t sh) {
+    bulk_wait_all();
+    fence_async_all();
+    st_release(flags + sh, kind);
+  };
   if (ok) {
     tc_fence_after();
     // thread (row of the stack, half of the columns): rows < 64 of Q K^T, the others of K K^T
     const int row = (warp & 3) * 32 + lane, t = row & 63, half = warp >> 2;
     const bool isP = (warp & 3) < 2;
     const uint32_t at = tb + ((uint32_t)((warp & 3) * 32) << 16);
-    for (int e = 0; e < a.share; ++e) {
-      const int h = hq * a.share + e;
-      const int64_t sh = slot * a.H + h;
+    for (int e = 0; e < heads; ++e) {
+      const int64_t sh = slot * a.H + h0 + e;
       if (e) {
-        if (tid == 0) bulk_wait_read_all();  // the tiles of the last head have left shared memory
+        if (tid == 0) {  // the tiles of the last head have left shared memory
+          if (FLAGS)
+            publish(sh - 1);
+          else
+            bulk_wait_read_all();
+        }
         scan();
         fetch(e + 1);
       }
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
         }
       }
       if (!isP) {
-        named_bar(1, 128);
+        named_bar(w.bar + 1, 128);
         if (half == 0) {  // Z of the four diagonal blocks, two by a warp, a column by a thread, in N's place
           const int r = (warp - 2) * 32 + (lane & 16), j = lane & 15;
           float zb[16];
@@ -331,14 +350,14 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
           }
         }
       }
-      __syncthreads();
+      team();
       // the block below each pair of them, then the one below both
       if ((warp & 3) < 2)
         below<16, 2, 2>(s, W + half * 16 * WPITCH, half * 32, 2 * (lane & 7), 8 * (warp & 1) + 2 * (lane >> 3),
-                        [&] { named_bar(2 + half, 64); });
-      __syncthreads();
-      if (warp < 4) below<32, 4, 2>(s, W, 0, 2 * (lane & 15), 8 * warp + 4 * (lane >> 4), [] { named_bar(1, 128); });
-      __syncthreads();
+                        [&] { named_bar(w.bar + 2 + half, 64); });
+      team();
+      if (warp < 4) below<32, 4, 2>(s, W, 0, 2 * (lane & 15), 8 * warp + 4 * (lane >> 4), [&] { named_bar(w.bar + 1, 128); });
+      team();
       const int zr = tid & 63, z0 = (tid >> 6) * 16;
       float sum = 0.f;
       uint32_t third[8];
@@ -359,7 +378,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
         st_shared_v4(o, hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(o + TILE, lo[0], lo[1], lo[2], lo[3]);
       }
-      const bool wide = __syncthreads_or(!(sum <= WIDE));
+      const bool wide = named_bar_any(w.bar, PREP_THREADS, !(sum <= WIDE));
       if (wide) {  // the third part takes Z's place
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -367,25 +386,58 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
                        third[4 * i + 2], third[4 * i + 3]);
       }
       fence_async_smem();
-      __syncthreads();
+      team();
       if (tid == 0) {
         a.gates[sh * GATES + G_WIDE] = wide ? 1.f : 0.f;
+        kind = wide ? READY_WIDE : READY;
         bulk_store(a.tiles + sh * TILES, sm, 4 * TILE);
         if (wide) bulk_store(a.tiles + sh * TILES + 4 * TILE, &s.N[0][0], TILE);
         bulk_commit();
       }
     }
-    follow_allow();
-    if (tid == 0) bulk_wait_all();
+    if (!FLAGS) follow_allow();
+    if (tid == 0) {
+      if (FLAGS)
+        publish(slot * a.H + h0 + heads - 1);
+      else
+        bulk_wait_all();
+    }
   } else if (tid == 0) {
-    mbar_wait(&full, 0, WAIT_CYCLES);
+    mbar_wait(w.full, phase, WAIT_CYCLES);
     set_device_error(a.err, GLACORE_ERR_TIMEOUT);
   }
   tc_fence_before();
+  return ok;
+}
+
+__global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __grid_constant__ PrepMaps maps,
+                                                                     const PrepArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full, done;
+  __shared__ uint32_t tmem_base;
+  __shared__ double warp0_total;
+  const PrepTeam w{(uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023), &full, &done, &tmem_base, &warp0_total,
+                   (int)threadIdx.x, 1};
+  const int hq = (int)(blockIdx.x % a.Hqk);
+  const int64_t slot = blockIdx.x / a.Hqk;
+  int64_t tok;
+  int L;
+  if (!chunk_in_slot(a.docs, slot, tok, L)) return;
+  if (w.tid == 0) {
+    mbar_init(&full, 1);
+    mbar_init(&done, 1);
+    fence_mbar_init();
+    prep_load(maps, w, hq, tok);
+  }
+  if (w.tid >> 5 == 1) {
+    tmem_alloc(&tmem_base, 64);
+    tmem_relinquish();
+  }
+  prep_chunk<false>(a, w, slot, hq * a.share, a.share, tok, L, 0, nullptr);
   __syncthreads();
-  if (warp == 1) {
+  if (w.tid >> 5 == 1) {
     tc_fence_after();
-    tmem_dealloc(tb, 64);
+    tmem_dealloc(tmem_base, 64);
   }
 }
 
@@ -407,7 +459,7 @@ __global__ void __launch_bounds__(PREP_THREADS, 4) delta_prep_kernel(const __gri
 //   warps 0..15  the chain: lanes of quarter w % 4, group w / 4 holds 32 of the
 //                state's key rows and 16 of the chunk's tokens (of its column v)
 //   warps 16..19 the output (none in STATES)
-//   warp 20      copies and products, one thread
+//   warps 20, 21 products, copies (a thread each)
 // TMEM columns: [0, 128) S^T, per group of 32 rows 16 columns of hi and 16 of
 // lo; the same columns take U'^T k once X and S^T q^T have read S.  [128, 384)
 // [X | S^T q^T] of even and odd chunks; E^T and then U^T P^T take X's place.  [384, 448)
@@ -443,6 +495,7 @@ struct ChainArgs {
   __nv_bfloat16 *o;
   const char *tiles;
   const float *gates;
+  const uint32_t *flags;  // of each chunk and head, when tiles and gates are made meanwhile; else null
   char *s_images, *e_images;  // STATES
   int *err;
 };
@@ -456,7 +509,7 @@ struct ChainSmem {
   static constexpr uint32_t BYTES = OUT + (STATES ? 0 : 16384) + 1024;
   static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BYTES <= 226 * 1024, "");
 };
-// 24 warps of 80 registers at launch (the last three of them idle), dealt out again by
+// 24 warps of 80 registers at launch (the last two or three of them idle), dealt out again by
 // warpgroup: 512 x 96 + 128 x 64 + 128 x 32 = 768 x 80.
 constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = 768;
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -498,12 +551,12 @@ __device__ __forceinline__ void put_state(uint32_t at, const float (&S)[32], cha
   }
 }
 
-template <bool STATES>
+template <bool STATES, bool FLAGS = false>
 __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArgs &a, int64_t unit) {
   using L_ = ChainSmem<STATES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, pu_full[2], o_free[2], drain;
+  __shared__ uint64_t full[2], s_ready, x_full, r_ready, e_full, u_ready, s_full, pu_full[2], o_free[2], stage_free[2], drain;
   __shared__ alignas(16) float o_into[2][CH];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
@@ -528,6 +581,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
       mbar_init(&full[i], 1);
       mbar_init(&pu_full[i], 1);
       mbar_init(&o_free[i], 4);
+      mbar_init(&stage_free[i], 1);
     }
     for (uint64_t *b : {&x_full, &e_full, &s_full, &drain}) mbar_init(b, 1);
     for (uint64_t *b : {&s_ready, &r_ready, &u_ready}) mbar_init(b, CHAIN_WARPS);
@@ -546,39 +600,6 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
   if (warp >= 20) {
     fewer_registers<48>();
     if (warp == 20 && lane == 0) {
-      const int hq = h / a.share;
-      tma_prefetch_desc(&maps.q);
-      tma_prefetch_desc(&maps.k);
-      tma_prefetch_desc(&maps.v);
-      int loaded = 0;
-      // whether chunk j is a wide one, read a chunk ahead of its copies
-      auto wide_of = [&](int j) -> float { return j < nch ? ldg_early(a.gates + ((slot0 + j) * a.H + h) * GATES + G_WIDE) : 0.f; };
-      float wide_next = wide_of(0);
-      auto load = [&](int j) {
-        uint8_t *p = sm + stage(j);
-        uint64_t *bar = &full[j & 1];
-        const int tok = (int)chunk_tok(j);
-        const bool wide = wide_next != 0.f;
-        wide_next = wide_of(j + 1);
-        mbar_expect_tx(bar, (STATES ? 2 : 3) * 16384 + (STATES ? 2 : 4) * TILE + (wide ? TILE : 0) + GATES * 4);
-        if (STATES) {
-          tma_load_3d(p + L_::KQ, &maps.k, 0, hq, tok, bar);
-          tma_load_3d(p + L_::KQ + 8192, &maps.k, 64, hq, tok, bar);
-        } else {
-          tma_load_3d(p + L_::KQ, &maps.k, 0, hq, tok, bar);
-          tma_load_3d(p + L_::KQ + 8192, &maps.q, 0, hq, tok, bar);
-          tma_load_3d(p + L_::KQ + 16384, &maps.k, 64, hq, tok, bar);
-          tma_load_3d(p + L_::KQ + 24576, &maps.q, 64, hq, tok, bar);
-        }
-        tma_load_3d(p + L_::V, &maps.v, 0, h, tok, bar);
-        tma_load_3d(p + L_::V + 8192, &maps.v, 64, h, tok, bar);
-        const int64_t sh = (slot0 + j) * a.H + h;
-        bulk_load(p + L_::Z, a.tiles + sh * TILES, 2 * TILE, bar);
-        if (wide) bulk_load(p + L_::Z + 2 * TILE, a.tiles + sh * TILES + 4 * TILE, TILE, bar);
-        if (!STATES) bulk_load(sm + L_::P + (uint32_t)(j % 3) * 2 * TILE, a.tiles + sh * TILES + 2 * TILE, 2 * TILE, bar);
-        bulk_load(p + L_::GT, a.gates + sh * GATES, GATES * 4, bar);
-        loaded = j + 1;
-      };
       constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), id128 = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idS = idesc_bf16(128, 128, false, true);
       constexpr uint32_t KROWS = STATES ? 64 : 128;  // rows of a 64-channel block of [k; q]
@@ -597,7 +618,6 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
         }
       };
       bool ok = true;
-      if (nch > 0) load(0);
       for (int j = 0; j < nch; ++j) {
         const uint32_t ph = (uint32_t)j & 1u, D = tb + T_XQ + ph * 128u;
         const uint32_t k = sb + stage(j) + L_::KQ, z = sb + stage(j) + L_::Z;
@@ -605,14 +625,14 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
         // the output has read this buffer's last values
         if (ok && !STATES && j >= 2) ok = mbar_wait(&o_free[ph], (uint32_t)((j - 2) >> 1) & 1u, WAIT_CYCLES);
         if (!ok) break;
+        // chunk j - 1 is through with its stage (its last product with k came before s_ready), j - 2 with its P
+        if (j) mbar_arrive(&stage_free[ph ^ 1u]);
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(D, s_col(tb, ks), kdesc(k, ks, KROWS), STATES ? id64 : id128, ks);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(D, s_col(tb, ks) + 16u, kdesc(k, ks, KROWS), STATES ? id64 : id128, 1);
         mma_commit(&x_full);
-        // chunk j - 1 is through with its stage (its last product with k before s_ready), j - 2 with its P
-        if (j + 1 < nch) load(j + 1);
         if (!STATES && j >= 1) pu(j - 1, true);
         ok = mbar_wait(&r_ready, ph, WAIT_CYCLES);
         if (!ok) break;
@@ -645,11 +665,76 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
         if (!STATES) pu(j, false);
       }
       if (!STATES && ok && nch > 0) pu(nch - 1, true);
-      // no copy or product of this block is in flight when it leaves
-      for (int j = max(0, loaded - 2); j < loaded; ++j)
-        if (!wait_full(j)) ok = false;
+      // no product of this block is in flight when it leaves
       mma_commit(&drain);
       if (!mbar_wait(&drain, 0, WAIT_CYCLES)) ok = false;
+      if (!ok) atomicExch(&abort_flag, 1);
+    } else if (warp == 21 && lane == 0) {
+      const int hq = h / a.share;
+      tma_prefetch_desc(&maps.q);
+      tma_prefetch_desc(&maps.k);
+      tma_prefetch_desc(&maps.v);
+      bool ok = true;
+      int loaded = 0;
+      // whether chunk j is a wide one, read a chunk ahead of its copies; with FLAGS told with its being ready, of
+      // up to AHEAD chunks at once: those before `ready`, in the bits of `wides`
+      constexpr int AHEAD = 8;
+      int ready = 0;
+      uint32_t wides = 0;
+      auto wide_of = [&](int j) -> bool {
+        if (j >= nch) return false;
+        const int64_t sh = (slot0 + j) * a.H + h;
+        if (!FLAGS) return ldg_early(a.gates + sh * GATES + G_WIDE) != 0.f;
+        if (j == ready) {
+          const long long t0 = clock64();
+          uint32_t f[AHEAD];
+          do {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) f[i] = j + i < nch ? ld_relaxed(a.flags + sh + (int64_t)i * a.H) : 0u;
+            if (clock64() - t0 > WAIT_CYCLES) ok = false;
+          } while (!f[0] && ok);
+          __threadfence();
+          fence_async_all();  // what was written before the flags is read by copies here
+          wides = 0;
+#pragma unroll
+          for (int i = 0; i < AHEAD; ++i)
+            if (ready == j + i && f[i]) {
+              ++ready;
+              wides |= f[i] == READY_WIDE ? 1u << ((j + i) % AHEAD) : 0u;
+            }
+        }
+        return wides >> (j % AHEAD) & 1u;
+      };
+      bool wide = wide_of(0);
+      for (int j = 0; j < nch; ++j) {
+        ok = ok && (j < 2 || mbar_wait(&stage_free[j & 1], (uint32_t)((j - 2) >> 1) & 1u, WAIT_CYCLES));
+        if (!ok) break;
+        uint8_t *p = sm + stage(j);
+        uint64_t *bar = &full[j & 1];
+        const int tok = (int)chunk_tok(j);
+        mbar_expect_tx(bar, (STATES ? 2 : 3) * 16384 + (STATES ? 2 : 4) * TILE + (wide ? TILE : 0) + GATES * 4);
+        if (STATES) {
+          tma_load_3d(p + L_::KQ, &maps.k, 0, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 8192, &maps.k, 64, hq, tok, bar);
+        } else {
+          tma_load_3d(p + L_::KQ, &maps.k, 0, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 8192, &maps.q, 0, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 16384, &maps.k, 64, hq, tok, bar);
+          tma_load_3d(p + L_::KQ + 24576, &maps.q, 64, hq, tok, bar);
+        }
+        tma_load_3d(p + L_::V, &maps.v, 0, h, tok, bar);
+        tma_load_3d(p + L_::V + 8192, &maps.v, 64, h, tok, bar);
+        const int64_t sh = (slot0 + j) * a.H + h;
+        bulk_load(p + L_::Z, a.tiles + sh * TILES, 2 * TILE, bar);
+        if (wide) bulk_load(p + L_::Z + 2 * TILE, a.tiles + sh * TILES + 4 * TILE, TILE, bar);
+        if (!STATES) bulk_load(sm + L_::P + (uint32_t)(j % 3) * 2 * TILE, a.tiles + sh * TILES + 2 * TILE, 2 * TILE, bar);
+        bulk_load(p + L_::GT, a.gates + sh * GATES, GATES * 4, bar);
+        loaded = j + 1;
+        wide = wide_of(j + 1);
+      }
+      // no copy of this block is in flight when it leaves
+      for (int j = max(0, loaded - 2); j < loaded; ++j)
+        if (!wait_full(j)) ok = false;
       if (!ok) atomicExch(&abort_flag, 1);
     }
     __syncwarp();
@@ -864,7 +949,8 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
 // token, [hi, lo][two blocks of 64 columns][64 rows]).
 //   warps 0..15  the chain, as in the forward
 //   warps 16..19 scale e^G dO as an operand, dv and dR on their way out
-//   warp 20      copies and products, one thread
+//   warp 20      copies and products, one thread (copies by another one, as in the forward: more registers
+//                spill in this kernel, 166 -> 238 us)
 // TMEM columns: [0, 128) dS1^T (hi, lo); [128, 192) dS1^T k^T, then (b dU)^T Z;
 // [192, 256) dO^T P; [256, 320) b dU, then dX; [320, 384) scale e^G dO;
 // [384, 512) the new part of dS0^T.
@@ -1260,6 +1346,66 @@ __global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_chain_kernel(const __g
                                                                        const ChainArgs a) {
   chain_walk<false>(maps, a, blockIdx.x);
 }
+// Few sequences leave most SMs without a walk: those make the tiles meanwhile,
+// chunk after chunk of all sequences, three teams of delta_prep_kernel's kind to a block.  Walks wait
+// for blocks of their launch, so it is a cooperative one: all of them run at once.
+struct OverlapArgs {
+  ChainArgs chain;
+  PrepArgs prep;
+  uint32_t *flags;  // 0 before the launch
+  uint32_t units, makers;  // blocks that walk, blocks that make tiles
+};
+constexpr int TEAMS = CHAIN_THREADS / PREP_THREADS;
+constexpr uint32_t TEAM_BYTES = 50 * 1024;
+static_assert(32768 + sizeof(PrepSmem) <= TEAM_BYTES && TEAMS * TEAM_BYTES + 1024 <= ChainSmem<false>::BYTES, "");
+
+__device__ __forceinline__ void make_tiles(const PrepMaps &maps, const OverlapArgs &a, uint32_t maker) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[TEAMS], done[TEAMS];
+  __shared__ uint32_t tmem_base[TEAMS];
+  __shared__ double warp0_total[TEAMS];
+  const int t = threadIdx.x / PREP_THREADS;
+  const PrepTeam w{(uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023) + t * TEAM_BYTES, &full[t], &done[t],
+                   &tmem_base[t], &warp0_total[t], (int)threadIdx.x % PREP_THREADS, 1 + 4 * t};
+  const PrepArgs &p = a.prep;
+  if (w.tid == 0) {
+    mbar_init(w.full, 1);
+    mbar_init(w.done, 1);
+    fence_mbar_init();
+  }
+  if (w.tid >> 5 == 1) tmem_alloc(w.tmem, 64);
+  __syncthreads();
+  const uint32_t wide = (uint32_t)p.docs.n * (uint32_t)p.H;  // (sequence, head) pairs
+  const uint32_t per = (uint32_t)((p.docs.T + CH - 1) / CH), n = wide * per;
+  uint32_t phase = 0;
+  for (uint32_t i = maker * TEAMS + t; i < n; i += a.makers * TEAMS, phase ^= 1u) {
+    const uint32_t j = i / wide, r = i % wide;
+    const int h = (int)(r % (uint32_t)p.H);
+    const int64_t slot = (int64_t)(r / (uint32_t)p.H) * per + j;
+    int64_t tok;
+    int L;
+    chunk_in_slot(p.docs, slot, tok, L);
+    if (w.tid == 0) prep_load(maps, w, h / p.share, tok);
+    if (!prep_chunk<true>(p, w, slot, h, 1, tok, L, phase, a.flags)) break;
+  }
+  __syncthreads();
+  if (w.tid >> 5 == 1) {
+    tc_fence_after();
+    tmem_dealloc(*w.tmem, 64);
+  }
+}
+struct OverlapMaps {
+  ChainMaps chain;
+  PrepMaps prep;
+};
+__global__ void __launch_bounds__(CHAIN_THREADS, 1) delta_overlap_kernel(const __grid_constant__ OverlapMaps maps,
+                                                                         const __grid_constant__ OverlapArgs a) {
+  if (blockIdx.x < a.units)
+    chain_walk<false, true>(maps.chain, a.chain, blockIdx.x);
+  else
+    make_tiles(maps.prep, a, blockIdx.x - a.units);
+}
+
 // The backward's two walks do not need one another: the first half of the
 // blocks goes backwards (the longer way), the second forwards.  4 x 16 heads: 128
 // of 152 SMs at work instead of 64 twice.
@@ -1806,7 +1952,7 @@ bool tc_supported(const glacore_problem *p) {
 // Scratch (byte offsets): tiles and gates of every chunk and head, the backward's images.
 namespace {
 struct TcLayout {
-  size_t order, tiles, gates, s, ds, e, r, total;
+  size_t order, flags, tiles, gates, s, ds, e, r, total;
 };
 TcLayout tc_layout(int64_t docs, int64_t slots, int64_t H, bool backward) {
   TcLayout l;
@@ -1818,6 +1964,10 @@ TcLayout tc_layout(int64_t docs, int64_t slots, int64_t H, bool backward) {
   };
   take(l.tiles, TILES);
   take(l.gates, GATES * sizeof(float));
+  if (!backward) {  // a flag per chunk and head
+    l.flags = off;
+    off = al256(off + (size_t)slots * H * sizeof(uint32_t));
+  }
   if (backward) {
     take(l.s, S_IMAGE);
     take(l.ds, S_IMAGE);
@@ -1840,10 +1990,11 @@ cudaError_t make_maps(const Call &c, const void *dO, Maps &m) {
                   (!dO || make_map(&m.dO, dO, true, c.p.V, c.p.H, c.p.BT, 64));
   return ok ? cudaSuccess : cudaErrorInvalidValue;
 }
-// `follow`: the kernel begins while the last one ends, and waits for it (follow_wait).
+// follow: the kernel begins while the last one ends, and waits for it (follow_wait); together: all blocks at once.
+enum class Start { behind, follow, together };
 template <auto kernel, typename M, typename A>
 cudaError_t launch(int64_t blocks, int threads, uint32_t smem, const Call &c, const M &maps, const A &a,
-                   const char *label, bool follow) {
+                   const char *label, Start start) {
   if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
   // shared memory is asked for once per kernel and device (the answer is the same for every call)
   static std::atomic<uint64_t> allowed{0};
@@ -1862,15 +2013,20 @@ cudaError_t launch(int64_t blocks, int threads, uint32_t smem, const Call &c, co
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.st;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (start == Start::together) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = follow ? 1 : 0;
+  cfg.numAttrs = start == Start::behind ? 0 : 1;
   const cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, maps, a);
   mark_launch(label, c.st);
   return r;
 }
-cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
+PrepArgs prep_args(const Call &c, char *ws, const TcLayout &l) {
   PrepArgs a;
   a.g = c.p.g;
   a.beta = c.beta;
@@ -1882,7 +2038,11 @@ cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
   a.tiles = ws + l.tiles;
   a.gates = (float *)(ws + l.gates);
   a.err = c.p.err;
-  return launch<delta_prep_kernel>(c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, a, "delta_prep", false);
+  return a;
+}
+cudaError_t prep(const Call &c, const Maps &m, char *ws, const TcLayout &l) {
+  return launch<delta_prep_kernel>(c.slots * c.p.Hqk, PREP_THREADS, PREP_BYTES, c, PrepMaps{m.q, m.k}, prep_args(c, ws, l),
+                                   "delta_prep", Start::behind);
 }
 // Packed documents that do not all run at once: the longest first, so that none
 // of them is begun when the others are done.
@@ -1893,6 +2053,18 @@ cudaError_t launch_order(const Call &c, int64_t blocks, char *ws, const int32_t 
   u.docs = c.docs;
   order = (const int32_t *)ws;
   return tc::launch_order_units(u, c.docs.n, (int32_t *)ws, c.st);
+}
+// Whether the tiles of the forward are made while the chains walk: sequences
+// of one length on at most half of the SMs (of packed documents the longest
+// would wait for the others' tiles), where what the tiles take alone, 0.019 us
+// a chunk and head, is more than what the walk loses, 0.4 us a chunk (its
+// copies wait for flags), and 2 to 6 us to begin with.  Heads x sequences, tokens,
+// us one after the other / at once: 64 x 2048: 164 / 143; 64 x 8192: 607 / 499; 76 x
+// 2048: 172 / 146; 64 x 640: 60 / 59; but 64 x 512: 49 / 51, 16 x 2048: 131 / 136,
+// 16 x 96: 21 / 27.
+bool overlaps(const Call &c, int64_t units) {
+  return !c.docs.start && units <= tc::sm_count() / 2 && (units - 24) * ((c.docs.T + CH - 1) / CH) > 320 &&
+         c.slots * c.p.H < ((int64_t)1 << 31);
 }
 ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   ChainArgs a;
@@ -1920,15 +2092,29 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
   Maps m;
   const int32_t *order = nullptr;
   cudaError_t e = make_maps(c, nullptr, m);
-  if (e == cudaSuccess) e = launch_order(c, c.docs.n * c.p.H, ws + l.order, order);
-  if (e == cudaSuccess) e = prep(c, m, ws, l);
-  if (e != cudaSuccess) return e;
+  const int64_t units = c.docs.n * c.p.H;
   ChainArgs a = chain_args(c, ws, l);
-  a.order = order;
   a.o = (__nv_bfloat16 *)o;
   a.ht = ht;
-  return launch<delta_chain_kernel>(c.docs.n * c.p.H, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
-                ChainMaps{m.q, m.k, m.v}, a, "delta_chain", true);
+  if (e == cudaSuccess && overlaps(c, units)) {
+    OverlapArgs x;
+    x.chain = a;
+    x.prep = prep_args(c, ws, l);
+    x.flags = (uint32_t *)(ws + l.flags);
+    x.units = (uint32_t)units;
+    x.chain.flags = x.flags;
+    x.makers = (uint32_t)std::min(tc::sm_count() - units, (c.slots * c.p.H + TEAMS - 1) / TEAMS);
+    e = cudaMemsetAsync(x.flags, 0, (size_t)(c.slots * c.p.H) * sizeof(uint32_t), c.st);
+    if (e != cudaSuccess) return e;
+    return launch<delta_overlap_kernel>(x.makers + units, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
+                                        OverlapMaps{{m.q, m.k, m.v}, {m.q, m.k}}, x, "delta_overlap", Start::together);
+  }
+  if (e == cudaSuccess) e = launch_order(c, units, ws + l.order, order);
+  if (e == cudaSuccess) e = prep(c, m, ws, l);
+  if (e != cudaSuccess) return e;
+  a.order = order;
+  return launch<delta_chain_kernel>(units, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
+                ChainMaps{m.q, m.k, m.v}, a, "delta_chain", Start::follow);
 }
 
 cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, void *dk, bool per_head, void *dv, float *dg,
@@ -1962,7 +2148,7 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   b.err = a.err;
   const int64_t units = c.docs.n * c.p.H;
   e = launch<delta_walks_kernel>(2 * units, CHAIN_THREADS, std::max(ChainSmem<true>::BYTES, BackSmem::BYTES), c,
-             WalkMaps{{m.q, m.k, m.v}, {m.q, m.k, m.dO}}, WalkArgs{a, b, units}, "delta_walks", true);
+             WalkMaps{{m.q, m.k, m.v}, {m.q, m.k, m.dO}}, WalkArgs{a, b, units}, "delta_walks", Start::follow);
   if (e != cudaSuccess) return e;
   GradArgs g;
   g.docs = a.docs;
@@ -1984,9 +2170,9 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   g.units = c.slots * c.p.H;
   const int64_t blocks = std::min(g.units, tc::sm_count());
   return per_head ? launch<delta_grads_kernel<true>>(blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
-                           "delta_grads", true)
+                           "delta_grads", Start::follow)
                   : launch<delta_grads_kernel<false>>(blocks, GRAD_THREADS, GradSmem::BYTES, c, GradMaps{m.q, m.k, m.dO}, g,
-                           "delta_grads", true);
+                           "delta_grads", Start::follow);
 }
 
 }  // namespace delta

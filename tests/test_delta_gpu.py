@@ -441,3 +441,39 @@ def test_many_chunks_against_the_other_kernels(cuda_ok, B, T, H, Hqk, V, docs):
         bound = 2 * (4 if name == "dg" else 1) * TOL * y.abs().max() + (2 * ULP[BF] * y.abs() if first[0].dtype == BF else 0)
         assert bool(((x - y).abs() <= bound).all()), (name, float((x - y).abs().max()), float(y.abs().max()))
     glc.get_device_error()
+
+
+@pytest.mark.parametrize("B,T,H,Hqk,K,V,kw", [
+    (2, 640, 32, 32, 128, 128, {}), (4, 2048, 16, 4, 128, 128, {}), (1, 777, 76, 19, 64, 48, {"states": True}),
+    (1, 64 * 41 + 1, 33, 11, 128, 64, {"states": True}), (4, 1000, 16, 16, 128, 128, {"same_key": True})])
+def test_tiles_made_while_the_chains_walk(cuda_ok, B, T, H, Hqk, K, V, kw):
+    """Sequences of one length on few SMs take one kernel; given as documents they take two: the same bits, every time,
+    also from a graph beside another stream's calls."""
+    x, dev, _, call, _ = make(B, T, H, Hqk, K, V, BF, 11, **kw)
+    if kw.get("same_key"):
+        dev["beta"].fill_(2.0)  # long rows of Z: their third part
+    args = [dev[n] for n in ("q", "k", "v", "g", "beta")]
+    seg = torch.arange(B, device="cuda", dtype=torch.int32)[:, None].expand(B, T).contiguous()
+    run = lambda **k: glc.delta_fwd(*args, initial_state=call["initial_state"], output_final_state=True, **k)
+    with glc.LaunchTimer(8) as t:
+        want = run(segment_ids=seg, n_seqs=B)
+    assert t.labels[-2:] == ["delta_prep", "delta_chain"]
+    with glc.LaunchTimer(8) as t:
+        got = run(poison=True)
+    if torch.cuda.get_device_properties(0).multi_processor_count // 2 >= B * H:
+        assert t.labels == ["delta_overlap"]
+    same = lambda a: all(torch.equal(x, y) for x, y in zip(a, want))
+    assert same(got)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        held = run()
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        for y in held:
+            y.zero_()
+        graph.replay()
+        with torch.cuda.stream(side):
+            other = run()
+        torch.cuda.synchronize()
+        assert same(held) and same(other)
+    glc.get_device_error()
