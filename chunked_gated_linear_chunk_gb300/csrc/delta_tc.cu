@@ -510,7 +510,8 @@ struct ChainSmem {
   static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BYTES <= 226 * 1024, "");
 };
 // 24 warps of 80 registers at launch (the last two or three of them idle), dealt out again by
-// warpgroup: 512 x 96 + 128 x 64 + 128 x 32 = 768 x 80.
+// warpgroup: 512 x 88 + 256 x 64 = 768 x 80.  (88, 80 and 48: more spills, the walks 169 instead of 164 us;
+// 96, 64 and 32: 10% slower.  22 warps without dealing out: 280 bytes spilt, 182 us.)
 constexpr int CHAIN_WARPS = 16, CHAIN_THREADS = 768;
 template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -598,7 +599,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
   auto wait_full = [&](int j) -> bool { return mbar_wait(&full[j & 1], (uint32_t)(j >> 1) & 1u, WAIT_CYCLES); };
 
   if (warp >= 20) {
-    fewer_registers<48>();
+    fewer_registers<64>();
     if (warp == 20 && lane == 0) {
       constexpr uint32_t id64 = idesc_bf16(128, 64, false, false), id128 = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idS = idesc_bf16(128, 128, false, true);
@@ -883,7 +884,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
         if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
     }
   } else {
-    fewer_registers<80>();
+    fewer_registers<64>();
     const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     bool ok = true;
@@ -949,8 +950,7 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
 // token, [hi, lo][two blocks of 64 columns][64 rows]).
 //   warps 0..15  the chain, as in the forward
 //   warps 16..19 scale e^G dO as an operand, dv and dR on their way out
-//   warp 20      copies and products, one thread (copies by another one, as in the forward: more registers
-//                spill in this kernel, 166 -> 238 us)
+//   warp 20      copies and products, one thread (copies by another one, as in the forward, gain nothing here)
 // TMEM columns: [0, 128) dS1^T (hi, lo); [128, 192) dS1^T k^T, then (b dU)^T Z;
 // [192, 256) dO^T P; [256, 320) b dU, then dX; [320, 384) scale e^G dO;
 // [384, 512) the new part of dS0^T.
@@ -1024,7 +1024,7 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
   auto wait_full = [&](int i) -> bool { return mbar_wait(&full[i & 1], (uint32_t)(i >> 1) & 1u, WAIT_CYCLES); };
 
   if (warp >= 20) {
-    fewer_registers<48>();
+    fewer_registers<64>();
     if (warp == 20 && lane == 0) {
       const int hq = h / a.share;
       tma_prefetch_desc(&maps.q);
@@ -1256,7 +1256,7 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
         if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
     }
   } else {
-    fewer_registers<80>();
+    fewer_registers<64>();
     const int qw = warp & 3, v = qw * 32 + lane, tid = threadIdx.x - 32 * CHAIN_WARPS;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     bool ok = true;
@@ -2059,7 +2059,7 @@ cudaError_t launch_order(const Call &c, int64_t blocks, char *ws, const int32_t 
 // would wait for the others' tiles), where what the tiles take alone, 0.019 us
 // a chunk and head, is more than what the walk loses, 0.4 us a chunk (its
 // copies wait for flags), and 2 to 6 us to begin with.  Heads x sequences, tokens,
-// us one after the other / at once: 64 x 2048: 164 / 143; 64 x 8192: 607 / 499; 76 x
+// us one after the other / at once: 64 x 2048: 164 / 137; 64 x 8192: 607 / 499; 76 x
 // 2048: 172 / 146; 64 x 640: 60 / 59; but 64 x 512: 49 / 51, 16 x 2048: 131 / 136,
 // 16 x 96: 21 / 27.
 bool overlaps(const Call &c, int64_t units) {
