@@ -9,8 +9,10 @@
 //     o_t = scale (e^g S^T q + (q . k) u),  u = b (v - e^g S^T k)
 // (both on the state before the token).  The other half of the block's warps
 // converts the next 16 tokens' q, k, v into shared memory meanwhile.  Bound by
-// the latency of that dependence; any decay is exact here.  The gradients of q, k, g and beta then take every chunk of 64 tokens
-// by itself (simt_grads), as products of 64 x 64 tiles.
+// the latency of that dependence, 0.26 us a token; any decay is exact here.  The
+// gradients of q, k, g and beta then take every chunk of 64 tokens
+// by itself (simt_grads), as products of 64 x 64 tiles.  333 tokens of 3 x 6 heads
+// of 72 x 41, fp32: passes 100 us (both in one launch), gradients 48 us.
 #include <algorithm>
 
 #include "delta.cuh"
@@ -318,10 +320,15 @@ cudaError_t scans_bwd(const Call &c, const void *dO, const float *dht, void *dv,
 //
 // One block per (chunk, head), 256 threads; thread (tx, ty) owns the 4 x 4
 // entries (ty + 16 i, tx + 16 j) of a 64 x 64 result (rows and columns 16
-// apart, so that its shared-memory reads are free of bank conflicts at a row pitch of PITCH).
+// apart, so that its shared-memory reads, four along the contraction at once, are free of
+// bank conflicts at a row pitch of PITCH).  Bound by those reads, and where
+// the chunks are few by the staging: all of a slice's loads are in flight at once.
+// 128 registers for two blocks on an SM: 1024 chunk heads of 128 x 128 fp32 551 -> 454 us,
+// 108 of 72 x 41 (a block on an SM) 54 -> 55 us.
 constexpr int W = 32;      // columns of a staged slice of the contraction
-constexpr int PITCH = 33;  // its row pitch
-constexpr int CP = C + 1;  // pitch of the C x C matrices
+constexpr int PITCH = 36;  // its row pitch
+constexpr int CP = C + 4;  // pitch of the C x C matrices
+constexpr int PER = C * W / 256;  // values of a slice that a thread stages
 
 template <typename T>
 struct GradArgs {
@@ -337,11 +344,14 @@ struct GradArgs {
   float *dg, *dbeta;
 };
 
-struct GradSmem {
-  float x[5][C][PITCH];  // staged slices
-  float dP[C][CP], dA[C][CP];
-  float kt[C][C + 1], qt[C][C + 1];  // 64 channels of k and q
-  double G[C];
+struct alignas(16) GradSmem {
+  union {
+    float x[5][C][PITCH];  // staged slices
+    float kq[2][C][C + 1];  // 64 channels of k and q
+    float w[C][CP];         // W_rs
+  };
+  float dP[C][CP], dPT[C][CP], dA[C][CP];  // dPd and its transpose, dA + dA^T
+  double G[C], half_total;
   float into[C], outof[C], beta[C];
   float gq[C], gk[C], gadd[C], db[C], pair[C];
   float red[32];
@@ -350,18 +360,19 @@ struct GradSmem {
 // acc[i][j] += sum over the slice of a[ty + 16 i][.] b[tx + 16 j][.]
 __device__ __forceinline__ void slice_product(float (&acc)[4][4], const float (*a)[PITCH], const float (*b)[PITCH],
                                               int tx, int ty) {
-#pragma unroll 8
-  for (int w = 0; w < W; ++w) {
-    float x[4], y[4];
+#pragma unroll 4
+  for (int w = 0; w < W; w += 4) {
+    float4 x[4], y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = a[ty + 16 * i][w];
-      y[i] = b[tx + 16 * i][w];
+      x[i] = *reinterpret_cast<const float4 *>(&a[ty + 16 * i][w]);
+      y[i] = *reinterpret_cast<const float4 *>(&b[tx + 16 * i][w]);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int j = 0; j < 4; ++j)
+        acc[i][j] = fmaf(x[i].w, y[j].w, fmaf(x[i].z, y[j].z, fmaf(x[i].y, y[j].y, fmaf(x[i].x, y[j].x, acc[i][j]))));
   }
 }
 __device__ __forceinline__ void zero(float (&acc)[4][4]) {
@@ -372,7 +383,7 @@ __device__ __forceinline__ void zero(float (&acc)[4][4]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
+__global__ void __launch_bounds__(256, 2) grads_kernel(const GradArgs<T> a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   GradSmem &s = *reinterpret_cast<GradSmem *>(smem_raw);
   const int h = (int)(blockIdx.x % a.H);
@@ -384,14 +395,20 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const T *q = a.q + (int64_t)hq * a.K, *k = a.k + (int64_t)hq * a.K;
 
+  double G = 0.0;
   if (tid < C) {
-    s.G[tid] = tid < L ? (double)fmaxf(a.g[(tok0 + tid) * a.H + h], -1e4f) : 0.0;  // exp of less is 0 as well
+    if (tid < L) G = (double)fmaxf(a.g[(tok0 + tid) * a.H + h], -1e4f);  // exp of less is 0 as well
     s.beta[tid] = tid < L ? a.beta[(tok0 + tid) * a.H + h] : 0.f;
-    s.gq[tid] = s.gk[tid] = s.gadd[tid] = s.db[tid] = 0.f;
+    s.gq[tid] = s.gk[tid] = s.gadd[tid] = 0.f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, G, o);
+      if ((tid & 31) >= o) G += y;
+    }
+    if (tid == 31) s.half_total = G;
   }
   __syncthreads();
-  if (tid == 0)
-    for (int t = 1; t < C; ++t) s.G[t] += s.G[t - 1];
+  if (tid < C) s.G[tid] = tid < 32 ? G : G + s.half_total;
   __syncthreads();
   if (tid < C) {
     s.into[tid] = expf((float)s.G[tid]);
@@ -400,47 +417,60 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
   const float over = expf((float)s.G[L - 1]);
 
   // token rows [tok0, tok0 + L) x columns [c0, c0 + W) of a per-head fp32 or T tensor
-  auto stage_rows = [&](float (*dst)[PITCH], auto *src, int64_t stride, int c0, int width) {
-    for (int i = tid; i < C * W; i += 256) {
-      const int r = i / W, c = i % W;
-      dst[r][c] = r < L && c0 + c < width ? to_f32(src[(tok0 + r) * stride + c0 + c]) : 0.f;
+  auto load_rows = [&](float (&v)[PER], auto *src, int64_t stride, int c0, int width) {
+#pragma unroll
+    for (int n = 0; n < PER; ++n) {
+      const int r = (tid + 256 * n) / W, c = tid % W;
+      v[n] = r < L && c0 + c < width ? to_f32(src[(tok0 + r) * stride + c0 + c]) : 0.f;
     }
+  };
+  auto put_rows = [&](float (*dst)[PITCH], const float (&v)[PER]) {
+#pragma unroll
+    for (int n = 0; n < PER; ++n) dst[(tid + 256 * n) / W][tid % W] = v[n];
   };
   const int64_t hv = (int64_t)a.H * a.V;
   const float *e = a.s.e + (int64_t)h * a.V, *dr = a.s.dr + (int64_t)h * a.V;
   const T *dO = a.dO + (int64_t)h * a.V;
 
   // C x C products over the value columns, then over the key channels
-  float b1[4][4], b2[4][4];
+  float b1[4][4], b2[4][4], db = 0.f;
   zero(b1);
   zero(b2);
   for (int c0 = 0; c0 < a.V; c0 += W) {
+    float v0[PER], v1[PER], v2[PER];
+    load_rows(v0, dO, hv, c0, a.V);
+    load_rows(v1, dr, hv, c0, a.V);
+    load_rows(v2, e, hv, c0, a.V);
     __syncthreads();
-    stage_rows(s.x[0], dO, hv, c0, a.V);
-    stage_rows(s.x[1], dr, hv, c0, a.V);
-    stage_rows(s.x[2], e, hv, c0, a.V);
+    put_rows(s.x[0], v0);
+    put_rows(s.x[1], v1);
+    put_rows(s.x[2], v2);
     __syncthreads();
     slice_product(b1, s.x[0], s.x[2], tx, ty);
     slice_product(b2, s.x[1], s.x[2], tx, ty);
-    if (tid < C) {
-      float x = 0.f;
-      for (int c = 0; c < W; ++c) x = fmaf(s.x[1][tid][c], s.x[2][tid][c], x);
-      s.db[tid] += x;
-    }
+#pragma unroll
+    for (int n = 0; n < W / 4; ++n)  // four threads to a row
+      db = fmaf(s.x[1][tid >> 2][(tid & 3) + 4 * n], s.x[2][tid >> 2][(tid & 3) + 4 * n], db);
   }
+  db += __shfl_xor_sync(0xffffffffu, db, 1);
+  db += __shfl_xor_sync(0xffffffffu, db, 2);
+  if ((tid & 3) == 0) s.db[tid >> 2] = db;
   float qk[4][4], kk[4][4];
   zero(qk);
   zero(kk);
   for (int c0 = 0; c0 < a.K; c0 += W) {
+    float v0[PER], v1[PER];
+    load_rows(v0, q, a.qs, c0, a.K);
+    load_rows(v1, k, a.ks, c0, a.K);
     __syncthreads();
-    stage_rows(s.x[0], q, a.qs, c0, a.K);
-    stage_rows(s.x[1], k, a.ks, c0, a.K);
+    put_rows(s.x[0], v0);
+    put_rows(s.x[1], v1);
     __syncthreads();
     slice_product(qk, s.x[0], s.x[1], tx, ty);
     slice_product(kk, s.x[1], s.x[1], tx, ty);
   }
   // dPd and dA; W_rs of the pairs r > s, kept in the staging area
-  float (*Wm)[CP] = reinterpret_cast<float (*)[CP]>(&s.x[0][0][0]);
+  float (*Wm)[CP] = s.w;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -453,24 +483,36 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
         dp = a.scale * D * b1[i][jj];
         if (r < t) da = -D * s.beta[t] * b2[i][jj];
       }
-      s.dP[t][r] = dp;
-      s.dA[t][r] = da;
+      s.dP[t][r] = s.dPT[r][t] = dp;
+      if (r <= t) s.dA[t][r] = s.dA[r][t] = da;
       Wm[t][r] = r < t ? fmaf(dp, qk[i][jj], da * kk[i][jj]) : 0.f;
     }
   __syncthreads();
   // pair[t] = sum over r >= t > s of W_rs: first every column's sums from below, then along each row
   if (tid < C) {
     float x = 0.f;
-    for (int r = C - 1; r >= 0; --r) {
-      x += Wm[r][tid];
-      Wm[r][tid] = x;
+    for (int r = C - 8; r >= 0; r -= 8) {
+      float y[8];
+#pragma unroll
+      for (int n = 0; n < 8; ++n) y[n] = Wm[r + n][tid];
+#pragma unroll
+      for (int n = 7; n >= 0; --n) {
+        x += y[n];
+        Wm[r + n][tid] = x;
+      }
     }
   }
   __syncthreads();
-  if (tid < C) {
+  {  // four threads to a row
     float x = 0.f;
-    for (int c = 0; c < tid; ++c) x += Wm[tid][c];
-    s.pair[tid] = x;
+#pragma unroll
+    for (int n = 0; n < C / 4; ++n) {
+      const int c = (tid & 3) + 4 * n;
+      x += c < tid >> 2 ? Wm[tid >> 2][c] : 0.f;
+    }
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    if ((tid & 3) == 0) s.pair[tid >> 2] = x;
   }
 
   // dq, dk for 64 channels at a time; <S0, dS1> on the way
@@ -482,31 +524,48 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
     zero(m2);
     zero(m3);
     for (int c0 = 0; c0 < a.V; c0 += W) {
-      __syncthreads();
-      stage_rows(s.x[0], dO, hv, c0, a.V);
-      stage_rows(s.x[1], dr, hv, c0, a.V);
-      stage_rows(s.x[2], e, hv, c0, a.V);
-      for (int i = tid; i < C * W; i += 256) {
-        const int r = i / W, c = i % W;
+      float v0[PER], v1[PER], v2[PER], v3[PER], v4[PER];
+      load_rows(v0, dO, hv, c0, a.V);
+      load_rows(v1, dr, hv, c0, a.V);
+      load_rows(v2, e, hv, c0, a.V);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) {
+        const int r = (tid + 256 * n) / W, c = tid % W;
         const bool in = k0 + r < a.K && c0 + c < a.V;
-        const float x = in ? S0[(int64_t)(k0 + r) * a.V + c0 + c] : 0.f, y = in ? S1[(int64_t)(k0 + r) * a.V + c0 + c] : 0.f;
-        s.x[3][r][c] = x;
-        s.x[4][r][c] = y;
-        sd = fmaf(x, y, sd);
+        const int64_t at = (int64_t)(k0 + r) * a.V + c0 + c;
+        v3[n] = in ? S0[at] : 0.f;
+        v4[n] = in ? S1[at] : 0.f;
       }
+      __syncthreads();
+      put_rows(s.x[0], v0);
+      put_rows(s.x[1], v1);
+      put_rows(s.x[2], v2);
+      put_rows(s.x[3], v3);
+      put_rows(s.x[4], v4);
+#pragma unroll
+      for (int n = 0; n < PER; ++n) sd = fmaf(v3[n], v4[n], sd);
       __syncthreads();
       slice_product(m1, s.x[0], s.x[3], tx, ty);
       slice_product(m2, s.x[1], s.x[3], tx, ty);
       slice_product(m3, s.x[2], s.x[4], tx, ty);
     }
-    __syncthreads();
-    for (int i = tid; i < C * 64; i += 256) {
-      const int r = i / 64, c = i % 64;
-      const bool in = r < L && k0 + c < a.K;
-      s.kt[r][c] = in ? to_f32(k[(tok0 + r) * a.ks + k0 + c]) : 0.f;
-      s.qt[r][c] = in ? to_f32(q[(tok0 + r) * a.qs + k0 + c]) : 0.f;
+    {
+      float kv[C / 4], qv[C / 4];
+#pragma unroll
+      for (int n = 0; n < C / 4; ++n) {
+        const int r = tid / 64 + 4 * n, c = tid % 64;
+        const bool in = r < L && k0 + c < a.K;
+        kv[n] = in ? to_f32(k[(tok0 + r) * a.ks + k0 + c]) : 0.f;
+        qv[n] = in ? to_f32(q[(tok0 + r) * a.qs + k0 + c]) : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < C / 4; ++n) {
+        s.kq[0][tid / 64 + 4 * n][tid % 64] = kv[n];
+        s.kq[1][tid / 64 + 4 * n][tid % 64] = qv[n];
+      }
+      __syncthreads();
     }
-    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = ty + 16 * i;
@@ -517,9 +576,9 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
         m1[i][jj] *= a.scale * s.into[t];
         m2[i][jj] *= -s.into[t] * s.beta[t];
         m3[i][jj] *= s.outof[t] * s.beta[t];
-        rq = fmaf(s.qt[t][c], m1[i][jj], rq);
-        rk = fmaf(s.kt[t][c], m2[i][jj], rk);
-        ra = fmaf(s.kt[t][c], m3[i][jj], ra);
+        rq = fmaf(s.kq[1][t][c], m1[i][jj], rq);
+        rk = fmaf(s.kq[0][t][c], m2[i][jj], rk);
+        ra = fmaf(s.kq[0][t][c], m3[i][jj], ra);
         m2[i][jj] += m3[i][jj];
       }
 #pragma unroll
@@ -534,23 +593,25 @@ __global__ void __launch_bounds__(256) grads_kernel(const GradArgs<T> a) {
         s.gadd[t] += ra;
       }
     }
-    for (int r = 0; r < L; ++r) {
-      float kx[4], qx[4], pr[4], ar[4], pc[4], ac[4];
+    for (int r = 0; r < L; r += 4) {  // what is past L is 0
+      float4 pr[4], pc[4], ar[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        kx[i] = s.kt[r][tx + 16 * i];
-        qx[i] = s.qt[r][tx + 16 * i];
-        pr[i] = s.dP[ty + 16 * i][r];
-        ar[i] = s.dA[ty + 16 * i][r];
-        pc[i] = s.dP[r][ty + 16 * i];
-        ac[i] = s.dA[r][ty + 16 * i];
+        pr[i] = *reinterpret_cast<const float4 *>(&s.dP[ty + 16 * i][r]);
+        pc[i] = *reinterpret_cast<const float4 *>(&s.dPT[ty + 16 * i][r]);
+        ar[i] = *reinterpret_cast<const float4 *>(&s.dA[ty + 16 * i][r]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
-          m1[i][jj] = fmaf(pr[i], kx[jj], m1[i][jj]);
-          m2[i][jj] = fmaf(pc[i], qx[jj], fmaf(ar[i] + ac[i], kx[jj], m2[i][jj]));
+          const float kx = s.kq[0][r + n][tx + 16 * jj], qx = s.kq[1][r + n][tx + 16 * jj];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float p = (&pr[i].x)[n], pt = (&pc[i].x)[n], at = (&ar[i].x)[n];
+            m1[i][jj] = fmaf(p, kx, m1[i][jj]);
+            m2[i][jj] = fmaf(pt, qx, fmaf(at, kx, m2[i][jj]));
+          }
         }
     }
 #pragma unroll
