@@ -16,6 +16,9 @@
 // in registers, with the loads of several rows in flight.  Rows that 16-byte accesses
 // or 8-channel steps do not fit take a kernel with a warp per row and the
 // row in shared memory.
+// 8192 tokens of 32 heads of 128, bf16, rotated: 24.6 us forward (82% of the copy
+// rate), 49 us backward (62%: three blocks' loads on an SM do not cover their
+// latency; two or four of them are slower) and 7 us for the sum of the weight gradients.
 #include <string.h>
 
 #include <algorithm>
