@@ -13,14 +13,24 @@ namespace {
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// bf16 operands that the tensor-core kernels cannot read in place (heads of no
+// multiple of 8, odd strides or addresses) go to them as padded copies, backwards always
+// and forwards from this many tokens times rounds of blocks (run_fwd) on.  Token by
+// token / copies, us forward and backward, heads of 72 x 41 and 6 of them: 8 tokens
+// 6 / 31, 52 / 45; 100: 31 / 35, 93 / 52; 128: 37 / 35, 101 / 53; 333: 89 / 47, 160 / 70;
+// 4 x 2048 tokens of 16 heads of 125 x 77: 756 / 207, 2127 / 522; 64 x 8 tokens of 16
+// heads of 90 x 90: 47 / 88, 385 / 234.
+constexpr int64_t PAD_TOKENS = 120;
+
 struct Layout {
   size_t start, cbase;          // document tables (segment_ids only)
   size_t s0, ds1, e, dr;        // backward
   size_t dq, dk;                // backward, shared q / k heads: per value head, fp32
   size_t tc;                    // the tensor-core kernels' own
+  size_t pq, pk, pv, po, pdv, pdq, pdk;  // padded copies (po: of o, of do in the backward)
   size_t total;
-  int64_t slots;
-  bool on_tc;
+  int64_t slots, Kp, Vp;
+  bool on_tc, pad;
 };
 
 Layout layout(const glacore_problem *p, bool backward) {
@@ -38,7 +48,26 @@ Layout layout(const glacore_problem *p, bool backward) {
   }
   // a document's last chunk may be short: at most one more than its tokens fill
   L.slots = p->segment_ids ? std::min(BT, BT / C + n) : p->B * ((p->T + C - 1) / C);
-  L.on_tc = tc_supported(p) && L.slots * p->H < ((int64_t)1 << 30) && n * p->H < ((int64_t)1 << 30);  // units in 32 bits
+  const bool fits = L.slots * p->H < ((int64_t)1 << 30) && n * p->H < ((int64_t)1 << 30);  // units in 32 bits
+  L.on_tc = fits && tc_supported(p);
+  L.pad = fits && tc_padded(p);
+  if (L.pad) {
+    L.Kp = (p->K + 7) / 8 * 8;
+    L.Vp = (p->V + 7) / 8 * 8;
+    take(L.pq, 2 * (size_t)BT * p->Hqk * L.Kp);
+    take(L.pk, 2 * (size_t)BT * p->Hqk * L.Kp);
+    take(L.pv, 2 * (size_t)BT * p->H * L.Vp);
+    take(L.po, 2 * (size_t)BT * p->H * L.Vp);
+    take(L.tc, tc_workspace(n, L.slots, p->H, backward));
+    if (backward) {
+      const size_t each = p->Hqk != p->H ? sizeof(float) : 2;
+      take(L.pdv, 2 * (size_t)BT * p->H * L.Vp);
+      take(L.pdq, each * (size_t)BT * p->H * L.Kp);
+      take(L.pdk, each * (size_t)BT * p->H * L.Kp);
+    }
+    L.total = off;
+    return L;
+  }
   // the scratch of one call serves either family: the addresses of the outputs decide (run_fwd, run_bwd)
   if (L.on_tc) take(L.tc, tc_workspace(n, L.slots, p->H, backward));
   if (backward) {
@@ -87,6 +116,8 @@ glacore_status begin(const glacore_problem *p, const float *beta, const Layout &
   if (!c.p.err) return GLACORE_ERR_CUDA;
   c.slots = L.slots;
   c.dtype = p->dtype;
+  c.sK = p->K;
+  c.sV = p->V;
   c.beta = beta;
   c.st = st;
   char *ws = (char *)p->workspace;
@@ -98,6 +129,23 @@ glacore_status begin(const glacore_problem *p, const float *beta, const Layout &
   if (!p->segment_ids) return GLACORE_OK;
   return status_of(launch_prep(p->segment_ids, p->B, p->T, p->n_seqs, C, (int64_t *)(ws + L.start),
                                (int64_t *)(ws + L.cbase), c.p.err, st));
+}
+
+// The same call on padded copies of q, k, v (and do).
+cudaError_t padded(const Call &c, const Layout &L, const void *dO, char *ws, Call &to) {
+  to = c;
+  Prob &p = to.p;
+  p.q = ws + L.pq;
+  p.k = ws + L.pk;
+  p.v = ws + L.pv;
+  p.K = L.Kp;
+  p.V = L.Vp;
+  p.qs = p.ks = p.Hqk * p.K;
+  p.vs = p.H * p.V;
+  const int H = (int)p.H, Hqk = (int)p.Hqk, K = (int)c.p.K, V = (int)c.p.V, Kp = (int)L.Kp, Vp = (int)L.Vp;
+  const Rows q{c.p.q, ws + L.pq, c.p.qs, Hqk, K, Kp}, k{c.p.k, ws + L.pk, c.p.ks, Hqk, K, Kp},
+      v{c.p.v, ws + L.pv, c.p.vs, H, V, Vp}, o{dO, ws + L.po, (int64_t)H * V, H, V, Vp};
+  return dO ? pad_rows(c, {q, k, v, o}) : pad_rows(c, {q, k, v});
 }
 
 glacore_status run_fwd(const glacore_problem *p, const float *beta, void *o, float *ht, cudaStream_t st) {
@@ -118,6 +166,14 @@ glacore_status run_fwd(const glacore_problem *p, const float *beta, void *o, flo
   const int64_t blocks = c.docs.n * p->H * ((p->V + 31) / 32), rounds = (blocks + 607) / 608;
   if (L.on_tc && p->T * rounds > 56 && !((uintptr_t)o & 15))
     return status_of(tc_fwd(c, o, ht, (char *)p->workspace + L.tc));
+  if (L.pad && p->T * rounds > PAD_TOKENS) {
+    char *ws = (char *)p->workspace;
+    Call t;
+    cudaError_t e = padded(c, L, nullptr, ws, t);
+    if (e == cudaSuccess) e = tc_fwd(t, ws + L.po, ht, ws + L.tc);
+    if (e == cudaSuccess) e = unpad_rows(c, {{ws + L.po, o, 0, (int)p->H, (int)p->V, (int)L.Vp}});
+    return status_of(e);
+  }
   return status_of(simt_fwd(c, o, ht));
 }
 
@@ -138,6 +194,19 @@ glacore_status run_bwd(const glacore_problem *p, const float *beta, const void *
   const bool shared = p->Hqk != p->H;
   void *hq = shared ? (void *)(ws + L.dq) : dq, *hk = shared ? (void *)(ws + L.dk) : dk;
   cudaError_t e;
+  if (L.pad) {
+    Call t;
+    e = padded(c, L, dO, ws, t);
+    if (e == cudaSuccess)
+      e = tc_bwd(t, ws + L.po, dht, ws + L.pdq, ws + L.pdk, shared, ws + L.pdv, dg, dbeta, dh0, ws + L.tc);
+    const int H = (int)p->H, K = (int)p->K;
+    const Rows v{ws + L.pdv, dv, 0, H, (int)p->V, (int)L.Vp}, q{ws + L.pdq, dq, 0, H, K, (int)L.Kp},
+        k{ws + L.pdk, dk, 0, H, K, (int)L.Kp};
+    if (e == cudaSuccess) e = shared ? unpad_rows(c, {v}) : unpad_rows(c, {v, q, k});
+    if (e == cudaSuccess && shared) e = reduce_heads(t, (const float *)(ws + L.pdq), dq);
+    if (e == cudaSuccess && shared) e = reduce_heads(t, (const float *)(ws + L.pdk), dk);
+    return status_of(e);
+  }
   if (L.on_tc && !(((uintptr_t)dO | (uintptr_t)dv | (uintptr_t)hq | (uintptr_t)hk) & 15)) {
     e = tc_bwd(c, dO, dht, hq, hk, shared, dv, dg, dbeta, dh0, ws + L.tc);
   } else {

@@ -19,6 +19,8 @@
 // the tokens s < t left in S1, and e^{G_C} <S0, dS1>.
 #pragma once
 
+#include <initializer_list>
+
 #include "internal.cuh"
 
 namespace glacore {
@@ -31,6 +33,7 @@ struct Call {
   Docs docs;         // tables for chunks of C tokens
   int64_t slots;     // chunk slots (of all documents)
   int dtype;
+  int64_t sK, sV;     // K and V of the states (p.K and p.V may be those of padded copies)
   const float *beta;  // [BT, H]
   cudaStream_t st;
 };
@@ -76,11 +79,22 @@ cudaError_t simt_scans(const Call &c, const void *dO, const float *dht, void *dv
 // summed by reduce_heads), [BT, H, K] dtype otherwise.
 cudaError_t simt_grads(const Call &c, const void *dO, const Saved &saved, void *dq, void *dk, bool per_head, float *dg,
                        float *dbeta);
-// out [BT, Hqk, K] dtype = sums of x [BT, H, K] fp32 over the heads of a group.
+// out [BT, Hqk, sK] dtype = sums of x [BT, H, p.K] fp32 over the heads of a group.
 cudaError_t reduce_heads(const Call &c, const float *x, void *out);
+// bf16 rows of D channels, `heads` to a token, `stride` values from token to
+// token, copied to dense rows of Dp (a multiple of 8; the rest 0), and back.
+struct Rows {
+  const void *src;
+  void *dst;
+  int64_t stride;
+  int heads, D, Dp;
+};
+cudaError_t pad_rows(const Call &c, std::initializer_list<Rows> tensors);
+cudaError_t unpad_rows(const Call &c, std::initializer_list<Rows> tensors);
 
 // ---- tensor-core kernels (delta_tc.cu): bf16, K and V multiples of 8 up to 128 ----
 bool tc_supported(const glacore_problem *p);  // sizes, strides and addresses of q, k, v
+bool tc_padded(const glacore_problem *p);     // not so, but dense copies of q, k, v with padded rows are
 size_t tc_workspace(int64_t docs, int64_t slots, int64_t H, bool backward);
 cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws);
 // dq and dk as in simt_grads

@@ -1,5 +1,7 @@
 // delta_simt.cu -- the gated delta rule on the CUDA cores, in fp32, for any
-// K and V up to 256 and both types (formulas in delta.cuh).
+// K and V up to 256 and both types (formulas in delta.cuh); sums over the heads
+// of a group, and the copies with padded rows that odd bf16 sizes go to the tensor
+// cores as.
 //
 // The forward and the two passes of the backward that carry a state run token
 // by token: a state's value columns do not see each other, so a warp owns 8
@@ -678,13 +680,58 @@ cudaError_t grads_as(const Call &c, const void *dO, const Saved &saved, void *dq
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) reduce_heads_kernel(const float *x, T *out, int64_t n, int64_t K, int share) {
+__global__ void __launch_bounds__(256) reduce_heads_kernel(const float *x, T *out, int64_t n, int64_t K, int64_t pitch,
+                                                           int share) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-    const float *src = x + (i / K) * share * K + i % K;
+    const float *src = x + (i / K) * share * pitch + i % K;
     float s = 0.f;
-    for (int e = 0; e < share; ++e) s += src[e * K];
+    for (int e = 0; e < share; ++e) s += src[e * pitch];
     out[i] = from_f32<T>(s);
   }
+}
+
+struct RowsArgs {
+  Rows t[4];
+  int64_t BT;
+};
+// Eight channels of a row to a thread; a tensor to blockIdx.y.
+template <bool BACK>
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ RowsArgs a) {
+  const Rows r = a.t[blockIdx.y];
+  const int per = r.Dp / 8;
+  const int64_t n = a.BT * r.heads * per;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / per, t = row / r.heads;
+    const int c = (int)(i % per) * 8;
+    uint16_t x[8];
+    if (BACK) {
+      *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>((const uint16_t *)r.src + row * r.Dp + c);
+      uint16_t *dst = (uint16_t *)r.dst + row * r.D + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (c + e < r.D) dst[e] = x[e];
+    } else {
+      const uint16_t *src = (const uint16_t *)r.src + t * r.stride + (row - t * r.heads) * r.D + c;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = c + e < r.D ? src[e] : (uint16_t)0;
+      *reinterpret_cast<uint4 *>((uint16_t *)r.dst + row * r.Dp + c) = *reinterpret_cast<const uint4 *>(x);
+    }
+  }
+}
+template <bool BACK>
+cudaError_t copy_rows(const Call &c, std::initializer_list<Rows> tensors, const char *label) {
+  RowsArgs a;
+  int64_t most = 0;
+  int n = 0;
+  a.BT = c.p.BT;
+  for (const Rows &r : tensors) {
+    a.t[n++] = r;
+    most = std::max(most, a.BT * r.heads * (r.Dp / 8));
+  }
+  const dim3 grid((unsigned)std::min<int64_t>((most + 255) / 256, 152 * 8), n);
+  rows_kernel<BACK><<<grid, 256, 0, c.st>>>(a);
+  mark_launch(label, c.st);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -704,14 +751,20 @@ cudaError_t simt_grads(const Call &c, const void *dO, const Saved &saved, void *
                                  : grads_as<float>(c, dO, saved, dq, dk, per_head, dg, dbeta);
 }
 
+cudaError_t pad_rows(const Call &c, std::initializer_list<Rows> tensors) {
+  return copy_rows<false>(c, tensors, "delta_pad");
+}
+cudaError_t unpad_rows(const Call &c, std::initializer_list<Rows> tensors) {
+  return copy_rows<true>(c, tensors, "delta_unpad");
+}
 cudaError_t reduce_heads(const Call &c, const float *x, void *out) {
-  const int64_t n = c.p.BT * c.p.Hqk * c.p.K;
+  const int64_t n = c.p.BT * c.p.Hqk * c.sK;
   const int blocks = (int)std::min<int64_t>((n + 255) / 256, 152 * 16);
   const int share = (int)(c.p.H / c.p.Hqk);
   if (c.dtype == GLACORE_BF16)
-    reduce_heads_kernel<<<blocks, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, n, c.p.K, share);
+    reduce_heads_kernel<<<blocks, 256, 0, c.st>>>(x, (__nv_bfloat16 *)out, n, c.sK, c.p.K, share);
   else
-    reduce_heads_kernel<<<blocks, 256, 0, c.st>>>(x, (float *)out, n, c.p.K, share);
+    reduce_heads_kernel<<<blocks, 256, 0, c.st>>>(x, (float *)out, n, c.sK, c.p.K, share);
   mark_launch("delta_reduce_heads", c.st);
   return cudaGetLastError();
 }

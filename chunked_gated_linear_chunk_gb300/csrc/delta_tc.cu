@@ -490,7 +490,7 @@ struct ChainMaps {
 struct ChainArgs {
   Docs docs;
   const int32_t *order;  // documents, longest first, or null
-  int H, share, K, V;
+  int H, share, V, sK, sV;  // V of o and dv; K and V of the states
   float scale;
   const float *h0;
   float *ht;
@@ -745,12 +745,12 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
     more_registers<88>();
     const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;  // this warp's lanes of tensor memory
-    const bool in = v < a.V;
+    const bool in = v < a.sV;
     float S[32];
     {
-      const int64_t at = ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+      const int64_t at = ((d * a.H + h) * a.sK + 32 * grp) * (int64_t)a.sV + v;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) S[i] = a.h0 && in && 32 * grp + i < a.K ? a.h0[at + (int64_t)i * a.V] : 0.f;
+      for (int i = 0; i < 32; ++i) S[i] = a.h0 && in && 32 * grp + i < a.sK ? a.h0[at + (int64_t)i * a.sV] : 0.f;
     }
     // Rows past the document's end hold other tokens: as zeros, nothing in them reaches a sum.
     auto clear_rows = [&](int j) -> bool {
@@ -880,10 +880,10 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
     }
     if (!ok) atomicExch(&abort_flag, 1);
     if (a.ht && in && ok) {
-      float *dst = a.ht + ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+      float *dst = a.ht + ((d * a.H + h) * a.sK + 32 * grp) * (int64_t)a.sV + v;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
+        if (32 * grp + i < a.sK) dst[(int64_t)i * a.sV] = S[i];
     }
   } else {
     fewer_registers<64>();
@@ -966,7 +966,7 @@ struct BackMaps {
 struct BackArgs {
   Docs docs;
   const int32_t *order;
-  int H, share, K, V;
+  int H, share, V, sK, sV;  // V of o and dv; K and V of the states
   float scale;
   const float *dht;
   float *dh0;
@@ -1131,12 +1131,12 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
     more_registers<88>();
     const int grp = warp >> 2, qw = warp & 3, v = qw * 32 + lane;
     const uint32_t lanes = (uint32_t)(qw * 32) << 16;
-    const bool in = v < a.V;
+    const bool in = v < a.sV;
     float S[32];
     {
-      const int64_t at = ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+      const int64_t at = ((d * a.H + h) * a.sK + 32 * grp) * (int64_t)a.sV + v;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) S[i] = a.dht && in && 32 * grp + i < a.K ? a.dht[at + (int64_t)i * a.V] : 0.f;
+      for (int i = 0; i < 32; ++i) S[i] = a.dht && in && 32 * grp + i < a.sK ? a.dht[at + (int64_t)i * a.sV] : 0.f;
     }
     auto clear_rows = [&](int i) -> bool {
       const int L = chunk_len(i);
@@ -1252,10 +1252,10 @@ __device__ __forceinline__ void back_walk(const BackMaps &maps, const BackArgs &
     }
     if (!ok) atomicExch(&abort_flag, 1);
     if (a.dh0 && in && ok) {
-      float *dst = a.dh0 + ((d * a.H + h) * a.K + 32 * grp) * (int64_t)a.V + v;
+      float *dst = a.dh0 + ((d * a.H + h) * a.sK + 32 * grp) * (int64_t)a.sV + v;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (32 * grp + i < a.K) dst[(int64_t)i * a.V] = S[i];
+        if (32 * grp + i < a.sK) dst[(int64_t)i * a.sV] = S[i];
     }
   } else {
     fewer_registers<64>();
@@ -1952,6 +1952,10 @@ bool tc_supported(const glacore_problem *p) {
          p->q_stride % 8 == 0 && p->k_stride % 8 == 0 && p->v_stride % 8 == 0 && p->B * p->T < ((int64_t)1 << 31) - CH &&
          !(((uintptr_t)p->q | (uintptr_t)p->k | (uintptr_t)p->v) & 15);
 }
+bool tc_padded(const glacore_problem *p) {
+  return p->dtype == GLACORE_BF16 && p->K <= D128 && p->V <= D128 && p->B * p->T < ((int64_t)1 << 31) - CH &&
+         !tc_supported(p);
+}
 
 // Scratch (byte offsets): tiles and gates of every chunk and head, the backward's images.
 namespace {
@@ -2076,8 +2080,9 @@ ChainArgs chain_args(const Call &c, char *ws, const TcLayout &l) {
   a.docs = c.docs;
   a.H = (int)c.p.H;
   a.share = (int)(c.p.H / c.p.Hqk);
-  a.K = (int)c.p.K;
   a.V = (int)c.p.V;
+  a.sK = (int)c.sK;
+  a.sV = (int)c.sV;
   a.scale = c.p.scale;
   a.h0 = c.p.h0;
   a.tiles = ws + l.tiles;
@@ -2139,8 +2144,9 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   b.order = order;
   b.H = a.H;
   b.share = a.share;
-  b.K = a.K;
   b.V = a.V;
+  b.sK = a.sK;
+  b.sV = a.sV;
   b.scale = a.scale;
   b.dht = dht;
   b.dh0 = dh0;
@@ -2158,7 +2164,7 @@ cudaError_t tc_bwd(const Call &c, const void *dO, const float *dht, void *dq, vo
   g.docs = a.docs;
   g.H = a.H;
   g.share = a.share;
-  g.K = a.K;
+  g.K = (int)c.p.K;
   g.scale = a.scale;
   g.g = c.p.g;
   g.beta = c.beta;

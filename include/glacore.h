@@ -219,18 +219,20 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  *   o, final_state, do_, dht, dq, dk, dv, dg, dh0   as in ssd_fwd / ssd_bwd
  *   dbeta        [B,T,H] fp32, written
  * Any decay is exact (g below -10^4 counts as -10^4: e^g is 0 either way).
- * No alignment but the elements' own is asked for.  bf16 with K and V multiples
- * of 8 up to 128 runs on the tensor cores where q, k, v, o, do_, dq, dk and dv
- * are 16-byte aligned and the token strides multiples of 8 (and, forwards, rows
- * are not so short that token by token is faster); everything else on the CUDA
- * cores in fp32.  On the tensor cores whatever is computed enters products in two
+ * No alignment but the elements' own is asked for.  bf16 with K and V up to
+ * 128 runs on the tensor cores (forwards, where rows are not so short that token
+ * by token is faster): in place where K and V are multiples of 8, q, k, v, o,
+ * do_, dq, dk and dv 16-byte aligned and the token strides multiples of 8, on padded
+ * copies in the workspace where K, V, q, k, v or their strides are not so;
+ * everything else on the CUDA cores in fp32.  On the tensor cores whatever is computed enters products in two
  * bf16 parts: fp32 outputs (states, dg, dbeta) are off by about 5e-6 of their size,
  * bf16 ones by their own rounding.  Results do not depend on the order in which
  * CTAs run.
  * Workspace, per 64 tokens and head: forward 41 KB; backward 233 KB (the state
  * before them and its gradient behind them in 64 KB each, and what their tokens
- * left in 64 KB), on the CUDA cores 8 K V bytes and 8 V per token; and 8 K
- * per token and head where heads share q and k. */
+ * left in 64 KB), on the CUDA cores 8 K V bytes and 8 V per token; 8 K
+ * per token and head where heads share q and k; and the padded copies, 2 bytes a
+ * value of q, k, v and o, backwards also of the gradients. */
 size_t delta_fwd_workspace_size(const glacore_problem *p);
 size_t delta_bwd_workspace_size(const glacore_problem *p);
 glacore_status delta_fwd(const glacore_problem *p, const float *beta, void *o,

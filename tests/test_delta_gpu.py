@@ -9,6 +9,7 @@ a chunk is off by decays with its state; on the CUDA cores 4 roundings of
 (a query's, a key's and the states'), up to four times the size of what is
 left: 4 TOL."""
 import ctypes
+import math
 
 import numpy as np
 import pytest
@@ -410,7 +411,7 @@ def test_no_tokens_and_refusals(cuda_ok):
 @pytest.mark.parametrize("B,T,H,Hqk,V,docs", [(4, 2048, 16, 16, 128, 1), (1, 8192, 16, 8, 128, 9), (2, 3001, 16, 4, 64, 5)])
 def test_many_chunks_against_the_other_kernels(cuda_ok, B, T, H, Hqk, V, docs):
     """Dozens of chunks on every SM at once: the tensor-core kernels, ten times the same bits, against the token by
-    token ones (which take operands at odd addresses).  Both are within half an ulp and TOL of the same values."""
+    token ones (which take outputs at odd addresses).  Both are within half an ulp and TOL of the same values."""
     gen = torch.Generator("cuda")
     gen.manual_seed(B + T)
     r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
@@ -425,17 +426,18 @@ def test_many_chunks_against_the_other_kernels(cuda_ok, B, T, H, Hqk, V, docs):
         seg = seg.cumsum(1).to(torch.int32)
 
     def odd(t):
-        x = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
-        return x.copy_(t)
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
 
-    def call(q):
-        o, ht = glc.delta_fwd(q, k, v, g, b, segment_ids=seg, output_final_state=True, n_seqs=B * docs, poison=True)
-        return (o, ht, *glc.delta_bwd(q, k, v, g, b, do, segment_ids=seg, n_seqs=B * docs, poison=True)[:5])
+    def call(at_odd=False):
+        outs = (*(odd(t) for t in (q, k, v, g, b)), None) if at_odd else None
+        o, ht = glc.delta_fwd(q, k, v, g, b, segment_ids=seg, output_final_state=True, n_seqs=B * docs, poison=True,
+                              out=odd(v) if at_odd else None)
+        return (o, ht, *glc.delta_bwd(q, k, v, g, b, do, segment_ids=seg, n_seqs=B * docs, poison=True, outs=outs)[:5])
 
-    want = call(odd(q))
-    first = call(q)
+    want = call(at_odd=True)
+    first = call()
     for _ in range(9):
-        assert all(torch.equal(x, y) for x, y in zip(first, call(q)))
+        assert all(torch.equal(x, y) for x, y in zip(first, call()))
     for name, x, y in zip(("o", "ht", *NAMES), first, want):
         x, y = x.double(), y.double()
         bound = 2 * (4 if name == "dg" else 1) * TOL * y.abs().max() + (2 * ULP[BF] * y.abs() if first[0].dtype == BF else 0)
@@ -476,4 +478,42 @@ def test_tiles_made_while_the_chains_walk(cuda_ok, B, T, H, Hqk, K, V, kw):
             other = run()
         torch.cuda.synchronize()
         assert same(held) and same(other)
+    glc.get_device_error()
+
+
+@pytest.mark.parametrize("B,T,H,Hqk,K,V,kw", [
+    (1, 333, 6, 2, 72, 41, {"docs": 4}), (2, 150, 4, 4, 125, 77, {"states": True}), (1, 200, 3, 3, 9, 127, {"fused": True}),
+    (2, 130, 4, 1, 128, 128, {"odd": True, "states": True}), (2, 700, 32, 32, 101, 128, {})])
+def test_sizes_strides_and_addresses_that_take_padded_copies(cuda_ok, B, T, H, Hqk, K, V, kw):
+    """Forwards and backwards on the tensor cores, whatever divides the operands: states, gradients and outputs of their own
+    sizes, nothing past them written."""
+    kw = dict(kw)
+    at_odd = kw.pop("odd", False)
+    x, dev, host, call, dht = make(B, T, H, Hqk, K, V, BF, 23, **kw)
+    if at_odd:
+        for n in "qkv":
+            y = torch.empty(dev[n].numel() + 1, dtype=BF, device="cuda")[1:].view(dev[n].shape)
+            dev[n] = y.copy_(dev[n])
+    args = [dev[n] for n in ("q", "k", "v", "g", "beta")]
+    shapes = ((B, T, Hqk, K), (B, T, Hqk, K), (B, T, H, V), (B, T, H), (B, T, H), (host["n"], H, K, V))
+    guard = 512
+    bufs = [torch.full((math.prod(s) + guard,), 77.0, dtype=t, device="cuda")
+            for s, t in zip(shapes, (BF, BF, BF, F32, F32, F32))]
+    outs = [b_[:b_.numel() - guard].view(s) for b_, s in zip(bufs, shapes)]
+    if not kw.get("states"):
+        outs[5] = None
+    o_buf = torch.full((B * T * H * V + guard,), 77.0, dtype=BF, device="cuda")
+    with glc.LaunchTimer(12) as t:
+        o, last = glc.delta_fwd(*args, output_final_state=True, out=o_buf[:-guard].view(B, T, H, V), **call)
+    assert "delta_pad" in t.labels and t.labels[-1] == "delta_unpad"
+    with glc.LaunchTimer(12) as t:
+        got = glc.delta_bwd(*args, dev["do"], dht=dht, outs=outs, **call)
+    assert "delta_pad" in t.labels
+    h = [x[n] for n in ("q", "k", "v", "g", "beta")]
+    want, state = delta.fwd(*h, K ** -0.5, host["seg"], host["h0"])
+    assert close(o, want) and close(last, state)
+    ref = delta.bwd(*h, x["do"], K ** -0.5, host["seg"], host["h0"], host["dht"])
+    for name, a in zip(NAMES, got):
+        assert a is None or close(a, ref[name], 4 * TOL if name == "dg" else TOL), name
+    assert all(torch.all(b_[-guard:] == 77.0) for b_ in (*bufs, o_buf))
     glc.get_device_error()
