@@ -26,16 +26,28 @@ namespace {
 
 constexpr int LK = 8;          // lanes along the key rows
 constexpr int TT = 16;         // tokens staged at once
-constexpr int COLS = 32;       // value columns of a block (4 warps x 8)
-constexpr int THREADS = 256;   // 4 warps that compute, 4 that stage
+constexpr int COLS = 32;       // value columns of a block
+constexpr int STAGERS = 4;     // warps that stage, behind those that compute
+constexpr int NC = 2;          // columns of a thread (1 or 4: 10 to 25% more time where tokens are in sequence)
+constexpr int CW = COLS / (4 * NC), THREADS = 32 * (CW + STAGERS);  // warps that compute; threads
 
-// Two columns at a time, as single operations: the packed ones take two cycles
-// each and want the key's channel twice in a register pair.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+// A thread's columns, one operation each (packed pairs take two cycles
+// and want the key's channel twice in a register pair).
+struct Cols {
+  float v[NC];
+};
+__device__ __forceinline__ Cols fma_cols(float a, const Cols &b, const Cols &c) {
+  Cols r;
+#pragma unroll
+  for (int n = 0; n < NC; ++n) r.v[n] = fmaf(a, b.v[n], c.v[n]);
+  return r;
 }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Cols mul_cols(float a, const Cols &b) {
+  Cols r;
+#pragma unroll
+  for (int n = 0; n < NC; ++n) r.v[n] = a * b.v[n];
+  return r;
+}
 
 enum Mode { FWD, STATES, BACK };
 
@@ -76,7 +88,7 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
   const int64_t n = s1 - s0;
   const int ntile = (int)((n + TT - 1) / TT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool stages = warp >= 4;
+  const bool stages = warp >= CW;
   const int64_t slot0 = a.docs.chunk_base(d);
 
   // tile i of the pass covers the tokens tile_of(i) * TT ... of the document
@@ -86,11 +98,11 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
     const int64_t t0 = (int64_t)tile_of(i) * TT;
     const int len = (int)min((int64_t)TT, n - t0);
     // a warp's four tokens at once: their loads are all in flight before the first is used
-    constexpr int N = TT / 4;
+    constexpr int N = TT / STAGERS;
     float kx[N][KP / 32], qx[N][KP / 32], vx[N], gx[N], bx[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = warp - 4 + 4 * n;
+      const int r = warp - CW + STAGERS * n;
       const int64_t tok = s0 + t0 + (r < len ? r : 0);
       const T *qr = a.q + tok * a.qs + (int64_t)hq * a.K, *kr = a.k + tok * a.ks + (int64_t)hq * a.K;
 #pragma unroll
@@ -105,7 +117,7 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = warp - 4 + 4 * n;
+      const int r = warp - CW + STAGERS * n;
       float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < KP / 32; ++e) {
@@ -125,30 +137,30 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
     }
   };
 
-  // thread (lk, c): rows 4 lk + 32 i + 0..3 of columns v0 + 8 warp + 2 c + 0..1
-  const int lk = lane & 7, cl = (warp & 3) * 8 + 2 * (lane >> 3), col = v0 + cl;
-  const bool in0 = col < a.V, in1 = col + 1 < a.V;
-  float2 S[KR];
+  // thread (lk, c): rows 4 lk + 32 i + 0..3 of columns v0 + 4 NC warp + NC c ...
+  const int lk = lane & 7, cl = (warp % CW) * 4 * NC + NC * (lane >> 3), col = v0 + cl;
+  bool in[NC];
+#pragma unroll
+  for (int n = 0; n < NC; ++n) in[n] = col + n < a.V;
+  Cols S[KR];
   const int64_t mat = (d * a.H + h) * a.K * a.V;
   auto put_state = [&](float *dst) {
 #pragma unroll
     for (int j = 0; j < KR; ++j) {
       const int row = 4 * lk + 32 * (j >> 2) + (j & 3);
-      if (row < a.K) {
-        if (in0) dst[(int64_t)row * a.V + col] = S[j].x;
-        if (in1) dst[(int64_t)row * a.V + col + 1] = S[j].y;
-      }
+      if (row < a.K)
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+          if (in[n]) dst[(int64_t)row * a.V + col + n] = S[j].v[n];
     }
   };
   if (!stages) {
 #pragma unroll
     for (int j = 0; j < KR; ++j) {
       const int row = 4 * lk + 32 * (j >> 2) + (j & 3);
-      S[j] = both(0.f);
-      if (a.seed && row < a.K) {
-        if (in0) S[j].x = a.seed[mat + (int64_t)row * a.V + col];
-        if (in1) S[j].y = a.seed[mat + (int64_t)row * a.V + col + 1];
-      }
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        S[j].v[n] = a.seed && row < a.K && in[n] ? a.seed[mat + (int64_t)row * a.V + col + n] : 0.f;
     }
   } else if (ntile > 0) {
     stage(0);
@@ -168,7 +180,7 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
       const int64_t at0 = ((s0 + t0) * a.H + h) * a.V + col, step = (int64_t)a.H * a.V;
       for (int rr = 0; rr < len; ++rr) {
         const int r = MODE == BACK ? len - 1 - rr : rr;
-        float2 xk = both(0.f), xq = both(0.f);
+        Cols xk = {}, xq = {}, xk2 = {};
         float4 kv[KR / 4], qv[KR / 4];
 #pragma unroll
         for (int j = 0; j < KR / 4; ++j) {
@@ -176,55 +188,53 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
           if (NEEDQ) qv[j] = *reinterpret_cast<const float4 *>(&t.q[r][4 * lk + 32 * j]);
         }
         const float *kp = reinterpret_cast<const float *>(kv), *qp = reinterpret_cast<const float *>(qv);
-        float2 xk2 = both(0.f);
 #pragma unroll
         for (int j = 0; j < KR; j += 2) {
-          xk = fma2(both(kp[j]), S[j], xk);
-          xk2 = fma2(both(kp[j + 1]), S[j + 1], xk2);
+          xk = fma_cols(kp[j], S[j], xk);
+          xk2 = fma_cols(kp[j + 1], S[j + 1], xk2);
         }
-        xk.x += xk2.x;
-        xk.y += xk2.y;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) xk.v[n] += xk2.v[n];
         if (MODE == FWD) {
 #pragma unroll
-          for (int j = 0; j < KR; ++j) xq = fma2(both(qp[j]), S[j], xq);
+          for (int j = 0; j < KR; ++j) xq = fma_cols(qp[j], S[j], xq);
         }
 #pragma unroll
-        for (int o = 1; o < LK; o <<= 1) {
-          xk.x += __shfl_xor_sync(0xffffffffu, xk.x, o);
-          xk.y += __shfl_xor_sync(0xffffffffu, xk.y, o);
-          if (MODE == FWD) {
-            xq.x += __shfl_xor_sync(0xffffffffu, xq.x, o);
-            xq.y += __shfl_xor_sync(0xffffffffu, xq.y, o);
+        for (int o = 1; o < LK; o <<= 1)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            xk.v[n] += __shfl_xor_sync(0xffffffffu, xk.v[n], o);
+            if (MODE == FWD) xq.v[n] += __shfl_xor_sync(0xffffffffu, xq.v[n], o);
           }
-        }
-        const float2 v = *reinterpret_cast<const float2 *>(&t.v[r][cl]);
+        Cols v;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) v.v[n] = t.v[r][cl + n];
         const float dec = t.a[r], b = t.b[r];
         const int64_t at = at0 + r * step;
         if (MODE != BACK) {
-          const float2 e = make_float2(v.x - dec * xk.x, v.y - dec * xk.y);
-          const float2 u = make_float2(b * e.x, b * e.y);
+          const Cols e = fma_cols(-dec, xk, v), u = mul_cols(b, e);
 #pragma unroll
-          for (int j = 0; j < KR; ++j) S[j] = fma2(both(kp[j]), u, mul2(both(dec), S[j]));
+          for (int j = 0; j < KR; ++j) S[j] = fma_cols(kp[j], u, mul_cols(dec, S[j]));
           if (MODE == FWD) {
             if (a.out && lk == 0) {
-              const float qk = t.qk[r];
-              if (in0) a.out[at] = from_f32<T>(a.scale * fmaf(qk, u.x, dec * xq.x));
-              if (in1) a.out[at + 1] = from_f32<T>(a.scale * fmaf(qk, u.y, dec * xq.y));
+              const Cols y = fma_cols(t.qk[r], u, mul_cols(dec, xq));
+#pragma unroll
+              for (int n = 0; n < NC; ++n)
+                if (in[n]) a.out[at + n] = from_f32<T>(a.scale * y.v[n]);
             }
           } else if (lk == 0) {
-            if (in0) a.rows[at] = e.x;
-            if (in1) a.rows[at + 1] = e.y;
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              if (in[n]) a.rows[at + n] = e.v[n];
           }
         } else {
-          const float sqk = a.scale * t.qk[r];
-          const float2 du = make_float2(fmaf(sqk, v.x, xk.x), fmaf(sqk, v.y, xk.y));
-          const float2 dy = make_float2(b * du.x, b * du.y), w = make_float2(a.scale * v.x, a.scale * v.y);
+          const Cols du = fma_cols(a.scale * t.qk[r], v, xk), dy = mul_cols(b, du), w = mul_cols(a.scale, v);
 #pragma unroll
-          for (int j = 0; j < KR; ++j)
-            S[j] = mul2(both(dec), fma2(both(-kp[j]), dy, fma2(both(qp[j]), w, S[j])));
+          for (int j = 0; j < KR; ++j) S[j] = mul_cols(dec, fma_cols(-kp[j], dy, fma_cols(qp[j], w, S[j])));
           if (lk == 0) {
-            if (in0) a.rows[at] = du.x, a.out[at] = from_f32<T>(dy.x);
-            if (in1) a.rows[at + 1] = du.y, a.out[at + 1] = from_f32<T>(dy.y);
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              if (in[n]) a.rows[at + n] = du.v[n], a.out[at + n] = from_f32<T>(dy.v[n]);
           }
         }
       }
@@ -280,6 +290,7 @@ template <template <int> class Kernel, typename F>
 cudaError_t by_rows(int64_t K, F go) {
   if (K <= 32) return go(Kernel<4>::get(), 2 * sizeof(Tile<4>));
   if (K <= 64) return go(Kernel<8>::get(), 2 * sizeof(Tile<8>));
+  if (K <= 96) return go(Kernel<12>::get(), 2 * sizeof(Tile<12>));
   if (K <= 128) return go(Kernel<16>::get(), 2 * sizeof(Tile<16>));
   return go(Kernel<32>::get(), 2 * sizeof(Tile<32>));
 }
