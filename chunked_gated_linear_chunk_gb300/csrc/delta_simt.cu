@@ -9,15 +9,18 @@
 // registers, and one exchange
 // over the 8 lanes of a column pair gives S^T k and S^T q of a token at once:
 //     o_t = scale (e^g S^T q + (q . k) u),  u = b (v - e^g S^T k)
-// (both on the state before the token).  The other half of the block's warps
-// converts the next 16 tokens' q, k, v into shared memory meanwhile.  Bound by
-// the latency of that dependence, 0.26 us a token; any decay is exact here.  The
-// gradients of q, k, g and beta then take every chunk of 64 tokens
-// by itself (simt_grads), as products of 64 x 64 tiles.  333 tokens of 3 x 6 heads
-// of 72 x 41, fp32: passes 100 us (both in one launch), gradients 48 us.
+// (both on the state before the token).  fp32 and backwards two tokens at a time
+// read the same state, the second corrected by k_1 . k_2 and k_1 . q_2, so that they
+// share that exchange.  The other half of the block's warps converts the next 16
+// tokens' q, k, v into shared memory meanwhile.  Bound by the latency of that
+// dependence: 0.21 us a token in fp32, 0.26 one by one; any decay is exact here.  The
+// gradients of q, k, g and beta then take every chunk of 64 tokens by itself
+// (simt_grads), as products of 64 x 64 tiles.  333 tokens of 3 x 6 heads of 72 x 41,
+// fp32: passes 70 us (both in one launch; token by token 85), gradients 48 us.
 #include <algorithm>
 
 #include "delta.cuh"
+#include "tc.cuh"
 
 namespace glacore {
 namespace delta {
@@ -70,6 +73,7 @@ struct alignas(16) Tile {
   float q[TT][LK * KR], k[TT][LK * KR];
   float v[TT][COLS];
   float a[TT], b[TT], qk[TT];
+  float kk[TT], kq[TT];  // of odd tokens: k of the token before with k and q
 };
 
 template <typename T, int KR, int MODE>
@@ -78,6 +82,7 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
   Tile<KR> *tiles = reinterpret_cast<Tile<KR> *>(smem);  // two
   constexpr int KP = LK * KR;
   constexpr bool NEEDQ = MODE != STATES;
+  constexpr bool TWO = KR <= 16 && !(MODE == FWD && sizeof(T) == 2);  // two tokens at a time
   const int slice = (int)(block % a.slices);
   const uint32_t dh = block / a.slices;
   const int h = (int)(dh % a.H);
@@ -102,7 +107,7 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
     float kx[N][KP / 32], qx[N][KP / 32], vx[N], gx[N], bx[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = warp - CW + STAGERS * n;
+      const int r = (warp - CW) * N + n;
       const int64_t tok = s0 + t0 + (r < len ? r : 0);
       const T *qr = a.q + tok * a.qs + (int64_t)hq * a.K, *kr = a.k + tok * a.ks + (int64_t)hq * a.K;
 #pragma unroll
@@ -117,22 +122,30 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int r = warp - CW + STAGERS * n;
-      float dot = 0.f;
+      const int r = (warp - CW) * N + n;
+      const bool odd = n & 1;
+      float dot = 0.f, kk = 0.f, kq = 0.f;
 #pragma unroll
       for (int e = 0; e < KP / 32; ++e) {
         t.k[r][lane + 32 * e] = kx[n][e];
         if (NEEDQ) t.q[r][lane + 32 * e] = qx[n][e];
         dot = fmaf(kx[n][e], qx[n][e], dot);
+        if (TWO && odd) kk = fmaf(kx[n - 1][e], kx[n][e], kk);
+        if (TWO && odd) kq = fmaf(kx[n - 1][e], qx[n][e], kq);
       }
       t.v[r][lane] = vx[n];
-      if (NEEDQ)
 #pragma unroll
-        for (int o = 16; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+      for (int o = 16; o; o >>= 1) {
+        if (NEEDQ) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        if (TWO && odd) kk += __shfl_xor_sync(0xffffffffu, kk, o);
+        if (TWO && odd && NEEDQ) kq += __shfl_xor_sync(0xffffffffu, kq, o);
+      }
       if (lane == 0) {
         t.a[r] = expf(gx[n]);
         t.b[r] = bx[n];
         t.qk[r] = dot;
+        if (odd) t.kk[r] = kk;
+        if (odd) t.kq[r] = kq;
       }
     }
   };
@@ -178,8 +191,7 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
       if (MODE == BACK && ((t0 + TT) % C == 0 || i == 0))
         put_state(a.states + ((slot0 + t0 / C) * a.H + h) * a.K * a.V);
       const int64_t at0 = ((s0 + t0) * a.H + h) * a.V + col, step = (int64_t)a.H * a.V;
-      for (int rr = 0; rr < len; ++rr) {
-        const int r = MODE == BACK ? len - 1 - rr : rr;
+      auto token = [&](int r) {
         Cols xk = {}, xq = {}, xk2 = {};
         float4 kv[KR / 4], qv[KR / 4];
 #pragma unroll
@@ -237,6 +249,96 @@ __device__ __forceinline__ void scan(const ScanArgs<T> &a, uint32_t block) {
               if (in[n]) a.rows[at + n] = du.v[n], a.out[at + n] = from_f32<T>(dy.v[n]);
           }
         }
+      };
+      // tokens r and r + 1 (1 and 2): both read the state before, or the gradient behind, the two of them
+      auto two_tokens = [&](int r) {
+        float4 kv[2][KR / 4], qv[2][KR / 4];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < KR / 4; ++j) {
+            kv[m][j] = *reinterpret_cast<const float4 *>(&t.k[r + m][4 * lk + 32 * j]);
+            if (NEEDQ) qv[m][j] = *reinterpret_cast<const float4 *>(&t.q[r + m][4 * lk + 32 * j]);
+          }
+        const float *k1 = reinterpret_cast<const float *>(kv[0]), *k2 = reinterpret_cast<const float *>(kv[1]);
+        const float *q1 = reinterpret_cast<const float *>(qv[0]), *q2 = reinterpret_cast<const float *>(qv[1]);
+        Cols x1 = {}, x2 = {}, y1 = {}, y2 = {}, v1, v2;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) v1.v[n] = t.v[r][cl + n], v2.v[n] = t.v[r + 1][cl + n];
+        const float d1 = t.a[r], d2 = t.a[r + 1], b1 = t.b[r], b2 = t.b[r + 1], kk = t.kk[r + 1], kq = t.kq[r + 1];
+        const float over = d1 * d2;
+#pragma unroll
+        for (int j = 0; j < KR; ++j) {
+          x1 = fma_cols(k1[j], S[j], x1);
+          x2 = fma_cols(k2[j], S[j], x2);
+          if (MODE == FWD) {
+            y1 = fma_cols(q1[j], S[j], y1);
+            y2 = fma_cols(q2[j], S[j], y2);
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < LK; o <<= 1)
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            x1.v[n] += __shfl_xor_sync(0xffffffffu, x1.v[n], o);
+            x2.v[n] += __shfl_xor_sync(0xffffffffu, x2.v[n], o);
+            if (MODE == FWD) {
+              y1.v[n] += __shfl_xor_sync(0xffffffffu, y1.v[n], o);
+              y2.v[n] += __shfl_xor_sync(0xffffffffu, y2.v[n], o);
+            }
+          }
+        const int64_t at = at0 + r * step;
+        if (MODE != BACK) {
+          const Cols e1 = fma_cols(-d1, x1, v1), u1 = mul_cols(b1, e1);
+          const Cols e2 = fma_cols(-d2, fma_cols(kk, u1, mul_cols(d1, x2)), v2), u2 = mul_cols(b2, e2);
+          const Cols w1 = mul_cols(d2, u1);
+#pragma unroll
+          for (int j = 0; j < KR; ++j) S[j] = fma_cols(k2[j], u2, fma_cols(k1[j], w1, mul_cols(over, S[j])));
+          if (MODE == FWD) {
+            if (a.out && lk == 0) {
+              const Cols o1 = fma_cols(t.qk[r], u1, mul_cols(d1, y1));
+              const Cols o2 = fma_cols(t.qk[r + 1], u2, mul_cols(d2, fma_cols(kq, u1, mul_cols(d1, y2))));
+#pragma unroll
+              for (int n = 0; n < NC; ++n)
+                if (in[n]) {
+                  a.out[at + n] = from_f32<T>(a.scale * o1.v[n]);
+                  a.out[at + step + n] = from_f32<T>(a.scale * o2.v[n]);
+                }
+            }
+          } else if (lk == 0) {
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              if (in[n]) a.rows[at + n] = e1.v[n], a.rows[at + step + n] = e2.v[n];
+          }
+        } else {
+          const Cols w1 = mul_cols(a.scale, v1), w2 = mul_cols(a.scale, v2);
+          const Cols du2 = fma_cols(t.qk[r + 1], w2, x2), dy2 = mul_cols(b2, du2);
+          const Cols du1 = fma_cols(t.qk[r], w1, mul_cols(d2, fma_cols(-kk, dy2, fma_cols(kq, w2, x1))));
+          const Cols dy1 = mul_cols(b1, du1);
+          const Cols aq1 = mul_cols(d1, w1), ak1 = mul_cols(-d1, dy1), aq2 = mul_cols(over, w2), ak2 = mul_cols(-over, dy2);
+#pragma unroll
+          for (int j = 0; j < KR; ++j)
+            S[j] = fma_cols(k1[j], ak1, fma_cols(q1[j], aq1, fma_cols(k2[j], ak2, fma_cols(q2[j], aq2, mul_cols(over, S[j])))));
+          if (lk == 0) {
+#pragma unroll
+            for (int n = 0; n < NC; ++n)
+              if (in[n]) {
+                a.rows[at + n] = du1.v[n], a.out[at + n] = from_f32<T>(dy1.v[n]);
+                a.rows[at + step + n] = du2.v[n], a.out[at + step + n] = from_f32<T>(dy2.v[n]);
+              }
+          }
+        }
+      };
+      // The last token of an odd number by itself; past 128 key rows registers do not hold two tokens, and
+      // forwards the build for bf16 is slower with two (2048 tokens of 16 heads of 128 x 128: 659 instead of 523 us;
+      // fp32: 436 instead of 512).
+      const int even = TWO ? len & ~1 : 0;
+      if (MODE == BACK) {
+        for (int r = len - 1; r >= even; --r) token(r);
+        for (int r = even - 2; r >= 0; r -= 2) two_tokens(r);
+      } else {
+        for (int r = 0; r < even; r += 2) two_tokens(r);
+        for (int r = even; r < len; ++r) token(r);
       }
     }
     __syncthreads();
@@ -249,9 +351,11 @@ __global__ void __launch_bounds__(THREADS) scan_kernel(const ScanArgs<T> a) {
   scan<T, KR, FWD>(a, blockIdx.x);
 }
 // The backward's two passes do not need one another: the first half of the
-// blocks goes backwards in time, the second forwards.
-template <typename T, int KR>
-__global__ void __launch_bounds__(THREADS) scans_kernel(const ScanArgs<T> back, const ScanArgs<T> states, uint32_t half) {
+// blocks goes backwards in time, the second forwards.  Two blocks to an SM (EACH) cost 16 rows
+// some spills: with 128 key channels 128 blocks of 2048 tokens take 504 us (one) or 610,
+// 512 of 1024 tokens 838 or 715.
+template <typename T, int KR, int EACH>
+__global__ void __launch_bounds__(THREADS, EACH) scans_kernel(const ScanArgs<T> back, const ScanArgs<T> states, uint32_t half) {
   if (blockIdx.x < half)
     scan<T, KR, BACK>(back, blockIdx.x);
   else
@@ -285,18 +389,27 @@ ScanArgs<T> scan_args(const Call &c, const void *v, int64_t vs, const float *see
   return a;
 }
 
-// go(kernel, bytes of shared memory) with the kernel for K's rows
+// go(kernel, bytes of shared memory) with the kernel for K's rows; few: no more blocks than SMs
 template <template <int> class Kernel, typename F>
-cudaError_t by_rows(int64_t K, F go) {
-  if (K <= 32) return go(Kernel<4>::get(), 2 * sizeof(Tile<4>));
-  if (K <= 64) return go(Kernel<8>::get(), 2 * sizeof(Tile<8>));
-  if (K <= 96) return go(Kernel<12>::get(), 2 * sizeof(Tile<12>));
-  if (K <= 128) return go(Kernel<16>::get(), 2 * sizeof(Tile<16>));
-  return go(Kernel<32>::get(), 2 * sizeof(Tile<32>));
+cudaError_t by_rows(int64_t K, bool few, F go) {
+  if (K <= 32) return go(Kernel<4>::get(few), 2 * sizeof(Tile<4>));
+  if (K <= 64) return go(Kernel<8>::get(few), 2 * sizeof(Tile<8>));
+  if (K <= 96 && Kernel<12>::ROWS == 12) return go(Kernel<12>::get(few), 2 * sizeof(Tile<12>));
+  if (K <= 128) return go(Kernel<16>::get(few), 2 * sizeof(Tile<16>));
+  return go(Kernel<32>::get(few), 2 * sizeof(Tile<32>));
 }
 template <typename T> struct Scan {
-  template <int KR> struct One { static auto get() { return scan_kernel<T, KR>; } };
-  template <int KR> struct Two { static auto get() { return scans_kernel<T, KR>; } };
+  template <int KR> struct One {
+    enum { ROWS = KR == 12 && sizeof(T) == 4 ? 0 : KR };  // fp32, 333 tokens of 72 channels: 12 rows 99 us, 16 rows 76
+    static auto get(bool) { return scan_kernel<T, KR>; }
+  };
+  template <int KR> struct Two {
+    enum { ROWS = KR };
+    static auto get(bool few) {
+      if constexpr (KR == 16) return few ? scans_kernel<T, KR, 1> : scans_kernel<T, KR, 2>;
+      else return scans_kernel<T, KR, KR < 16 ? 2 : 1>;
+    }
+  };
 };
 
 template <typename T>
@@ -304,7 +417,7 @@ cudaError_t scan_fwd(const Call &c, void *o, float *ht) {
   const ScanArgs<T> a = scan_args<T>(c, c.p.v, c.p.vs, c.p.h0, ht, o, nullptr, nullptr);
   const int64_t ctas = c.docs.n * c.p.H * a.slices;
   if (ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = by_rows<Scan<T>::template One>(c.p.K, [&](auto kernel, size_t smem) -> cudaError_t {
+  const cudaError_t e = by_rows<Scan<T>::template One>(c.p.K, ctas <= tc::sm_count(), [&](auto kernel, size_t smem) -> cudaError_t {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)ctas, THREADS, smem, c.st>>>(a);
@@ -319,7 +432,7 @@ cudaError_t scans_bwd(const Call &c, const void *dO, const float *dht, void *dv,
   const ScanArgs<T> bk = scan_args<T>(c, dO, c.p.H * c.p.V, dht, dh0, dv, saved.ds1, saved.dr);
   const int64_t ctas = c.docs.n * c.p.H * st.slices;
   if (2 * ctas >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = by_rows<Scan<T>::template Two>(c.p.K, [&](auto kernel, size_t smem) -> cudaError_t {
+  const cudaError_t e = by_rows<Scan<T>::template Two>(c.p.K, 2 * ctas <= tc::sm_count(), [&](auto kernel, size_t smem) -> cudaError_t {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(2 * ctas), THREADS, smem, c.st>>>(bk, st, (uint32_t)ctas);
