@@ -232,7 +232,8 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  * before them and its gradient behind them in 64 KB each, and what their tokens
  * left in 64 KB), on the CUDA cores 8 K V bytes and 8 V per token; 8 K
  * per token and head where heads share q and k; and the padded copies, 2 bytes a
- * value of q, k, v and o, backwards also of the gradients. */
+ * value of q, k, v and o, backwards also of the gradients.  (The size goes by
+ * the problem's addresses and strides as well: ask with those of the call.) */
 size_t delta_fwd_workspace_size(const glacore_problem *p);
 size_t delta_bwd_workspace_size(const glacore_problem *p);
 glacore_status delta_fwd(const glacore_problem *p, const float *beta, void *o,
