@@ -22,6 +22,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.cuh"
 
@@ -120,8 +121,12 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 // The row of the tables of a token (-1: no rotation, recorded as an error).
+// x / y of values that nearly always fit in 32 bits
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+}
 __device__ __forceinline__ int64_t table_row(const Args &a, int64_t token) {
-  const int64_t p = a.pos ? (int64_t)a.pos[token] : token % a.T;
+  const int64_t p = a.pos ? (int64_t)a.pos[token] : token - quotient(token, a.T) * a.T;
   if (p >= 0 && p < a.P) return p;
   set_device_error(a.err, GLACORE_ERR_INDEX);
   return -1;
@@ -328,9 +333,9 @@ __global__ void __launch_bounds__(THREADS, 3) bwd_kernel(const Args a) {
 }
 
 // Rows of any D, R, stride and alignment: a warp per row, the row in shared memory.
-template <typename T, bool BWD>
+template <typename T, bool BWD, int E>
 __global__ void __launch_bounds__(THREADS) rows_kernel(const Args a) {
-  __shared__ float buf[WARPS][MAXD];
+  __shared__ float buf[WARPS][32 * E];
   extern __shared__ float sums[];  // BWD: [WARPS][2][D]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float inv = a.mean ? 1.f / (float)a.D : 1.f;
@@ -341,8 +346,8 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Args a) {
     __syncwarp();
   }
   for (int64_t unit = (int64_t)blockIdx.x * WARPS + warp; unit < a.tokens * heads; unit += (int64_t)gridDim.x * WARPS) {
-    const int64_t token = unit / heads;
-    int h = (int)(unit % heads);
+    const int64_t token = quotient(unit, heads);
+    int h = (int)(unit - token * heads);
     const int z = h >= a.H[0];
     if (z) h -= a.H[0];
     const T *x = (const T *)a.x[z] + token * a.xs[z] + (int64_t)h * a.D;
@@ -351,16 +356,17 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Args a) {
     int64_t p = -1;
     if (a.R) p = table_row(a, token);
     // channel c of a row in shared memory, rotated by dir
+    const float *cs = a.cs + (p < 0 ? 0 : p) * a.R, *sn = a.sn + (p < 0 ? 0 : p) * a.R;
     auto turned = [&](int c, float dir) -> float {
       if (p < 0 || c >= 2 * a.R) return row[c];
       const bool first = a.inter ? (c & 1) == 0 : c < a.R;
       const int i = a.inter ? c / 2 : (first ? c : c - a.R), o = a.inter ? c ^ 1 : (first ? c + a.R : c - a.R);
-      const float s = dir * __ldg(a.sn + p * a.R + i);
-      return fmaf(first ? -s : s, row[o], __ldg(a.cs + p * a.R + i) * row[c]);
+      const float s = dir * __ldg(sn + i);
+      return fmaf(first ? -s : s, row[o], __ldg(cs + i) * row[c]);
     };
-    float f[MAXD / 32], d[MAXD / 32], ss = 0.f, sa = 0.f;
+    float f[E], d[E], ss = 0.f, sa = 0.f;
 #pragma unroll
-    for (int e = 0; e < MAXD / 32; ++e) {
+    for (int e = 0; e < E; ++e) {
       const int c = lane + 32 * e;
       f[e] = c < a.D ? to_f32(x[c]) : 0.f;
       ss = fmaf(f[e], f[e], ss);
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Args a) {
     __syncwarp();
     if (BWD) {
 #pragma unroll
-      for (int e = 0; e < MAXD / 32; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int c = lane + 32 * e;
         d[e] = c < a.D ? turned(c, -1.f) : 0.f;
         sa = fmaf(c < a.D && w ? d[e] * __ldg(w + c) : d[e], f[e], sa);
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Args a) {
     if (BWD) {
       const float m = sa * r * inv;
 #pragma unroll
-      for (int e = 0; e < MAXD / 32; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int c = lane + 32 * e;
         if (c < a.D) {
           const float n = f[e] * r;
@@ -391,12 +397,17 @@ __global__ void __launch_bounds__(THREADS) rows_kernel(const Args a) {
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < MAXD / 32; ++e) {
+      for (int e = 0; e < E; ++e) {
         const int c = lane + 32 * e;
         if (c < a.D) row[c] = f[e] * r * (w ? __ldg(w + c) : 1.f);
       }
       __syncwarp();
-      for (int c = lane; c < a.D; c += 32) ((T *)a.y[z])[at + c] = from_f32<T>(turned(c, 1.f));
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = lane + 32 * e < a.D ? turned(lane + 32 * e, 1.f) : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (lane + 32 * e < a.D) ((T *)a.y[z])[at + lane + 32 * e] = from_f32<T>(y[e]);
     }
     __syncwarp();
   }
@@ -488,11 +499,21 @@ bool vectors(const glacore_qk_norm *p, const Args &a) {
          a.xs[1] % step == 0 && !(at & 15);
 }
 
+// go(E), 32 E channels holding a row
+template <typename F>
+void by_channels(int64_t D, F go) {
+  if (D <= 32) go(std::integral_constant<int, 1>());
+  else if (D <= 64) go(std::integral_constant<int, 2>());
+  else if (D <= 128) go(std::integral_constant<int, 4>());
+  else go(std::integral_constant<int, 8>());
+}
+
 template <typename T>
 cudaError_t run_fwd(const glacore_qk_norm *p, Args &a, cudaStream_t st) {
   if (!vectors(p, a)) {
     const int64_t rows = a.tokens * (a.H[0] + a.H[1]);
-    rows_kernel<T, false><<<(unsigned)std::min<int64_t>((rows + WARPS - 1) / WARPS, 152 * 64), THREADS, 0, st>>>(a);
+    const unsigned blocks = (unsigned)std::min<int64_t>((rows + WARPS - 1) / WARPS, 152 * 64);
+    by_channels(p->D, [&](auto e) { rows_kernel<T, false, decltype(e)::value><<<blocks, THREADS, 0, st>>>(a); });
     return cudaGetLastError();
   }
   // A warp takes all heads of a token's queries (keys); few tokens: fewer heads,
@@ -525,7 +546,9 @@ cudaError_t run_bwd(const glacore_qk_norm *p, Args &a, float *dwq, float *dwk, c
   const int64_t blocks = bwd_blocks(a.tokens);
   const size_t row = 2 * sizeof(float) * a.D;
   if (!vectors(p, a)) {
-    rows_kernel<T, true><<<(unsigned)blocks, THREADS, WARPS * row, st>>>(a);
+    by_channels(p->D, [&](auto e) {
+      rows_kernel<T, true, decltype(e)::value><<<(unsigned)blocks, THREADS, WARPS * row, st>>>(a);
+    });
   } else {
     const int lpr = p->D <= 64 ? 8 : p->D <= 128 ? 16 : 32;
     auto go = [&](auto kernel) { kernel<<<(unsigned)blocks, THREADS, WARPS * (32 / lpr) * row, st>>>(a); };
