@@ -227,7 +227,8 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  * everything else on the CUDA cores in fp32.  On the tensor cores whatever is computed enters products in two
  * bf16 parts: fp32 outputs (states, dg, dbeta) are off by about 5e-6 of their size,
  * bf16 ones by their own rounding.  Results do not depend on the order in which
- * CTAs run.
+ * CTAs run.  Forwards, few long rows on the tensor cores take one cooperative launch
+ * with a CTA on every SM, which waits for kernels of other streams to leave.
  * Workspace, per 64 tokens and head: forward 41 KB; backward 233 KB (the state
  * before them and its gradient behind them in 64 KB each, and what their tokens
  * left in 64 KB), on the CUDA cores 8 K V bytes and 8 V per token; 8 K
