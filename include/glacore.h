@@ -225,7 +225,7 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  * do_, dq, dk and dv 16-byte aligned and the token strides multiples of 8, on padded
  * copies in the workspace where K, V, q, k, v or their strides are not so;
  * everything else on the CUDA cores in fp32.  On the tensor cores whatever is computed enters products in two
- * bf16 parts: fp32 outputs (states, dg, dbeta) are off by about 5e-6 of their size,
+ * bf16 parts: fp32 outputs (states, dg, dbeta) are off by about 5e-6 of what they sum,
  * bf16 ones by their own rounding.  Results do not depend on the order in which
  * CTAs run.  Forwards, few long rows on the tensor cores take one cooperative launch
  * with a CTA on every SM, which waits for kernels of other streams to leave.
