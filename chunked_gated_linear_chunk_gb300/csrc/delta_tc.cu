@@ -752,12 +752,14 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
 #pragma unroll
       for (int i = 0; i < 32; ++i) S[i] = a.h0 && in && 32 * grp + i < a.sK ? a.h0[at + (int64_t)i * a.sV] : 0.f;
     }
-    // Rows past the document's end hold other tokens: as zeros, nothing in them reaches a sum.
+    // Rows past the document's end hold other tokens: as zeros, nothing in them reaches a sum.  Those of the
+    // products' operands, which wait for every warp (s_ready); v is masked where it is read, right behind this
+    // warp's own share.
     auto clear_rows = [&](int j) -> bool {
       const int L = chunk_len(j);
       if (L == CH) return true;
       if (!wait_full(j)) return false;
-      constexpr int BLOCKS = STATES ? 4 : 6;  // tiles of 64 rows: k, (q), v
+      constexpr int BLOCKS = STATES ? 2 : 4;  // tiles of 64 rows: k, (q)
       for (int i = threadIdx.x; i < (CH - L) * BLOCKS * 8; i += 32 * CHAIN_WARPS) {
         const int c = i % 8, b = i / 8 % BLOCKS, r = L + i / (8 * BLOCKS);
         st_shared_v4(sb + stage(j) + b * 8192u + r * 128u + c * 16u, 0u, 0u, 0u, 0u);
@@ -787,6 +789,11 @@ __device__ __forceinline__ void chain_walk(const ChainMaps &maps, const ChainArg
         const ColBf16 col(sb + stage(j) + L_::V, 16 * grp, v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) Y[i] = bf16_bits_to_f32(lds_u16(col.at(i)));
+        // rows past the end hold other tokens: an infinity there times their b = 0 would be NaN in R
+        const int left = chunk_len(j) - 16 * grp;
+        if (left < 16)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) Y[i] = i < left ? Y[i] : 0.f;
       }
       const bool wide = gates[G_WIDE] != 0.f;
       ok = ok && mbar_wait(&x_full, ph, WAIT_CYCLES);
