@@ -63,6 +63,10 @@ __device__ __forceinline__ bool chunk_in_slot(const Docs &docs, int64_t slot, in
   return true;
 }
 
+// A token's log decay as a chunk's sums take it: below -10^4 e^g is 0 as well, and
+// the sums stay finite.  (Not by fmaxf, which takes NaN for the bound.)
+__device__ __forceinline__ float log_decay(float g) { return g < -1e4f ? -1e4f : g; }
+
 // Scratch of the backward, all fp32: states before and state gradients after
 // every chunk [slots, H, K, V], E and dR of every token [BT, H, V].
 struct Saved {

@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(256, 2) grads_kernel(const GradArgs<T> a) {
 
   double G = 0.0;
   if (tid < C) {
-    if (tid < L) G = (double)fmaxf(a.g[(tok0 + tid) * a.H + h], -1e4f);  // exp of less is 0 as well
+    if (tid < L) G = (double)log_decay(a.g[(tok0 + tid) * a.H + h]);
     s.beta[tid] = tid < L ? a.beta[(tok0 + tid) * a.H + h] : 0.f;
     s.gq[tid] = s.gk[tid] = s.gadd[tid] = 0.f;
 #pragma unroll

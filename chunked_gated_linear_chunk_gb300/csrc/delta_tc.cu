@@ -226,7 +226,7 @@ __device__ __forceinline__ bool prep_chunk(const PrepArgs &a, const PrepTeam &w,
     }
   };
   auto scan = [&]() {  // begins and ends with a barrier of the team
-    double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;  // e^g of less is 0 as well
+    double G = (double)log_decay(g_next) * 1.4426950408889634;
     const float b = b_next;
     if (tid < CH) {
 #pragma unroll
@@ -1651,7 +1651,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 1) delta_grads_kernel(const __gr
       tok = tok_next;
       L = L_next;
       // decays, while the copies run
-      double G = (double)fmaxf(g_next, -1e4f) * 1.4426950408889634;
+      double G = (double)log_decay(g_next) * 1.4426950408889634;
       const float b = b_next;
       if (tid < CH) {
 #pragma unroll
