@@ -2038,8 +2038,22 @@ cudaError_t launch(int64_t blocks, int threads, uint32_t smem, const Call &c, co
   cfg.attrs = attr;
   cfg.numAttrs = start == Start::behind ? 0 : 1;
   const cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, maps, a);
-  mark_launch(label, c.st);
+  if (r == cudaSuccess) mark_launch(label, c.st);
   return r;
+}
+// Whether a stream's kernels may run on all SMs of the device: not one that a
+// partition of it (a green context) made.
+bool on_all_sms(cudaStream_t st) {
+  typedef CUresult(CUDAAPI * Fn)(CUstream, CUgreenCtx *);
+  static const Fn partition_of = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuStreamGetGreenCtx", &p, 12040, cudaEnableDefault, &q) == cudaSuccess &&
+                    q == cudaDriverEntryPointSuccess;
+    return ok ? (Fn)p : nullptr;
+  }();
+  CUgreenCtx partition = nullptr;
+  return !partition_of || (partition_of((CUstream)st, &partition) == CUDA_SUCCESS && !partition);
 }
 PrepArgs prep_args(const Call &c, char *ws, const TcLayout &l) {
   PrepArgs a;
@@ -2112,7 +2126,7 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
   ChainArgs a = chain_args(c, ws, l);
   a.o = (__nv_bfloat16 *)o;
   a.ht = ht;
-  if (e == cudaSuccess && overlaps(c, units)) {
+  if (e == cudaSuccess && overlaps(c, units) && on_all_sms(c.st)) {
     OverlapArgs x;
     x.chain = a;
     x.prep = prep_args(c, ws, l);
@@ -2121,9 +2135,13 @@ cudaError_t tc_fwd(const Call &c, void *o, float *ht, char *ws) {
     x.chain.flags = x.flags;
     x.makers = (uint32_t)std::min(tc::sm_count() - units, (c.slots * c.p.H + TEAMS - 1) / TEAMS);
     e = cudaMemsetAsync(x.flags, 0, (size_t)(c.slots * c.p.H) * sizeof(uint32_t), c.st);
-    if (e != cudaSuccess) return e;
-    return launch<delta_overlap_kernel>(x.makers + units, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
-                                        OverlapMaps{{m.q, m.k, m.v}, {m.q, m.k}}, x, "delta_overlap", Start::together);
+    if (e == cudaSuccess)
+      e = launch<delta_overlap_kernel>(x.makers + units, CHAIN_THREADS, ChainSmem<false>::BYTES, c,
+                                       OverlapMaps{{m.q, m.k, m.v}, {m.q, m.k}}, x, "delta_overlap", Start::together);
+    // fewer SMs than the device has are to be had (a share of them): one kernel after the other
+    if (e != cudaErrorCooperativeLaunchTooLarge) return e;
+    cudaGetLastError();
+    e = cudaSuccess;
   }
   if (e == cudaSuccess) e = launch_order(c, units, ws + l.order, order);
   if (e == cudaSuccess) e = prep(c, m, ws, l);

@@ -228,7 +228,8 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  * bf16 parts: fp32 outputs (states, dg, dbeta) are off by about 5e-6 of what they sum,
  * bf16 ones by their own rounding.  Results do not depend on the order in which
  * CTAs run.  Forwards, few long rows on the tensor cores take one cooperative launch
- * with a CTA on every SM, which waits for kernels of other streams to leave.
+ * with a CTA on every SM, which waits for kernels of other streams to leave (on a
+ * stream that has a part of the SMs, or where the launch is refused: two launches).
  * Workspace, per 64 tokens and head: forward 41 KB; backward 233 KB (the state
  * before them and its gradient behind them in 64 KB each, and what their tokens
  * left in 64 KB), on the CUDA cores 8 K V bytes and 8 V per token; 8 K
