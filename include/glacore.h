@@ -226,7 +226,11 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  * copies in the workspace where K, V, q, k, v or their strides are not so;
  * everything else on the CUDA cores in fp32.  On the tensor cores whatever is computed enters products in two
  * bf16 parts: fp32 outputs (states, dg, dbeta) are off by about 5e-6 of what they sum,
- * bf16 ones by their own rounding.  Results do not depend on the order in which
+ * bf16 ones by their own rounding (q, k and v given as fp32: 4e-7).  There a token's infinity or
+ * NaN also reaches the tokens before it in its chunk of 64 (counted from the document's
+ * start), where products have a zero for it: what stands behind a row's last token and is not
+ * finite wants segment_ids of its own.  No other document, head or earlier chunk sees it.
+ * Results do not depend on the order in which
  * CTAs run.  Forwards, few long rows on the tensor cores take one cooperative launch
  * with a CTA on every SM, which waits for kernels of other streams to leave (on a
  * stream that has a part of the SMs, or where the launch is refused: two launches).

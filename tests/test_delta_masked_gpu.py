@@ -119,3 +119,23 @@ def test_nan_in_a_step(cuda_ok, dtype, K, V, T, name):
     bad[1, T // 2:, 1] = True
     assert torch.equal(torch.isnan(o), bad[..., None].expand_as(o))
     assert torch.equal(torch.isnan(pool), bad.any(1)[..., None, None].expand_as(pool))
+
+
+@pytest.mark.parametrize("B,T,H,Hqk,K,V,dtype,docs,last", PATHS)
+def test_how_far_an_infinity_reaches(cuda_ok, B, T, H, Hqk, K, V, dtype, docs, last):
+    """One in a token's v: the tokens behind it, and of those before it at most its chunk of 64 (token by token: none)."""
+    x = operands(B, T, H, Hqk, K, V, dtype, 5)
+    end = T // docs
+    at = int(0.4 * (end - 1))
+    seg = (torch.arange(T, device="cuda") // end).clamp(max=docs - 1).int().expand(B, T).contiguous() if docs > 1 else None
+    want, states = forward(x, seg, B * docs)
+    x["v"][0, at, 0, V // 2] = INF
+    o, s = forward(x, seg, B * docs)
+    clean = torch.ones(B, T, H, dtype=torch.bool, device="cuda")
+    clean[0, at if last == "delta_scan" else at // 64 * 64:end, 0] = False
+    assert torch.equal(o[clean], want[clean])
+    assert not torch.isfinite(o[0, at:end, 0, V // 2]).any()
+    assert torch.equal(s[1:], states[1:]) and torch.equal(s[0, 1:], states[0, 1:])
+    columns = [c for c in range(V) if c != V // 2]  # they do not see each other
+    assert torch.equal(o[..., columns], want[..., columns]) and torch.equal(s[..., columns], states[..., columns])
+    glc.get_device_error()
