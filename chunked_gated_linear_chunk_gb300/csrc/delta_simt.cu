@@ -394,13 +394,18 @@ template <template <int> class Kernel, typename F>
 cudaError_t by_rows(int64_t K, bool few, F go) {
   if (K <= 32) return go(Kernel<4>::get(few), 2 * sizeof(Tile<4>));
   if (K <= 64) return go(Kernel<8>::get(few), 2 * sizeof(Tile<8>));
-  if (K <= 96 && Kernel<12>::ROWS == 12) return go(Kernel<12>::get(few), 2 * sizeof(Tile<12>));
+  if constexpr (Kernel<12>::ROWS == 12)
+    if (K <= 96) return go(Kernel<12>::get(few), 2 * sizeof(Tile<12>));
   if (K <= 128) return go(Kernel<16>::get(few), 2 * sizeof(Tile<16>));
   return go(Kernel<32>::get(few), 2 * sizeof(Tile<32>));
 }
+// 65 to 96 channels: 12 rows of a thread but for fp32 forwards, which take 16 (12 rows / 16, us, forward: 3 x 333 tokens of
+// 6 heads of 72 x 41 bf16 82 / 88, fp32 99 / 74; 2048 of 16 of 96 x 128 477 / 522, 579 / 436; 16 x 256 of 16 of 72 x 128
+// 275 / 340, 371 / 308; 64 x 128 of 8 of 96 x 64 142 / 174, 191 / 158; 48 of 16 of 96 x 128 17 / 17, 19 / 15.  Backward, whole
+// call, fp32: 123 / 135, 633 / 701, 887 / 1018, 538 / 602, 82 / 84; bf16 9 to 15% the same way).
 template <typename T> struct Scan {
   template <int KR> struct One {
-    enum { ROWS = KR == 12 && sizeof(T) == 4 ? 0 : KR };  // fp32, 333 tokens of 72 channels: 12 rows 99 us, 16 rows 76
+    enum { ROWS = KR == 12 && sizeof(T) == 4 ? 0 : KR };
     static auto get(bool) { return scan_kernel<T, KR>; }
   };
   template <int KR> struct Two {
