@@ -17,7 +17,7 @@ inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 // multiple of 8, odd strides or addresses) go to them as padded copies, backwards always
 // and forwards from this many tokens times rounds of blocks (run_fwd) on.  Token by
 // token / copies, us forward and backward, heads of 72 x 41 and 6 of them: 8 tokens
-// 6 / 31, 52 / 45; 100: 31 / 35, 93 / 52; 128: 37 / 35, 101 / 53; 333: 89 / 47, 160 / 70;
+// 6 / 31, 52 / 45; 100: 29 / 35, 93 / 52; 128: 35 / 35, 101 / 53; 333: 89 / 47, 160 / 70;
 // 4 x 2048 tokens of 16 heads of 125 x 77: 756 / 207, 2127 / 522; 64 x 8 tokens of 16
 // heads of 90 x 90: 47 / 88, 385 / 234.
 constexpr int64_t PAD_TOKENS = 120;
@@ -160,9 +160,12 @@ glacore_status run_fwd(const glacore_problem *p, const float *beta, void *o, flo
   Call c;
   if ((s = begin(p, beta, L, st, c))) return s;
   // Short rows: token by token, all slices of all documents at once, 4 us and
-  // 0.26 us per token and round of blocks, against 19 us and 4 us per further chunk
-  // (one row of 16 heads of 128 x 128: 48 tokens 16.6 us against 18.6, 64 tokens
-  // 20.8 against 18.6; 64 rows of 8 tokens 62 us against 84, of 16 tokens 98 against 82).
+  // 0.26 us per token and round of blocks, against 13 us and 4 us per chunk
+  // (one row of 16 heads of 128 x 128: 48 tokens 16.6 us against 18.5, 56 tokens 18.7 against
+  // 17.7, 64 tokens 20.7 against 17.0; 64 rows of 8 tokens 62 us against 80, of 16 tokens 98 against
+  // 80).  Of packed documents the row bounds the longest, whose tokens are in sequence; their
+  // number does not tell it: 64 of 8 tokens in a row would take 68 us against 92, but one of 1793 beside 255
+  // of one token (2 heads of 32 x 32) 340 against 134.
   const int64_t blocks = c.docs.n * p->H * ((p->V + 31) / 32), rounds = (blocks + 607) / 608;
   if (L.on_tc && p->T * rounds > 56 && !((uintptr_t)o & 15))
     return status_of(tc_fwd(c, o, ht, (char *)p->workspace + L.tc));

@@ -14,7 +14,7 @@
 //     o = scale (e^g S^T q + (q . k) u),
 // so that a token costs one exchange over the CTA: partial sums of the warps
 // in shared memory, added by every thread in a fixed order.  Arithmetic is
-// fp32 throughout.  256 sequences of 16 heads of 128 x 128: 87 us in 8192 CTAs, 93%
+// fp32 throughout.  256 sequences of 16 heads of 128 x 128: 90 us in 8192 CTAs, 89%
 // of the copy rate (one sequence: 6 us from a graph, its launch and two latencies).
 #include <algorithm>
 

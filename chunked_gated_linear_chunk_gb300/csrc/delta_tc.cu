@@ -2088,9 +2088,9 @@ cudaError_t launch_order(const Call &c, int64_t blocks, char *ws, const int32_t 
 // would wait for the others' tiles), where what the tiles take alone, 0.019 us
 // a chunk and head, is more than what the walk loses, 0.4 us a chunk (its
 // copies wait for flags), and 2 to 6 us to begin with.  Heads x sequences, tokens,
-// us one after the other / at once: 64 x 2048: 164 / 137; 64 x 8192: 607 / 499; 76 x
-// 2048: 172 / 146; 64 x 640: 60 / 59; but 64 x 512: 49 / 51, 16 x 2048: 131 / 136,
-// 16 x 96: 21 / 27.
+// us one after the other / at once: 64 x 2048: 165 / 137; 64 x 8192: 612 / 475; 76 x
+// 2048: 173 / 142; 64 x 640: 60 / 58; but 64 x 512: 49 / 50, 16 x 2048: 132 / 133,
+// 16 x 512: 41 / 49, 16 x 96: 21 / 27.
 bool overlaps(const Call &c, int64_t units) {
   return !c.docs.start && units <= tc::sm_count() / 2 && (units - 24) * ((c.docs.T + CH - 1) / CH) > 320 &&
          c.slots * c.p.H < ((int64_t)1 << 31);

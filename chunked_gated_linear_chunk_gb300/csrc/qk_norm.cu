@@ -16,10 +16,11 @@
 // in registers, with the loads of several rows in flight.  Rows that 16-byte accesses
 // or 8-channel steps do not fit take a kernel with a warp per row and the
 // row in shared memory.
-// 8192 tokens of 32 heads of 128, bf16, rotated: 24.6 us forward (82% of the copy
-// rate), 49 us backward (62%: three blocks' loads on an SM do not cover their
-// latency; two or four of them are slower) and 7 us for the sum of the weight gradients.
-// Heads of 101 channels: 121 and 165 us (single values, the table read for each; a row
+// 8192 tokens of 32 heads of 128, bf16, rotated: 26.8 us forward (75% of the copy
+// rate), 55 us backward (55%: three blocks' loads on an SM do not cover their
+// latency; two or four of them are slower), 7 us of it the sum of the weight gradients.
+// fp32: 48 and 81 us (84 and 75%).
+// Heads of 101 channels, bf16: 122 and 162 us (single values, the table read for each; a row
 // fetched ahead gains nothing and costs 20% at 250 channels).
 #include <string.h>
 

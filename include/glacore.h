@@ -234,11 +234,13 @@ glacore_status ssd_step(const glacore_problem *p, float *state,
  * CTAs run.  Forwards, few long rows on the tensor cores take one cooperative launch
  * with a CTA on every SM, which waits for kernels of other streams to leave (on a
  * stream that has a part of the SMs, or where the launch is refused: two launches).
- * Workspace, per 64 tokens and head: forward 41 KB; backward 233 KB (the state
- * before them and its gradient behind them in 64 KB each, and what their tokens
- * left in 64 KB), on the CUDA cores 8 K V bytes and 8 V per token; 8 K
- * per token and head where heads share q and k; and the padded copies, 2 bytes a
- * value of q, k, v and o, backwards also of the gradients.  (The size goes by
+ * Workspace, per chunk and head, whatever K and V and whichever kernels run (bf16, K and V up
+ * to 128): forward 41 KB; backward 233 KB (the state before a chunk and its gradient
+ * behind it in 64 KB each, and what its tokens left in 64 KB); on the CUDA
+ * cores 8 K V bytes and 8 V per token.  Chunks: B ceil(T / 64); with segment_ids
+ * up to B T / 64 + n_seqs (and no more than B T), so that documents of 8 tokens take 9
+ * times what a row of the same tokens takes.  Besides, 8 K per token and head where
+ * heads share q and k, and the padded copies, 2 bytes a value of q, k, v and o, backwards also of the gradients.  (The size goes by
  * the problem's addresses and strides as well: ask with those of the call.) */
 size_t delta_fwd_workspace_size(const glacore_problem *p);
 size_t delta_bwd_workspace_size(const glacore_problem *p);
@@ -389,7 +391,8 @@ glacore_status short_conv_bwd(const void *x, const float *w, const float *b,
  * without weights), the latter reduced deterministically through the workspace
  * (at least qk_norm_bwd_workspace_size bytes, 256-byte aligned).
  * D and R multiples of 8 (interleaved: R of 4) with 16-byte aligned addresses
- * and strides are the fast case (others take about 3 times as long). */
+ * and strides are the fast case (others take 4 to 6 times as long for the same bytes,
+ * backward 3 to 4 times). */
 typedef struct glacore_qk_norm {
   int64_t B, T, Hq, Hk, D, R;
   int32_t dtype;
